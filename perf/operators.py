@@ -1,0 +1,580 @@
+"""Cases of the fine-tuning operators around the QLoRA linear: what is timed
+and what their results are compared with.
+
+Operators (``op`` of a case):
+  norm_fwd    h' = h + a g post(o),  y = RMSNorm(h') w_pre   [+ the 8-bit copy of y]
+  norm_bwd    its gradients
+  act8_store  an activation into its 8-bit checkpoint and back
+  act8_bwd    the QLoRA linear's backward with x read from such a checkpoint
+  lp_fwd      log probabilities of given tokens, entropy, top alternatives
+  lp_bwd      the gradient of the first two with respect to the logits
+
+With ``own`` false every pass is elementary torch operations in fp32, rounded
+once at the end; with ``own`` true the calls of quantized_fine_tuning_nf4_amd.
+"""
+import math
+
+import torch
+
+own = False
+
+BLOCK = 64  # columns of an activation that share one power-of-two scale
+
+NF4 = [-1.0, -0.6961928009986877, -0.5250730514526367, -0.39491748809814453,
+       -0.28444138169288635, -0.18477343022823334, -0.09105003625154495, 0.0,
+       0.07958029955625534, 0.16093020141124725, 0.24611230194568634, 0.33791524171829224,
+       0.44070982933044434, 0.5626170039176941, 0.7229568362236023, 1.0]
+
+
+# ------------------------------------------------------------------ the cases
+def listed():
+    return [
+        # one token of a served model: residual add, both norms, layer gate
+        dict(name="norm_fwd_1x4096", op="norm_fwd", M=1, D=4096, res32=False, w32=False,
+             post="norm", gate="channel", pack=False),
+        # a training batch through a block's end into the next block's input
+        # and its 8-bit checkpoint, residual stream in fp32
+        dict(name="norm_fwd_4096x4096_act8", op="norm_fwd", M=4096, D=4096, res32=True, w32=True,
+             post="norm", gate="channel", pack=True),
+        # the training workload's batch: every gradient, norms trained too
+        dict(name="norm_bwd_8192x4096", op="norm_bwd", M=8192, D=4096, res32=False, w32=True,
+             post="norm", gate="channel", weights=True),
+        # a ragged batch of an odd width, one gate a token, frozen norms
+        dict(name="norm_bwd_1003x1001_rowgate", op="norm_bwd", M=1003, D=1001, res32=False,
+             w32=False, post="norm", gate="row", weights=False),
+        # the decoder layer's widest activation, kept for the backward
+        dict(name="act8_store_4096x14336", op="act8_store", M=4096, D=14336),
+        # a short ragged activation: the last block of a row is partial
+        dict(name="act8_store_77x1000", op="act8_store", M=77, D=1000),
+        # the training workload's linear, backward from the checkpoint
+        dict(name="act8_bwd_8192x4096x4096", op="act8_bwd", M=8192, rows=4096, cols=4096, r=16,
+             p=0.0, dx=True),
+        # k_proj of the decoder layer at rank 64 with adapter dropout, nothing
+        # below it trained: adapter gradients alone
+        dict(name="act8_bwd_4096x1024x4096_r64", op="act8_bwd", M=4096, rows=1024, cols=4096,
+             r=64, p=0.05, dx=False),
+        # one served token: its log probability, entropy and 20 alternatives
+        dict(name="lp_fwd_1x131072_top20", op="lp_fwd", T=1, V=131072, f32=True, k=20, pad=0,
+             masked=0.0),
+        # loss of a training batch
+        dict(name="lp_fwd_8192x32000", op="lp_fwd", T=8192, V=32000, f32=False, k=0, pad=0,
+             masked=0.0),
+        # its gradient, with an entropy term, over a large vocabulary
+        dict(name="lp_bwd_4096x131072", op="lp_bwd", T=4096, V=131072, f32=False, k=0, pad=0,
+             masked=0.0, entropy=True),
+        # scoring of a ragged batch: odd vocabulary inside wider rows, banned
+        # tokens at -inf, five alternatives
+        dict(name="lp_fwd_301x50021_top5", op="lp_fwd", T=301, V=50021, f32=True, k=5, pad=27,
+             masked=0.2),
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["norm_fwd", "norm_bwd", "act8_store", "act8_bwd", "lp_fwd", "lp_bwd"])
+    if op in ("norm_fwd", "norm_bwd"):
+        M, D = _log(rng, 1, 8192), _log(rng, 64, 8192)
+        D = rng.choice([D, D // 8 * 8, D // 64 * 64, D // 64 * 64])
+        M = min(M, (1 << 25) // D)
+        case = dict(op=op, M=M, D=D, res32=rng.random() < 0.5, w32=rng.random() < 0.5,
+                    post=rng.choice(["none", "add", "norm", "norm"]),
+                    gate=rng.choice(["none", "channel", "row", "element"]))
+        if case["post"] == "none":
+            case["gate"] = "none"
+        if op == "norm_fwd":
+            case["pack"] = rng.random() < 0.5
+        else:
+            case["weights"] = rng.random() < 0.5
+        return case
+    if op == "act8_store":
+        D = _log(rng, 64, 14336)
+        D = rng.choice([D, D // 64 * 64, D // 64 * 64])
+        return dict(op=op, M=min(_log(rng, 1, 8192), 4096 * 14336 // D), D=D)
+    if op == "act8_bwd":
+        rows, cols = _log(rng, 64, 4096) // 8 * 8, _log(rng, 64, 4096) // 64 * 64
+        return dict(op=op, M=_log(rng, 1, 8192), rows=rows, cols=cols, r=_log(rng, 1, 64),
+                    p=rng.choice([0.0, 0.0, 0.05, 0.1]), dx=rng.random() < 0.5)
+    V = _log(rng, 1000, 131072)
+    T = min(_log(rng, 1, 8192), (4096 * 131072 if op == "lp_bwd" else 8192 * 32000) // V)
+    case = dict(op=op, T=T, V=V, f32=rng.random() < 0.5, k=0, pad=rng.choice([0, 0, 24, 5]),
+                masked=rng.choice([0.0, 0.0, 0.3]))
+    if op == "lp_bwd":
+        case["entropy"] = rng.random() < 0.5
+    elif rng.random() < 0.5:
+        case["k"] = _log(rng, 1, 32)
+    return case
+
+
+# -------------------------------------------------------------------- inputs
+class _Draw:
+    """Seeded device tensors."""
+
+    def __init__(self, seed):
+        self.g = torch.Generator(device="cuda").manual_seed(int(seed))
+
+    def normal(self, *shape, std=1.0, mean=0.0, dtype=torch.float32):
+        x = torch.randn(*shape, generator=self.g, device="cuda")
+        return x.mul_(std).add_(mean).to(dtype)
+
+    def uniform(self, *shape):
+        return torch.rand(*shape, generator=self.g, device="cuda")
+
+    def below(self, n, *shape):
+        return torch.randint(0, n, shape, generator=self.g, device="cuda")
+
+
+def _encode(x):
+    """Codes and exponent bytes of a bf16 or fp32 matrix in blocks of 64
+    columns: the smallest power of two 2^e with absmax <= 127 2^e, e >= -126."""
+    M, D = x.shape
+    nb = (D + BLOCK - 1) // BLOCK
+    v = torch.nn.functional.pad(x.float(), (0, nb * BLOCK - D)).view(M, nb, BLOCK)
+    mant, ex = torch.frexp(v.abs().amax(dim=2))  # absmax = mant 2^ex, mant in [0.5, 1)
+    e = (ex - 7 + (mant > 127 / 128).to(ex.dtype)).clamp(min=-126)
+    e = torch.where(mant == 0, torch.full_like(e, -126), e)
+    codes = torch.round(torch.ldexp(v, -e.unsqueeze(2))).to(torch.int8)
+    return codes.view(M, nb * BLOCK)[:, :D].contiguous(), (e + 127).to(torch.uint8)
+
+
+def _decode(codes, exps):
+    """The values that codes and exponent bytes stand for, fp32."""
+    M, D = codes.shape
+    scale = torch.ldexp(torch.ones_like(exps, dtype=torch.float32), exps.to(torch.int32) - 127)
+    return codes.float() * scale.repeat_interleave(BLOCK, dim=1)[:, :D]
+
+
+def _quantize(W):
+    """NF4 codes in blocks of 64 with double-quantized scales of W [rows, cols]."""
+    levels = torch.tensor(NF4, device="cuda")
+    blocks = W.reshape(-1, 64)
+    s = blocks.abs().amax(dim=1)
+    mid = (levels[1:] + levels[:-1]) / 2
+    codes = torch.bucketize(blocks / s[:, None], mid).to(torch.uint8).view(-1, 2)
+    nb = s.numel()
+    mu = s.mean()
+    d = torch.nn.functional.pad(s - mu, (0, -nb % 256)).view(-1, 256)
+    s2 = d.abs().amax(dim=1) / 448
+    q = (d / s2[:, None]).to(torch.float8_e4m3fn).view(torch.uint8).reshape(-1)[:nb]
+    return (codes[:, 0] | (codes[:, 1] << 4)).contiguous(), q.contiguous(), s2, mu.view(1)
+
+
+def _inputs(case, seed):
+    """The tensors of a case, from the seed alone."""
+    d, bf, op = _Draw(seed), torch.bfloat16, case["op"]
+    if op in ("norm_fwd", "norm_bwd"):
+        M, D = case["M"], case["D"]
+        wt = torch.float32 if case["w32"] else bf
+        rt = torch.float32 if case["res32"] else bf
+        t = dict(h=d.normal(M, D, std=2.0, dtype=rt), o=None, w_post=None, gate=None,
+                 w_pre=d.normal(D, std=0.2, mean=1.0, dtype=wt), scale=0.5, eps=1e-6)
+        if case["post"] != "none":
+            t["o"] = d.normal(M, D, dtype=bf)
+        if case["post"] == "norm":
+            t["w_post"] = d.normal(D, std=0.2, mean=1.0, dtype=wt)
+        if case["gate"] != "none":
+            shape, kind = {"channel": ((D,), wt), "row": ((M,), bf), "element": ((M, D), bf)}[
+                case["gate"]]
+            t["gate"] = d.normal(*shape, std=0.3, mean=0.7, dtype=kind)
+        if op == "norm_bwd":
+            t["dy"] = d.normal(M, D, std=0.1, dtype=bf)
+            t["dh_new"] = d.normal(M, D, std=0.1, dtype=rt)
+        return t
+    if op == "act8_store":
+        x = d.normal(case["M"], case["D"])
+        x[:, :: 97] *= 8.0  # a few strong channels
+        return dict(x=x.to(bf))
+    if op == "act8_bwd":
+        M, rows, cols, r = case["M"], case["rows"], case["cols"], case["r"]
+        packed, qscale, scale2, offset = _quantize(d.normal(rows, cols, std=0.02))
+        A, B = d.normal(r, cols, std=0.01, dtype=bf), d.normal(rows, r, std=0.01, dtype=bf)
+        x = d.normal(M, cols, dtype=bf)
+        codes, exps = _encode(x)
+        mask = None
+        if case["p"]:
+            bits = torch.tensor([1 << b for b in range(8)], device="cuda")
+            mask = ((d.uniform(M * cols // 8, 8) >= case["p"]) * bits).sum(dim=1).to(torch.uint8)
+        u = x.float() * _keep(mask, M, cols) if mask is not None else x.float()
+        return dict(packed=packed, qscale=qscale, scale2=scale2, offset=offset, A=A, B=B,
+                    codes=codes, exps=exps, mask=mask, u=u @ A.float().t(),
+                    dY=d.normal(M, rows, dtype=bf), alpha=2.0 * r)
+    T, V = case["T"], case["V"]
+    wide = d.normal(T, V + case["pad"], std=2.5)
+    t = dict(targets=d.below(V, T), scale=1.0)
+    t["targets"] = torch.where(d.uniform(T) < 0.1, torch.full_like(t["targets"], -1), t["targets"])
+    # a model's logits: most targets stand out, and so does a token beside them
+    at, rows = t["targets"].clamp(min=0), torch.arange(T, device="cuda")
+    wide[rows, at] += 8.0 * (d.uniform(T) < 0.7)
+    wide[rows, d.below(V, T)] += 6.0
+    if case["masked"]:
+        ban = d.uniform(V + case["pad"]) < case["masked"]
+        wide.masked_fill_(ban, -math.inf)
+    t["logits"] = wide.to(torch.float32 if case["f32"] else bf)[:, :V]
+    if op == "lp_bwd":
+        t["dlogp"] = d.normal(T, std=0.1, mean=-1.0) / T
+        t["dentropy"] = d.normal(T, std=0.01) / T if case["entropy"] else None
+        x = t["logits"].float()
+        m = x.amax(dim=1).clamp(min=torch.finfo(torch.float32).min)
+        z = x.sub_(m[:, None])
+        ez = torch.exp(z)
+        S = ez.sum(dim=1)
+        H = S.log() - (ez * z.clamp(min=-1e30)).sum(dim=1) / S
+        t["stats"], t["entropy"] = torch.stack([m, S.log()], dim=1), H
+    return t
+
+
+def _keep(mask, M, cols):
+    """1.0 where a bit-packed keep mask lets an element of x [M, cols] through."""
+    bits = torch.arange(8, device=mask.device, dtype=torch.uint8)
+    return ((mask[:, None] >> bits) & 1).view(M, cols).float()
+
+
+def prepare(case, seed):
+    return dict(case=dict(case), **_inputs(case, seed))
+
+
+# ----------------------------------------------------------------- plain forms
+def _branch(s, o):
+    """post(o) and its gate, both ready to broadcast over [M, D]; fp32."""
+    p = o
+    if s["w_post"] is not None:
+        p = o * torch.rsqrt(o.square().mean(dim=1, keepdim=True) + s["eps"]) * s["w_post"].float()
+    g = None if s["gate"] is None else s["gate"].float()
+    if s["case"]["gate"] == "row":
+        g = g[:, None]
+    return p, g
+
+
+def _plain_norm_fwd(s):
+    h = s["h"].float()
+    if s["o"] is not None:
+        p, g = _branch(s, s["o"].float())
+        h = h + s["scale"] * (p if g is None else g * p)
+    y = h * torch.rsqrt(h.square().mean(dim=1, keepdim=True) + s["eps"]) * s["w_pre"].float()
+    y = y.to(torch.bfloat16)
+    out = dict(h=h.to(s["h"].dtype), y=y)
+    if s["case"]["pack"]:
+        out["x8"] = _decode(*_encode(y)).to(torch.bfloat16)
+    return out
+
+
+def _plain_norm_bwd(s):
+    h, dy, w = s["h"].float(), s["dy"].float(), s["w_pre"].float()
+    r = torch.rsqrt(h.square().mean(dim=1, keepdim=True) + s["eps"])
+    n, dn = h * r, dy * w
+    dh = s["dh_new"].float() + r * (dn - n * (dn * n).mean(dim=1, keepdim=True))
+    out = dict(dh=dh.to(s["h"].dtype))
+    if s["case"]["weights"]:
+        out["dw_pre"] = (dy * n).sum(dim=0)
+    if s["o"] is None:
+        return out
+    o = s["o"].float()
+    p, g = _branch(s, o)
+    a = s["scale"] * dh
+    if g is not None:
+        dg = a * p
+        out["dgate"] = {"channel": lambda: dg.sum(dim=0), "row": lambda: dg.sum(dim=1),
+                        "element": lambda: dg.to(torch.bfloat16)}[s["case"]["gate"]]()
+        a = a * g
+    if s["w_post"] is not None:
+        r1 = torch.rsqrt(o.square().mean(dim=1, keepdim=True) + s["eps"])
+        q, dq = o * r1, a * s["w_post"].float()
+        if s["case"]["weights"]:
+            out["dw_post"] = (a * q).sum(dim=0)
+        a = r1 * (dq - q * (dq * q).mean(dim=1, keepdim=True))
+    out["do"] = a.to(torch.bfloat16)
+    return out
+
+
+def _plain_act8_store(s):
+    return _decode(*_encode(s["x"])).to(torch.bfloat16)
+
+
+def _dequantized(s, dtype):
+    """The values of the 4-bit weight."""
+    c = s["case"]
+    nib = torch.stack([s["packed"] & 15, s["packed"] >> 4], dim=1).view(-1, 64).long()
+    grp = torch.arange(s["qscale"].numel(), device="cuda") // 256
+    sb = (s["qscale"].view(torch.float8_e4m3fn).to(dtype) * s["scale2"].to(dtype)[grp]
+          + s["offset"].to(dtype))
+    return (torch.tensor(NF4, device="cuda", dtype=dtype)[nib] * sb[:, None]).view(
+        c["rows"], c["cols"])
+
+
+def _plain_act8_bwd(s):
+    c = s["case"]
+    G, A, B = s["dY"].float(), s["A"].float(), s["B"].float()
+    x = _decode(s["codes"], s["exps"])
+    k = s["alpha"] / c["r"] / (1 - c["p"])
+    keep = None if s["mask"] is None else _keep(s["mask"], c["M"], c["cols"])
+    if keep is not None:
+        x = x * keep
+    v = G @ B
+    out = dict(dA=k * (v.t() @ x), dB=k * (G.t() @ s["u"]))
+    if c["dx"]:
+        dv = k * (v @ A)
+        out["dX"] = (G @ _dequantized(s, torch.float32)
+                     + (dv if keep is None else dv * keep)).to(torch.bfloat16)
+    return out
+
+
+def _plain_lp_fwd(s):
+    x, t, c, k = s["logits"].float(), s["targets"], s["scale"], s["case"]["k"]
+    m = x.amax(dim=1, keepdim=True)
+    z = (x - m) * c
+    e = torch.exp(z)
+    S = e.sum(dim=1)
+    lse = S.log()
+    # masked tokens take no part: 0 (-inf) counts as 0
+    ent = lse - (e * z.clamp(min=-1e30)).sum(dim=1) / S
+    got = z.gather(1, t.clamp(min=0)[:, None])[:, 0] - lse
+    out = dict(logp=torch.where(t < 0, torch.zeros_like(got), got), entropy=ent)
+    if k:
+        # (value, lowest index first) as one ordered whole number: no ties
+        b = (x + 0.0).view(torch.int32)
+        key = (b ^ ((b >> 31) & 0x7fffffff)).long() * (1 << 20)
+        key += (1 << 20) - 1 - torch.arange(x.shape[1], device=x.device)
+        ids = (1 << 20) - 1 - (key.topk(k, dim=1).values & ((1 << 20) - 1))
+        out["top_ids"] = ids.to(torch.int32)
+        out["top_logp"] = z.gather(1, ids) - lse[:, None]
+    return out
+
+
+def _plain_lp_bwd(s):
+    t, c = s["targets"], s["scale"]
+    lp = (s["logits"].float() - s["stats"][:, :1]) * c - s["stats"][:, 1:]
+    p = torch.exp(lp)
+    g = torch.where(t < 0, torch.zeros_like(s["dlogp"]), s["dlogp"])
+    d = -g[:, None] * p
+    if s["dentropy"] is not None:
+        d -= s["dentropy"][:, None] * p * (lp.clamp(min=-1e30) + s["entropy"][:, None])
+    d[torch.arange(t.numel(), device=t.device), t.clamp(min=0)] += g
+    return (d * c).to(s["logits"].dtype)
+
+
+# ------------------------------------------------------ the framework's own calls
+def _own_norm_fwd(s):
+    import quantized_fine_tuning_nf4_amd as qn
+    h, y, x8 = qn.block_norm_fwd(s["h"], s["w_pre"], o=s["o"], w_post=s["w_post"], gate=s["gate"],
+                                 scale=s["scale"], eps=s["eps"], pack=s["case"]["pack"])
+    out = dict(h=h, y=y)
+    if x8 is not None:
+        out["x8"] = qn.act8_unpack(x8)
+    return out
+
+
+def _own_norm_bwd(s):
+    import quantized_fine_tuning_nf4_amd as qn
+    g = qn.block_norm_bwd(s["dy"], s["h"], s["w_pre"], dh_new=s["dh_new"], o=s["o"],
+                          w_post=s["w_post"], gate=s["gate"], scale=s["scale"], eps=s["eps"],
+                          need_weights=s["case"]["weights"])
+    out = dict(dh=g.dh)
+    if g.dw_pre is not None:
+        out["dw_pre"] = g.dw_pre
+    if g.dgate is not None:
+        out["dgate"] = g.dgate
+    if g.dw_post is not None:
+        out["dw_post"] = g.dw_post
+    if g.do is not None:
+        out["do"] = g.do
+    return out
+
+
+def _own_act8_store(s):
+    import quantized_fine_tuning_nf4_amd as qn
+    return qn.act8_unpack(qn.act8_pack(s["x"]))
+
+
+def _own_act8_bwd(s):
+    import quantized_fine_tuning_nf4_amd as qn
+    c = s["case"]
+    st = qn.NF4State(s["packed"], s["qscale"], s["scale2"], s["offset"], c["rows"], c["cols"])
+    dX, dA, dB = qn.qlora_linear_bwd_act8(st, qn.Act8(s["codes"], s["exps"]), s["dY"], s["A"],
+                                          s["B"], s["alpha"], s["u"], need_dx=c["dx"],
+                                          dropout_mask=s["mask"], dropout_p=c["p"])
+    out = dict(dA=dA, dB=dB)
+    if dX is not None:
+        out["dX"] = dX
+    return out
+
+
+def _own_lp_fwd(s):
+    import quantized_fine_tuning_nf4_amd as qn
+    r = qn.token_logprobs_fwd(s["logits"], s["targets"], scale=s["scale"], top_k=s["case"]["k"])
+    out = dict(logp=r.logp, entropy=r.entropy)
+    if s["case"]["k"]:
+        out["top_ids"], out["top_logp"] = r.top_ids, r.top_logp
+    return out
+
+
+def _own_lp_bwd(s):
+    import quantized_fine_tuning_nf4_amd as qn
+    return qn.token_logprobs_bwd(s["logits"], s["targets"], s["stats"], s["entropy"], s["dlogp"],
+                                 dentropy=s["dentropy"], scale=s["scale"])
+
+
+PLAIN = dict(norm_fwd=_plain_norm_fwd, norm_bwd=_plain_norm_bwd, act8_store=_plain_act8_store,
+             act8_bwd=_plain_act8_bwd, lp_fwd=_plain_lp_fwd, lp_bwd=_plain_lp_bwd)
+OWN = dict(norm_fwd=_own_norm_fwd, norm_bwd=_own_norm_bwd, act8_store=_own_act8_store,
+           act8_bwd=_own_act8_bwd, lp_fwd=_own_lp_fwd, lp_bwd=_own_lp_bwd)
+
+
+def run(state):
+    return (OWN if own else PLAIN)[state["case"]["op"]](state)
+
+
+# ------------------------------------------------------------------------ work
+def work(case):
+    """Bytes: every input read once, every output written once (a checkpoint
+    counts as stored and as read back).  FLOPs: the products, and for the
+    rest a count of the additions and multiplications an element takes."""
+    op = case["op"]
+    if op in ("norm_fwd", "norm_bwd"):
+        M, D = case["M"], case["D"]
+        n, res, w = M * D, 4 if case["res32"] else 2, 4 if case["w32"] else 2
+        wide = {"none": 0, "channel": w * D, "row": 2 * M, "element": 2 * n}[case["gate"]]
+        b = w * D + wide
+        if op == "norm_fwd":
+            b += 2 * res * n + 2 * n  # h, h', y
+            if case["post"] != "none":
+                b += 2 * n
+            if case["pack"]:
+                b += 2 * (n + M * ((D + 63) // 64)) + 2 * n
+            flops = 12 * n
+        else:
+            b += 3 * res * n + 2 * n  # h', dh', dh, dy
+            if case["post"] != "none":
+                b += 4 * n
+                b += {"none": 0, "channel": 4 * D, "row": 4 * M, "element": 2 * n}[case["gate"]]
+            if case["weights"]:
+                b += 8 * D
+            flops = 30 * n
+        if case["post"] == "norm":
+            b += w * D
+        return dict(bytes=b, flops=flops)
+    if op == "act8_store":
+        n = case["M"] * case["D"]
+        return dict(bytes=4 * n + 2 * (n + case["M"] * ((case["D"] + 63) // 64)), flops=4 * n)
+    if op == "act8_bwd":
+        M, N, K, r = case["M"], case["rows"], case["cols"], case["r"]
+        b = M * K + M * K // 64 + 2 * M * N + 2 * r * N + 4 * M * r + 4 * r * (N + K)
+        flops = 2 * M * r * (2 * N + K)  # v, dB, dA
+        if case["p"]:
+            b += M * K // 8
+        if case["dx"]:
+            b += 2 * M * K + 2 * r * K + N * K // 2 + N * K // 64 + N * K // 4096
+            flops += 2 * M * K * (N + r)
+        return dict(bytes=b, flops=flops)
+    n, size = case["T"] * case["V"], 4 if case["f32"] else 2
+    if op == "lp_fwd":
+        return dict(bytes=n * size + case["T"] * (16 + 8 * case["k"]), flops=6 * n)
+    return dict(bytes=2 * n * size + 28 * case["T"], flops=6 * n)
+
+
+# ------------------------------------------------------- the definitions in 64 bits
+def _exact_norm(case, seed):
+    t = _inputs(case, seed)
+    f = lambda v: None if v is None else v.double()  # noqa: E731
+    bwd = case["op"] == "norm_bwd"
+    h, w2, o, w1, g = f(t["h"]), f(t["w_pre"]), f(t["o"]), f(t["w_post"]), f(t["gate"])
+    w2.requires_grad_(bwd)
+    o, w1, g = (None if v is None else v.requires_grad_(bwd) for v in (o, w1, g))
+
+    def rms(v):
+        return v / (v.pow(2).sum(-1, keepdim=True) / v.shape[-1] + t["eps"]).sqrt()
+
+    add = 0.0
+    if o is not None:
+        add = o if w1 is None else rms(o) * w1
+        if g is not None:
+            add = add * (g.unsqueeze(1) if g.dim() == 1 and case["gate"] == "row" else g)
+        add = add * t["scale"]
+    if not bwd:
+        new = h + add
+        y = rms(new) * w2
+        return dict(h=new, y=y, **({"x8": None} if case["pack"] else {}))
+    # the residual that makes the given h' what the forward gives
+    h0 = (h - (add.detach() if o is not None else 0.0)).requires_grad_(True)
+    new = h0 + add
+    torch.autograd.backward([rms(new) * w2, new], [f(t["dy"]), f(t["dh_new"])])
+    out = dict(dh=h0.grad)
+    if case["weights"]:
+        out["dw_pre"] = w2.grad
+        if w1 is not None:
+            out["dw_post"] = w1.grad
+    if o is not None:
+        out["do"] = o.grad
+    if g is not None:
+        out["dgate"] = g.grad
+    return out
+
+
+def _exact_store(case, seed):
+    """A block's scale by search: the first power of two that holds it."""
+    x = _inputs(case, seed)["x"].double()
+    M, D = x.shape
+    v = torch.nn.functional.pad(x, (0, -D % 64)).view(M, -1, 64)
+    top = v.abs().max(dim=2, keepdim=True).values
+    tries = torch.floor(torch.log2(top.clamp(min=2.0 ** -126))) - 8 + torch.arange(
+        4, device="cuda").double()
+    holds = (top <= 127 * torch.exp2(tries)).to(torch.uint8)
+    step = torch.exp2(tries.gather(2, holds.argmax(dim=2, keepdim=True)).clamp(min=-126))
+    return ((v / step).round() * step).view(M, -1)[:, :D]
+
+
+def _exact_bwd(case, seed):
+    t = _inputs(case, seed)
+    t["case"] = case
+    M, N, K = case["M"], case["rows"], case["cols"]
+    G, A, B = t["dY"].double(), t["A"].double(), t["B"].double()
+    col = torch.arange(K, device="cuda") // 64
+    x = t["codes"].double() * torch.exp2(t["exps"].double() - 127)[:, col]
+    k = t["alpha"] / (case["r"] * (1 - case["p"]))
+    low = (G @ B) * k
+    if t["mask"] is not None:
+        n = torch.arange(M * K, device="cuda")
+        kept = ((t["mask"][n >> 3].int() >> (n & 7).int()) & 1).view(M, K).double()
+        x = x * kept
+    out = dict(dA=torch.matmul(low.t(), x), dB=torch.matmul(G.t(), t["u"].double()) * k)
+    if case["dx"]:
+        share = torch.matmul(low, A)
+        out["dX"] = torch.matmul(G, _dequantized(t, torch.float64)) + (
+            share if t["mask"] is None else share * kept)
+    return out
+
+
+def _exact_lp(case, seed):
+    t = _inputs(case, seed)
+    x = t["logits"].double()
+    bwd = case["op"] == "lp_bwd"
+    c = t["scale"]
+    lse = torch.logsumexp(x * c, dim=1, keepdim=True)
+    logp = x * c - lse
+    p = logp.exp()
+    plogp = torch.where(p > 0, p * logp, torch.zeros_like(p))
+    H = -plogp.sum(dim=1)
+    valid = t["targets"] >= 0
+    at = torch.where(valid, t["targets"], torch.zeros_like(t["targets"])).unsqueeze(1)
+    if not bwd:
+        got = torch.where(valid, logp.gather(1, at).squeeze(1), torch.zeros_like(H))
+        out = dict(logp=got, entropy=H)
+        if case["k"]:
+            out["top_ids"] = None
+            out["top_logp"] = logp.topk(case["k"], dim=1).values
+        return out
+    # d logp_t = onehot - p, d H = -p (log p + H)
+    g = torch.where(valid, t["dlogp"].double(), torch.zeros_like(H)).unsqueeze(1)
+    dx = -(g * p)
+    dx.scatter_add_(1, at, g)
+    if t["dentropy"] is not None:
+        dx -= t["dentropy"].double().unsqueeze(1) * (plogp + p * H.unsqueeze(1))
+    return dx * c
+
+
+def exact(case, seed):
+    op = case["op"]
+    if op in ("norm_fwd", "norm_bwd"):
+        return _exact_norm(case, seed)
+    return {"act8_store": _exact_store, "act8_bwd": _exact_bwd}.get(op, _exact_lp)(case, seed)
