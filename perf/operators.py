@@ -128,14 +128,15 @@ class _Draw:
 
 def _encode(x):
     """Codes and exponent bytes of a bf16 or fp32 matrix in blocks of 64
-    columns: the smallest power of two 2^e with absmax <= 127 2^e, e >= -126."""
+    columns: the smallest power of two 2^e with absmax <= 127 2^e, -126 <= e
+    <= 121 (where bf16 ends: held to 127)."""
     M, D = x.shape
     nb = (D + BLOCK - 1) // BLOCK
     v = torch.nn.functional.pad(x.float(), (0, nb * BLOCK - D)).view(M, nb, BLOCK)
     mant, ex = torch.frexp(v.abs().amax(dim=2))  # absmax = mant 2^ex, mant in [0.5, 1)
-    e = (ex - 7 + (mant > 127 / 128).to(ex.dtype)).clamp(min=-126)
+    e = (ex - 7 + (mant > 127 / 128).to(ex.dtype)).clamp(-126, 121)
     e = torch.where(mant == 0, torch.full_like(e, -126), e)
-    codes = torch.round(torch.ldexp(v, -e.unsqueeze(2))).to(torch.int8)
+    codes = torch.round(torch.ldexp(v, -e.unsqueeze(2))).clamp(-127, 127).to(torch.int8)
     return codes.view(M, nb * BLOCK)[:, :D].contiguous(), (e + 127).to(torch.uint8)
 
 
@@ -175,7 +176,7 @@ def _inputs(case, seed):
         if case["post"] == "norm":
             t["w_post"] = d.normal(D, std=0.2, mean=1.0, dtype=wt)
         if case["gate"] != "none":
-            shape, kind = {"channel": ((D,), wt), "row": ((M,), bf), "element": ((M, D), bf)}[
+            shape, kind = {"channel": ((D,), wt), "row": ((M, 1), bf), "element": ((M, D), bf)}[
                 case["gate"]]
             t["gate"] = d.normal(*shape, std=0.3, mean=0.7, dtype=kind)
         if op == "norm_bwd":
@@ -241,10 +242,7 @@ def _branch(s, o):
     p = o
     if s["w_post"] is not None:
         p = o * torch.rsqrt(o.square().mean(dim=1, keepdim=True) + s["eps"]) * s["w_post"].float()
-    g = None if s["gate"] is None else s["gate"].float()
-    if s["case"]["gate"] == "row":
-        g = g[:, None]
-    return p, g
+    return p, None if s["gate"] is None else s["gate"].float()
 
 
 def _plain_norm_fwd(s):
@@ -275,7 +273,8 @@ def _plain_norm_bwd(s):
     a = s["scale"] * dh
     if g is not None:
         dg = a * p
-        out["dgate"] = {"channel": lambda: dg.sum(dim=0), "row": lambda: dg.sum(dim=1),
+        out["dgate"] = {"channel": lambda: dg.sum(dim=0),
+                        "row": lambda: dg.sum(dim=1, keepdim=True),
                         "element": lambda: dg.to(torch.bfloat16)}[s["case"]["gate"]]()
         a = a * g
     if s["w_post"] is not None:
@@ -489,7 +488,7 @@ def _exact_norm(case, seed):
     if o is not None:
         add = o if w1 is None else rms(o) * w1
         if g is not None:
-            add = add * (g.unsqueeze(1) if g.dim() == 1 and case["gate"] == "row" else g)
+            add = add * g
         add = add * t["scale"]
     if not bwd:
         new = h + add
