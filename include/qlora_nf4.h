@@ -323,6 +323,134 @@ qn_status lora_linear_bf16(const uint16_t* x, int64_t M, const uint16_t* W, int6
                            int64_t cols, const float* V, const uint16_t* L, int r, float alpha,
                            uint16_t* y, void* stream);
 
+/* ---- Around the linear in a fine-tuning step (and in serving the tuned
+ * model).  None of these calls uses arrival counters: their workspaces need
+ * no clearing. ---- */
+
+/* Activation checkpoints in 8 bits.  An activation x [M, cols] bf16 is kept
+ * for the backward as
+ *   codes int8  [M, cols]              c
+ *   exps  uint8 [M, ceil(cols / 64)]   E, one for every 64 columns of a row
+ *                                      (a row's last block may be shorter)
+ * with x~ = c 2^(E-127): E - 127 is the smallest e in -126 .. 121 with
+ * max|x| <= 127 2^e over the block (121 where there is none: the largest
+ * finite bf16), c = x 2^-e rounded to the nearest whole number (ties to even)
+ * and held to -127 .. 127.  A power-of-two scale makes every x~ a bf16 number
+ * exactly, so the products of the backward take it without another rounding;
+ * |x - x~| <= 2^(e-1), at most 1/127 of the block's largest magnitude.  A block
+ * that holds a NaN or an infinity gets E = 255 and reads back as NaN. */
+#define QN_ACT8_BLOCK 64
+typedef struct {
+  const int8_t* codes; /* [M, cols] device, 16-byte aligned */
+  const uint8_t* exps; /* [M, ceil(cols / 64)] device, 16-byte aligned */
+} qn_act8;
+
+/* x [M, cols] bf16 -> codes, exps.  M >= 0, 1 <= cols <= 2^20. */
+qn_status act8_pack(const uint16_t* x, int64_t M, int64_t cols, int8_t* codes, uint8_t* exps,
+                    void* stream);
+
+/* codes, exps -> x~ [M, cols] bf16. */
+qn_status act8_unpack(const qn_act8* x8, int64_t M, int64_t cols, uint16_t* out, void* stream);
+
+/* Workspace bytes of qlora_linear_bwd_act8. */
+size_t qlora_linear_bwd_act8_workspace(int64_t M, int64_t rows, int64_t cols, int r, int need_dx);
+
+/* qlora_linear_bwd_ex with the forward's input kept as an 8-bit checkpoint:
+ *   dX = G Qhat(W) + s (G B) A   (skipped if dX == NULL),
+ *   dA = s (G B)^T x~,  dB = s G^T u.
+ * u (required) is the forward's u_out, formed there from the x that was
+ * packed; x itself is read for dA only.  Under dropout (opts) the mask is
+ * applied to x~ and to the branch's share of dX.  Shape rules and outputs as
+ * qlora_linear_bwd; M == 0 writes zero dA and dB. */
+qn_status qlora_linear_bwd_act8(const qn_nf4dq* w, const qn_act8* x8, const uint16_t* dY,
+                                int64_t M, const uint16_t* A, const uint16_t* B, int r,
+                                float alpha, const qn_lora_opts* opts, const float* u,
+                                uint16_t* dX, float* dA, float* dB, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* Norms before and after a block, fused with its gate and residual scale.
+ * With h [M, D] the residual stream and o [M, D] bf16 the block's output:
+ *   p  = o                                   (w_post == NULL)
+ *   p  = o / sqrt(mean(o^2) + eps) * w_post  (post norm)
+ *   h' = h + scale * gate * p                (o == NULL: h' = h, not written)
+ *   y  = h' / sqrt(mean(h'^2) + eps) * w_pre
+ * means over a row's D values; y is the next block's input.  h and h' are
+ * res_dtype (QN_BF16 or QN_F32); y is formed from h' before its rounding.
+ * w_pre, w_post [D] and a channel gate are w_dtype (QN_BF16 or QN_F32), row
+ * and element gates bf16.  Sums and all arithmetic are fp32. */
+enum {
+  QN_GATE_NONE = 0,    /* gate == NULL */
+  QN_GATE_CHANNEL = 1, /* gate [D]     */
+  QN_GATE_ROW = 2,     /* gate [M]     */
+  QN_GATE_ELEMENT = 3  /* gate [M, D]  */
+};
+#define QN_NORM_MAX_COLS 32768
+typedef struct {
+  int64_t M, D;       /* M >= 0, 1 <= D <= QN_NORM_MAX_COLS */
+  const void* w_pre;  /* [D] */
+  const void* w_post; /* [D] or NULL */
+  const void* gate;   /* by gate_kind, or NULL */
+  int32_t res_dtype, w_dtype, gate_kind;
+  float scale, eps;   /* finite; eps > 0 */
+} qn_block_norm;
+
+/* h_new and y are written; with codes and exps (both or neither) also y's
+ * 8-bit checkpoint (the same as act8_pack of y).  o == NULL (the first norm of
+ * a model): only y, and w_post, gate and h_new must be NULL.  Outputs must not
+ * overlap inputs. */
+qn_status block_norm_fwd(const qn_block_norm* n, const void* h, const uint16_t* o, void* h_new,
+                         uint16_t* y, int8_t* codes, uint8_t* exps, void* stream);
+
+/* Workspace bytes of block_norm_bwd (0 when neither weight gradients nor a
+ * channel gate's gradient are wanted). */
+size_t block_norm_bwd_workspace(const qn_block_norm* n, int need_weights, int need_gate);
+
+/* Gradients, from dy [M, D] bf16 and dh_new [M, D] res_dtype (nullable: zero)
+ * of y and h', with the saved h_new (h itself when o == NULL) and o:
+ *   dh [M, D] res_dtype, dout [M, D] bf16 (NULL exactly when o is),
+ *   dgate (nullable): fp32 [D] or [M], or bf16 [M, D], by gate_kind,
+ *   dw_post, dw_pre (nullable) fp32 [D].
+ * The norms' statistics are formed again from h_new and o.  M == 0 writes
+ * zeros to the [D] gradients.  Sums over rows are taken in a fixed order. */
+qn_status block_norm_bwd(const qn_block_norm* n, const uint16_t* dy, const void* dh_new,
+                         const void* h_new, const uint16_t* o, void* dh, uint16_t* dout,
+                         void* dgate, float* dw_post, float* dw_pre, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Log probabilities of given tokens, with entropy and top alternatives.
+ * logits [T, V] (QN_BF16 or QN_F32; row stride ld >= V elements, element
+ * aligned), scale > 0 (an inverse temperature).  With m = max_i x_i and
+ * p_i = exp(scale (x_i - m)) / S:
+ *   logp    [T] = scale (x_t - m) - ln S, t = targets[row] (nullable pair)
+ *   entropy [T] = - sum_i p_i ln p_i
+ *   stats   [T, 2] = (m, ln S), for the backward
+ *   top_logp, top_ids [T, top_k]: the top_k largest logits in descending
+ *     order, ties to the lower index, as log probabilities (top_k <= 32,
+ *     top_k <= V; 0: both NULL).
+ * A logit of -inf (a banned token) has probability 0 and is no alternative;
+ * missing alternatives are (-inf, -1).  A row of -inf only has logp -inf,
+ * entropy 0, stats (lowest fp32, -inf).  A negative target is ignored: logp
+ * 0.  A target >= V reads nothing: logp NaN.  A row with a NaN or +inf has
+ * NaN logp and entropy. */
+#define QN_LOGPROB_MAX_TOP 32
+size_t token_logprobs_workspace(int64_t T, int64_t V, qn_dtype dtype, int top_k);
+qn_status token_logprobs_fwd(const void* logits, qn_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                             const int64_t* targets, float scale, int top_k, float* logp,
+                             float* entropy, float* stats, float* top_logp, int32_t* top_ids,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient with respect to the logits, from dlogp [T] (nullable, needs
+ * targets) and dentropy [T] (nullable, needs entropy), not both NULL, and the
+ * forward's stats and entropy:
+ *   dlogits [T, V] = scale (dlogp (1[i = t] - p_i) - dentropy p_i (ln p_i + H))
+ * in the logits' type, row stride ldd >= V.  Targets outside 0 .. V-1 take no
+ * part (dlogp counts as 0); rows of -inf only get zeros.  dlogits may be
+ * logits itself (same ld). */
+qn_status token_logprobs_bwd(const void* logits, qn_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                             const int64_t* targets, float scale, const float* stats,
+                             const float* entropy, const float* dlogp, const float* dentropy,
+                             void* dlogits, int64_t ldd, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

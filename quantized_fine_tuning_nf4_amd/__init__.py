@@ -31,7 +31,10 @@ EXPORTS = ["qn_abi_version", "qn_status_str", "qn_nf4_codebook", "nf4_quantize_d
            "qlora_linear_bwd", "lora_linear_bf16", "qlora_linear_route",
            "qlora_linear_fwd_noalloc", "nf4_merge_lora", "qlora_linear_workspace_ex",
            "qlora_linear_fwd_ex", "qlora_linear_bwd_ex", "qn_quantize",
-           "qlora_linear_workspace_state", "qn_fp4_codebook", "adamw8_step"]
+           "qlora_linear_workspace_state", "qn_fp4_codebook", "adamw8_step", "act8_pack",
+           "act8_unpack", "qlora_linear_bwd_act8_workspace", "qlora_linear_bwd_act8",
+           "block_norm_fwd", "block_norm_bwd_workspace", "block_norm_bwd",
+           "token_logprobs_workspace", "token_logprobs_fwd", "token_logprobs_bwd"]
 ROUTES = {1: "decode_rows", 2: "decode_tiles", 3: "decode_split", 4: "fused_small", 5: "fused",
           6: "dense"}
 
@@ -58,6 +61,17 @@ class _NF4DQ(ctypes.Structure):
                 ("scale2", ctypes.c_void_p), ("offset", ctypes.c_void_p),
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
                 ("absmax", ctypes.c_void_p), ("codebook", ctypes.c_int32)]
+
+
+class _Act8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("exps", ctypes.c_void_p)]
+
+
+class _BlockNorm(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("D", ctypes.c_int64), ("w_pre", ctypes.c_void_p),
+                ("w_post", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("res_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("gate_kind", ctypes.c_int32), ("scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 CODEBOOKS = {"nf4": 0, "fp4": 1}
@@ -121,6 +135,23 @@ def load_library(path: str = LIB_PATH):
     L.nf4_merge_lora.restype = ctypes.c_int
     L.qlora_linear_route.argtypes = [I64, I64, I64, ctypes.c_int, ctypes.c_int]
     L.qlora_linear_route.restype = ctypes.c_int
+    I32, F32 = ctypes.c_int, ctypes.c_float
+    A8, BN = ctypes.POINTER(_Act8), ctypes.POINTER(_BlockNorm)
+    for name, res, args in [
+            ("act8_pack", I32, [P, I64, I64, P, P, P]),
+            ("act8_unpack", I32, [A8, I64, I64, P, P]),
+            ("qlora_linear_bwd_act8_workspace", SZ, [I64, I64, I64, I32, I32]),
+            ("qlora_linear_bwd_act8", I32, [ctypes.POINTER(_NF4DQ), A8, P, I64, P, P, I32, F32, OP,
+                                            P, P, P, P, P, SZ, P]),
+            ("block_norm_fwd", I32, [BN, P, P, P, P, P, P, P]),
+            ("block_norm_bwd_workspace", SZ, [BN, I32, I32]),
+            ("block_norm_bwd", I32, [BN, P, P, P, P, P, P, P, P, P, P, SZ, P]),
+            ("token_logprobs_workspace", SZ, [I64, I64, I32, I32]),
+            ("token_logprobs_fwd", I32, [P, I32, I64, I64, I64, P, F32, I32, P, P, P, P, P, P, SZ,
+                                         P]),
+            ("token_logprobs_bwd", I32, [P, I32, I64, I64, I64, P, F32, P, P, P, P, P, I64, P])]:
+        f = getattr(L, name)
+        f.restype, f.argtypes = res, args
     _lib = L
     return L
 
@@ -485,16 +516,42 @@ class _QLoRAFn(torch.autograd.Function):
         return dX, dA.to(A.dtype), dB.to(B.dtype), None, None, None, None, None
 
 
+class _QLoRAAct8Fn(torch.autograd.Function):
+    """_QLoRAFn that keeps x for the backward as an 8-bit checkpoint."""
+
+    @staticmethod
+    def forward(ctx, x, A, B, st, alpha, rslora, mask, p, x8):
+        y, u = qlora_linear_fwd(st, x, A, B, alpha, rslora=rslora, dropout_mask=mask,
+                                dropout_p=p)
+        if x8 is None:
+            x8 = act8_pack(x)
+        ctx.save_for_backward(x8.codes, x8.exps, A, B, u, mask)
+        ctx.st, ctx.alpha, ctx.rslora, ctx.p = st, alpha, rslora, p
+        return y
+
+    @staticmethod
+    def backward(ctx, dY):
+        codes, exps, A, B, u, mask = ctx.saved_tensors
+        dX, dA, dB = qlora_linear_bwd_act8(ctx.st, Act8(codes, exps), dY.contiguous(), A, B,
+                                           ctx.alpha, u, need_dx=ctx.needs_input_grad[0],
+                                           rslora=ctx.rslora, dropout_mask=mask, dropout_p=ctx.p)
+        return dX, dA.to(A.dtype), dB.to(B.dtype), None, None, None, None, None, None
+
+
 class QLoRALinear(torch.nn.Module):
     """Frozen NF4+DQ base weight with a rank-r adapter: y = x Qhat(W)^T +
     s x A^T B^T, s = alpha/r (alpha/sqrt(r) with rslora), and dropout with
     probability `dropout` on the adapter branch's input in training mode.
     A: (r, d_in), B: (d_out, r), bf16 (B starts at zero, A Kaiming-uniform,
-    as in the course notebook's LoRALinear)."""
+    as in the course notebook's LoRALinear).  act8: what the backward needs
+    of x is kept as an 8-bit checkpoint instead of x itself; forward's x8
+    passes one that is at hand already (BlockNorm makes it, and the linears
+    that share an input share it)."""
 
     def __init__(self, weight: torch.Tensor, r: int = 16, alpha: float = 32.0,
-                 dropout: float = 0.0, rslora: bool = False):
+                 dropout: float = 0.0, rslora: bool = False, act8: bool = False):
         super().__init__()
+        self.act8 = bool(act8)
         d_out, d_in = weight.shape
         self.st = nf4_quantize_dq(weight.detach().float().contiguous())
         self.r, self.alpha, self.dropout, self.rslora = r, alpha, float(dropout), bool(rslora)
@@ -504,11 +561,22 @@ class QLoRALinear(torch.nn.Module):
         self.lora_B = torch.nn.Parameter(torch.zeros(d_out, r, dtype=torch.bfloat16,
                                                      device=weight.device))
 
-    def forward(self, x):
+    def forward(self, x, x8=None):
+        if x8 is not None and not self.act8:
+            raise ValueError("x8 is for a layer with act8=True")
         shp = x.shape
         x2 = x.reshape(-1, shp[-1]).contiguous()
         p = self.dropout if self.training else 0.0
         mask = dropout_mask(x2.shape[0], x2.shape[1], p, x2.device) if p > 0 else None
-        y = _QLoRAFn.apply(x2, self.lora_A, self.lora_B, self.st, self.alpha, self.rslora, mask,
-                           p)
+        if self.act8:
+            y = _QLoRAAct8Fn.apply(x2, self.lora_A, self.lora_B, self.st, self.alpha, self.rslora,
+                                   mask, p, x8)
+        else:
+            y = _QLoRAFn.apply(x2, self.lora_A, self.lora_B, self.st, self.alpha, self.rslora,
+                               mask, p)
         return y.reshape(*shp[:-1], y.shape[-1])
+
+
+from .finetune import (Act8, BlockNorm, BlockNormGrads, TokenLogprobs, act8_pack,  # noqa: E402
+                       act8_unpack, block_norm_bwd, block_norm_fwd, qlora_linear_bwd_act8,
+                       token_logprobs, token_logprobs_bwd, token_logprobs_fwd)

@@ -166,9 +166,11 @@ struct BwdWs {
   uint16_t* wt;   // [cols, ldt] bf16 Qhat(W)^T (dense path)
   int64_t ldt;
   uint16_t* At;   // [cols, r] A^T (dense path)
+  uint16_t* x;    // [M, cols] the 8-bit checkpoint's values (act8)
 };
 
-BwdWs carve_bwd(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool need_u) {
+BwdWs carve_bwd(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool need_u,
+                bool act8 = false) {
   BwdWs b;
   b.arrivals = c.take<unsigned>(kArrivalWords);
   if (need_u) {
@@ -192,6 +194,7 @@ BwdWs carve_bwd(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool ne
   const bool dense = M > 0 && dense_path(M, cols);
   b.wt = dense ? c.take<uint16_t>((size_t)cols * b.ldt) : nullptr;
   b.At = dense ? c.take<uint16_t>((size_t)cols * r) : nullptr;
+  b.x = act8 ? c.take<uint16_t>((size_t)M * cols) : nullptr;
   return b;
 }
 
@@ -273,6 +276,152 @@ qn_status forward(const qn_nf4dq* w, const uint16_t* x, int64_t M, const uint16_
   } else if (e == hipSuccess) {
     e = launch_qgemm_fwd(to_state(w), x, M, u, B, r, scale, y, st);
   }
+  return from_hip(e);
+}
+
+qn_status check_act8_shape(int64_t M, int64_t cols) {
+  if (M < 0 || M > kMaxRowsM || cols < 1 || cols > kMaxDim) return QN_EINVAL;
+  return QN_OK;
+}
+
+qn_status check_norm(const qn_block_norm* n, BlockNorm* out) {
+  if (!n || n->M < 0 || n->M > kMaxRowsM || n->D < 1 || n->D > QN_NORM_MAX_COLS) return QN_EINVAL;
+  if (n->res_dtype != QN_F32 && n->res_dtype != QN_BF16) return QN_EINVAL;
+  if (n->w_dtype != QN_F32 && n->w_dtype != QN_BF16) return QN_EINVAL;
+  if (n->gate_kind < QN_GATE_NONE || n->gate_kind > QN_GATE_ELEMENT) return QN_EINVAL;
+  if (!std::isfinite(n->scale) || !std::isfinite(n->eps) || !(n->eps > 0.f)) return QN_EINVAL;
+  if (!n->w_pre) return QN_EINVAL;
+  // no element gate has storage for an empty batch
+  if ((n->gate_kind == QN_GATE_NONE) != (n->gate == nullptr) && n->M > 0) return QN_EINVAL;
+  if (!aligned16(n->w_pre) || !aligned16(n->w_post) || !aligned16(n->gate)) return QN_EALIGN;
+  *out = BlockNorm{n->M, n->D, n->w_pre, n->w_post, n->gate, n->res_dtype == QN_F32,
+                   n->w_dtype == QN_F32, n->gate_kind, n->scale, n->eps};
+  return QN_OK;
+}
+
+// Logits rows are addressed from their own start (64-bit), elements of a row
+// by 32-bit numbers.
+constexpr int64_t kMaxVocab = (int64_t)1 << 28;
+constexpr int64_t kMaxLd = (int64_t)1 << 40;
+qn_status check_logits(const void* x, qn_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                       float scale) {
+  if (dtype != QN_F32 && dtype != QN_BF16) return QN_EINVAL;
+  if (T < 0 || T > kMaxRowsM || V < 1 || V > kMaxVocab || ld < V || ld > kMaxLd) return QN_EINVAL;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return QN_EINVAL;
+  if (T == 0) return QN_OK;
+  if (!x) return QN_EINVAL;
+  if (reinterpret_cast<uintptr_t>(x) & (dtype == QN_F32 ? 3u : 1u)) return QN_EALIGN;
+  return QN_OK;
+}
+
+// The backward; the forward's input comes as x (bf16) or as x8 (an 8-bit
+// checkpoint, with u_saved).
+qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, const uint16_t* dY,
+                   int64_t M, const uint16_t* A, const uint16_t* B, int r, float alpha,
+                   const qn_lora_opts* opts, const float* u_saved, uint16_t* dX, float* dA,
+                   float* dB, void* workspace, size_t workspace_bytes, void* stream) {
+  qn_status s = check_linear(w, M, r);
+  if (s != QN_OK) return s;
+  Lora lo;
+  s = lora_options(opts, alpha, r, &lo);
+  if (s != QN_OK) return s;
+  const bool drop = lo.mask != nullptr;
+  if (!A || !B || !dA || !dB) return QN_EINVAL;
+  if (M > 0 && !dY) return QN_EINVAL;
+  if (M > 0 && (x8 ? (!x8->codes || !x8->exps || !u_saved) : !x)) return QN_EINVAL;
+  if (x8 && (!aligned16(x8->codes) || !aligned16(x8->exps))) return QN_EALIGN;
+  if (!aligned16(x) || !aligned16(dY) || !aligned16(A) || !aligned16(B) || !aligned16(dA) ||
+      !aligned16(dB) || (dX && !aligned16(dX)) || (u_saved && !aligned16(u_saved)))
+    return QN_EALIGN;
+  const int64_t N = w->rows, K = w->cols;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (M == 0) {
+    // empty batch: the gradients of the adapters are zero
+    hipError_t e = launch_fill_zero(dA, (int64_t)r * K, st);
+    if (e == hipSuccess) e = launch_fill_zero(dB, N * (int64_t)r, st);
+    return from_hip(e);
+  }
+  Carver probe(nullptr);
+  carve_bwd(probe, M, N, K, r, u_saved == nullptr, x8 != nullptr);
+  if (!workspace) return QN_EINVAL;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return QN_EALIGN;
+  if (workspace_bytes < probe.used) return QN_EWORKSPACE;
+  Carver c(workspace);
+  BwdWs b = carve_bwd(c, M, N, K, r, u_saved == nullptr, x8 != nullptr);
+  const float scale = lo.s;
+  hipError_t e = hipSuccess;
+  const float* u = u_saved;
+  if (x8) {
+    e = launch_act8_unpack(x8->codes, x8->exps, M, K, b.x, st);
+    x = b.x;
+  }
+  // an early launch of the call zeroes the arrival counters the adapter
+  // gradients' launch counts on, so the backward never depends on what the
+  // workspace held before
+  Clear clr{b.arrivals, kArrivalWords};
+  if (!u && e == hipSuccess) {
+    e = launch_thin_nt(x, A, M, K, r, b.fu.u, b.fu.upart, b.fu.S, st, true, false, clr, lo.mask);
+    clr = Clear{nullptr, 0};
+    u = b.fu.u;
+  }
+  // v = G B as slices (added below); the product takes B as stored when it
+  // can, else B^T made first
+  const bool b_rows = thin_nt_rows_ok(M, N, r);
+  if (e == hipSuccess && !b_rows) {
+    if (clr.n) {  // (no earlier launch: a kernel, not a memset, for graph capture)
+      e = launch_fill_zero(reinterpret_cast<float*>(clr.p), clr.n, st);
+      clr = Clear{nullptr, 0};
+    }
+    BwdAux t{};
+    t.B = B;
+    t.Bt = b.Bt;
+    t.N = N;
+    t.r = r;
+    e = launch_bwd_aux(t, st);
+  }
+  if (e == hipSuccess)
+    e = launch_thin_nt(dY, b_rows ? B : b.Bt, M, N, r, b.v, b.vpart, b.Sv, st, false, b_rows,
+                       clr);
+  // the small jobs: v's slice sum, (s u)^T and (s v)^T split for the
+  // transposed products, A^T for the dense dX product; in spare workgroups of
+  // the transposed dequantization when there is one
+  const bool dense_dx = dX && b.wt;
+  BwdAux aux{};
+  aux.A = A;
+  aux.At = dense_dx ? b.At : nullptr;
+  aux.K = K;
+  aux.u = u;
+  aux.su = b.su;
+  aux.Mpu = thin_tn_rows_padded(M, N, r);
+  aux.vpart = b.vpart;
+  aux.Sv = b.Sv;
+  aux.v = b.v;
+  aux.sv = b.sv;
+  aux.Mpv = thin_tn_rows_padded(M, K, r);
+  aux.M = M;
+  aux.r = r;
+  aux.s = scale;
+  if (e == hipSuccess) {
+    if (dense_dx)
+      e = launch_dequant_t(w->packed, w->qscale, w->scale2, w->offset, N, K, b.wt, b.ldt, aux,
+                           st, w->codebook, w->absmax);
+    else
+      e = launch_bwd_aux(aux, st);
+  }
+  if (e == hipSuccess && dX) {
+    // under dropout the branch's share is added masked after the base product
+    const float sx = drop ? 0.f : scale;
+    if (dense_dx)
+      e = launch_gemm_nt(dY, N, N, b.wt, b.ldt, M, K, b.v, b.At, r, sx, dX, st);
+    else
+      e = launch_qgemm_dx(to_state(w), dY, M, b.v, A, r, sx, dX, st);
+    if (e == hipSuccess && drop) e = launch_lora_masked_add(dX, b.v, A, lo.mask, M, K, r, scale, st);
+  }
+  // dB = s G^T u and dA = s v^T X in one launch (and their slice sums in one)
+  if (e == hipSuccess)
+    e = launch_thin_tn2(ThinTn{dY, b.su, N, dB, false, b.dBpart},
+                        ThinTn{x, b.sv, K, dA, true, b.dApart, lo.mask}, M, r, b.arrivals,
+                        st);
   return from_hip(e);
 }
 
@@ -470,103 +619,8 @@ qn_status qlora_linear_bwd_ex(const qn_nf4dq* w, const uint16_t* x, const uint16
                               const qn_lora_opts* opts, const float* u_saved, uint16_t* dX,
                               float* dA, float* dB, void* workspace, size_t workspace_bytes,
                               void* stream) {
-  qn_status s = check_linear(w, M, r);
-  if (s != QN_OK) return s;
-  Lora lo;
-  s = lora_options(opts, alpha, r, &lo);
-  if (s != QN_OK) return s;
-  const bool drop = lo.mask != nullptr;
-  if (!A || !B || !dA || !dB) return QN_EINVAL;
-  if (M > 0 && (!x || !dY)) return QN_EINVAL;
-  if (!aligned16(x) || !aligned16(dY) || !aligned16(A) || !aligned16(B) || !aligned16(dA) ||
-      !aligned16(dB) || (dX && !aligned16(dX)) || (u_saved && !aligned16(u_saved)))
-    return QN_EALIGN;
-  const int64_t N = w->rows, K = w->cols;
-  hipStream_t st = static_cast<hipStream_t>(stream);
-  if (M == 0) {
-    // empty batch: the gradients of the adapters are zero
-    hipError_t e = launch_fill_zero(dA, (int64_t)r * K, st);
-    if (e == hipSuccess) e = launch_fill_zero(dB, N * (int64_t)r, st);
-    return from_hip(e);
-  }
-  Carver probe(nullptr);
-  carve_bwd(probe, M, N, K, r, u_saved == nullptr);
-  if (!workspace) return QN_EINVAL;
-  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return QN_EALIGN;
-  if (workspace_bytes < probe.used) return QN_EWORKSPACE;
-  Carver c(workspace);
-  BwdWs b = carve_bwd(c, M, N, K, r, u_saved == nullptr);
-  const float scale = lo.s;
-  hipError_t e = hipSuccess;
-  const float* u = u_saved;
-  // an early launch of the call zeroes the arrival counters the adapter
-  // gradients' launch counts on, so the backward never depends on what the
-  // workspace held before
-  Clear clr{b.arrivals, kArrivalWords};
-  if (!u && e == hipSuccess) {
-    e = launch_thin_nt(x, A, M, K, r, b.fu.u, b.fu.upart, b.fu.S, st, true, false, clr, lo.mask);
-    clr = Clear{nullptr, 0};
-    u = b.fu.u;
-  }
-  // v = G B as slices (added below); the product takes B as stored when it
-  // can, else B^T made first
-  const bool b_rows = thin_nt_rows_ok(M, N, r);
-  if (e == hipSuccess && !b_rows) {
-    if (clr.n) {  // (no earlier launch: a kernel, not a memset, for graph capture)
-      e = launch_fill_zero(reinterpret_cast<float*>(clr.p), clr.n, st);
-      clr = Clear{nullptr, 0};
-    }
-    BwdAux t{};
-    t.B = B;
-    t.Bt = b.Bt;
-    t.N = N;
-    t.r = r;
-    e = launch_bwd_aux(t, st);
-  }
-  if (e == hipSuccess)
-    e = launch_thin_nt(dY, b_rows ? B : b.Bt, M, N, r, b.v, b.vpart, b.Sv, st, false, b_rows,
-                       clr);
-  // the small jobs: v's slice sum, (s u)^T and (s v)^T split for the
-  // transposed products, A^T for the dense dX product; in spare workgroups of
-  // the transposed dequantization when there is one
-  const bool dense_dx = dX && b.wt;
-  BwdAux aux{};
-  aux.A = A;
-  aux.At = dense_dx ? b.At : nullptr;
-  aux.K = K;
-  aux.u = u;
-  aux.su = b.su;
-  aux.Mpu = thin_tn_rows_padded(M, N, r);
-  aux.vpart = b.vpart;
-  aux.Sv = b.Sv;
-  aux.v = b.v;
-  aux.sv = b.sv;
-  aux.Mpv = thin_tn_rows_padded(M, K, r);
-  aux.M = M;
-  aux.r = r;
-  aux.s = scale;
-  if (e == hipSuccess) {
-    if (dense_dx)
-      e = launch_dequant_t(w->packed, w->qscale, w->scale2, w->offset, N, K, b.wt, b.ldt, aux,
-                           st, w->codebook, w->absmax);
-    else
-      e = launch_bwd_aux(aux, st);
-  }
-  if (e == hipSuccess && dX) {
-    // under dropout the branch's share is added masked after the base product
-    const float sx = drop ? 0.f : scale;
-    if (dense_dx)
-      e = launch_gemm_nt(dY, N, N, b.wt, b.ldt, M, K, b.v, b.At, r, sx, dX, st);
-    else
-      e = launch_qgemm_dx(to_state(w), dY, M, b.v, A, r, sx, dX, st);
-    if (e == hipSuccess && drop) e = launch_lora_masked_add(dX, b.v, A, lo.mask, M, K, r, scale, st);
-  }
-  // dB = s G^T u and dA = s v^T X in one launch (and their slice sums in one)
-  if (e == hipSuccess)
-    e = launch_thin_tn2(ThinTn{dY, b.su, N, dB, false, b.dBpart},
-                        ThinTn{x, b.sv, K, dA, true, b.dApart, lo.mask}, M, r, b.arrivals,
-                        st);
-  return from_hip(e);
+  return backward(w, x, nullptr, dY, M, A, B, r, alpha, opts, u_saved, dX, dA, dB, workspace,
+                  workspace_bytes, stream);
 }
 
 qn_status nf4_merge_lora(const qn_nf4dq* w, const uint16_t* A, const uint16_t* B, int r,
@@ -631,6 +685,153 @@ qn_status lora_linear_bf16(const uint16_t* x, int64_t M, const uint16_t* W, int6
     return QN_EALIGN;
   return from_hip(launch_gemm_nt(x, cols, cols, W, cols, M, rows, V, L, r, alpha / (float)r, y,
                                  static_cast<hipStream_t>(stream)));
+}
+
+qn_status act8_pack(const uint16_t* x, int64_t M, int64_t cols, int8_t* codes, uint8_t* exps,
+                    void* stream) {
+  qn_status s = check_act8_shape(M, cols);
+  if (s != QN_OK || M == 0) return s;
+  if (!x || !codes || !exps) return QN_EINVAL;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(exps)) return QN_EALIGN;
+  return from_hip(launch_act8_pack(x, M, cols, codes, exps, static_cast<hipStream_t>(stream)));
+}
+
+qn_status act8_unpack(const qn_act8* x8, int64_t M, int64_t cols, uint16_t* out, void* stream) {
+  qn_status s = check_act8_shape(M, cols);
+  if (s != QN_OK || M == 0) return s;
+  if (!x8 || !x8->codes || !x8->exps || !out) return QN_EINVAL;
+  if (!aligned16(x8->codes) || !aligned16(x8->exps) || !aligned16(out)) return QN_EALIGN;
+  return from_hip(launch_act8_unpack(x8->codes, x8->exps, M, cols, out,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+size_t qlora_linear_bwd_act8_workspace(int64_t M, int64_t rows, int64_t cols, int r, int need_dx) {
+  (void)need_dx;
+  if (M < 0 || rows < 1 || cols < 1 || r < 1 || r > 64) return 0;
+  Carver c(nullptr);
+  carve_bwd(c, M, rows, cols, r, false, true);
+  return c.used;
+}
+
+qn_status qlora_linear_bwd_act8(const qn_nf4dq* w, const qn_act8* x8, const uint16_t* dY,
+                                int64_t M, const uint16_t* A, const uint16_t* B, int r,
+                                float alpha, const qn_lora_opts* opts, const float* u,
+                                uint16_t* dX, float* dA, float* dB, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  if (!x8 && M != 0) return QN_EINVAL;
+  return backward(w, nullptr, x8, dY, M, A, B, r, alpha, opts, u, dX, dA, dB, workspace,
+                  workspace_bytes, stream);
+}
+
+qn_status block_norm_fwd(const qn_block_norm* n, const void* h, const uint16_t* o, void* h_new,
+                         uint16_t* y, int8_t* codes, uint8_t* exps, void* stream) {
+  BlockNorm b;
+  qn_status s = check_norm(n, &b);
+  if (s != QN_OK) return s;
+  if ((codes == nullptr) != (exps == nullptr)) return QN_EINVAL;
+  if (n->M == 0) return QN_OK;
+  if (!o && (n->w_post || n->gate || h_new)) return QN_EINVAL;
+  if (!h || !y || (o && !h_new)) return QN_EINVAL;
+  if (!aligned16(h) || !aligned16(o) || !aligned16(h_new) || !aligned16(y) || !aligned16(codes) ||
+      !aligned16(exps))
+    return QN_EALIGN;
+  return from_hip(launch_block_norm_fwd(b, h, o, h_new, y, codes, exps,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+size_t block_norm_bwd_workspace(const qn_block_norm* n, int need_weights, int need_gate) {
+  if (!n || n->M < 0 || n->D < 1 || n->D > QN_NORM_MAX_COLS) return 0;
+  if (!need_weights && !(need_gate && n->gate_kind == QN_GATE_CHANNEL)) return 0;
+  Carver c(nullptr);
+  c.take<float>((size_t)block_norm_slices(n->M, n->D) * 3 * n->D);
+  return c.used;
+}
+
+qn_status block_norm_bwd(const qn_block_norm* n, const uint16_t* dy, const void* dh_new,
+                         const void* h_new, const uint16_t* o, void* dh, uint16_t* dout,
+                         void* dgate, float* dw_post, float* dw_pre, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  BlockNorm b;
+  qn_status s = check_norm(n, &b);
+  if (s != QN_OK) return s;
+  if ((o == nullptr) != (dout == nullptr) && n->M > 0) return QN_EINVAL;
+  if (n->M > 0 && !o && (n->w_post || n->gate)) return QN_EINVAL;
+  if ((dw_post && !n->w_post) || (dgate && !n->gate)) return QN_EINVAL;
+  if (n->M > 0 && (!dy || !h_new || !dh)) return QN_EINVAL;
+  if (!aligned16(dy) || !aligned16(dh_new) || !aligned16(h_new) || !aligned16(o) ||
+      !aligned16(dh) || !aligned16(dout) || !aligned16(dgate) || !aligned16(dw_post) ||
+      !aligned16(dw_pre))
+    return QN_EALIGN;
+  const bool chan = dgate && n->gate_kind == QN_GATE_CHANNEL;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (n->M == 0) {  // sums over no rows
+    hipError_t e = hipSuccess;
+    if (dw_pre) e = launch_fill_zero(dw_pre, n->D, st);
+    if (e == hipSuccess && dw_post) e = launch_fill_zero(dw_post, n->D, st);
+    if (e == hipSuccess && chan) e = launch_fill_zero(static_cast<float*>(dgate), n->D, st);
+    return from_hip(e);
+  }
+  float* part = nullptr;
+  if (dw_pre || dw_post || chan) {
+    if (!workspace) return QN_EINVAL;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return QN_EALIGN;
+    if (workspace_bytes < block_norm_bwd_workspace(n, dw_pre || dw_post, chan)) return QN_EWORKSPACE;
+    Carver c(workspace);
+    part = c.take<float>((size_t)block_norm_slices(n->M, n->D) * 3 * n->D);
+  }
+  return from_hip(launch_block_norm_bwd(b, dy, dh_new, h_new, o, dh, dout, dgate, dw_post, dw_pre,
+                                        part, st));
+}
+
+size_t token_logprobs_workspace(int64_t T, int64_t V, qn_dtype dtype, int top_k) {
+  (void)T;
+  (void)V;
+  (void)dtype;
+  (void)top_k;
+  return 0;
+}
+
+qn_status token_logprobs_fwd(const void* logits, qn_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                             const int64_t* targets, float scale, int top_k, float* logp,
+                             float* entropy, float* stats, float* top_logp, int32_t* top_ids,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  qn_status s = check_logits(logits, dtype, T, V, ld, scale);
+  if (s != QN_OK) return s;
+  if (top_k < 0 || top_k > QN_LOGPROB_MAX_TOP || top_k > V) return QN_EINVAL;
+  if ((targets == nullptr) != (logp == nullptr) && T > 0) return QN_EINVAL;
+  if (T == 0) return QN_OK;
+  if (!entropy || !stats || (top_k > 0 && (!top_logp || !top_ids))) return QN_EINVAL;
+  if (!aligned16(targets) || !aligned16(logp) || !aligned16(entropy) || !aligned16(stats) ||
+      !aligned16(top_logp) || !aligned16(top_ids))
+    return QN_EALIGN;
+  const size_t need = token_logprobs_workspace(T, V, dtype, top_k);
+  if (need > 0) {
+    if (!workspace) return QN_EINVAL;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return QN_EALIGN;
+    if (workspace_bytes < need) return QN_EWORKSPACE;
+  }
+  return from_hip(launch_logprobs_fwd(logits, dtype == QN_F32, T, V, ld, targets, scale, top_k,
+                                      logp, entropy, stats, top_logp, top_ids,
+                                      static_cast<hipStream_t>(stream)));
+}
+
+qn_status token_logprobs_bwd(const void* logits, qn_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                             const int64_t* targets, float scale, const float* stats,
+                             const float* entropy, const float* dlogp, const float* dentropy,
+                             void* dlogits, int64_t ldd, void* stream) {
+  qn_status s = check_logits(logits, dtype, T, V, ld, scale);
+  if (s != QN_OK) return s;
+  if (ldd < V || ldd > kMaxLd) return QN_EINVAL;
+  if (T == 0) return QN_OK;
+  if (!stats || !dlogits || (!dlogp && !dentropy) || (dlogp && !targets) || (dentropy && !entropy))
+    return QN_EINVAL;
+  if (dlogits == logits && ldd != ld) return QN_EINVAL;
+  if (!aligned16(targets) || !aligned16(stats) || !aligned16(entropy) || !aligned16(dlogp) ||
+      !aligned16(dentropy) || (reinterpret_cast<uintptr_t>(dlogits) & (dtype == QN_F32 ? 3u : 1u)))
+    return QN_EALIGN;
+  return from_hip(launch_logprobs_bwd(logits, dtype == QN_F32, T, V, ld, targets, scale, stats,
+                                      entropy, dlogp, dentropy, dlogits, ldd,
+                                      static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -117,4 +117,44 @@ struct ScaleSrc {
   const float* absmax;
 };
 
+// 8-bit activation checkpoints: 64 columns of a row share the scale
+// 2^(E-127); E from the block's largest magnitude (its bf16 bits without the
+// sign).  127 = 1.984375 x 2^6 is bf16, so only the significand 255/128 above
+// it needs the next power of two; the largest finite magnitude, 255 x 2^120,
+// has none that bf16 can hold (64 x 2^122 is infinite) and saturates at
+// 127 x 2^121.
+constexpr int kAct8Block = 64;
+constexpr uint32_t kAct8NaN = 255;  // E of a block with a NaN or an infinity
+__device__ __forceinline__ uint32_t act8_exp(uint32_t absmax_bits) {
+  if (absmax_bits >= 0x7f80u) return kAct8NaN;
+  const int e = (int)(absmax_bits >> 7) - 6 + ((absmax_bits & 0x7fu) == 0x7fu ? 1 : 0);
+  return (uint32_t)min(max(e, 1), 248);
+}
+// what a value is multiplied by to become its code, and back
+__device__ __forceinline__ float act8_inv(uint32_t E) {
+  return E == kAct8NaN ? 0.f : as_f32((254u - E) << 23);
+}
+__device__ __forceinline__ float act8_scale(uint32_t E) {
+  return as_f32(E == kAct8NaN ? 0x7fc00000u : E << 23);
+}
+// code of a value (a block's NaN or infinity: whatever, the block reads NaN)
+__device__ __forceinline__ int act8_code(float x, float inv) {
+  return (int)fminf(fmaxf(__builtin_rintf(x * inv), -127.f), 127.f);
+}
+
+// bf16 or fp32 elements as fp32, and back (round to nearest even)
+__device__ __forceinline__ float load_f32(const float* p) { return *p; }
+__device__ __forceinline__ float load_f32(const uint16_t* p) { return as_f32((uint32_t)*p << 16); }
+__device__ __forceinline__ uint16_t to_bf16(float x) {
+  return (uint16_t)(pack_bf16x2(x, 0.f) & 0xffffu);
+}
+__device__ __forceinline__ void store_f32(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store_f32(uint16_t* p, float x) { *p = to_bf16(x); }
+
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) x += __shfl_xor(x, o);
+  return x;
+}
+
 }  // namespace qn

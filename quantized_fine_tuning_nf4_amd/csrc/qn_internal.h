@@ -324,4 +324,39 @@ hipError_t launch_qgemm_fwd(const WState& w, const uint16_t* X, int64_t M, const
 hipError_t launch_qgemm_dx(const WState& w, const uint16_t* G, int64_t M, const float* v,
                            const uint16_t* A, int r, float s, uint16_t* dX, hipStream_t st);
 
+// 8-bit activation checkpoints (format in the header): x [M, K] bf16 ->
+// codes [M, K], exps [M, ceil(K / 64)], and back.
+hipError_t launch_act8_pack(const uint16_t* x, int64_t M, int64_t K, int8_t* codes, uint8_t* exps,
+                            hipStream_t st);
+hipError_t launch_act8_unpack(const int8_t* codes, const uint8_t* exps, int64_t M, int64_t K,
+                              uint16_t* out, hipStream_t st);
+
+// Block norms.  gate_kind: 0 none, 1 channel, 2 row, 3 element.
+struct BlockNorm {
+  int64_t M, D;
+  const void *w_pre, *w_post, *gate;
+  bool res32, w32;
+  int gate_kind;
+  float scale, eps;
+};
+hipError_t launch_block_norm_fwd(const BlockNorm& n, const void* h, const uint16_t* o, void* h_new,
+                                 uint16_t* y, int8_t* codes, uint8_t* exps, hipStream_t st);
+// Row slices whose column sums (dw_pre, dw_post, channel dgate) are added by
+// a second launch; part [slices][sums][D] fp32.
+int block_norm_slices(int64_t M, int64_t D);
+hipError_t launch_block_norm_bwd(const BlockNorm& n, const uint16_t* dy, const void* dh_new,
+                                 const void* h_new, const uint16_t* o, void* dh, uint16_t* dout,
+                                 void* dgate, float* dw_post, float* dw_pre, float* part,
+                                 hipStream_t st);
+
+// Token log probabilities (see the header).
+hipError_t launch_logprobs_fwd(const void* x, bool f32, int64_t T, int64_t V, int64_t ld,
+                               const int64_t* targets, float scale, int k, float* logp,
+                               float* entropy, float* stats, float* top_logp, int32_t* top_ids,
+                               hipStream_t st);
+hipError_t launch_logprobs_bwd(const void* x, bool f32, int64_t T, int64_t V, int64_t ld,
+                               const int64_t* targets, float scale, const float* stats,
+                               const float* entropy, const float* dlogp, const float* dent,
+                               void* dx, int64_t ldd, hipStream_t st);
+
 }  // namespace qn
