@@ -151,10 +151,42 @@ __device__ __forceinline__ uint16_t to_bf16(float x) {
 __device__ __forceinline__ void store_f32(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_f32(uint16_t* p, float x) { *p = to_bf16(x); }
 
+// A lane's value from the lane that DPP control CTRL names (every lane has
+// one for the controls used here).
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xf, 0xf, true);
+}
+constexpr int kDppXor1 = 0xb1, kDppXor2 = 0x4e;              // quad_perm
+constexpr int kDppMirror8 = 0x141, kDppMirror16 = 0x140;     // row_half_mirror, row_mirror
+
+// Reductions over a wave, the result in every lane: within rows of 16 by DPP,
+// across them by the two permlane swaps.  f joins two values.
+template <typename F>
+__device__ __forceinline__ uint32_t reduce_8_lanes(uint32_t x, F f) {
+  x = f(x, dpp<kDppXor1>(x));
+  x = f(x, dpp<kDppXor2>(x));
+  return f(x, dpp<kDppMirror8>(x));
+}
+template <typename F>
+__device__ __forceinline__ uint32_t reduce_wave(uint32_t x, F f) {
+  x = reduce_8_lanes(x, f);
+  x = f(x, dpp<kDppMirror16>(x));
+  auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  x = f(a[0], a[1]);
+  auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  return f(b[0], b[1]);
+}
 __device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) x += __shfl_xor(x, o);
-  return x;
+  return as_f32(reduce_wave(as_u32(x), [](uint32_t a, uint32_t b) {
+    return as_u32(as_f32(a) + as_f32(b));
+  }));
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t x) {
+  return reduce_wave(x, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+__device__ __forceinline__ uint32_t max_of_8_lanes(uint32_t x) {
+  return reduce_8_lanes(x, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 
 }  // namespace qn
