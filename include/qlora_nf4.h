@@ -384,7 +384,7 @@ enum {
   QN_GATE_ROW = 2,     /* gate [M]     */
   QN_GATE_ELEMENT = 3  /* gate [M, D]  */
 };
-#define QN_NORM_MAX_COLS 32768
+#define QN_NORM_MAX_COLS 16384
 typedef struct {
   int64_t M, D;       /* M >= 0, 1 <= D <= QN_NORM_MAX_COLS */
   const void* w_pre;  /* [D] */

@@ -744,6 +744,7 @@ size_t block_norm_bwd_workspace(const qn_block_norm* n, int need_weights, int ne
   if (!need_weights && !(need_gate && n->gate_kind == QN_GATE_CHANNEL)) return 0;
   Carver c(nullptr);
   c.take<float>((size_t)block_norm_slices(n->M, n->D) * 3 * n->D);
+  c.take<float>((size_t)block_norm_stats(n->M, n->D));
   return c.used;
 }
 
@@ -771,16 +772,17 @@ qn_status block_norm_bwd(const qn_block_norm* n, const uint16_t* dy, const void*
     if (e == hipSuccess && chan) e = launch_fill_zero(static_cast<float*>(dgate), n->D, st);
     return from_hip(e);
   }
-  float* part = nullptr;
+  float *part = nullptr, *stats = nullptr;
   if (dw_pre || dw_post || chan) {
     if (!workspace) return QN_EINVAL;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return QN_EALIGN;
     if (workspace_bytes < block_norm_bwd_workspace(n, dw_pre || dw_post, chan)) return QN_EWORKSPACE;
     Carver c(workspace);
     part = c.take<float>((size_t)block_norm_slices(n->M, n->D) * 3 * n->D);
+    stats = c.take<float>((size_t)block_norm_stats(n->M, n->D));
   }
   return from_hip(launch_block_norm_bwd(b, dy, dh_new, h_new, o, dh, dout, dgate, dw_post, dw_pre,
-                                        part, st));
+                                        part, stats, st));
 }
 
 size_t token_logprobs_workspace(int64_t T, int64_t V, qn_dtype dtype, int top_k) {

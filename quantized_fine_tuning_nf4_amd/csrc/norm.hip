@@ -11,8 +11,8 @@
 //
 // Both directions are bound by HBM: a row's values are read once, stay in
 // registers through its two dependent reductions, and leave once.  A row
-// belongs to TPR threads (a wave, or a workgroup of 256 to 1024), each holding
-// NV vectors of 8 values.
+// belongs to TPR threads (a wave, or a workgroup of up to 512), each holding NV
+// vectors of 8 values.
 #include <algorithm>
 #include <type_traits>
 
@@ -30,6 +30,10 @@ struct NormArgs {
   int gate_kind;
   float scale, eps;
 };
+
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(1)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
 enum { kGateNone = 0, kGateChannel = 1, kGateRow = 2, kGateElement = 3 };
 
@@ -53,108 +57,106 @@ struct Raw8<float> {
   __device__ __forceinline__ float get(int j) const { return j < 4 ? a[j & 3] : b[j & 3]; }
 };
 
-// Column of value j of vector v of thread t.  VEC (D a multiple of 8, so that
-// every row starts on 16 bytes): eight neighbours, a 16-byte access; otherwise
-// one column per thread and value, neighbouring threads side by side.
-template <int TPR, bool VEC>
-__device__ __forceinline__ int column(int v, int j, int t) {
-  return VEC ? (v * TPR + t) * 8 + j : (v * 8 + j) * TPR + t;
+// Vector v of thread t holds the columns from here on.  Rows of odd lengths
+// (TAIL: D no multiple of 8) start on any element -- vector accesses need no
+// alignment on this target -- and their last vector is partial.
+template <int TPR>
+__device__ __forceinline__ int column(int v, int t) {
+  return (v * TPR + t) * 8;
 }
 
 // The values are zero past the row's end.
-template <int TPR, bool VEC>
+template <int TPR, bool TAIL>
 __device__ __forceinline__ Raw8<uint16_t> load8(const uint16_t* row, int v, int t, int D) {
   Raw8<uint16_t> r;
-  if constexpr (VEC) {
-    const int c = column<TPR, VEC>(v, 0, t);
-    if (c < D) r.v = *reinterpret_cast<const u32x4*>(row + c);
-  } else {
-    uint32_t x[8];
+  const int c = column<TPR>(v, t);
+  if (TAIL ? c + 8 <= D : c < D) {
+    r.v = *reinterpret_cast<const u32x4_any*>(row + c);
+  } else if (TAIL) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = column<TPR, VEC>(v, j, t);
-      x[j] = c < D ? row[c] : 0u;
-    }
-    r.v = u32x4{x[0] | (x[1] << 16), x[2] | (x[3] << 16), x[4] | (x[5] << 16), x[6] | (x[7] << 16)};
+    for (int j = 0; j < 7; ++j)
+      if (c + j < D) r.v[j >> 1] |= (uint32_t)row[c + j] << (16 * (j & 1));
   }
   return r;
 }
-template <int TPR, bool VEC>
+template <int TPR, bool TAIL>
 __device__ __forceinline__ Raw8<float> load8(const float* row, int v, int t, int D) {
   Raw8<float> r;
-  if constexpr (VEC) {
-    const int c = column<TPR, VEC>(v, 0, t);
-    if (c < D) {
-      r.a = *reinterpret_cast<const f32x4*>(row + c);
-      r.b = *reinterpret_cast<const f32x4*>(row + c + 4);
-    }
-  } else {
+  const int c = column<TPR>(v, t);
+  if (TAIL ? c + 8 <= D : c < D) {
+    r.a = *reinterpret_cast<const f32x4_any*>(row + c);
+    r.b = *reinterpret_cast<const f32x4_any*>(row + c + 4);
+  } else if (TAIL) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = column<TPR, VEC>(v, j, t);
-      const float x = c < D ? row[c] : 0.f;
-      if (j < 4)
-        r.a[j & 3] = x;
-      else
-        r.b[j & 3] = x;
-    }
+    for (int j = 0; j < 7; ++j)
+      if (c + j < D) (j < 4 ? r.a : r.b)[j & 3] = row[c + j];
   }
   return r;
 }
 
-template <int TPR, bool VEC>
+template <int TPR, bool TAIL>
 __device__ __forceinline__ void store8(uint16_t* row, int v, int t, int D, const float (&x)[8]) {
-  if constexpr (VEC) {
-    const int c = column<TPR, VEC>(v, 0, t);
-    if (c < D)
-      *reinterpret_cast<u32x4*>(row + c) = u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                 pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
-  } else {
+  const int c = column<TPR>(v, t);
+  const u32x4 w = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                   pack_bf16x2(x[6], x[7])};
+  if (TAIL ? c + 8 <= D : c < D) {
+    *reinterpret_cast<u32x4_any*>(row + c) = w;
+  } else if (TAIL) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = column<TPR, VEC>(v, j, t);
-      if (c < D) row[c] = to_bf16(x[j]);
-    }
+    for (int j = 0; j < 7; ++j)
+      if (c + j < D) row[c + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
   }
 }
-template <int TPR, bool VEC>
+template <int TPR, bool TAIL>
 __device__ __forceinline__ void store8(float* row, int v, int t, int D, const float (&x)[8]) {
-  if constexpr (VEC) {
-    const int c = column<TPR, VEC>(v, 0, t);
-    if (c < D) {
-      *reinterpret_cast<f32x4*>(row + c) = f32x4{x[0], x[1], x[2], x[3]};
-      *reinterpret_cast<f32x4*>(row + c + 4) = f32x4{x[4], x[5], x[6], x[7]};
-    }
-  } else {
+  const int c = column<TPR>(v, t);
+  if (TAIL ? c + 8 <= D : c < D) {
+    *reinterpret_cast<f32x4_any*>(row + c) = f32x4{x[0], x[1], x[2], x[3]};
+    *reinterpret_cast<f32x4_any*>(row + c + 4) = f32x4{x[4], x[5], x[6], x[7]};
+  } else if (TAIL) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = column<TPR, VEC>(v, j, t);
-      if (c < D) row[c] = x[j];
-    }
+    for (int j = 0; j < 7; ++j)
+      if (c + j < D) row[c + j] = x[j];
   }
 }
 
-// Eight values of a [D] parameter, bf16 or fp32: both forms' bits are loaded
-// and told apart where they are used, so that no load is waited for at a
-// branch.
+// Keeps the loaded form from here on: without it the compiler holds the
+// values it has unpacked for one pass over the row until the next one.
+__device__ __forceinline__ void as_loaded(Raw8<uint16_t>& r) { asm volatile("" : "+v"(r.v)); }
+__device__ __forceinline__ void as_loaded(Raw8<float>&) {}
+
+// Eight values of a [D] parameter, bf16 or fp32: the loaded bits, told apart
+// where they are used, so that no load is waited for at a branch.
 struct Param8 {
-  Raw8<uint16_t> h;
-  Raw8<float> f;
-  __device__ __forceinline__ float get(bool w32, int j) const { return w32 ? f.get(j) : h.get(j); }
+  u32x4 lo = {0u, 0u, 0u, 0u}, hi = {0u, 0u, 0u, 0u};  // fp32: values 0-3, 4-7; bf16: all in lo
+  __device__ __forceinline__ float get(bool w32, int j) const {
+    const uint32_t f = j < 4 ? lo[j & 3] : hi[j & 3];
+    const uint32_t h = (j & 1) ? lo[j >> 1] & 0xffff0000u : lo[j >> 1] << 16;
+    return as_f32(w32 ? f : h);
+  }
 };
-template <int TPR, bool VEC>
+template <int TPR, bool TAIL>
 __device__ __forceinline__ Param8 load_param(const void* w, bool w32, int v, int t, int D) {
   Param8 p;
-  if (w32)
-    p.f = load8<TPR, VEC>(static_cast<const float*>(w), v, t, D);
-  else
-    p.h = load8<TPR, VEC>(static_cast<const uint16_t*>(w), v, t, D);
+  if (w32) {
+    const Raw8<float> f = load8<TPR, TAIL>(static_cast<const float*>(w), v, t, D);
+    p.lo = __builtin_bit_cast(u32x4, f.a);
+    p.hi = __builtin_bit_cast(u32x4, f.b);
+  } else {
+    p.lo = load8<TPR, TAIL>(static_cast<const uint16_t*>(w), v, t, D).v;
+  }
   return p;
 }
 
-// N sums over the TPR threads of a row, the same in each of them.  s: LDS of
-// N floats per wave; the caller alternates two of them between reductions, so
-// one barrier each is enough.
+// N sums over the threads of a row, the same in each of them.  s: LDS of
+// N floats for each of TPR / 64 waves; the caller alternates two of them between
+// reductions, so one barrier each is enough, and has cleared those of waves
+// that are not there (clear_sums).
+template <int COUNT>
+__device__ __forceinline__ void clear_sums(float* s) {
+  for (int i = threadIdx.x; i < COUNT; i += blockDim.x) s[i] = 0.f;
+  __syncthreads();
+}
 template <int TPR, int N>
 __device__ __forceinline__ void row_sums(float (&x)[N], float* s) {
 #pragma unroll
@@ -175,149 +177,172 @@ __device__ __forceinline__ void row_sums(float (&x)[N], float* s) {
   }
 }
 
-constexpr int group_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
+// Most threads of a workgroup: four rows' waves, or one row's threads (no more
+// waves than hold the row).
+constexpr int group_threads(int tpr) { return tpr == 64 ? 256 : tpr; }
+// A thread's row group in its workgroup (a wave's, in a scalar register).
+template <int TPR>
+__device__ __forceinline__ int row_group() {
+  return TPR > 64 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+}
 
-template <int TPR, int NV, bool VEC, typename R>
+// Whether a row's threads keep the [D] parameters in registers from row to row
+// (one vector a thread, registers to spare; otherwise they come from L2 again
+// for every row), and whether they go from row to row, the next one's loads
+// sent ahead of the current one's reductions.
+constexpr bool keeps(int tpr, int nv) { return nv == 1 && tpr < 1024; }
+constexpr bool walks(int nv) { return nv == 1; }
+
+template <int TPR, int NV, bool TAIL, typename R>
 __global__ __launch_bounds__(group_threads(TPR)) void k_norm_fwd(
     NormArgs n, const R* __restrict__ h, const uint16_t* __restrict__ o, R* __restrict__ hn,
     uint16_t* __restrict__ y, int8_t* __restrict__ codes, uint8_t* __restrict__ exps) {
-  __shared__ float s[2][TPR / 64];
+  constexpr bool KEEP = keeps(TPR, NV);
+  constexpr int G = group_threads(TPR) / TPR;
+  __shared__ float s[2][2][TPR / 64];
+  if (TPR > 64) clear_sums<4 * (TPR / 64)>(&s[0][0][0]);
   const int t = threadIdx.x % TPR, D = n.D;
-  const int64_t m = (int64_t)blockIdx.x * (group_threads(TPR) / TPR) + threadIdx.x / TPR;
-  if (TPR == 64 && m >= n.M) return;  // whole wave; no barrier follows
-  const int64_t row = m * D;
+  const int nb = (D + kAct8Block - 1) / kAct8Block;
+  const bool post = n.w_post != nullptr, chan = n.gate_kind == kGateChannel,
+             elem = n.gate_kind == kGateElement, rowg = n.gate_kind == kGateRow;
+  Param8 w1, w2, gc;  // of vector 0, with KEEP
+  auto param = [&](const void* w, int v) {
+    if (!KEEP) asm volatile("" : "+s"(w) : : "memory");  // loaded here, no earlier
+    return load_param<TPR, TAIL>(w, n.w32, v, t, D);
+  };
   Raw8<R> hv[NV];
   Raw8<uint16_t> ov[NV], gv[NV];
-  Param8 w1[NV], w2[NV], gc[NV];
-  float gr = n.scale;
+  auto load_row = [&](int64_t m) {
+    const int64_t row = m * D;
 #pragma unroll
-  for (int v = 0; v < NV; ++v) hv[v] = load8<TPR, VEC>(h + row, v, t, D);
-  if (o) {
-#pragma unroll
-    for (int v = 0; v < NV; ++v) ov[v] = load8<TPR, VEC>(o + row, v, t, D);
-    if (n.w_post) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) w1[v] = load_param<TPR, VEC>(n.w_post, n.w32, v, t, D);
+    for (int v = 0; v < NV; ++v) {
+      hv[v] = load8<TPR, TAIL>(h + row, v, t, D);
+      if (o) ov[v] = load8<TPR, TAIL>(o + row, v, t, D);
+      if (elem) gv[v] = load8<TPR, TAIL>(static_cast<const uint16_t*>(n.gate) + row, v, t, D);
     }
-    if (n.gate_kind == kGateChannel) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) gc[v] = load_param<TPR, VEC>(n.gate, n.w32, v, t, D);
-    } else if (n.gate_kind == kGateElement) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-        gv[v] = load8<TPR, VEC>(static_cast<const uint16_t*>(n.gate) + row, v, t, D);
-    } else if (n.gate_kind == kGateRow) {
-      gr *= load_f32(static_cast<const uint16_t*>(n.gate) + m);
-    }
+  };
+  const int64_t step = (int64_t)gridDim.x * G;
+  int64_t m = (int64_t)blockIdx.x * G + row_group<TPR>();
+  if (m < n.M) load_row(m);
+  if (KEEP) {
+    if (post) w1 = param(n.w_post, 0);
+    if (chan) gc = param(n.gate, 0);
+    w2 = param(n.w_pre, 0);
   }
+  // a group that is a whole workgroup runs the same rows in all its threads; a
+  // wave's own rows need no barrier
+  for (int par = 0; m < n.M; m += step, par ^= 1) {
+    const int64_t row = m * D;
+    Raw8<uint16_t> o_[NV], g_[NV];
+    float x[NV][8];
 #pragma unroll
-  for (int v = 0; v < NV; ++v) w2[v] = load_param<TPR, VEC>(n.w_pre, n.w32, v, t, D);
-
-  float x[NV][8];
+    for (int v = 0; v < NV; ++v) {
+      o_[v] = ov[v];
+      g_[v] = gv[v];
 #pragma unroll
-  for (int v = 0; v < NV; ++v)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[v][j] = hv[v].get(j);
-  if (o) {
-    float r1 = 1.f;
-    if (n.w_post) {
-      float q[1] = {0.f};
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q[0] = __builtin_fmaf(ov[v].get(j), ov[v].get(j), q[0]);
-      row_sums<TPR, 1>(q, s[0]);
-      r1 = 1.f / __builtin_sqrtf(q[0] / (float)D + n.eps);
+      for (int j = 0; j < 8; ++j) x[v][j] = hv[v].get(j);
     }
-    const float k = gr * r1;
+    float k = n.scale;
+    if (rowg) k *= load_f32(static_cast<const uint16_t*>(n.gate) + m);
+    if (walks(NV) && m + step < n.M) load_row(m + step);
+    if (o) {
+      if (post) {
+        float q[1] = {0.f};
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) q[0] = __builtin_fmaf(o_[v].get(j), o_[v].get(j), q[0]);
+        row_sums<TPR, 1>(q, s[par][0]);
+        k *= 1.f / __builtin_sqrtf(q[0] / (float)D + n.eps);
+      }
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float out[8];
+        if (!KEEP && post) w1 = param(n.w_post, v);
+        if (!KEEP && chan) gc = param(n.gate, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float p = o_[v].get(j) * k;
+          if (post) p *= w1.get(n.w32, j);
+          if (chan) p *= gc.get(n.w32, j);
+          if (elem) p *= g_[v].get(j);
+          out[j] = x[v][j] = x[v][j] + p;
+        }
+        store8<TPR, TAIL>(hn + row, v, t, D, out);
+      }
+    }
+    float q[1] = {0.f};
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[0] = __builtin_fmaf(x[v][j], x[v][j], q[0]);
+    row_sums<TPR, 1>(q, s[par][1]);
+    const float r2 = 1.f / __builtin_sqrtf(q[0] / (float)D + n.eps);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float out[8];
+      if (!KEEP) w2 = param(n.w_pre, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) out[j] = x[v][j] * r2 * w2.get(n.w32, j);
+      store8<TPR, TAIL>(y + row, v, t, D, out);
+      if (!codes) continue;
+      // the checkpoint of y as it is stored, a block of 64 columns in 8 lanes'
+      // vectors; values past the row's end are zero
+      uint32_t b[8], top = 0u;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        float p = ov[v].get(j) * k;
-        if (n.w_post) p *= w1[v].get(n.w32, j);
-        if (n.gate_kind == kGateChannel) p *= gc[v].get(n.w32, j);
-        if (n.gate_kind == kGateElement) p *= gv[v].get(j);
-        out[j] = x[v][j] = x[v][j] + p;
+        b[j] = to_bf16(out[j]);
+        top = max(top, b[j] & 0x7fffu);
       }
-      store8<TPR, VEC>(hn + row, v, t, D, out);
-    }
-  }
-  float q[1] = {0.f};
-#pragma unroll
-  for (int v = 0; v < NV; ++v)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) q[0] = __builtin_fmaf(x[v][j], x[v][j], q[0]);
-  row_sums<TPR, 1>(q, s[1]);
-  const float r2 = 1.f / __builtin_sqrtf(q[0] / (float)D + n.eps);
-  const int nb = (D + kAct8Block - 1) / kAct8Block;
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    float out[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) out[j] = x[v][j] * r2 * w2[v].get(n.w32, j);
-    store8<TPR, VEC>(y + row, v, t, D, out);
-    if (!codes) continue;
-    // the checkpoint of y as it is stored; values past the row's end are zero
-    uint32_t b[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) b[j] = to_bf16(out[j]);
-    if constexpr (VEC) {  // a block of 64 columns is 8 lanes' vectors
-      uint32_t top = 0u;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, b[j] & 0x7fffu);
       top = max_of_8_lanes(top);
       const uint32_t E = act8_exp(top);
       const float inv = act8_inv(E);
-      const int c = column<TPR, VEC>(v, 0, t);
-      if (c < D) {
-        u32x2 w = {0u, 0u};
+      const int c = column<TPR>(v, t);
+      u32x2 w = {0u, 0u};
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          w[j >> 2] |= ((uint32_t)act8_code(as_f32(b[j] << 16), inv) & 0xffu) << (8 * (j & 3));
-        if (E == kAct8NaN) w = u32x2{0u, 0u};
-        *reinterpret_cast<u32x2*>(codes + row + c) = w;
-        if ((t & 7) == 0) exps[m * nb + c / kAct8Block] = (uint8_t)E;
-      }
-    } else {  // a block is one value of each of a wave's lanes
+      for (int j = 0; j < 8; ++j)
+        w[j >> 2] |= ((uint32_t)act8_code(as_f32(b[j] << 16), inv) & 0xffu) << (8 * (j & 3));
+      if (E == kAct8NaN) w = u32x2{0u, 0u};
+      if (TAIL ? c + 8 <= D : c < D) {
+        *reinterpret_cast<u32x2_any*>(codes + row + c) = w;
+      } else if (TAIL) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int c = column<TPR, VEC>(v, j, t);
-        const uint32_t E = act8_exp(wave_max_u32(b[j] & 0x7fffu));
-        if (c < D) {
-          codes[row + c] =
-              E == kAct8NaN ? 0 : (int8_t)act8_code(as_f32(b[j] << 16), act8_inv(E));
-          if ((t & 63) == 0) exps[m * nb + c / kAct8Block] = (uint8_t)E;
-        }
+        for (int j = 0; j < 7; ++j)
+          if (c + j < D) codes[row + c + j] = (int8_t)(w[j >> 2] >> (8 * (j & 3)));
       }
+      if (c < D && (t & 7) == 0) exps[m * nb + c / kAct8Block] = (uint8_t)E;
     }
   }
 }
 
 // Row group z takes rows z, z + groups, ...  With SUMS a thread keeps its
 // columns' sums over those rows in registers; a workgroup's groups meet in
-// LDS and leave part [workgroup][3][D] (dw_pre, dw_post, channel dgate).  The
-// next row's loads go out before the current row's reductions.
-template <int TPR, int NV, bool VEC, bool SUMS, typename R>
+// LDS and leave part [workgroup][3][D] (dw_pre, dw_post, channel dgate).
+template <int TPR, int NV, bool TAIL, bool SUMS, typename R>
 __global__ __launch_bounds__(group_threads(TPR)) void k_norm_bwd(
     NormArgs n, const uint16_t* __restrict__ dy, const R* __restrict__ dhn,
     const R* __restrict__ hn, const uint16_t* __restrict__ o, R* __restrict__ dh,
-    uint16_t* __restrict__ dout, void* __restrict__ dgate, float* __restrict__ part) {
+    uint16_t* __restrict__ dout, void* __restrict__ dgate, float* __restrict__ part,
+    f32x4* __restrict__ stats) {
   constexpr int G = group_threads(TPR) / TPR;  // row groups of a workgroup
   constexpr int W = TPR / 64;
+  constexpr bool KEEP = keeps(TPR, NV);
   __shared__ float s[2][2][3 * W];
-  const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR, D = n.D;
+  if (TPR > 64) clear_sums<12 * W>(&s[0][0][0]);
+  const int t = threadIdx.x % TPR, grp = row_group<TPR>(), D = n.D;
   const float rD = 1.f / (float)D;
   const bool post = n.w_post != nullptr, chan = n.gate_kind == kGateChannel,
              elem = n.gate_kind == kGateElement, rowg = n.gate_kind == kGateRow;
   float sp[NV][8] = {}, so[NV][8] = {}, sg[NV][8] = {};
-  Param8 w1[NV], w2[NV], gc[NV];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    w2[v] = load_param<TPR, VEC>(n.w_pre, n.w32, v, t, D);
-    if (post) w1[v] = load_param<TPR, VEC>(n.w_post, n.w32, v, t, D);
-    if (chan) gc[v] = load_param<TPR, VEC>(n.gate, n.w32, v, t, D);
+  Param8 w1, w2, gc;  // of vector 0, with KEEP
+  auto param = [&](const void* w, int v) {
+    if (!KEEP) asm volatile("" : "+s"(w) : : "memory");  // loaded here, no earlier
+    return load_param<TPR, TAIL>(w, n.w32, v, t, D);
+  };
+  if (KEEP) {
+    w2 = param(n.w_pre, 0);
+    if (post) w1 = param(n.w_post, 0);
+    if (chan) gc = param(n.gate, 0);
   }
   Raw8<R> hv[NV], dv[NV];
   Raw8<uint16_t> yv[NV], ov[NV], gv[NV];
@@ -325,21 +350,22 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_bwd(
     const int64_t row = m * D;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      hv[v] = load8<TPR, VEC>(hn + row, v, t, D);
-      yv[v] = load8<TPR, VEC>(dy + row, v, t, D);
-      if (o) ov[v] = load8<TPR, VEC>(o + row, v, t, D);
-      if (dhn) dv[v] = load8<TPR, VEC>(dhn + row, v, t, D);
-      if (elem) gv[v] = load8<TPR, VEC>(static_cast<const uint16_t*>(n.gate) + row, v, t, D);
+      hv[v] = load8<TPR, TAIL>(hn + row, v, t, D);
+      yv[v] = load8<TPR, TAIL>(dy + row, v, t, D);
+      if (o) ov[v] = load8<TPR, TAIL>(o + row, v, t, D);
+      if (dhn) dv[v] = load8<TPR, TAIL>(dhn + row, v, t, D);
+      if (elem) gv[v] = load8<TPR, TAIL>(static_cast<const uint16_t*>(n.gate) + row, v, t, D);
     }
   };
   const int64_t step = (int64_t)gridDim.x * G;
   int64_t m = (int64_t)blockIdx.x * G + grp;
-  if (m < n.M) load_row(m);
+  if (walks(NV) && m < n.M) load_row(m);
   int par = 0;
   // the rows of a group that is a whole workgroup are the same for all its
   // threads; a wave's own rows need no barrier
   for (; m < n.M; m += step, par ^= 1) {
     const int64_t row = m * D;
+    if (!walks(NV)) load_row(m);
     Raw8<R> h_[NV], d_[NV];
     Raw8<uint16_t> y_[NV], o_[NV], g_[NV];
 #pragma unroll
@@ -351,44 +377,58 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_bwd(
       g_[v] = gv[v];
     }
     const float grow = rowg ? n.scale * load_f32(static_cast<const uint16_t*>(n.gate) + m) : n.scale;
-    if (SUMS && m + step < n.M) load_row(m + step);
+    if (walks(NV) && m + step < n.M) load_row(m + step);
     float q[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int v = 0; v < NV; ++v) {
+      if (!KEEP) w2 = param(n.w_pre, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float x = h_[v].get(j);
         q[0] = __builtin_fmaf(x, x, q[0]);
-        q[1] = __builtin_fmaf(y_[v].get(j) * w2[v].get(n.w32, j), x, q[1]);
+        q[1] = __builtin_fmaf(y_[v].get(j) * w2.get(n.w32, j), x, q[1]);
         if (post) q[2] = __builtin_fmaf(o_[v].get(j), o_[v].get(j), q[2]);
       }
+    }
     row_sums<TPR, 3>(q, s[par][0]);
+    if (!KEEP) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        as_loaded(h_[v]);
+        as_loaded(y_[v]);
+        as_loaded(o_[v]);
+      }
+    }
     const float r2 = 1.f / __builtin_sqrtf(q[0] * rD + n.eps);
     const float c2 = q[1] * r2 * rD * r2;  // r2 mean(dn n)
     const float r1 = post ? 1.f / __builtin_sqrtf(q[2] * rD + n.eps) : 1.f;
+    if (!SUMS && stats && t == 0) stats[m] = f32x4{r2, c2, r1, grow};
     float d[NV][8], e[2] = {0.f, 0.f};
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float out[8];
+      if (!KEEP) w2 = param(n.w_pre, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float x = h_[v].get(j), g = y_[v].get(j);
-        const float dn = g * w2[v].get(n.w32, j);
+        const float dn = g * w2.get(n.w32, j);
         out[j] = d[v][j] = __builtin_fmaf(r2, dn - x * c2, d_[v].get(j));
         if (SUMS) sp[v][j] = __builtin_fmaf(g, x * r2, sp[v][j]);
       }
-      store8<TPR, VEC>(dh + row, v, t, D, out);
+      store8<TPR, TAIL>(dh + row, v, t, D, out);
     }
     if (!o) continue;
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int v = 0; v < NV; ++v) {
+      if (!KEEP && post) w1 = param(n.w_post, v);
+      if (!KEEP && chan) gc = param(n.gate, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         // d becomes dq (or a, without a post norm)
-        const float x = o_[v].get(j) * r1, wp = post ? w1[v].get(n.w32, j) : 1.f;
+        const float x = o_[v].get(j) * r1, wp = post ? w1.get(n.w32, j) : 1.f;
         const float base = d[v][j];
         float a = base * grow;
-        if (chan) a *= gc[v].get(n.w32, j);
+        if (chan) a *= gc.get(n.w32, j);
         if (elem) a *= g_[v].get(j);
         d[v][j] = a * wp;
         e[0] = __builtin_fmaf(a * wp, x, e[0]);
@@ -399,7 +439,12 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_bwd(
         }
         if (elem) g_[v].put(j, base * n.scale * (x * wp));
       }
+    }
     if (post || rowg) row_sums<TPR, 2>(e, s[par][1]);
+    if (!KEEP) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) as_loaded(o_[v]);
+    }
     if (rowg && dgate && t == 0) static_cast<float*>(dgate)[m] = e[1];
     const float c1 = e[0] * rD * r1;
 #pragma unroll
@@ -410,8 +455,8 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_bwd(
         out[j] = post ? r1 * (d[v][j] - o_[v].get(j) * c1) : d[v][j];
         dg[j] = g_[v].get(j);
       }
-      store8<TPR, VEC>(dout + row, v, t, D, out);
-      if (elem && dgate) store8<TPR, VEC>(static_cast<uint16_t*>(dgate) + row, v, t, D, dg);
+      store8<TPR, TAIL>(dout + row, v, t, D, out);
+      if (elem && dgate) store8<TPR, TAIL>(static_cast<uint16_t*>(dgate) + row, v, t, D, dg);
     }
   }
   if constexpr (SUMS) {
@@ -419,9 +464,9 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_bwd(
     if constexpr (G == 1) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        store8<TPR, VEC>(dst, v, t, D, sp[v]);
-        store8<TPR, VEC>(dst + D, v, t, D, so[v]);
-        store8<TPR, VEC>(dst + 2 * D, v, t, D, sg[v]);
+        store8<TPR, TAIL>(dst, v, t, D, sp[v]);
+        store8<TPR, TAIL>(dst + D, v, t, D, so[v]);
+        store8<TPR, TAIL>(dst + 2 * D, v, t, D, sg[v]);
       }
     } else {
       __shared__ float acc[G][3 * NV * 8 * TPR];
@@ -440,11 +485,58 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_bwd(
 #pragma unroll
         for (int k = 0; k < G; ++k) x += acc[k][i];
         const int which = i / (NV * 8 * TPR), l = i % (NV * 8 * TPR);
-        const int c = column<TPR, VEC>(l / TPR / 8, l / TPR % 8, l % TPR);
+        const int c = column<TPR>(l / TPR / 8, l % TPR) + l / TPR % 8;
         if (c < D) dst[which * D + c] = x;
       }
     }
   }
+}
+
+// The column sums of rows past kSumCols columns, whose threads have no
+// registers to keep them beside a row: from the rows again and their stats
+// (r2, r2 mean(dn n), r1, scale times the row's gate).  Workgroup (x, z):
+// columns 8 (256 x + thread) .. + 7, rows z, z + S, ...; part as above.
+template <bool TAIL, typename R>
+__global__ __launch_bounds__(256) void k_norm_columns(
+    NormArgs n, const uint16_t* __restrict__ dy, const R* __restrict__ dhn,
+    const R* __restrict__ hn, const uint16_t* __restrict__ o, const f32x4* __restrict__ stats,
+    float* __restrict__ part) {
+  const int t = blockIdx.x * 256 + threadIdx.x, D = n.D;
+  const bool post = n.w_post != nullptr, chan = n.gate_kind == kGateChannel,
+             elem = n.gate_kind == kGateElement;
+  auto param = [&](const void* w) { return load_param<1, TAIL>(w, n.w32, 0, t, D); };
+  Param8 w1, w2 = param(n.w_pre), gc;
+  if (post) w1 = param(n.w_post);
+  if (chan) gc = param(n.gate);
+  float sp[8] = {}, so[8] = {}, sg[8] = {};
+  for (int64_t m = blockIdx.y; m < n.M; m += gridDim.y) {
+    const int64_t row = m * D;
+    const f32x4 st = stats[m];
+    const Raw8<R> h = load8<1, TAIL>(hn + row, 0, t, D);
+    const Raw8<uint16_t> y = load8<1, TAIL>(dy + row, 0, t, D);
+    Raw8<R> d;
+    Raw8<uint16_t> ov, g;
+    if (dhn) d = load8<1, TAIL>(dhn + row, 0, t, D);
+    if (o) ov = load8<1, TAIL>(o + row, 0, t, D);
+    if (elem) g = load8<1, TAIL>(static_cast<const uint16_t*>(n.gate) + row, 0, t, D);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = h.get(j), dn = y.get(j) * w2.get(n.w32, j);
+      const float base = __builtin_fmaf(st[0], dn - x * st[1], d.get(j));
+      sp[j] = __builtin_fmaf(y.get(j), x * st[0], sp[j]);
+      if (!o) continue;
+      const float q = ov.get(j) * st[2];
+      float a = base * st[3];
+      if (chan) a *= gc.get(n.w32, j);
+      if (elem) a *= g.get(j);
+      so[j] = __builtin_fmaf(a, q, so[j]);
+      if (chan) sg[j] = __builtin_fmaf(base * n.scale, post ? q * w1.get(n.w32, j) : q, sg[j]);
+    }
+  }
+  float* dst = part + (int64_t)blockIdx.y * 3 * D;
+  store8<1, TAIL>(dst, 0, t, D, sp);
+  store8<1, TAIL>(dst + D, 0, t, D, so);
+  store8<1, TAIL>(dst + 2 * D, 0, t, D, sg);
 }
 
 // out_j[c] = sum over the S slices of part[z][j][c]: a workgroup takes 64
@@ -484,31 +576,46 @@ __global__ __launch_bounds__(64 * kSumGroups) void k_norm_sums(const float* __re
   }
 }
 
+// Threads of a launch whose workgroups go from row to row, for 256 compute
+// units: as many as stay resident.
+constexpr int64_t kFwdThreads = 256 * 2048, kBwdThreads = 256 * 1024, kSumThreads = 256 * 512;
+// Columns up to which a row's threads keep the column sums.  One vector a
+// thread and its 24 sums take 162-176 registers, which 1024 threads do not
+// have: spilling, 4096 x 8192 took 255 us, in a pass of its own XXX.
+constexpr int64_t kSumCols = 4096;
+constexpr int kColumnSlices = 64;
+
 NormArgs args_of(const BlockNorm& n) {
   return NormArgs{n.M, (int)n.D, n.w_pre, n.w_post, n.gate, n.w32, n.gate_kind, n.scale, n.eps};
 }
 
-// Threads of a row: a wave up to 1024 columns, then the fewest of 256, 512 and
-// 1024 that hold the row in few vectors each.
-int row_threads(int64_t D) { return D <= 1024 ? 64 : D <= 2048 ? 256 : D <= 8192 ? 512 : 1024; }
+// Threads of a row: as many as hold it in one vector each; two past 8192
+// columns.
+int row_threads(int64_t D) {
+  int t = 64;
+  while (t < 1024 && 8 * t < D) t *= 2;
+  return t;
+}
 
 // Calls f<TPR, NV>() for the row length D.
 template <typename F>
 hipError_t by_columns(int64_t D, F&& f) {
   using I1 = std::integral_constant<int, 1>;
   using I2 = std::integral_constant<int, 2>;
-  using I4 = std::integral_constant<int, 4>;
-  using T64 = std::integral_constant<int, 64>;
-  using T256 = std::integral_constant<int, 256>;
-  using T512 = std::integral_constant<int, 512>;
+  switch (row_threads(D)) {
+    case 64: return f(std::integral_constant<int, 64>{}, I1{});
+    case 128: return f(std::integral_constant<int, 128>{}, I1{});
+    case 256: return f(std::integral_constant<int, 256>{}, I1{});
+    case 512: return f(std::integral_constant<int, 512>{}, I1{});
+  }
   using T1024 = std::integral_constant<int, 1024>;
-  if (D <= 512) return f(T64{}, I1{});
-  if (D <= 1024) return f(T64{}, I2{});
-  if (D <= 2048) return f(T256{}, I1{});
-  if (D <= 4096) return f(T512{}, I1{});
-  if (D <= 8192) return f(T512{}, I2{});
-  if (D <= 16384) return f(T1024{}, I2{});
-  return f(T1024{}, I4{});
+  return D <= 8192 ? f(T1024{}, I1{}) : f(T1024{}, I2{});
+}
+
+// Threads of a workgroup for the row length D.
+template <int TPR, int NV>
+int threads_of(int64_t D) {
+  return TPR == 64 || NV > 1 ? group_threads(TPR) : (int)((D + 511) / 512 * 64);
 }
 
 template <typename R>
@@ -516,40 +623,61 @@ hipError_t norm_fwd(const BlockNorm& n, const void* h, const uint16_t* o, void* 
                     int8_t* codes, uint8_t* exps, hipStream_t st) {
   return by_columns(n.D, [&](auto tpr, auto nv) {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-    constexpr int T = group_threads(TPR), G = T / TPR;
-    const dim3 grid((unsigned)((n.M + G - 1) / G));
+    constexpr int G = group_threads(TPR) / TPR;
+    const int T = threads_of<TPR, NV>(n.D);
+    const int64_t groups = (n.M + G - 1) / G;
+    const dim3 grid((unsigned)(walks(NV) ? std::min<int64_t>(groups, kFwdThreads / T) : groups));
     const NormArgs a = args_of(n);
     const R* hp = static_cast<const R*>(h);
     R* hn = static_cast<R*>(h_new);
     if (n.D % 8 == 0)
-      hipLaunchKernelGGL((k_norm_fwd<TPR, NV, true, R>), grid, dim3(T), 0, st, a, hp, o, hn, y,
+      hipLaunchKernelGGL((k_norm_fwd<TPR, NV, false, R>), grid, dim3(T), 0, st, a, hp, o, hn, y,
                          codes, exps);
     else
-      hipLaunchKernelGGL((k_norm_fwd<TPR, NV, false, R>), grid, dim3(T), 0, st, a, hp, o, hn, y,
+      hipLaunchKernelGGL((k_norm_fwd<TPR, NV, true, R>), grid, dim3(T), 0, st, a, hp, o, hn, y,
                          codes, exps);
     return hipGetLastError();
   });
 }
 
-template <typename R, bool SUMS>
+template <typename R>
 hipError_t norm_bwd(const BlockNorm& n, const uint16_t* dy, const void* dh_new, const void* h_new,
                     const uint16_t* o, void* dh, uint16_t* dout, void* dgate, float* part,
-                    hipStream_t st) {
-  return by_columns(n.D, [&](auto tpr, auto nv) {
+                    void* stats, hipStream_t st) {
+  const NormArgs a = args_of(n);
+  const R *dp = static_cast<const R*>(dh_new), *hp = static_cast<const R*>(h_new);
+  R* out = static_cast<R*>(dh);
+  f32x4* rows = static_cast<f32x4*>(stats);
+  hipError_t e = by_columns(n.D, [&](auto tpr, auto nv) {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-    constexpr int T = group_threads(TPR), G = T / TPR;
-    const dim3 grid((unsigned)(SUMS ? block_norm_slices(n.M, n.D) : (n.M + G - 1) / G));
-    const NormArgs a = args_of(n);
-    const R *dp = static_cast<const R*>(dh_new), *hp = static_cast<const R*>(h_new);
-    R* out = static_cast<R*>(dh);
-    if (n.D % 8 == 0)
-      hipLaunchKernelGGL((k_norm_bwd<TPR, NV, true, SUMS, R>), grid, dim3(T), 0, st, a, dy, dp, hp,
-                         o, out, dout, dgate, part);
-    else
-      hipLaunchKernelGGL((k_norm_bwd<TPR, NV, false, SUMS, R>), grid, dim3(T), 0, st, a, dy, dp,
-                         hp, o, out, dout, dgate, part);
-    return hipGetLastError();
+    constexpr int G = group_threads(TPR) / TPR;
+    const int T = threads_of<TPR, NV>(n.D);
+    const int64_t groups = (n.M + G - 1) / G;
+    auto launch = [&](auto sums, int64_t blocks) {
+      constexpr bool SUMS = decltype(sums)::value;
+      const dim3 grid((unsigned)blocks);
+      if (n.D % 8 == 0)
+        hipLaunchKernelGGL((k_norm_bwd<TPR, NV, false, SUMS, R>), grid, dim3(T), 0, st, a, dy, dp,
+                           hp, o, out, dout, dgate, part, rows);
+      else
+        hipLaunchKernelGGL((k_norm_bwd<TPR, NV, true, SUMS, R>), grid, dim3(T), 0, st, a, dy, dp,
+                           hp, o, out, dout, dgate, part, rows);
+      return hipGetLastError();
+    };
+    if constexpr (TPR < 1024) {
+      if (part) return launch(std::true_type{}, block_norm_slices(n.M, n.D));
+    }
+    return launch(std::false_type{}, walks(NV) ? std::min<int64_t>(groups, kBwdThreads / T) : groups);
   });
+  if (e != hipSuccess || !part || n.D <= kSumCols) return e;
+  const dim3 grid((unsigned)((n.D + 2047) / 2048), (unsigned)block_norm_slices(n.M, n.D));
+  if (n.D % 8 == 0)
+    hipLaunchKernelGGL((k_norm_columns<false, R>), grid, dim3(256), 0, st, a, dy, dp, hp, o, rows,
+                       part);
+  else
+    hipLaunchKernelGGL((k_norm_columns<true, R>), grid, dim3(256), 0, st, a, dy, dp, hp, o, rows,
+                       part);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -561,25 +689,22 @@ hipError_t launch_block_norm_fwd(const BlockNorm& n, const void* h, const uint16
                  : norm_fwd<uint16_t>(n, h, o, h_new, y, codes, exps, st);
 }
 
-// Workgroups of a backward that sums over rows: two for each of 256 compute
-// units, as many as stay resident, unless the rows are fewer.
 int block_norm_slices(int64_t M, int64_t D) {
-  const int64_t G = group_threads(row_threads(D)) / row_threads(D);
-  return (int)std::min<int64_t>((M + G - 1) / G, 512);
+  if (D > kSumCols) return (int)std::min<int64_t>(M, kColumnSlices * 16384 / (2048 * ((D + 2047) / 2048)));
+  const int64_t T = D <= 512 ? 256 : (D + 511) / 512 * 64, G = D <= 512 ? 4 : 1;
+  return (int)std::min<int64_t>((M + G - 1) / G, kSumThreads / T);
 }
+int64_t block_norm_stats(int64_t M, int64_t D) { return D > kSumCols ? 4 * M : 0; }
 
 hipError_t launch_block_norm_bwd(const BlockNorm& n, const uint16_t* dy, const void* dh_new,
                                  const void* h_new, const uint16_t* o, void* dh, uint16_t* dout,
                                  void* dgate, float* dw_post, float* dw_pre, float* part,
-                                 hipStream_t st) {
+                                 float* stats, hipStream_t st) {
   if (n.M == 0) return hipSuccess;
-  hipError_t e;
-  if (!part)
-    return n.res32 ? norm_bwd<float, false>(n, dy, dh_new, h_new, o, dh, dout, dgate, part, st)
-                   : norm_bwd<uint16_t, false>(n, dy, dh_new, h_new, o, dh, dout, dgate, part, st);
-  e = n.res32 ? norm_bwd<float, true>(n, dy, dh_new, h_new, o, dh, dout, dgate, part, st)
-              : norm_bwd<uint16_t, true>(n, dy, dh_new, h_new, o, dh, dout, dgate, part, st);
-  if (e != hipSuccess) return e;
+  hipError_t e =
+      n.res32 ? norm_bwd<float>(n, dy, dh_new, h_new, o, dh, dout, dgate, part, stats, st)
+              : norm_bwd<uint16_t>(n, dy, dh_new, h_new, o, dh, dout, dgate, part, stats, st);
+  if (e != hipSuccess || !part) return e;
   float* dg = n.gate_kind == kGateChannel ? static_cast<float*>(dgate) : nullptr;
   hipLaunchKernelGGL(k_norm_sums, dim3((unsigned)((3 * n.D + 63) / 64)), dim3(64 * kSumGroups), 0,
                      st, part, block_norm_slices(n.M, n.D), (int)n.D, dw_pre, dw_post, dg);

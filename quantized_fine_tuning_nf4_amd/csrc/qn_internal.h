@@ -341,13 +341,15 @@ struct BlockNorm {
 };
 hipError_t launch_block_norm_fwd(const BlockNorm& n, const void* h, const uint16_t* o, void* h_new,
                                  uint16_t* y, int8_t* codes, uint8_t* exps, hipStream_t st);
-// Row slices whose column sums (dw_pre, dw_post, channel dgate) are added by
-// a second launch; part [slices][sums][D] fp32.
+// Backward.  part (nullable: no sums over rows wanted): the slices of dw_pre,
+// dw_post and the channel dgate, [block_norm_slices][3][D], added by a last
+// launch; stats: block_norm_stats floats beside it (16-byte aligned).
 int block_norm_slices(int64_t M, int64_t D);
+int64_t block_norm_stats(int64_t M, int64_t D);
 hipError_t launch_block_norm_bwd(const BlockNorm& n, const uint16_t* dy, const void* dh_new,
                                  const void* h_new, const uint16_t* o, void* dh, uint16_t* dout,
                                  void* dgate, float* dw_post, float* dw_pre, float* part,
-                                 hipStream_t st);
+                                 float* stats, hipStream_t st);
 
 // Token log probabilities (see the header).
 hipError_t launch_logprobs_fwd(const void* x, bool f32, int64_t T, int64_t V, int64_t ld,

@@ -97,7 +97,7 @@ def _codes64(y):
 
 SHAPES = [(1, 4096), (3, 1), (2, 7), (5, 8), (4, 63), (7, 64), (3, 65), (300, 128), (33, 520),
           (9, 1000), (17, 1001), (6, 2048), (5, 4096), (4, 4100), (3, 5121), (3, 8192), (2, 8200),
-          (2, 16384), (2, 16387), (2, 32768), (1, 32761)]
+          (2, 16384), (2, 16381), (3, 1024), (5, 1032)]
 MODES = [("none", "none"), ("add", "none"), ("add", "row"), ("norm", "none"), ("norm", "channel"),
          ("norm", "row"), ("norm", "element"), ("add", "channel")]
 
