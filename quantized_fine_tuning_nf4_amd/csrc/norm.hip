@@ -59,23 +59,25 @@ struct Raw8<float> {
 
 // Vector v of thread t holds the columns from here on.  Rows of odd lengths
 // (TAIL: D no multiple of 8) start on any element -- vector accesses need no
-// alignment on this target -- and their last vector is partial.
+// alignment on this target -- and end inside a vector: its thread loads the
+// row's last eight values instead, and in_place moves them where they belong
+// once they are here (a branch that only the row's last wave takes).
 template <int TPR>
 __device__ __forceinline__ int column(int v, int t) {
   return (v * TPR + t) * 8;
 }
 
-// The values are zero past the row's end.
+// Values past the row's end are zero (with TAIL: after in_place).
 template <int TPR, bool TAIL>
 __device__ __forceinline__ Raw8<uint16_t> load8(const uint16_t* row, int v, int t, int D) {
   Raw8<uint16_t> r;
   const int c = column<TPR>(v, t);
-  if (TAIL ? c + 8 <= D : c < D) {
-    r.v = *reinterpret_cast<const u32x4_any*>(row + c);
-  } else if (TAIL) {
+  if (!TAIL || D >= 8) {
+    if (c < D) r.v = *reinterpret_cast<const u32x4_any*>(row + (TAIL ? min(c, D - 8) : c));
+  } else if (c == 0) {
 #pragma unroll
     for (int j = 0; j < 7; ++j)
-      if (c + j < D) r.v[j >> 1] |= (uint32_t)row[c + j] << (16 * (j & 1));
+      if (j < D) r.v[j >> 1] |= (uint32_t)row[j] << (16 * (j & 1));
   }
   return r;
 }
@@ -83,15 +85,52 @@ template <int TPR, bool TAIL>
 __device__ __forceinline__ Raw8<float> load8(const float* row, int v, int t, int D) {
   Raw8<float> r;
   const int c = column<TPR>(v, t);
-  if (TAIL ? c + 8 <= D : c < D) {
-    r.a = *reinterpret_cast<const f32x4_any*>(row + c);
-    r.b = *reinterpret_cast<const f32x4_any*>(row + c + 4);
-  } else if (TAIL) {
+  if (!TAIL || D >= 8) {
+    if (c < D) {
+      const float* p = row + (TAIL ? min(c, D - 8) : c);
+      r.a = *reinterpret_cast<const f32x4_any*>(p);
+      r.b = *reinterpret_cast<const f32x4_any*>(p + 4);
+    }
+  } else if (c == 0) {
 #pragma unroll
     for (int j = 0; j < 7; ++j)
-      if (c + j < D) (j < 4 ? r.a : r.b)[j & 3] = row[c + j];
+      if (j < D) (j < 4 ? r.a : r.b)[j & 3] = row[j];
   }
   return r;
+}
+
+template <int TPR, bool TAIL>
+__device__ __forceinline__ void in_place(Raw8<uint16_t>& r, int v, int t, int D) {
+  if constexpr (TAIL) {
+    const int by = column<TPR>(v, t) + 8 - D;  // values that lie past the row's end
+    if (D < 8 || !__any(by > 0 && by < 8)) return;
+    if (by <= 0 || by >= 8) return;
+    const uint64_t lo = (uint64_t)r.v[0] | ((uint64_t)r.v[1] << 32);
+    const uint64_t hi = (uint64_t)r.v[2] | ((uint64_t)r.v[3] << 32);
+    const int bits = 16 * by;
+    const uint64_t a = bits < 64 ? (lo >> bits) | (hi << (64 - bits)) : hi >> (bits - 64);
+    const uint64_t b = bits < 64 ? hi >> bits : 0;
+    r.v = u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
+  }
+}
+template <int TPR, bool TAIL>
+__device__ __forceinline__ void in_place(Raw8<float>& r, int v, int t, int D) {
+  if constexpr (TAIL) {
+    const int by = column<TPR>(v, t) + 8 - D;
+    if (D < 8 || !__any(by > 0 && by < 8)) return;
+    if (by <= 0 || by >= 8) return;
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = r.get(j);
+#pragma unroll
+    for (int k = 4; k >= 1; k >>= 1)
+      if (by & k) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = j + k < 8 ? x[(j + k) & 7] : 0.f;
+      }
+    r.a = f32x4{x[0], x[1], x[2], x[3]};
+    r.b = f32x4{x[4], x[5], x[6], x[7]};
+  }
 }
 
 template <int TPR, bool TAIL>
@@ -139,11 +178,14 @@ template <int TPR, bool TAIL>
 __device__ __forceinline__ Param8 load_param(const void* w, bool w32, int v, int t, int D) {
   Param8 p;
   if (w32) {
-    const Raw8<float> f = load8<TPR, TAIL>(static_cast<const float*>(w), v, t, D);
+    Raw8<float> f = load8<TPR, TAIL>(static_cast<const float*>(w), v, t, D);
+    in_place<TPR, TAIL>(f, v, t, D);
     p.lo = __builtin_bit_cast(u32x4, f.a);
     p.hi = __builtin_bit_cast(u32x4, f.b);
   } else {
-    p.lo = load8<TPR, TAIL>(static_cast<const uint16_t*>(w), v, t, D).v;
+    Raw8<uint16_t> h = load8<TPR, TAIL>(static_cast<const uint16_t*>(w), v, t, D);
+    in_place<TPR, TAIL>(h, v, t, D);
+    p.lo = h.v;
   }
   return p;
 }
@@ -237,6 +279,9 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_fwd(
     float x[NV][8];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
+      in_place<TPR, TAIL>(hv[v], v, t, D);
+      if (o) in_place<TPR, TAIL>(ov[v], v, t, D);
+      if (elem) in_place<TPR, TAIL>(gv[v], v, t, D);
       o_[v] = ov[v];
       g_[v] = gv[v];
 #pragma unroll
@@ -370,6 +415,11 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_bwd(
     Raw8<uint16_t> y_[NV], o_[NV], g_[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
+      in_place<TPR, TAIL>(hv[v], v, t, D);
+      in_place<TPR, TAIL>(yv[v], v, t, D);
+      if (dhn) in_place<TPR, TAIL>(dv[v], v, t, D);
+      if (o) in_place<TPR, TAIL>(ov[v], v, t, D);
+      if (elem) in_place<TPR, TAIL>(gv[v], v, t, D);
       h_[v] = hv[v];
       d_[v] = dv[v];
       y_[v] = yv[v];
@@ -512,13 +562,18 @@ __global__ __launch_bounds__(256) void k_norm_columns(
   for (int64_t m = blockIdx.y; m < n.M; m += gridDim.y) {
     const int64_t row = m * D;
     const f32x4 st = stats[m];
-    const Raw8<R> h = load8<1, TAIL>(hn + row, 0, t, D);
-    const Raw8<uint16_t> y = load8<1, TAIL>(dy + row, 0, t, D);
+    Raw8<R> h = load8<1, TAIL>(hn + row, 0, t, D);
+    Raw8<uint16_t> y = load8<1, TAIL>(dy + row, 0, t, D);
     Raw8<R> d;
     Raw8<uint16_t> ov, g;
     if (dhn) d = load8<1, TAIL>(dhn + row, 0, t, D);
     if (o) ov = load8<1, TAIL>(o + row, 0, t, D);
     if (elem) g = load8<1, TAIL>(static_cast<const uint16_t*>(n.gate) + row, 0, t, D);
+    in_place<1, TAIL>(h, 0, t, D);
+    in_place<1, TAIL>(y, 0, t, D);
+    in_place<1, TAIL>(d, 0, t, D);
+    in_place<1, TAIL>(ov, 0, t, D);
+    in_place<1, TAIL>(g, 0, t, D);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float x = h.get(j), dn = y.get(j) * w2.get(n.w32, j);
@@ -626,7 +681,8 @@ hipError_t norm_fwd(const BlockNorm& n, const void* h, const uint16_t* o, void* 
     constexpr int G = group_threads(TPR) / TPR;
     const int T = threads_of<TPR, NV>(n.D);
     const int64_t groups = (n.M + G - 1) / G;
-    const dim3 grid((unsigned)(walks(NV) ? std::min<int64_t>(groups, kFwdThreads / T) : groups));
+    const int64_t wgs = T > 512 ? kFwdThreads / 2048 * (1280 / T) : kFwdThreads / T;
+    const dim3 grid((unsigned)(walks(NV) ? std::min<int64_t>(groups, wgs) : groups));
     const NormArgs a = args_of(n);
     const R* hp = static_cast<const R*>(h);
     R* hn = static_cast<R*>(h_new);
