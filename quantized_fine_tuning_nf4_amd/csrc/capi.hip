@@ -786,11 +786,9 @@ qn_status block_norm_bwd(const qn_block_norm* n, const uint16_t* dy, const void*
 }
 
 size_t token_logprobs_workspace(int64_t T, int64_t V, qn_dtype dtype, int top_k) {
-  (void)T;
-  (void)V;
   (void)dtype;
-  (void)top_k;
-  return 0;
+  if (T < 1 || T > kMaxRowsM || V < 1 || V > kMaxVocab || top_k < 0) return 0;
+  return logprob_workspace(T, V, top_k);
 }
 
 qn_status token_logprobs_fwd(const void* logits, qn_dtype dtype, int64_t T, int64_t V, int64_t ld,
@@ -813,7 +811,7 @@ qn_status token_logprobs_fwd(const void* logits, qn_dtype dtype, int64_t T, int6
     if (workspace_bytes < need) return QN_EWORKSPACE;
   }
   return from_hip(launch_logprobs_fwd(logits, dtype == QN_F32, T, V, ld, targets, scale, top_k,
-                                      logp, entropy, stats, top_logp, top_ids,
+                                      logp, entropy, stats, top_logp, top_ids, workspace,
                                       static_cast<hipStream_t>(stream)));
 }
 
