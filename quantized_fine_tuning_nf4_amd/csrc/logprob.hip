@@ -165,18 +165,30 @@ struct Best {
       todo &= __ballot(x > bar);
     }
   }
-  // Before anything was offered: `top` is the best of a few of each lane's
-  // logits.  The k-th largest of the 64 bounds the k-th best logit from below.
-  __device__ __forceinline__ void start(float top, int k) {
-    const uint32_t u = ordered(top);
-    int above = 0;
+  // Before anything was offered: tops holds the best of a few logits of each
+  // lane of the workgroup, as ordered numbers.  The k-th largest of them bounds
+  // the k-th best logit from below; its leading 16 bits are enough (and all of
+  // a bf16), found bit by bit from how many lanes reach them.
+  __device__ __forceinline__ void start(const uint32_t* tops, int k) {
+    uint32_t u[kWaves], low = 0;
 #pragma unroll
-    for (int l = 0; l < 64; ++l) above += read_lane(u, l) > u ? 1 : 0;
-    const uint32_t low = reduce_wave(above < k ? u : 0xffffffffu,
-                                     [](uint32_t a, uint32_t b) { return min(a, b); });
+    for (int w = 0; w < kWaves; ++w) u[w] = tops[64 * w + (threadIdx.x & 63)];
+#pragma unroll
+    for (int b = 31; b >= 16; --b) {
+      const uint32_t c = low | (1u << b);
+      int n = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) n += __builtin_popcountll(__ballot(u[w] >= c));
+      if (n >= k) low = c;
+    }
+    at_least(low);
+  }
+  // k logits at least as large (as ordered numbers) are known.
+  __device__ __forceinline__ void at_least(uint32_t low) {
     const Key b = (Key)low << 32;  // below every key of that value
     if (b > bar) raise(b);
   }
+  __device__ __forceinline__ uint32_t known() const { return (uint32_t)(bar >> 32); }
 };
 
 // The other lane's key at distance D.
@@ -280,6 +292,14 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_fwd(const L* __restrict__
   }
   Stat a{-FLT_MAX, 0.f, 0.f};
   Best best;
+  // what each wave's bar is by now: a logit below any of them is none of the
+  // row's best.  Read and written without order: an old value only lets more
+  // through.
+  __shared__ uint32_t bars[kWaves], tops[TOP ? kThreads : 1];
+  if constexpr (TOP) {
+    if (tid < kWaves) bars[tid] = 0u;
+    __syncthreads();
+  }
   auto take = [&](Vec<L>(&v)[kU], int64_t i, bool first) {
     float top[kU], mx;
 #pragma unroll
@@ -299,7 +319,16 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_fwd(const L* __restrict__
         a.W = __builtin_fmaf(e, fmaxf(d, kFarBelow), a.W);
       }
     if constexpr (TOP) {
-      if (first) best.start(mx, out.k);
+      if (first) {
+        tops[tid] = ordered(mx);
+        __syncthreads();
+        best.start(tops, out.k);
+      } else {
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+          best.at_least(__builtin_amdgcn_readfirstlane(__hip_atomic_load(
+              &bars[w], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP)));
+      }
       if (__any(mx >= best.bar_value)) {
 #pragma unroll
         for (int u = 0; u < kU; ++u)
@@ -309,6 +338,9 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_fwd(const L* __restrict__
               best.offer(key_of(v[u].get(j), (uint32_t)(i + u * kStep + j)), out.k);
           }
       }
+      if (lane == 0)
+        __hip_atomic_store(&bars[wave], best.known(), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_WORKGROUP);
     }
   };
   int64_t i = begin + (int64_t)tid * N;
