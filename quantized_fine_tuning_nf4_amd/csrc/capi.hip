@@ -159,14 +159,13 @@ struct BwdWs {
   int Sv;
   float* dBpart;  // [Sb, rows, r]
   int Sb;
-  uint16_t* su;   // [2][rp][Mpb] (s u)^T high and remainder parts
+  uint16_t* su;   // [2][rp][Mpb] (s u)^T high and remainder parts ([3]: x in 8 bits)
   float* dApart;  // [Sa, cols, r]
   int Sa;
   uint16_t* sv;   // [2][rp][Mpa] (s v)^T
   uint16_t* wt;   // [cols, ldt] bf16 Qhat(W)^T (dense path)
   int64_t ldt;
   uint16_t* At;   // [cols, r] A^T (dense path)
-  uint16_t* x;    // [M, cols] the 8-bit checkpoint's values (act8)
 };
 
 BwdWs carve_bwd(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool need_u,
@@ -186,15 +185,15 @@ BwdWs carve_bwd(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool ne
   const int64_t rp = 16 * ((r + 15) / 16);
   b.Sb = thin_tn_slices(M, rows, r);
   b.dBpart = c.take<float>((size_t)b.Sb * rows * r);
-  b.su = c.take<uint16_t>((size_t)2 * rp * thin_tn_rows_padded(M, rows, r));
+  const size_t parts = act8 ? 3 : 2;
+  b.su = c.take<uint16_t>(parts * rp * thin_tn_rows_padded(M, rows, r));
   b.Sa = thin_tn_slices(M, cols, r);
   b.dApart = c.take<float>((size_t)b.Sa * cols * r);
-  b.sv = c.take<uint16_t>((size_t)2 * rp * thin_tn_rows_padded(M, cols, r));
+  b.sv = c.take<uint16_t>(parts * rp * thin_tn_rows_padded(M, cols, r));
   b.ldt = round_up(rows, 64);
   const bool dense = M > 0 && dense_path(M, cols);
   b.wt = dense ? c.take<uint16_t>((size_t)cols * b.ldt) : nullptr;
   b.At = dense ? c.take<uint16_t>((size_t)cols * r) : nullptr;
-  b.x = act8 ? c.take<uint16_t>((size_t)M * cols) : nullptr;
   return b;
 }
 
@@ -351,10 +350,6 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
   const float scale = lo.s;
   hipError_t e = hipSuccess;
   const float* u = u_saved;
-  if (x8) {
-    e = launch_act8_unpack(x8->codes, x8->exps, M, K, b.x, st);
-    x = b.x;
-  }
   // an early launch of the call zeroes the arrival counters the adapter
   // gradients' launch counts on, so the backward never depends on what the
   // workspace held before
@@ -401,6 +396,7 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
   aux.M = M;
   aux.r = r;
   aux.s = scale;
+  aux.three_parts = x8 != nullptr;
   if (e == hipSuccess) {
     if (dense_dx)
       e = launch_dequant_t(w->packed, w->qscale, w->scale2, w->offset, N, K, b.wt, b.ldt, aux,
@@ -420,8 +416,9 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
   // dB = s G^T u and dA = s v^T X in one launch (and their slice sums in one)
   if (e == hipSuccess)
     e = launch_thin_tn2(ThinTn{dY, b.su, N, dB, false, b.dBpart},
-                        ThinTn{x, b.sv, K, dA, true, b.dApart, lo.mask}, M, r, b.arrivals,
-                        st);
+                        ThinTn{x, b.sv, K, dA, true, b.dApart, lo.mask, x8 ? x8->codes : nullptr,
+                               x8 ? x8->exps : nullptr},
+                        M, r, b.arrivals, st);
   return from_hip(e);
 }
 

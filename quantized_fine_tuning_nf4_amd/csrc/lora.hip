@@ -6,7 +6,8 @@
 //                                     M rows, split in slices whose partial
 //                                     sums are added in slice order.
 // All use v_mfma_f32_16x16x32_bf16; fp32 operands (u, v) enter the MFMA as a
-// bf16 high part plus a bf16 remainder, so they keep ~16 significant bits.
+// bf16 high part plus a bf16 remainder, so they keep ~16 significant bits (or,
+// in the backward from an 8-bit checkpoint, as three parts: all 24).
 #include <algorithm>
 #include <type_traits>
 
@@ -408,10 +409,13 @@ constexpr int TN_NST = 3;  // stages (two steps in flight; three: 1.5 us slower 
 // Z row y's 16-byte chunk c sits at unit c ^ 2(y & 3); the A operand (16
 // columns x 32 rows) is read transposed with ds_read_b64_tr_b16, lane t of a
 // 16-lane group addressing row 4h + t/4, columns 4(t%4)..+3, so that lane t
-// receives column t, four consecutive rows.  NJ = ceil(r/16).
+// receives column t, four consecutive rows.  NJ = ceil(r/16); SP: the parts of
+// (s V)^T.
 struct TnJob {
-  const uint16_t* Z;   // [M, P] bf16
-  const uint16_t* vt;  // [2][16 NJ][Mp] (s V)^T high and remainder parts
+  const uint16_t* Z;   // [M, P] bf16 ...
+  const int8_t* codes; // ... or an 8-bit checkpoint of it: codes [M, P]
+  const uint8_t* exps; // and exponents [M, ceil(P / 64)]
+  const uint16_t* vt;  // [SP][16 NJ][Mp] (s V)^T in parts
   int64_t Mp;
   int64_t P;
   int64_t slice;       // rows per slice, a multiple of 32
@@ -437,15 +441,8 @@ constexpr int kDeviceScope = 16;  // sc1: the level every XCD shares
 // vmcnt wait for the given count (an immediate of the instruction).
 template <int N>
 __device__ __forceinline__ void wait_vm() {
-  static_assert(N >= 4 && N <= 11, "counts of k_thin_tn's steps");
-  if constexpr (N == 4) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
-  else if constexpr (N == 5) asm volatile("s_waitcnt vmcnt(5)" ::: "memory");
-  else if constexpr (N == 6) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
-  else if constexpr (N == 7) asm volatile("s_waitcnt vmcnt(7)" ::: "memory");
-  else if constexpr (N == 8) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
-  else if constexpr (N == 9) asm volatile("s_waitcnt vmcnt(9)" ::: "memory");
-  else if constexpr (N == 10) asm volatile("s_waitcnt vmcnt(10)" ::: "memory");
-  else asm volatile("s_waitcnt vmcnt(11)" ::: "memory");
+  static_assert(N >= 4 && N <= 63, "counts of k_thin_tn's steps");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
 // MASK: a job may carry keep bits of Z (dropout on the adapter branch's
@@ -453,11 +450,26 @@ __device__ __forceinline__ void wait_vm() {
 // beside Z (one 4-byte-per-lane load in waves 0 and 1: rows 16w .. 16w+15;
 // the direct-to-LDS path writes one dword per lane), and the dropped values
 // are zeroed in the A operand after the transposed reads.
-template <int NJ, bool MASK>
+//
+// Z8: the second job's Z is an 8-bit checkpoint.  Its 32 rows of 128 codes are
+// half the bytes of bf16 rows: one 16-byte-per-lane load per wave (8 rows each;
+// row y's 16-byte chunk c at unit c ^ ((y >> 1) & 7), so that the 16 rows of a
+// transposed read fill 256 bytes of banks), read as columns by
+// ds_read_b64_tr_b8 (lane t of a 16-lane group addresses row t / 2, columns
+// 8 (t % 2) .. + 7 and receives column t, eight rows: a lane's whole part of the
+// A operand).  A lane loads one of its group's eight rows' exponents into a
+// register, two steps ahead; the rows' scales reach the 16 lanes by DPP, and
+// code times scale is a bf16 number exactly, so the MFMA sees the checkpoint's
+// values.
+template <int Q>
+__device__ __forceinline__ float row_scale(float scale) {
+  return as_f32(dpp<0x150 + Q>(as_u32(scale)));  // row_newbcast: lane Q of each 16
+}
+template <int NJ, bool MASK, int SP, bool Z8>
 __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_t M, int r,
                                                       unsigned* __restrict__ arrivals) {
   constexpr int ZB = 32 * TN_ROWB;             // Z bytes per stage
-  constexpr int VB = 2 * 16 * NJ * 64;         // (sV)^T bytes per stage
+  constexpr int VB = SP * 16 * NJ * 64;        // (sV)^T bytes per stage
   constexpr int KB = MASK ? 32 * 16 : 0;       // keep bits per stage
   constexpr int SB = ZB + VB + KB;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -472,6 +484,7 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
   float* part = second ? j1.part : j0.part;
   const uint8_t* zmask = MASK ? (second ? j1.zmask : j0.zmask) : nullptr;
   const bool hm = MASK && zmask != nullptr;  // workgroup-uniform
+  const bool z8 = Z8 && second;              // workgroup-uniform
   if ((int)blockIdx.y >= S) return;
   const int64_t p0 = (int64_t)((int)blockIdx.x - (second ? j0.tiles : 0)) * TN_COLS;
   const int64_t mb = (int64_t)blockIdx.y * slice;
@@ -483,16 +496,24 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
   // (l%16) ^ 2(row & 3).  Rows past M repeat row M-1 (their sV is zero);
   // columns past P repeat the last chunk (their outputs are not stored).
   // (sV)^T loads: 4 of its 64-byte rows per 4-byte-per-lane instruction
-  // (lane l: row 4q + l/16, word l%16), instruction q = 2 NJ w + k of the
+  // (lane l: row 4q + l/16, word l%16), instruction q = SP NJ w + k of the
   // step (all lanes active: no branch around a load into LDS).
   // descriptors start at the slice's first row, so that only one slice's
   // bytes (below 2^31, thin_tn_slice_rows) are ever addressed by an offset
-  const rsrc_t rz = make_rs(Z + mb * P, (uint32_t)((me - mb) * P * 2));
-  const rsrc_t rv = make_rs(vt + mb, (uint32_t)((2 * 16 * NJ * Mp - mb) * 2));
+  const rsrc_t rz = make_rs(z8 ? reinterpret_cast<const void*>(j1.codes + mb * P)
+                               : reinterpret_cast<const void*>(Z + mb * P),
+                            (uint32_t)((me - mb) * P * (z8 ? 1 : 2)));
+  const rsrc_t rv = make_rs(vt + mb, (uint32_t)((SP * 16 * NJ * Mp - mb) * 2));
   // keep bits from the slice's first row (P % 64 == 0: rows start on a byte);
   // bytes past the slice read as zero (columns past P are not stored)
-  const rsrc_t rk = make_rs(hm ? zmask + mb * P / 8 : reinterpret_cast<const uint8_t*>(Z),
+  const rsrc_t rk = make_rs(hm ? zmask + mb * P / 8 : reinterpret_cast<const uint8_t*>(vt),
                             hm ? (uint32_t)((me - mb) * P / 8) : 0u);
+  // the checkpoint's exponents from the slice's first row, this wave's block of
+  // columns
+  const int64_t nb = (P + kAct8Block - 1) / kAct8Block;
+  const rsrc_t re = make_rs(z8 ? j1.exps + mb * nb : reinterpret_cast<const uint8_t*>(vt),
+                            z8 ? (uint32_t)((me - mb) * nb) : 0u);
+  const uint32_t eoff = (uint32_t)min((p0 + 32 * wave) / kAct8Block, nb - 1);
   uint32_t zoff[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -501,134 +522,194 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
     const int64_t col = min(p0 + 8 * chunk, P - 8);
     zoff[h] = (uint32_t)(col * 2);
   }
-  uint32_t voff[2 * NJ];
+  uint32_t voff[SP * NJ];
 #pragma unroll
-  for (int k = 0; k < 2 * NJ; ++k) {
-    const int q = 2 * NJ * wave + k, row = 4 * q + (lane >> 4);
+  for (int k = 0; k < SP * NJ; ++k) {
+    const int q = SP * NJ * wave + k, row = 4 * q + (lane >> 4);
     voff[k] = (uint32_t)(row * Mp * 2 + 4 * (lane & 15));
   }
-  auto load_step = [&](int st, int stage) {
-    uint8_t* base = smem + stage * SB;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = 2 * wave + h, row = 4 * i + (lane >> 4);
-      const int64_t mm = min(mb + 32 * (int64_t)st + row, M - 1);
-      dma16(rz, zoff[h] + (uint32_t)((mm - mb) * P * 2), 0, base + 1024 * i);
-    }
-#pragma unroll
-    for (int k = 0; k < 2 * NJ; ++k)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_void*)(base + ZB + 256 * (2 * NJ * wave + k)),
-                                               4, voff[k] + (uint32_t)(64 * st), 0, 0, 0);
-    if constexpr (MASK) {
-      if (hm && wave < 2) {  // lane l: row 16w + l/4, bytes 4(l%4) .. +3 of the tile's 16
-        const int row = 16 * wave + (lane >> 2);
-        const int64_t mm = min(mb + 32 * (int64_t)st + row, M - 1);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rk, (lds_void*)(base + ZB + VB + 256 * wave), 4,
-            (uint32_t)((((mm - mb) * P + p0) >> 3) + 4 * (lane & 3)), 0, 0, 0);
-      }
-    }
-  };
-  // all but the newest step's loads (2 + 2 NJ per wave) have landed
-  // (one more in waves 0 and 1 when the keep bits come along)
-  auto wait_step = [&]() {
-    static_assert(TN_NST == 3, "one step in flight beyond the next");
-    if (MASK && hm && wave < 2)
-      wait_vm<2 + 2 * NJ + (MASK ? 1 : 0)>();
-    else
-      wait_vm<2 + 2 * NJ>();
-  };
-  for (int k = 0; k < TN_NST - 1; ++k) load_step(min(k, steps - 1), k);
-  wait_step();
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-
-  // transposed-read addresses: lane l, group g = l/16, t = l%16; p-tile pt,
-  // half h: row 8g + 4h + t/4, column 32w + 16pt + 4(t%4)
+  // the steps, on codes or on bf16
   const int g = lane >> 4, t = lane & 15;
-  int aoff[2][2];
-#pragma unroll
-  for (int pt = 0; pt < 2; ++pt)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = 8 * g + 4 * h + (t >> 2);
-      const int col = 32 * wave + 16 * pt + 4 * (t & 3);
-      aoff[pt][h] = row * TN_ROWB + 16 * ((col >> 3) ^ (2 * (row & 3))) + 2 * (col & 7);
-    }
   f32x4 acc[2][NJ] = {};
-  // one step on stage P (a constant, so that the compiler sees the loads of
-  // step st+2 and this step's LDS reads touch different stages)
-  auto body = [&](auto p_t, int st) {
-    constexpr int P = decltype(p_t)::value;
-    load_step(min(st + TN_NST - 1, steps - 1), (P + TN_NST - 1) % TN_NST);
-    const uint8_t* zs = smem + P * SB;
-    // the four transposed reads in one block that also waits for them (the
-    // compiler would otherwise treat them as possibly overlapping the loads
-    // in flight to the other stages and wait for all of those first)
-    const uint32_t zb = (uint32_t)reinterpret_cast<uintptr_t>(zs);
-    u32x2 x00, x01, x10, x11;
-    asm volatile(
-        "ds_read_b64_tr_b16 %0, %4\n\t"
-        "ds_read_b64_tr_b16 %1, %5\n\t"
-        "ds_read_b64_tr_b16 %2, %6\n\t"
-        "ds_read_b64_tr_b16 %3, %7\n\t"
-        "s_waitcnt lgkmcnt(0)"
-        // early-clobber: a result must not share a register with an address
-        // that a later read of the block still has to issue with
-        : "=&v"(x00), "=&v"(x01), "=&v"(x10), "=&v"(x11)
-        : "v"(zb + aoff[0][0]), "v"(zb + aoff[0][1]), "v"(zb + aoff[1][0]), "v"(zb + aoff[1][1])
-        : "memory");
-    u32x4 za[2] = {u32x4{x00[0], x00[1], x01[0], x01[1]}, u32x4{x10[0], x10[1], x11[0], x11[1]}};
-    if constexpr (MASK) {
-      if (hm) {
-        // word i of za[pt] holds rows 8g + 2i, 8g + 2i + 1 of column
-        // 32w + 16pt + t, whose keep bits are bit 16pt + t of the word at
-        // byte 4w of each row's 16 bytes
-        const uint8_t* ks = zs + ZB + VB + 4 * wave;
-        uint32_t kw[8];
+  auto run = [&](auto q8_t) {
+    constexpr bool Q8 = decltype(q8_t)::value;
+    uint32_t ex[TN_NST] = {};  // per stage: the exponent of row 8 (l / 16) + l % 8
+    auto load_step = [&](int st, auto stage_t) {
+      constexpr int stage = decltype(stage_t)::value;
+      uint8_t* base = smem + stage * SB;
+      if constexpr (Q8) {  // row 8w + l/8, unit l%8
+        const int row = 8 * wave + (lane >> 3);
+        const int chunk = (lane & 7) ^ ((row >> 1) & 7);
+        const int64_t mm = min(mb + 32 * (int64_t)st + row, M - 1);
+        dma16(rz, (uint32_t)((mm - mb) * P + min(p0 + 16 * chunk, P - 16)), 0, base + 1024 * wave);
+        const int64_t me8 = min(mb + 32 * (int64_t)st + 8 * (lane >> 4) + (lane & 7), M - 1);
+        ex[stage] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(
+            re, (uint32_t)((me8 - mb) * nb) + eoff, 0, 0);
+      } else {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          kw[q] = *reinterpret_cast<const uint32_t*>(ks + 16 * (8 * g + q));
-#pragma unroll
-        for (int pt = 0; pt < 2; ++pt) {
-          const int sh = 16 * pt + t;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            za[pt][i] &= (((kw[2 * i] >> sh) & 1u) * 0xffffu) |
-                         (((kw[2 * i + 1] >> sh) & 1u) * 0xffff0000u);
+        for (int h = 0; h < 2; ++h) {
+          const int i = 2 * wave + h, row = 4 * i + (lane >> 4);
+          const int64_t mm = min(mb + 32 * (int64_t)st + row, M - 1);
+          dma16(rz, zoff[h] + (uint32_t)((mm - mb) * P * 2), 0, base + 1024 * i);
         }
       }
-    }
-    bf16x8 a[2];
-    a[0] = as_bf16x8(za[0]);
-    a[1] = as_bf16x8(za[1]);
 #pragma unroll
-    for (int jt = 0; jt < NJ; ++jt) {
-      // B operand: column j = 16jt + l%16, rows 8g..8g+7 of the step
-      const uint8_t* vs = zs + ZB + (16 * jt + t) * 64 + 16 * g;
-      const bf16x8 bh = as_bf16x8(*reinterpret_cast<const u32x4*>(vs));
-      const bf16x8 bl = as_bf16x8(*reinterpret_cast<const u32x4*>(vs + 16 * NJ * 64));
-#pragma unroll
-      for (int pt = 0; pt < 2; ++pt) {
-        acc[pt][jt] = mfma16(a[pt], bh, acc[pt][jt]);
-        acc[pt][jt] = mfma16(a[pt], bl, acc[pt][jt]);
+      for (int k = 0; k < SP * NJ; ++k)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rv, (lds_void*)(base + ZB + 256 * (SP * NJ * wave + k)), 4,
+            voff[k] + (uint32_t)(64 * st), 0, 0, 0);
+      if constexpr (MASK) {
+        if (hm && wave < 2) {  // lane l: row 16w + l/4, bytes 4(l%4) .. +3 of the tile's 16
+          const int row = 16 * wave + (lane >> 2);
+          const int64_t mm = min(mb + 32 * (int64_t)st + row, M - 1);
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(
+              rk, (lds_void*)(base + ZB + VB + 256 * wave), 4,
+              (uint32_t)((((mm - mb) * P + p0) >> 3) + 4 * (lane & 3)), 0, 0, 0);
+        }
       }
-    }
-    // step st+1's loads (issued 2 steps ago) have landed everywhere before
-    // anyone reads them or overwrites this stage
+    };
+    // all but the newest step's loads (2 + SP NJ per wave: Z or the codes and
+    // their exponents, then (sV)^T) have landed (one more in waves 0 and 1 when
+    // the keep bits come along)
+    auto wait_step = [&]() {
+      static_assert(TN_NST == 3, "one step in flight beyond the next");
+      if (MASK && hm && wave < 2)
+        wait_vm<2 + SP * NJ + (MASK ? 1 : 0)>();
+      else
+        wait_vm<2 + SP * NJ>();
+    };
+    load_step(0, std::integral_constant<int, 0>{});
+    load_step(min(1, steps - 1), std::integral_constant<int, 1>{});
     wait_step();
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+    // transposed-read addresses: lane l, group g = l/16, t = l%16; p-tile pt,
+    // half h: row 8g + 4h + t/4, column 32w + 16pt + 4(t%4)
+    int aoff[2][2];
+#pragma unroll
+    for (int pt = 0; pt < 2; ++pt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = 8 * g + 4 * h + (t >> 2);
+        const int col = 32 * wave + 16 * pt + 4 * (t & 3);
+        aoff[pt][h] = row * TN_ROWB + 16 * ((col >> 3) ^ (2 * (row & 3))) + 2 * (col & 7);
+      }
+    // the same for codes: p-tile pt, row 8g + t/2, columns 32w + 16pt + 8(t%2)
+    int aoff8[2];
+#pragma unroll
+    for (int pt = 0; pt < 2; ++pt) {
+      const int row = 8 * g + (t >> 1);
+      aoff8[pt] = row * TN_COLS + 16 * ((2 * wave + pt) ^ ((row >> 1) & 7)) + 8 * (t & 1);
+    }
+    // one step on stage P (a constant, so that the compiler sees the loads of
+    // step st+2 and this step's LDS reads touch different stages)
+    auto body = [&](auto p_t, int st) {
+      constexpr int P = decltype(p_t)::value;
+      load_step(min(st + TN_NST - 1, steps - 1),
+                std::integral_constant<int, (P + TN_NST - 1) % TN_NST>{});
+      const uint8_t* zs = smem + P * SB;
+      // the four transposed reads in one block that also waits for them (the
+      // compiler would otherwise treat them as possibly overlapping the loads
+      // in flight to the other stages and wait for all of those first)
+      const uint32_t zb = (uint32_t)reinterpret_cast<uintptr_t>(zs);
+      u32x4 za[2];
+      if constexpr (Q8) {
+        u32x2 c[2];
+        asm volatile(
+            "ds_read_b64_tr_b8 %0, %2\n\t"
+            "ds_read_b64_tr_b8 %1, %3\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(c[0]), "=&v"(c[1])
+            : "v"(zb + aoff8[0]), "v"(zb + aoff8[1])
+            : "memory");
+        const float scale = act8_scale(ex[P]);
+        const float rs[8] = {row_scale<0>(scale), row_scale<1>(scale), row_scale<2>(scale),
+                             row_scale<3>(scale), row_scale<4>(scale), row_scale<5>(scale),
+                             row_scale<6>(scale), row_scale<7>(scale)};
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w = c[pt][i >> 1] >> (16 * (i & 1));
+            za[pt][i] = pack_bf16x2((float)(int8_t)w * rs[2 * i], (float)(int8_t)(w >> 8) * rs[2 * i + 1]);
+          }
+      } else {
+        u32x2 x00, x01, x10, x11;
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %4\n\t"
+            "ds_read_b64_tr_b16 %1, %5\n\t"
+            "ds_read_b64_tr_b16 %2, %6\n\t"
+            "ds_read_b64_tr_b16 %3, %7\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            // early-clobber: a result must not share a register with an address
+            // that a later read of the block still has to issue with
+            : "=&v"(x00), "=&v"(x01), "=&v"(x10), "=&v"(x11)
+            : "v"(zb + aoff[0][0]), "v"(zb + aoff[0][1]), "v"(zb + aoff[1][0]), "v"(zb + aoff[1][1])
+            : "memory");
+        za[0] = u32x4{x00[0], x00[1], x01[0], x01[1]};
+        za[1] = u32x4{x10[0], x10[1], x11[0], x11[1]};
+      }
+      if constexpr (MASK) {
+        if (hm) {
+          // word i of za[pt] holds rows 8g + 2i, 8g + 2i + 1 of column
+          // 32w + 16pt + t, whose keep bits are bit 16pt + t of the word at
+          // byte 4w of each row's 16 bytes
+          const uint8_t* ks = zs + ZB + VB + 4 * wave;
+          uint32_t kw[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            kw[q] = *reinterpret_cast<const uint32_t*>(ks + 16 * (8 * g + q));
+#pragma unroll
+          for (int pt = 0; pt < 2; ++pt) {
+            const int sh = 16 * pt + t;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              za[pt][i] &= (((kw[2 * i] >> sh) & 1u) * 0xffffu) |
+                           (((kw[2 * i + 1] >> sh) & 1u) * 0xffff0000u);
+          }
+        }
+      }
+      bf16x8 a[2];
+      a[0] = as_bf16x8(za[0]);
+      a[1] = as_bf16x8(za[1]);
+#pragma unroll
+      for (int jt = 0; jt < NJ; ++jt) {
+        // B operand: column j = 16jt + l%16, rows 8g..8g+7 of the step
+        const uint8_t* vs = zs + ZB + (16 * jt + t) * 64 + 16 * g;
+        bf16x8 b[SP];
+#pragma unroll
+        for (int q = 0; q < SP; ++q)
+          b[q] = as_bf16x8(*reinterpret_cast<const u32x4*>(vs + q * 16 * NJ * 64));
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt)
+#pragma unroll
+          for (int q = 0; q < SP; ++q) acc[pt][jt] = mfma16(a[pt], b[q], acc[pt][jt]);
+      }
+      // step st+1's loads (issued 2 steps ago) have landed everywhere before
+      // anyone reads them or overwrites this stage
+      wait_step();
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    };
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
+    using S2 = std::integral_constant<int, 2>;
+    int st = 0;
+    for (; st + 3 <= steps; st += 3) {
+      body(S0{}, st);
+      body(S1{}, st + 1);
+      body(S2{}, st + 2);
+    }
+    if (st < steps) body(S0{}, st);
+    if (st + 1 < steps) body(S1{}, st + 1);
   };
-  using S0 = std::integral_constant<int, 0>;
-  using S1 = std::integral_constant<int, 1>;
-  using S2 = std::integral_constant<int, 2>;
-  int st = 0;
-  for (; st + 3 <= steps; st += 3) {
-    body(S0{}, st);
-    body(S1{}, st + 1);
-    body(S2{}, st + 2);
+  if constexpr (Z8) {
+    if (z8)
+      run(std::true_type{});
+    else
+      run(std::false_type{});
+  } else {
+    run(std::false_type{});
   }
-  if (st < steps) body(S0{}, st);
-  if (st + 1 < steps) body(S1{}, st + 1);
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   // lane: column j = 16jt + l%16, rows p = 16pt + 4(l/16) + i of the wave
   const int S_ = S;
@@ -800,12 +881,14 @@ hipError_t launch_thin_tn2(const ThinTn& a, const ThinTn& b, int64_t M, int r,
     const ThinTn& x = *in[k];
     TnJob& j = job[k];
     j.Z = x.Z;
+    j.codes = x.codes;
+    j.exps = x.exps;
     j.vt = x.vt;
     j.Mp = thin_tn_rows_padded(M, x.P, r);
     j.P = x.P;
     j.slice = thin_tn_slice_rows(M, x.P, r);
     j.S = thin_tn_slices(M, x.P, r);
-    j.tiles = x.Z ? (int)((x.P + TN_COLS - 1) / TN_COLS) : 0;
+    j.tiles = x.Z || x.codes ? (int)((x.P + TN_COLS - 1) / TN_COLS) : 0;
     j.part = x.part;
     j.out = x.out;
     j.transposed = x.transposed ? 1 : 0;
@@ -818,15 +901,23 @@ hipError_t launch_thin_tn2(const ThinTn& a, const ThinTn& b, int64_t M, int r,
   // tile), else by a second launch
   unsigned* ctr = tiles <= kTnMaxTiles ? arrivals : nullptr;
   const bool mask = (job[0].tiles > 0 && job[0].zmask) || (job[1].tiles > 0 && job[1].zmask);
-  const size_t lds = (size_t)TN_NST * (32 * TN_ROWB + 2 * 16 * nj * 64 + (mask ? 32 * 16 : 0));
+  const bool z8 = b.codes != nullptr;
+  if (a.codes) return hipErrorInvalidValue;  // a checkpoint is the second job's
+  const size_t lds =
+      (size_t)TN_NST * (32 * TN_ROWB + (z8 ? 3 : 2) * 16 * nj * 64 + (mask ? 32 * 16 : 0));
   const dim3 grid((unsigned)tiles, (unsigned)s_max);
-#define QN_TN(NJ)                                                                              \
-  if (mask)                                                                                    \
-    hipLaunchKernelGGL((k_thin_tn<NJ, true>), grid, dim3(kThreads), lds, st, job[0], job[1], M, \
-                       r, ctr);                                                                \
-  else                                                                                         \
-    hipLaunchKernelGGL((k_thin_tn<NJ, false>), grid, dim3(kThreads), lds, st, job[0], job[1], M, \
-                       r, ctr)
+#define QN_TN2(NJ, MASK, SP, Z8)                                                           \
+  hipLaunchKernelGGL((k_thin_tn<NJ, MASK, SP, Z8>), grid, dim3(kThreads), lds, st, job[0], job[1], \
+                     M, r, ctr)
+#define QN_TN(NJ)                      \
+  if (z8 && mask)                      \
+    QN_TN2(NJ, true, 3, true);         \
+  else if (z8)                         \
+    QN_TN2(NJ, false, 3, true);        \
+  else if (mask)                       \
+    QN_TN2(NJ, true, 2, false);        \
+  else                                 \
+    QN_TN2(NJ, false, 2, false)
   switch (nj) {
     case 1: QN_TN(1); break;
     case 2: QN_TN(2); break;
@@ -834,12 +925,13 @@ hipError_t launch_thin_tn2(const ThinTn& a, const ThinTn& b, int64_t M, int r,
     default: QN_TN(4); break;
   }
 #undef QN_TN
+#undef QN_TN2
   if (ctr) return hipGetLastError();
   TnSum sum[2];
   int64_t count = 0;
   for (int k = 0; k < 2; ++k) {
     const ThinTn& x = *in[k];
-    sum[k] = TnSum{x.part, x.Z ? x.P : 0, job[k].S, x.transposed, x.out};
+    sum[k] = TnSum{x.part, job[k].tiles > 0 ? x.P : 0, job[k].S, x.transposed, x.out};
     count += sum[k].P * r;
   }
   hipLaunchKernelGGL(k_sum_slices_tn, dim3((unsigned)((count + 255) / 256)), dim3(256), 0, st,

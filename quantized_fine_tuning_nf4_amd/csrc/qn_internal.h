@@ -52,7 +52,8 @@ hipError_t launch_dequant(const uint8_t* packed, const uint8_t* qscale, const fl
 // Small backward jobs, run by spare workgroups of another launch or alone:
 //   Bt [r, N] = B[N, r]^T and At [K, r] = A[r, K]^T (bf16);
 //   su = (s u)^T and sv = (s v)^T, each [2][16 ceil(r/16)][Mp] bf16 (high
-//   parts, then remainders; zero for j >= r or m >= M), u and v fp32 [M, r];
+//   parts, then remainders; with three_parts [3][...]: the remainder in two;
+//   zero for j >= r or m >= M), u and v fp32 [M, r];
 //   when Sv > 1, v is first written as the slice sum of vpart [Sv][M][r].
 // A null destination skips its job.  One thread per output element.
 struct BwdAux {
@@ -73,6 +74,7 @@ struct BwdAux {
   int64_t M;
   int r;
   float s;
+  bool three_parts;
 };
 // The jobs are rows, one per thread: a row n of B (Bt[j][n] = B[n][j]), a
 // column k of A (At[k][j] = A[j][k]), a column m of su and of sv (all rp
@@ -82,11 +84,15 @@ struct BwdAux {
 __host__ __device__ inline int64_t bwd_aux_count(const BwdAux& a) {
   return (a.Bt ? a.N : 0) + (a.At ? a.K : 0) + (a.su ? a.Mpu : 0) + (a.sv ? a.Mpv : 0);
 }
-// x as bf16 at dst[idx] and its remainder as bf16 at dst[half + idx]
-__device__ inline void put_split(uint16_t* dst, int64_t half, int64_t idx, float x) {
+// x as bf16 at dst[idx] and its remainder as bf16 at dst[half + idx] (three:
+// what that leaves at dst[2 half + idx])
+__device__ inline void put_split(uint16_t* dst, int64_t half, int64_t idx, float x, bool three) {
   const uint32_t h = pack_bf16x2(x, 0.f) & 0xffffu;
   dst[idx] = (uint16_t)h;
-  dst[half + idx] = (uint16_t)(pack_bf16x2(x - bf16_lo(h), 0.f) & 0xffffu);
+  const float rest = x - bf16_lo(h);
+  const uint32_t l = pack_bf16x2(rest, 0.f) & 0xffffu;
+  dst[half + idx] = (uint16_t)l;
+  if (three) dst[2 * half + idx] = (uint16_t)(pack_bf16x2(rest - bf16_lo(l), 0.f) & 0xffffu);
 }
 // row job i of the concatenated jobs (Bt, At, su, sv in that order)
 __device__ inline void bwd_aux_at(const BwdAux& a, int64_t i) {
@@ -184,7 +190,8 @@ __device__ inline void bwd_aux_at(const BwdAux& a, int64_t i) {
       }
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) put_split(dst, half, (int64_t)(j0 + q) * Mp + m, a.s * x[q]);
+    for (int q = 0; q < 4; ++q) put_split(dst, half, (int64_t)(j0 + q) * Mp + m, a.s * x[q],
+                                         a.three_parts);
   }
 }
 hipError_t launch_bwd_aux(const BwdAux& a, hipStream_t st);
@@ -258,8 +265,9 @@ hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t st);
 
 
 // One transposed adapter product out = Z^T (s V), reduced over the M rows:
-// Z bf16 [M, P] (null: no product), vt = (s V)^T split as BwdAux makes it
-// with Mp = thin_tn_rows_padded(M, P, r); transposed == false: out fp32
+// Z bf16 [M, P] (null: no product) or, for the second product, an 8-bit
+// checkpoint of it (codes and exps; P % 64 == 0), vt = (s V)^T split as BwdAux
+// makes it (in three parts for both products when there are codes) with Mp = thin_tn_rows_padded(M, P, r); transposed == false: out fp32
 // [P, r]; true: out fp32 [r, P].  Split over thin_tn_slices(M, P, r) row
 // slices with partials part[S][P][r], summed in slice order.  P % 8 == 0.
 struct ThinTn {
@@ -270,6 +278,8 @@ struct ThinTn {
   bool transposed;
   float* part;
   const uint8_t* zmask = nullptr;  // keep bits of Z [M, P] (dropout), or null
+  const int8_t* codes = nullptr;
+  const uint8_t* exps = nullptr;
 };
 // Two such products (same M and r) in one launch; the slices are added by
 // the last workgroup of each column tile to finish (arrivals: kArrivalWords
