@@ -402,10 +402,9 @@ constexpr int TN_NST = 3;  // stages (two steps in flight; three: 1.5 us slower 
 // independent products (dB and dA of one backward) share the launch: grid x
 // runs over the column tiles of job 0, then those of job 1.  Workgroup
 // (pt, z): columns 128 pt .. +127, wave w: 32w .. 32w+31 (two 16-column MFMA
-// tiles).  A step is 32 rows: their Z (8 KB) and their (s V)^T high and
-// remainder parts (2 x 16 NJ rows of 64 B) go global -> LDS by buffer loads
-// into one stage, three stages deep, every wave issuing 2 + 2 NJ loads per
-// step.
+// tiles).  A step is 32 rows: their Z (8 KB) and their (s V)^T parts (SP x 16 NJ
+// rows of 64 B) go global -> LDS by 16-byte-per-lane buffer loads into one
+// stage, three stages deep.
 // Z row y's 16-byte chunk c sits at unit c ^ 2(y & 3); the A operand (16
 // columns x 32 rows) is read transposed with ds_read_b64_tr_b16, lane t of a
 // 16-lane group addressing row 4h + t/4, columns 4(t%4)..+3, so that lane t
@@ -441,7 +440,7 @@ constexpr int kDeviceScope = 16;  // sc1: the level every XCD shares
 // vmcnt wait for the given count (an immediate of the instruction).
 template <int N>
 __device__ __forceinline__ void wait_vm() {
-  static_assert(N >= 4 && N <= 63, "counts of k_thin_tn's steps");
+  static_assert(N >= 3 && N <= 63, "counts of k_thin_tn's steps");
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
@@ -495,9 +494,10 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
   // issues i = 2w, 2w+1; lane l -> row 4i + l/16, unit l%16, source chunk
   // (l%16) ^ 2(row & 3).  Rows past M repeat row M-1 (their sV is zero);
   // columns past P repeat the last chunk (their outputs are not stored).
-  // (sV)^T loads: 4 of its 64-byte rows per 4-byte-per-lane instruction
-  // (lane l: row 4q + l/16, word l%16), instruction q = SP NJ w + k of the
-  // step (all lanes active: no branch around a load into LDS).
+  // (sV)^T loads: 16 of its 64-byte rows per instruction (lane l: row 16q + l/4,
+  // bytes 16 (l%4)), instruction q = VL w + k of the step; where SP NJ is no
+  // multiple of four, the last waves load the last rows again (the same bytes
+  // to the same place), so that every wave counts the same loads.
   // descriptors start at the slice's first row, so that only one slice's
   // bytes (below 2^31, thin_tn_slice_rows) are ever addressed by an offset
   const rsrc_t rz = make_rs(z8 ? reinterpret_cast<const void*>(j1.codes + mb * P)
@@ -522,11 +522,14 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
     const int64_t col = min(p0 + 8 * chunk, P - 8);
     zoff[h] = (uint32_t)(col * 2);
   }
-  uint32_t voff[SP * NJ];
+  constexpr int VL = (SP * NJ + 3) / 4;
+  uint32_t voff[VL];
+  int vdst[VL];
 #pragma unroll
-  for (int k = 0; k < SP * NJ; ++k) {
-    const int q = SP * NJ * wave + k, row = 4 * q + (lane >> 4);
-    voff[k] = (uint32_t)(row * Mp * 2 + 4 * (lane & 15));
+  for (int k = 0; k < VL; ++k) {
+    const int q = min(VL * wave + k, SP * NJ - 1), row = 16 * q + (lane >> 2);
+    voff[k] = (uint32_t)(row * Mp * 2 + 16 * (lane & 3));
+    vdst[k] = ZB + 1024 * q;
   }
   // the steps, on codes or on bf16
   const int g = lane >> 4, t = lane & 15;
@@ -554,10 +557,8 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
         }
       }
 #pragma unroll
-      for (int k = 0; k < SP * NJ; ++k)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rv, (lds_void*)(base + ZB + 256 * (SP * NJ * wave + k)), 4,
-            voff[k] + (uint32_t)(64 * st), 0, 0, 0);
+      for (int k = 0; k < VL; ++k)
+        dma16(rv, voff[k] + (uint32_t)(64 * st), 0, base + vdst[k]);
       if constexpr (MASK) {
         if (hm && wave < 2) {  // lane l: row 16w + l/4, bytes 4(l%4) .. +3 of the tile's 16
           const int row = 16 * wave + (lane >> 2);
@@ -568,15 +569,15 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
         }
       }
     };
-    // all but the newest step's loads (2 + SP NJ per wave: Z or the codes and
+    // all but the newest step's loads (2 + VL per wave: Z or the codes and
     // their exponents, then (sV)^T) have landed (one more in waves 0 and 1 when
     // the keep bits come along)
     auto wait_step = [&]() {
       static_assert(TN_NST == 3, "one step in flight beyond the next");
       if (MASK && hm && wave < 2)
-        wait_vm<2 + SP * NJ + (MASK ? 1 : 0)>();
+        wait_vm<2 + VL + (MASK ? 1 : 0)>();
       else
-        wait_vm<2 + SP * NJ>();
+        wait_vm<2 + VL>();
     };
     load_step(0, std::integral_constant<int, 0>{});
     load_step(min(1, steps - 1), std::integral_constant<int, 1>{});

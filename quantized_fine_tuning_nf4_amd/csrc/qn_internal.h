@@ -76,13 +76,14 @@ struct BwdAux {
   float s;
   bool three_parts;
 };
-// The jobs are rows, one per thread: a row n of B (Bt[j][n] = B[n][j]), a
-// column k of A (At[k][j] = A[j][k]), a column m of su and of sv (all rp
-// ranks of it).  A thread reads its row of B, u or v's slices whole (16-byte
-// loads when r allows), the threads of a wave read neighbouring elements of
-// A's rows, and the transposed writes of neighbouring threads are neighbours.
+// The jobs are rows in blocks of 16 ranks, one per thread: a row n of B (Bt[j][n]
+// = B[n][j]), a column k of A (At[k][j] = A[j][k]), a column m of su and of sv.
+// A thread reads its ranks of B, u or v's slices in 16-byte loads when r allows,
+// the threads of a wave read neighbouring elements of A's rows, and the
+// transposed writes of neighbouring threads are neighbours.
 __host__ __device__ inline int64_t bwd_aux_count(const BwdAux& a) {
-  return (a.Bt ? a.N : 0) + (a.At ? a.K : 0) + (a.su ? a.Mpu : 0) + (a.sv ? a.Mpv : 0);
+  return ((a.Bt ? a.N : 0) + (a.At ? a.K : 0) + (a.su ? a.Mpu : 0) + (a.sv ? a.Mpv : 0)) *
+         ((a.r + 15) / 16);
 }
 // x as bf16 at dst[idx] and its remainder as bf16 at dst[half + idx] (three:
 // what that leaves at dst[2 half + idx])
@@ -94,23 +95,32 @@ __device__ inline void put_split(uint16_t* dst, int64_t half, int64_t idx, float
   dst[half + idx] = (uint16_t)l;
   if (three) dst[2 * half + idx] = (uint16_t)(pack_bf16x2(rest - bf16_lo(l), 0.f) & 0xffffu);
 }
-// row job i of the concatenated jobs (Bt, At, su, sv in that order)
+// row job i of the concatenated jobs (Bt, At, su, sv in that order; a block of
+// ranks of all of them before the next block)
 __device__ inline void bwd_aux_at(const BwdAux& a, int64_t i) {
   const int r = a.r;
   const int64_t rp = 16 * ((r + 15) / 16);
+  int jb = 0;  // this block's ranks: jb .. je - 1
+  if (r > 16) {
+    const int64_t rows = bwd_aux_count(a) / ((r + 15) / 16);
+    const int64_t b = i / rows;
+    jb = (int)b * 16;
+    i -= b * rows;
+  }
+  const int je = jb + 16 < r ? jb + 16 : r;
   const int64_t nb = a.Bt ? a.N : 0;
   if (i < nb) {  // Bt[j][n] = B[n][j]
     const int64_t n = i;
     const uint16_t* row = a.B + n * r;
     if ((r & 7) == 0) {
-      for (int j0 = 0; j0 < r; j0 += 8) {
+      for (int j0 = jb; j0 < je; j0 += 8) {
         const u32x4 v = *reinterpret_cast<const u32x4*>(row + j0);
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           a.Bt[(int64_t)(j0 + q) * a.N + n] = (uint16_t)(v[q >> 1] >> (16 * (q & 1)));
       }
     } else {
-      for (int j = 0; j < r; ++j) a.Bt[(int64_t)j * a.N + n] = row[j];
+      for (int j = jb; j < je; ++j) a.Bt[(int64_t)j * a.N + n] = row[j];
     }
     return;
   }
@@ -120,7 +130,7 @@ __device__ inline void bwd_aux_at(const BwdAux& a, int64_t i) {
     const int64_t k = i;
     uint16_t* row = a.At + k * r;
     if ((r & 7) == 0) {
-      for (int j0 = 0; j0 < r; j0 += 8) {
+      for (int j0 = jb; j0 < je; j0 += 8) {
         uint32_t w[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -129,7 +139,7 @@ __device__ inline void bwd_aux_at(const BwdAux& a, int64_t i) {
         *reinterpret_cast<u32x4*>(row + j0) = u32x4{w[0], w[1], w[2], w[3]};
       }
     } else {
-      for (int j = 0; j < r; ++j) row[j] = a.A[(int64_t)j * a.K + k];
+      for (int j = jb; j < je; ++j) row[j] = a.A[(int64_t)j * a.K + k];
     }
     return;
   }
@@ -144,7 +154,7 @@ __device__ inline void bwd_aux_at(const BwdAux& a, int64_t i) {
   const int64_t half = rp * Mp;
   const bool in = m < a.M;
   const bool vec = (r & 3) == 0;
-  for (int j0 = 0; j0 < rp; j0 += 4) {
+  for (int j0 = jb; j0 < jb + 16; j0 += 4) {
     float x[4] = {0.f, 0.f, 0.f, 0.f};
     if (in && j0 < r) {
       const int64_t e = m * r + j0;
