@@ -62,7 +62,9 @@ __device__ __forceinline__ void clear_words(const Clear& clr) {
 // MFMA lane l holds row l%16 and the eight columns 8(l/16).. of each 32-wide
 // step of both operands (rows of Z and of T are contiguous along the
 // reduction).  U steps' loads are issued before their MFMAs.  Columns past
-// the slice load as zero (P is a multiple of 8).  NJ = ceil(r/16).
+// the slice count as zero in both operands, and a lane whose chunk lies there
+// loads the slice's first columns instead (P is a multiple of 8): past the row
+// there may be the buffer's end, or, in a workspace, a NaN.  NJ = ceil(r/16).
 template <int NJ>
 __global__ __launch_bounds__(kThreads) void k_thin_nt(const uint16_t* __restrict__ Z,
                                                       const uint16_t* __restrict__ T, int64_t M,
@@ -89,7 +91,7 @@ __global__ __launch_bounds__(kThreads) void k_thin_nt(const uint16_t* __restrict
     for (int u = 0; u < U; ++u) {
       const int64_t off = 32 * (int64_t)(s0 + u);
       const bool ok = off < lim;
-      const int64_t o = ok ? off : 0;
+      const int64_t o = ok ? off : -8 * g;
       za[u] = *reinterpret_cast<const u32x4*>(zp + o);
 #pragma unroll
       for (int jt = 0; jt < NJ; ++jt) tb[u][jt] = *reinterpret_cast<const u32x4*>(tp[jt] + o);
@@ -101,7 +103,7 @@ __global__ __launch_bounds__(kThreads) void k_thin_nt(const uint16_t* __restrict
 #pragma unroll
       for (int jt = 0; jt < NJ; ++jt) {
         u32x4 b = tb[u][jt];
-        if (16 * jt + l16 >= r) b = u32x4{0u, 0u, 0u, 0u};
+        if (16 * jt + l16 >= r || 32 * (int64_t)(s0 + u) >= lim) b = u32x4{0u, 0u, 0u, 0u};
         acc[jt] = mfma16(as_bf16x8(za[u]), as_bf16x8(b), acc[jt]);
       }
   }
@@ -158,7 +160,8 @@ __global__ __launch_bounds__(kThreads) void k_thin_nt1(const uint16_t* __restric
 #pragma unroll
     for (int u = 0; u < TN1_U; ++u) {
       const int64_t off = 32 * (int64_t)(TN1_U * b + u);
-      za[buf][u] = *reinterpret_cast<const u32x4*>(zp + (off < lim ? off : 0));
+      // (past the slice: its first columns, never past the row)
+      za[buf][u] = *reinterpret_cast<const u32x4*>(zp + (off < lim ? off : -8 * g));
     }
     if (zmask) {
 #pragma unroll
