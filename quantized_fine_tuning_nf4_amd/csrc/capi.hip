@@ -183,13 +183,13 @@ BwdWs carve_bwd(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool ne
   b.v = c.take<float>((size_t)M * r);
   b.vpart = b.Sv > 1 ? c.take<float>((size_t)b.Sv * M * r) : nullptr;
   const int64_t rp = 16 * ((r + 15) / 16);
-  b.Sb = thin_tn_slices(M, rows, r);
+  b.Sb = thin_tn_slices(M, rows, act8);
   b.dBpart = c.take<float>((size_t)b.Sb * rows * r);
   const size_t parts = act8 ? 3 : 2;
-  b.su = c.take<uint16_t>(parts * rp * thin_tn_rows_padded(M, rows, r));
-  b.Sa = thin_tn_slices(M, cols, r);
+  b.su = c.take<uint16_t>(parts * rp * thin_tn_rows_padded(M, rows, act8));
+  b.Sa = thin_tn_slices(M, cols, act8);
   b.dApart = c.take<float>((size_t)b.Sa * cols * r);
-  b.sv = c.take<uint16_t>(parts * rp * thin_tn_rows_padded(M, cols, r));
+  b.sv = c.take<uint16_t>(parts * rp * thin_tn_rows_padded(M, cols, act8));
   b.ldt = round_up(rows, 64);
   const bool dense = M > 0 && dense_path(M, cols);
   b.wt = dense ? c.take<uint16_t>((size_t)cols * b.ldt) : nullptr;
@@ -352,8 +352,12 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
   const float* u = u_saved;
   // an early launch of the call zeroes the arrival counters the adapter
   // gradients' launch counts on, so the backward never depends on what the
-  // workspace held before
-  Clear clr{b.arrivals, kArrivalWords};
+  // workspace held before.  With x in 8 bits and more than 16 ranks the slices
+  // of those gradients (r times as many values as a column tile is wide) are
+  // added by a launch of their own instead: one workgroup a tile took 66 us
+  // for 4096x1024x4096 at r = 64 where the whole call now takes 50
+  unsigned* arrivals = x8 && r > 16 ? nullptr : b.arrivals;
+  Clear clr{arrivals, arrivals ? kArrivalWords : 0};
   if (!u && e == hipSuccess) {
     e = launch_thin_nt(x, A, M, K, r, b.fu.u, b.fu.upart, b.fu.S, st, true, false, clr, lo.mask);
     clr = Clear{nullptr, 0};
@@ -387,12 +391,12 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
   aux.K = K;
   aux.u = u;
   aux.su = b.su;
-  aux.Mpu = thin_tn_rows_padded(M, N, r);
+  aux.Mpu = thin_tn_rows_padded(M, N, x8 != nullptr);
   aux.vpart = b.vpart;
   aux.Sv = b.Sv;
   aux.v = b.v;
   aux.sv = b.sv;
-  aux.Mpv = thin_tn_rows_padded(M, K, r);
+  aux.Mpv = thin_tn_rows_padded(M, K, x8 != nullptr);
   aux.M = M;
   aux.r = r;
   aux.s = scale;
@@ -418,7 +422,7 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
     e = launch_thin_tn2(ThinTn{dY, b.su, N, dB, false, b.dBpart},
                         ThinTn{x, b.sv, K, dA, true, b.dApart, lo.mask, x8 ? x8->codes : nullptr,
                                x8 ? x8->exps : nullptr},
-                        M, r, b.arrivals, st);
+                        M, r, arrivals, st);
   return from_hip(e);
 }
 

@@ -723,6 +723,17 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
   for (int jt = 0; jt < NJ; ++jt) {
     const int j = 16 * jt + t;
     if (j >= r) continue;
+    if (Z8 && !arrivals && (second ? j1.transposed : j0.transposed)) {
+      // as the output lies: four columns of one rank
+#pragma unroll
+      for (int pt = 0; pt < 2; ++pt) {
+        const int64_t p = p0 + 32 * wave + 16 * pt + 4 * g;
+        if (p < P)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[pt][jt]), rp,
+                                                 (uint32_t)((sl_off + j * P + p) * 4), 0, 0);
+      }
+      continue;
+    }
 #pragma unroll
     for (int pt = 0; pt < 2; ++pt)
 #pragma unroll
@@ -845,6 +856,30 @@ __global__ void k_sum_slices_tn(TnSum a, TnSum b, int r) {
   J.out[t] = slice_sum(J.part, count, J.S, i);
 }
 
+// out[i] = sum over the slices of part[s][i], in slice order, for the two
+// products of one launch whose slices lie as their outputs do; four elements a
+// thread (counts are multiples of 8).
+__global__ void k_sum_parts(TnSum a, TnSum b, int r) {
+  int64_t i = 4 * ((int64_t)blockIdx.x * blockDim.x + threadIdx.x);
+  const int64_t count_a = a.P * r;
+  const bool second = i >= count_a;
+  const TnSum& J = second ? b : a;
+  if (second) i -= count_a;
+  const int64_t count = J.P * r;
+  if (i >= count) return;
+  f32x4 acc = *reinterpret_cast<const f32x4*>(J.part + i);
+  for (int s0 = 1; s0 < J.S; s0 += 8) {
+    f32x4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      v[k] = *reinterpret_cast<const f32x4*>(J.part + (int64_t)min(s0 + k, J.S - 1) * count + i);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (s0 + k < J.S) acc += v[k];
+  }
+  *reinterpret_cast<f32x4*>(J.out + i) = acc;
+}
+
 // Slices of the M rows for the transposed products: enough workgroups to
 // fill the chip (about 512 per product), a multiple of 32 rows each, and
 // small enough that a slice of Z spans less than 2^31 bytes (the kernel
@@ -853,10 +888,12 @@ __global__ void k_sum_slices_tn(TnSum a, TnSum b, int r) {
 // column tile: the tile's last workgroup adds the slices, and with 64 of them
 // (a 1024-column dB at M = 4096) that sum took longer than the products
 // (the k_proj backward's dA/dB launch: 24 us).
-int64_t thin_tn_slice_rows(int64_t M, int64_t P, int r) {
-  (void)r;
+// With x in 8 bits (act8) at most 8: a slice's partial sums weigh as much
+// against half the bytes of x, and the sums are nearer (4096x1024x4096, r = 64:
+// 48.4 -> 45.8 us; 8192x4096x4096, r = 16: 45.0 -> 43.1).
+int64_t thin_tn_slice_rows(int64_t M, int64_t P, bool act8) {
   const int64_t pt = (P + TN_COLS - 1) / TN_COLS;
-  const int64_t S = std::min<int64_t>((512 + pt - 1) / pt, 16);
+  const int64_t S = std::min<int64_t>((512 + pt - 1) / pt, act8 ? 8 : 16);
   int64_t slice = (M + S - 1) / S;
   slice = (slice + 31) / 32 * 32;
   const int64_t cap = ((((int64_t)1 << 31) - 1) / (2 * P)) / 32 * 32;
@@ -865,19 +902,20 @@ int64_t thin_tn_slice_rows(int64_t M, int64_t P, int r) {
   return slice;
 }
 
-int thin_tn_slices(int64_t M, int64_t P, int r) {
-  const int64_t slice = thin_tn_slice_rows(M, P, r);
+int thin_tn_slices(int64_t M, int64_t P, bool act8) {
+  const int64_t slice = thin_tn_slice_rows(M, P, act8);
   return (int)((M + slice - 1) / slice);
 }
 
 // Row length of the staged (sV)^T: every slice's rows exist (zero past M).
-int64_t thin_tn_rows_padded(int64_t M, int64_t P, int r) {
-  return (int64_t)thin_tn_slices(M, P, r) * thin_tn_slice_rows(M, P, r);
+int64_t thin_tn_rows_padded(int64_t M, int64_t P, bool act8) {
+  return (int64_t)thin_tn_slices(M, P, act8) * thin_tn_slice_rows(M, P, act8);
 }
 
 hipError_t launch_thin_tn2(const ThinTn& a, const ThinTn& b, int64_t M, int r,
                            unsigned* arrivals, hipStream_t st) {
   const int nj = (r + 15) / 16;
+  const bool z8 = b.codes != nullptr;
   TnJob job[2];
   const ThinTn* in[2] = {&a, &b};
   int s_max = 1;
@@ -888,10 +926,10 @@ hipError_t launch_thin_tn2(const ThinTn& a, const ThinTn& b, int64_t M, int r,
     j.codes = x.codes;
     j.exps = x.exps;
     j.vt = x.vt;
-    j.Mp = thin_tn_rows_padded(M, x.P, r);
+    j.Mp = thin_tn_rows_padded(M, x.P, z8);
     j.P = x.P;
-    j.slice = thin_tn_slice_rows(M, x.P, r);
-    j.S = thin_tn_slices(M, x.P, r);
+    j.slice = thin_tn_slice_rows(M, x.P, z8);
+    j.S = thin_tn_slices(M, x.P, z8);
     j.tiles = x.Z || x.codes ? (int)((x.P + TN_COLS - 1) / TN_COLS) : 0;
     j.part = x.part;
     j.out = x.out;
@@ -905,7 +943,6 @@ hipError_t launch_thin_tn2(const ThinTn& a, const ThinTn& b, int64_t M, int r,
   // tile), else by a second launch
   unsigned* ctr = tiles <= kTnMaxTiles ? arrivals : nullptr;
   const bool mask = (job[0].tiles > 0 && job[0].zmask) || (job[1].tiles > 0 && job[1].zmask);
-  const bool z8 = b.codes != nullptr;
   if (a.codes) return hipErrorInvalidValue;  // a checkpoint is the second job's
   const size_t lds =
       (size_t)TN_NST * (32 * TN_ROWB + (z8 ? 3 : 2) * 16 * nj * 64 + (mask ? 32 * 16 : 0));
@@ -938,8 +975,12 @@ hipError_t launch_thin_tn2(const ThinTn& a, const ThinTn& b, int64_t M, int r,
     sum[k] = TnSum{x.part, job[k].tiles > 0 ? x.P : 0, job[k].S, x.transposed, x.out};
     count += sum[k].P * r;
   }
-  hipLaunchKernelGGL(k_sum_slices_tn, dim3((unsigned)((count + 255) / 256)), dim3(256), 0, st,
-                     sum[0], sum[1], r);
+  if (z8)
+    hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)((count / 4 + 255) / 256)), dim3(256), 0, st,
+                       sum[0], sum[1], r);
+  else
+    hipLaunchKernelGGL(k_sum_slices_tn, dim3((unsigned)((count + 255) / 256)), dim3(256), 0, st,
+                       sum[0], sum[1], r);
   return hipGetLastError();
 }
 

@@ -277,8 +277,8 @@ hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t st);
 // One transposed adapter product out = Z^T (s V), reduced over the M rows:
 // Z bf16 [M, P] (null: no product) or, for the second product, an 8-bit
 // checkpoint of it (codes and exps; P % 64 == 0), vt = (s V)^T split as BwdAux
-// makes it (in three parts for both products when there are codes) with Mp = thin_tn_rows_padded(M, P, r); transposed == false: out fp32
-// [P, r]; true: out fp32 [r, P].  Split over thin_tn_slices(M, P, r) row
+// makes it (in three parts for both products when there are codes) with Mp = thin_tn_rows_padded(M, P, act8); transposed == false: out fp32
+// [P, r]; true: out fp32 [r, P].  Split over thin_tn_slices(M, P, act8) row
 // slices with partials part[S][P][r], summed in slice order.  P % 8 == 0.
 struct ThinTn {
   const uint16_t* Z;
@@ -297,8 +297,8 @@ struct ThinTn {
 // column tiles or with arrivals == null, by a second launch.
 hipError_t launch_thin_tn2(const ThinTn& a, const ThinTn& b, int64_t M, int r,
                            unsigned* arrivals, hipStream_t st);
-int thin_tn_slices(int64_t M, int64_t P, int r);
-int64_t thin_tn_rows_padded(int64_t M, int64_t P, int r);
+int thin_tn_slices(int64_t M, int64_t P, bool act8);
+int64_t thin_tn_rows_padded(int64_t M, int64_t P, bool act8);
 
 // Decode forward, u = X A^T included (written to u_out [M, r]); workspace
 // part [S, M, rows] and upart [S, M, r] fp32, S = decode_slices(...).
