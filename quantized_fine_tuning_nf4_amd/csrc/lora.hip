@@ -450,8 +450,9 @@ __device__ __forceinline__ void wait_vm() {
 // MASK: a job may carry keep bits of Z (dropout on the adapter branch's
 // input, for dA): the step's 32 rows x 16 bytes of bits go global -> LDS
 // beside Z (one 4-byte-per-lane load in waves 0 and 1: rows 16w .. 16w+15;
-// the direct-to-LDS path writes one dword per lane), and the dropped values
-// are zeroed in the A operand after the transposed reads.
+// the direct-to-LDS path writes one dword per lane), word by word, so that a
+// lane's eight rows of its wave's word are 32 bytes in a row, and the dropped
+// values are zeroed in the A operand after the transposed reads.
 //
 // Z8: the second job's Z is an 8-bit checkpoint.  Its 32 rows of 128 codes are
 // half the bytes of bf16 rows: one 16-byte-per-lane load per wave (8 rows each;
@@ -563,12 +564,12 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
       for (int k = 0; k < VL; ++k)
         dma16(rv, voff[k] + (uint32_t)(64 * st), 0, base + vdst[k]);
       if constexpr (MASK) {
-        if (hm && wave < 2) {  // lane l: row 16w + l/4, bytes 4(l%4) .. +3 of the tile's 16
-          const int row = 16 * wave + (lane >> 2);
+        if (hm && wave < 2) {  // lane l: row 16w + l%16, bytes 4(l/16) .. +3 of the tile's 16
+          const int row = 16 * wave + (lane & 15);
           const int64_t mm = min(mb + 32 * (int64_t)st + row, M - 1);
           __builtin_amdgcn_raw_ptr_buffer_load_lds(
               rk, (lds_void*)(base + ZB + VB + 256 * wave), 4,
-              (uint32_t)((((mm - mb) * P + p0) >> 3) + 4 * (lane & 3)), 0, 0, 0);
+              (uint32_t)((((mm - mb) * P + p0) >> 3) + 4 * (lane >> 4)), 0, 0, 0);
         }
       }
     };
@@ -656,20 +657,20 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
       if constexpr (MASK) {
         if (hm) {
           // word i of za[pt] holds rows 8g + 2i, 8g + 2i + 1 of column
-          // 32w + 16pt + t, whose keep bits are bit 16pt + t of the word at
-          // byte 4w of each row's 16 bytes
-          const uint8_t* ks = zs + ZB + VB + 4 * wave;
-          uint32_t kw[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            kw[q] = *reinterpret_cast<const uint32_t*>(ks + 16 * (8 * g + q));
+          // 32w + 16pt + t, whose keep bits are bit 16pt + t of this wave's
+          // words of the two rows
+          const u32x4* ks = reinterpret_cast<const u32x4*>(zs + ZB + VB + 256 * (g >> 1) +
+                                                           64 * wave + 32 * (g & 1));
+          const u32x4 kw[2] = {ks[0], ks[1]};
 #pragma unroll
           for (int pt = 0; pt < 2; ++pt) {
             const int sh = 16 * pt + t;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              za[pt][i] &= (((kw[2 * i] >> sh) & 1u) * 0xffffu) |
-                           (((kw[2 * i + 1] >> sh) & 1u) * 0xffff0000u);
+            for (int i = 0; i < 4; ++i) {  // a bit as all ones or zeros, in each half
+              const uint32_t lo = (uint32_t)__builtin_amdgcn_sbfe(kw[i >> 1][2 * (i & 1)], sh, 1);
+              const uint32_t hi = (uint32_t)__builtin_amdgcn_sbfe(kw[i >> 1][2 * (i & 1) + 1], sh, 1);
+              za[pt][i] &= __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+            }
           }
         }
       }
