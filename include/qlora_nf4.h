@@ -391,7 +391,7 @@ typedef struct {
   const void* w_post; /* [D] or NULL */
   const void* gate;   /* by gate_kind, or NULL */
   int32_t res_dtype, w_dtype, gate_kind;
-  float scale, eps;   /* finite; eps > 0 */
+  float scale, eps;   /* finite; eps a positive normal number */
 } qn_block_norm;
 
 /* h_new and y are written; with codes and exps (both or neither) also y's

@@ -3,6 +3,7 @@
 // launches nothing on error.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -288,7 +289,8 @@ qn_status check_norm(const qn_block_norm* n, BlockNorm* out) {
   if (n->res_dtype != QN_F32 && n->res_dtype != QN_BF16) return QN_EINVAL;
   if (n->w_dtype != QN_F32 && n->w_dtype != QN_BF16) return QN_EINVAL;
   if (n->gate_kind < QN_GATE_NONE || n->gate_kind > QN_GATE_ELEMENT) return QN_EINVAL;
-  if (!std::isfinite(n->scale) || !std::isfinite(n->eps) || !(n->eps > 0.f)) return QN_EINVAL;
+  if (!std::isfinite(n->scale) || !std::isfinite(n->eps) || !(n->eps >= FLT_MIN))
+    return QN_EINVAL;
   if (!n->w_pre) return QN_EINVAL;
   // no element gate has storage for an empty batch
   if ((n->gate_kind == QN_GATE_NONE) != (n->gate == nullptr) && n->M > 0) return QN_EINVAL;

@@ -210,13 +210,25 @@ __device__ __forceinline__ void row_sums(float (&x)[N], float* s) {
       for (int k = 0; k < N; ++k) s[k * W + (threadIdx.x >> 6)] = x[k];
     }
     __syncthreads();
+    // every group of W lanes adds the W waves' sums
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      x[k] = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) x[k] += s[k * W + w];
+      float v = s[k * W + (threadIdx.x & (W - 1))];
+      v += as_f32(dpp<kDppXor1>(as_u32(v)));
+      if (W >= 4) v += as_f32(dpp<kDppXor2>(as_u32(v)));
+      if (W >= 8) v += as_f32(dpp<kDppMirror8>(as_u32(v)));
+      if (W >= 16) v += as_f32(dpp<kDppMirror16>(as_u32(v)));
+      x[k] = v;
     }
   }
+}
+
+// 1 / sqrt(x), x normal, infinite or NaN: the instruction's estimate and one
+// Newton step, off by 2^-23.
+__device__ __forceinline__ float inv_sqrt(float x) {
+  const float y = __builtin_amdgcn_rsqf(x);
+  const float z = __builtin_fmaf(0.5f * y, __builtin_fmaf(-x * y, y, 1.f), y);
+  return y == 0.f ? 0.f : z;  // squares past fp32
 }
 
 // Most threads of a workgroup: four rows' waves, or one row's threads (no more
@@ -228,17 +240,94 @@ __device__ __forceinline__ int row_group() {
   return TPR > 64 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 }
 
-// Whether a row's threads keep the [D] parameters in registers from row to row
-// (one vector a thread, registers to spare; otherwise they come from L2 again
-// for every row), and whether they go from row to row, the next one's loads
-// sent ahead of the current one's reductions.
+// Where a row's threads have the [D] parameters (w_pre, w_post, the channel
+// gate) and, in the backward, the column sums of their gradients, from row to
+// row: in registers with one vector a thread in up to 512 threads, else in LDS,
+// every thread its own values, as far as that goes, else the parameters come
+// from L2 again for every row and the sums from k_norm_columns.
 constexpr bool keeps(int tpr, int nv) { return nv == 1 && tpr < 1024; }
-constexpr bool walks(int nv) { return nv == 1; }
+// Whether the next row's loads go out ahead of the current row's reductions.
+constexpr bool prefetches(int nv) { return nv == 1; }
+
+// Slots of 16 bytes a vector and thread: the first of each parameter and each
+// sum (fp32 values take two), or -1.
+struct Slots {
+  int par[3], sum[3], count;
+};
+constexpr size_t kSlotBytes = 144 * 1024;  // of 160 KB a compute unit
+// keep: parameters in registers.  sums: which of them go to LDS.
+Slots slots_of(const BlockNorm& n, bool keep, const bool (&sums)[3], int threads, int nv) {
+  Slots s{{-1, -1, -1}, {-1, -1, -1}, 0};
+  const int most = (int)(kSlotBytes / ((size_t)16 * threads * nv));
+  auto take = [&](int& slot, int need) {
+    if (s.count + need > most) return;
+    slot = s.count;
+    s.count += need;
+  };
+  for (int k = 0; k < 3; ++k)
+    if (sums[k]) take(s.sum[k], 2);
+  const bool there[3] = {true, n.w_post != nullptr, n.gate_kind == kGateChannel};
+  for (int k = 0; k < 3; ++k)
+    if (!keep && there[k]) take(s.par[k], n.w32 ? 2 : 1);
+  return s;
+}
+
+template <int TPR, int NV, bool TAIL>
+struct Lds {
+  u32x4* base;
+  const Slots& s;
+  int t;
+  __device__ __forceinline__ u32x4& at(int slot, int v) const {
+    return base[(slot * NV + v) * (int)blockDim.x + t];
+  }
+  __device__ __forceinline__ void stage(const NormArgs& n, int which, const void* w) const {
+    if (s.par[which] < 0) return;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const Param8 p = load_param<TPR, TAIL>(w, n.w32, v, t, n.D);
+      at(s.par[which], v) = p.lo;
+      if (n.w32) at(s.par[which] + 1, v) = p.hi;
+    }
+  }
+  __device__ __forceinline__ Param8 param(const NormArgs& n, int which, const void* w, int v) const {
+    if (s.par[which] < 0) {
+      asm volatile("" : "+s"(w) : : "memory");  // loaded here, no earlier
+      return load_param<TPR, TAIL>(w, n.w32, v, t, n.D);
+    }
+    Param8 p;
+    p.lo = at(s.par[which], v);
+    if (n.w32) p.hi = at(s.par[which] + 1, v);
+    return p;
+  }
+  __device__ __forceinline__ void clear(int which) const {
+    if (s.sum[which] >= 0)
+      at(s.sum[which], 0) = at(s.sum[which] + 1, 0) = u32x4{0u, 0u, 0u, 0u};
+  }
+  __device__ __forceinline__ void add(int which, const float (&x)[8]) const {
+    if (s.sum[which] < 0) return;
+    f32x4* lo = reinterpret_cast<f32x4*>(&at(s.sum[which], 0));
+    f32x4* hi = reinterpret_cast<f32x4*>(&at(s.sum[which] + 1, 0));
+    *lo += f32x4{x[0], x[1], x[2], x[3]};
+    *hi += f32x4{x[4], x[5], x[6], x[7]};
+  }
+  __device__ __forceinline__ void store(int which, float* row, int D) const {
+    float x[8] = {};
+    if (s.sum[which] >= 0) {
+      const f32x4 lo = __builtin_bit_cast(f32x4, at(s.sum[which], 0));
+      const f32x4 hi = __builtin_bit_cast(f32x4, at(s.sum[which] + 1, 0));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = j < 4 ? lo[j & 3] : hi[j & 3];
+    }
+    store8<TPR, TAIL>(row, 0, t, D, x);
+  }
+};
+extern __shared__ u32x4 slots_lds[];
 
 template <int TPR, int NV, bool TAIL, typename R>
 __global__ __launch_bounds__(group_threads(TPR)) void k_norm_fwd(
-    NormArgs n, const R* __restrict__ h, const uint16_t* __restrict__ o, R* __restrict__ hn,
-    uint16_t* __restrict__ y, int8_t* __restrict__ codes, uint8_t* __restrict__ exps) {
+    NormArgs n, Slots slots, const R* __restrict__ h, const uint16_t* __restrict__ o,
+    R* __restrict__ hn, uint16_t* __restrict__ y, int8_t* __restrict__ codes,
+    uint8_t* __restrict__ exps) {
   constexpr bool KEEP = keeps(TPR, NV);
   constexpr int G = group_threads(TPR) / TPR;
   __shared__ float s[2][2][TPR / 64];
@@ -248,10 +337,7 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_fwd(
   const bool post = n.w_post != nullptr, chan = n.gate_kind == kGateChannel,
              elem = n.gate_kind == kGateElement, rowg = n.gate_kind == kGateRow;
   Param8 w1, w2, gc;  // of vector 0, with KEEP
-  auto param = [&](const void* w, int v) {
-    if (!KEEP) asm volatile("" : "+s"(w) : : "memory");  // loaded here, no earlier
-    return load_param<TPR, TAIL>(w, n.w32, v, t, D);
-  };
+  const Lds<TPR, NV, TAIL> lds{slots_lds, slots, t};
   Raw8<R> hv[NV];
   Raw8<uint16_t> ov[NV], gv[NV];
   auto load_row = [&](int64_t m) {
@@ -265,16 +351,21 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_fwd(
   };
   const int64_t step = (int64_t)gridDim.x * G;
   int64_t m = (int64_t)blockIdx.x * G + row_group<TPR>();
-  if (m < n.M) load_row(m);
+  if (prefetches(NV) && m < n.M) load_row(m);
   if (KEEP) {
-    if (post) w1 = param(n.w_post, 0);
-    if (chan) gc = param(n.gate, 0);
-    w2 = param(n.w_pre, 0);
+    if (post) w1 = load_param<TPR, TAIL>(n.w_post, n.w32, 0, t, D);
+    if (chan) gc = load_param<TPR, TAIL>(n.gate, n.w32, 0, t, D);
+    w2 = load_param<TPR, TAIL>(n.w_pre, n.w32, 0, t, D);
+  } else {
+    lds.stage(n, 0, n.w_pre);
+    lds.stage(n, 1, n.w_post);
+    lds.stage(n, 2, n.gate);
   }
   // a group that is a whole workgroup runs the same rows in all its threads; a
   // wave's own rows need no barrier
   for (int par = 0; m < n.M; m += step, par ^= 1) {
     const int64_t row = m * D;
+    if (!prefetches(NV)) load_row(m);
     Raw8<uint16_t> o_[NV], g_[NV];
     float x[NV][8];
 #pragma unroll
@@ -289,7 +380,7 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_fwd(
     }
     float k = n.scale;
     if (rowg) k *= load_f32(static_cast<const uint16_t*>(n.gate) + m);
-    if (walks(NV) && m + step < n.M) load_row(m + step);
+    if (prefetches(NV) && m + step < n.M) load_row(m + step);
     if (o) {
       if (post) {
         float q[1] = {0.f};
@@ -298,13 +389,13 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_fwd(
 #pragma unroll
           for (int j = 0; j < 8; ++j) q[0] = __builtin_fmaf(o_[v].get(j), o_[v].get(j), q[0]);
         row_sums<TPR, 1>(q, s[par][0]);
-        k *= 1.f / __builtin_sqrtf(q[0] / (float)D + n.eps);
+        k *= inv_sqrt(q[0] / (float)D + n.eps);
       }
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         float out[8];
-        if (!KEEP && post) w1 = param(n.w_post, v);
-        if (!KEEP && chan) gc = param(n.gate, v);
+        if (!KEEP && post) w1 = lds.param(n, 1, n.w_post, v);
+        if (!KEEP && chan) gc = lds.param(n, 2, n.gate, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           float p = o_[v].get(j) * k;
@@ -322,11 +413,11 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_fwd(
 #pragma unroll
       for (int j = 0; j < 8; ++j) q[0] = __builtin_fmaf(x[v][j], x[v][j], q[0]);
     row_sums<TPR, 1>(q, s[par][1]);
-    const float r2 = 1.f / __builtin_sqrtf(q[0] / (float)D + n.eps);
+    const float r2 = inv_sqrt(q[0] / (float)D + n.eps);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float out[8];
-      if (!KEEP) w2 = param(n.w_pre, v);
+      if (!KEEP) w2 = lds.param(n, 0, n.w_pre, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) out[j] = x[v][j] * r2 * w2.get(n.w32, j);
       store8<TPR, TAIL>(y + row, v, t, D, out);
@@ -360,15 +451,18 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_fwd(
   }
 }
 
-// Row group z takes rows z, z + groups, ...  With SUMS a thread keeps its
-// columns' sums over those rows in registers; a workgroup's groups meet in
-// LDS and leave part [workgroup][3][D] (dw_pre, dw_post, channel dgate).
-template <int TPR, int NV, bool TAIL, bool SUMS, typename R>
+// Row group z takes rows z, z + groups, ...  A thread keeps its columns' sums
+// over those rows in registers (kSumsRegs; a workgroup's groups meet in LDS) or
+// LDS (kSumsLds); a workgroup leaves part [workgroup][3][D] (dw_pre, dw_post,
+// channel dgate).
+enum { kSumsNone = 0, kSumsRegs = 1, kSumsLds = 2 };
+template <int TPR, int NV, bool TAIL, int SUMS, typename R>
 __global__ __launch_bounds__(group_threads(TPR)) void k_norm_bwd(
-    NormArgs n, const uint16_t* __restrict__ dy, const R* __restrict__ dhn,
+    NormArgs n, Slots slots, const uint16_t* __restrict__ dy, const R* __restrict__ dhn,
     const R* __restrict__ hn, const uint16_t* __restrict__ o, R* __restrict__ dh,
     uint16_t* __restrict__ dout, void* __restrict__ dgate, float* __restrict__ part,
     f32x4* __restrict__ stats) {
+  constexpr bool REGS = SUMS == kSumsRegs;
   constexpr int G = group_threads(TPR) / TPR;  // row groups of a workgroup
   constexpr int W = TPR / 64;
   constexpr bool KEEP = keeps(TPR, NV);
@@ -380,14 +474,19 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_bwd(
              elem = n.gate_kind == kGateElement, rowg = n.gate_kind == kGateRow;
   float sp[NV][8] = {}, so[NV][8] = {}, sg[NV][8] = {};
   Param8 w1, w2, gc;  // of vector 0, with KEEP
-  auto param = [&](const void* w, int v) {
-    if (!KEEP) asm volatile("" : "+s"(w) : : "memory");  // loaded here, no earlier
-    return load_param<TPR, TAIL>(w, n.w32, v, t, D);
-  };
+  const Lds<TPR, NV, TAIL> lds{slots_lds, slots, t};
   if (KEEP) {
-    w2 = param(n.w_pre, 0);
-    if (post) w1 = param(n.w_post, 0);
-    if (chan) gc = param(n.gate, 0);
+    w2 = load_param<TPR, TAIL>(n.w_pre, n.w32, 0, t, D);
+    if (post) w1 = load_param<TPR, TAIL>(n.w_post, n.w32, 0, t, D);
+    if (chan) gc = load_param<TPR, TAIL>(n.gate, n.w32, 0, t, D);
+  } else {
+    lds.stage(n, 0, n.w_pre);
+    lds.stage(n, 1, n.w_post);
+    lds.stage(n, 2, n.gate);
+  }
+  if (SUMS == kSumsLds) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) lds.clear(k);
   }
   Raw8<R> hv[NV], dv[NV];
   Raw8<uint16_t> yv[NV], ov[NV], gv[NV];
@@ -404,13 +503,13 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_bwd(
   };
   const int64_t step = (int64_t)gridDim.x * G;
   int64_t m = (int64_t)blockIdx.x * G + grp;
-  if (walks(NV) && m < n.M) load_row(m);
+  if (prefetches(NV) && m < n.M) load_row(m);
   int par = 0;
   // the rows of a group that is a whole workgroup are the same for all its
   // threads; a wave's own rows need no barrier
   for (; m < n.M; m += step, par ^= 1) {
     const int64_t row = m * D;
-    if (!walks(NV)) load_row(m);
+    if (!prefetches(NV)) load_row(m);
     Raw8<R> h_[NV], d_[NV];
     Raw8<uint16_t> y_[NV], o_[NV], g_[NV];
 #pragma unroll
@@ -427,11 +526,11 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_bwd(
       g_[v] = gv[v];
     }
     const float grow = rowg ? n.scale * load_f32(static_cast<const uint16_t*>(n.gate) + m) : n.scale;
-    if (walks(NV) && m + step < n.M) load_row(m + step);
+    if (prefetches(NV) && m + step < n.M) load_row(m + step);
     float q[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      if (!KEEP) w2 = param(n.w_pre, v);
+      if (!KEEP) w2 = lds.param(n, 0, n.w_pre, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float x = h_[v].get(j);
@@ -449,29 +548,31 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_bwd(
         as_loaded(o_[v]);
       }
     }
-    const float r2 = 1.f / __builtin_sqrtf(q[0] * rD + n.eps);
+    const float r2 = inv_sqrt(q[0] * rD + n.eps);
     const float c2 = q[1] * r2 * rD * r2;  // r2 mean(dn n)
-    const float r1 = post ? 1.f / __builtin_sqrtf(q[2] * rD + n.eps) : 1.f;
-    if (!SUMS && stats && t == 0) stats[m] = f32x4{r2, c2, r1, grow};
+    const float r1 = post ? inv_sqrt(q[2] * rD + n.eps) : 1.f;
+    if (SUMS == kSumsNone && stats && t == 0) stats[m] = f32x4{r2, c2, r1, grow};
     float d[NV][8], e[2] = {0.f, 0.f};
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float out[8];
-      if (!KEEP) w2 = param(n.w_pre, v);
+      if (!KEEP) w2 = lds.param(n, 0, n.w_pre, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float x = h_[v].get(j), g = y_[v].get(j);
         const float dn = g * w2.get(n.w32, j);
         out[j] = d[v][j] = __builtin_fmaf(r2, dn - x * c2, d_[v].get(j));
-        if (SUMS) sp[v][j] = __builtin_fmaf(g, x * r2, sp[v][j]);
+        if (REGS) sp[v][j] = __builtin_fmaf(g, x * r2, sp[v][j]);
+        if (SUMS == kSumsLds) sp[v][j] = g * (x * r2);
       }
+      if (SUMS == kSumsLds) lds.add(0, sp[v]);
       store8<TPR, TAIL>(dh + row, v, t, D, out);
     }
     if (!o) continue;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      if (!KEEP && post) w1 = param(n.w_post, v);
-      if (!KEEP && chan) gc = param(n.gate, v);
+      if (!KEEP && post) w1 = lds.param(n, 1, n.w_post, v);
+      if (!KEEP && chan) gc = lds.param(n, 2, n.gate, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         // d becomes dq (or a, without a post norm)
@@ -483,11 +584,19 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_bwd(
         d[v][j] = a * wp;
         e[0] = __builtin_fmaf(a * wp, x, e[0]);
         if (rowg) e[1] = __builtin_fmaf(base * n.scale, x * wp, e[1]);
-        if (SUMS) {
+        if (REGS) {
           so[v][j] = __builtin_fmaf(a, x, so[v][j]);
           if (chan) sg[v][j] = __builtin_fmaf(base * n.scale, x * wp, sg[v][j]);
         }
+        if (SUMS == kSumsLds) {
+          so[v][j] = a * x;
+          if (chan) sg[v][j] = base * n.scale * (x * wp);
+        }
         if (elem) g_[v].put(j, base * n.scale * (x * wp));
+      }
+      if (SUMS == kSumsLds) {
+        lds.add(1, so[v]);
+        if (chan) lds.add(2, sg[v]);
       }
     }
     if (post || rowg) row_sums<TPR, 2>(e, s[par][1]);
@@ -509,7 +618,12 @@ __global__ __launch_bounds__(group_threads(TPR)) void k_norm_bwd(
       if (elem && dgate) store8<TPR, TAIL>(static_cast<uint16_t*>(dgate) + row, v, t, D, dg);
     }
   }
-  if constexpr (SUMS) {
+  if constexpr (SUMS == kSumsLds) {
+    float* dst = part + (int64_t)blockIdx.x * 3 * D;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) lds.store(k, dst + k * D, D);
+  }
+  if constexpr (REGS) {
     float* dst = part + (int64_t)blockIdx.x * 3 * D;
     if constexpr (G == 1) {
 #pragma unroll
@@ -631,13 +745,14 @@ __global__ __launch_bounds__(64 * kSumGroups) void k_norm_sums(const float* __re
   }
 }
 
-// Threads of a launch whose workgroups go from row to row, for 256 compute
-// units: as many as stay resident.
+// Threads of a launch, for 256 compute units: as many as stay resident (at
+// 8192 x 4096 the forward took 52 / 51 / 58 us with half, this and twice as
+// many, the backward with column sums 91 / 97 us with this and twice as many).
+// Rows of more than 512 threads: two workgroups a compute unit in the forward
+// where they fit, one in the backward.
 constexpr int64_t kFwdThreads = 256 * 2048, kBwdThreads = 256 * 1024, kSumThreads = 256 * 512;
-// Columns up to which a row's threads keep the column sums.  One vector a
-// thread and its 24 sums take 162-176 registers, which 1024 threads do not
-// have: spilling, 4096 x 8192 took 255 us, in a pass of its own XXX.
-constexpr int64_t kSumCols = 4096;
+// Columns up to which a row's threads keep the column sums.
+constexpr int64_t kSumCols = 8192;
 constexpr int kColumnSlices = 64;
 
 NormArgs args_of(const BlockNorm& n) {
@@ -667,6 +782,19 @@ hipError_t by_columns(int64_t D, F&& f) {
   return D <= 8192 ? f(T1024{}, I1{}) : f(T1024{}, I2{});
 }
 
+// Launches a kernel with that much LDS beside its own.
+template <typename... P, typename... A>
+hipError_t run(void (*f)(P...), dim3 grid, int threads, size_t lds, hipStream_t st, A... args) {
+  if (lds > 48 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(f),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)kSlotBytes);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(f, grid, dim3(threads), lds, st, args...);
+  return hipGetLastError();
+}
+
 // Threads of a workgroup for the row length D.
 template <int TPR, int NV>
 int threads_of(int64_t D) {
@@ -682,17 +810,18 @@ hipError_t norm_fwd(const BlockNorm& n, const void* h, const uint16_t* o, void* 
     const int T = threads_of<TPR, NV>(n.D);
     const int64_t groups = (n.M + G - 1) / G;
     const int64_t wgs = T > 512 ? kFwdThreads / 2048 * (1280 / T) : kFwdThreads / T;
-    const dim3 grid((unsigned)(walks(NV) ? std::min<int64_t>(groups, wgs) : groups));
+    const dim3 grid((unsigned)std::min<int64_t>(groups, wgs));
     const NormArgs a = args_of(n);
+    const Slots slots = slots_of(n, keeps(TPR, NV), {false, false, false}, T, NV);
+    const size_t lds = (size_t)slots.count * 16 * T * NV;
     const R* hp = static_cast<const R*>(h);
     R* hn = static_cast<R*>(h_new);
+    hipError_t e;
     if (n.D % 8 == 0)
-      hipLaunchKernelGGL((k_norm_fwd<TPR, NV, false, R>), grid, dim3(T), 0, st, a, hp, o, hn, y,
-                         codes, exps);
+      e = run(k_norm_fwd<TPR, NV, false, R>, grid, T, lds, st, a, slots, hp, o, hn, y, codes, exps);
     else
-      hipLaunchKernelGGL((k_norm_fwd<TPR, NV, true, R>), grid, dim3(T), 0, st, a, hp, o, hn, y,
-                         codes, exps);
-    return hipGetLastError();
+      e = run(k_norm_fwd<TPR, NV, true, R>, grid, T, lds, st, a, slots, hp, o, hn, y, codes, exps);
+    return e;
   });
 }
 
@@ -710,20 +839,26 @@ hipError_t norm_bwd(const BlockNorm& n, const uint16_t* dy, const void* dh_new, 
     const int T = threads_of<TPR, NV>(n.D);
     const int64_t groups = (n.M + G - 1) / G;
     auto launch = [&](auto sums, int64_t blocks) {
-      constexpr bool SUMS = decltype(sums)::value;
+      constexpr int SUMS = decltype(sums)::value;
       const dim3 grid((unsigned)blocks);
-      if (n.D % 8 == 0)
-        hipLaunchKernelGGL((k_norm_bwd<TPR, NV, false, SUMS, R>), grid, dim3(T), 0, st, a, dy, dp,
-                           hp, o, out, dout, dgate, part, rows);
-      else
-        hipLaunchKernelGGL((k_norm_bwd<TPR, NV, true, SUMS, R>), grid, dim3(T), 0, st, a, dy, dp,
-                           hp, o, out, dout, dgate, part, rows);
-      return hipGetLastError();
+      constexpr bool in_lds = SUMS == kSumsLds;
+      const Slots slots =
+          slots_of(n, keeps(TPR, NV), {in_lds, in_lds && n.w_post, in_lds && n.gate_kind == kGateChannel},
+                   T, NV);
+      const size_t lds = (size_t)slots.count * 16 * T * NV;
+      return n.D % 8 == 0 ? run(k_norm_bwd<TPR, NV, false, SUMS, R>, grid, T, lds, st, a, slots, dy,
+                                dp, hp, o, out, dout, dgate, part, rows)
+                          : run(k_norm_bwd<TPR, NV, true, SUMS, R>, grid, T, lds, st, a, slots, dy,
+                                dp, hp, o, out, dout, dgate, part, rows);
     };
-    if constexpr (TPR < 1024) {
-      if (part) return launch(std::true_type{}, block_norm_slices(n.M, n.D));
+    using Regs = std::integral_constant<int, kSumsRegs>;
+    using InLds = std::integral_constant<int, kSumsLds>;
+    if constexpr (NV == 1) {
+      if (part)
+        return launch(std::conditional_t<(TPR < 1024), Regs, InLds>{}, block_norm_slices(n.M, n.D));
     }
-    return launch(std::false_type{}, walks(NV) ? std::min<int64_t>(groups, kBwdThreads / T) : groups);
+    return launch(std::integral_constant<int, kSumsNone>{},
+                  std::min<int64_t>(groups, T > 512 ? 256 : kBwdThreads / T));
   });
   if (e != hipSuccess || !part || n.D <= kSumCols) return e;
   const dim3 grid((unsigned)((n.D + 2047) / 2048), (unsigned)block_norm_slices(n.M, n.D));
@@ -748,7 +883,7 @@ hipError_t launch_block_norm_fwd(const BlockNorm& n, const void* h, const uint16
 int block_norm_slices(int64_t M, int64_t D) {
   if (D > kSumCols) return (int)std::min<int64_t>(M, kColumnSlices * 16384 / (2048 * ((D + 2047) / 2048)));
   const int64_t T = D <= 512 ? 256 : (D + 511) / 512 * 64, G = D <= 512 ? 4 : 1;
-  return (int)std::min<int64_t>((M + G - 1) / G, kSumThreads / T);
+  return (int)std::min<int64_t>((M + G - 1) / G, D > 4096 ? 256 : kSumThreads / T);
 }
 int64_t block_norm_stats(int64_t M, int64_t D) { return D > kSumCols ? 4 * M : 0; }
 

@@ -71,7 +71,7 @@ def _norm(qn, **kw):
 
 BAD_NORMS = [dict(M=-1), dict(D=0), dict(D=16385), dict(w_pre=None), dict(res_dtype=2),
              dict(w_dtype=-1), dict(gate_kind=4), dict(gate_kind=0), dict(gate=None),
-             dict(eps=0.0), dict(eps=-1.0), dict(eps=math.nan), dict(scale=math.inf)]
+             dict(eps=0.0), dict(eps=1e-40), dict(eps=-1.0), dict(eps=math.nan), dict(scale=math.inf)]
 
 
 def test_block_norm_refusals(qn):

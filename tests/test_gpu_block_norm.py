@@ -271,6 +271,17 @@ def test_nan_and_inf_stay_in_their_row(qn):
     assert torch.isnan(back[1]).all() and torch.isnan(back[3, :64]).all()
 
 
+def test_squares_past_fp32(qn):
+    """A row whose squares overflow has norm zero in fp32, and harms no other."""
+    t = _dev(_inputs(3, 200, True, True, "norm", "channel", seed=9))
+    t["o"][1] = 1e30
+    t["h"][2] = 1e30
+    hn, y, _ = qn.block_norm_fwd(t["h"], t["w_pre"], o=t["o"], w_post=t["w_post"],
+                                 gate=t["gate"])
+    assert torch.equal(hn[1], t["h"][1]) and not y[2].any()
+    assert torch.isfinite(y).all()
+
+
 def test_leading_dimensions_and_another_stream(qn):
     t = _dev(_inputs(12, 256, False, True, "norm", "row", seed=4))
     v = {k: x.view(3, 4, -1) for k, x in t.items() if x is not None and x.dim() == 2}
