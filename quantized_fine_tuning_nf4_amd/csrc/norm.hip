@@ -745,12 +745,15 @@ __global__ __launch_bounds__(64 * kSumGroups) void k_norm_sums(const float* __re
   }
 }
 
-// Threads of a launch, for 256 compute units: as many as stay resident (at
-// 8192 x 4096 the forward took 52 / 51 / 58 us with half, this and twice as
-// many, the backward with column sums 91 / 97 us with this and twice as many).
-// Rows of more than 512 threads: two workgroups a compute unit in the forward
-// where they fit, one in the backward.
-constexpr int64_t kFwdThreads = 256 * 2048, kBwdThreads = 256 * 1024, kSumThreads = 256 * 512;
+// Workgroups that stay resident on 256 compute units when their registers leave
+// room for `waves` waves on each: 20 in the forward, 16 in the backward, 12 with
+// column sums (10 taken: fewer partial sums).  A launch takes no other number,
+// or the last ones run alone: 8192 x 2560 with 409 workgroups 78 us, with 512
+// 66.
+int64_t resident(int waves, int threads) {
+  return 256 * std::max(1, waves / (threads / 64));
+}
+constexpr int kFwdWaves = 20, kBwdWaves = 16, kSumWaves = 10;
 // Columns up to which a row's threads keep the column sums.
 constexpr int64_t kSumCols = 8192;
 constexpr int kColumnSlices = 64;
@@ -809,8 +812,9 @@ hipError_t norm_fwd(const BlockNorm& n, const void* h, const uint16_t* o, void* 
     constexpr int G = group_threads(TPR) / TPR;
     const int T = threads_of<TPR, NV>(n.D);
     const int64_t groups = (n.M + G - 1) / G;
-    const int64_t wgs = T > 512 ? kFwdThreads / 2048 * (1280 / T) : kFwdThreads / T;
-    const dim3 grid((unsigned)std::min<int64_t>(groups, wgs));
+    // (two rounds of them run as fast, and end more evenly)
+    const int64_t wgs = resident(kFwdWaves, T) * (T > 512 ? 1 : 2);
+    const dim3 grid((unsigned)std::min(groups, wgs));
     const NormArgs a = args_of(n);
     const Slots slots = slots_of(n, keeps(TPR, NV), {false, false, false}, T, NV);
     const size_t lds = (size_t)slots.count * 16 * T * NV;
@@ -858,7 +862,7 @@ hipError_t norm_bwd(const BlockNorm& n, const uint16_t* dy, const void* dh_new, 
         return launch(std::conditional_t<(TPR < 1024), Regs, InLds>{}, block_norm_slices(n.M, n.D));
     }
     return launch(std::integral_constant<int, kSumsNone>{},
-                  std::min<int64_t>(groups, T > 512 ? 256 : kBwdThreads / T));
+                  std::min(groups, resident(kBwdWaves, T)));
   });
   if (e != hipSuccess || !part || n.D <= kSumCols) return e;
   const dim3 grid((unsigned)((n.D + 2047) / 2048), (unsigned)block_norm_slices(n.M, n.D));
@@ -883,7 +887,7 @@ hipError_t launch_block_norm_fwd(const BlockNorm& n, const void* h, const uint16
 int block_norm_slices(int64_t M, int64_t D) {
   if (D > kSumCols) return (int)std::min<int64_t>(M, kColumnSlices * 16384 / (2048 * ((D + 2047) / 2048)));
   const int64_t T = D <= 512 ? 256 : (D + 511) / 512 * 64, G = D <= 512 ? 4 : 1;
-  return (int)std::min<int64_t>((M + G - 1) / G, D > 4096 ? 256 : kSumThreads / T);
+  return (int)std::min<int64_t>((M + G - 1) / G, resident(kSumWaves, (int)T));
 }
 int64_t block_norm_stats(int64_t M, int64_t D) { return D > kSumCols ? 4 * M : 0; }
 
