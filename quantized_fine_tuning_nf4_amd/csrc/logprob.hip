@@ -191,16 +191,19 @@ struct Best {
   __device__ __forceinline__ uint32_t known() const { return (uint32_t)(bar >> 32); }
 };
 
-// The other lane's key at distance D.
+// The value of the lane at distance D (lane ^ D), without a trip through LDS.
 template <int D>
 __device__ __forceinline__ uint32_t xor_lanes(uint32_t x) {
   if constexpr (D == 1) return dpp<kDppXor1>(x);
   if constexpr (D == 2) return dpp<kDppXor2>(x);
-  if constexpr (D == 4 || D == 8 || D == 16)
-    return (uint32_t)__builtin_amdgcn_ds_swizzle((int)x, (D << 10) | 0x1f);
-  const bool upper = (threadIdx.x & 32) != 0;
+  if constexpr (D == 4) return dpp<0x1b>(dpp<kDppMirror8>(x));  // (i ^ 7) ^ 3
+  if constexpr (D == 8) return dpp<0x128>(x);                   // row_ror:8
+  if constexpr (D == 16) {
+    auto s = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return (threadIdx.x & 16) ? s[0] : s[1];
+  }
   auto s = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-  return upper ? s[0] : s[1];
+  return (threadIdx.x & 32) ? s[0] : s[1];
 }
 template <int D>
 __device__ __forceinline__ void merge_step(Key& x) {
