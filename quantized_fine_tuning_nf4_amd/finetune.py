@@ -24,6 +24,7 @@ from . import (QN_BF16, QN_F32, NF4State, _Act8, _BlockNorm, _check, _dev, _line
                _ptr, _stream, load_library)
 
 ACT8_BLOCK = 64
+MAX_TOP = 32  # alternatives of a row
 GATE_NONE, GATE_CHANNEL, GATE_ROW, GATE_ELEMENT = range(4)
 _DTYPES = {torch.bfloat16: QN_BF16, torch.float32: QN_F32}
 
@@ -312,6 +313,8 @@ def token_logprobs_fwd(logits: torch.Tensor, targets: torch.Tensor | None = None
     None with top_k = 0)."""
     L = load_library()
     T, V, ld = _logits(logits, targets)
+    if not 0 <= top_k <= min(MAX_TOP, V):
+        raise ValueError(f"top_k must be 0 .. {min(MAX_TOP, V)}")
     dev = logits.device
     f32 = torch.float32
     logp = None if targets is None else torch.empty(T, dtype=f32, device=dev)

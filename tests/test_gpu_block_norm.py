@@ -350,3 +350,29 @@ def test_autograd(qn):
     h3 = t["h"].cuda().requires_grad_(True)
     norm(h3, o.detach())[0].sum().backward()
     assert torch.allclose(h3.grad, torch.ones_like(h3))
+
+
+def test_rows_past_32_bit_offsets(qn):
+    """More than 2^31 values: the last rows are those of a small call."""
+    M, D, k = 1 << 19, 4160, 8
+    t = _dev(_inputs(k, D, False, True, "norm", "channel", seed=21))
+    say(f"[norm far rows] M={M} D={D}")
+    big = {n: torch.zeros(M, D, dtype=torch.bfloat16, device="cuda")
+           for n in ("h", "o", "dy", "dh_new")}
+    for n, v in big.items():
+        v[-k:] = t[n]
+    args = dict(w_post=t["w_post"], gate=t["gate"], scale=0.5)
+    hn, y, x8 = qn.block_norm_fwd(big["h"], t["w_pre"], o=big["o"], pack=True, **args)
+    rh, ry, r8 = qn.block_norm_fwd(t["h"], t["w_pre"], o=t["o"], pack=True, **args)
+    assert torch.equal(hn[-k:], rh) and torch.equal(y[-k:], ry)
+    assert torch.equal(x8.codes[-k:], r8.codes) and torch.equal(x8.exps[-k:], r8.exps)
+    del y
+    g = qn.block_norm_bwd(big["dy"], hn, t["w_pre"], dh_new=big["dh_new"], o=big["o"], **args)
+    r = qn.block_norm_bwd(t["dy"], rh, t["w_pre"], dh_new=t["dh_new"], o=t["o"], **args)
+    assert torch.equal(g.dh[-k:], r.dh) and torch.equal(g.do[-k:], r.do)
+    # the zero rows add nothing to the sums, in whatever order
+    for a, b in ((g.dw_pre, r.dw_pre), (g.dw_post, r.dw_post), (g.dgate, r.dgate)):
+        assert torch.allclose(a, b, rtol=1e-5, atol=1e-5 * float(b.abs().max()))
+    # and a checkpoint of as many values, read back
+    back = qn.act8_unpack(qn.act8_pack(hn))
+    assert torch.equal(back[-k:], qn.act8_unpack(qn.act8_pack(rh)))
