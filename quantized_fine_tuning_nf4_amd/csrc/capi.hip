@@ -789,9 +789,8 @@ qn_status block_norm_bwd(const qn_block_norm* n, const uint16_t* dy, const void*
 }
 
 size_t token_logprobs_workspace(int64_t T, int64_t V, qn_dtype dtype, int top_k) {
-  (void)dtype;
   if (T < 1 || T > kMaxRowsM || V < 1 || V > kMaxVocab || top_k < 0) return 0;
-  return logprob_workspace(T, V, top_k);
+  return logprob_workspace(T, V, dtype == QN_F32, top_k);
 }
 
 qn_status token_logprobs_fwd(const void* logits, qn_dtype dtype, int64_t T, int64_t V, int64_t ld,

@@ -25,7 +25,6 @@ namespace qn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
 constexpr int kU = 4;     // vectors of a thread in flight
 constexpr int kList = 32; // alternatives of a list
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
@@ -166,19 +165,21 @@ struct Best {
     }
   }
   // Before anything was offered: tops holds the best of a few logits of each
-  // lane of the workgroup, as ordered numbers.  The k-th largest of them bounds
-  // the k-th best logit from below; its leading 16 bits are enough (and all of
-  // a bf16), found bit by bit from how many lanes reach them.
+  // lane of the workgroup's W waves, as ordered numbers.  The k-th largest of
+  // 256 of them (each the best of W / 4 lanes) bounds the k-th best logit from
+  // below; its leading 16 bits are enough (and all of a bf16), found bit by bit
+  // from how many reach them.
+  template <int W>
   __device__ __forceinline__ void start(const uint32_t* tops, int k) {
-    uint32_t u[kWaves], low = 0;
+    uint32_t u[4] = {}, low = 0;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) u[w] = tops[64 * w + (threadIdx.x & 63)];
+    for (int w = 0; w < W; ++w) u[w & 3] = max(u[w & 3], tops[64 * w + (threadIdx.x & 63)]);
 #pragma unroll
     for (int b = 31; b >= 16; --b) {
       const uint32_t c = low | (1u << b);
       int n = 0;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) n += __builtin_popcountll(__ballot(u[w] >= c));
+      for (int w = 0; w < 4; ++w) n += __builtin_popcountll(__ballot(u[w] >= c));
       if (n >= k) low = c;
     }
     at_least(low);
@@ -272,15 +273,16 @@ __device__ __forceinline__ void write_row(const RowOut& r, int64_t row, const St
   }
 }
 
-// Workgroup b: slice b % S of row b / S.  A slice's results go to parts and
-// lists, or, when S is 1, straight to the outputs.
-template <typename L, bool TOP>
-__global__ __launch_bounds__(kThreads) void k_logprobs_fwd(const L* __restrict__ x, int64_t V,
+// Workgroup b of W waves: slice b % S of row b / S, U vectors a thread in flight.
+// A slice's results go to parts and lists, or, when S is 1, straight to the
+// outputs.
+template <typename L, bool TOP, int W, int U>
+__global__ __launch_bounds__(64 * W) void k_logprobs_fwd(const L* __restrict__ x, int64_t V,
                                                            int64_t ld, int S, int64_t slice,
                                                            RowOut out, Stat* __restrict__ parts,
                                                            Key* __restrict__ lists) {
   constexpr int N = Vec<L>::N;
-  constexpr int64_t kStep = kThreads * N;
+  constexpr int64_t kStep = 64 * W * N;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int64_t row = S == 1 ? (int64_t)blockIdx.x : (int64_t)(blockIdx.x / (unsigned)S);
   const int64_t z = blockIdx.x - row * S;
@@ -298,23 +300,25 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_fwd(const L* __restrict__
   // what each wave's bar is by now: a logit below any of them is none of the
   // row's best.  Read and written without order: an old value only lets more
   // through.
-  __shared__ uint32_t bars[kWaves], tops[TOP ? kThreads : 1];
+  __shared__ uint32_t bars[W], tops[TOP ? 64 * W : 1];
   if constexpr (TOP) {
-    if (tid < kWaves) bars[tid] = 0u;
+    if (tid < W) bars[tid] = 0u;
     __syncthreads();
   }
-  auto take = [&](Vec<L>(&v)[kU], int64_t i, bool first) {
-    float top[kU], mx;
+  auto take = [&](Vec<L>(&v)[U], int64_t i, bool first) {
+    float top[U], mx;
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
+    for (int u = 0; u < U; ++u) {
       top[u] = v[u].get(0);
 #pragma unroll
       for (int j = 1; j < N; ++j) top[u] = fmaxf(top[u], v[u].get(j));
     }
-    mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    mx = top[0];
+#pragma unroll
+    for (int u = 1; u < U; ++u) mx = fmaxf(mx, top[u]);
     if (__any(mx > a.m)) rebase(a, fmaxf(a.m, mx), k2);
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const float d = (v[u].get(j) - a.m) * k2, e = exp2_of(d);
@@ -325,16 +329,16 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_fwd(const L* __restrict__
       if (first) {
         tops[tid] = ordered(mx);
         __syncthreads();
-        best.start(tops, out.k);
+        best.template start<W>(tops, out.k);
       } else {
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w)
+        for (int w = 0; w < W; ++w)
           best.at_least(__builtin_amdgcn_readfirstlane(__hip_atomic_load(
               &bars[w], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP)));
       }
       if (__any(mx >= best.bar_value)) {
 #pragma unroll
-        for (int u = 0; u < kU; ++u)
+        for (int u = 0; u < U; ++u)
           if (__any(top[u] >= best.bar_value)) {
 #pragma unroll
             for (int j = 0; j < N; ++j)
@@ -347,26 +351,26 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_fwd(const L* __restrict__
     }
   };
   int64_t i = begin + (int64_t)tid * N;
-  for (int64_t b = begin; b < end; b += kU * kStep, i += kU * kStep) {
-    Vec<L> v[kU];
-    if (b + kU * kStep <= end) {
+  for (int64_t b = begin; b < end; b += U * kStep, i += U * kStep) {
+    Vec<L> v[U];
+    if (b + U * kStep <= end) {
 #pragma unroll
-      for (int u = 0; u < kU; ++u)
+      for (int u = 0; u < U; ++u)
         v[u].v = *reinterpret_cast<const typename Vec<L>::any*>(p + i + u * kStep);
     } else {
 #pragma unroll
-      for (int u = 0; u < kU; ++u) v[u] = load_part<L>(p, i + u * kStep, end);
+      for (int u = 0; u < U; ++u) v[u] = load_part<L>(p, i + u * kStep, end);
     }
     take(v, i, b == begin);
   }
   wave_join(a, k2);
-  __shared__ Stat s[kWaves];
-  __shared__ Key sk[TOP ? kWaves / 2 : 1][kList];
+  __shared__ Stat s[W];
+  __shared__ Key sk[TOP ? W / 2 : 1][kList];
   if (lane == 0) s[wave] = a;
-  if constexpr (TOP) join_lists<kWaves>(best.mine, sk);
+  if constexpr (TOP) join_lists<W>(best.mine, sk);
   __syncthreads();
   if (wave != 0) return;
-  a = lane < kWaves ? s[lane] : Stat{-FLT_MAX, 0.f, 0.f};
+  a = lane < W ? s[lane] : Stat{-FLT_MAX, 0.f, 0.f};
   wave_join(a, k2);
   if (S == 1) {
     write_row(out, row, a, t, V, xt, best.mine);
@@ -464,32 +468,43 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_bwd(
   }
 }
 
-// Slices of a row: one, unless the rows are too few to keep 256 compute units
-// reading (four workgroups each); then as many as leave every thread two
-// vectors, at most 64.
-int64_t slice_length(int64_t T, int64_t V) {
-  const int64_t least = 2 * kThreads * 8;
+// How a call reads its rows.  Many rows, or short ones: a workgroup of four
+// waves each.  Up to 256 rows of up to 128 KB: a workgroup of 16 waves each (128
+// rows of 32000 bf16 logits 5.4 us, in slices 8.0; but one row of 131072 fp32 10.8
+// us, in slices 4.4: one compute unit reads no faster).  Other few rows: cut in
+// slices that leave every thread of a small workgroup two vectors, at most 64,
+// joined by a second launch.
+constexpr int64_t kWideBytes = 128 * 1024;
+constexpr int64_t kWideRows = 256;
+constexpr int64_t kLeastSlice = 2 * kThreads * 8;
+bool wide(int64_t T, int64_t V, bool f32) {
+  return T <= kWideRows && V >= 2 * kLeastSlice && V * (f32 ? 4 : 2) <= kWideBytes;
+}
+int64_t slice_length(int64_t T, int64_t V, bool f32) {
   int64_t S = std::min<int64_t>((1024 + T - 1) / T, 64);
-  S = std::max<int64_t>(1, std::min<int64_t>(S, V / least));
-  const int64_t len = (V + S - 1) / S;
-  return S == 1 ? V : (len + 511) / 512 * 512;
+  S = std::min<int64_t>(S, V / kLeastSlice);
+  if (S <= 1 || wide(T, V, f32)) return V;
+  return ((V + S - 1) / S + 511) / 512 * 512;
 }
 
 template <typename L>
 hipError_t logprobs_fwd(const L* x, int64_t T, int64_t V, int64_t ld, const RowOut& out, void* ws,
                         hipStream_t st) {
-  const int64_t slice = slice_length(T, V);
-  const int S = logprob_slices(T, V);
+  constexpr bool f32 = sizeof(L) == 4;
+  const int64_t slice = slice_length(T, V, f32);
+  const int S = logprob_slices(T, V, f32);
   Stat* parts = static_cast<Stat*>(ws);
   Key* lists = reinterpret_cast<Key*>(static_cast<char*>(ws) + logprob_parts_bytes(T, S));
   const dim3 grid((unsigned)(T * S));
-  if (out.k > 0)
-    hipLaunchKernelGGL((k_logprobs_fwd<L, true>), grid, dim3(kThreads), 0, st, x, V, ld, S, slice,
-                       out, parts, lists);
-  else
-    hipLaunchKernelGGL((k_logprobs_fwd<L, false>), grid, dim3(kThreads), 0, st, x, V, ld, S, slice,
-                       out, parts, lists);
-  const hipError_t e = hipGetLastError();
+  auto launch = [&](auto f, int threads) {
+    hipLaunchKernelGGL(f, grid, dim3(threads), 0, st, x, V, ld, S, slice, out, parts, lists);
+    return hipGetLastError();
+  };
+  if (wide(T, V, f32))
+    return out.k > 0 ? launch(k_logprobs_fwd<L, true, 16, kU>, 1024)
+                     : launch(k_logprobs_fwd<L, false, 16, kU>, 1024);
+  const hipError_t e = out.k > 0 ? launch(k_logprobs_fwd<L, true, 4, kU>, kThreads)
+                                 : launch(k_logprobs_fwd<L, false, 4, kU>, kThreads);
   if (e != hipSuccess || S == 1) return e;
   if (out.k == 0)
     hipLaunchKernelGGL((k_logprobs_join<L, 1>), dim3((unsigned)T), dim3(64), 0, st, x, V, ld, S, out,
@@ -505,13 +520,13 @@ hipError_t logprobs_fwd(const L* x, int64_t T, int64_t V, int64_t ld, const RowO
 
 }  // namespace
 
-int logprob_slices(int64_t T, int64_t V) {
-  const int64_t slice = slice_length(T, V);
+int logprob_slices(int64_t T, int64_t V, bool f32) {
+  const int64_t slice = slice_length(T, V, f32);
   return (int)((V + slice - 1) / slice);
 }
 size_t logprob_parts_bytes(int64_t T, int S) { return ((size_t)T * S * sizeof(Stat) + 15) / 16 * 16; }
-size_t logprob_workspace(int64_t T, int64_t V, int k) {
-  const int S = logprob_slices(T, V);
+size_t logprob_workspace(int64_t T, int64_t V, bool f32, int k) {
+  const int S = logprob_slices(T, V, f32);
   if (S == 1) return 0;
   return logprob_parts_bytes(T, S) + (k > 0 ? (size_t)T * S * kList * sizeof(Key) : 0);
 }

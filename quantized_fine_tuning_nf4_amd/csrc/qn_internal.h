@@ -374,9 +374,9 @@ hipError_t launch_block_norm_bwd(const BlockNorm& n, const uint16_t* dy, const v
 // Token log probabilities (see the header).  ws: logprob_workspace bytes,
 // 16-byte aligned (rows cut in logprob_slices slices, joined by a second
 // launch).
-int logprob_slices(int64_t T, int64_t V);
+int logprob_slices(int64_t T, int64_t V, bool f32);
 size_t logprob_parts_bytes(int64_t T, int S);
-size_t logprob_workspace(int64_t T, int64_t V, int k);
+size_t logprob_workspace(int64_t T, int64_t V, bool f32, int k);
 hipError_t launch_logprobs_fwd(const void* x, bool f32, int64_t T, int64_t V, int64_t ld,
                                const int64_t* targets, float scale, int k, float* logp,
                                float* entropy, float* stats, float* top_logp, int32_t* top_ids,

@@ -96,6 +96,7 @@ def _check(qn, x, t, scale=1.0, k=0):
 
 SIZES = [(1, 1), (3, 2), (2, 7), (5, 63), (4, 64), (7, 65), (1, 511), (6, 513), (3, 1000),
          (2, 2047), (300, 257), (1, 4099), (17, 8192), (2, 32000), (9, 50021), (1, 131072),
+         (256, 8192), (100, 30011),
          (5, 131075), (40, 16384), (600, 1024)]
 
 
