@@ -532,7 +532,7 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
 #pragma unroll
   for (int k = 0; k < VL; ++k) {
     const int q = min(VL * wave + k, SP * NJ - 1), row = 16 * q + (lane >> 2);
-    voff[k] = (uint32_t)(row * Mp * 2 + 16 * (lane & 3));
+    voff[k] = (uint32_t)(row * Mp * 2 + 16 * ((lane & 3) ^ (lane >> 4)));
     vdst[k] = ZB + 1024 * q;
   }
   // the steps, on codes or on bf16
@@ -680,7 +680,7 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
 #pragma unroll
       for (int jt = 0; jt < NJ; ++jt) {
         // B operand: column j = 16jt + l%16, rows 8g..8g+7 of the step
-        const uint8_t* vs = zs + ZB + (16 * jt + t) * 64 + 16 * g;
+        const uint8_t* vs = zs + ZB + (16 * jt + t) * 64 + 16 * (g ^ (t >> 2));
         bf16x8 b[SP];
 #pragma unroll
         for (int q = 0; q < SP; ++q)

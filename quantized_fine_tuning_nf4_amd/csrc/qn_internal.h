@@ -76,14 +76,16 @@ struct BwdAux {
   float s;
   bool three_parts;
 };
-// The jobs are rows in blocks of 16 ranks, one per thread: a row n of B (Bt[j][n]
+constexpr int kAuxRanks = 4;
+// The jobs are rows in blocks of kAuxRanks ranks (16 ceil(r / 16) in all), one per
+// thread: a row n of B (Bt[j][n]
 // = B[n][j]), a column k of A (At[k][j] = A[j][k]), a column m of su and of sv.
 // A thread reads its ranks of B, u or v's slices in 16-byte loads when r allows,
 // the threads of a wave read neighbouring elements of A's rows, and the
 // transposed writes of neighbouring threads are neighbours.
 __host__ __device__ inline int64_t bwd_aux_count(const BwdAux& a) {
   return ((a.Bt ? a.N : 0) + (a.At ? a.K : 0) + (a.su ? a.Mpu : 0) + (a.sv ? a.Mpv : 0)) *
-         ((a.r + 15) / 16);
+         ((a.r + 15) / 16 * (16 / kAuxRanks));
 }
 // x as bf16 at dst[idx] and its remainder as bf16 at dst[half + idx] (three:
 // what that leaves at dst[2 half + idx])
@@ -100,23 +102,19 @@ __device__ inline void put_split(uint16_t* dst, int64_t half, int64_t idx, float
 __device__ inline void bwd_aux_at(const BwdAux& a, int64_t i) {
   const int r = a.r;
   const int64_t rp = 16 * ((r + 15) / 16);
-  int jb = 0;  // this block's ranks: jb .. je - 1
-  if (r > 16) {
-    const int64_t rows = bwd_aux_count(a) / ((r + 15) / 16);
-    const int64_t b = i / rows;
-    jb = (int)b * 16;
-    i -= b * rows;
-  }
-  const int je = jb + 16 < r ? jb + 16 : r;
+  const int64_t rows = bwd_aux_count(a) / (rp / kAuxRanks);
+  const int jb = (int)(i / rows) * kAuxRanks;  // this block's ranks: jb .. je - 1
+  i %= rows;
+  const int je = min(jb + kAuxRanks, r);
   const int64_t nb = a.Bt ? a.N : 0;
   if (i < nb) {  // Bt[j][n] = B[n][j]
     const int64_t n = i;
     const uint16_t* row = a.B + n * r;
-    if ((r & 7) == 0) {
-      for (int j0 = jb; j0 < je; j0 += 8) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(row + j0);
+    if ((r & 3) == 0) {
+      for (int j0 = jb; j0 < je; j0 += 4) {
+        const u32x2 v = *reinterpret_cast<const u32x2*>(row + j0);
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
+        for (int q = 0; q < 4; ++q)
           a.Bt[(int64_t)(j0 + q) * a.N + n] = (uint16_t)(v[q >> 1] >> (16 * (q & 1)));
       }
     } else {
@@ -129,14 +127,14 @@ __device__ inline void bwd_aux_at(const BwdAux& a, int64_t i) {
   if (i < na) {  // At[k][j] = A[j][k]
     const int64_t k = i;
     uint16_t* row = a.At + k * r;
-    if ((r & 7) == 0) {
-      for (int j0 = jb; j0 < je; j0 += 8) {
-        uint32_t w[4];
+    if ((r & 3) == 0) {
+      for (int j0 = jb; j0 < je; j0 += 4) {
+        uint32_t w[2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 2; ++q)
           w[q] = (uint32_t)a.A[(int64_t)(j0 + 2 * q) * a.K + k] |
                  ((uint32_t)a.A[(int64_t)(j0 + 2 * q + 1) * a.K + k] << 16);
-        *reinterpret_cast<u32x4*>(row + j0) = u32x4{w[0], w[1], w[2], w[3]};
+        *reinterpret_cast<u32x2*>(row + j0) = u32x2{w[0], w[1]};
       }
     } else {
       for (int j = jb; j < je; ++j) row[j] = a.A[(int64_t)j * a.K + k];
@@ -154,7 +152,7 @@ __device__ inline void bwd_aux_at(const BwdAux& a, int64_t i) {
   const int64_t half = rp * Mp;
   const bool in = m < a.M;
   const bool vec = (r & 3) == 0;
-  for (int j0 = jb; j0 < jb + 16; j0 += 4) {
+  for (int j0 = jb; j0 < jb + kAuxRanks; j0 += 4) {
     float x[4] = {0.f, 0.f, 0.f, 0.f};
     if (in && j0 < r) {
       const int64_t e = m * r + j0;
