@@ -154,7 +154,7 @@ FwdWs carve_fwd(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool ne
 struct BwdWs {
   unsigned* arrivals;  // [kArrivalWords] arrival counters
   FwdWs fu;      // recomputed u (if not saved)
-  uint16_t* Bt;  // [r, rows]
+  uint16_t* Bt;  // [r, rows]; x in 8 bits: B in launch_thin_v's order, [rp, rows up to 32]
   float* v;      // [M, r]
   float* vpart;  // [Sv, M, r]
   int Sv;
@@ -179,11 +179,11 @@ BwdWs carve_bwd(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool ne
     b.fu = FwdWs{};
     b.fu.S = 1;
   }
-  b.Bt = c.take<uint16_t>((size_t)r * rows);
+  const int64_t rp = 16 * ((r + 15) / 16);
+  b.Bt = c.take<uint16_t>((size_t)(act8 ? rp * round_up(rows, 32) : r * rows));
   b.Sv = thin_nt_slices(M, rows);
   b.v = c.take<float>((size_t)M * r);
-  b.vpart = b.Sv > 1 ? c.take<float>((size_t)b.Sv * M * r) : nullptr;
-  const int64_t rp = 16 * ((r + 15) / 16);
+  b.vpart = b.Sv > 1 && !act8 ? c.take<float>((size_t)b.Sv * M * r) : nullptr;
   b.Sb = thin_tn_slices(M, rows, act8);
   b.dBpart = c.take<float>((size_t)b.Sb * rows * r);
   const size_t parts = act8 ? 3 : 2;
@@ -354,21 +354,41 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
   const float* u = u_saved;
   // an early launch of the call zeroes the arrival counters the adapter
   // gradients' launch counts on, so the backward never depends on what the
-  // workspace held before.  With x in 8 bits and more than 16 ranks the slices
-  // of those gradients (r times as many values as a column tile is wide) are
-  // added by a launch of their own instead: one workgroup a tile took 66 us
-  // for 4096x1024x4096 at r = 64 where the whole call now takes 50
-  unsigned* arrivals = x8 && r > 16 ? nullptr : b.arrivals;
+  // workspace held before.  With x in 8 bits the slices of those gradients are
+  // added by a launch of their own instead, unless the call is so short that it
+  // waits for its launches: without dX 8192x4096x4096 at r = 16 40.3 -> 38.0 us,
+  // 4096x4096x2048 at r = 8 25.8 -> 23.6, but 1024x1024x2048 17.3 -> 21.6; past 16
+  // ranks a tile's last workgroup has too many values to add (4096x1024x4096 at
+  // r = 64: 66 us for what takes 30)
+  const bool few_launches = r <= 16 && M * (N + K) < (int64_t)1 << 24;
+  unsigned* arrivals = x8 && !few_launches ? nullptr : b.arrivals;
   Clear clr{arrivals, arrivals ? kArrivalWords : 0};
   if (!u && e == hipSuccess) {
     e = launch_thin_nt(x, A, M, K, r, b.fu.u, b.fu.upart, b.fu.S, st, true, false, clr, lo.mask);
     clr = Clear{nullptr, 0};
     u = b.fu.u;
   }
-  // v = G B as slices (added below); the product takes B as stored when it
-  // can, else B^T made first
+  // v = G B.  With x in 8 bits: whole, and (s v)^T with it, from B in the order of
+  // the product's operands, made first (and with that (s u)^T).  Else in slices
+  // (added below); the product takes B as stored when it can, else B^T made first.
   const bool b_rows = thin_nt_rows_ok(M, N, r);
-  if (e == hipSuccess && !b_rows) {
+  if (e == hipSuccess && x8) {
+    BwdAux t{};
+    t.B = B;
+    t.Bf = b.Bt;
+    t.N = N;
+    t.u = u;
+    t.su = b.su;
+    t.Mpu = thin_tn_rows_padded(M, N, true);
+    t.M = M;
+    t.r = r;
+    t.s = scale;
+    t.three_parts = true;
+    e = launch_bwd_aux(t, st, clr);
+    if (e == hipSuccess)
+      e = launch_thin_v(dY, b.Bt, M, N, r, b.v, b.sv, thin_tn_rows_padded(M, K, true), scale, st);
+  }
+  if (e == hipSuccess && !x8 && !b_rows) {
     if (clr.n) {  // (no earlier launch: a kernel, not a memset, for graph capture)
       e = launch_fill_zero(reinterpret_cast<float*>(clr.p), clr.n, st);
       clr = Clear{nullptr, 0};
@@ -380,10 +400,10 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
     t.r = r;
     e = launch_bwd_aux(t, st);
   }
-  if (e == hipSuccess)
+  if (e == hipSuccess && !x8)
     e = launch_thin_nt(dY, b_rows ? B : b.Bt, M, N, r, b.v, b.vpart, b.Sv, st, false, b_rows,
                        clr);
-  // the small jobs: v's slice sum, (s u)^T and (s v)^T split for the
+  // the small jobs: v's slice sum, (s u)^T and (s v)^T split (unless made above) for the
   // transposed products, A^T for the dense dX product; in spare workgroups of
   // the transposed dequantization when there is one
   const bool dense_dx = dX && b.wt;
@@ -392,17 +412,16 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
   aux.At = dense_dx ? b.At : nullptr;
   aux.K = K;
   aux.u = u;
-  aux.su = b.su;
-  aux.Mpu = thin_tn_rows_padded(M, N, x8 != nullptr);
+  aux.su = x8 ? nullptr : b.su;
+  aux.Mpu = thin_tn_rows_padded(M, N, false);
   aux.vpart = b.vpart;
   aux.Sv = b.Sv;
   aux.v = b.v;
-  aux.sv = b.sv;
-  aux.Mpv = thin_tn_rows_padded(M, K, x8 != nullptr);
+  aux.sv = x8 ? nullptr : b.sv;
+  aux.Mpv = thin_tn_rows_padded(M, K, false);
   aux.M = M;
   aux.r = r;
   aux.s = scale;
-  aux.three_parts = x8 != nullptr;
   if (e == hipSuccess) {
     if (dense_dx)
       e = launch_dequant_t(w->packed, w->qscale, w->scale2, w->offset, N, K, b.wt, b.ldt, aux,

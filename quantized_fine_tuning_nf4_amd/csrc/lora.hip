@@ -121,6 +121,106 @@ __global__ __launch_bounds__(kThreads) void k_thin_nt(const uint16_t* __restrict
   }
 }
 
+// v[M, r] = G[M, N] B[N, r] whole, and with it (s v)^T in three bf16 parts as
+// the transposed product takes it (parts of 16 NJ rows of Mp, zero past r and M).
+// Workgroup: 16 RT rows; its eight waves take U steps of 32 columns in turn, with
+// the operands as in k_thin_nt, and their sums meet in LDS, added in wave order.
+// So v is never in slices: with k_thin_nt's column slices and a launch that adds and
+// splits them the whole backward without dX takes 39.4 us for 4096x1024x4096 at
+// r = 64 (29.7 here), 85 for 8192x4096x4096 at r = 64 (59), 51 at r = 8 (37).  Bound
+// by the rows of G from HBM where r is small, else by B from the L2, which every
+// workgroup reads whole: in the order of the operands a wave's load is 1 KB in a
+// row.  From the rows of B^T (64 bytes of 16 rows a load) the three took 31.9, 79
+// and 49 us; 32 rows a workgroup, half the bytes of B, 33.0 and 61, since twice
+// the workgroups hide more of the latency.
+constexpr int kVWaves = 8;
+template <int NJ>
+__global__ __launch_bounds__(64 * kVWaves) void k_thin_v(const uint16_t* __restrict__ G,
+                                                         const uint16_t* __restrict__ Bf,
+                                                         int64_t M, int64_t N, int r,
+                                                         float* __restrict__ v,
+                                                         uint16_t* __restrict__ sv, int64_t Mp,
+                                                         float s) {
+  constexpr int U = 4, PITCH = 16 + 4;
+  __shared__ __attribute__((aligned(16))) float sums[kVWaves][16 * NJ][PITCH];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int g = lane >> 4, l16 = lane & 15;
+  const int64_t m0 = 16 * (int64_t)blockIdx.x;
+  const int64_t steps = (N + 31) / 32;
+  const uint16_t* gp = G + min(m0 + l16, M - 1) * N + 8 * g;
+  const int64_t lim = N - 8 * g;  // columns left for this lane's chunk
+  f32x4 acc[NJ] = {};
+  for (int64_t s0 = U * wave; s0 < steps; s0 += U * kVWaves) {
+    u32x4 za[U], tb[U][NJ];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t off = 32 * (s0 + u);
+      // past the row: its first columns
+      za[u] = *reinterpret_cast<const u32x4*>(gp + (off < lim ? off : -8 * g));
+#pragma unroll
+      for (int jt = 0; jt < NJ; ++jt)
+        tb[u][jt] = *reinterpret_cast<const u32x4*>(
+            Bf + ((min(s0 + u, steps - 1) * NJ + jt) * 64 + lane) * 8);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool ok = 32 * (s0 + u) < lim;
+      if (!ok) za[u] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int jt = 0; jt < NJ; ++jt) {
+        u32x4 b = tb[u][jt];
+        if (!ok) b = u32x4{0u, 0u, 0u, 0u};
+        acc[jt] = mfma16(as_bf16x8(za[u]), as_bf16x8(b), acc[jt]);
+      }
+    }
+  }
+  // lane: column j = 16jt + l%16, rows 4(l/16) + i
+#pragma unroll
+  for (int jt = 0; jt < NJ; ++jt)
+    *reinterpret_cast<f32x4*>(&sums[wave][16 * jt + l16][4 * g]) = acc[jt];
+  __syncthreads();
+  // four rows of one column a thread
+  if (tid < 64 * NJ) {
+    const int j = tid >> 2, q = tid & 3;
+    f32x4 x = *reinterpret_cast<const f32x4*>(&sums[0][j][4 * q]);
+#pragma unroll
+    for (int w = 1; w < kVWaves; ++w) x += *reinterpret_cast<const f32x4*>(&sums[w][j][4 * q]);
+    const int64_t m = m0 + 4 * q;
+    u32x2 part[3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in = j < r && m + i < M;
+      if (in) v[(m + i) * r + j] = x[i];
+      float rest = in ? s * x[i] : 0.f;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const uint32_t h = pack_bf16x2(rest, 0.f) & 0xffffu;
+        part[k][i >> 1] = i & 1 ? part[k][i >> 1] | (h << 16) : h;
+        rest -= bf16_lo(h);
+      }
+    }
+    if (m < Mp)
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        *reinterpret_cast<u32x2*>(sv + ((int64_t)k * 16 * NJ + j) * Mp + m) = part[k];
+  }
+}
+
+hipError_t launch_thin_v(const uint16_t* G, const uint16_t* Bf, int64_t M, int64_t N, int r,
+                         float* v, uint16_t* sv, int64_t Mp, float s, hipStream_t st) {
+#define QN_V(NJ)                                                                              \
+  hipLaunchKernelGGL(k_thin_v<NJ>, dim3((unsigned)((Mp + 15) / 16)), dim3(64 * kVWaves), 0, st, G, \
+                     Bf, M, N, r, v, sv, Mp, s)
+  switch ((r + 15) / 16) {
+    case 1: QN_V(1); break;
+    case 2: QN_V(2); break;
+    case 3: QN_V(3); break;
+    default: QN_V(4); break;
+  }
+#undef QN_V
+  return hipGetLastError();
+}
+
 // r <= 16: the same product with T's slice (rows 0..15, zero past r)
 // staged in LDS once per workgroup (row pitch 64 steps + 16 bytes, so the
 // 16-byte reads of 8 consecutive rows fall in distinct bank groups), and Z
@@ -365,15 +465,17 @@ hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t st) {
   return hipGetLastError();
 }
 
-__global__ void k_bwd_aux(BwdAux a) {
+__global__ void k_bwd_aux(BwdAux a, Clear clr) {
+  clear_words(clr);
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i < bwd_aux_count(a)) bwd_aux_at(a, i);
 }
 
-hipError_t launch_bwd_aux(const BwdAux& a, hipStream_t st) {
+hipError_t launch_bwd_aux(const BwdAux& a, hipStream_t st, Clear clr) {
   const int64_t count = bwd_aux_count(a);
   if (count == 0) return hipSuccess;
-  hipLaunchKernelGGL(k_bwd_aux, dim3((unsigned)((count + 255) / 256)), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(k_bwd_aux, dim3((unsigned)((count + 255) / 256)), dim3(256), 0, st, a,
+                     clr);
   return hipGetLastError();
 }
 
@@ -396,18 +498,22 @@ __device__ __forceinline__ void dma16(rsrc_t rs, uint32_t voff, uint32_t soff, u
 
 constexpr int TN_COLS = 128;             // columns of Z per workgroup
 constexpr int TN_ROWB = TN_COLS * 2;     // 256 B per staged Z row
-constexpr int TN_NST = 3;  // stages (two steps in flight; three: 1.5 us slower per backward)
+// Stages (two steps in flight; three: 1.5 us slower per backward, and 46 us
+// against 39 for 4096x1024x4096 at r = 64 from an 8-bit checkpoint, whose LDS then
+// holds one workgroup a CU).
+constexpr int TN_NST = 3;
 
 }  // namespace
 
 // part[z][p][j] = sum over the rows m of slice z of Z[m, p] * (s V)[m, j]
 // (a transposed product: the reduction runs down the columns of Z).  Two
-// independent products (dB and dA of one backward) share the launch: grid x
-// runs over the column tiles of job 0, then those of job 1.  Workgroup
-// (pt, z): columns 128 pt .. +127, wave w: 32w .. 32w+31 (two 16-column MFMA
-// tiles).  A step is 32 rows: their Z (8 KB) and their (s V)^T parts (SP x 16 NJ
-// rows of 64 B) go global -> LDS by 16-byte-per-lane buffer loads into one
-// stage, three stages deep.
+// independent products (dB and dA of one backward) share the launch (the order
+// of their workgroups: tn_per_xcd).  Workgroup (pt, z): columns 128 pt .. +127,
+// wave w: 32w .. 32w+31 (two 16-column MFMA tiles).  A step is 32 rows: their
+// Z (8 KB) and their (s V)^T parts (SP x 16 NJ rows of 64 B) go global -> LDS by
+// 16-byte-per-lane buffer loads into one stage, three stages deep.  A 16-byte unit
+// c of (s V)^T row y sits at c ^ ((y >> 2) & 3), so that the 16 lanes that read one
+// unit of 16 rows touch 256 different bytes.
 // Z row y's 16-byte chunk c sits at unit c ^ 2(y & 3); the A operand (16
 // columns x 32 rows) is read transposed with ds_read_b64_tr_b16, lane t of a
 // 16-lane group addressing row 4h + t/4, columns 4(t%4)..+3, so that lane t
@@ -428,6 +534,16 @@ struct TnJob {
   int transposed;
   const uint8_t* zmask;  // keep bits of Z (dropout on x), or null
 };
+
+// With an 8-bit checkpoint (one-dimensional grid): workgroups of a job per XCD.
+// The XCDs take workgroups round robin; each takes a run of each job's
+// workgroups, ordered slice by slice, so that an XCD's L2 holds the (s V)^T of its
+// own slices alone (an eighth of it) rather than all of it, and every XCD has the
+// same share of both jobs (8192x4096x4096, r = 16 with dropout: 47.2 -> 42.9 us;
+// 4096x1024x4096, r = 64: 40.6 -> 39.4).  With bf16 rows, whose slices are added
+// by the tiles' last workgroups, that order is slower (r = 64: 48.2 -> 51.4): there
+// grid x runs over the column tiles of job 0, then job 1's, and y over the slices.
+__host__ __device__ inline int tn_per_xcd(const TnJob& j) { return (j.tiles * j.S + 7) / 8; }
 
 // Arrival counters of the column tiles of one launch (both jobs' tiles in
 // grid order) sit in the caller's workspace: zero when the launch starts,
@@ -464,6 +580,14 @@ __device__ __forceinline__ void wait_vm() {
 // register, two steps ahead; the rows' scales reach the 16 lanes by DPP, and
 // code times scale is a bf16 number exactly, so the MFMA sees the checkpoint's
 // values.
+// f(0), f(1), .. f(N - 1), each with its index as a constant.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void unrolled(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    unrolled<N, I + 1>(f);
+  }
+}
 template <int Q>
 __device__ __forceinline__ float row_scale(float scale) {
   return as_f32(dpp<0x150 + Q>(as_u32(scale)));  // row_newbcast: lane Q of each 16
@@ -475,9 +599,24 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
   constexpr int VB = SP * 16 * NJ * 64;        // (sV)^T bytes per stage
   constexpr int KB = MASK ? 32 * 16 : 0;       // keep bits per stage
   constexpr int SB = ZB + VB + KB;
+  constexpr int NST = TN_NST;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const bool second = (int)blockIdx.x >= j0.tiles;
+  // this workgroup's job, column tile and slice
+  bool second;
+  int pt_wg, z_wg;
+  if constexpr (Z8) {
+    const int xcd = (int)blockIdx.x & 7, n0 = tn_per_xcd(j0), ci = (int)blockIdx.x >> 3;
+    second = ci >= n0;
+    const int wi = second ? xcd * tn_per_xcd(j1) + ci - n0 : xcd * n0 + ci;
+    const int tiles = second ? j1.tiles : j0.tiles;
+    pt_wg = wi % tiles;
+    z_wg = wi / tiles;
+  } else {
+    second = (int)blockIdx.x >= j0.tiles;
+    pt_wg = (int)blockIdx.x - (second ? j0.tiles : 0);
+    z_wg = (int)blockIdx.y;
+  }
   const uint16_t* Z = second ? j1.Z : j0.Z;
   const uint16_t* vt = second ? j1.vt : j0.vt;
   const int64_t Mp = second ? j1.Mp : j0.Mp;
@@ -488,9 +627,9 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
   const uint8_t* zmask = MASK ? (second ? j1.zmask : j0.zmask) : nullptr;
   const bool hm = MASK && zmask != nullptr;  // workgroup-uniform
   const bool z8 = Z8 && second;              // workgroup-uniform
-  if ((int)blockIdx.y >= S) return;
-  const int64_t p0 = (int64_t)((int)blockIdx.x - (second ? j0.tiles : 0)) * TN_COLS;
-  const int64_t mb = (int64_t)blockIdx.y * slice;
+  if (z_wg >= S) return;  // past the job's workgroups
+  const int64_t p0 = (int64_t)pt_wg * TN_COLS;
+  const int64_t mb = (int64_t)z_wg * slice;
   const int64_t me = min(mb + slice, M);
   const int steps = (int)((me - mb + 31) / 32);
 
@@ -540,7 +679,7 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
   f32x4 acc[2][NJ] = {};
   auto run = [&](auto q8_t) {
     constexpr bool Q8 = decltype(q8_t)::value;
-    uint32_t ex[TN_NST] = {};  // per stage: the exponent of row 8 (l / 16) + l % 8
+    uint32_t ex[NST] = {};  // per stage: the exponent of row 8 (l / 16) + l % 8
     auto load_step = [&](int st, auto stage_t) {
       constexpr int stage = decltype(stage_t)::value;
       uint8_t* base = smem + stage * SB;
@@ -577,14 +716,12 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
     // their exponents, then (sV)^T) have landed (one more in waves 0 and 1 when
     // the keep bits come along)
     auto wait_step = [&]() {
-      static_assert(TN_NST == 3, "one step in flight beyond the next");
       if (MASK && hm && wave < 2)
-        wait_vm<2 + VL + (MASK ? 1 : 0)>();
+        wait_vm<(NST - 2) * (2 + VL + (MASK ? 1 : 0))>();
       else
-        wait_vm<2 + VL>();
+        wait_vm<(NST - 2) * (2 + VL)>();
     };
-    load_step(0, std::integral_constant<int, 0>{});
-    load_step(min(1, steps - 1), std::integral_constant<int, 1>{});
+    unrolled<NST - 1>([&](auto i) { load_step(min((int)i, steps - 1), i); });
     wait_step();
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
@@ -607,11 +744,11 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
       aoff8[pt] = row * TN_COLS + 16 * ((2 * wave + pt) ^ ((row >> 1) & 7)) + 8 * (t & 1);
     }
     // one step on stage P (a constant, so that the compiler sees the loads of
-    // step st+2 and this step's LDS reads touch different stages)
+    // the newest step and this step's LDS reads touch different stages)
     auto body = [&](auto p_t, int st) {
       constexpr int P = decltype(p_t)::value;
-      load_step(min(st + TN_NST - 1, steps - 1),
-                std::integral_constant<int, (P + TN_NST - 1) % TN_NST>{});
+      load_step(min(st + NST - 1, steps - 1),
+                std::integral_constant<int, (P + NST - 1) % NST>{});
       const uint8_t* zs = smem + P * SB;
       // the four transposed reads in one block that also waits for them (the
       // compiler would otherwise treat them as possibly overlapping the loads
@@ -690,22 +827,16 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
 #pragma unroll
           for (int q = 0; q < SP; ++q) acc[pt][jt] = mfma16(a[pt], b[q], acc[pt][jt]);
       }
-      // step st+1's loads (issued 2 steps ago) have landed everywhere before
+      // step st+1's loads (issued NST - 1 steps ago) have landed everywhere before
       // anyone reads them or overwrites this stage
       wait_step();
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     };
-    using S0 = std::integral_constant<int, 0>;
-    using S1 = std::integral_constant<int, 1>;
-    using S2 = std::integral_constant<int, 2>;
     int st = 0;
-    for (; st + 3 <= steps; st += 3) {
-      body(S0{}, st);
-      body(S1{}, st + 1);
-      body(S2{}, st + 2);
-    }
-    if (st < steps) body(S0{}, st);
-    if (st + 1 < steps) body(S1{}, st + 1);
+    for (; st + NST <= steps; st += NST) unrolled<NST>([&](auto i) { body(i, st + (int)i); });
+    unrolled<NST - 1>([&](auto i) {
+      if (st + (int)i < steps) body(i, st + (int)i);
+    });
   };
   if constexpr (Z8) {
     if (z8)
@@ -719,7 +850,7 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
   // lane: column j = 16jt + l%16, rows p = 16pt + 4(l/16) + i of the wave
   const int S_ = S;
   const rsrc_t rp = make_rs(part, (uint32_t)((int64_t)S_ * P * r * 4));
-  const int64_t sl_off = (int64_t)blockIdx.y * P * r;
+  const int64_t sl_off = (int64_t)z_wg * P * r;
 #pragma unroll
   for (int jt = 0; jt < NJ; ++jt) {
     const int j = 16 * jt + t;
@@ -752,7 +883,7 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   __shared__ int s_last;
-  unsigned* ctr = arrivals + blockIdx.x;
+  unsigned* ctr = arrivals + (second ? j0.tiles : 0) + pt_wg;
   if (tid == 0)
     s_last = __hip_atomic_fetch_add(ctr, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
              (unsigned)(S_ - 1);
@@ -947,7 +1078,8 @@ hipError_t launch_thin_tn2(const ThinTn& a, const ThinTn& b, int64_t M, int r,
   if (a.codes) return hipErrorInvalidValue;  // a checkpoint is the second job's
   const size_t lds =
       (size_t)TN_NST * (32 * TN_ROWB + (z8 ? 3 : 2) * 16 * nj * 64 + (mask ? 32 * 16 : 0));
-  const dim3 grid((unsigned)tiles, (unsigned)s_max);
+  const dim3 grid = z8 ? dim3(8u * (unsigned)(tn_per_xcd(job[0]) + tn_per_xcd(job[1])))
+                       : dim3((unsigned)tiles, (unsigned)s_max);
 #define QN_TN2(NJ, MASK, SP, Z8)                                                           \
   hipLaunchKernelGGL((k_thin_tn<NJ, MASK, SP, Z8>), grid, dim3(kThreads), lds, st, job[0], job[1], \
                      M, r, ctr)

@@ -51,6 +51,9 @@ hipError_t launch_dequant(const uint8_t* packed, const uint8_t* qscale, const fl
 
 // Small backward jobs, run by spare workgroups of another launch or alone:
 //   Bt [r, N] = B[N, r]^T and At [K, r] = A[r, K]^T (bf16);
+//   Bf: B^T as launch_thin_v takes it, in the order of its MFMA operands: value
+//   B[n][j] at (((n / 32) nj + j / 16) 4 + n % 32 / 8) 128 + 8 (j % 16) + n % 8
+//   with nj = ceil(r / 16), zero for j >= r and N <= n < N rounded up to 32;
 //   su = (s u)^T and sv = (s v)^T, each [2][16 ceil(r/16)][Mp] bf16 (high
 //   parts, then remainders; with three_parts [3][...]: the remainder in two;
 //   zero for j >= r or m >= M), u and v fp32 [M, r];
@@ -59,6 +62,7 @@ hipError_t launch_dequant(const uint8_t* packed, const uint8_t* qscale, const fl
 struct BwdAux {
   const uint16_t* B;
   uint16_t* Bt;
+  uint16_t* Bf;
   int64_t N;
   const uint16_t* A;
   uint16_t* At;
@@ -83,8 +87,12 @@ constexpr int kAuxRanks = 4;
 // A thread reads its ranks of B, u or v's slices in 16-byte loads when r allows,
 // the threads of a wave read neighbouring elements of A's rows, and the
 // transposed writes of neighbouring threads are neighbours.
+__host__ __device__ inline int64_t bwd_frags(const BwdAux& a) {  // 16-byte pieces of Bf
+  return a.Bf ? (a.N + 31) / 32 * 64 * ((a.r + 15) / 16) : 0;
+}
 __host__ __device__ inline int64_t bwd_aux_count(const BwdAux& a) {
-  return ((a.Bt ? a.N : 0) + (a.At ? a.K : 0) + (a.su ? a.Mpu : 0) + (a.sv ? a.Mpv : 0)) *
+  return bwd_frags(a) +
+         ((a.Bt ? a.N : 0) + (a.At ? a.K : 0) + (a.su ? a.Mpu : 0) + (a.sv ? a.Mpv : 0)) *
          ((a.r + 15) / 16 * (16 / kAuxRanks));
 }
 // x as bf16 at dst[idx] and its remainder as bf16 at dst[half + idx] (three:
@@ -97,12 +105,23 @@ __device__ inline void put_split(uint16_t* dst, int64_t half, int64_t idx, float
   dst[half + idx] = (uint16_t)l;
   if (three) dst[2 * half + idx] = (uint16_t)(pack_bf16x2(rest - bf16_lo(l), 0.f) & 0xffffu);
 }
-// row job i of the concatenated jobs (Bt, At, su, sv in that order; a block of
+// job i of the concatenated jobs (Bf; then by rows Bt, At, su, sv in that order; a block of
 // ranks of all of them before the next block)
 __device__ inline void bwd_aux_at(const BwdAux& a, int64_t i) {
   const int r = a.r;
   const int64_t rp = 16 * ((r + 15) / 16);
-  const int64_t rows = bwd_aux_count(a) / (rp / kAuxRanks);
+  const int64_t frags = bwd_frags(a);
+  if (i < frags) {  // rows n .. n + 7 of rank j
+    const int64_t n = i / (4 * rp) * 32 + (i >> 4) % 4 * 8, j = (i >> 6) % (rp / 16) * 16 + i % 16;
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (j < r && n + q < a.N) w[q >> 1] |= (uint32_t)a.B[(n + q) * r + j] << (16 * (q & 1));
+    *reinterpret_cast<u32x4*>(a.Bf + 8 * i) = u32x4{w[0], w[1], w[2], w[3]};
+    return;
+  }
+  i -= frags;
+  const int64_t rows = (bwd_aux_count(a) - frags) / (rp / kAuxRanks);
   const int jb = (int)(i / rows) * kAuxRanks;  // this block's ranks: jb .. je - 1
   i %= rows;
   const int je = min(jb + kAuxRanks, r);
@@ -202,7 +221,8 @@ __device__ inline void bwd_aux_at(const BwdAux& a, int64_t i) {
                                          a.three_parts);
   }
 }
-hipError_t launch_bwd_aux(const BwdAux& a, hipStream_t st);
+// clr: words the first workgroup zeroes.
+hipError_t launch_bwd_aux(const BwdAux& a, hipStream_t st, Clear clr = Clear{nullptr, 0});
 
 // out[k][n] = Qhat(W)[n][k] as bf16 with row length ldt (ldt % 8 == 0,
 // ldt >= rows); zero for rows <= n < ldt.  cols % 64 == 0.  The jobs of
@@ -266,6 +286,10 @@ hipError_t launch_lora_masked_add(uint16_t* dX, const float* v, const uint16_t* 
                                   const uint8_t* mask, int64_t M, int64_t K, int r, float s,
                                   hipStream_t st);
 int thin_nt_slices(int64_t M, int64_t P);
+// v [M, r] = G [M, N] B [N, r] in fp32 (Bf as BwdAux makes it), and sv = (s v)^T in three parts as
+// BwdAux makes it with three_parts; N % 8 == 0, Mp % 4 == 0.
+hipError_t launch_thin_v(const uint16_t* G, const uint16_t* Bf, int64_t M, int64_t N, int r,
+                         float* v, uint16_t* sv, int64_t Mp, float s, hipStream_t st);
 bool thin_nt_rows_ok(int64_t M, int64_t P, int r);
 
 // p[0..n) = 0 (a kernel, so it may sit in a captured graph).
