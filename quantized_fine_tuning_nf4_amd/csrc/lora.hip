@@ -122,7 +122,7 @@ __global__ __launch_bounds__(kThreads) void k_thin_nt(const uint16_t* __restrict
 }
 
 // v[M, r] = G[M, N] B[N, r] whole, and with it (s v)^T in three bf16 parts as
-// the transposed product takes it (parts of 16 NJ rows of Mp, zero past r and M).
+// the transposed product takes it (up to row Mp, zero past r and M).
 // Workgroup: 16 RT rows; its eight waves take U steps of 32 columns in turn, with
 // the operands as in k_thin_nt, and their sums meet in LDS, added in wave order.
 // So v is never in slices: with k_thin_nt's column slices and a launch that adds and
@@ -202,7 +202,8 @@ __global__ __launch_bounds__(64 * kVWaves) void k_thin_v(const uint16_t* __restr
     if (m < Mp)
 #pragma unroll
       for (int k = 0; k < 3; ++k)
-        *reinterpret_cast<u32x2*>(sv + ((int64_t)k * 16 * NJ + j) * Mp + m) = part[k];
+        *reinterpret_cast<u32x2*>(sv + (((m >> 5) * 3 + k) * 16 * NJ + j) * 32 + (m & 31)) =
+            part[k];
   }
 }
 
@@ -523,8 +524,7 @@ struct TnJob {
   const uint16_t* Z;   // [M, P] bf16 ...
   const int8_t* codes; // ... or an 8-bit checkpoint of it: codes [M, P]
   const uint8_t* exps; // and exponents [M, ceil(P / 64)]
-  const uint16_t* vt;  // [SP][16 NJ][Mp] (s V)^T in parts
-  int64_t Mp;
+  const uint16_t* vt;  // (s V)^T in parts, 32 rows [SP][16 NJ][32] after another
   int64_t P;
   int64_t slice;       // rows per slice, a multiple of 32
   int S;               // slices
@@ -619,7 +619,6 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
   }
   const uint16_t* Z = second ? j1.Z : j0.Z;
   const uint16_t* vt = second ? j1.vt : j0.vt;
-  const int64_t Mp = second ? j1.Mp : j0.Mp;
   const int64_t P = second ? j1.P : j0.P;
   const int64_t slice = second ? j1.slice : j0.slice;
   const int S = second ? j1.S : j0.S;
@@ -646,7 +645,7 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
   const rsrc_t rz = make_rs(z8 ? reinterpret_cast<const void*>(j1.codes + mb * P)
                                : reinterpret_cast<const void*>(Z + mb * P),
                             (uint32_t)((me - mb) * P * (z8 ? 1 : 2)));
-  const rsrc_t rv = make_rs(vt + mb, (uint32_t)((SP * 16 * NJ * Mp - mb) * 2));
+  const rsrc_t rv = make_rs(vt + SP * 16 * NJ * mb, (uint32_t)(slice * SP * 16 * NJ * 2));
   // keep bits from the slice's first row (P % 64 == 0: rows start on a byte);
   // bytes past the slice read as zero (columns past P are not stored)
   const rsrc_t rk = make_rs(hm ? zmask + mb * P / 8 : reinterpret_cast<const uint8_t*>(vt),
@@ -671,7 +670,7 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
 #pragma unroll
   for (int k = 0; k < VL; ++k) {
     const int q = min(VL * wave + k, SP * NJ - 1), row = 16 * q + (lane >> 2);
-    voff[k] = (uint32_t)(row * Mp * 2 + 16 * ((lane & 3) ^ (lane >> 4)));
+    voff[k] = (uint32_t)(row * 64 + 16 * ((lane & 3) ^ (lane >> 4)));
     vdst[k] = ZB + 1024 * q;
   }
   // the steps, on codes or on bf16
@@ -701,7 +700,7 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
       }
 #pragma unroll
       for (int k = 0; k < VL; ++k)
-        dma16(rv, voff[k] + (uint32_t)(64 * st), 0, base + vdst[k]);
+        dma16(rv, voff[k] + (uint32_t)(VB * st), 0, base + vdst[k]);
       if constexpr (MASK) {
         if (hm && wave < 2) {  // lane l: row 16w + l%16, bytes 4(l/16) .. +3 of the tile's 16
           const int row = 16 * wave + (lane & 15);
@@ -1014,8 +1013,9 @@ __global__ void k_sum_parts(TnSum a, TnSum b, int r) {
 
 // Slices of the M rows for the transposed products: enough workgroups to
 // fill the chip (about 512 per product), a multiple of 32 rows each, and
-// small enough that a slice of Z spans less than 2^31 bytes (the kernel
-// addresses one slice through a 32-bit buffer offset).
+// small enough that a slice of Z or of the (s V)^T parts (384 bytes a row at most)
+// spans less than 2^31 bytes (the kernel addresses one slice through a 32-bit
+// buffer offset).
 // Rows per slice: about 512 workgroups per job, but at most 16 slices per
 // column tile: the tile's last workgroup adds the slices, and with 64 of them
 // (a 1024-column dB at M = 4096) that sum took longer than the products
@@ -1028,7 +1028,7 @@ int64_t thin_tn_slice_rows(int64_t M, int64_t P, bool act8) {
   const int64_t S = std::min<int64_t>((512 + pt - 1) / pt, act8 ? 8 : 16);
   int64_t slice = (M + S - 1) / S;
   slice = (slice + 31) / 32 * 32;
-  const int64_t cap = ((((int64_t)1 << 31) - 1) / (2 * P)) / 32 * 32;
+  const int64_t cap = ((((int64_t)1 << 31) - 1) / std::max<int64_t>(2 * P, 384)) / 32 * 32;
   if (slice > cap) slice = cap;
   if (slice < 32) slice = 32;
   return slice;
@@ -1058,7 +1058,6 @@ hipError_t launch_thin_tn2(const ThinTn& a, const ThinTn& b, int64_t M, int r,
     j.codes = x.codes;
     j.exps = x.exps;
     j.vt = x.vt;
-    j.Mp = thin_tn_rows_padded(M, x.P, z8);
     j.P = x.P;
     j.slice = thin_tn_slice_rows(M, x.P, z8);
     j.S = thin_tn_slices(M, x.P, z8);

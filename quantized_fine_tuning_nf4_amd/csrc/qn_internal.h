@@ -54,9 +54,10 @@ hipError_t launch_dequant(const uint8_t* packed, const uint8_t* qscale, const fl
 //   Bf: B^T as launch_thin_v takes it, in the order of its MFMA operands: value
 //   B[n][j] at (((n / 32) nj + j / 16) 4 + n % 32 / 8) 128 + 8 (j % 16) + n % 8
 //   with nj = ceil(r / 16), zero for j >= r and N <= n < N rounded up to 32;
-//   su = (s u)^T and sv = (s v)^T, each [2][16 ceil(r/16)][Mp] bf16 (high
-//   parts, then remainders; with three_parts [3][...]: the remainder in two;
-//   zero for j >= r or m >= M), u and v fp32 [M, r];
+//   su = (s u)^T and sv = (s v)^T, each [Mp / 32][2][16 ceil(r/16)][32] bf16 (per
+//   32 columns the high parts, then the remainders; with three_parts [3]: the
+//   remainder in two; zero for j >= r or m >= M), u and v fp32 [M, r]: what a step
+//   of the transposed products takes lies in a row;
 //   when Sv > 1, v is first written as the slice sum of vpart [Sv][M][r].
 // A null destination skips its job.  One thread per output element.
 struct BwdAux {
@@ -166,9 +167,8 @@ __device__ inline void bwd_aux_at(const BwdAux& a, int64_t i) {
   const int64_t nu = a.su ? a.Mpu : 0;
   const bool is_u = i < nu;
   const int64_t m = is_u ? i : i - nu;
-  const int64_t Mp = is_u ? a.Mpu : a.Mpv;
   uint16_t* dst = is_u ? a.su : a.sv;
-  const int64_t half = rp * Mp;
+  const int64_t step = 32 * rp * (a.three_parts ? 3 : 2);  // values per 32 columns
   const bool in = m < a.M;
   const bool vec = (r & 3) == 0;
   for (int j0 = jb; j0 < jb + kAuxRanks; j0 += 4) {
@@ -217,8 +217,8 @@ __device__ inline void bwd_aux_at(const BwdAux& a, int64_t i) {
       }
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) put_split(dst, half, (int64_t)(j0 + q) * Mp + m, a.s * x[q],
-                                         a.three_parts);
+    for (int q = 0; q < 4; ++q) put_split(dst + (m >> 5) * step, 32 * rp, (j0 + q) * 32 + (m & 31),
+                                         a.s * x[q], a.three_parts);
   }
 }
 // clr: words the first workgroup zeroes.
