@@ -68,8 +68,9 @@
  *     workspace is first used (allocate it zeroed, or clear it once); every
  *     call leaves them at zero when it completes, so a workspace may then
  *     serve any number of calls, of any shape, on one stream.  The backward
- *     also clears them in its first kernel.  nf4_quantize_dq leaves the same
- *     bytes of its workspace untouched, so one buffer may serve all calls.
+ *     also clears them in its first kernel.  nf4_quantize_dq and the calls
+ *     around the linear (below) leave the same bytes of their workspaces
+ *     untouched or at zero, so one buffer may serve all calls.
  *   - Sizes the linear calls accept: M <= 2^23 rows, rows and cols <= 2^20
  *     (QN_EINVAL beyond).
  */
@@ -324,8 +325,7 @@ qn_status lora_linear_bf16(const uint16_t* x, int64_t M, const uint16_t* W, int6
                            uint16_t* y, void* stream);
 
 /* ---- Around the linear in a fine-tuning step (and in serving the tuned
- * model).  None of these calls uses arrival counters: their workspaces need
- * no clearing. ---- */
+ * model).  Their own workspaces need no clearing. ---- */
 
 /* Activation checkpoints in 8 bits.  An activation x [M, cols] bf16 is kept
  * for the backward as

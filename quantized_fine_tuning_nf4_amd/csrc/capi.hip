@@ -769,6 +769,7 @@ size_t block_norm_bwd_workspace(const qn_block_norm* n, int need_weights, int ne
   if (!n || n->M < 0 || n->D < 1 || n->D > QN_NORM_MAX_COLS) return 0;
   if (!need_weights && !(need_gate && n->gate_kind == QN_GATE_CHANNEL)) return 0;
   Carver c(nullptr);
+  c.take<unsigned>(kArrivalWords);  // left alone, as above
   c.take<float>((size_t)block_norm_slices(n->M, n->D) * 3 * n->D);
   c.take<float>((size_t)block_norm_stats(n->M, n->D));
   return c.used;
@@ -804,6 +805,7 @@ qn_status block_norm_bwd(const qn_block_norm* n, const uint16_t* dy, const void*
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return QN_EALIGN;
     if (workspace_bytes < block_norm_bwd_workspace(n, dw_pre || dw_post, chan)) return QN_EWORKSPACE;
     Carver c(workspace);
+    c.take<unsigned>(kArrivalWords);
     part = c.take<float>((size_t)block_norm_slices(n->M, n->D) * 3 * n->D);
     stats = c.take<float>((size_t)block_norm_stats(n->M, n->D));
   }
@@ -813,7 +815,8 @@ qn_status block_norm_bwd(const qn_block_norm* n, const uint16_t* dy, const void*
 
 size_t token_logprobs_workspace(int64_t T, int64_t V, qn_dtype dtype, int top_k) {
   if (T < 1 || T > kMaxRowsM || V < 1 || V > kMaxVocab || top_k < 0) return 0;
-  return logprob_workspace(T, V, dtype == QN_F32, top_k);
+  const size_t used = logprob_workspace(T, V, dtype == QN_F32, top_k);
+  return used ? QN_ARRIVAL_BYTES + used : 0;  // (the counters left alone, as above)
 }
 
 qn_status token_logprobs_fwd(const void* logits, qn_dtype dtype, int64_t T, int64_t V, int64_t ld,
@@ -836,7 +839,9 @@ qn_status token_logprobs_fwd(const void* logits, qn_dtype dtype, int64_t T, int6
     if (workspace_bytes < need) return QN_EWORKSPACE;
   }
   return from_hip(launch_logprobs_fwd(logits, dtype == QN_F32, T, V, ld, targets, scale, top_k,
-                                      logp, entropy, stats, top_logp, top_ids, workspace,
+                                      logp, entropy, stats, top_logp, top_ids,
+                                      need ? static_cast<char*>(workspace) + QN_ARRIVAL_BYTES
+                                           : nullptr,
                                       static_cast<hipStream_t>(stream)));
 }
 
