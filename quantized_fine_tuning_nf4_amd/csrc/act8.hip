@@ -7,6 +7,12 @@
 // one run of chunks; otherwise a row's last block and its last chunk are
 // partial, and rows start on any byte (vector accesses need no alignment on
 // this target).
+//
+// Both are bound by HBM: 177 MB each for 4096 x 14336, 30.3 us packing and 31.0
+// unpacking (5.8 and 5.7 TB/s, a large copy's rate).  A wave for every block, a
+// column a lane, took 129 us each: 2-byte requests, and six exchanges for a
+// maximum.  At 77 x 1000 a kernel takes 5 us, nearly all of it the start of the
+// launch and two trips to memory.
 #include "qn_device.h"
 #include "qn_internal.h"
 
