@@ -27,6 +27,8 @@ ACT8_BLOCK = 64
 MAX_TOP = 32  # alternatives of a row
 GATE_NONE, GATE_CHANNEL, GATE_ROW, GATE_ELEMENT = range(4)
 _DTYPES = {torch.bfloat16: QN_BF16, torch.float32: QN_F32}
+# Allocations below are written torch.empty(M, cols, ..) or empty_like: 1.2 us of a
+# small call's host time each, where torch.empty((M, cols), ..) takes 1.7.
 
 
 # ------------------------------------------------- activation checkpoints in 8 bits
@@ -59,8 +61,8 @@ def _act8(x8: Act8, M: int, cols: int, name: str = "x8") -> Act8:
 
 
 def _empty_act8(M: int, cols: int, device) -> Act8:
-    return Act8(torch.empty((M, cols), dtype=torch.int8, device=device),
-                torch.empty((M, _blocks(cols)), dtype=torch.uint8, device=device))
+    return Act8(torch.empty(M, cols, dtype=torch.int8, device=device),
+                torch.empty(M, _blocks(cols), dtype=torch.uint8, device=device))
 
 
 def act8_pack(x: torch.Tensor, out: Act8 | None = None) -> Act8:
@@ -84,7 +86,7 @@ def act8_unpack(x8: Act8, out: torch.Tensor | None = None) -> torch.Tensor:
     M, cols = x8.codes.shape
     _act8(x8, M, cols)
     if out is None:
-        out = torch.empty((M, cols), dtype=torch.bfloat16, device=x8.codes.device)
+        out = torch.empty(M, cols, dtype=torch.bfloat16, device=x8.codes.device)
     elif _dev(out, torch.bfloat16, "out").shape != (M, cols):
         raise ValueError(f"out must be [{M}, {cols}]")
     s = x8.c_struct()
@@ -116,9 +118,9 @@ def qlora_linear_bwd_act8(st: NF4State, x8: Act8, dY: torch.Tensor, A: torch.Ten
     if dropout_mask is not None and dropout_mask.numel() * 8 < M * st.cols:
         raise ValueError(f"dropout_mask must hold {M * st.cols} bits")
     dev = dY.device
-    dX = torch.empty((M, st.cols), dtype=torch.bfloat16, device=dev) if need_dx else None
-    dA = torch.empty((r, st.cols), dtype=torch.float32, device=dev)
-    dB = torch.empty((st.rows, r), dtype=torch.float32, device=dev)
+    dX = torch.empty(M, st.cols, dtype=torch.bfloat16, device=dev) if need_dx else None
+    dA = torch.empty(r, st.cols, dtype=torch.float32, device=dev)
+    dB = torch.empty(st.rows, r, dtype=torch.float32, device=dev)
     o = _opts(rslora, dropout_mask, dropout_p)
     need = L.qlora_linear_bwd_act8_workspace(M, st.rows, st.cols, r, int(need_dx))
     if workspace is None or workspace.numel() < need:
@@ -186,7 +188,7 @@ def block_norm_fwd(h: torch.Tensor, w_pre: torch.Tensor, o: torch.Tensor | None 
     n = _norm_args(h, w_pre, o, w_post, gate, scale, eps)
     dev = h.device
     h_new = None if o is None else torch.empty_like(h)
-    y = torch.empty(h.shape, dtype=torch.bfloat16, device=dev)
+    y = torch.empty_like(h, dtype=torch.bfloat16)
     x8 = _empty_act8(n.M, n.D, dev) if pack else None
     _check(load_library().block_norm_fwd(
         ctypes.byref(n), h.data_ptr(), _ptr(o), _ptr(h_new), y.data_ptr(),
@@ -317,13 +319,13 @@ def token_logprobs_fwd(logits: torch.Tensor, targets: torch.Tensor | None = None
         raise ValueError(f"top_k must be 0 .. {min(MAX_TOP, V)}")
     dev = logits.device
     f32 = torch.float32
-    logp = None if targets is None else torch.empty(T, dtype=f32, device=dev)
     entropy = torch.empty(T, dtype=f32, device=dev)
-    stats = torch.empty((T, 2), dtype=f32, device=dev)
+    logp = None if targets is None else torch.empty_like(entropy)
+    stats = torch.empty(T, 2, dtype=f32, device=dev)
     top_logp = top_ids = None
     if top_k:
-        top_logp = torch.empty((T, top_k), dtype=f32, device=dev)
-        top_ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        top_logp = torch.empty(T, top_k, dtype=f32, device=dev)
+        top_ids = torch.empty(T, top_k, dtype=torch.int32, device=dev)
     dt = _DTYPES[logits.dtype]
     need = L.token_logprobs_workspace(T, V, dt, top_k)
     if need > 0 and (workspace is None or workspace.numel() < need):
@@ -356,7 +358,7 @@ def token_logprobs_bwd(logits: torch.Tensor, targets: torch.Tensor | None, stats
         if t is not None and _dev(t, torch.float32, name).shape != (T,):
             raise ValueError(f"{name} must be [{T}]")
     if out is None:
-        out = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+        out = torch.empty(T, V, dtype=logits.dtype, device=logits.device)
     elif out.dtype != logits.dtype or out.shape != logits.shape:
         raise ValueError("out must have the logits' type and shape")
     _, _, ldd = _logits(out, None, "out")
