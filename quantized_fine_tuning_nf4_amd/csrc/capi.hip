@@ -170,7 +170,7 @@ struct BwdWs {
 };
 
 BwdWs carve_bwd(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool need_u,
-                bool act8 = false) {
+                bool act8 = false, bool need_dx = true) {
   BwdWs b;
   b.arrivals = c.take<unsigned>(kArrivalWords);
   if (need_u) {
@@ -196,7 +196,7 @@ BwdWs carve_bwd(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool ne
   // beat the dequantizing product, whose tiles walk the rows of W at 57 us per
   // 1024 (M = 300, 4096x4096: 285 us with it, 57 from the copy; M = 1, 1024x4096:
   // 64 and 30; even at 64 rows, 24 us)
-  const bool dense = M > 0 && (act8 || dense_path(M, cols));
+  const bool dense = M > 0 && (act8 ? need_dx : dense_path(M, cols));
   b.wt = dense ? c.take<uint16_t>((size_t)cols * b.ldt) : nullptr;
   b.At = dense ? c.take<uint16_t>((size_t)cols * r) : nullptr;
   return b;
@@ -347,12 +347,12 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
     return from_hip(e);
   }
   Carver probe(nullptr);
-  carve_bwd(probe, M, N, K, r, u_saved == nullptr, x8 != nullptr);
+  carve_bwd(probe, M, N, K, r, u_saved == nullptr, x8 != nullptr, dX != nullptr);
   if (!workspace) return QN_EINVAL;
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return QN_EALIGN;
   if (workspace_bytes < probe.used) return QN_EWORKSPACE;
   Carver c(workspace);
-  BwdWs b = carve_bwd(c, M, N, K, r, u_saved == nullptr, x8 != nullptr);
+  BwdWs b = carve_bwd(c, M, N, K, r, u_saved == nullptr, x8 != nullptr, dX != nullptr);
   const float scale = lo.s;
   hipError_t e = hipSuccess;
   const float* u = u_saved;
@@ -732,10 +732,9 @@ qn_status act8_unpack(const qn_act8* x8, int64_t M, int64_t cols, uint16_t* out,
 }
 
 size_t qlora_linear_bwd_act8_workspace(int64_t M, int64_t rows, int64_t cols, int r, int need_dx) {
-  (void)need_dx;
   if (M < 0 || rows < 1 || cols < 1 || r < 1 || r > 64) return 0;
   Carver c(nullptr);
-  carve_bwd(c, M, rows, cols, r, false, true);
+  carve_bwd(c, M, rows, cols, r, false, true, need_dx != 0);
   return c.used;
 }
 

@@ -158,3 +158,14 @@ def test_binding_refuses_what_the_kernels_do_not_take(qn):
         qn.block_norm_fwd(z(4, 64), z(64))
     with pytest.raises(ValueError):
         qn.token_logprobs_fwd(z(4, 64))
+
+
+def test_linear_bwd_act8_workspace_holds_a_weight_copy_for_dx_only(qn):
+    L = qn.load_library()
+    for M, rows, cols, r in [(1, 8, 64, 1), (300, 1000, 576, 17), (4096, 1024, 4096, 64)]:
+        without, with_dx = (L.qlora_linear_bwd_act8_workspace(M, rows, cols, r, d) for d in (0, 1))
+        assert with_dx - without >= 2 * rows * cols
+        st = qn._NF4DQ(FAKE, FAKE, FAKE, FAKE, rows, cols)
+        assert L.qlora_linear_bwd_act8(
+            ctypes.byref(st), ctypes.byref(qn._Act8(FAKE, FAKE)), FAKE, M, FAKE, FAKE, r, 8.0, None,
+            FAKE, FAKE, FAKE, FAKE, FAKE, without, None) == qn.QN_EWORKSPACE
