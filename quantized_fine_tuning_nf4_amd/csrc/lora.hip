@@ -772,7 +772,8 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t w = c[pt][i >> 1] >> (16 * (i & 1));
-            za[pt][i] = pack_bf16x2((float)(int8_t)w * rs[2 * i], (float)(int8_t)(w >> 8) * rs[2 * i + 1]);
+            za[pt][i] = pack_bf16x2((float)(int8_t)w * rs[2 * i],
+                                    (float)(int8_t)(w >> 8) * rs[2 * i + 1]);
           }
       } else {
         u32x2 x00, x01, x10, x11;
@@ -804,7 +805,8 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
 #pragma unroll
             for (int i = 0; i < 4; ++i) {  // a bit as all ones or zeros, in each half
               const uint32_t lo = (uint32_t)__builtin_amdgcn_sbfe(kw[i >> 1][2 * (i & 1)], sh, 1);
-              const uint32_t hi = (uint32_t)__builtin_amdgcn_sbfe(kw[i >> 1][2 * (i & 1) + 1], sh, 1);
+              const uint32_t hi =
+                  (uint32_t)__builtin_amdgcn_sbfe(kw[i >> 1][2 * (i & 1) + 1], sh, 1);
               za[pt][i] &= __builtin_amdgcn_perm(hi, lo, 0x05040100u);
             }
           }

@@ -898,7 +898,8 @@ hipError_t launch_block_norm_fwd(const BlockNorm& n, const void* h, const uint16
 }
 
 int block_norm_slices(int64_t M, int64_t D) {
-  if (D > kSumCols) return (int)std::min<int64_t>(M, kColumnSlices * 16384 / (2048 * ((D + 2047) / 2048)));
+  if (D > kSumCols)
+    return (int)std::min<int64_t>(M, kColumnSlices * 16384 / (2048 * ((D + 2047) / 2048)));
   const int64_t T = D <= 512 ? 256 : (D + 511) / 512 * 64, G = D <= 512 ? 4 : 1;
   return (int)std::min<int64_t>((M + G - 1) / G, resident(kSumWaves, (int)T));
 }

@@ -299,9 +299,10 @@ hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t st);
 // One transposed adapter product out = Z^T (s V), reduced over the M rows:
 // Z bf16 [M, P] (null: no product) or, for the second product, an 8-bit
 // checkpoint of it (codes and exps; P % 64 == 0), vt = (s V)^T split as BwdAux
-// makes it (in three parts for both products when there are codes) with Mp = thin_tn_rows_padded(M, P, act8); transposed == false: out fp32
-// [P, r]; true: out fp32 [r, P].  Split over thin_tn_slices(M, P, act8) row
-// slices with partials part[S][P][r], summed in slice order.  P % 8 == 0.
+// makes it (in three parts for both products when there are codes) up to row
+// thin_tn_rows_padded(M, P, act8); transposed == false: out fp32 [P, r]; true: out
+// fp32 [r, P].  Split over thin_tn_slices(M, P, act8) row slices with partials
+// part[S][P][r], summed in slice order.  P % 8 == 0.
 struct ThinTn {
   const uint16_t* Z;
   const uint16_t* vt;
