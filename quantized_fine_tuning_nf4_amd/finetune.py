@@ -218,8 +218,8 @@ def block_norm_bwd(dy: torch.Tensor, h_new: torch.Tensor, w_pre: torch.Tensor,
     do = None if o is None else torch.empty_like(o)
     dgate = None
     if gate is not None and need_gate:
-        dgate = torch.empty(gate.shape, device=dev, dtype=torch.bfloat16
-                            if n.gate_kind == GATE_ELEMENT else torch.float32)
+        dgate = torch.empty_like(gate, dtype=torch.bfloat16
+                                 if n.gate_kind == GATE_ELEMENT else torch.float32)
     dw_pre = dw_post = None
     if need_weights:
         dw_pre = torch.empty(D, dtype=torch.float32, device=dev)
