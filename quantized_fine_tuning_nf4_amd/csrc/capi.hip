@@ -373,9 +373,12 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
     u = b.fu.u;
   }
   // v = G B.  With x in 8 bits: whole, and (s v)^T with it, from B in the order of
-  // the product's operands, made first (and with that (s u)^T).  Else in slices
+  // the product's operands, made first (and with that (s u)^T, and A^T for the dense
+  // dX product; in spare workgroups of the transposed dequantization when there is
+  // one).  Else in slices
   // (added below); the product takes B as stored when it can, else B^T made first.
   const bool b_rows = thin_nt_rows_ok(M, N, r);
+  const bool dense_dx = dX && b.wt;
   if (e == hipSuccess && x8) {
     BwdAux t{};
     t.B = B;
@@ -388,9 +391,17 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
     t.r = r;
     t.s = scale;
     t.three_parts = true;
-    e = launch_bwd_aux(t, st, clr);
+    t.A = A;
+    t.At = dense_dx ? b.At : nullptr;
+    t.K = K;
+    if (dense_dx)
+      e = launch_dequant_t(w->packed, w->qscale, w->scale2, w->offset, N, K, b.wt, b.ldt, t, st,
+                           w->codebook, w->absmax);
+    else
+      e = launch_bwd_aux(t, st);
     if (e == hipSuccess)
-      e = launch_thin_v(dY, b.Bt, M, N, r, b.v, b.sv, thin_tn_rows_padded(M, K, true), scale, st);
+      e = launch_thin_v(dY, b.Bt, M, N, r, b.v, b.sv, thin_tn_rows_padded(M, K, true), scale, st,
+                        clr);
   }
   if (e == hipSuccess && !x8 && !b_rows) {
     if (clr.n) {  // (no earlier launch: a kernel, not a memset, for graph capture)
@@ -407,26 +418,25 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
   if (e == hipSuccess && !x8)
     e = launch_thin_nt(dY, b_rows ? B : b.Bt, M, N, r, b.v, b.vpart, b.Sv, st, false, b_rows,
                        clr);
-  // the small jobs: v's slice sum, (s u)^T and (s v)^T split (unless made above) for the
+  // the small jobs: v's slice sum, (s u)^T and (s v)^T split for the
   // transposed products, A^T for the dense dX product; in spare workgroups of
   // the transposed dequantization when there is one
-  const bool dense_dx = dX && b.wt;
-  BwdAux aux{};
-  aux.A = A;
-  aux.At = dense_dx ? b.At : nullptr;
-  aux.K = K;
-  aux.u = u;
-  aux.su = x8 ? nullptr : b.su;
-  aux.Mpu = thin_tn_rows_padded(M, N, false);
-  aux.vpart = b.vpart;
-  aux.Sv = b.Sv;
-  aux.v = b.v;
-  aux.sv = x8 ? nullptr : b.sv;
-  aux.Mpv = thin_tn_rows_padded(M, K, false);
-  aux.M = M;
-  aux.r = r;
-  aux.s = scale;
-  if (e == hipSuccess) {
+  if (e == hipSuccess && !x8) {
+    BwdAux aux{};
+    aux.A = A;
+    aux.At = dense_dx ? b.At : nullptr;
+    aux.K = K;
+    aux.u = u;
+    aux.su = b.su;
+    aux.Mpu = thin_tn_rows_padded(M, N, false);
+    aux.vpart = b.vpart;
+    aux.Sv = b.Sv;
+    aux.v = b.v;
+    aux.sv = b.sv;
+    aux.Mpv = thin_tn_rows_padded(M, K, false);
+    aux.M = M;
+    aux.r = r;
+    aux.s = scale;
     if (dense_dx)
       e = launch_dequant_t(w->packed, w->qscale, w->scale2, w->offset, N, K, b.wt, b.ldt, aux,
                            st, w->codebook, w->absmax);

@@ -140,11 +140,12 @@ __global__ __launch_bounds__(64 * kVWaves) void k_thin_v(const uint16_t* __restr
                                                          int64_t M, int64_t N, int r,
                                                          float* __restrict__ v,
                                                          uint16_t* __restrict__ sv, int64_t Mp,
-                                                         float s) {
+                                                         float s, Clear clr) {
   constexpr int U = 4, PITCH = 16 + 4;
   __shared__ __attribute__((aligned(16))) float sums[kVWaves][16 * NJ][PITCH];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int g = lane >> 4, l16 = lane & 15;
+  clear_words(clr);
   const int64_t m0 = 16 * (int64_t)blockIdx.x;
   const int64_t steps = (N + 31) / 32;
   const uint16_t* gp = G + min(m0 + l16, M - 1) * N + 8 * g;
@@ -208,10 +209,10 @@ __global__ __launch_bounds__(64 * kVWaves) void k_thin_v(const uint16_t* __restr
 }
 
 hipError_t launch_thin_v(const uint16_t* G, const uint16_t* Bf, int64_t M, int64_t N, int r,
-                         float* v, uint16_t* sv, int64_t Mp, float s, hipStream_t st) {
+                         float* v, uint16_t* sv, int64_t Mp, float s, hipStream_t st, Clear clr) {
 #define QN_V(NJ)                                                                              \
   hipLaunchKernelGGL(k_thin_v<NJ>, dim3((unsigned)((Mp + 15) / 16)), dim3(64 * kVWaves), 0, st, G, \
-                     Bf, M, N, r, v, sv, Mp, s)
+                     Bf, M, N, r, v, sv, Mp, s, clr)
   switch ((r + 15) / 16) {
     case 1: QN_V(1); break;
     case 2: QN_V(2); break;
@@ -466,17 +467,15 @@ hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t st) {
   return hipGetLastError();
 }
 
-__global__ void k_bwd_aux(BwdAux a, Clear clr) {
-  clear_words(clr);
+__global__ void k_bwd_aux(BwdAux a) {
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i < bwd_aux_count(a)) bwd_aux_at(a, i);
 }
 
-hipError_t launch_bwd_aux(const BwdAux& a, hipStream_t st, Clear clr) {
+hipError_t launch_bwd_aux(const BwdAux& a, hipStream_t st) {
   const int64_t count = bwd_aux_count(a);
   if (count == 0) return hipSuccess;
-  hipLaunchKernelGGL(k_bwd_aux, dim3((unsigned)((count + 255) / 256)), dim3(256), 0, st, a,
-                     clr);
+  hipLaunchKernelGGL(k_bwd_aux, dim3((unsigned)((count + 255) / 256)), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

@@ -223,8 +223,7 @@ __device__ inline void bwd_aux_at(const BwdAux& a, int64_t i) {
                                          a.s * x[q], a.three_parts);
   }
 }
-// clr: words the first workgroup zeroes.
-hipError_t launch_bwd_aux(const BwdAux& a, hipStream_t st, Clear clr = Clear{nullptr, 0});
+hipError_t launch_bwd_aux(const BwdAux& a, hipStream_t st);
 
 // out[k][n] = Qhat(W)[n][k] as bf16 with row length ldt (ldt % 8 == 0,
 // ldt >= rows); zero for rows <= n < ldt.  cols % 64 == 0.  The jobs of
@@ -289,9 +288,11 @@ hipError_t launch_lora_masked_add(uint16_t* dX, const float* v, const uint16_t* 
                                   hipStream_t st);
 int thin_nt_slices(int64_t M, int64_t P);
 // v [M, r] = G [M, N] B [N, r] in fp32 (Bf as BwdAux makes it), and sv = (s v)^T in three parts as
-// BwdAux makes it with three_parts; N % 8 == 0, Mp % 4 == 0.
+// BwdAux makes it with three_parts; N % 8 == 0, Mp % 4 == 0.  clr: words the first
+// workgroup zeroes.
 hipError_t launch_thin_v(const uint16_t* G, const uint16_t* Bf, int64_t M, int64_t N, int r,
-                         float* v, uint16_t* sv, int64_t Mp, float s, hipStream_t st);
+                         float* v, uint16_t* sv, int64_t Mp, float s, hipStream_t st,
+                         Clear clr);
 bool thin_nt_rows_ok(int64_t M, int64_t P, int r);
 
 // p[0..n) = 0 (a kernel, so it may sit in a captured graph).
