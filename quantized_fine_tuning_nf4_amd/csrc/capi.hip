@@ -194,7 +194,7 @@ BwdWs carve_bwd(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool ne
   b.ldt = round_up(rows, 64);
   // with x in 8 bits at every size: a weight read once and a product of few tiles
   // beat the dequantizing product, whose tiles walk the rows of W at 57 us per
-  // 1024 (M = 300, 4096x4096: 285 us with it, 57 from the copy; M = 1, 1024x4096:
+  // 1024 (M = 300, 4096x4096: 285 us with it, 55 from the copy; M = 1, 1024x4096:
   // 64 and 30; even at 64 rows, 24 us)
   const bool dense = M > 0 && (act8 ? need_dx : dense_path(M, cols));
   b.wt = dense ? c.take<uint16_t>((size_t)cols * b.ldt) : nullptr;

@@ -243,3 +243,14 @@ def test_layer_keeps_the_checkpoint(qn):
     assert 0 < _rel(ga[1][2].float(), ga[0][2].cpu().double()) < 2e-2
     with pytest.raises(ValueError):
         ref(x, x8=x8)
+
+
+# calls long enough that the slices of dA and dB are added by a launch of their
+# own at every rank; rows, columns and slices that end inside tiles
+LONG = [(4100, 2056, 2112, 16, 0.0), (8195, 1032, 1088, 3, 0.1), (8224, 520, 1664, 11, 0.0),
+        (2500, 4104, 2752, 33, 0.05)]
+
+
+@pytest.mark.parametrize("M,rows,cols,r,p", LONG)
+def test_backward_of_long_calls(qn, M, rows, cols, r, p):
+    test_backward_from_the_checkpoint(qn, M, rows, cols, r, p)
