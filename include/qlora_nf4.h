@@ -214,8 +214,9 @@ qn_status qlora_linear_fwd_noalloc(const qn_nf4dq* w, const uint16_t* x, int64_t
  *     caller draws it.  Kept elements pass
  *     unchanged and the branch's scale becomes s / (1 - dropout_p); the
  *     backward takes the same mask (the dA product masks x where it loads
- *     it, the branch's share of dX is masked).  Forwards with dropout take the GEMM routes,
- *     never the decode kernels.
+ *     it, the branch's share of dX is masked in fp32 before dX is rounded, and
+ *     is zero where an element was dropped).  Forwards with dropout take the
+ *     GEMM routes, never the decode kernels.
  *   dropout_p: in [0, 1) with a mask; 0 without one. */
 typedef struct {
   int rslora;

@@ -330,7 +330,6 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
   Lora lo;
   s = lora_options(opts, alpha, r, &lo);
   if (s != QN_OK) return s;
-  const bool drop = lo.mask != nullptr;
   if (!A || !B || !dA || !dB) return QN_EINVAL;
   if (M > 0 && !dY) return QN_EINVAL;
   if (M > 0 && (x8 ? (!x8->codes || !x8->exps || !u_saved) : !x)) return QN_EINVAL;
@@ -444,13 +443,10 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
       e = launch_bwd_aux(aux, st);
   }
   if (e == hipSuccess && dX) {
-    // under dropout the branch's share is added masked after the base product
-    const float sx = drop ? 0.f : scale;
     if (dense_dx)
-      e = launch_gemm_nt(dY, N, N, b.wt, b.ldt, M, K, b.v, b.At, r, sx, dX, st);
+      e = launch_gemm_nt(dY, N, N, b.wt, b.ldt, M, K, b.v, b.At, r, scale, dX, st, lo.mask);
     else
-      e = launch_qgemm_dx(to_state(w), dY, M, b.v, A, r, sx, dX, st);
-    if (e == hipSuccess && drop) e = launch_lora_masked_add(dX, b.v, A, lo.mask, M, K, r, scale, st);
+      e = launch_qgemm_dx(to_state(w), dY, M, b.v, A, r, scale, dX, st, lo.mask);
   }
   // dB = s G^T u and dA = s v^T X in one launch (and their slice sums in one)
   if (e == hipSuccess)

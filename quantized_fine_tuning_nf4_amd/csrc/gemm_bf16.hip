@@ -1,11 +1,12 @@
 // bf16 GEMM with the LoRA term fused in the epilogue, for large batches:
 //
-//   C[M, Nc] (bf16) = A[M, R] Bm[Nc, R]^T + s V[M, r] L[Nc, r]^T
+//   C[M, Nc] (bf16) = A[M, R] Bm[Nc, R]^T + s V[M, r] L[Nc, r]^T (.) mask
 //
 // used for the forward (A = x, Bm = Qhat(W) [N, K], V = u, L = B) and for
 // dX (A = dY, Bm = Qhat(W)^T [K, N], V = v, L = A^T) of the page "QLoRA: NF4
 // storage, gradients and local integration" (paragraph after the teaching
-// listing), once the weight has been dequantized to bf16 in a workspace.
+// listing), once the weight has been dequantized to bf16 in a workspace.  The
+// mask (dX under dropout on the adapter branch's input) is optional.
 //
 // Workgroup tile 256 x 256, four waves (2 x 2), each wave 128 x 128 as 8 x 8
 // tiles of v_mfma_f32_16x16x32_bf16 (256 accumulators, pinned in AGPRs); for
@@ -106,12 +107,14 @@ __device__ __forceinline__ void wait_all_loads() { asm volatile("s_waitcnt vmcnt
 // than the steps cover (R < ldb), so A's chunks past R are moved back; with
 // R == ldb the A loads need no address arithmetic per step (the 64-bit
 // clamp in the loop cost 12% of the main loop's cycles at 8192x4096x4096).
-template <bool LORA16, int WTM, int WTN, bool ATAIL>
+// MASK: the LoRA term counts only where the keep mask (bit-packed over the
+// row-major elements of C; Nc % 64 == 0) has a bit set.
+template <bool LORA16, int WTM, int WTN, bool ATAIL, bool MASK>
 __global__ __launch_bounds__(T, 1) void k_gemm_nt(
     const uint16_t* __restrict__ A, int64_t lda, int64_t R, const uint16_t* __restrict__ Bm,
     int64_t ldb, int steps, int64_t M, int64_t Nc, const float* __restrict__ V,
     const uint16_t* __restrict__ L, int r, float s, uint16_t* __restrict__ C, int tiles_m,
-    int tiles_c) {
+    int tiles_c, const uint8_t* __restrict__ mask) {
   using G = Geo<WTM, WTN>;
   constexpr int BM = G::BM, BN = G::BN, WRM = G::WRM, WRN = G::WRN, OPA = G::OPA, STB = G::STB;
   constexpr int OUTP = G::OUTP, OUTW = G::OUTW, NST = G::NST, LPS = G::LPS;
@@ -238,6 +241,144 @@ __global__ __launch_bounds__(T, 1) void k_gemm_nt(
     for (int q = 0; q < LPS; ++q) load_one(q, min(k, steps - 1), k);
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LPS * (NST - 1)) : "memory");
   barrier_lds();
+  // Wherever control flow joins after MFMAs (the loop's exit, the end of a
+  // conditional step) the compiler may copy an accumulator to another AGPR
+  // for the join; 32 wait states first let the last products complete (it
+  // cannot know that the asm MFMAs write late: at the 256 x 224 tile's loop
+  // exit it copied the last accumulator 4 cycles after its MFMA issued).
+  // The exit test sits at the end of the body, so the back edge skips them.
+  auto drain = [&]() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); };
+  // The compiler cannot see that the asm MFMAs write the accumulators some
+  // cycles after they issue, so nothing it places may read one before the
+  // last products are complete: 32 wait states, then an empty asm that
+  // "rewrites" every accumulator, which no read of it can move above (a
+  // register copy is not ordered by a memory clobber alone; without the ties
+  // the compiler hoisted the output conversion's AGPR reads above the wait
+  // states and read partial sums).
+  auto settle = [&]() {
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < WTM; ++i)
+#pragma unroll
+      for (int j = 0; j < WTN; ++j) asm volatile("" : "+a"(acc[i][j]));
+  };
+
+  // ---- LoRA term: acc += (s V) L^T, 16 ranks per MFMA reduction of 32: lane
+  // group g4 < 2 carries the bf16 high part of s V, g4 >= 2 its remainder,
+  // both against the same eight ranks 8(g4 & 1) .. +7 of L.
+  auto lora_term = [&]() {
+    const bool vec = (r % 8) == 0;
+    const bool lo_part = g4 >= 2;
+    if constexpr (LORA16) {
+      // from LDS: L row (tile column) wn WRN + 16 j + l16, ranks 8 (g4 & 1) ..;
+      // V row (tile row) wm WRM + 16 i + l16, the same ranks
+      const int jb = 8 * (g4 & 1);
+      bf16x8 lh[WTN];
+#pragma unroll
+      for (int j = 0; j < WTN; ++j)
+        lh[j] = as_bf16x8(*reinterpret_cast<const u32x4*>(
+            smem + LDS_L + (wn * WRN + 16 * j + l16) * (LORA_R * 2) + 2 * jb));
+#pragma unroll
+      for (int i = 0; i < WTM; ++i) {
+        const uint8_t* vp = smem + LDS_V + (wm * WRM + 16 * i + l16) * (LORA_R * 4) + 4 * jb;
+        const f32x4 v0 = *reinterpret_cast<const f32x4*>(vp);
+        const f32x4 v1 = *reinterpret_cast<const f32x4*>(vp + 16);
+        const float vr[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float x0 = s * vr[2 * q], x1 = s * vr[2 * q + 1];
+          const uint32_t h = pack_bf16x2(x0, x1);
+          w[q] = lo_part ? pack_bf16x2(x0 - bf16_lo(h), x1 - bf16_hi(h)) : h;
+        }
+        const bf16x8 av = as_bf16x8(u32x4{w[0], w[1], w[2], w[3]});
+#pragma unroll
+        for (int j = 0; j < WTN; ++j) mfma16_acc(lh[j], av, acc[i][j]);
+      }
+    }
+    for (int j0 = 0; j0 < (LORA16 ? 0 : r); j0 += 16) {
+      const int jl = j0 + 8 * (g4 & 1);
+      bf16x8 lh[WTN];
+#pragma unroll
+      for (int j = 0; j < WTN; ++j) {
+        const int64_t col = min(c0 + wn * WRN + 16 * j + l16, Nc - 1);
+        const uint16_t* lp = L + col * r;
+        if (vec) {
+          lh[j] = jl < r ? as_bf16x8(*reinterpret_cast<const u32x4*>(lp + jl)) : bf16x8{};
+        } else {
+          uint32_t e[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) e[q] = jl + q < r ? lp[min(jl + q, r - 1)] : 0u;
+          lh[j] = as_bf16x8(u32x4{e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16),
+                                  e[6] | (e[7] << 16)});
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < WTM; ++i) {
+        const int64_t m = min(m0 + wm * WRM + 16 * i + l16, M - 1);
+        const float* vp = V + m * r;
+        float vr[8];
+        if (vec && jl < r) {
+          const f32x4 v0 = *reinterpret_cast<const f32x4*>(vp + jl);
+          const f32x4 v1 = *reinterpret_cast<const f32x4*>(vp + jl + 4);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            vr[q] = v0[q];
+            vr[4 + q] = v1[q];
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) vr[q] = jl + q < r ? vp[min(jl + q, r - 1)] : 0.f;
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float x0 = s * vr[2 * q], x1 = s * vr[2 * q + 1];
+          const uint32_t h = pack_bf16x2(x0, x1);
+          w[q] = lo_part ? pack_bf16x2(x0 - bf16_lo(h), x1 - bf16_hi(h)) : h;
+        }
+        const bf16x8 av = as_bf16x8(u32x4{w[0], w[1], w[2], w[3]});
+#pragma unroll
+        for (int j = 0; j < WTN; ++j) mfma16_acc(lh[j], av, acc[i][j]);
+      }
+      drain();  // (a loop: its exit is a join)
+    }
+  };
+  // MASK: the term comes first, into the zero accumulators, and what is dropped
+  // becomes zero again; so it needs no accumulators of its own, and the sum of both
+  // products is rounded once (8192x4096x4096, r = 16, the whole backward from an 8-bit
+  // checkpoint: 16 us over the one without dropout, at r = 64 18; added to a
+  // finished bf16 dX by a kernel of its own 36 and 297).  Keep bits of row 16i + l%16 in this lane's four
+  // columns of tile j: nibble j of keep[i] (rows past M read zeros; bits past Nc are of
+  // columns that are not stored).
+  if constexpr (MASK) {
+    const rsrc_t rsK = make_rs(mask + m0 * (Nc / 8), (uint32_t)(mrows * (Nc / 8)));
+    uint32_t keep[WTM] = {};
+#pragma unroll
+    for (int i = 0; i < WTM; ++i) {
+      const int64_t row = wm * WRM + 16 * i + l16;
+#pragma unroll
+      for (int j = 0; j < WTN; ++j) {
+        const uint32_t b = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+            rsK, (uint32_t)(row * (Nc / 8) + (c0 + wn * WRN) / 8 + 2 * j), 0, 0);
+        keep[i] |= ((b >> (4 * g4)) & 15u) << (4 * j);
+      }
+    }
+    lora_term();
+    settle();
+#pragma unroll
+    for (int i = 0; i < WTM; ++i) {
+#pragma unroll
+      for (int j = 0; j < WTN; ++j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[i][j][e] = as_f32(as_u32(acc[i][j][e]) &
+                                (uint32_t)__builtin_amdgcn_sbfe((int)keep[i], 4 * j + e, 1));
+        asm volatile("" : "+a"(acc[i][j]));  // back in its AGPRs
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
 #pragma unroll
   for (int t = 0; t < WTM; ++t) fa[t] = frag(0, abase, t, 0);
 #pragma unroll
@@ -286,13 +427,6 @@ __global__ __launch_bounds__(T, 1) void k_gemm_nt(
     half(p_t, S0{}, st);
     half(p_t, S1{}, st);
   };
-  // Wherever control flow joins after MFMAs (the loop's exit, the end of a
-  // conditional step) the compiler may copy an accumulator to another AGPR
-  // for the join; 32 wait states first let the last products complete (it
-  // cannot know that the asm MFMAs write late: at the 256 x 224 tile's loop
-  // exit it copied the last accumulator 4 cycles after its MFMA issued).
-  // The exit test sits at the end of the body, so the back edge skips them.
-  auto drain = [&]() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); };
   int st = 0;
   if (steps >= NST) {
     for (;;) {
@@ -324,105 +458,13 @@ __global__ __launch_bounds__(T, 1) void k_gemm_nt(
       drain();
     }
   }
-  // The compiler cannot see that the asm MFMAs write the accumulators some
-  // cycles after they issue, so nothing it places may read one before the
-  // last products are complete: 32 wait states, then an empty asm that
-  // "rewrites" every accumulator, which no read of it can move above (a
-  // register copy is not ordered by a memory clobber alone; without the ties
-  // the compiler hoisted the output conversion's AGPR reads above the wait
-  // states and read partial sums).
-  auto settle = [&]() {
-    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < WTM; ++i)
-#pragma unroll
-      for (int j = 0; j < WTN; ++j) asm volatile("" : "+a"(acc[i][j]));
-  };
   // every wave's loads have landed and all reads are done before the stages
   // are reused for the output staging below
   settle();
   wait_all_loads();
   barrier_lds();
 
-  // ---- LoRA term: acc += (s V) L^T, 16 ranks per MFMA reduction of 32: lane
-  // group g4 < 2 carries the bf16 high part of s V, g4 >= 2 its remainder,
-  // both against the same eight ranks 8(g4 & 1) .. +7 of L.
-  const bool vec = (r % 8) == 0;
-  const bool lo_part = g4 >= 2;
-  if constexpr (LORA16) {
-    // from LDS: L row (tile column) wn WRN + 16 j + l16, ranks 8 (g4 & 1) ..;
-    // V row (tile row) wm WRM + 16 i + l16, the same ranks
-    const int jb = 8 * (g4 & 1);
-    bf16x8 lh[WTN];
-#pragma unroll
-    for (int j = 0; j < WTN; ++j)
-      lh[j] = as_bf16x8(*reinterpret_cast<const u32x4*>(
-          smem + LDS_L + (wn * WRN + 16 * j + l16) * (LORA_R * 2) + 2 * jb));
-#pragma unroll
-    for (int i = 0; i < WTM; ++i) {
-      const uint8_t* vp = smem + LDS_V + (wm * WRM + 16 * i + l16) * (LORA_R * 4) + 4 * jb;
-      const f32x4 v0 = *reinterpret_cast<const f32x4*>(vp);
-      const f32x4 v1 = *reinterpret_cast<const f32x4*>(vp + 16);
-      const float vr[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
-      uint32_t w[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float x0 = s * vr[2 * q], x1 = s * vr[2 * q + 1];
-        const uint32_t h = pack_bf16x2(x0, x1);
-        w[q] = lo_part ? pack_bf16x2(x0 - bf16_lo(h), x1 - bf16_hi(h)) : h;
-      }
-      const bf16x8 av = as_bf16x8(u32x4{w[0], w[1], w[2], w[3]});
-#pragma unroll
-      for (int j = 0; j < WTN; ++j) mfma16_acc(lh[j], av, acc[i][j]);
-    }
-  }
-  for (int j0 = 0; j0 < (LORA16 ? 0 : r); j0 += 16) {
-    const int jl = j0 + 8 * (g4 & 1);
-    bf16x8 lh[WTN];
-#pragma unroll
-    for (int j = 0; j < WTN; ++j) {
-      const int64_t col = min(c0 + wn * WRN + 16 * j + l16, Nc - 1);
-      const uint16_t* lp = L + col * r;
-      if (vec) {
-        lh[j] = jl < r ? as_bf16x8(*reinterpret_cast<const u32x4*>(lp + jl)) : bf16x8{};
-      } else {
-        uint32_t e[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) e[q] = jl + q < r ? lp[min(jl + q, r - 1)] : 0u;
-        lh[j] = as_bf16x8(u32x4{e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16),
-                                e[6] | (e[7] << 16)});
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < WTM; ++i) {
-      const int64_t m = min(m0 + wm * WRM + 16 * i + l16, M - 1);
-      const float* vp = V + m * r;
-      float vr[8];
-      if (vec && jl < r) {
-        const f32x4 v0 = *reinterpret_cast<const f32x4*>(vp + jl);
-        const f32x4 v1 = *reinterpret_cast<const f32x4*>(vp + jl + 4);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          vr[q] = v0[q];
-          vr[4 + q] = v1[q];
-        }
-      } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) vr[q] = jl + q < r ? vp[min(jl + q, r - 1)] : 0.f;
-      }
-      uint32_t w[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float x0 = s * vr[2 * q], x1 = s * vr[2 * q + 1];
-        const uint32_t h = pack_bf16x2(x0, x1);
-        w[q] = lo_part ? pack_bf16x2(x0 - bf16_lo(h), x1 - bf16_hi(h)) : h;
-      }
-      const bf16x8 av = as_bf16x8(u32x4{w[0], w[1], w[2], w[3]});
-#pragma unroll
-      for (int j = 0; j < WTN; ++j) mfma16_acc(lh[j], av, acc[i][j]);
-    }
-    drain();  // (a loop: its exit is a join)
-  }
+  if constexpr (!MASK) lora_term();
 
   // ---- store.  Tile (i, j) is held transposed: lane l has row 16i + l%16
   // and columns 16j + 4(l/16) .. +3 in its four registers; they go to the
@@ -466,16 +508,16 @@ __global__ __launch_bounds__(T, 1) void k_gemm_nt(
 size_t gemm_nt_lds_bytes() { return Geo<8, 8>::LDS_BYTES; }
 
 namespace {
-template <int WTM, int WTN>
+template <int WTM, int WTN, bool MASK>
 hipError_t launch_wt(const uint16_t* A, int64_t lda, int64_t R, const uint16_t* Bm, int64_t ldb,
                      int64_t M, int64_t Nc, const float* V, const uint16_t* L, int r, float s,
-                     uint16_t* C, hipStream_t st) {
+                     uint16_t* C, const uint8_t* mask, hipStream_t st) {
   using G = Geo<WTM, WTN>;
   static hipError_t attr = [] {
-    const void* k16[2] = {reinterpret_cast<const void*>(k_gemm_nt<true, WTM, WTN, false>),
-                          reinterpret_cast<const void*>(k_gemm_nt<true, WTM, WTN, true>)};
-    const void* kr[2] = {reinterpret_cast<const void*>(k_gemm_nt<false, WTM, WTN, false>),
-                         reinterpret_cast<const void*>(k_gemm_nt<false, WTM, WTN, true>)};
+    const void* k16[2] = {reinterpret_cast<const void*>(k_gemm_nt<true, WTM, WTN, false, MASK>),
+                          reinterpret_cast<const void*>(k_gemm_nt<true, WTM, WTN, true, MASK>)};
+    const void* kr[2] = {reinterpret_cast<const void*>(k_gemm_nt<false, WTM, WTN, false, MASK>),
+                         reinterpret_cast<const void*>(k_gemm_nt<false, WTM, WTN, true, MASK>)};
     for (int t = 0; t < 2; ++t) {
       hipError_t e = hipFuncSetAttribute(k16[t], hipFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)G::LDS_BYTES);
@@ -491,9 +533,9 @@ hipError_t launch_wt(const uint16_t* A, int64_t lda, int64_t R, const uint16_t* 
   const int steps = (int)(ldb / BK);
   const dim3 grid((unsigned)(tm * tc)), block(T);
 #define QN_GEMM(L16, TAIL)                                                                     \
-  hipLaunchKernelGGL((k_gemm_nt<L16, WTM, WTN, TAIL>), grid, block,                           \
+  hipLaunchKernelGGL((k_gemm_nt<L16, WTM, WTN, TAIL, MASK>), grid, block,                     \
                      L16 ? G::LDS_BYTES : G::LDS_MAIN, st, A, lda, R, Bm, ldb, steps, M, Nc, V, \
-                     L, r, s, C, (int)tm, (int)tc)
+                     L, r, s, C, (int)tm, (int)tc, mask)
   const bool tail = R != ldb;
   if (r == LORA_R) {
     if (tail) QN_GEMM(true, true); else QN_GEMM(true, false);
@@ -502,6 +544,13 @@ hipError_t launch_wt(const uint16_t* A, int64_t lda, int64_t R, const uint16_t* 
   }
 #undef QN_GEMM
   return hipGetLastError();
+}
+template <int WTM, int WTN>
+hipError_t launch_tiles(const uint16_t* A, int64_t lda, int64_t R, const uint16_t* Bm, int64_t ldb,
+                        int64_t M, int64_t Nc, const float* V, const uint16_t* L, int r, float s,
+                        uint16_t* C, const uint8_t* mask, hipStream_t st) {
+  return mask ? launch_wt<WTM, WTN, true>(A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, mask, st)
+              : launch_wt<WTM, WTN, false>(A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, mask, st);
 }
 
 int compute_units() {
@@ -522,13 +571,13 @@ bool gemm_nt_small_tiles(int64_t M, int64_t Nc) {
 
 hipError_t launch_gemm_nt(const uint16_t* A, int64_t lda, int64_t R, const uint16_t* Bm,
                           int64_t ldb, int64_t M, int64_t Nc, const float* V, const uint16_t* L,
-                          int r, float s, uint16_t* C, hipStream_t st) {
+                          int r, float s, uint16_t* C, hipStream_t st, const uint8_t* mask) {
   if (M <= 0) return hipSuccess;
-  if (ldb % BK != 0 || R < 8 || R > ldb) return hipErrorInvalidValue;
+  if (ldb % BK != 0 || R < 8 || R > ldb || (mask && Nc % 64 != 0)) return hipErrorInvalidValue;
   // 256 x 256 tiles once there are about as many as compute units; fewer
   // would leave most of the chip idle, so 128 x 128 tiles then
   if (gemm_nt_small_tiles(M, Nc))
-    return launch_wt<4, 4>(A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, st);
+    return launch_tiles<4, 4>(A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, mask, st);
   // 256 x 224 tiles where they take fewer tile-widths of rounds: with 14336
   // output columns at M = 4096, 896 tiles of 256 fill 3.5 rounds of the
   // chip and the last round runs half empty, while 1024 tiles of 224 fill
@@ -537,8 +586,8 @@ hipError_t launch_gemm_nt(const uint16_t* A, int64_t lda, int64_t R, const uint1
   const int64_t r256 = (tm * ((Nc + 255) / 256) + cu - 1) / cu;
   const int64_t r224 = (tm * ((Nc + 223) / 224) + cu - 1) / cu;
   if (r224 * 224 < r256 * 256)
-    return launch_wt<8, 7>(A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, st);
-  return launch_wt<8, 8>(A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, st);
+    return launch_tiles<8, 7>(A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, mask, st);
+  return launch_tiles<8, 8>(A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, mask, st);
 }
 
 }  // namespace qn

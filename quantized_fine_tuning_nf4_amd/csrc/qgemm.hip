@@ -1,7 +1,7 @@
 // Fused NF4-dequant bf16 MFMA GEMMs of the QLoRA linear (gfx950).
 //
 //   forward  Y  = X Qhat(W)^T + s (X A^T) B^T      (u = X A^T precomputed)
-//   backward dX = G Qhat(W)   + s (G B) A          (v = G B precomputed)
+//   backward dX = G Qhat(W)   + s (G B) A [(.) mask]  (v = G B precomputed)
 // (page "QLoRA: NF4 storage, gradients and local integration", paragraph
 // after the teaching listing; s = alpha / r as in the course notebook's
 // LoRALinear.)  Qhat(W) is the dequantized weight w' = L[c] * s', rounded to
@@ -278,13 +278,17 @@ __global__ __launch_bounds__(64 * WM * WN) void k_qgemm_fwd(
 // the weight tile is rows n0..n0+63, columns k0..k0+BN-1 of W, stored in LDS
 // transposed (sB[k][n]).  A thread unit is 8 rows x 8 columns: eight u32 of
 // codes (one per row, one scale per row), written as eight 16-byte LDS rows
-// of eight n-values.  Rows past N are zero.
-template <int WM, int WN, int TM, int TN, int CB, bool ABS>
+// of eight n-values.  Rows past N are zero.  MASK: the LoRA term counts only
+// where the keep mask (dropout on the adapter branch's input: bit-packed over
+// the row-major elements of dX) has a bit set; it is masked in fp32, so that dX
+// is rounded once, as without a mask.
+template <int WM, int WN, int TM, int TN, int CB, bool ABS, bool MASK>
 __global__ __launch_bounds__(64 * WM * WN) void k_qgemm_dx(
     const uint8_t* __restrict__ packed, const uint8_t* __restrict__ qscale,
     const float* __restrict__ scale2, const float* __restrict__ offset,
     const float* __restrict__ absmax, const uint16_t* __restrict__ G, const float* __restrict__ Vv, const uint16_t* __restrict__ Al,
-    int64_t M, int64_t N, int64_t K, int r, float s, uint16_t* __restrict__ dX, int tiles_k) {
+    int64_t M, int64_t N, int64_t K, int r, float s, uint16_t* __restrict__ dX, int tiles_k,
+    const uint8_t* __restrict__ mask) {
   using Cfg = Tile<WM, WN, TM, TN>;
   constexpr int BM = Cfg::BM, BN = Cfg::BN, T = Cfg::T;
   constexpr int UPT = (BN + T - 1) / T;  // 8x8 units per thread (BN units in all)
@@ -372,6 +376,21 @@ __global__ __launch_bounds__(64 * WM * WN) void k_qgemm_dx(
   {
     const int lane = tid & 63, wave = tid >> 6;
     const int wm = wave / WN, wn = wave % WN;
+    // bit e of keep[i][j]: this lane's e-th element of tile (i, j)
+    uint32_t keep[TM][TN] = {};
+    if constexpr (MASK) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const int64_t k = min(k0 + wn * TN * 32 + j * 32 + (lane & 31), K - 1);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int64_t m = min(m0 + wm * TM * 32 + i * 32 + acc_row(e, lane), M - 1);
+            keep[i][j] |= ((uint32_t)(mask[(m * K + k) >> 3] >> (k & 7)) & 1u) << e;
+          }
+        }
+    }
     for (int j0 = 0; j0 < r; j0 += 16) {
       const int jl = j0 + 8 * (lane >> 5);
       bf16x8 bh[TN];
@@ -395,8 +414,16 @@ __global__ __launch_bounds__(64 * WM * WN) void k_qgemm_dx(
         lora_rows(Vv, m, r, jl, s, ah, al);
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-          acc[i][j] = mfma32(ah, bh[j], acc[i][j]);
-          acc[i][j] = mfma32(al, bh[j], acc[i][j]);
+          if constexpr (MASK) {
+            const f32x16 t = mfma32(al, bh[j], mfma32(ah, bh[j], f32x16{}));
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              acc[i][j][e] += as_f32(as_u32(t[e]) &
+                                     (uint32_t)__builtin_amdgcn_sbfe((int)keep[i][j], e, 1));
+          } else {
+            acc[i][j] = mfma32(ah, bh[j], acc[i][j]);
+            acc[i][j] = mfma32(al, bh[j], acc[i][j]);
+          }
         }
       }
     }
@@ -424,17 +451,18 @@ hipError_t run_fwd_f(const WState& w, const uint16_t* X, int64_t M, const float*
   return hipGetLastError();
 }
 
-template <int WM, int WN, int TM, int TN, int CB, bool ABS>
+template <int WM, int WN, int TM, int TN, int CB, bool ABS, bool MASK>
 hipError_t run_dx_f(const WState& w, const uint16_t* G, int64_t M, const float* v,
-                    const uint16_t* A, int r, float s, uint16_t* dX, hipStream_t st) {
+                    const uint16_t* A, int r, float s, uint16_t* dX, const uint8_t* mask,
+                    hipStream_t st) {
   using Cfg = Tile<WM, WN, TM, TN>;
-  auto kern = k_qgemm_dx<WM, WN, TM, TN, CB, ABS>;
+  auto kern = k_qgemm_dx<WM, WN, TM, TN, CB, ABS, MASK>;
   static hipError_t attr = set_lds(kern, Cfg::LDS);
   if (attr != hipSuccess) return attr;
   const int64_t tm = (M + Cfg::BM - 1) / Cfg::BM, tk = (w.cols + Cfg::BN - 1) / Cfg::BN;
   hipLaunchKernelGGL(kern, dim3((unsigned)(tm * tk)), dim3(Cfg::T), Cfg::LDS, st, w.packed,
                      w.qscale, w.scale2, w.offset, w.absmax, G, v, A, M, w.rows, w.cols, r, s, dX,
-                     (int)tk);
+                     (int)tk, mask);
   return hipGetLastError();
 }
 
@@ -449,14 +477,15 @@ hipError_t run_fwd(const WState& w, const uint16_t* X, int64_t M, const float* u
                   : run_fwd_f<WM, WN, TM, TN, kCodeNF4, false>(w, X, M, u, B, r, s, Y, st);
 }
 
-template <int WM, int WN, int TM, int TN>
-hipError_t run_dx(const WState& w, const uint16_t* G, int64_t M, const float* v,
-                  const uint16_t* A, int r, float s, uint16_t* dX, hipStream_t st) {
+template <int WM, int WN, int TM, int TN, bool MASK>
+hipError_t run_dx(const WState& w, const uint16_t* G, int64_t M, const float* v, const uint16_t* A,
+                  int r, float s, uint16_t* dX, const uint8_t* mask, hipStream_t st) {
+  auto run = [&](auto f) { return f(w, G, M, v, A, r, s, dX, mask, st); };
   if (w.codebook == kCodeFP4)
-    return w.absmax ? run_dx_f<WM, WN, TM, TN, kCodeFP4, true>(w, G, M, v, A, r, s, dX, st)
-                    : run_dx_f<WM, WN, TM, TN, kCodeFP4, false>(w, G, M, v, A, r, s, dX, st);
-  return w.absmax ? run_dx_f<WM, WN, TM, TN, kCodeNF4, true>(w, G, M, v, A, r, s, dX, st)
-                  : run_dx_f<WM, WN, TM, TN, kCodeNF4, false>(w, G, M, v, A, r, s, dX, st);
+    return w.absmax ? run(run_dx_f<WM, WN, TM, TN, kCodeFP4, true, MASK>)
+                    : run(run_dx_f<WM, WN, TM, TN, kCodeFP4, false, MASK>);
+  return w.absmax ? run(run_dx_f<WM, WN, TM, TN, kCodeNF4, true, MASK>)
+                  : run(run_dx_f<WM, WN, TM, TN, kCodeNF4, false, MASK>);
 }
 
 // Tile choice: a 32-row tile for decode-sized batches, else 128x128 (larger
@@ -473,10 +502,14 @@ hipError_t launch_qgemm_fwd(const WState& w, const uint16_t* X, int64_t M, const
 }
 
 hipError_t launch_qgemm_dx(const WState& w, const uint16_t* G, int64_t M, const float* v,
-                           const uint16_t* A, int r, float s, uint16_t* dX, hipStream_t st) {
+                           const uint16_t* A, int r, float s, uint16_t* dX, hipStream_t st,
+                           const uint8_t* mask) {
   if (w.codebook != kCodeNF4 && w.codebook != kCodeFP4) return hipErrorInvalidValue;
-  if (pick(M) == 0) return run_dx<1, 4, 1, 1>(w, G, M, v, A, r, s, dX, st);
-  return run_dx<2, 2, 2, 2>(w, G, M, v, A, r, s, dX, st);
+  if (pick(M) == 0)
+    return mask ? run_dx<1, 4, 1, 1, true>(w, G, M, v, A, r, s, dX, mask, st)
+                : run_dx<1, 4, 1, 1, false>(w, G, M, v, A, r, s, dX, mask, st);
+  return mask ? run_dx<2, 2, 2, 2, true>(w, G, M, v, A, r, s, dX, mask, st)
+              : run_dx<2, 2, 2, 2, false>(w, G, M, v, A, r, s, dX, mask, st);
 }
 
 }  // namespace qn

@@ -235,10 +235,12 @@ hipError_t launch_dequant_t(const uint8_t* packed, const uint8_t* qscale, const 
 
 // C[M, Nc] bf16 = A[M, R] (row stride lda) * Bm[Nc, :R]^T (row stride ldb,
 // ldb % 64 == 0, zero in columns R..ldb) + s * V[M, r] * L[Nc, r]^T.
-// lda >= R, R % 8 == 0, Nc % 8 == 0; 16-byte aligned pointers.
+// lda >= R, R % 8 == 0, Nc % 8 == 0; 16-byte aligned pointers.  mask (nullable;
+// Nc % 64 == 0): keep bits of the second term (bit-packed over the elements of C).
 hipError_t launch_gemm_nt(const uint16_t* A, int64_t lda, int64_t R, const uint16_t* Bm,
                           int64_t ldb, int64_t M, int64_t Nc, const float* V, const uint16_t* L,
-                          int r, float s, uint16_t* C, hipStream_t st);
+                          int r, float s, uint16_t* C, hipStream_t st,
+                          const uint8_t* mask = nullptr);
 
 // Weight state as the kernels take it.
 struct WState;
@@ -280,12 +282,6 @@ struct AdamScalars {
 hipError_t launch_adamw8(float* p, const float* g, int64_t n, uint8_t* mq, float* ms, uint8_t* vq,
                          float* vs, uint16_t* pb, const AdamScalars& h, hipStream_t st);
 
-// dX[m][k] (bf16) += s (v A)[m][k] where mask bit (m, k) is set: the
-// adapter branch's input gradient under dropout.  v fp32 [M, r], A bf16
-// [r, K], K % 8 == 0, 1 <= r <= 64.
-hipError_t launch_lora_masked_add(uint16_t* dX, const float* v, const uint16_t* A,
-                                  const uint8_t* mask, int64_t M, int64_t K, int r, float s,
-                                  hipStream_t st);
 int thin_nt_slices(int64_t M, int64_t P);
 // v [M, r] = G [M, N] B [N, r] in fp32 (Bf as BwdAux makes it), and sv = (s v)^T in three parts as
 // BwdAux makes it with three_parts; N % 8 == 0, Mp % 4 == 0.  clr: words the first
@@ -366,9 +362,11 @@ hipError_t launch_merge(const WState& w, const uint16_t* A, const uint16_t* B, i
 hipError_t launch_qgemm_fwd(const WState& w, const uint16_t* X, int64_t M, const float* u,
                             const uint16_t* B, int r, float s, uint16_t* Y, hipStream_t st);
 
-// dX[M, K] bf16 = G[M, N] * W'[N, K] + s * v[M, r] * A[r, K].
+// dX[M, K] bf16 = G[M, N] * W'[N, K] + s * v[M, r] * A[r, K], the second term under
+// mask (nullable; bit-packed over the elements of dX).
 hipError_t launch_qgemm_dx(const WState& w, const uint16_t* G, int64_t M, const float* v,
-                           const uint16_t* A, int r, float s, uint16_t* dX, hipStream_t st);
+                           const uint16_t* A, int r, float s, uint16_t* dX, hipStream_t st,
+                           const uint8_t* mask = nullptr);
 
 // 8-bit activation checkpoints (format in the header): x [M, K] bf16 ->
 // codes [M, K], exps [M, ceil(K / 64)], and back.
