@@ -81,6 +81,9 @@ typedef __amdgpu_buffer_rsrc_t rsrc_t;
 __device__ __forceinline__ void mfma16_acc(bf16x8 a, bf16x8 b, f32x4& c) {
   asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
+// An operand that the vector unit has just written has to be two wait states old
+// when an MFMA reads it; the compiler does not know that asm reads it so.
+__device__ __forceinline__ void settle_operand(bf16x8& a) { asm volatile("s_nop 1" : "+v"(a)); }
 __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
 // Descriptor over [base, base + bytes) from wave-uniform values (kept in SGPRs).
@@ -291,7 +294,8 @@ __global__ __launch_bounds__(T, 1) void k_gemm_nt(
           const uint32_t h = pack_bf16x2(x0, x1);
           w[q] = lo_part ? pack_bf16x2(x0 - bf16_lo(h), x1 - bf16_hi(h)) : h;
         }
-        const bf16x8 av = as_bf16x8(u32x4{w[0], w[1], w[2], w[3]});
+        bf16x8 av = as_bf16x8(u32x4{w[0], w[1], w[2], w[3]});
+        settle_operand(av);
 #pragma unroll
         for (int j = 0; j < WTN; ++j) mfma16_acc(lh[j], av, acc[i][j]);
       }
@@ -337,7 +341,8 @@ __global__ __launch_bounds__(T, 1) void k_gemm_nt(
           const uint32_t h = pack_bf16x2(x0, x1);
           w[q] = lo_part ? pack_bf16x2(x0 - bf16_lo(h), x1 - bf16_hi(h)) : h;
         }
-        const bf16x8 av = as_bf16x8(u32x4{w[0], w[1], w[2], w[3]});
+        bf16x8 av = as_bf16x8(u32x4{w[0], w[1], w[2], w[3]});
+        settle_operand(av);
 #pragma unroll
         for (int j = 0; j < WTN; ++j) mfma16_acc(lh[j], av, acc[i][j]);
       }
