@@ -49,7 +49,8 @@
  *     the qn_nf4dq struct itself, which lives in host memory and holds
  *     device pointers).  The library allocates nothing; scratch memory comes
  *     from the caller as `workspace` (sizes from the *_workspace functions;
- *     256-byte aligned).  Device pointers must be 16-byte aligned.
+ *     256-byte aligned).  Device pointers must be 16-byte aligned unless a
+ *     call says otherwise.
  *   - `stream` is a hipStream_t (NULL: the null stream).  All calls are
  *     stream-ordered and asynchronous, except nf4_quantize_dq without a
  *     `nonfinite` flag pointer, which synchronizes `stream` so that it can
@@ -326,7 +327,10 @@ qn_status lora_linear_bf16(const uint16_t* x, int64_t M, const uint16_t* W, int6
                            uint16_t* y, void* stream);
 
 /* ---- Around the linear in a fine-tuning step (and in serving the tuned
- * model).  Their own workspaces need no clearing. ---- */
+ * model).  Their own workspaces need no clearing.  Buffers of rows of an odd
+ * width (cols or D no multiple of 8: x, codes, exps, and a block norm's
+ * [M, D] buffers) may start on any element, so that slices of rows serve;
+ * gates [M] on any element, targets on 8 bytes, logits on any element. ---- */
 
 /* Activation checkpoints in 8 bits.  An activation x [M, cols] bf16 is kept
  * for the backward as

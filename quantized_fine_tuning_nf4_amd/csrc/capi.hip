@@ -32,6 +32,13 @@ struct Carver {
 };
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Rows of `cols` elements end to end: where their starts do not keep 16-byte
+// boundaries (cols % 8 != 0) the kernels take them on any element of `size` bytes,
+// so that a slice of rows is as good a buffer as the whole.
+bool aligned_rows(const void* p, int64_t cols, unsigned size) {
+  return (reinterpret_cast<uintptr_t>(p) & (cols % 8 == 0 ? 15u : size - 1u)) == 0;
+}
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
 int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
 int64_t groups_of(int64_t nb) { return (nb + kGroup - 1) / kGroup; }
@@ -298,7 +305,12 @@ qn_status check_norm(const qn_block_norm* n, BlockNorm* out) {
   if (!n->w_pre) return QN_EINVAL;
   // no element gate has storage for an empty batch
   if ((n->gate_kind == QN_GATE_NONE) != (n->gate == nullptr) && n->M > 0) return QN_EINVAL;
-  if (!aligned16(n->w_pre) || !aligned16(n->w_post) || !aligned16(n->gate)) return QN_EALIGN;
+  if (!aligned16(n->w_pre) || !aligned16(n->w_post)) return QN_EALIGN;
+  // (a row's gate is read by itself)
+  if (n->gate_kind == QN_GATE_ROW ? reinterpret_cast<uintptr_t>(n->gate) & 1u
+      : n->gate_kind == QN_GATE_ELEMENT ? !aligned_rows(n->gate, n->D, 2)
+                                        : !aligned16(n->gate))
+    return QN_EALIGN;
   *out = BlockNorm{n->M, n->D, n->w_pre, n->w_post, n->gate, n->res_dtype == QN_F32,
                    n->w_dtype == QN_F32, n->gate_kind, n->scale, n->eps};
   return QN_OK;
@@ -724,7 +736,8 @@ qn_status act8_pack(const uint16_t* x, int64_t M, int64_t cols, int8_t* codes, u
   qn_status s = check_act8_shape(M, cols);
   if (s != QN_OK || M == 0) return s;
   if (!x || !codes || !exps) return QN_EINVAL;
-  if (!aligned16(x) || !aligned16(codes) || !aligned16(exps)) return QN_EALIGN;
+  if (!aligned_rows(x, cols, 2) || !aligned_rows(codes, cols, 1) || !aligned_rows(exps, cols, 1))
+    return QN_EALIGN;
   return from_hip(launch_act8_pack(x, M, cols, codes, exps, static_cast<hipStream_t>(stream)));
 }
 
@@ -732,7 +745,9 @@ qn_status act8_unpack(const qn_act8* x8, int64_t M, int64_t cols, uint16_t* out,
   qn_status s = check_act8_shape(M, cols);
   if (s != QN_OK || M == 0) return s;
   if (!x8 || !x8->codes || !x8->exps || !out) return QN_EINVAL;
-  if (!aligned16(x8->codes) || !aligned16(x8->exps) || !aligned16(out)) return QN_EALIGN;
+  if (!aligned_rows(x8->codes, cols, 1) || !aligned_rows(x8->exps, cols, 1) ||
+      !aligned_rows(out, cols, 2))
+    return QN_EALIGN;
   return from_hip(launch_act8_unpack(x8->codes, x8->exps, M, cols, out,
                                      static_cast<hipStream_t>(stream)));
 }
@@ -763,8 +778,10 @@ qn_status block_norm_fwd(const qn_block_norm* n, const void* h, const uint16_t* 
   if (n->M == 0) return QN_OK;
   if (!o && (n->w_post || n->gate || h_new)) return QN_EINVAL;
   if (!h || !y || (o && !h_new)) return QN_EINVAL;
-  if (!aligned16(h) || !aligned16(o) || !aligned16(h_new) || !aligned16(y) || !aligned16(codes) ||
-      !aligned16(exps))
+  const int64_t D = n->D;
+  const unsigned res = b.res32 ? 4 : 2;
+  if (!aligned_rows(h, D, res) || !aligned_rows(o, D, 2) || !aligned_rows(h_new, D, res) ||
+      !aligned_rows(y, D, 2) || !aligned_rows(codes, D, 1) || !aligned_rows(exps, D, 1))
     return QN_EALIGN;
   return from_hip(launch_block_norm_fwd(b, h, o, h_new, y, codes, exps,
                                         static_cast<hipStream_t>(stream)));
@@ -791,9 +808,12 @@ qn_status block_norm_bwd(const qn_block_norm* n, const uint16_t* dy, const void*
   if (n->M > 0 && !o && (n->w_post || n->gate)) return QN_EINVAL;
   if ((dw_post && !n->w_post) || (dgate && !n->gate)) return QN_EINVAL;
   if (n->M > 0 && (!dy || !h_new || !dh)) return QN_EINVAL;
-  if (!aligned16(dy) || !aligned16(dh_new) || !aligned16(h_new) || !aligned16(o) ||
-      !aligned16(dh) || !aligned16(dout) || !aligned16(dgate) || !aligned16(dw_post) ||
-      !aligned16(dw_pre))
+  const int64_t D = n->D;
+  const unsigned res = b.res32 ? 4 : 2;
+  if (!aligned_rows(dy, D, 2) || !aligned_rows(dh_new, D, res) || !aligned_rows(h_new, D, res) ||
+      !aligned_rows(o, D, 2) || !aligned_rows(dh, D, res) || !aligned_rows(dout, D, 2) ||
+      (n->gate_kind == QN_GATE_ELEMENT ? !aligned_rows(dgate, D, 2) : !aligned16(dgate)) ||
+      !aligned16(dw_post) || !aligned16(dw_pre))
     return QN_EALIGN;
   const bool chan = dgate && n->gate_kind == QN_GATE_CHANNEL;
   hipStream_t st = static_cast<hipStream_t>(stream);
@@ -834,7 +854,7 @@ qn_status token_logprobs_fwd(const void* logits, qn_dtype dtype, int64_t T, int6
   if ((targets == nullptr) != (logp == nullptr) && T > 0) return QN_EINVAL;
   if (T == 0) return QN_OK;
   if (!entropy || !stats || (top_k > 0 && (!top_logp || !top_ids))) return QN_EINVAL;
-  if (!aligned16(targets) || !aligned16(logp) || !aligned16(entropy) || !aligned16(stats) ||
+  if (!aligned8(targets) || !aligned16(logp) || !aligned16(entropy) || !aligned16(stats) ||
       !aligned16(top_logp) || !aligned16(top_ids))
     return QN_EALIGN;
   const size_t need = token_logprobs_workspace(T, V, dtype, top_k);
@@ -861,7 +881,7 @@ qn_status token_logprobs_bwd(const void* logits, qn_dtype dtype, int64_t T, int6
   if (!stats || !dlogits || (!dlogp && !dentropy) || (dlogp && !targets) || (dentropy && !entropy))
     return QN_EINVAL;
   if (dlogits == logits && ldd != ld) return QN_EINVAL;
-  if (!aligned16(targets) || !aligned16(stats) || !aligned16(entropy) || !aligned16(dlogp) ||
+  if (!aligned8(targets) || !aligned16(stats) || !aligned16(entropy) || !aligned16(dlogp) ||
       !aligned16(dentropy) || (reinterpret_cast<uintptr_t>(dlogits) & (dtype == QN_F32 ? 3u : 1u)))
     return QN_EALIGN;
   return from_hip(launch_logprobs_bwd(logits, dtype == QN_F32, T, V, ld, targets, scale, stats,

@@ -31,6 +31,15 @@ _DTYPES = {torch.bfloat16: QN_BF16, torch.float32: QN_F32}
 # small call's host time each, where torch.empty((M, cols), ..) takes 1.7.
 
 
+def _start(t: torch.Tensor | None, cols: int = 8):
+    """An input as the kernels take it: a view that starts between 16-byte boundaries
+    (a slice of a larger tensor) is copied, except rows of an odd width, which may start
+    anywhere.  The caller holds the result until its launch."""
+    if t is None or cols % 8 or t.data_ptr() % 16 == 0:
+        return t
+    return t.clone()
+
+
 # ------------------------------------------------- activation checkpoints in 8 bits
 @dataclass
 class Act8:
@@ -41,6 +50,12 @@ class Act8:
 
     def nbytes(self) -> int:
         return self.codes.numel() + self.exps.numel()
+
+    def start(self) -> Act8:
+        """Itself, or a copy where it starts as the kernels do not take it."""
+        cols = self.codes.shape[1]
+        codes, exps = _start(self.codes, cols), _start(self.exps, cols)
+        return self if codes is self.codes and exps is self.exps else Act8(codes, exps)
 
     def c_struct(self) -> _Act8:
         return _Act8(self.codes.data_ptr(), self.exps.data_ptr())
@@ -73,6 +88,7 @@ def act8_pack(x: torch.Tensor, out: Act8 | None = None) -> Act8:
         raise ValueError("x must be [..., cols] with cols >= 1")
     cols = x.shape[-1]
     M = x.numel() // cols
+    x = _start(x, cols)
     out = _empty_act8(M, cols, x.device) if out is None else _act8(out, M, cols, "out")
     _check(load_library().act8_pack(x.data_ptr(), M, cols, out.codes.data_ptr(),
                                     out.exps.data_ptr(), _stream(x.device)))
@@ -84,7 +100,7 @@ def act8_unpack(x8: Act8, out: torch.Tensor | None = None) -> torch.Tensor:
     if not isinstance(x8, Act8) or x8.codes.dim() != 2:
         raise ValueError("x8 must be an Act8 with codes [M, cols]")
     M, cols = x8.codes.shape
-    _act8(x8, M, cols)
+    x8 = _act8(x8, M, cols).start()
     if out is None:
         out = torch.empty(M, cols, dtype=torch.bfloat16, device=x8.codes.device)
     elif _dev(out, torch.bfloat16, "out").shape != (M, cols):
@@ -117,6 +133,7 @@ def qlora_linear_bwd_act8(st: NF4State, x8: Act8, dY: torch.Tensor, A: torch.Ten
         raise ValueError(f"u must be [{M}, {r}]")
     if dropout_mask is not None and dropout_mask.numel() * 8 < M * st.cols:
         raise ValueError(f"dropout_mask must hold {M * st.cols} bits")
+    x8, dY, A, B, u = x8.start(), _start(dY), _start(A), _start(B), _start(u)
     dev = dY.device
     dX = torch.empty(M, st.cols, dtype=torch.bfloat16, device=dev) if need_dx else None
     dA = torch.empty(r, st.cols, dtype=torch.float32, device=dev)
@@ -139,7 +156,8 @@ BlockNormGrads = namedtuple("BlockNormGrads", "dh do dgate dw_post dw_pre")
 
 
 def _norm_args(h, w_pre, o, w_post, gate, scale, eps):
-    """The C argument struct of a block norm on h [..., D]."""
+    """The C argument struct of a block norm on h [..., D], and h, o and what else it
+    points to as the kernels take them."""
     if not isinstance(h, torch.Tensor) or h.dtype not in _DTYPES:
         raise ValueError("h must be a bfloat16 or float32 tensor")
     _dev(h, h.dtype, "h")
@@ -173,8 +191,12 @@ def _norm_args(h, w_pre, o, w_post, gate, scale, eps):
             _dev(gate, torch.bfloat16, "gate")
         else:
             raise ValueError(f"gate must be [{D}], [..., 1] or h's shape")
-    return _BlockNorm(M, D, w_pre.data_ptr(), _ptr(w_post), _ptr(gate), _DTYPES[h.dtype],
-                      _DTYPES[wt], kind, scale, eps)
+    h, o, w_pre, w_post = _start(h, D), _start(o, D), _start(w_pre), _start(w_post)
+    if kind != GATE_ROW:
+        gate = _start(gate, D if kind == GATE_ELEMENT else 8)
+    n = _BlockNorm(M, D, w_pre.data_ptr(), _ptr(w_post), _ptr(gate), _DTYPES[h.dtype],
+                   _DTYPES[wt], kind, scale, eps)
+    return n, h, o, (w_pre, w_post, gate)
 
 
 def block_norm_fwd(h: torch.Tensor, w_pre: torch.Tensor, o: torch.Tensor | None = None,
@@ -185,13 +207,13 @@ def block_norm_fwd(h: torch.Tensor, w_pre: torch.Tensor, o: torch.Tensor | None 
     gate: [D] (a channel's), [..., 1] (a row's) or h's shape.  Without o: the
     norm of h alone.  Returns (h' in h's type -- h itself without o --, y bf16,
     y's Act8 with pack or None)."""
-    n = _norm_args(h, w_pre, o, w_post, gate, scale, eps)
+    n, hk, ok, held = _norm_args(h, w_pre, o, w_post, gate, scale, eps)
     dev = h.device
     h_new = None if o is None else torch.empty_like(h)
     y = torch.empty_like(h, dtype=torch.bfloat16)
     x8 = _empty_act8(n.M, n.D, dev) if pack else None
     _check(load_library().block_norm_fwd(
-        ctypes.byref(n), h.data_ptr(), _ptr(o), _ptr(h_new), y.data_ptr(),
+        ctypes.byref(n), hk.data_ptr(), _ptr(ok), _ptr(h_new), y.data_ptr(),
         x8.codes.data_ptr() if pack else None, x8.exps.data_ptr() if pack else None,
         _stream(dev)))
     return (h if o is None else h_new), y, x8
@@ -208,12 +230,13 @@ def block_norm_bwd(dy: torch.Tensor, h_new: torch.Tensor, w_pre: torch.Tensor,
     dgate (fp32 for [D] and [..., 1] gates, bf16 for full ones), dw_post and
     dw_pre fp32 [D] (None without need_weights, for frozen norms)."""
     L = load_library()
-    n = _norm_args(h_new, w_pre, o, w_post, gate, scale, eps)
+    n, h_new, o, held = _norm_args(h_new, w_pre, o, w_post, gate, scale, eps)
     if _dev(dy, torch.bfloat16, "dy").shape != h_new.shape:
         raise ValueError("dy must have h_new's shape")
     if dh_new is not None and _dev(dh_new, h_new.dtype, "dh_new").shape != h_new.shape:
         raise ValueError("dh_new must have h_new's shape")
     dev, D = h_new.device, n.D
+    dy, dh_new = _start(dy, D), _start(dh_new, D)
     dh = torch.empty_like(h_new)
     do = None if o is None else torch.empty_like(o)
     dgate = None
@@ -357,6 +380,7 @@ def token_logprobs_bwd(logits: torch.Tensor, targets: torch.Tensor | None, stats
     for name, t in (("entropy", entropy), ("dlogp", dlogp), ("dentropy", dentropy)):
         if t is not None and _dev(t, torch.float32, name).shape != (T,):
             raise ValueError(f"{name} must be [{T}]")
+    stats, entropy, dlogp, dentropy = map(_start, (stats, entropy, dlogp, dentropy))
     if out is None:
         out = torch.empty(T, V, dtype=logits.dtype, device=logits.device)
     elif out.dtype != logits.dtype or out.shape != logits.shape:
