@@ -18,6 +18,7 @@
 #include <algorithm>
 #include <cfloat>
 
+#include "launch_rows.h"
 #include "qn_device.h"
 #include "qn_internal.h"
 
@@ -553,8 +554,8 @@ hipError_t launch_logprobs_bwd(const void* x, bool f32, int64_t T, int64_t V, in
                                void* dx, int64_t ldd, hipStream_t st) {
   if (T == 0) return hipSuccess;
   const int64_t per = (int64_t)kThreads * kU * (f32 ? 4 : 8), chunks = (V + per - 1) / per;
-  // rows whose chunks a launch can number
-  const int64_t most = (((int64_t)1 << 31) - 1) / chunks;
+  // rows whose work items a launch can count
+  const int64_t most = rows_per_launch(chunks, kThreads);
   for (int64_t r = 0; r < T; r += most) {
     const dim3 grid((unsigned)(std::min<int64_t>(most, T - r) * chunks));
     const int64_t* tg = targets ? targets + r : nullptr;
