@@ -436,7 +436,7 @@ qn_status block_norm_bwd(const qn_block_norm* n, const uint16_t* dy, const void*
  * missing alternatives are (-inf, -1).  A row of -inf only has logp -inf,
  * entropy 0, stats (lowest fp32, -inf).  A negative target is ignored: logp
  * 0.  A target >= V reads nothing: logp NaN.  A row with a NaN or +inf has
- * NaN logp and entropy. */
+ * NaN logp, entropy and top_logp; a NaN is no alternative. */
 #define QN_LOGPROB_MAX_TOP 32
 size_t token_logprobs_workspace(int64_t T, int64_t V, qn_dtype dtype, int top_k);
 qn_status token_logprobs_fwd(const void* logits, qn_dtype dtype, int64_t T, int64_t V, int64_t ld,

@@ -119,7 +119,9 @@ typedef unsigned long long Key;  // 0: none
 constexpr Key kNoKey = ((Key)0x007fffffu << 32) | 0xffffffffu;  // above every key of -inf
 
 __device__ __forceinline__ uint32_t ordered(float x) {
-  const uint32_t b = as_u32(x + 0.f);  // -0 counts as 0
+  // -0 counts as 0, a NaN as -inf: none of the best, whatever the order in which
+  // the waves' bars reach each other
+  const uint32_t b = as_u32(fmaxf(x + 0.f, -__builtin_inff()));
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ Key key_of(float x, uint32_t i) {
