@@ -40,6 +40,14 @@ def _start(t: torch.Tensor | None, cols: int = 8):
     return t.clone()
 
 
+def _written(*ts: torch.Tensor) -> None:
+    """Tells autograd that a call wrote tensors it was given: one that was saved for a
+    backward before raises there, as after any other write in place."""
+    for t in ts:
+        if not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 # ------------------------------------------------- activation checkpoints in 8 bits
 @dataclass
 class Act8:
@@ -89,9 +97,12 @@ def act8_pack(x: torch.Tensor, out: Act8 | None = None) -> Act8:
     cols = x.shape[-1]
     M = x.numel() // cols
     x = _start(x, cols)
-    out = _empty_act8(M, cols, x.device) if out is None else _act8(out, M, cols, "out")
+    given = out is not None
+    out = _act8(out, M, cols, "out") if given else _empty_act8(M, cols, x.device)
     _check(load_library().act8_pack(x.data_ptr(), M, cols, out.codes.data_ptr(),
                                     out.exps.data_ptr(), _stream(x.device)))
+    if given:
+        _written(out.codes, out.exps)
     return out
 
 
@@ -101,13 +112,16 @@ def act8_unpack(x8: Act8, out: torch.Tensor | None = None) -> torch.Tensor:
         raise ValueError("x8 must be an Act8 with codes [M, cols]")
     M, cols = x8.codes.shape
     x8 = _act8(x8, M, cols).start()
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty(M, cols, dtype=torch.bfloat16, device=x8.codes.device)
     elif _dev(out, torch.bfloat16, "out").shape != (M, cols):
         raise ValueError(f"out must be [{M}, {cols}]")
     s = x8.c_struct()
     _check(load_library().act8_unpack(ctypes.byref(s), M, cols, out.data_ptr(),
                                       _stream(out.device)))
+    if given:
+        _written(out)
     return out
 
 
@@ -381,7 +395,8 @@ def token_logprobs_bwd(logits: torch.Tensor, targets: torch.Tensor | None, stats
         if t is not None and _dev(t, torch.float32, name).shape != (T,):
             raise ValueError(f"{name} must be [{T}]")
     stats, entropy, dlogp, dentropy = map(_start, (stats, entropy, dlogp, dentropy))
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty(T, V, dtype=logits.dtype, device=logits.device)
     elif out.dtype != logits.dtype or out.shape != logits.shape:
         raise ValueError("out must have the logits' type and shape")
@@ -389,6 +404,8 @@ def token_logprobs_bwd(logits: torch.Tensor, targets: torch.Tensor | None, stats
     _check(L.token_logprobs_bwd(logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld, _ptr(targets),
                                 scale, stats.data_ptr(), _ptr(entropy), _ptr(dlogp),
                                 _ptr(dentropy), out.data_ptr(), ldd, _stream(logits.device)))
+    if given:
+        _written(out)
     return out
 
 

@@ -1,0 +1,50 @@
+"""What autograd has to know of the calls around the linear: tensors written in place,
+checkpoints that do not belong to the input, derivatives that are not there."""
+import pytest
+import torch
+
+from tests._gpu import needs_gpu
+
+pytestmark = [pytest.mark.gpu, needs_gpu]
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def qn():
+    import quantized_fine_tuning_nf4_amd as qn
+    qn.load_library()
+    return qn
+
+
+def rnd(*shape, dtype=BF):
+    return torch.randn(*shape, device="cuda").to(dtype)
+
+
+def test_a_checkpoint_packed_again_before_the_backward(qn):
+    lin = qn.QLoRALinear(rnd(64, 128, dtype=F32), r=4, act8=True)
+    x, buf = rnd(5, 128).requires_grad_(True), qn.act8_pack(rnd(5, 128))
+    y = lin(x, x8=qn.act8_pack(x.detach(), out=buf))
+    qn.act8_pack(rnd(5, 128), out=buf)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.sum().backward()
+
+
+def test_outputs_written_in_place_count_as_modified(qn):
+    x8 = qn.act8_pack(rnd(4, 128))
+    out = rnd(4, 128)
+    before = out._version, x8.codes._version, x8.exps._version
+    qn.act8_unpack(x8, out=out)
+    qn.act8_pack(out, out=x8)
+    assert out._version > before[0]
+    assert x8.codes._version > before[1] and x8.exps._version > before[2]
+    logits = rnd(3, 50, dtype=F32).requires_grad_(True)
+    h = logits * 1.0
+    t = torch.zeros(3, dtype=torch.int64, device="cuda")
+    r = qn.token_logprobs(h, t)
+    qn.token_logprobs_bwd(h.detach(), t, r.stats, r.entropy.detach(),
+                          torch.ones(3, device="cuda"), out=h.detach())
+    with pytest.raises(RuntimeError, match="inplace"):
+        r.logp.sum().backward()
+    with torch.inference_mode():  # (such tensors count nothing)
+        z = rnd(4, 128)
+        qn.act8_unpack(qn.act8_pack(z, out=qn.act8_pack(z)), out=z)
