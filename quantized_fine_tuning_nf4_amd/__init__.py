@@ -523,6 +523,8 @@ class _QLoRAAct8Fn(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, A, B, st, alpha, rslora, mask, p, x8):
+        if x8 is not None:
+            _act8(x8, *x.shape)
         y, u = qlora_linear_fwd(st, x, A, B, alpha, rslora=rslora, dropout_mask=mask,
                                 dropout_p=p)
         if x8 is None:
@@ -579,6 +581,7 @@ class QLoRALinear(torch.nn.Module):
         return y.reshape(*shp[:-1], y.shape[-1])
 
 
-from .finetune import (Act8, BlockNorm, BlockNormGrads, TokenLogprobs, act8_pack,  # noqa: E402
-                       act8_unpack, block_norm_bwd, block_norm_fwd, qlora_linear_bwd_act8,
-                       token_logprobs, token_logprobs_bwd, token_logprobs_fwd)
+from .finetune import (Act8, BlockNorm, BlockNormGrads, TokenLogprobs, _act8,  # noqa: E402
+                       act8_pack, act8_unpack, block_norm_bwd, block_norm_fwd,
+                       qlora_linear_bwd_act8, token_logprobs, token_logprobs_bwd,
+                       token_logprobs_fwd)

@@ -48,3 +48,16 @@ def test_outputs_written_in_place_count_as_modified(qn):
     with torch.inference_mode():  # (such tensors count nothing)
         z = rnd(4, 128)
         qn.act8_unpack(qn.act8_pack(z, out=qn.act8_pack(z)), out=z)
+
+
+def test_a_checkpoint_of_another_shape_is_refused_in_the_forward(qn):
+    lin = qn.QLoRALinear(rnd(64, 128, dtype=F32), r=4, act8=True)
+    x = rnd(2, 3, 128)
+    good = qn.act8_pack(x)
+    assert lin(x, x8=good).shape == (2, 3, 64)
+    for bad in (qn.act8_pack(rnd(5, 128)), qn.act8_pack(rnd(6, 64)), qn.act8_pack(rnd(3, 256)),
+                qn.Act8(good.codes, good.exps[:, :1].contiguous()),
+                qn.Act8(good.codes.float(), good.exps), qn.Act8(good.codes.cpu(), good.exps),
+                (good.codes, good.exps)):
+        with pytest.raises(ValueError):
+            lin(x, x8=bad)
