@@ -19,6 +19,7 @@ import os
 from dataclasses import dataclass
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqlora_nf4.so")
@@ -510,6 +511,7 @@ class _QLoRAFn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         x, A, B, u, mask = ctx.saved_tensors
         dX, dA, dB = qlora_linear_bwd(ctx.st, x, dY.contiguous(), A, B, ctx.alpha, u,
@@ -534,6 +536,7 @@ class _QLoRAAct8Fn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         codes, exps, A, B, u, mask = ctx.saved_tensors
         dX, dA, dB = qlora_linear_bwd_act8(ctx.st, Act8(codes, exps), dY.contiguous(), A, B,

@@ -19,6 +19,7 @@ from collections import namedtuple
 from dataclasses import dataclass
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (QN_BF16, QN_F32, NF4State, _Act8, _BlockNorm, _check, _dev, _linear_args, _opts,
                _ptr, _stream, load_library)
@@ -286,6 +287,7 @@ class _BlockNormFn(torch.autograd.Function):
         return (None if o is None else h_new), y, codes, exps
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dh_new, dy, *_):
         h_new, o, w_pre, w_post, gate = ctx.saved_tensors
         if dy is None:
@@ -421,6 +423,7 @@ class _TokenLogprobsFn(torch.autograd.Function):
         return r.logp, r.entropy, r.stats, r.top_logp, r.top_ids
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dlogp, dentropy, *_):
         logits, targets, stats, entropy = ctx.saved_tensors
         if dlogp is None and dentropy is None:

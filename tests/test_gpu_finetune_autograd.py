@@ -61,3 +61,27 @@ def test_a_checkpoint_of_another_shape_is_refused_in_the_forward(qn):
                 (good.codes, good.exps)):
         with pytest.raises(ValueError):
             lin(x, x8=bad)
+
+
+@pytest.mark.parametrize("what", ["linear", "linear_act8", "norm", "norm_alone", "logprobs"])
+def test_second_derivatives_are_refused(qn, what):
+    """First derivatives under create_graph are right; asking for more of them raises
+    (it gave the part that does not go through the call, and no word)."""
+    if what.startswith("linear"):
+        x = rnd(5, 128).requires_grad_(True)
+        lin = qn.QLoRALinear(rnd(64, 128, dtype=F32), r=4, act8=what == "linear_act8")
+        f = lambda v: lin(v).float()  # noqa: E731
+    elif what.startswith("norm"):
+        x, o = rnd(5, 128, dtype=F32).requires_grad_(True), rnd(5, 128)
+        norm = qn.BlockNorm(128, post=True, gate=True)
+        f = lambda v: norm(v, o if what == "norm" else None)[1].float()  # noqa: E731
+    else:
+        x = rnd(5, 40, dtype=F32).requires_grad_(True)
+        t = torch.arange(5, device="cuda")
+        f = lambda v: qn.token_logprobs(v, t).logp  # noqa: E731
+    ref, = torch.autograd.grad((f(x) ** 2).sum(), x)
+    y = f(x)
+    g, = torch.autograd.grad((y ** 2).sum(), x, create_graph=True)
+    assert torch.equal(g, ref)
+    with pytest.raises(RuntimeError, match="differentiate twice"):
+        (g.float().pow(2).sum() + x.float().pow(2).sum()).backward()
