@@ -290,9 +290,11 @@ class _BlockNormFn(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dh_new, dy, *_):
         h_new, o, w_pre, w_post, gate = ctx.saved_tensors
-        if dy is None:
-            dy = torch.zeros(h_new.shape, dtype=torch.bfloat16, device=h_new.device)
         need = ctx.needs_input_grad
+        if dy is None:
+            if not (need[1] or need[3] or need[4]):  # h' alone, and only h behind it
+                return dh_new, None, None, None, None, None, None, None
+            dy = torch.zeros(h_new.shape, dtype=torch.bfloat16, device=h_new.device)
         g = block_norm_bwd(dy.contiguous(), h_new, w_pre,
                            dh_new=None if dh_new is None else dh_new.contiguous(), o=o,
                            w_post=w_post, gate=gate, scale=ctx.scale, eps=ctx.eps,

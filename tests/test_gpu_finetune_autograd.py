@@ -85,3 +85,20 @@ def test_second_derivatives_are_refused(qn, what):
     assert torch.equal(g, ref)
     with pytest.raises(RuntimeError, match="differentiate twice"):
         (g.float().pow(2).sum() + x.float().pow(2).sum()).backward()
+
+
+@pytest.mark.parametrize("with_o", [False, True])
+def test_only_the_residual_stream_has_a_gradient(qn, with_o):
+    """y unused and nothing of the block wants a gradient: h's is h''s, also where h'
+    is no number (a backward from dy = 0 made those rows NaN)."""
+    norm = qn.BlockNorm(96, post=with_o).requires_grad_(False)
+    h, o, g = rnd(5, 96, dtype=F32), rnd(5, 96), rnd(5, 96, dtype=F32)
+    h[2, 7], h[3, 0] = float("inf"), float("nan")
+    h.requires_grad_(True)
+    hn, y, _ = norm(h, o if with_o else None)
+    hn.backward(g)
+    assert torch.equal(h.grad, g)
+    h.grad = None
+    hn, y, _ = norm(h, o if with_o else None)
+    y.float().sum().backward()
+    assert torch.isnan(h.grad[2:4]).any(1).all() and torch.isfinite(h.grad[[0, 1, 4]]).all()
