@@ -849,8 +849,10 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   // lane: column j = 16jt + l%16, rows p = 16pt + 4(l/16) + i of the wave
   const int S_ = S;
-  const rsrc_t rp = make_rs(part, (uint32_t)((int64_t)S_ * P * r * 4));
-  const int64_t sl_off = (int64_t)z_wg * P * r;
+  // (all slices, below 2^32 bytes, where this launch adds them, else this one alone)
+  const rsrc_t rp = make_rs(arrivals ? part : part + (int64_t)z_wg * P * r,
+                            (uint32_t)((int64_t)(arrivals ? S_ : 1) * P * r * 4));
+  const int64_t sl_off = arrivals ? (int64_t)z_wg * P * r : 0;
 #pragma unroll
   for (int jt = 0; jt < NJ; ++jt) {
     const int j = 16 * jt + t;
@@ -1072,8 +1074,10 @@ hipError_t launch_thin_tn2(const ThinTn& a, const ThinTn& b, int64_t M, int r,
   const int tiles = job[0].tiles + job[1].tiles;
   if (tiles == 0) return hipSuccess;
   // slices added by the last workgroup of each tile (one arrival counter per
-  // tile), else by a second launch
-  unsigned* ctr = tiles <= kTnMaxTiles ? arrivals : nullptr;
+  // tile, a job's slices through 32-bit offsets), else by a second launch
+  bool here = tiles <= kTnMaxTiles;
+  for (const TnJob& j : job) here = here && (int64_t)j.S * j.P * r < (int64_t)1 << 30;
+  unsigned* ctr = here ? arrivals : nullptr;
   const bool mask = (job[0].tiles > 0 && job[0].zmask) || (job[1].tiles > 0 && job[1].zmask);
   if (a.codes) return hipErrorInvalidValue;  // a checkpoint is the second job's
   const size_t lds =
