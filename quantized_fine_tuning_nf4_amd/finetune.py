@@ -21,8 +21,8 @@ from dataclasses import dataclass
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (QN_BF16, QN_F32, NF4State, _Act8, _BlockNorm, _check, _dev, _linear_args, _opts,
-               _ptr, _stream, load_library)
+from . import (QN_BF16, QN_EALIGN, QN_F32, NF4State, _Act8, _BlockNorm, _check, _dev,
+               _linear_args, _opts, _ptr, _stream, load_library)
 
 ACT8_BLOCK = 64
 MAX_TOP = 32  # alternatives of a row
@@ -32,13 +32,13 @@ _DTYPES = {torch.bfloat16: QN_BF16, torch.float32: QN_F32}
 # small call's host time each, where torch.empty((M, cols), ..) takes 1.7.
 
 
-def _start(t: torch.Tensor | None, cols: int = 8):
-    """An input as the kernels take it: a view that starts between 16-byte boundaries
-    (a slice of a larger tensor) is copied, except rows of an odd width, which may start
-    anywhere.  The caller holds the result until its launch."""
-    if t is None or cols % 8 or t.data_ptr() % 16 == 0:
-        return t
-    return t.clone()
+def _aligned(status: int, *ts: torch.Tensor | None):
+    """After a call that returned QN_EALIGN: its inputs, those that start between 16-byte
+    boundaries (slices of larger tensors) as copies, for a second try; None where that
+    is not it.  (Asked beforehand, it is 0.3 to 0.7 us of every small call.)"""
+    if status != QN_EALIGN or not any(t is not None and t.data_ptr() % 16 for t in ts):
+        return None
+    return [t.clone() if t is not None and t.data_ptr() % 16 else t for t in ts]
 
 
 def _written(*ts: torch.Tensor) -> None:
@@ -59,12 +59,6 @@ class Act8:
 
     def nbytes(self) -> int:
         return self.codes.numel() + self.exps.numel()
-
-    def start(self) -> Act8:
-        """Itself, or a copy where it starts as the kernels do not take it."""
-        cols = self.codes.shape[1]
-        codes, exps = _start(self.codes, cols), _start(self.exps, cols)
-        return self if codes is self.codes and exps is self.exps else Act8(codes, exps)
 
     def c_struct(self) -> _Act8:
         return _Act8(self.codes.data_ptr(), self.exps.data_ptr())
@@ -97,11 +91,13 @@ def act8_pack(x: torch.Tensor, out: Act8 | None = None) -> Act8:
         raise ValueError("x must be [..., cols] with cols >= 1")
     cols = x.shape[-1]
     M = x.numel() // cols
-    x = _start(x, cols)
     given = out is not None
     out = _act8(out, M, cols, "out") if given else _empty_act8(M, cols, x.device)
-    _check(load_library().act8_pack(x.data_ptr(), M, cols, out.codes.data_ptr(),
-                                    out.exps.data_ptr(), _stream(x.device)))
+    rc = load_library().act8_pack(x.data_ptr(), M, cols, out.codes.data_ptr(),
+                                  out.exps.data_ptr(), _stream(x.device))
+    if rc:
+        again = _aligned(rc, x)
+        return act8_pack(*again, out=out) if again else _check(rc)
     if given:
         _written(out.codes, out.exps)
     return out
@@ -112,15 +108,18 @@ def act8_unpack(x8: Act8, out: torch.Tensor | None = None) -> torch.Tensor:
     if not isinstance(x8, Act8) or x8.codes.dim() != 2:
         raise ValueError("x8 must be an Act8 with codes [M, cols]")
     M, cols = x8.codes.shape
-    x8 = _act8(x8, M, cols).start()
+    _act8(x8, M, cols)
     given = out is not None
     if not given:
         out = torch.empty(M, cols, dtype=torch.bfloat16, device=x8.codes.device)
     elif _dev(out, torch.bfloat16, "out").shape != (M, cols):
         raise ValueError(f"out must be [{M}, {cols}]")
     s = x8.c_struct()
-    _check(load_library().act8_unpack(ctypes.byref(s), M, cols, out.data_ptr(),
-                                      _stream(out.device)))
+    rc = load_library().act8_unpack(ctypes.byref(s), M, cols, out.data_ptr(),
+                                    _stream(out.device))
+    if rc:
+        again = _aligned(rc, x8.codes, x8.exps)
+        return act8_unpack(Act8(*again), out=out) if again else _check(rc)
     if given:
         _written(out)
     return out
@@ -148,7 +147,6 @@ def qlora_linear_bwd_act8(st: NF4State, x8: Act8, dY: torch.Tensor, A: torch.Ten
         raise ValueError(f"u must be [{M}, {r}]")
     if dropout_mask is not None and dropout_mask.numel() * 8 < M * st.cols:
         raise ValueError(f"dropout_mask must hold {M * st.cols} bits")
-    x8, dY, A, B, u = x8.start(), _start(dY), _start(A), _start(B), _start(u)
     dev = dY.device
     dX = torch.empty(M, st.cols, dtype=torch.bfloat16, device=dev) if need_dx else None
     dA = torch.empty(r, st.cols, dtype=torch.float32, device=dev)
@@ -158,11 +156,19 @@ def qlora_linear_bwd_act8(st: NF4State, x8: Act8, dY: torch.Tensor, A: torch.Ten
     if workspace is None or workspace.numel() < need:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
     s, c = st.c_struct(), x8.c_struct()
-    _check(L.qlora_linear_bwd_act8(ctypes.byref(s), ctypes.byref(c), dY.data_ptr(), M,
-                                   A.data_ptr(), B.data_ptr(), r, float(alpha),
-                                   ctypes.byref(o) if o is not None else None, u.data_ptr(),
-                                   _ptr(dX), dA.data_ptr(), dB.data_ptr(), workspace.data_ptr(),
-                                   workspace.numel(), _stream(dev)))
+    rc = L.qlora_linear_bwd_act8(ctypes.byref(s), ctypes.byref(c), dY.data_ptr(), M,
+                                 A.data_ptr(), B.data_ptr(), r, float(alpha),
+                                 ctypes.byref(o) if o is not None else None, u.data_ptr(),
+                                 _ptr(dX), dA.data_ptr(), dB.data_ptr(), workspace.data_ptr(),
+                                 workspace.numel(), _stream(dev))
+    if rc:
+        again = _aligned(rc, x8.codes, x8.exps, dY, A, B, u)
+        if not again:
+            _check(rc)
+        codes, exps, dY, A, B, u = again
+        return qlora_linear_bwd_act8(st, Act8(codes, exps), dY, A, B, alpha, u, need_dx=need_dx,
+                                     workspace=workspace, rslora=rslora,
+                                     dropout_mask=dropout_mask, dropout_p=dropout_p)
     return dX, dA, dB
 
 
@@ -171,8 +177,7 @@ BlockNormGrads = namedtuple("BlockNormGrads", "dh do dgate dw_post dw_pre")
 
 
 def _norm_args(h, w_pre, o, w_post, gate, scale, eps):
-    """The C argument struct of a block norm on h [..., D], and h, o and what else it
-    points to as the kernels take them."""
+    """The C argument struct of a block norm on h [..., D]."""
     if not isinstance(h, torch.Tensor) or h.dtype not in _DTYPES:
         raise ValueError("h must be a bfloat16 or float32 tensor")
     _dev(h, h.dtype, "h")
@@ -206,12 +211,8 @@ def _norm_args(h, w_pre, o, w_post, gate, scale, eps):
             _dev(gate, torch.bfloat16, "gate")
         else:
             raise ValueError(f"gate must be [{D}], [..., 1] or h's shape")
-    h, o, w_pre, w_post = _start(h, D), _start(o, D), _start(w_pre), _start(w_post)
-    if kind != GATE_ROW:
-        gate = _start(gate, D if kind == GATE_ELEMENT else 8)
-    n = _BlockNorm(M, D, w_pre.data_ptr(), _ptr(w_post), _ptr(gate), _DTYPES[h.dtype],
-                   _DTYPES[wt], kind, scale, eps)
-    return n, h, o, (w_pre, w_post, gate)
+    return _BlockNorm(M, D, w_pre.data_ptr(), _ptr(w_post), _ptr(gate), _DTYPES[h.dtype],
+                      _DTYPES[wt], kind, scale, eps)
 
 
 def block_norm_fwd(h: torch.Tensor, w_pre: torch.Tensor, o: torch.Tensor | None = None,
@@ -222,15 +223,20 @@ def block_norm_fwd(h: torch.Tensor, w_pre: torch.Tensor, o: torch.Tensor | None 
     gate: [D] (a channel's), [..., 1] (a row's) or h's shape.  Without o: the
     norm of h alone.  Returns (h' in h's type -- h itself without o --, y bf16,
     y's Act8 with pack or None)."""
-    n, hk, ok, held = _norm_args(h, w_pre, o, w_post, gate, scale, eps)
+    n = _norm_args(h, w_pre, o, w_post, gate, scale, eps)
     dev = h.device
     h_new = None if o is None else torch.empty_like(h)
     y = torch.empty_like(h, dtype=torch.bfloat16)
     x8 = _empty_act8(n.M, n.D, dev) if pack else None
-    _check(load_library().block_norm_fwd(
-        ctypes.byref(n), hk.data_ptr(), _ptr(ok), _ptr(h_new), y.data_ptr(),
+    rc = load_library().block_norm_fwd(
+        ctypes.byref(n), h.data_ptr(), _ptr(o), _ptr(h_new), y.data_ptr(),
         x8.codes.data_ptr() if pack else None, x8.exps.data_ptr() if pack else None,
-        _stream(dev)))
+        _stream(dev))
+    if rc:
+        again = _aligned(rc, h, w_pre, o, w_post, gate)
+        if not again:
+            _check(rc)
+        h_new, y, x8 = block_norm_fwd(*again, scale=scale, eps=eps, pack=pack)
     return (h if o is None else h_new), y, x8
 
 
@@ -245,13 +251,12 @@ def block_norm_bwd(dy: torch.Tensor, h_new: torch.Tensor, w_pre: torch.Tensor,
     dgate (fp32 for [D] and [..., 1] gates, bf16 for full ones), dw_post and
     dw_pre fp32 [D] (None without need_weights, for frozen norms)."""
     L = load_library()
-    n, h_new, o, held = _norm_args(h_new, w_pre, o, w_post, gate, scale, eps)
+    n = _norm_args(h_new, w_pre, o, w_post, gate, scale, eps)
     if _dev(dy, torch.bfloat16, "dy").shape != h_new.shape:
         raise ValueError("dy must have h_new's shape")
     if dh_new is not None and _dev(dh_new, h_new.dtype, "dh_new").shape != h_new.shape:
         raise ValueError("dh_new must have h_new's shape")
     dev, D = h_new.device, n.D
-    dy, dh_new = _start(dy, D), _start(dh_new, D)
     dh = torch.empty_like(h_new)
     do = None if o is None else torch.empty_like(o)
     dgate = None
@@ -266,10 +271,14 @@ def block_norm_bwd(dy: torch.Tensor, h_new: torch.Tensor, w_pre: torch.Tensor,
     need = L.block_norm_bwd_workspace(ctypes.byref(n), int(need_weights), int(dgate is not None))
     if need > 0 and (workspace is None or workspace.numel() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _check(L.block_norm_bwd(ctypes.byref(n), dy.data_ptr(), _ptr(dh_new), h_new.data_ptr(),
-                            _ptr(o), dh.data_ptr(), _ptr(do), _ptr(dgate), _ptr(dw_post),
-                            _ptr(dw_pre), _ptr(workspace),
-                            0 if workspace is None else workspace.numel(), _stream(dev)))
+    rc = L.block_norm_bwd(ctypes.byref(n), dy.data_ptr(), _ptr(dh_new), h_new.data_ptr(),
+                          _ptr(o), dh.data_ptr(), _ptr(do), _ptr(dgate), _ptr(dw_post),
+                          _ptr(dw_pre), _ptr(workspace),
+                          0 if workspace is None else workspace.numel(), _stream(dev))
+    if rc:
+        again = _aligned(rc, dy, h_new, w_pre, dh_new, o, w_post, gate)
+        return block_norm_bwd(*again, scale=scale, eps=eps, need_weights=need_weights,
+                              need_gate=need_gate, workspace=workspace) if again else _check(rc)
     return BlockNormGrads(dh, do, dgate, dw_post, dw_pre)
 
 
@@ -398,16 +407,19 @@ def token_logprobs_bwd(logits: torch.Tensor, targets: torch.Tensor | None, stats
     for name, t in (("entropy", entropy), ("dlogp", dlogp), ("dentropy", dentropy)):
         if t is not None and _dev(t, torch.float32, name).shape != (T,):
             raise ValueError(f"{name} must be [{T}]")
-    stats, entropy, dlogp, dentropy = map(_start, (stats, entropy, dlogp, dentropy))
     given = out is not None
     if not given:
         out = torch.empty(T, V, dtype=logits.dtype, device=logits.device)
     elif out.dtype != logits.dtype or out.shape != logits.shape:
         raise ValueError("out must have the logits' type and shape")
     _, _, ldd = _logits(out, None, "out")
-    _check(L.token_logprobs_bwd(logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld, _ptr(targets),
-                                scale, stats.data_ptr(), _ptr(entropy), _ptr(dlogp),
-                                _ptr(dentropy), out.data_ptr(), ldd, _stream(logits.device)))
+    rc = L.token_logprobs_bwd(logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld, _ptr(targets),
+                              scale, stats.data_ptr(), _ptr(entropy), _ptr(dlogp),
+                              _ptr(dentropy), out.data_ptr(), ldd, _stream(logits.device))
+    if rc:
+        again = _aligned(rc, stats, entropy, dlogp, dentropy)
+        return token_logprobs_bwd(logits, targets, *again, scale=scale,
+                                  out=out) if again else _check(rc)
     if given:
         _written(out)
     return out
