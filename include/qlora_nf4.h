@@ -342,8 +342,10 @@ qn_status lora_linear_bf16(const uint16_t* x, int64_t M, const uint16_t* W, int6
  * finite bf16), c = x 2^-e rounded to the nearest whole number (ties to even)
  * and held to -127 .. 127.  A power-of-two scale makes every x~ a bf16 number
  * exactly, so the products of the backward take it without another rounding;
- * |x - x~| <= 2^(e-1), at most 1/127 of the block's largest magnitude.  A block
- * that holds a NaN or an infinity gets E = 255 and reads back as NaN. */
+ * |x - x~| <= 2^(e-1), less than 1/127 of the block's largest magnitude where
+ * e > -126.  At e = -126 a block may be smaller than its scale: there is the
+ * absolute bound 2^-127 alone, and magnitudes up to it read back as zeros.  A
+ * block that holds a NaN or an infinity gets E = 255 and reads back as NaN. */
 #define QN_ACT8_BLOCK 64
 typedef struct {
   const int8_t* codes; /* [M, cols] device, 16-byte aligned */
