@@ -32,6 +32,10 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417
 // below any t whose 2^t is not zero, and finite: 0 times it is 0
 constexpr float kFarBelow = -1e4f;
 
+// scale log2 e, finite for every scale: 0 times it, a largest logit's, is 0
+__device__ __forceinline__ float base2_scale(float scale) {
+  return fminf(scale * kLog2e, FLT_MAX);
+}
 __device__ __forceinline__ float exp2_of(float t) { return __builtin_amdgcn_exp2f(t); }
 __device__ __forceinline__ float log2_of(float s) { return __builtin_amdgcn_logf(s); }
 
@@ -296,7 +300,7 @@ __global__ __launch_bounds__(64 * W) void k_logprobs_fwd(const L* __restrict__ x
   const int64_t z = blockIdx.x - row * S;
   const L* p = x + row * ld;
   const int64_t begin = z * slice, end = min(begin + slice, V);
-  const float k2 = out.scale * kLog2e;
+  const float k2 = base2_scale(out.scale);
   int64_t t = -1;
   float xt = 0.f;
   if (S == 1 && out.logp) {
@@ -422,7 +426,7 @@ __global__ __launch_bounds__(64 * W) void k_logprobs_join(const L* __restrict__ 
     join_lists<W>(mine, sk);
   }
   if (wave != 0) return;
-  wave_join(a, out.scale * kLog2e);
+  wave_join(a, base2_scale(out.scale));
   write_row(out, row, a, t, V, xt, mine);
 }
 
