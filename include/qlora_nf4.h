@@ -458,6 +458,105 @@ qn_status token_logprobs_bwd(const void* logits, qn_dtype dtype, int64_t T, int6
                              const float* entropy, const float* dlogp, const float* dentropy,
                              void* dlogits, int64_t ldd, void* stream);
 
+/* ---- Dropout on the adapter branch's input (or on an activation) without a stored
+ * mask: the keep bits come from a counter and are drawn where they are used, in the
+ * forward and again in the backward.  Philox 4x32 with ten rounds: the counter
+ * (b, offset + *step), both 64 bits, low words first, under the key `seed` gives
+ * four 32-bit words for the elements 8b .. 8b + 7 of the row-major tensor; elements
+ * 8b + 2i and 8b + 2i + 1 take the low and the high half of word i and are dropped
+ * where it is less than t = p 2^16, rounded (at most 2^16 - 1).  Kept elements are
+ * multiplied by 2^16 / (2^16 - t).
+ *   offset: tells the uses of one seed apart (layers, say);
+ *   step (nullable, 8-byte aligned): a number in device memory that is added to
+ *     it, read when the kernels run, so that a captured graph draws another mask at
+ *     every replay once the caller has changed it.  A forward and its backward have
+ *     to find the same number. */
+typedef struct {
+  uint64_t seed, offset;
+  const uint64_t* step;
+  float p; /* in [0, 1) */
+} qn_dropout;
+
+/* out [n] = kept ? x * 2^16 / (2^16 - t) : 0 in x's type (QN_BF16 or QN_F32; a dropped NaN
+ * is 0); out may be x.  Its gradient is the same call on the gradient.  Element
+ * aligned; 0 <= n <= 2^40. */
+qn_status dropout_apply(const void* x, qn_dtype dtype, int64_t n, const qn_dropout* drop,
+                        void* out, void* stream);
+
+/* qlora_linear_fwd and qlora_linear_bwd (from x, or from x8, the other NULL) under
+ * such dropout (drop nullable; rslora 0 or 1 as in qn_lora_opts): the same results
+ * as with a stored mask of the same bits and the branch's scale times
+ * 2^16 / (2^16 - t).  The backward holds the bits in its workspace while it runs. */
+size_t qlora_linear_drop_workspace(int64_t M, int64_t rows, int64_t cols, int r, int backward,
+                                   int act8);
+qn_status qlora_linear_fwd_drop(const qn_nf4dq* w, const uint16_t* x, int64_t M, const uint16_t* A,
+                                const uint16_t* B, int r, float alpha, int rslora,
+                                const qn_dropout* drop, uint16_t* y, float* u_out, void* workspace,
+                                size_t workspace_bytes, void* stream);
+qn_status qlora_linear_bwd_drop(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8,
+                                const uint16_t* dY, int64_t M, const uint16_t* A,
+                                const uint16_t* B, int r, float alpha, int rslora,
+                                const qn_dropout* drop, const float* u_saved, uint16_t* dX,
+                                float* dA, float* dB, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* ---- MXFP4: the 4-bit format that the matrix cores multiply as it is (OCP
+ * Microscaling Formats: E2M1 elements, an E8M0 scale for 32 of them).  A matrix
+ * [rows, cols] in blocks of 32 columns of a row (the last one of a row may be shorter):
+ *   element = level[c & 7] 2^(E-127), negative where c & 8,
+ *   levels 0, 1/2, 1, 3/2, 2, 3, 4, 6;
+ *   E - 127 = floor(log2 max|x|) - 2 over the block, at least -127 (also where all
+ *   are zero); c: the level nearest x 2^(127-E), ties to an even c, magnitudes past
+ *   6 to 6.  A block that holds a NaN or an infinity has E = 255 and reads back as
+ *   NaN.
+ * With J = ceil(cols / 256):
+ *   codes  uint8 [rows, 128 J]: two codes a byte, even columns low; 0 past cols
+ *   scales uint8 [ceil(rows / 32), J, 256]: E in the order in which a wave's 64
+ *     lanes take four each: byte 4 (16 (b % 4) + n % 16) + 2 (n / 16) + b / 4 is that of row
+ *     n of the 32 and block b of the eight; 127 past the matrix. */
+#define QN_MX4_BLOCK 32
+typedef struct {
+  const uint8_t* codes;  /* device, 16-byte aligned */
+  const uint8_t* scales; /* device, 16-byte aligned */
+  int64_t rows, cols;
+} qn_mx4;
+
+/* x [rows, cols] fp32 or bf16 -> codes, scales.  0 <= rows <= 2^23, 1 <= cols <= 2^20;
+ * rows of a width that is no multiple of 8 may start on any element. */
+qn_status mx4_quantize(const void* x, qn_dtype dtype, int64_t rows, int64_t cols, uint8_t* codes,
+                       uint8_t* scales, void* stream);
+
+/* codes, scales -> the values [rows, cols], fp32 or bf16 (exact). */
+qn_status mx4_dequantize(const qn_mx4* w, qn_dtype out_dtype, void* out, void* stream);
+
+/* Workspace bytes of the linear calls below (act8, drop: a backward from an 8-bit
+ * checkpoint, under dropout). */
+size_t mx4_linear_workspace(int64_t M, int64_t rows, int64_t cols, int r, int backward, int act8,
+                            int drop);
+
+/* y [M, rows] bf16 = Q(x) W^T + s u B^T,  u = drop(x) A^T fp32 [M, r] (u_out, nullable),
+ * where Q rounds x [M, cols] bf16 to MXFP4 as mx4_quantize does: the product is the
+ * matrix cores' own on two such operands, fp32 sums.  s = alpha / r (alpha / sqrt(r) with
+ * rslora) times the dropout's factor.  r == 0: no adapter (A, B, u_out and drop NULL or
+ * unused) and any rows and cols up to 2^20; 1 <= r <= 64: rows a multiple of 8 and cols
+ * of 64.  M == 0: no work. */
+qn_status mx4_linear_fwd(const qn_mx4* w, const uint16_t* x, int64_t M, const uint16_t* A,
+                         const uint16_t* B, int r, float alpha, int rslora, const qn_dropout* drop,
+                         uint16_t* y, float* u_out, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* Its backward, Q's gradient taken as one (each element's own):
+ *   dX = G W + s drop(G B A)  (skipped if dX == NULL),  dA = s (G B)^T drop(x),
+ *   dB = s G^T u
+ * from x or x8 as above, u_saved nullable with x.  rows a multiple of 8, cols of 64;
+ * r == 0: dX alone (the other outputs and x unused).  W enters the product as bf16,
+ * which holds its values exactly where they are at least 2^-126. */
+qn_status mx4_linear_bwd(const qn_mx4* w, const uint16_t* x, const qn_act8* x8,
+                         const uint16_t* dY, int64_t M, const uint16_t* A, const uint16_t* B,
+                         int r, float alpha, int rslora, const qn_dropout* drop,
+                         const float* u_saved, uint16_t* dX, float* dA, float* dB, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

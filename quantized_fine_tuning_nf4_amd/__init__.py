@@ -35,7 +35,10 @@ EXPORTS = ["qn_abi_version", "qn_status_str", "qn_nf4_codebook", "nf4_quantize_d
            "qlora_linear_workspace_state", "qn_fp4_codebook", "adamw8_step", "act8_pack",
            "act8_unpack", "qlora_linear_bwd_act8_workspace", "qlora_linear_bwd_act8",
            "block_norm_fwd", "block_norm_bwd_workspace", "block_norm_bwd",
-           "token_logprobs_workspace", "token_logprobs_fwd", "token_logprobs_bwd"]
+           "token_logprobs_workspace", "token_logprobs_fwd", "token_logprobs_bwd",
+           "dropout_apply", "qlora_linear_drop_workspace", "qlora_linear_fwd_drop",
+           "qlora_linear_bwd_drop", "mx4_quantize", "mx4_dequantize", "mx4_linear_workspace",
+           "mx4_linear_fwd", "mx4_linear_bwd"]
 ROUTES = {1: "decode_rows", 2: "decode_tiles", 3: "decode_split", 4: "fused_small", 5: "fused",
           6: "dense"}
 
@@ -66,6 +69,16 @@ class _NF4DQ(ctypes.Structure):
 
 class _Act8(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("exps", ctypes.c_void_p)]
+
+
+class _Dropout(ctypes.Structure):
+    _fields_ = [("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("step", ctypes.c_void_p), ("p", ctypes.c_float)]
+
+
+class _MX4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
 
 
 class _BlockNorm(ctypes.Structure):
@@ -138,6 +151,7 @@ def load_library(path: str = LIB_PATH):
     L.qlora_linear_route.restype = ctypes.c_int
     I32, F32 = ctypes.c_int, ctypes.c_float
     A8, BN = ctypes.POINTER(_Act8), ctypes.POINTER(_BlockNorm)
+    DO, MX = ctypes.POINTER(_Dropout), ctypes.POINTER(_MX4)
     for name, res, args in [
             ("act8_pack", I32, [P, I64, I64, P, P, P]),
             ("act8_unpack", I32, [A8, I64, I64, P, P]),
@@ -150,7 +164,19 @@ def load_library(path: str = LIB_PATH):
             ("token_logprobs_workspace", SZ, [I64, I64, I32, I32]),
             ("token_logprobs_fwd", I32, [P, I32, I64, I64, I64, P, F32, I32, P, P, P, P, P, P, SZ,
                                          P]),
-            ("token_logprobs_bwd", I32, [P, I32, I64, I64, I64, P, F32, P, P, P, P, P, I64, P])]:
+            ("token_logprobs_bwd", I32, [P, I32, I64, I64, I64, P, F32, P, P, P, P, P, I64, P]),
+            ("dropout_apply", I32, [P, I32, I64, DO, P, P]),
+            ("qlora_linear_drop_workspace", SZ, [I64, I64, I64, I32, I32, I32]),
+            ("qlora_linear_fwd_drop", I32, [ctypes.POINTER(_NF4DQ), P, I64, P, P, I32, F32, I32, DO,
+                                            P, P, P, SZ, P]),
+            ("qlora_linear_bwd_drop", I32, [ctypes.POINTER(_NF4DQ), P, A8, P, I64, P, P, I32, F32,
+                                            I32, DO, P, P, P, P, P, SZ, P]),
+            ("mx4_quantize", I32, [P, I32, I64, I64, P, P, P]),
+            ("mx4_dequantize", I32, [MX, I32, P, P]),
+            ("mx4_linear_workspace", SZ, [I64, I64, I64, I32, I32, I32, I32]),
+            ("mx4_linear_fwd", I32, [MX, P, I64, P, P, I32, F32, I32, DO, P, P, P, SZ, P]),
+            ("mx4_linear_bwd", I32, [MX, P, A8, P, I64, P, P, I32, F32, I32, DO, P, P, P, P, P, SZ,
+                                     P])]:
         f = getattr(L, name)
         f.restype, f.argtypes = res, args
     _lib = L
@@ -415,13 +441,20 @@ def _opts(rslora, mask, p):
     return _LoraOpts(int(bool(rslora)), _ptr(mask), float(p))
 
 
+def _one_dropout(mask, p):
+    if mask is not None or p:
+        raise ValueError("give dropout_mask and dropout_p, or drop, not both")
+
+
 def qlora_linear_fwd(st: NF4State, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
                      alpha: float, save_u: bool = True, y: torch.Tensor | None = None,
                      workspace: torch.Tensor | None = None, rslora: bool = False,
-                     dropout_mask: torch.Tensor | None = None, dropout_p: float = 0.0):
+                     dropout_mask: torch.Tensor | None = None, dropout_p: float = 0.0,
+                     drop: Dropout | None = None):
     """y = x Qhat(W)^T + s (x A^T) B^T with s = alpha / r (alpha / sqrt(r)
     with rslora); dropout_mask / dropout_p: dropout on the adapter branch's
-    input (see dropout_mask()).  Returns (y bf16 [M, d_out], u fp32 [M, r] or
+    input (see dropout_mask()); drop: the same by a mask that the kernels draw
+    from a counter (see Dropout).  Returns (y bf16 [M, d_out], u fp32 [M, r] or
     None; u is the branch's x A^T, masked under dropout)."""
     L = load_library()
     x = _dev(x, torch.bfloat16, "x")
@@ -431,6 +464,9 @@ def qlora_linear_fwd(st: NF4State, x: torch.Tensor, A: torch.Tensor, B: torch.Te
     if y is None:
         y = torch.empty((M, st.rows), dtype=torch.bfloat16, device=x.device)
     u = torch.empty((M, r), dtype=torch.float32, device=x.device) if save_u else None
+    if drop is not None:
+        _one_dropout(dropout_mask, dropout_p)
+        return _qlora_fwd_drop(st, x, A, B, r, alpha, rslora, drop, y, u, workspace)
     o = _opts(rslora, dropout_mask, dropout_p)
     op = ctypes.byref(o) if o is not None else None
     sc = st.c_struct()
@@ -448,8 +484,9 @@ def qlora_linear_bwd(st: NF4State, x: torch.Tensor, dY: torch.Tensor, A: torch.T
                      B: torch.Tensor, alpha: float, u: torch.Tensor | None = None,
                      need_dx: bool = True, workspace: torch.Tensor | None = None,
                      rslora: bool = False, dropout_mask: torch.Tensor | None = None,
-                     dropout_p: float = 0.0):
-    """Returns (dX bf16 [M, d_in] or None, dA fp32 [r, d_in], dB fp32 [d_out, r])."""
+                     dropout_p: float = 0.0, drop: Dropout | None = None):
+    """Returns (dX bf16 [M, d_in] or None, dA fp32 [r, d_in], dB fp32 [d_out, r]).
+    The dropout options are the forward's."""
     L = load_library()
     x = _dev(x, torch.bfloat16, "x")
     dY = _dev(dY, torch.bfloat16, "dY")
@@ -465,6 +502,11 @@ def qlora_linear_bwd(st: NF4State, x: torch.Tensor, dY: torch.Tensor, A: torch.T
     dX = torch.empty((M, st.cols), dtype=torch.bfloat16, device=x.device) if need_dx else None
     dA = torch.empty((r, st.cols), dtype=torch.float32, device=x.device)
     dB = torch.empty((st.rows, r), dtype=torch.float32, device=x.device)
+    if drop is not None:
+        _one_dropout(dropout_mask, dropout_p)
+        _check(_qlora_bwd_drop(st, x, None, dY, A, B, r, alpha, rslora, drop, u, dX, dA, dB,
+                               workspace))
+        return dX, dA, dB
     o = _opts(rslora, dropout_mask, dropout_p)
     op = ctypes.byref(o) if o is not None else None
     sc = st.c_struct()
@@ -553,14 +595,27 @@ class QLoRALinear(torch.nn.Module):
     as in the course notebook's LoRALinear).  act8: what the backward needs
     of x is kept as an 8-bit checkpoint instead of x itself; forward's x8
     passes one that is at hand already (BlockNorm makes it, and the linears
-    that share an input share it)."""
+    that share an input share it).  base: "nf4", or "mx4" for MXFP4 weights,
+    whose product takes x in MXFP4 too (mx4_linear_fwd).  seed: the dropout's
+    mask is drawn by the kernels from a counter and not kept, each forward's from
+    an offset of its own (Dropout; give every layer its seed); step: its device
+    tensor, for captured graphs, where the offset of the capture stays."""
 
     def __init__(self, weight: torch.Tensor, r: int = 16, alpha: float = 32.0,
-                 dropout: float = 0.0, rslora: bool = False, act8: bool = False):
+                 dropout: float = 0.0, rslora: bool = False, act8: bool = False,
+                 base: str = "nf4", seed: int | None = None, step: torch.Tensor | None = None):
         super().__init__()
         self.act8 = bool(act8)
+        if base not in ("nf4", "mx4"):
+            raise ValueError('base must be "nf4" or "mx4"')
+        if base == "mx4" and dropout and seed is None:
+            raise ValueError('dropout with base="mx4" needs a seed')
+        if step is not None and seed is None:
+            raise ValueError("step belongs to a seed")
+        self.seed, self.step, self.draws = seed, step, 0
         d_out, d_in = weight.shape
-        self.st = nf4_quantize_dq(weight.detach().float().contiguous())
+        W = weight.detach().float().contiguous()
+        self.st = nf4_quantize_dq(W) if base == "nf4" else mx4_quantize(W)
         self.r, self.alpha, self.dropout, self.rslora = r, alpha, float(dropout), bool(rslora)
         A = torch.empty(r, d_in, dtype=torch.float32, device=weight.device)
         torch.nn.init.kaiming_uniform_(A, a=5 ** 0.5)
@@ -574,6 +629,14 @@ class QLoRALinear(torch.nn.Module):
         shp = x.shape
         x2 = x.reshape(-1, shp[-1]).contiguous()
         p = self.dropout if self.training else 0.0
+        if isinstance(self.st, MX4) or (self.seed is not None and p > 0):
+            drop = None
+            if p > 0:
+                drop = Dropout(p, self.seed, self.draws, self.step)
+                self.draws += 1
+            y = _LinearFn.apply(x2, self.lora_A, self.lora_B, self.st, self.alpha, self.rslora,
+                                drop, self.act8, x8)
+            return y.reshape(*shp[:-1], y.shape[-1])
         mask = dropout_mask(x2.shape[0], x2.shape[1], p, x2.device) if p > 0 else None
         if self.act8:
             y = _QLoRAAct8Fn.apply(x2, self.lora_A, self.lora_B, self.st, self.alpha, self.rslora,
@@ -588,3 +651,6 @@ from .finetune import (Act8, BlockNorm, BlockNormGrads, TokenLogprobs, _act8,  #
                        act8_pack, act8_unpack, block_norm_bwd, block_norm_fwd,
                        qlora_linear_bwd_act8, token_logprobs, token_logprobs_bwd,
                        token_logprobs_fwd)
+from .mx4 import (MX4, Dropout, _LinearFn, _qlora_bwd_drop, _qlora_fwd_drop,  # noqa: E402
+                  dropout, dropout_apply, mx4_dequantize, mx4_linear_bwd, mx4_linear_fwd,
+                  mx4_quantize)

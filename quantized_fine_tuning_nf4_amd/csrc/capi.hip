@@ -3,6 +3,7 @@
 // launches nothing on error.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <cstring>
@@ -118,6 +119,8 @@ bool dense_path(int64_t M, int64_t out_cols) {
 }
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
+Mx4 to_mx4(const qn_mx4* w) { return Mx4{w->codes, w->scales, w->rows, w->cols}; }
+
 struct FwdWs {
   unsigned* arrivals;  // [kArrivalWords] arrival counters (zero between calls)
   float* u;      // [M, r] when the caller gives no u_out
@@ -174,10 +177,12 @@ struct BwdWs {
   uint16_t* wt;   // [cols, ldt] bf16 Qhat(W)^T (dense path)
   int64_t ldt;
   uint16_t* At;   // [cols, r] A^T (dense path)
+  uint8_t* bits;  // [M cols / 8] keep bits (dropout from a counter)
 };
 
 BwdWs carve_bwd(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool need_u,
-                bool act8 = false, bool need_dx = true) {
+                bool act8 = false, bool need_dx = true, bool always_dense = false,
+                bool drop = false) {
   BwdWs b;
   b.arrivals = c.take<unsigned>(kArrivalWords);
   if (need_u) {
@@ -203,16 +208,18 @@ BwdWs carve_bwd(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool ne
   // beat the dequantizing product, whose tiles walk the rows of W at 57 us per
   // 1024 (M = 300, 4096x4096: 285 us with it, 55 from the copy; M = 1, 1024x4096:
   // 64 and 30; even at 64 rows, 24 us)
-  const bool dense = M > 0 && (act8 ? need_dx : dense_path(M, cols));
+  const bool dense = M > 0 && (act8 || always_dense ? need_dx : dense_path(M, cols));
   b.wt = dense ? c.take<uint16_t>((size_t)cols * b.ldt) : nullptr;
   b.At = dense ? c.take<uint16_t>((size_t)cols * r) : nullptr;
+  b.bits = drop ? c.take<uint8_t>((size_t)M * cols / 8) : nullptr;
   return b;
 }
 
 // The adapter branch's options (nullable: alpha / r, no dropout).
 struct Lora {
   float s;               // branch scale
-  const uint8_t* mask;   // dropout keep mask (nullable)
+  const uint8_t* mask;   // dropout keep mask (nullable) ...
+  Drop drop = Drop{};    // ... or dropout from a counter
 };
 
 qn_status lora_options(const qn_lora_opts* o, float alpha, int r, Lora* out) {
@@ -234,6 +241,37 @@ qn_status lora_options(const qn_lora_opts* o, float alpha, int r, Lora* out) {
   return QN_OK;
 }
 
+// Dropout from a counter (nullable or p == 0: none): its threshold in steps of 2^-16
+// and the share of the elements that it keeps (exact).
+qn_status drop_options(const qn_dropout* o, Drop* d, float* share) {
+  *d = Drop{};
+  *share = 1.f;
+  if (!o) return QN_OK;
+  if (!(o->p >= 0.f && o->p < 1.f)) return QN_EINVAL;
+  if (reinterpret_cast<uintptr_t>(o->step) & 7u) return QN_EALIGN;
+  const int t = (int)std::min(std::nearbyint((double)o->p * 65536.0), 65535.0);
+  if (t == 0) return QN_OK;
+  d->key0 = (uint32_t)o->seed;
+  d->key1 = (uint32_t)(o->seed >> 32);
+  d->offset = o->offset;
+  d->step = o->step;
+  d->less = (uint32_t)(t - 1);
+  d->on = true;
+  *share = (float)(65536 - t) * 0x1p-16f;
+  return QN_OK;
+}
+
+// The same for the adapter branch, with its scale.
+qn_status lora_drop_options(int rslora, const qn_dropout* o, float alpha, int r, Lora* out) {
+  if (rslora != 0 && rslora != 1) return QN_EINVAL;
+  float share;
+  qn_status s = drop_options(o, &out->drop, &share);
+  if (s != QN_OK) return s;
+  out->mask = nullptr;
+  out->s = r == 0 ? 0.f : (rslora ? alpha / sqrtf((float)r) : alpha / (float)r) / share;
+  return QN_OK;
+}
+
 // The forward, on a workspace of ws_bytes at ws; clear: zero the arrival
 // counters with a kernel before the launch that counts on them.
 qn_status forward(const qn_nf4dq* w, const uint16_t* x, int64_t M, const uint16_t* A,
@@ -247,7 +285,7 @@ qn_status forward(const qn_nf4dq* w, const uint16_t* x, int64_t M, const uint16_
       (u_out && !aligned16(u_out)))
     return QN_EALIGN;
   Carver probe(nullptr);
-  const bool drop = lo.mask != nullptr;
+  const bool drop = lo.mask != nullptr || lo.drop.on;
   carve_fwd(probe, M, w->rows, w->cols, r, u_out == nullptr, true, drop);
   if (probe.used > 0) {
     if (!workspace) return QN_EINVAL;
@@ -277,7 +315,7 @@ qn_status forward(const qn_nf4dq* w, const uint16_t* x, int64_t M, const uint16_
   // dequantization launch that follows
   const bool fold = f.wd && f.S > 1;
   hipError_t e = launch_thin_nt(x, A, M, K, r, u, f.upart, f.S, st, !fold, false,
-                                Clear{nullptr, 0}, lo.mask);
+                                Clear{nullptr, 0}, lo.mask, lo.drop);
   if (f.wd) {
     if (e == hipSuccess)
       e = launch_dequant(w->packed, w->qscale, w->scale2, w->offset, N * K, true, f.wd, st,
@@ -331,17 +369,27 @@ qn_status check_logits(const void* x, qn_dtype dtype, int64_t T, int64_t V, int6
   return QN_OK;
 }
 
-// The backward; the forward's input comes as x (bf16) or as x8 (an 8-bit
-// checkpoint, with u_saved).
-qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, const uint16_t* dY,
-                   int64_t M, const uint16_t* A, const uint16_t* B, int r, float alpha,
-                   const qn_lora_opts* opts, const float* u_saved, uint16_t* dX, float* dA,
-                   float* dB, void* workspace, size_t workspace_bytes, void* stream) {
-  qn_status s = check_linear(w, M, r);
-  if (s != QN_OK) return s;
-  Lora lo;
-  s = lora_options(opts, alpha, r, &lo);
-  if (s != QN_OK) return s;
+// The frozen weight of a backward: a 4-bit state with a codebook or MXFP4.
+struct Base {
+  const qn_nf4dq* w;
+  const qn_mx4* mx;
+  int64_t rows() const { return mx ? mx->rows : w->rows; }
+  int64_t cols() const { return mx ? mx->cols : w->cols; }
+  // its transpose in bf16, with the jobs of aux beside it
+  hipError_t dequant_t(uint16_t* out, int64_t ldt, const BwdAux& aux, hipStream_t st) const {
+    if (mx) return launch_mx4_dequant_t(to_mx4(mx), out, ldt, aux, st);
+    return launch_dequant_t(w->packed, w->qscale, w->scale2, w->offset, w->rows, w->cols, out, ldt,
+                            aux, st, w->codebook, w->absmax);
+  }
+};
+
+// The backward (base and r checked); the forward's input comes as x (bf16) or as x8
+// (an 8-bit checkpoint, with u_saved).  Under dropout from a counter its keep bits
+// are drawn again, into the call's workspace.
+qn_status backward(const Base& base, const uint16_t* x, const qn_act8* x8, const uint16_t* dY,
+                   int64_t M, const uint16_t* A, const uint16_t* B, int r, Lora lo,
+                   const float* u_saved, uint16_t* dX, float* dA, float* dB, void* workspace,
+                   size_t workspace_bytes, void* stream) {
   if (!A || !B || !dA || !dB) return QN_EINVAL;
   if (M > 0 && !dY) return QN_EINVAL;
   if (M > 0 && (x8 ? (!x8->codes || !x8->exps || !u_saved) : !x)) return QN_EINVAL;
@@ -349,7 +397,7 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
   if (!aligned16(x) || !aligned16(dY) || !aligned16(A) || !aligned16(B) || !aligned16(dA) ||
       !aligned16(dB) || (dX && !aligned16(dX)) || (u_saved && !aligned16(u_saved)))
     return QN_EALIGN;
-  const int64_t N = w->rows, K = w->cols;
+  const int64_t N = base.rows(), K = base.cols();
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (M == 0) {
     // empty batch: the gradients of the adapters are zero
@@ -358,14 +406,21 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
     return from_hip(e);
   }
   Carver probe(nullptr);
-  carve_bwd(probe, M, N, K, r, u_saved == nullptr, x8 != nullptr, dX != nullptr);
+  const bool always_dense = base.mx != nullptr;  // MXFP4 has no dequantizing product
+  carve_bwd(probe, M, N, K, r, u_saved == nullptr, x8 != nullptr, dX != nullptr, always_dense,
+            lo.drop.on);
   if (!workspace) return QN_EINVAL;
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return QN_EALIGN;
   if (workspace_bytes < probe.used) return QN_EWORKSPACE;
   Carver c(workspace);
-  BwdWs b = carve_bwd(c, M, N, K, r, u_saved == nullptr, x8 != nullptr, dX != nullptr);
+  BwdWs b = carve_bwd(c, M, N, K, r, u_saved == nullptr, x8 != nullptr, dX != nullptr,
+                      always_dense, lo.drop.on);
   const float scale = lo.s;
   hipError_t e = hipSuccess;
+  if (lo.drop.on) {
+    e = launch_keep_bits(M * K, lo.drop, b.bits, st);
+    lo.mask = b.bits;
+  }
   const float* u = u_saved;
   // an early launch of the call zeroes the arrival counters the adapter
   // gradients' launch counts on, so the backward never depends on what the
@@ -406,8 +461,7 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
     t.At = dense_dx ? b.At : nullptr;
     t.K = K;
     if (dense_dx)
-      e = launch_dequant_t(w->packed, w->qscale, w->scale2, w->offset, N, K, b.wt, b.ldt, t, st,
-                           w->codebook, w->absmax);
+      e = base.dequant_t(b.wt, b.ldt, t, st);
     else
       e = launch_bwd_aux(t, st);
     if (e == hipSuccess)
@@ -449,8 +503,7 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
     aux.r = r;
     aux.s = scale;
     if (dense_dx)
-      e = launch_dequant_t(w->packed, w->qscale, w->scale2, w->offset, N, K, b.wt, b.ldt, aux,
-                           st, w->codebook, w->absmax);
+      e = base.dequant_t(b.wt, b.ldt, aux, st);
     else
       e = launch_bwd_aux(aux, st);
   }
@@ -458,7 +511,7 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
     if (dense_dx)
       e = launch_gemm_nt(dY, N, N, b.wt, b.ldt, M, K, b.v, b.At, r, scale, dX, st, lo.mask);
     else
-      e = launch_qgemm_dx(to_state(w), dY, M, b.v, A, r, scale, dX, st, lo.mask);
+      e = launch_qgemm_dx(to_state(base.w), dY, M, b.v, A, r, scale, dX, st, lo.mask);
   }
   // dB = s G^T u and dA = s v^T X in one launch (and their slice sums in one)
   if (e == hipSuccess)
@@ -468,6 +521,41 @@ qn_status backward(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8, cons
                         M, r, arrivals, st);
   return from_hip(e);
 }
+
+// Sizes the linear calls on MXFP4 weights take: with an adapter those of the other
+// linear calls, without one any width.
+qn_status check_mx4(const qn_mx4* w, int64_t M, int r) {
+  if (!w || !w->codes || !w->scales) return QN_EINVAL;
+  if (w->rows < 1 || w->rows > kMaxDim || w->cols < 1 || w->cols > kMaxDim) return QN_EINVAL;
+  if (M < 0 || M > kMaxRowsM || r < 0 || r > 64) return QN_EINVAL;
+  if (r > 0 && (w->rows % 8 != 0 || w->cols % kBlock != 0)) return QN_EINVAL;
+  if (!aligned16(w->codes) || !aligned16(w->scales)) return QN_EALIGN;
+  return QN_OK;
+}
+
+struct Mx4Ws {
+  uint8_t* xc;   // x in MXFP4
+  uint8_t* xs;
+  float* u;      // [M, r] when the caller gives no u_out
+  float* upart;  // [S, M, r] when S > 1
+  int S;
+};
+Mx4Ws carve_mx4(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool need_u) {
+  Mx4Ws f;
+  c.take<unsigned>(kArrivalWords);  // left alone, as above
+  f.xc = c.take<uint8_t>((size_t)mx4_code_bytes(M, cols));
+  f.xs = c.take<uint8_t>((size_t)mx4_scale_bytes(M, cols));
+  f.S = r > 0 ? thin_nt_slices(M, cols) : 1;
+  f.u = need_u && r > 0 ? c.take<float>((size_t)M * r) : nullptr;
+  f.upart = f.S > 1 ? c.take<float>((size_t)f.S * M * r) : nullptr;
+  return f;
+}
+// the transposed bf16 copy of a backward without an adapter
+uint16_t* carve_mx4_dx(Carver& c, int64_t rows, int64_t cols) {
+  c.take<unsigned>(kArrivalWords);
+  return c.take<uint16_t>((size_t)cols * round_up(rows, 64));
+}
+constexpr int64_t kMaxElements = (int64_t)1 << 40;
 
 // Scratch of qlora_linear_fwd_noalloc: a file-scope device array, one copy
 // per GPU, held until the process ends.  Host code never passes its name to
@@ -644,7 +732,7 @@ qn_status qlora_linear_fwd_noalloc(const qn_nf4dq* w, const uint16_t* x, int64_t
   if (s != QN_OK) return s;
   // the array keeps what the last call left in it: its counters are cleared
   // by a kernel before the launch that counts on them
-  return forward(w, x, M, A, B, r, Lora{alpha / (float)r, nullptr}, y, u_out, ptr,
+  return forward(w, x, M, A, B, r, Lora{alpha / (float)r, nullptr, Drop{}}, y, u_out, ptr,
                  kStaticScratchBytes, stream, true);
 }
 
@@ -663,7 +751,11 @@ qn_status qlora_linear_bwd_ex(const qn_nf4dq* w, const uint16_t* x, const uint16
                               const qn_lora_opts* opts, const float* u_saved, uint16_t* dX,
                               float* dA, float* dB, void* workspace, size_t workspace_bytes,
                               void* stream) {
-  return backward(w, x, nullptr, dY, M, A, B, r, alpha, opts, u_saved, dX, dA, dB, workspace,
+  Lora lo;
+  qn_status s = check_linear(w, M, r);
+  if (s == QN_OK) s = lora_options(opts, alpha, r, &lo);
+  if (s != QN_OK) return s;
+  return backward(Base{w, nullptr}, x, nullptr, dY, M, A, B, r, lo, u_saved, dX, dA, dB, workspace,
                   workspace_bytes, stream);
 }
 
@@ -765,7 +857,11 @@ qn_status qlora_linear_bwd_act8(const qn_nf4dq* w, const qn_act8* x8, const uint
                                 uint16_t* dX, float* dA, float* dB, void* workspace,
                                 size_t workspace_bytes, void* stream) {
   if (!x8 && M != 0) return QN_EINVAL;
-  return backward(w, nullptr, x8, dY, M, A, B, r, alpha, opts, u, dX, dA, dB, workspace,
+  Lora lo;
+  qn_status s = check_linear(w, M, r);
+  if (s == QN_OK) s = lora_options(opts, alpha, r, &lo);
+  if (s != QN_OK) return s;
+  return backward(Base{w, nullptr}, nullptr, x8, dY, M, A, B, r, lo, u, dX, dA, dB, workspace,
                   workspace_bytes, stream);
 }
 
@@ -887,6 +983,172 @@ qn_status token_logprobs_bwd(const void* logits, qn_dtype dtype, int64_t T, int6
   return from_hip(launch_logprobs_bwd(logits, dtype == QN_F32, T, V, ld, targets, scale, stats,
                                       entropy, dlogp, dentropy, dlogits, ldd,
                                       static_cast<hipStream_t>(stream)));
+}
+
+// ---- dropout from a counter
+
+qn_status dropout_apply(const void* x, qn_dtype dtype, int64_t n, const qn_dropout* drop,
+                        void* out, void* stream) {
+  if ((dtype != QN_F32 && dtype != QN_BF16) || n < 0 || n > kMaxElements || !drop)
+    return QN_EINVAL;
+  Drop d;
+  float share;
+  qn_status s = drop_options(drop, &d, &share);
+  if (s != QN_OK || n == 0) return s;
+  if (!x || !out) return QN_EINVAL;
+  const uintptr_t mask = dtype == QN_F32 ? 3u : 1u;
+  if ((reinterpret_cast<uintptr_t>(x) & mask) || (reinterpret_cast<uintptr_t>(out) & mask))
+    return QN_EALIGN;
+  return from_hip(launch_dropout(x, dtype == QN_F32, n, d, 1.f / share, out,
+                                 static_cast<hipStream_t>(stream)));
+}
+
+size_t qlora_linear_drop_workspace(int64_t M, int64_t rows, int64_t cols, int r, int backward,
+                                   int act8) {
+  if (M < 0 || M > kMaxRowsM || rows < 1 || rows > kMaxDim || cols < 1 || cols > kMaxDim ||
+      r < 1 || r > 64)
+    return 0;
+  Carver c(nullptr);
+  if (backward)
+    carve_bwd(c, M, rows, cols, r, !act8, act8 != 0, true, false, true);
+  else
+    carve_fwd(c, M, rows, cols, r, true, true, true);
+  return c.used;
+}
+
+qn_status qlora_linear_fwd_drop(const qn_nf4dq* w, const uint16_t* x, int64_t M, const uint16_t* A,
+                                const uint16_t* B, int r, float alpha, int rslora,
+                                const qn_dropout* drop, uint16_t* y, float* u_out, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  if (r < 1 || r > 64) return QN_EINVAL;
+  Lora lo;
+  qn_status s = lora_drop_options(rslora, drop, alpha, r, &lo);
+  if (s != QN_OK) return s;
+  return forward(w, x, M, A, B, r, lo, y, u_out, workspace, workspace_bytes, stream, false);
+}
+
+qn_status qlora_linear_bwd_drop(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8,
+                                const uint16_t* dY, int64_t M, const uint16_t* A,
+                                const uint16_t* B, int r, float alpha, int rslora,
+                                const qn_dropout* drop, const float* u_saved, uint16_t* dX,
+                                float* dA, float* dB, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  qn_status s = check_linear(w, M, r);
+  if (s != QN_OK) return s;
+  if (M > 0 && (x == nullptr) == (x8 == nullptr)) return QN_EINVAL;
+  Lora lo;
+  s = lora_drop_options(rslora, drop, alpha, r, &lo);
+  if (s != QN_OK) return s;
+  return backward(Base{w, nullptr}, x, x8, dY, M, A, B, r, lo, u_saved, dX, dA, dB, workspace,
+                  workspace_bytes, stream);
+}
+
+// ---- MXFP4
+
+qn_status mx4_quantize(const void* x, qn_dtype dtype, int64_t rows, int64_t cols, uint8_t* codes,
+                       uint8_t* scales, void* stream) {
+  if (dtype != QN_F32 && dtype != QN_BF16) return QN_EINVAL;
+  if (rows < 0 || rows > kMaxRowsM || cols < 1 || cols > kMaxDim) return QN_EINVAL;
+  if (rows == 0) return QN_OK;
+  if (!x || !codes || !scales) return QN_EINVAL;
+  if (!aligned_rows(x, cols, dtype == QN_F32 ? 4 : 2) || !aligned16(codes) || !aligned16(scales))
+    return QN_EALIGN;
+  return from_hip(launch_mx4_quant(x, dtype == QN_F32, rows, cols, codes, scales,
+                                   static_cast<hipStream_t>(stream)));
+}
+
+qn_status mx4_dequantize(const qn_mx4* w, qn_dtype out_dtype, void* out, void* stream) {
+  if (out_dtype != QN_F32 && out_dtype != QN_BF16) return QN_EINVAL;
+  if (!w || w->rows < 0 || w->rows > kMaxRowsM || w->cols < 1 || w->cols > kMaxDim)
+    return QN_EINVAL;
+  if (w->rows == 0) return QN_OK;
+  if (!w->codes || !w->scales || !out) return QN_EINVAL;
+  if (!aligned16(w->codes) || !aligned16(w->scales) ||
+      !aligned_rows(out, w->cols, out_dtype == QN_F32 ? 4 : 2))
+    return QN_EALIGN;
+  return from_hip(launch_mx4_dequant(to_mx4(w), out_dtype == QN_F32, out,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+size_t mx4_linear_workspace(int64_t M, int64_t rows, int64_t cols, int r, int backward, int act8,
+                            int drop) {
+  if (M < 0 || M > kMaxRowsM || rows < 1 || rows > kMaxDim || cols < 1 || cols > kMaxDim ||
+      r < 0 || r > 64)
+    return 0;
+  Carver c(nullptr);
+  if (!backward)
+    carve_mx4(c, M, rows, cols, r, true);
+  else if (r == 0)
+    carve_mx4_dx(c, rows, cols);
+  else
+    carve_bwd(c, M, rows, cols, r, !act8, act8 != 0, true, true, drop != 0);
+  return c.used;
+}
+
+qn_status mx4_linear_fwd(const qn_mx4* w, const uint16_t* x, int64_t M, const uint16_t* A,
+                         const uint16_t* B, int r, float alpha, int rslora, const qn_dropout* drop,
+                         uint16_t* y, float* u_out, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  qn_status s = check_mx4(w, M, r);
+  if (s != QN_OK) return s;
+  Lora lo;
+  s = lora_drop_options(rslora, drop, alpha, r, &lo);
+  if (s != QN_OK) return s;
+  if (M == 0) return QN_OK;
+  if (!x || !y || (r > 0 && (!A || !B)) || (r == 0 && u_out)) return QN_EINVAL;
+  if (!aligned_rows(x, w->cols, 2) || !aligned_rows(y, w->rows, 2) || !aligned16(A) ||
+      !aligned16(B) || !aligned16(u_out))
+    return QN_EALIGN;
+  Carver probe(nullptr);
+  carve_mx4(probe, M, w->rows, w->cols, r, u_out == nullptr);
+  if (!workspace) return QN_EINVAL;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return QN_EALIGN;
+  if (workspace_bytes < probe.used) return QN_EWORKSPACE;
+  Carver c(workspace);
+  Mx4Ws f = carve_mx4(c, M, w->rows, w->cols, r, u_out == nullptr);
+  float* u = u_out ? u_out : f.u;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  hipError_t e = launch_mx4_quant(x, false, M, w->cols, f.xc, f.xs, st);
+  if (e == hipSuccess && r > 0)
+    e = launch_thin_nt(x, A, M, w->cols, r, u, f.upart, f.S, st, true, false, Clear{nullptr, 0},
+                       nullptr, lo.drop);
+  if (e == hipSuccess) e = launch_mx4_mm(to_mx4(w), f.xc, f.xs, M, u, B, r, lo.s, y, st);
+  return from_hip(e);
+}
+
+qn_status mx4_linear_bwd(const qn_mx4* w, const uint16_t* x, const qn_act8* x8,
+                         const uint16_t* dY, int64_t M, const uint16_t* A, const uint16_t* B,
+                         int r, float alpha, int rslora, const qn_dropout* drop,
+                         const float* u_saved, uint16_t* dX, float* dA, float* dB, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  qn_status s = check_mx4(w, M, r);
+  if (s != QN_OK) return s;
+  if (w->rows % 8 != 0 || w->cols % kBlock != 0) return QN_EINVAL;
+  Lora lo;
+  s = lora_drop_options(rslora, drop, alpha, r, &lo);
+  if (s != QN_OK) return s;
+  if (r > 0) {
+    if (M > 0 && (x == nullptr) == (x8 == nullptr)) return QN_EINVAL;
+    return backward(Base{nullptr, w}, x, x8, dY, M, A, B, r, lo, u_saved, dX, dA, dB, workspace,
+                    workspace_bytes, stream);
+  }
+  // no adapter: dX alone
+  if (M == 0) return QN_OK;
+  if (!dY || !dX) return QN_EINVAL;
+  if (!aligned16(dY) || !aligned16(dX)) return QN_EALIGN;
+  Carver probe(nullptr);
+  carve_mx4_dx(probe, w->rows, w->cols);
+  if (!workspace) return QN_EINVAL;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return QN_EALIGN;
+  if (workspace_bytes < probe.used) return QN_EWORKSPACE;
+  Carver c(workspace);
+  uint16_t* wt = carve_mx4_dx(c, w->rows, w->cols);
+  const int64_t N = w->rows, ldt = round_up(N, 64);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  hipError_t e = launch_mx4_dequant_t(to_mx4(w), wt, ldt, BwdAux{}, st);
+  if (e == hipSuccess)
+    e = launch_gemm_nt(dY, N, N, wt, ldt, M, w->cols, nullptr, nullptr, 0, 0.f, dX, st);
+  return from_hip(e);
 }
 
 }  // extern "C"

@@ -65,12 +65,12 @@ __device__ __forceinline__ void clear_words(const Clear& clr) {
 // the slice count as zero in both operands, and a lane whose chunk lies there
 // loads the slice's first columns instead (P is a multiple of 8): past the row
 // there may be the buffer's end, or, in a workspace, a NaN.  NJ = ceil(r/16).
-template <int NJ>
+template <int NJ, bool DROP>
 __global__ __launch_bounds__(kThreads) void k_thin_nt(const uint16_t* __restrict__ Z,
                                                       const uint16_t* __restrict__ T, int64_t M,
                                                       int64_t P, int r, int64_t slice,
                                                       float* __restrict__ out, Clear clr,
-                                                      const uint8_t* __restrict__ zmask) {
+                                                      const uint8_t* __restrict__ zmask, Drop d) {
   constexpr int U = NJ <= 2 ? 8 : 4;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   clear_words(clr);
@@ -84,6 +84,7 @@ __global__ __launch_bounds__(kThreads) void k_thin_nt(const uint16_t* __restrict
 #pragma unroll
   for (int jt = 0; jt < NJ; ++jt) tp[jt] = T + (int64_t)min(16 * jt + l16, r - 1) * P + pb + 8 * g;
   const int64_t lim = pe - pb - 8 * g;  // in-slice columns left for this lane's chunk
+  const uint64_t offset = DROP ? drop_offset(d) : 0;
   f32x4 acc[NJ] = {};
   for (int s0 = 0; s0 < steps; s0 += U) {
     u32x4 za[U], tb[U][NJ];
@@ -99,13 +100,17 @@ __global__ __launch_bounds__(kThreads) void k_thin_nt(const uint16_t* __restrict
       if (!ok) za[u] = u32x4{0u, 0u, 0u, 0u};
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      if constexpr (DROP)
+        za[u] = drop8(za[u], philox(d, offset, (uint64_t)(m * P + pb + 8 * g + 32 * (s0 + u)) >> 3),
+                      d.less);
 #pragma unroll
       for (int jt = 0; jt < NJ; ++jt) {
         u32x4 b = tb[u][jt];
         if (16 * jt + l16 >= r || 32 * (int64_t)(s0 + u) >= lim) b = u32x4{0u, 0u, 0u, 0u};
         acc[jt] = mfma16(as_bf16x8(za[u]), as_bf16x8(b), acc[jt]);
       }
+    }
   }
   // lane l: column j = 16jt + l%16, rows mw + 4(l/16) + i
   float* dst = out + (int64_t)blockIdx.y * M * r;
@@ -231,12 +236,13 @@ hipError_t launch_thin_v(const uint16_t* G, const uint16_t* Bf, int64_t M, int64
 // slice read as zero (selected at use, so no load waits at a branch).
 constexpr int TN1_U = 4;
 constexpr int64_t kThinNt1MaxSlice = 2048;
-template <int TMODE>
+template <int TMODE, bool DROP = false>
 __global__ __launch_bounds__(kThreads) void k_thin_nt1(const uint16_t* __restrict__ Z,
                                                        const uint16_t* __restrict__ T, int64_t M,
                                                        int64_t P, int r, int64_t slice,
                                                        float* __restrict__ out, Clear clr,
-                                                       const uint8_t* __restrict__ zmask) {
+                                                       const uint8_t* __restrict__ zmask,
+                                                       Drop d) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   clear_words(clr);
@@ -349,6 +355,8 @@ __global__ __launch_bounds__(kThreads) void k_thin_nt1(const uint16_t* __restric
   // LDS-only barrier: the first Z batch stays in flight
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   const uint8_t* trow = smem + l16 * pitch + 16 * g;
+  const uint64_t offset = DROP ? drop_offset(d) : 0;
+  const uint64_t block0 = (uint64_t)(m * P + pb + 8 * g) >> 3;  // of the lane's first chunk
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   auto compute_batch = [&](int buf, int b) {
 #pragma unroll
@@ -360,6 +368,7 @@ __global__ __launch_bounds__(kThreads) void k_thin_nt1(const uint16_t* __restric
           const uint32_t w = (u & 1) ? zk[buf][u >> 1].y : zk[buf][u >> 1].x;
           z = keep8(z, (w >> (8 * g)) & 0xffu);
         }
+        if constexpr (DROP) z = drop8(z, philox(d, offset, block0 + 4 * st), d.less);
         const u32x4 t = *reinterpret_cast<const u32x4*>(trow + 64 * st);
         acc = mfma16(as_bf16x8(z), as_bf16x8(t), acc);
       }
@@ -414,13 +423,14 @@ int thin_nt_slices(int64_t M, int64_t P) {
 
 hipError_t launch_thin_nt(const uint16_t* Z, const uint16_t* T, int64_t M, int64_t P, int r,
                           float* out, float* part, int S, hipStream_t st, bool sum, bool t_rows,
-                          Clear clr, const uint8_t* zmask) {
+                          Clear clr, const uint8_t* zmask, const Drop& d) {
   const int64_t slice = thin_nt_slice(P, S);
   const dim3 grid((unsigned)((M + 63) / 64), (unsigned)S);
   float* dst = S > 1 ? part : out;
   if (r <= 16 && slice <= kThinNt1MaxSlice) {
-    const int mode = !t_rows ? 0 : r == 16 ? 1 : 2;
-    static const hipError_t attr[3] = {
+    if (d.on && t_rows) return hipErrorInvalidValue;  // (T of a dropped Z is A, as rows)
+    const int mode = d.on ? 3 : !t_rows ? 0 : r == 16 ? 1 : 2;
+    static const hipError_t attr[4] = {
         hipFuncSetAttribute(reinterpret_cast<const void*>(k_thin_nt1<0>),
                             hipFuncAttributeMaxDynamicSharedMemorySize,
                             (int)(16 * (kThinNt1MaxSlice * 2 + 16))),
@@ -429,24 +439,33 @@ hipError_t launch_thin_nt(const uint16_t* Z, const uint16_t* T, int64_t M, int64
                             (int)(16 * (kThinNt1MaxSlice * 2 + 16))),
         hipFuncSetAttribute(reinterpret_cast<const void*>(k_thin_nt1<2>),
                             hipFuncAttributeMaxDynamicSharedMemorySize,
+                            (int)(16 * (kThinNt1MaxSlice * 2 + 16))),
+        hipFuncSetAttribute(reinterpret_cast<const void*>(k_thin_nt1<0, true>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize,
                             (int)(16 * (kThinNt1MaxSlice * 2 + 16)))};
     if (attr[mode] != hipSuccess) return attr[mode];
     const int steps = (int)((slice + 31) / 32);
     const size_t lds = (size_t)16 * (steps * 64 + 16);
     if (mode == 0)
-      hipLaunchKernelGGL(k_thin_nt1<0>, grid, dim3(kThreads), lds, st, Z, T, M, P, r, slice, dst, clr, zmask);
+      hipLaunchKernelGGL(k_thin_nt1<0>, grid, dim3(kThreads), lds, st, Z, T, M, P, r, slice, dst, clr, zmask, d);
+    else if (mode == 3)
+      hipLaunchKernelGGL((k_thin_nt1<0, true>), grid, dim3(kThreads), lds, st, Z, T, M, P, r, slice, dst, clr, zmask, d);
     else if (mode == 1)
-      hipLaunchKernelGGL(k_thin_nt1<1>, grid, dim3(kThreads), lds, st, Z, T, M, P, r, slice, dst, clr, zmask);
+      hipLaunchKernelGGL(k_thin_nt1<1>, grid, dim3(kThreads), lds, st, Z, T, M, P, r, slice, dst, clr, zmask, d);
     else
-      hipLaunchKernelGGL(k_thin_nt1<2>, grid, dim3(kThreads), lds, st, Z, T, M, P, r, slice, dst, clr, zmask);
+      hipLaunchKernelGGL(k_thin_nt1<2>, grid, dim3(kThreads), lds, st, Z, T, M, P, r, slice, dst, clr, zmask, d);
   } else {
     if (t_rows) return hipErrorInvalidValue;  // the general kernel takes T as [r, P]
-  switch ((r + 15) / 16) {
-    case 1: hipLaunchKernelGGL(k_thin_nt<1>, grid, dim3(kThreads), 0, st, Z, T, M, P, r, slice, dst, clr, zmask); break;
-    case 2: hipLaunchKernelGGL(k_thin_nt<2>, grid, dim3(kThreads), 0, st, Z, T, M, P, r, slice, dst, clr, zmask); break;
-    case 3: hipLaunchKernelGGL(k_thin_nt<3>, grid, dim3(kThreads), 0, st, Z, T, M, P, r, slice, dst, clr, zmask); break;
-    default: hipLaunchKernelGGL(k_thin_nt<4>, grid, dim3(kThreads), 0, st, Z, T, M, P, r, slice, dst, clr, zmask); break;
-  }
+#define QN_NT(NJ, DROP)                                                                      \
+  hipLaunchKernelGGL((k_thin_nt<NJ, DROP>), grid, dim3(kThreads), 0, st, Z, T, M, P, r, slice, dst, \
+                     clr, zmask, d)
+    switch ((r + 15) / 16) {
+      case 1: if (d.on) QN_NT(1, true); else QN_NT(1, false); break;
+      case 2: if (d.on) QN_NT(2, true); else QN_NT(2, false); break;
+      case 3: if (d.on) QN_NT(3, true); else QN_NT(3, false); break;
+      default: if (d.on) QN_NT(4, true); else QN_NT(4, false); break;
+    }
+#undef QN_NT
   }
   if (S > 1 && sum) {
     const int64_t count = M * r;

@@ -189,4 +189,86 @@ __device__ __forceinline__ uint32_t max_of_8_lanes(uint32_t x) {
   return reduce_8_lanes(x, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 
+// ---- Dropout without a stored mask.  Philox 4x32 with ten rounds (Salmon, Moraes,
+// Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC 2011): the
+// counter (block, offset) under the key (seed) gives four words; block b holds the
+// elements 8b .. 8b + 7 of the row-major tensor, element 8b + 2i and 8b + 2i + 1 the
+// low and the high half of word i, and an element is dropped where its half is less
+// than the threshold (p 2^16).  Ten rounds are twenty 32 x 32 -> 64 bit products
+// (a quarter of the vector rate each) and forty exclusive ors for eight elements:
+// about 480 issue cycles for 512 elements of a wave.
+struct Drop {
+  uint32_t key0 = 0, key1 = 0;     // the seed
+  uint64_t offset = 0;             // what tells the uses of one seed apart ...
+  const uint64_t* step = nullptr;  // ... and a number on the device added to it, or null
+  uint32_t less = 0;               // threshold - 1; only used where drop is on
+  bool on = false;
+};
+__device__ __forceinline__ uint64_t drop_offset(const Drop& d) {
+  return d.offset + (d.step ? *d.step : 0u);
+}
+__device__ __forceinline__ u32x4 philox(const Drop& d, uint64_t offset, uint64_t block) {
+  uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32);
+  uint32_t c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
+  uint32_t k0 = d.key0, k1 = d.key1;
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const uint64_t p = (uint64_t)c0 * 0xD2511F53u, q = (uint64_t)c2 * 0xCD9E8D57u;
+    c0 = (uint32_t)(q >> 32) ^ c1 ^ k0;
+    c1 = (uint32_t)q;
+    c2 = (uint32_t)(p >> 32) ^ c3 ^ k1;
+    c3 = (uint32_t)p;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return u32x4{c0, c1, c2, c3};
+}
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+// 1 in each half of w that lets its element through: w - less, held to 0 .. 1.
+__device__ __forceinline__ u16x2 kept(uint32_t w, uint32_t less) {
+  const unsigned short l = (unsigned short)less;
+  return __builtin_elementwise_min(
+      __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, w), u16x2{l, l}), u16x2{1, 1});
+}
+// eight 16-bit values with the dropped ones zeroed
+__device__ __forceinline__ u32x4 drop8(u32x4 v, u32x4 words, uint32_t less) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    v[q] &= __builtin_bit_cast(uint32_t, (u16x2)(u16x2{0, 0} - kept(words[q], less)));
+  return v;
+}
+// the eight keep bits as a mask's byte
+__device__ __forceinline__ uint32_t keep_byte(u32x4 words, uint32_t less) {
+  uint32_t b = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t k = __builtin_bit_cast(uint32_t, kept(words[q], less));
+    b |= ((k | (k >> 15)) & 3u) << (2 * q);
+  }
+  return b;
+}
+
+// ---- MXFP4 (format in the header): 32 columns of a row share the scale 2^(E-127).
+constexpr int kMx4Block = 32;
+constexpr int kMx4Step = 256;     // columns of a step: 128 bytes of codes, 8 scales
+constexpr uint32_t kMx4NaN = 255;  // E of a block with a NaN or an infinity
+// E from the largest magnitude of a block (fp32 bits): two powers of two below it
+__device__ __forceinline__ uint32_t mx4_exp(uint32_t absmax_bits) {
+  const uint32_t ex = absmax_bits >> 23;
+  return ex == 255u ? kMx4NaN : ex > 2u ? ex - 2u : 0u;
+}
+// what a value is multiplied by before it becomes a code, and back (exact: powers of
+// two; a block of no numbers has codes of zero)
+__device__ __forceinline__ float mx4_inv(uint32_t E) {
+  return E == kMx4NaN ? 0.f : as_f32((254u - E) << 23);
+}
+__device__ __forceinline__ float mx4_scale(uint32_t E) {
+  return as_f32(E == kMx4NaN ? 0x7fc00000u : E ? E << 23 : 0x00400000u);
+}
+// byte of row n (of 32) and block b (of 8) in a step's 256 scale bytes: lane
+// 16 (b % 4) + n % 16 takes four, byte 2 (n / 16) + b / 4
+__host__ __device__ constexpr int mx4_scale_at(int n, int b) {
+  return 4 * (16 * (b & 3) + (n & 15)) + 2 * (n >> 4) + (b >> 2);
+}
+
 }  // namespace qn

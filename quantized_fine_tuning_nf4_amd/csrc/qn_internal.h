@@ -265,11 +265,11 @@ struct WState {
 // T is given as its transpose [P, r] (r <= 16 only).  clr: words the first
 // workgroup zeroes.  zmask (nullable): Z's elements whose bit is clear read
 // as zero (bit-packed over the row-major elements, bit e % 8 of byte e / 8;
-// P % 8 == 0).
+// P % 8 == 0).  d: the same by keep bits that the kernel draws (T as rows only).
 hipError_t launch_thin_nt(const uint16_t* Z, const uint16_t* T, int64_t M, int64_t P, int r,
                           float* out, float* part, int S, hipStream_t st, bool sum = true,
                           bool t_rows = false, Clear clr = Clear{nullptr, 0},
-                          const uint8_t* zmask = nullptr);
+                          const uint8_t* zmask = nullptr, const Drop& d = Drop{});
 
 // fp32 scalars of one 8-bit AdamW step (the 1 - b, bias corrections and
 // decay formed on the host).
@@ -409,5 +409,35 @@ hipError_t launch_logprobs_bwd(const void* x, bool f32, int64_t T, int64_t V, in
                                const int64_t* targets, float scale, const float* stats,
                                const float* entropy, const float* dlogp, const float* dent,
                                void* dx, int64_t ldd, hipStream_t st);
+
+// Dropout from a counter (qn_device.h): out = x scale where kept, else 0, over n
+// elements of bf16 or fp32 (out may be x), and the keep bits of n elements
+// (n % 32 == 0), bit e % 8 of byte e / 8.
+hipError_t launch_dropout(const void* x, bool f32, int64_t n, const Drop& d, float scale,
+                          void* out, hipStream_t st);
+hipError_t launch_keep_bits(int64_t n, const Drop& d, uint8_t* bits, hipStream_t st);
+
+// MXFP4 (format in the header).
+struct Mx4 {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t rows, cols;
+};
+inline int64_t mx4_steps(int64_t cols) { return (cols + kMx4Step - 1) / kMx4Step; }
+inline int64_t mx4_code_bytes(int64_t rows, int64_t cols) { return rows * 128 * mx4_steps(cols); }
+inline int64_t mx4_scale_bytes(int64_t rows, int64_t cols) {
+  return (rows + 31) / 32 * 256 * mx4_steps(cols);
+}
+hipError_t launch_mx4_quant(const void* x, bool f32, int64_t rows, int64_t K, uint8_t* codes,
+                            uint8_t* scales, hipStream_t st);
+hipError_t launch_mx4_dequant(const Mx4& w, bool f32, void* out, hipStream_t st);
+// out[k][n] = W[n][k] as bf16, row length ldt (ldt % 32 == 0, ldt >= rows; zero for
+// rows <= n < ldt).  The jobs of aux run in extra workgroups of the same launch.
+hipError_t launch_mx4_dequant_t(const Mx4& w, uint16_t* out, int64_t ldt, const BwdAux& aux,
+                                hipStream_t st);
+// y [M, rows] bf16 = x W^T + s u B^T, x [M, cols] in MXFP4; r == 0: no second term.
+hipError_t launch_mx4_mm(const Mx4& w, const uint8_t* xc, const uint8_t* xs, int64_t M,
+                         const float* u, const uint16_t* B, int r, float s, uint16_t* y,
+                         hipStream_t st);
 
 }  // namespace qn

@@ -128,7 +128,8 @@ def act8_unpack(x8: Act8, out: torch.Tensor | None = None) -> torch.Tensor:
 def qlora_linear_bwd_act8(st: NF4State, x8: Act8, dY: torch.Tensor, A: torch.Tensor,
                           B: torch.Tensor, alpha: float, u: torch.Tensor, need_dx: bool = True,
                           workspace: torch.Tensor | None = None, rslora: bool = False,
-                          dropout_mask: torch.Tensor | None = None, dropout_p: float = 0.0):
+                          dropout_mask: torch.Tensor | None = None, dropout_p: float = 0.0,
+                          drop=None):
     """qlora_linear_bwd with the forward's input kept as an 8-bit checkpoint
     and u the forward's saved u.  Returns (dX bf16 [M, d_in] or None,
     dA fp32 [r, d_in], dB fp32 [d_out, r])."""
@@ -151,6 +152,20 @@ def qlora_linear_bwd_act8(st: NF4State, x8: Act8, dY: torch.Tensor, A: torch.Ten
     dX = torch.empty(M, st.cols, dtype=torch.bfloat16, device=dev) if need_dx else None
     dA = torch.empty(r, st.cols, dtype=torch.float32, device=dev)
     dB = torch.empty(st.rows, r, dtype=torch.float32, device=dev)
+    if drop is not None:
+        from . import _one_dropout, _qlora_bwd_drop
+        _one_dropout(dropout_mask, dropout_p)
+        rc = _qlora_bwd_drop(st, None, x8, dY, A, B, r, alpha, rslora, drop, u, dX, dA, dB,
+                             workspace)
+        if rc:
+            again = _aligned(rc, x8.codes, x8.exps, dY, A, B, u)
+            if not again:
+                _check(rc)
+            codes, exps, dY, A, B, u = again
+            return qlora_linear_bwd_act8(st, Act8(codes, exps), dY, A, B, alpha, u,
+                                         need_dx=need_dx, workspace=workspace, rslora=rslora,
+                                         drop=drop)
+        return dX, dA, dB
     o = _opts(rslora, dropout_mask, dropout_p)
     need = L.qlora_linear_bwd_act8_workspace(M, st.rows, st.cols, r, int(need_dx))
     if workspace is None or workspace.numel() < need:
