@@ -1,6 +1,8 @@
 // MXFP4: matrices in 4 bits with a power-of-two scale for every 32 columns of a row
 // (format in the header), into the format and back, and the linear's product on two
 // of them with the adapter term.
+#include <type_traits>
+
 #include "qn_device.h"
 #include "qn_internal.h"
 
@@ -210,6 +212,317 @@ __global__ __launch_bounds__(kThreads) void k_mx4_mm(
   }
 }
 
+// ---- The product of many rows.  Workgroup tile 64 WM x 64 WN (rows of x, rows of W), four
+// waves (2 x 2) of 32 WM x 32 WN as WM x WN tiles of v_mfma_scale_f32_32x32x64_f8f6f4.
+// A step is 256 columns: rows of 128 bytes of codes and 256 scale bytes per 32 rows go
+// from global memory straight into LDS, two stages deep.  Chunk c (16 bytes, a block) of
+// row y sits at unit c ^ ((y >> 1) & 7), so that 16 rows of a fragment read sit on
+// distinct banks.  In the step's product t of four, lane (h, n) = (l / 32, l % 32) takes
+// row n's block 2 h + t % 2 + 4 (t / 2): its four scales are two 16-bit pieces of the
+// stored order.
+template <int WM, int WN>
+struct MxGeo {
+  static constexpr int BM = 64 * WM, BN = 64 * WN;
+  static constexpr int XB = BM * 128, WB = BN * 128;                // codes of a stage
+  static constexpr int XS = XB + WB, WS = XS + BM * 8;              // its scales
+  static constexpr int STB = WS + BN * 8;                           // bytes of a stage
+  static constexpr int OUTP = 64 * WN + 16, OUTW = 32 * WM * OUTP;  // output staging of a wave
+  static constexpr int LDS_MAIN = 2 * STB > 4 * OUTW ? 2 * STB : 4 * OUTW;
+  static constexpr int LDS_V = LDS_MAIN, LDS_L = LDS_V + BM * 64;   // r == 16: u and B of the tile
+  static constexpr int LDS_BYTES = LDS_L + BN * 32;
+  static constexpr int LPS = 2 * WM + 2 * WN + 1;                   // loads of a wave and step
+  static_assert(LDS_BYTES <= 160 * 1024, "LDS");
+};
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ rsrc_t make_rs(const void* base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  const uint64_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+  const uint64_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(lo | (hi << 32)), 0,
+                                           __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
+}
+__device__ __forceinline__ void dma16(rsrc_t rs, uint32_t voff, uint32_t soff, uint8_t* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)lds, 16, voff, soff, 0, 0);
+}
+__device__ __forceinline__ void barrier_lds() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+__device__ __forceinline__ i32x8 frag4(u32x4 v) {
+  return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+}
+
+template <int WM, int WN, bool LORA16>
+__global__ __launch_bounds__(kThreads, 1) void k_mx4_gemm(
+    const uint8_t* __restrict__ wc, const uint8_t* __restrict__ ws,
+    const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs, int64_t M, int64_t N, int J,
+    const float* __restrict__ V, const uint16_t* __restrict__ L, int r, float s,
+    uint16_t* __restrict__ y, int tiles_m, int tiles_n) {
+  using G = MxGeo<WM, WN>;
+  constexpr int BM = G::BM, BN = G::BN, STB = G::STB;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 1, wn = wave & 1;
+
+  // tile order: each XCD (they take workgroups round robin) a contiguous run of the
+  // tiles, four tile rows at a time across the columns
+  int bid = blockIdx.x;
+  const int ntiles = tiles_m * tiles_n;
+  if (ntiles % 8 == 0) bid = (bid & 7) * (ntiles >> 3) + (bid >> 3);
+  int tm, tn;
+  if (tiles_m % 4 == 0) {
+    const int grp = bid / (4 * tiles_n), in = bid % (4 * tiles_n);
+    tm = 4 * grp + (in & 3);
+    tn = in >> 2;
+  } else {
+    tm = bid / tiles_n;
+    tn = bid % tiles_n;
+  }
+  tm = __builtin_amdgcn_readfirstlane(tm);
+  tn = __builtin_amdgcn_readfirstlane(tn);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  const int mrows = (int)min((int64_t)BM, M - m0), nrows = (int)min((int64_t)BN, N - n0);
+  const int pitch = 128 * J;
+
+  // loads: instruction i of wave w covers rows 8 (2 W w + i) + l / 8 (rows past the matrix
+  // repeat its last one: nothing of them is stored)
+  const rsrc_t rx = make_rs(xc + m0 * pitch, (uint32_t)(mrows * pitch));
+  const rsrc_t rw = make_rs(wc + n0 * pitch, (uint32_t)(nrows * pitch));
+  uint32_t xoff[2 * WM], woff[2 * WN];
+#pragma unroll
+  for (int i = 0; i < 2 * WM; ++i) {
+    const int row = 8 * (2 * WM * wave + i) + (lane >> 3);
+    xoff[i] = (uint32_t)(min(row, mrows - 1) * pitch + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
+  }
+#pragma unroll
+  for (int i = 0; i < 2 * WN; ++i) {
+    const int row = 8 * (2 * WN * wave + i) + (lane >> 3);
+    woff[i] = (uint32_t)(min(row, nrows - 1) * pitch + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
+  }
+  // scales: 1 KB (four groups of 32 rows) an instruction, those of x then those of W;
+  // with half as many as waves the upper waves load the same again
+  constexpr int SQ = (2 * WM + 2 * WN) / 4;
+  const int sq = wave % SQ;
+  const bool sx = sq < WM / 2;
+  const int sg = 4 * (sx ? sq : sq - WM / 2) + (lane >> 4);  // group of the tile
+  const int sgroups = ((sx ? mrows : nrows) + 31) >> 5;
+  const rsrc_t rs = make_rs(sx ? xs + m0 / 32 * J * 256 : ws + n0 / 32 * J * 256,
+                            (uint32_t)(sgroups * J * 256));
+  const uint32_t soff = (uint32_t)(min(sg, sgroups - 1) * J * 256 + 16 * (lane & 15));
+  auto load_one = [&](int q, int st, int stage) {
+    uint8_t* base = smem + stage * STB;
+    const uint32_t so = (uint32_t)st * 128;
+    if (q < 2 * WM)
+      dma16(rx, xoff[q], so, base + 1024 * (2 * WM * wave + q));
+    else if (q < 2 * WM + 2 * WN)
+      dma16(rw, woff[q - 2 * WM], so, base + G::XB + 1024 * (2 * WN * wave + q - 2 * WM));
+    else
+      dma16(rs, soff, 2 * so, base + G::XS + 1024 * sq);
+  };
+
+  // fragment reads
+  const int n = lane & 31, h = lane >> 5;
+  int roff[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+    roff[t] = n * 128 + 16 * ((2 * h + (t & 1) + 4 * (t >> 1)) ^ ((n >> 1) & 7));
+  const int xbase = wm * 32 * WM * 128, wbase = G::XB + wn * 32 * WN * 128;
+  const int xsb = G::XS + wm * WM * 256, wsb = G::WS + wn * WN * 256;
+  const int so0 = 4 * (32 * h + (n & 15)) + 2 * (n >> 4);
+  auto frag = [&](int stage, int base, int g, int t) {
+    return *reinterpret_cast<const u32x4*>(smem + stage * STB + base + g * 4096 + roff[t]);
+  };
+  auto scale = [&](int stage, int base, int g) {
+    const uint8_t* p = smem + stage * STB + base + g * 256 + so0;
+    return (int)((uint32_t)*reinterpret_cast<const uint16_t*>(p) |
+                 ((uint32_t)*reinterpret_cast<const uint16_t*>(p + 64) << 16));
+  };
+
+  f32x16 acc[WM][WN];
+#pragma unroll
+  for (int i = 0; i < WM; ++i)
+#pragma unroll
+    for (int j = 0; j < WN; ++j) acc[i][j] = f32x16{};
+  u32x4 fx[2][WM], fw[2][WN];
+  int ex[2][WM], ew[2][WN];
+
+  if constexpr (LORA16) {  // u and B of the tile (rows past it read zeros)
+    const rsrc_t rv = make_rs(V + m0 * 16, (uint32_t)(mrows * 64));
+    const rsrc_t rl = make_rs(L + n0 * 16, (uint32_t)(nrows * 32));
+#pragma unroll
+    for (int k = 0; k < WM; ++k) {
+      const int q = WM * wave + k;
+      dma16(rv, (uint32_t)(1024 * q + 16 * lane), 0, smem + G::LDS_V + 1024 * q);
+    }
+#pragma unroll
+    for (int k = 0; k < (2 * WN + 3) / 4; ++k) {
+      const int q = 4 * k + wave;
+      if (q < 2 * WN) dma16(rl, (uint32_t)(1024 * q + 16 * lane), 0, smem + G::LDS_L + 1024 * q);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int q = 0; q < G::LPS; ++q) load_one(q, min(k, J - 1), k);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(G::LPS) : "memory");
+  barrier_lds();
+#pragma unroll
+  for (int i = 0; i < WM; ++i) {
+    fx[0][i] = frag(0, xbase, i, 0);
+    ex[0][i] = scale(0, xsb, i);
+  }
+#pragma unroll
+  for (int j = 0; j < WN; ++j) {
+    fw[0][j] = frag(0, wbase, j, 0);
+    ew[0][j] = scale(0, wsb, j);
+  }
+
+  // product t of step st on stage P = st % 2.  The fragments of the next product are read
+  // while this one's run; before the last product every wave has read the stage and
+  // step st + 1 has landed; the loads of step st + 2 then go into the stage.
+  auto product = [&](auto p_t, auto t_t, int st) {
+    constexpr int P = decltype(p_t)::value, TT = decltype(t_t)::value;
+    constexpr int C = TT & 1, RS = TT == 3 ? P ^ 1 : P, RT = (TT + 1) & 3;
+    constexpr int OP = 2 * (TT & 1) + (TT >> 1);
+    const int lst = min(st + 2, J - 1);
+#pragma unroll
+    for (int i = 0; i < WM; ++i) {
+#pragma unroll
+      for (int j = 0; j < WN; ++j) {
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            frag4(fw[C][j]), frag4(fx[C][i]), acc[i][j], 4, 4, OP, ew[P][j], OP, ex[P][i]);
+        if (i == 0) {
+          fw[C ^ 1][j] = frag(RS, wbase, j, RT);
+          if (TT == 3) ew[P ^ 1][j] = scale(RS, wsb, j);
+        }
+        if (i == 1) {
+          if (j < WM) fx[C ^ 1][j] = frag(RS, xbase, j, RT);
+          if (TT == 3 && j < WM) ex[P ^ 1][j] = scale(RS, xsb, j);
+        }
+        if (TT == 3) {
+          constexpr int PER = (G::LPS + WM * WN - 1) / (WM * WN);
+#pragma unroll
+          for (int k = 0; k < PER; ++k)
+            if (PER * (WN * i + j) + k < G::LPS) load_one(PER * (WN * i + j) + k, lst, P);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (TT == 2) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      barrier_lds();
+    }
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  using I3 = std::integral_constant<int, 3>;
+  auto step = [&](auto p_t, int st) {
+    product(p_t, I0{}, st);
+    product(p_t, I1{}, st);
+    product(p_t, I2{}, st);
+    product(p_t, I3{}, st);
+  };
+  int st = 0;
+  for (; st + 2 <= J; st += 2) {
+    step(I0{}, st);
+    step(I1{}, st + 1);
+  }
+  if (st < J) step(I0{}, st);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  barrier_lds();
+
+  // the adapter: acc += B (s u)^T, s u as a bf16 high part and a remainder, 16 ranks a
+  // product (lane half h: ranks 8 h .. 8 h + 7)
+  for (int j0 = 0; j0 < r; j0 += 16) {
+    const int jl = j0 + 8 * h;
+    bf16x8 lb[WN];
+#pragma unroll
+    for (int j = 0; j < WN; ++j) {
+      if constexpr (LORA16) {
+        lb[j] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(
+            smem + G::LDS_L + (32 * (WN * wn + j) + n) * 32 + 16 * h));
+      } else {
+        const uint16_t* lp = L + min(n0 + 32 * (WN * wn + j) + n, N - 1) * r;
+        uint32_t e[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) e[q] = jl + q < r ? lp[min(jl + q, r - 1)] : 0u;
+        lb[j] = __builtin_bit_cast(bf16x8, u32x4{e[0] | (e[1] << 16), e[2] | (e[3] << 16),
+                                                 e[4] | (e[5] << 16), e[6] | (e[7] << 16)});
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < WM; ++i) {
+      float v[8];
+      if constexpr (LORA16) {
+        const uint8_t* vp = smem + G::LDS_V + (32 * (WM * wm + i) + n) * 64 + 32 * h;
+        const f32x4 a = *reinterpret_cast<const f32x4*>(vp);
+        const f32x4 b = *reinterpret_cast<const f32x4*>(vp + 16);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          v[q] = a[q];
+          v[4 + q] = b[q];
+        }
+      } else {
+        const float* vp = V + min(m0 + 32 * (WM * wm + i) + n, M - 1) * r;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = jl + q < r ? vp[min(jl + q, r - 1)] : 0.f;
+      }
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float a = s * v[2 * q], b = s * v[2 * q + 1];
+        hi[q] = pack_bf16x2(a, b);
+        lo[q] = pack_bf16x2(a - bf16_lo(hi[q]), b - bf16_hi(hi[q]));
+      }
+      const bf16x8 vh = __builtin_bit_cast(bf16x8, u32x4{hi[0], hi[1], hi[2], hi[3]});
+      const bf16x8 vl = __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], lo[2], lo[3]});
+#pragma unroll
+      for (int j = 0; j < WN; ++j) {
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lb[j], vh, acc[i][j], 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lb[j], vl, acc[i][j], 0, 0, 0);
+      }
+    }
+  }
+
+  // store: lane (h, n) holds row n of tile (i, j), columns 8 q + 4 h + 0 .. 3 in its
+  // registers 4 q ..; through the wave's LDS staging tile, which leaves as rows of 64 WN
+  // bytes
+  uint8_t* stg = smem + wave * G::OUTW;
+#pragma unroll
+  for (int i = 0; i < WM; ++i)
+#pragma unroll
+    for (int j = 0; j < WN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<u32x2*>(stg + (32 * i + n) * G::OUTP + 2 * (32 * j + 8 * q + 4 * h)) =
+            u32x2{pack_bf16x2(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
+                  pack_bf16x2(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3])};
+  // (a wave's LDS accesses execute in order)
+  constexpr int LR = 4 * WN, RPS = 64 / LR;  // lanes of a row, rows a store
+  const int lc = lane % LR;
+  const int64_t col = n0 + 32 * WN * wn + 8 * lc;
+  const bool whole = (N & 7) == 0;
+#pragma unroll
+  for (int q = 0; q < 32 * WM / RPS; ++q) {
+    const int rl = RPS * q + lane / LR;
+    const int64_t row = m0 + 32 * WM * wm + rl;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(stg + rl * G::OUTP + 16 * lc);
+    if (row >= M || col >= N) continue;
+    uint16_t* dst = y + row * N + col;
+    if (whole) {
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(dst));
+    } else if (col + 8 <= N) {
+      *reinterpret_cast<u32x4_any*>(dst) = v;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (col + k < N) dst[k] = (uint16_t)(v[k >> 1] >> (16 * (k & 1)));
+    }
+  }
+}
+
 // out[k][n] = W[n][k] as bf16, row length ldt (zero for rows <= n < ldt).  A
 // workgroup takes 32 rows x 256 columns as above, through LDS.
 __global__ __launch_bounds__(kThreads) void k_mx4_dequant_t(
@@ -289,9 +602,42 @@ hipError_t launch_mx4_dequant_t(const Mx4& w, uint16_t* out, int64_t ldt, const 
   return hipGetLastError();
 }
 
+namespace {
+template <int WM, int WN>
+hipError_t launch_tiles(const Mx4& w, const uint8_t* xc, const uint8_t* xs, int64_t M,
+                        const float* u, const uint16_t* B, int r, float s, uint16_t* y,
+                        hipStream_t st) {
+  using G = MxGeo<WM, WN>;
+  static const hipError_t attr = [] {
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_mx4_gemm<WM, WN, true>),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, G::LDS_BYTES);
+    return e != hipSuccess
+               ? e
+               : hipFuncSetAttribute(reinterpret_cast<const void*>(k_mx4_gemm<WM, WN, false>),
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, G::LDS_MAIN);
+  }();
+  if (attr != hipSuccess) return attr;
+  const int64_t tm = (M + G::BM - 1) / G::BM, tn = (w.rows + G::BN - 1) / G::BN;
+  const dim3 grid((unsigned)(tm * tn));
+  const int J = (int)mx4_steps(w.cols);
+  if (r == 16)
+    hipLaunchKernelGGL((k_mx4_gemm<WM, WN, true>), grid, dim3(kThreads), G::LDS_BYTES, st, w.codes,
+                       w.scales, xc, xs, M, w.rows, J, u, B, r, s, y, (int)tm, (int)tn);
+  else
+    hipLaunchKernelGGL((k_mx4_gemm<WM, WN, false>), grid, dim3(kThreads), G::LDS_MAIN, st, w.codes,
+                       w.scales, xc, xs, M, w.rows, J, u, B, r, s, y, (int)tm, (int)tn);
+  return hipGetLastError();
+}
+}  // namespace
+
 hipError_t launch_mx4_mm(const Mx4& w, const uint8_t* xc, const uint8_t* xs, int64_t M,
                          const float* u, const uint16_t* B, int r, float s, uint16_t* y,
                          hipStream_t st) {
+  if (M > 64) {
+    if ((M + 255) / 256 * ((w.rows + 255) / 256) >= 240)
+      return launch_tiles<4, 4>(w, xc, xs, M, u, B, r, s, y, st);
+    return launch_tiles<2, 2>(w, xc, xs, M, u, B, r, s, y, st);
+  }
   const uint32_t cols_wgs = (uint32_t)((w.rows + 127) / 128);
   const dim3 grid(cols_wgs * (uint32_t)((M + 31) / 32));  // (at most 2^31)
   hipLaunchKernelGGL(k_mx4_mm, grid, dim3(kThreads), 0, st, w.codes, w.scales, xc, xs, M, w.rows,

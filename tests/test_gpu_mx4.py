@@ -134,7 +134,8 @@ def _check(got, want, tol, name):
 # M, rows, cols, r: no adapter at odd sizes, then ranks of one block of 16 and several,
 # tiles that end inside, one row, few and many
 PLAIN = [(1, 1, 1), (1, 5, 33), (3, 17, 100), (16, 64, 256), (17, 31, 1000), (33, 257, 511),
-         (100, 130, 2048), (128, 128, 64), (129, 129, 300), (300, 1001, 129), (256, 512, 4096)]
+         (100, 130, 2048), (128, 128, 64), (129, 129, 300), (300, 1001, 129), (256, 512, 4096),
+         (65, 33, 4000), (4001, 4099, 300), (3841, 4096, 1025)]
 
 
 @pytest.mark.parametrize("M,rows,cols", PLAIN)
@@ -151,7 +152,8 @@ def test_product(qn, M, rows, cols):
 
 
 ADAPTED = [(1, 8, 64, 1), (2, 64, 128, 16), (16, 72, 192, 5), (31, 136, 320, 17), (40, 256, 1024, 64),
-           (130, 264, 576, 16), (257, 512, 832, 33), (1, 1024, 4096, 16), (520, 768, 2048, 8)]
+           (130, 264, 576, 16), (257, 512, 832, 33), (1, 1024, 4096, 16), (520, 768, 2048, 8),
+           (4000, 4104, 320, 16), (3841, 4000, 832, 40)]
 
 
 def _linear(qn, M, rows, cols, r, seed=0):
