@@ -212,26 +212,28 @@ __global__ __launch_bounds__(kThreads) void k_mx4_mm(
   }
 }
 
-// ---- The product of many rows.  Workgroup tile 64 WM x 64 WN (rows of x, rows of W), four
-// waves (2 x 2) of 32 WM x 32 WN as WM x WN tiles of v_mfma_scale_f32_32x32x64_f8f6f4.
-// A step is 256 columns: rows of 128 bytes of codes and 256 scale bytes per 32 rows go
-// from global memory straight into LDS, two stages deep.  Chunk c (16 bytes, a block) of
-// row y sits at unit c ^ ((y >> 1) & 7), so that 16 rows of a fragment read sit on
-// distinct banks.  In the step's product t of four, lane (h, n) = (l / 32, l % 32) takes
-// row n's block 2 h + t % 2 + 4 (t / 2): its four scales are two 16-bit pieces of the
-// stored order.
-template <int WM, int WN>
+// ---- The product of many rows.  Workgroup tile BM x BN (rows of x, rows of W), WVM x WVN
+// waves of TM x TN tiles of v_mfma_scale_f32_16x16x128_f8f6f4.  A step is 256 columns:
+// rows of 128 bytes of codes and 256 scale bytes per 32 rows go from global memory
+// straight into LDS, two stages deep.  Chunk c (16 bytes, a block) of row y sits at unit
+// c ^ ((y >> 1) & 7), so that 16 rows of a fragment read sit on distinct banks.  In
+// half t of a step lane (g, n) = (l / 16, l % 16) takes row n's block 4 t + g, whose scale
+// is byte 2 (tile % 2) + t of the lane's four.
+template <int WVM, int WVN, int TM, int TN>
 struct MxGeo {
-  static constexpr int BM = 64 * WM, BN = 64 * WN;
-  static constexpr int XB = BM * 128, WB = BN * 128;                // codes of a stage
-  static constexpr int XS = XB + WB, WS = XS + BM * 8;              // its scales
-  static constexpr int STB = WS + BN * 8;                           // bytes of a stage
-  static constexpr int OUTP = 64 * WN + 16, OUTW = 32 * WM * OUTP;  // output staging of a wave
-  static constexpr int LDS_MAIN = 2 * STB > 4 * OUTW ? 2 * STB : 4 * OUTW;
-  static constexpr int LDS_V = LDS_MAIN, LDS_L = LDS_V + BM * 64;   // r == 16: u and B of the tile
+  static constexpr int WAVES = WVM * WVN, THREADS = 64 * WAVES;
+  static constexpr int BM = 16 * TM * WVM, BN = 16 * TN * WVN;
+  static constexpr int XB = BM * 128, WB = BN * 128;   // codes of a stage
+  static constexpr int XS = XB + WB, WS = XS + BM * 8;  // its scales
+  static constexpr int STB = WS + BN * 8;              // bytes of a stage
+  // output staging of a wave: half its rows at a time
+  static constexpr int OUTP = 32 * TN + 16, OUTW = 8 * TM * OUTP;
+  static constexpr int LDS_MAIN = 2 * STB > WAVES * OUTW ? 2 * STB : WAVES * OUTW;
+  static constexpr int LDS_V = LDS_MAIN, LDS_L = LDS_V + BM * 64;  // r == 16: u and B of the tile
   static constexpr int LDS_BYTES = LDS_L + BN * 32;
-  static constexpr int LPS = 2 * WM + 2 * WN + 1;                   // loads of a wave and step
-  static_assert(LDS_BYTES <= 160 * 1024, "LDS");
+  static constexpr int XL = BM / 8 / WAVES, WL = BN / 8 / WAVES;   // loads of a wave and step ...
+  static constexpr int SL = (BM + BN) / 128;                       // ... and of all, of scales
+  static_assert(LDS_BYTES <= 160 * 1024 && WAVES % SL == 0, "LDS");
 };
 
 typedef __attribute__((address_space(3))) void lds_void;
@@ -253,17 +255,26 @@ __device__ __forceinline__ i32x8 frag4(u32x4 v) {
   return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
 }
 
-template <int WM, int WN, bool LORA16>
-__global__ __launch_bounds__(kThreads, 1) void k_mx4_gemm(
+// f(0), f(1), .. f(N - 1), each with its index as a constant.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void unrolled(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    unrolled<N, I + 1>(f);
+  }
+}
+
+template <int WVM, int WVN, int TM, int TN, bool LORA16>
+__global__ __launch_bounds__(64 * WVM * WVN, 2) void k_mx4_gemm(
     const uint8_t* __restrict__ wc, const uint8_t* __restrict__ ws,
     const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs, int64_t M, int64_t N, int J,
     const float* __restrict__ V, const uint16_t* __restrict__ L, int r, float s,
     uint16_t* __restrict__ y, int tiles_m, int tiles_n) {
-  using G = MxGeo<WM, WN>;
-  constexpr int BM = G::BM, BN = G::BN, STB = G::STB;
+  using G = MxGeo<WVM, WVN, TM, TN>;
+  constexpr int BM = G::BM, BN = G::BN, STB = G::STB, XL = G::XL, WL = G::WL, LPS = XL + WL;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 1, wn = wave & 1;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WVN, wn = wave % WVN;
 
   // tile order: each XCD (they take workgroups round robin) a contiguous run of the
   // tiles, four tile rows at a time across the columns
@@ -285,166 +296,152 @@ __global__ __launch_bounds__(kThreads, 1) void k_mx4_gemm(
   const int mrows = (int)min((int64_t)BM, M - m0), nrows = (int)min((int64_t)BN, N - n0);
   const int pitch = 128 * J;
 
-  // loads: instruction i of wave w covers rows 8 (2 W w + i) + l / 8 (rows past the matrix
+  // loads: instruction i of wave w covers rows 8 (XL w + i) + l / 8 (rows past the matrix
   // repeat its last one: nothing of them is stored)
   const rsrc_t rx = make_rs(xc + m0 * pitch, (uint32_t)(mrows * pitch));
   const rsrc_t rw = make_rs(wc + n0 * pitch, (uint32_t)(nrows * pitch));
-  uint32_t xoff[2 * WM], woff[2 * WN];
+  uint32_t xoff[XL], woff[WL];
 #pragma unroll
-  for (int i = 0; i < 2 * WM; ++i) {
-    const int row = 8 * (2 * WM * wave + i) + (lane >> 3);
+  for (int i = 0; i < XL; ++i) {
+    const int row = 8 * (XL * wave + i) + (lane >> 3);
     xoff[i] = (uint32_t)(min(row, mrows - 1) * pitch + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
   }
 #pragma unroll
-  for (int i = 0; i < 2 * WN; ++i) {
-    const int row = 8 * (2 * WN * wave + i) + (lane >> 3);
+  for (int i = 0; i < WL; ++i) {
+    const int row = 8 * (WL * wave + i) + (lane >> 3);
     woff[i] = (uint32_t)(min(row, nrows - 1) * pitch + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
   }
-  // scales: 1 KB (four groups of 32 rows) an instruction, those of x then those of W;
-  // with half as many as waves the upper waves load the same again
-  constexpr int SQ = (2 * WM + 2 * WN) / 4;
-  const int sq = wave % SQ;
-  const bool sx = sq < WM / 2;
-  const int sg = 4 * (sx ? sq : sq - WM / 2) + (lane >> 4);  // group of the tile
+  // scales: 1 KB (four groups of 32 rows) a wave, those of x first; there are twice as
+  // many waves, and the upper ones load the same again
+  const int sq = wave % G::SL;
+  const bool sx = sq < BM / 128;
+  const int sg = 4 * (sx ? sq : sq - BM / 128) + (lane >> 4);  // group of the tile
   const int sgroups = ((sx ? mrows : nrows) + 31) >> 5;
   const rsrc_t rs = make_rs(sx ? xs + m0 / 32 * J * 256 : ws + n0 / 32 * J * 256,
                             (uint32_t)(sgroups * J * 256));
   const uint32_t soff = (uint32_t)(min(sg, sgroups - 1) * J * 256 + 16 * (lane & 15));
+  // load q (0 .. LPS) of step st
   auto load_one = [&](int q, int st, int stage) {
     uint8_t* base = smem + stage * STB;
     const uint32_t so = (uint32_t)st * 128;
-    if (q < 2 * WM)
-      dma16(rx, xoff[q], so, base + 1024 * (2 * WM * wave + q));
-    else if (q < 2 * WM + 2 * WN)
-      dma16(rw, woff[q - 2 * WM], so, base + G::XB + 1024 * (2 * WN * wave + q - 2 * WM));
+    if (q < XL)
+      dma16(rx, xoff[q], so, base + 1024 * (XL * wave + q));
+    else if (q < LPS)
+      dma16(rw, woff[q - XL], so, base + G::XB + 1024 * (WL * wave + q - XL));
     else
       dma16(rs, soff, 2 * so, base + G::XS + 1024 * sq);
   };
 
   // fragment reads
-  const int n = lane & 31, h = lane >> 5;
-  int roff[4];
+  const int n = lane & 15, g = lane >> 4;
+  int roff[2];
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
-    roff[t] = n * 128 + 16 * ((2 * h + (t & 1) + 4 * (t >> 1)) ^ ((n >> 1) & 7));
-  const int xbase = wm * 32 * WM * 128, wbase = G::XB + wn * 32 * WN * 128;
-  const int xsb = G::XS + wm * WM * 256, wsb = G::WS + wn * WN * 256;
-  const int so0 = 4 * (32 * h + (n & 15)) + 2 * (n >> 4);
-  auto frag = [&](int stage, int base, int g, int t) {
-    return *reinterpret_cast<const u32x4*>(smem + stage * STB + base + g * 4096 + roff[t]);
+  for (int t = 0; t < 2; ++t) roff[t] = n * 128 + 16 * ((4 * t + g) ^ ((n >> 1) & 7));
+  const int xbase = wm * 16 * TM * 128, wbase = G::XB + wn * 16 * TN * 128;
+  const int xsb = G::XS + wm * TM * 128 + 4 * lane, wsb = G::WS + wn * TN * 128 + 4 * lane;
+  auto frag = [&](int stage, int base, int k, int t) {
+    return *reinterpret_cast<const u32x4*>(smem + stage * STB + base + k * 2048 + roff[t]);
   };
-  auto scale = [&](int stage, int base, int g) {
-    const uint8_t* p = smem + stage * STB + base + g * 256 + so0;
-    return (int)((uint32_t)*reinterpret_cast<const uint16_t*>(p) |
-                 ((uint32_t)*reinterpret_cast<const uint16_t*>(p + 64) << 16));
+  auto scale = [&](int stage, int base, int k) {  // of tiles 2 k and 2 k + 1
+    return *reinterpret_cast<const int*>(smem + stage * STB + base + k * 256);
   };
 
-  f32x16 acc[WM][WN];
+  f32x4 acc[TM][TN];
 #pragma unroll
-  for (int i = 0; i < WM; ++i)
+  for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int j = 0; j < WN; ++j) acc[i][j] = f32x16{};
-  u32x4 fx[2][WM], fw[2][WN];
-  int ex[2][WM], ew[2][WN];
+    for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{};
+  u32x4 fx[TM], fw[2][TN];
+  int ex[2][TM / 2], ew[2][TN / 2];
 
   if constexpr (LORA16) {  // u and B of the tile (rows past it read zeros)
     const rsrc_t rv = make_rs(V + m0 * 16, (uint32_t)(mrows * 64));
     const rsrc_t rl = make_rs(L + n0 * 16, (uint32_t)(nrows * 32));
 #pragma unroll
-    for (int k = 0; k < WM; ++k) {
-      const int q = WM * wave + k;
+    for (int k = 0; k < BM / 16 / G::WAVES; ++k) {
+      const int q = BM / 16 / G::WAVES * wave + k;
       dma16(rv, (uint32_t)(1024 * q + 16 * lane), 0, smem + G::LDS_V + 1024 * q);
     }
 #pragma unroll
-    for (int k = 0; k < (2 * WN + 3) / 4; ++k) {
-      const int q = 4 * k + wave;
-      if (q < 2 * WN) dma16(rl, (uint32_t)(1024 * q + 16 * lane), 0, smem + G::LDS_L + 1024 * q);
+    for (int k = 0; k < BN / 32 / G::WAVES; ++k) {
+      const int q = BN / 32 / G::WAVES * wave + k;
+      dma16(rl, (uint32_t)(1024 * q + 16 * lane), 0, smem + G::LDS_L + 1024 * q);
     }
   }
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
-    for (int q = 0; q < G::LPS; ++q) load_one(q, min(k, J - 1), k);
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(G::LPS) : "memory");
+    for (int q = 0; q <= LPS; ++q) load_one(q, min(k, J - 1), k);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LPS + 1) : "memory");
   barrier_lds();
 #pragma unroll
-  for (int i = 0; i < WM; ++i) {
-    fx[0][i] = frag(0, xbase, i, 0);
-    ex[0][i] = scale(0, xsb, i);
-  }
+  for (int i = 0; i < TM; ++i) fx[i] = frag(0, xbase, i, 0);
 #pragma unroll
-  for (int j = 0; j < WN; ++j) {
-    fw[0][j] = frag(0, wbase, j, 0);
-    ew[0][j] = scale(0, wsb, j);
-  }
+  for (int j = 0; j < TN; ++j) fw[0][j] = frag(0, wbase, j, 0);
+#pragma unroll
+  for (int i = 0; i < TM / 2; ++i) ex[0][i] = scale(0, xsb, i);
+#pragma unroll
+  for (int j = 0; j < TN / 2; ++j) ew[0][j] = scale(0, wsb, j);
 
-  // product t of step st on stage P = st % 2.  The fragments of the next product are read
-  // while this one's run; before the last product every wave has read the stage and
-  // step st + 1 has landed; the loads of step st + 2 then go into the stage.
-  auto product = [&](auto p_t, auto t_t, int st) {
-    constexpr int P = decltype(p_t)::value, TT = decltype(t_t)::value;
-    constexpr int C = TT & 1, RS = TT == 3 ? P ^ 1 : P, RT = (TT + 1) & 3;
-    constexpr int OP = 2 * (TT & 1) + (TT >> 1);
+  // half t of step st on stage P = st % 2.  The fragments of the next half are read while
+  // this one's products run (those of W in a second set, those of x in place after their
+  // row).  At the end of half 0 every wave has read the stage and step st + 1 has
+  // landed; half 1 sends the loads of step st + 2 into the stage.
+  auto half = [&](auto p_t, auto t_t, int st) {
+    constexpr int P = decltype(p_t)::value, H = decltype(t_t)::value;
+    constexpr int RS = H == 0 ? P : P ^ 1, RH = H ^ 1;
     const int lst = min(st + 2, J - 1);
-#pragma unroll
-    for (int i = 0; i < WM; ++i) {
-#pragma unroll
-      for (int j = 0; j < WN; ++j) {
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-            frag4(fw[C][j]), frag4(fx[C][i]), acc[i][j], 4, 4, OP, ew[P][j], OP, ex[P][i]);
-        if (i == 0) {
-          fw[C ^ 1][j] = frag(RS, wbase, j, RT);
-          if (TT == 3) ew[P ^ 1][j] = scale(RS, wsb, j);
-        }
-        if (i == 1) {
-          if (j < WM) fx[C ^ 1][j] = frag(RS, xbase, j, RT);
-          if (TT == 3 && j < WM) ex[P ^ 1][j] = scale(RS, xsb, j);
-        }
-        if (TT == 3) {
-          constexpr int PER = (G::LPS + WM * WN - 1) / (WM * WN);
-#pragma unroll
-          for (int k = 0; k < PER; ++k)
-            if (PER * (WN * i + j) + k < G::LPS) load_one(PER * (WN * i + j) + k, lst, P);
-        }
-      }
+    unrolled<TM>([&](auto i_t) {
+      constexpr int i = decltype(i_t)::value;
+      unrolled<TN>([&](auto j_t) {
+        constexpr int j = decltype(j_t)::value;
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            frag4(fw[H][j]), frag4(fx[i]), acc[i][j], 4, 4, 2 * (j & 1) + H, ew[P][j / 2],
+            2 * (i & 1) + H, ex[P][i / 2]);
+        if (i == 0) fw[RH][j] = frag(RS, wbase, j, RH);
+        if (H == 1 && i == 1 && j < TN / 2) ew[P ^ 1][j] = scale(RS, wsb, j);
+        if (H == 1 && i >= 2 && j == 0 && i - 2 < TM / 2) ex[P ^ 1][i - 2] = scale(RS, xsb, i - 2);
+        if (H == 1 && j == TN / 2)
+          for (int q = (LPS + TM) / TM * i; q < (LPS + TM) / TM * (i + 1); ++q)
+            if (q <= LPS) load_one(q, lst, P);
+      });
+      fx[i] = frag(RS, xbase, i, RH);
       __builtin_amdgcn_sched_barrier(0);
-    }
-    if (TT == 2) {
+    });
+    if (H == 0) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       barrier_lds();
     }
   };
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
-  using I2 = std::integral_constant<int, 2>;
-  using I3 = std::integral_constant<int, 3>;
-  auto step = [&](auto p_t, int st) {
-    product(p_t, I0{}, st);
-    product(p_t, I1{}, st);
-    product(p_t, I2{}, st);
-    product(p_t, I3{}, st);
-  };
   int st = 0;
   for (; st + 2 <= J; st += 2) {
-    step(I0{}, st);
-    step(I1{}, st + 1);
+    half(I0{}, I0{}, st);
+    half(I0{}, I1{}, st);
+    half(I1{}, I0{}, st + 1);
+    half(I1{}, I1{}, st + 1);
   }
-  if (st < J) step(I0{}, st);
+  if (st < J) {
+    half(I0{}, I0{}, st);
+    half(I0{}, I1{}, st);
+  }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   barrier_lds();
 
-  // the adapter: acc += B (s u)^T, s u as a bf16 high part and a remainder, 16 ranks a
-  // product (lane half h: ranks 8 h .. 8 h + 7)
+  // the adapter: acc += B (s u)^T, 16 ranks a product of 32: lane groups 0 and 1 carry the
+  // bf16 high part of s u, 2 and 3 its remainder, against the same ranks of B
   for (int j0 = 0; j0 < r; j0 += 16) {
-    const int jl = j0 + 8 * h;
-    bf16x8 lb[WN];
+    const int jl = j0 + 8 * (g & 1);
+    bf16x8 lb[TN];
 #pragma unroll
-    for (int j = 0; j < WN; ++j) {
+    for (int j = 0; j < TN; ++j) {
+      const int row = 16 * (TN * wn + j) + n;
       if constexpr (LORA16) {
         lb[j] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(
-            smem + G::LDS_L + (32 * (WN * wn + j) + n) * 32 + 16 * h));
+            smem + G::LDS_L + row * 32 + 16 * (g & 1)));
       } else {
-        const uint16_t* lp = L + min(n0 + 32 * (WN * wn + j) + n, N - 1) * r;
+        const uint16_t* lp = L + min(n0 + row, N - 1) * r;
         uint32_t e[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) e[q] = jl + q < r ? lp[min(jl + q, r - 1)] : 0u;
@@ -453,10 +450,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_mx4_gemm(
       }
     }
 #pragma unroll
-    for (int i = 0; i < WM; ++i) {
+    for (int i = 0; i < TM; ++i) {
+      const int row = 16 * (TM * wm + i) + n;
       float v[8];
       if constexpr (LORA16) {
-        const uint8_t* vp = smem + G::LDS_V + (32 * (WM * wm + i) + n) * 64 + 32 * h;
+        const uint8_t* vp = smem + G::LDS_V + row * 64 + 32 * (g & 1);
         const f32x4 a = *reinterpret_cast<const f32x4*>(vp);
         const f32x4 b = *reinterpret_cast<const f32x4*>(vp + 16);
 #pragma unroll
@@ -465,60 +463,62 @@ __global__ __launch_bounds__(kThreads, 1) void k_mx4_gemm(
           v[4 + q] = b[q];
         }
       } else {
-        const float* vp = V + min(m0 + 32 * (WM * wm + i) + n, M - 1) * r;
+        const float* vp = V + min(m0 + row, M - 1) * r;
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[q] = jl + q < r ? vp[min(jl + q, r - 1)] : 0.f;
       }
-      uint32_t hi[4], lo[4];
+      uint32_t w[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float a = s * v[2 * q], b = s * v[2 * q + 1];
-        hi[q] = pack_bf16x2(a, b);
-        lo[q] = pack_bf16x2(a - bf16_lo(hi[q]), b - bf16_hi(hi[q]));
+        const uint32_t hi = pack_bf16x2(a, b);
+        w[q] = g >= 2 ? pack_bf16x2(a - bf16_lo(hi), b - bf16_hi(hi)) : hi;
       }
-      const bf16x8 vh = __builtin_bit_cast(bf16x8, u32x4{hi[0], hi[1], hi[2], hi[3]});
-      const bf16x8 vl = __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], lo[2], lo[3]});
+      const bf16x8 vh = __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
 #pragma unroll
-      for (int j = 0; j < WN; ++j) {
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lb[j], vh, acc[i][j], 0, 0, 0);
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lb[j], vl, acc[i][j], 0, 0, 0);
-      }
+      for (int j = 0; j < TN; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lb[j], vh, acc[i][j], 0, 0, 0);
     }
   }
 
-  // store: lane (h, n) holds row n of tile (i, j), columns 8 q + 4 h + 0 .. 3 in its
-  // registers 4 q ..; through the wave's LDS staging tile, which leaves as rows of 64 WN
-  // bytes
+  // store: lane (g, n) holds row n of tile (i, j), columns 4 g .. 4 g + 3; through the
+  // wave's LDS staging tile, half the rows at a time, which leaves as rows of 32 TN bytes
   uint8_t* stg = smem + wave * G::OUTW;
-#pragma unroll
-  for (int i = 0; i < WM; ++i)
-#pragma unroll
-    for (int j = 0; j < WN; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<u32x2*>(stg + (32 * i + n) * G::OUTP + 2 * (32 * j + 8 * q + 4 * h)) =
-            u32x2{pack_bf16x2(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
-                  pack_bf16x2(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3])};
-  // (a wave's LDS accesses execute in order)
-  constexpr int LR = 4 * WN, RPS = 64 / LR;  // lanes of a row, rows a store
+  constexpr int LR = 2 * TN, RPS = 64 / LR;  // lanes of a row, rows a store
   const int lc = lane % LR;
-  const int64_t col = n0 + 32 * WN * wn + 8 * lc;
+  const int64_t col = n0 + 16 * TN * wn + 8 * lc;
   const bool whole = (N & 7) == 0;
 #pragma unroll
-  for (int q = 0; q < 32 * WM / RPS; ++q) {
-    const int rl = RPS * q + lane / LR;
-    const int64_t row = m0 + 32 * WM * wm + rl;
-    const u32x4 v = *reinterpret_cast<const u32x4*>(stg + rl * G::OUTP + 16 * lc);
-    if (row >= M || col >= N) continue;
-    uint16_t* dst = y + row * N + col;
-    if (whole) {
-      __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(dst));
-    } else if (col + 8 <= N) {
-      *reinterpret_cast<u32x4_any*>(dst) = v;
-    } else {
+  for (int p = 0; p < 2; ++p) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (col + k < N) dst[k] = (uint16_t)(v[k >> 1] >> (16 * (k & 1)));
+    for (int i = 0; i < TM / 2; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const f32x4 c = acc[p * TM / 2 + i][j];
+        *reinterpret_cast<u32x2*>(stg + (16 * i + n) * G::OUTP + 2 * (16 * j + 4 * g)) =
+            u32x2{pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3])};
+      }
+    // (a wave's LDS accesses execute in order)
+    const int64_t row0 = m0 + 16 * TM * wm + 8 * TM * p;
+    if (whole) {
+#pragma unroll
+      for (int q = 0; q < 8 * TM / RPS; ++q) {
+        const int rl = RPS * q + lane / LR;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(stg + rl * G::OUTP + 16 * lc);
+        if (row0 + rl < M && col < N)
+          __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y + (row0 + rl) * N + col));
+      }
+    } else {  // rows of y on any element
+      for (int q = 0; q < 8 * TM / RPS; ++q) {
+        const int rl = RPS * q + lane / LR;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(stg + rl * G::OUTP + 16 * lc);
+        if (row0 + rl >= M || col >= N) continue;
+        uint16_t* dst = y + (row0 + rl) * N + col;
+        if (col + 8 <= N)
+          *reinterpret_cast<u32x4_any*>(dst) = v;
+        else
+          for (int k = 0; col + k < N; ++k) dst[k] = (uint16_t)(v[k >> 1] >> (16 * (k & 1)));
+      }
     }
   }
 }
@@ -603,28 +603,30 @@ hipError_t launch_mx4_dequant_t(const Mx4& w, uint16_t* out, int64_t ldt, const 
 }
 
 namespace {
-template <int WM, int WN>
+template <int WVM, int WVN, int TM, int TN>
 hipError_t launch_tiles(const Mx4& w, const uint8_t* xc, const uint8_t* xs, int64_t M,
                         const float* u, const uint16_t* B, int r, float s, uint16_t* y,
                         hipStream_t st) {
-  using G = MxGeo<WM, WN>;
+  using G = MxGeo<WVM, WVN, TM, TN>;
   static const hipError_t attr = [] {
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_mx4_gemm<WM, WN, true>),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, G::LDS_BYTES);
+    const hipError_t e = hipFuncSetAttribute(
+        reinterpret_cast<const void*>(k_mx4_gemm<WVM, WVN, TM, TN, true>),
+        hipFuncAttributeMaxDynamicSharedMemorySize, G::LDS_BYTES);
     return e != hipSuccess
                ? e
-               : hipFuncSetAttribute(reinterpret_cast<const void*>(k_mx4_gemm<WM, WN, false>),
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, G::LDS_MAIN);
+               : hipFuncSetAttribute(
+                     reinterpret_cast<const void*>(k_mx4_gemm<WVM, WVN, TM, TN, false>),
+                     hipFuncAttributeMaxDynamicSharedMemorySize, G::LDS_MAIN);
   }();
   if (attr != hipSuccess) return attr;
   const int64_t tm = (M + G::BM - 1) / G::BM, tn = (w.rows + G::BN - 1) / G::BN;
-  const dim3 grid((unsigned)(tm * tn));
+  const dim3 grid((unsigned)(tm * tn)), block(G::THREADS);
   const int J = (int)mx4_steps(w.cols);
   if (r == 16)
-    hipLaunchKernelGGL((k_mx4_gemm<WM, WN, true>), grid, dim3(kThreads), G::LDS_BYTES, st, w.codes,
+    hipLaunchKernelGGL((k_mx4_gemm<WVM, WVN, TM, TN, true>), grid, block, G::LDS_BYTES, st, w.codes,
                        w.scales, xc, xs, M, w.rows, J, u, B, r, s, y, (int)tm, (int)tn);
   else
-    hipLaunchKernelGGL((k_mx4_gemm<WM, WN, false>), grid, dim3(kThreads), G::LDS_MAIN, st, w.codes,
+    hipLaunchKernelGGL((k_mx4_gemm<WVM, WVN, TM, TN, false>), grid, block, G::LDS_MAIN, st, w.codes,
                        w.scales, xc, xs, M, w.rows, J, u, B, r, s, y, (int)tm, (int)tn);
   return hipGetLastError();
 }
@@ -635,8 +637,8 @@ hipError_t launch_mx4_mm(const Mx4& w, const uint8_t* xc, const uint8_t* xs, int
                          hipStream_t st) {
   if (M > 64) {
     if ((M + 255) / 256 * ((w.rows + 255) / 256) >= 240)
-      return launch_tiles<4, 4>(w, xc, xs, M, u, B, r, s, y, st);
-    return launch_tiles<2, 2>(w, xc, xs, M, u, B, r, s, y, st);
+      return launch_tiles<2, 4, 8, 4>(w, xc, xs, M, u, B, r, s, y, st);
+    return launch_tiles<2, 2, 4, 4>(w, xc, xs, M, u, B, r, s, y, st);
   }
   const uint32_t cols_wgs = (uint32_t)((w.rows + 127) / 128);
   const dim3 grid(cols_wgs * (uint32_t)((M + 31) / 32));  // (at most 2^31)
