@@ -533,21 +533,22 @@ qn_status check_mx4(const qn_mx4* w, int64_t M, int r) {
   return QN_OK;
 }
 
-struct Mx4Ws {
-  uint8_t* xc;   // x in MXFP4
-  uint8_t* xs;
-  float* u;      // [M, r] when the caller gives no u_out
-  float* upart;  // [S, M, r] when S > 1
-  int S;
-};
-Mx4Ws carve_mx4(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool need_u) {
-  Mx4Ws f;
+// The forward's input in the workspace (u given or there).
+Mx4X carve_mx4(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, float* u, bool need_u) {
+  Mx4X f{};
   c.take<unsigned>(kArrivalWords);  // left alone, as above
-  f.xc = c.take<uint8_t>((size_t)mx4_code_bytes(M, cols));
-  f.xs = c.take<uint8_t>((size_t)mx4_scale_bytes(M, cols));
-  f.S = r > 0 ? thin_nt_slices(M, cols) : 1;
-  f.u = need_u && r > 0 ? c.take<float>((size_t)M * r) : nullptr;
+  f.M = M;
+  f.r = r;
+  f.codes = c.take<uint8_t>((size_t)mx4_code_bytes(M, cols));
+  f.scales = c.take<uint8_t>((size_t)mx4_scale_bytes(M, cols));
+  f.S = r > 0 ? mx4_x_slices(M, cols) : 1;
+  f.u = need_u && r > 0 ? c.take<float>((size_t)M * r) : u;
   f.upart = f.S > 1 ? c.take<float>((size_t)f.S * M * r) : nullptr;
+  if (r > 0 && !mx4_few_rows(M)) {
+    const size_t nj = (r + 15) / 16;
+    f.su = c.take<uint16_t>((size_t)round_up(M, 32) * nj * 32);
+    f.bo = c.take<uint16_t>((size_t)round_up(rows, 16) * nj * 16);
+  }
   return f;
 }
 // the transposed bf16 copy of a backward without an adapter
@@ -1077,7 +1078,7 @@ size_t mx4_linear_workspace(int64_t M, int64_t rows, int64_t cols, int r, int ba
     return 0;
   Carver c(nullptr);
   if (!backward)
-    carve_mx4(c, M, rows, cols, r, true);
+    carve_mx4(c, M, rows, cols, r, nullptr, true);
   else if (r == 0)
     carve_mx4_dx(c, rows, cols);
   else
@@ -1100,19 +1101,15 @@ qn_status mx4_linear_fwd(const qn_mx4* w, const uint16_t* x, int64_t M, const ui
       !aligned16(B) || !aligned16(u_out))
     return QN_EALIGN;
   Carver probe(nullptr);
-  carve_mx4(probe, M, w->rows, w->cols, r, u_out == nullptr);
+  carve_mx4(probe, M, w->rows, w->cols, r, u_out, u_out == nullptr);
   if (!workspace) return QN_EINVAL;
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return QN_EALIGN;
   if (workspace_bytes < probe.used) return QN_EWORKSPACE;
   Carver c(workspace);
-  Mx4Ws f = carve_mx4(c, M, w->rows, w->cols, r, u_out == nullptr);
-  float* u = u_out ? u_out : f.u;
+  const Mx4X f = carve_mx4(c, M, w->rows, w->cols, r, u_out, u_out == nullptr);
   hipStream_t st = static_cast<hipStream_t>(stream);
-  hipError_t e = launch_mx4_quant(x, false, M, w->cols, f.xc, f.xs, st);
-  if (e == hipSuccess && r > 0)
-    e = launch_thin_nt(x, A, M, w->cols, r, u, f.upart, f.S, st, true, false, Clear{nullptr, 0},
-                       nullptr, lo.drop);
-  if (e == hipSuccess) e = launch_mx4_mm(to_mx4(w), f.xc, f.xs, M, u, B, r, lo.s, y, st);
+  hipError_t e = launch_mx4_x(x, w->cols, f, lo.drop, A, B, w->rows, lo.s, st);
+  if (e == hipSuccess) e = launch_mx4_mm(to_mx4(w), f, B, lo.s, y, st);
   return from_hip(e);
 }
 

@@ -1,6 +1,7 @@
 // MXFP4: matrices in 4 bits with a power-of-two scale for every 32 columns of a row
 // (format in the header), into the format and back, and the linear's product on two
 // of them with the adapter term.
+#include <algorithm>
 #include <type_traits>
 
 #include "qn_device.h"
@@ -87,6 +88,15 @@ __device__ __forceinline__ void decode8(uint32_t c, float scale, float v[8]) {
 #undef QN_PAIR
 }
 
+// f(0), f(1), .. f(N - 1), each with its index as a constant.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void unrolled(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    unrolled<N, I + 1>(f);
+  }
+}
+
 // A workgroup takes 32 rows x 256 columns, a step of the scales' layout: pass p,
 // thread t -> row 8 p + t / 32, columns 8 (t % 32) .. + 7; four lanes to a block.  The
 // 256 scale bytes leave together.
@@ -154,61 +164,196 @@ __global__ __launch_bounds__(kThreads) void k_mx4_dequant(const uint8_t* __restr
   }
 }
 
-// y[M, N] = x W^T + s u B^T.  A wave takes 32 rows of W (the MFMA's A operand, so
-// that a lane ends with four columns of y in a row) and 32 rows of x; lane l holds row
-// l % 16 and block 4 t + l / 16 of the step's eight in product t.
-__global__ __launch_bounds__(kThreads) void k_mx4_mm(
-    const uint8_t* __restrict__ wc, const uint8_t* __restrict__ ws,
-    const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs, int64_t M, int64_t N, int J,
-    const float* __restrict__ u, const uint16_t* __restrict__ B, int r, float s,
-    uint16_t* __restrict__ y, uint32_t cols_wgs) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, n = lane & 15;
-  const uint32_t bm = blockIdx.x / cols_wgs, bn = blockIdx.x - bm * cols_wgs;
-  const int64_t n0 = 32 * ((int64_t)bn * 4 + wave), m0 = 32 * (int64_t)bm;
-  if (n0 >= N) return;
-  const uint8_t *wp[2], *xp[2];
+// ---- The linear's input: x [M, K] bf16 read once, into MXFP4 and, with the adapter, u =
+// drop(x) A^T.  A workgroup takes 16 RT rows and one of S slices of the steps (256
+// columns each), its waves a step in turn.  Lane (g, n) = (l / 16, l % 16) holds columns
+// 8 g .. 8 g + 7 of row n in each block of 32: an operand of the bf16 product for u as it
+// is, and a quarter of the block, whose largest magnitude meets over the four lanes of
+// the row by two exchanges (two blocks a word).  Four blocks' codes are turned around
+// between those lanes, so that each stores one block's 16 bytes.  With one slice the
+// waves' sums of u meet in LDS, and the workgroup writes u and (s u) as the
+// product's epilogue takes it; else the slices' sums are written, for the product's
+// workgroups to add.
+constexpr int kXWaves = 8;
+__device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                __builtin_bit_cast(u16x2, b)));
+}
+// the eight codes of a lane's part of a block (the words by themselves: a bit cast of a
+// vector's element is one of its first)
+__device__ __forceinline__ uint32_t encode8(u32x4 v, uint32_t E) {
+  const float scale = mx4_scale(E);
+  const uint32_t v0 = v[0], v1 = v[1], v2 = v[2], v3 = v[3];
+  uint32_t c = 0;
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, v0), scale, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, v1), scale, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, v2), scale, 2);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, v3), scale, 3);
+  return E == kMx4NaN ? 0u : c;
+}
+// B [N, r] as the product's epilogue takes it: 16 rows and 16 ranks are 512 bytes, 16 of
+// them rows n's ranks 8 h .. 8 h + 7 at 16 h + n (zero past N and r); piece i of them
+__device__ __forceinline__ void order_b(const uint16_t* B, int64_t N, int r, int nj, int64_t i,
+                                        uint16_t* out) {
+  const int n = (int)(i & 15), h = (int)(i >> 4) & 1;
+  const int64_t t = i >> 5, row = t / nj * 16 + n;
+  const int j = (int)(t % nj) * 16 + 8 * h;
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  if (row < N) {
+    if (r % 8 == 0) {
+      if (j < r) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(B + row * r + j);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    wp[i] = wc + min(n0 + 16 * i + n, N - 1) * 128 * J + 16 * g;
-    xp[i] = xc + min(m0 + 16 * i + n, M - 1) * 128 * J + 16 * g;
-  }
-  const uint32_t* wsp = reinterpret_cast<const uint32_t*>(ws + (n0 / 32) * J * 256) + lane;
-  const uint32_t* xsp = reinterpret_cast<const uint32_t*>(xs + (m0 / 32) * J * 256) + lane;
-  f32x4 acc[2][2] = {};
-  for (int j = 0; j < J; ++j) {
-    const int sw = (int)wsp[64 * j], sx = (int)xsp[64 * j];
-    i32x8 a[2][2], b[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const u32x4 p = *reinterpret_cast<const u32x4*>(wp[i] + 128 * j + 64 * t);
-        const u32x4 q = *reinterpret_cast<const u32x4*>(xp[i] + 128 * j + 64 * t);
-        a[i][t] = i32x8{(int)p[0], (int)p[1], (int)p[2], (int)p[3], 0, 0, 0, 0};
-        b[i][t] = i32x8{(int)q[0], (int)q[1], (int)q[2], (int)q[3], 0, 0, 0, 0};
+        for (int q = 0; q < 4; ++q) w[q] = v[q];
       }
-#define QN_MM(i, k, t)                                                                      \
-  acc[i][k] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(                             \
-      a[i][t], b[k][t], acc[i][k], 4, 4, 2 * i + t, sw, 2 * k + t, sx)
-    QN_MM(0, 0, 0); QN_MM(0, 1, 0); QN_MM(1, 0, 0); QN_MM(1, 1, 0);
-    QN_MM(0, 0, 1); QN_MM(0, 1, 1); QN_MM(1, 0, 1); QN_MM(1, 1, 1);
-#undef QN_MM
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (j + q < r) w[q >> 1] |= (uint32_t)B[row * r + j + q] << (16 * (q & 1));
+    }
   }
-  // lane: row m0 + 16 k + l % 16 of y, columns n0 + 16 i + 4 (l / 16) + q
+  reinterpret_cast<u32x4*>(out)[i] = u32x4{w[0], w[1], w[2], w[3]};
+}
+
+template <int RT, int NJ, bool DROP>
+__global__ __launch_bounds__(64 * kXWaves) void k_mx4_x(
+    const uint16_t* __restrict__ x, int64_t M, int64_t K, int J, int S, Drop d,
+    const uint16_t* __restrict__ A, const uint16_t* __restrict__ B, int64_t N, int r, float s,
+    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, float* __restrict__ u,
+    float* __restrict__ upart, uint16_t* __restrict__ su, uint16_t* __restrict__ bo, int b_wgs) {
+  constexpr int PITCH = 16 * RT + 4;
+  __shared__ __attribute__((aligned(16))) float sums[kXWaves][16 * NJ][PITCH];
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if ((int)blockIdx.x < b_wgs) {
+    const int64_t i = (int64_t)blockIdx.x * (64 * kXWaves) + tid;
+    if (i < (N + 15) / 16 * NJ * 32) order_b(B, N, r, NJ, i, bo);
+    return;
+  }
+  const int64_t bid = (int64_t)blockIdx.x - b_wgs, rt = bid / S;
+  const int z = (int)(bid - rt * S);
+  const int j0 = (int)((int64_t)J * z / S), j1 = (int)((int64_t)J * (z + 1) / S);
+  const int64_t m0 = 16 * RT * rt;
+  const uint64_t offset = DROP ? drop_offset(d) : 0;
+  const uint16_t* xp[RT];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int64_t m = m0 + 16 * k + n;
-    if (m >= M) continue;
+  for (int i = 0; i < RT; ++i) xp[i] = x + min(m0 + 16 * i + n, M - 1) * K + 8 * g;
+  const uint16_t* ap[NJ];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+  for (int q = 0; q < NJ; ++q) ap[q] = A + (int64_t)min(16 * q + n, r - 1) * K + 8 * g;
+  f32x4 acc[RT][NJ] = {};
+  for (int j = j0 + wave; j < j1; j += kXWaves) {
+    const int64_t k0 = (int64_t)j * kMx4Step;
+    const int blocks = (int)min((K - k0) / kMx4Block, (int64_t)8);  // (K is a multiple of 64)
+    u32x4 v[RT][8];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t col = n0 + 16 * i + 4 * g + q;
-        if (col >= N) continue;
-        float low = 0.f;
-        for (int e = 0; e < r; ++e) low += u[m * r + e] * load_f32(B + col * r + e);
-        y[m * N + col] = to_bf16(acc[i][k][q] + s * low);
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {  // past the row: its first columns, zeroed below
+        v[i][b] = *reinterpret_cast<const u32x4*>(xp[i] + (b < blocks ? k0 + 32 * b : 0));
       }
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      if (b >= blocks) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) v[i][b] = u32x4{0u, 0u, 0u, 0u};
+        continue;
+      }
+      bf16x8 a[NJ];
+#pragma unroll
+      for (int q = 0; q < NJ; ++q) {
+        u32x4 w = *reinterpret_cast<const u32x4*>(ap[q] + k0 + 32 * b);
+        if (16 * q + n >= r) w = u32x4{0u, 0u, 0u, 0u};
+        a[q] = __builtin_bit_cast(bf16x8, w);
+      }
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        u32x4 w = v[i][b];
+        if constexpr (DROP) {
+          const int64_t m = min(m0 + 16 * i + n, M - 1);
+          w = drop8(w, philox(d, offset, (uint64_t)(m * K + k0 + 32 * b + 8 * g) >> 3), d.less);
+        }
+#pragma unroll
+        for (int q = 0; q < NJ; ++q)
+          acc[i][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), a[q],
+                                                              acc[i][q], 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int64_t m = m0 + 16 * i + n;
+      uint32_t e0 = 0, e1 = 0;  // exponents of blocks g and g + 4
+      u32x4 out[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t c[4];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {  // two blocks at a time
+          const u32x4 a = v[i][4 * h + 2 * p], b = v[i][4 * h + 2 * p + 1];
+          const uint32_t mask = 0x7fff7fffu;
+          const uint32_t ma = pk_max(pk_max(a[0] & mask, a[1] & mask),
+                                     pk_max(a[2] & mask, a[3] & mask));
+          const uint32_t mb = pk_max(pk_max(b[0] & mask, b[1] & mask),
+                                     pk_max(b[2] & mask, b[3] & mask));
+          uint32_t top = pk_max(__builtin_amdgcn_perm(mb, ma, 0x05040100u),
+                                __builtin_amdgcn_perm(mb, ma, 0x07060302u));
+          const auto s16 = __builtin_amdgcn_permlane16_swap(top, top, false, false);
+          top = pk_max(s16[0], s16[1]);
+          const auto s32 = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+          top = pk_max(s32[0], s32[1]);
+          const uint32_t Ea = mx4_exp(top << 16), Eb = mx4_exp(top & 0xffff0000u);
+          c[2 * p] = encode8(a, Ea);
+          c[2 * p + 1] = encode8(b, Eb);
+          uint32_t& e = h ? e1 : e0;
+          e = g == 2 * p ? Ea : g == 2 * p + 1 ? Eb : e;
+        }
+        // c[b] of lane g -> word g of block b at lane b
+        auto t0 = __builtin_amdgcn_permlane32_swap(c[0], c[2], false, false);
+        auto t1 = __builtin_amdgcn_permlane32_swap(c[1], c[3], false, false);
+        auto w0 = __builtin_amdgcn_permlane16_swap(t0[0], t1[0], false, false);
+        auto w1 = __builtin_amdgcn_permlane16_swap(t0[1], t1[1], false, false);
+        out[h] = u32x4{w0[0], w0[1], w1[0], w1[1]};
+      }
+      if (m < M) {
+        uint8_t* dst = codes + m * 128 * J + 128 * j + 16 * g;
+        *reinterpret_cast<u32x4*>(dst) = out[0];
+        *reinterpret_cast<u32x4*>(dst + 64) = out[1];
+        *reinterpret_cast<uint16_t*>(scales + ((m >> 5) * J + j) * 256 + 4 * lane +
+                                     2 * ((m >> 4) & 1)) = (uint16_t)(e0 | (e1 << 8));
+      }
+    }
+  }
+  // lane: rank 16 q + n, rows 16 i + 4 g + 0 .. 3
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int q = 0; q < NJ; ++q)
+      *reinterpret_cast<f32x4*>(&sums[wave][16 * q + n][16 * i + 4 * g]) = acc[i][q];
+  __syncthreads();
+  float* dst = S > 1 ? upart + (int64_t)z * M * r : u;
+  for (int e = tid; e < 16 * RT * 16 * NJ; e += 64 * kXWaves) {
+    const int row = e / (16 * NJ), j = e % (16 * NJ);
+    float t = sums[0][j][row];
+#pragma unroll
+    for (int w = 1; w < kXWaves; ++w) t += sums[w][j][row];
+    sums[0][j][row] = t;  // (read and written by this thread alone)
+    if (j < r && m0 + row < M) dst[(m0 + row) * r + j] = t;
+  }
+  if (!su) return;
+  __syncthreads();
+  // (s u): 16 rows and 16 ranks are 1 KB in the order of the product's lanes
+  for (int e = tid; e < 64 * RT * NJ; e += 64 * kXWaves) {
+    const int l = e & 63, q = (e >> 6) % NJ, i = (e >> 6) / NJ;
+    uint32_t w[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const int j = 16 * q + 8 * ((l >> 4) & 1) + 2 * p, row = 16 * i + (l & 15);
+      const float a = j < r ? s * sums[0][j][row] : 0.f;
+      const float b = j + 1 < r ? s * sums[0][j + 1][row] : 0.f;
+      const uint32_t hi = pack_bf16x2(a, b);
+      w[p] = l >= 32 ? pack_bf16x2(a - bf16_lo(hi), b - bf16_hi(hi)) : hi;
+    }
+    reinterpret_cast<u32x4*>(su)[((rt * RT + i) * NJ + q) * 64 + l] = u32x4{w[0], w[1], w[2], w[3]};
   }
 }
 
@@ -229,7 +374,7 @@ struct MxGeo {
   // output staging of a wave: half its rows at a time
   static constexpr int OUTP = 32 * TN + 16, OUTW = 8 * TM * OUTP;
   static constexpr int LDS_MAIN = 2 * STB > WAVES * OUTW ? 2 * STB : WAVES * OUTW;
-  static constexpr int LDS_V = LDS_MAIN, LDS_L = LDS_V + BM * 64;  // r == 16: u and B of the tile
+  static constexpr int LDS_V = LDS_MAIN, LDS_L = LDS_V + BM * 64;  // r <= 16: s u and B
   static constexpr int LDS_BYTES = LDS_L + BN * 32;
   static constexpr int XL = BM / 8 / WAVES, WL = BN / 8 / WAVES;   // loads of a wave and step ...
   static constexpr int SL = (BM + BN) / 128;                       // ... and of all, of scales
@@ -255,20 +400,11 @@ __device__ __forceinline__ i32x8 frag4(u32x4 v) {
   return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
 }
 
-// f(0), f(1), .. f(N - 1), each with its index as a constant.
-template <int N, int I = 0, typename F>
-__device__ __forceinline__ void unrolled(F&& f) {
-  if constexpr (I < N) {
-    f(std::integral_constant<int, I>{});
-    unrolled<N, I + 1>(f);
-  }
-}
-
-template <int WVM, int WVN, int TM, int TN, bool LORA16>
+template <int WVM, int WVN, int TM, int TN, bool ONE>
 __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_mx4_gemm(
     const uint8_t* __restrict__ wc, const uint8_t* __restrict__ ws,
     const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs, int64_t M, int64_t N, int J,
-    const float* __restrict__ V, const uint16_t* __restrict__ L, int r, float s,
+    const uint16_t* __restrict__ su, const uint16_t* __restrict__ bo, int nj,
     uint16_t* __restrict__ y, int tiles_m, int tiles_n) {
   using G = MxGeo<WVM, WVN, TM, TN>;
   constexpr int BM = G::BM, BN = G::BN, STB = G::STB, XL = G::XL, WL = G::WL, LPS = XL + WL;
@@ -354,18 +490,21 @@ __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_mx4_gemm(
   u32x4 fx[TM], fw[2][TN];
   int ex[2][TM / 2], ew[2][TN / 2];
 
-  if constexpr (LORA16) {  // u and B of the tile (rows past it read zeros)
-    const rsrc_t rv = make_rs(V + m0 * 16, (uint32_t)(mrows * 64));
-    const rsrc_t rl = make_rs(L + n0 * 16, (uint32_t)(nrows * 32));
+  // the adapter's operands: one block of 16 ranks goes to LDS ahead of everything (tiles
+  // past the matrix read zeros)
+  const int mt = (mrows + 15) >> 4, nt = (nrows + 15) >> 4;
+  if constexpr (ONE) {
+    const rsrc_t ru = make_rs(su + m0 * 32, (uint32_t)(mt * 1024));
+    const rsrc_t rb = make_rs(bo + n0 * 16, (uint32_t)(nt * 512));
 #pragma unroll
     for (int k = 0; k < BM / 16 / G::WAVES; ++k) {
       const int q = BM / 16 / G::WAVES * wave + k;
-      dma16(rv, (uint32_t)(1024 * q + 16 * lane), 0, smem + G::LDS_V + 1024 * q);
+      dma16(ru, (uint32_t)(1024 * q + 16 * lane), 0, smem + G::LDS_V + 1024 * q);
     }
 #pragma unroll
     for (int k = 0; k < BN / 32 / G::WAVES; ++k) {
       const int q = BN / 32 / G::WAVES * wave + k;
-      dma16(rl, (uint32_t)(1024 * q + 16 * lane), 0, smem + G::LDS_L + 1024 * q);
+      dma16(rb, (uint32_t)(1024 * q + 16 * lane), 0, smem + G::LDS_L + 1024 * q);
     }
   }
 #pragma unroll
@@ -429,55 +568,50 @@ __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_mx4_gemm(
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   barrier_lds();
 
+  // (the lane's number anew: nothing of it has to last through the loop)
+  const int l = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
   // the adapter: acc += B (s u)^T, 16 ranks a product of 32: lane groups 0 and 1 carry the
   // bf16 high part of s u, 2 and 3 its remainder, against the same ranks of B
-  for (int j0 = 0; j0 < r; j0 += 16) {
-    const int jl = j0 + 8 * (g & 1);
-    bf16x8 lb[TN];
+  if constexpr (ONE) {
+    u32x4 lb[TN];
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const int row = 16 * (TN * wn + j) + n;
-      if constexpr (LORA16) {
-        lb[j] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(
-            smem + G::LDS_L + row * 32 + 16 * (g & 1)));
-      } else {
-        const uint16_t* lp = L + min(n0 + row, N - 1) * r;
-        uint32_t e[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) e[q] = jl + q < r ? lp[min(jl + q, r - 1)] : 0u;
-        lb[j] = __builtin_bit_cast(bf16x8, u32x4{e[0] | (e[1] << 16), e[2] | (e[3] << 16),
-                                                 e[4] | (e[5] << 16), e[6] | (e[7] << 16)});
-      }
-    }
+    for (int j = 0; j < TN; ++j)
+      lb[j] = *reinterpret_cast<const u32x4*>(smem + G::LDS_L + (TN * wn + j) * 512 +
+                                              16 * (l & 31));
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-      const int row = 16 * (TM * wm + i) + n;
-      float v[8];
-      if constexpr (LORA16) {
-        const uint8_t* vp = smem + G::LDS_V + row * 64 + 32 * (g & 1);
-        const f32x4 a = *reinterpret_cast<const f32x4*>(vp);
-        const f32x4 b = *reinterpret_cast<const f32x4*>(vp + 16);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          v[q] = a[q];
-          v[4 + q] = b[q];
-        }
-      } else {
-        const float* vp = V + min(m0 + row, M - 1) * r;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = jl + q < r ? vp[min(jl + q, r - 1)] : 0.f;
-      }
-      uint32_t w[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float a = s * v[2 * q], b = s * v[2 * q + 1];
-        const uint32_t hi = pack_bf16x2(a, b);
-        w[q] = g >= 2 ? pack_bf16x2(a - bf16_lo(hi), b - bf16_hi(hi)) : hi;
-      }
-      const bf16x8 vh = __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
+      const u32x4 v = *reinterpret_cast<const u32x4*>(smem + G::LDS_V + (TM * wm + i) * 1024 +
+                                                      16 * l);
 #pragma unroll
       for (int j = 0; j < TN; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lb[j], vh, acc[i][j], 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, lb[j]),
+                                                            __builtin_bit_cast(bf16x8, v),
+                                                            acc[i][j], 0, 0, 0);
+    }
+  } else {
+    // (tiles past the matrix repeat its last one: nothing of them is stored)
+    const u32x4 *up[TM], *bp[TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+      up[i] = reinterpret_cast<const u32x4*>(su) +
+              (m0 / 16 + min(TM * wm + i, mt - 1)) * nj * 64 + l;
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+      bp[j] = reinterpret_cast<const u32x4*>(bo) +
+              (n0 / 16 + min(TN * wn + j, nt - 1)) * nj * 32 + (l & 31);
+    for (int q = 0; q < nj; ++q) {
+      u32x4 v[TM], lb[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) lb[j] = bp[j][32 * q];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) v[i] = up[i][64 * q];
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, lb[j]),
+                                                              __builtin_bit_cast(bf16x8, v[i]),
+                                                              acc[i][j], 0, 0, 0);
     }
   }
 
@@ -485,7 +619,7 @@ __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_mx4_gemm(
   // wave's LDS staging tile, half the rows at a time, which leaves as rows of 32 TN bytes
   uint8_t* stg = smem + wave * G::OUTW;
   constexpr int LR = 2 * TN, RPS = 64 / LR;  // lanes of a row, rows a store
-  const int lc = lane % LR;
+  const int lc = l % LR;
   const int64_t col = n0 + 16 * TN * wn + 8 * lc;
   const bool whole = (N & 7) == 0;
 #pragma unroll
@@ -495,7 +629,7 @@ __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_mx4_gemm(
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
         const f32x4 c = acc[p * TM / 2 + i][j];
-        *reinterpret_cast<u32x2*>(stg + (16 * i + n) * G::OUTP + 2 * (16 * j + 4 * g)) =
+        *reinterpret_cast<u32x2*>(stg + (16 * i + (l & 15)) * G::OUTP + 2 * (16 * j + 4 * (l >> 4))) =
             u32x2{pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3])};
       }
     // (a wave's LDS accesses execute in order)
@@ -503,14 +637,14 @@ __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_mx4_gemm(
     if (whole) {
 #pragma unroll
       for (int q = 0; q < 8 * TM / RPS; ++q) {
-        const int rl = RPS * q + lane / LR;
+        const int rl = RPS * q + l / LR;
         const u32x4 v = *reinterpret_cast<const u32x4*>(stg + rl * G::OUTP + 16 * lc);
         if (row0 + rl < M && col < N)
           __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y + (row0 + rl) * N + col));
       }
     } else {  // rows of y on any element
       for (int q = 0; q < 8 * TM / RPS; ++q) {
-        const int rl = RPS * q + lane / LR;
+        const int rl = RPS * q + l / LR;
         const u32x4 v = *reinterpret_cast<const u32x4*>(stg + rl * G::OUTP + 16 * lc);
         if (row0 + rl >= M || col >= N) continue;
         uint16_t* dst = y + (row0 + rl) * N + col;
@@ -520,6 +654,98 @@ __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_mx4_gemm(
           for (int k = 0; col + k < N; ++k) dst[k] = (uint16_t)(v[k >> 1] >> (16 * (k & 1)));
       }
     }
+  }
+}
+
+// ---- The product of few rows: W is read once, straight into registers.  A workgroup
+// takes 16 NT rows of W and all of x's 16 MT, its waves the steps in turn; their sums meet
+// in LDS.  u comes whole or in S slices, which every workgroup adds (u_out: the first
+// one writes the sum).
+template <int MT, int NT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_mx4_rows(
+    const uint8_t* __restrict__ wc, const uint8_t* __restrict__ ws,
+    const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs, int M, int64_t N, int J,
+    const float* __restrict__ u, const float* __restrict__ upart, int S, float* __restrict__ u_out,
+    const uint16_t* __restrict__ B, int r, float s, uint16_t* __restrict__ y) {
+  constexpr int ROWS = 16 * NT, PITCH = ROWS + 4;
+  __shared__ __attribute__((aligned(16))) float sums[WAVES][16 * MT][PITCH];
+  extern __shared__ __attribute__((aligned(16))) float us[];  // u of all rows
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * ROWS;
+  const uint8_t *wp[NT], *xp[MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) wp[i] = wc + min(n0 + 16 * i + n, N - 1) * 128 * J + 16 * g;
+#pragma unroll
+  for (int i = 0; i < MT; ++i) xp[i] = xc + (int64_t)min(16 * i + n, M - 1) * 128 * J + 16 * g;
+  // (16 rows of W: their half of the 32 rows' scales)
+  const uint8_t* wsp = ws + n0 / 32 * J * 256 + 4 * lane + (NT == 1 ? 2 * ((n0 >> 4) & 1) : 0);
+  const uint32_t* xsp = reinterpret_cast<const uint32_t*>(xs) + lane;
+  f32x4 acc[NT][MT] = {};
+  constexpr int U = 2;  // steps whose loads go out together
+  for (int j0 = wave; j0 < J; j0 += U * WAVES) {
+    u32x4 a[U][NT][2], b[U][MT][2];
+    int sa[U], sb[U][(MT + 1) / 2];
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      const int64_t j = min(j0 + q * WAVES, J - 1);
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          a[q][i][t] = *reinterpret_cast<const u32x4*>(wp[i] + 128 * j + 64 * t);
+      sa[q] = NT == 1 ? (int)*reinterpret_cast<const uint16_t*>(wsp + 256 * j)
+                      : *reinterpret_cast<const int*>(wsp + 256 * j);
+    }
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      const int64_t j = min(j0 + q * WAVES, J - 1);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          b[q][i][t] = *reinterpret_cast<const u32x4*>(xp[i] + 128 * j + 64 * t);
+#pragma unroll
+      for (int i = 0; i < (MT + 1) / 2; ++i)  // (past M's groups: the last one's)
+        sb[q][i] = (int)xsp[(min(i, (M - 1) >> 5) * (int64_t)J + j) * 64];
+    }
+    unrolled<U>([&](auto q_t) {
+      constexpr int q = decltype(q_t)::value;
+      if (j0 + q * WAVES < J)
+        unrolled<2 * NT * MT>([&](auto k_t) {
+          constexpr int k = decltype(k_t)::value, t = k & 1, i = (k >> 1) % NT, m = (k >> 1) / NT;
+          acc[i][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              frag4(a[q][i][t]), frag4(b[q][m][t]), acc[i][m], 4, 4, 2 * i + t, sa[q],
+              2 * (m & 1) + t, sb[q][m >> 1]);
+        });
+    });
+  }
+  // u (all threads; while the last products run)
+  for (int e = tid; e < M * r; e += 64 * WAVES) {
+    const float t = S > 1 ? slice_sum(upart, (int64_t)M * r, S, e) : u[e];
+    us[e] = t;
+    if (u_out && blockIdx.x == 0) u_out[e] = t;
+  }
+  // lane: row 16 m + n of y, columns 16 i + 4 g + 0 .. 3
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      *reinterpret_cast<f32x4*>(&sums[wave][16 * m + n][16 * i + 4 * g]) = acc[i][m];
+  __syncthreads();
+  for (int e = tid; e < M * ROWS; e += 64 * WAVES) {
+    const int m = e / ROWS, c = e % ROWS;
+    if (n0 + c >= N) continue;
+    float t = sums[0][m][c];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) t += sums[w][m][c];
+    if (r > 0) {
+      float low = 0.f;
+      const uint16_t* bp = B + (n0 + c) * r;
+      for (int k = 0; k < r; ++k) low += us[m * r + k] * load_f32(bp + k);
+      t += s * low;
+    }
+    y[(int64_t)m * N + n0 + c] = to_bf16(t);
   }
 }
 
@@ -604,9 +830,7 @@ hipError_t launch_mx4_dequant_t(const Mx4& w, uint16_t* out, int64_t ldt, const 
 
 namespace {
 template <int WVM, int WVN, int TM, int TN>
-hipError_t launch_tiles(const Mx4& w, const uint8_t* xc, const uint8_t* xs, int64_t M,
-                        const float* u, const uint16_t* B, int r, float s, uint16_t* y,
-                        hipStream_t st) {
+hipError_t launch_tiles(const Mx4& w, const Mx4X& x, uint16_t* y, hipStream_t st) {
   using G = MxGeo<WVM, WVN, TM, TN>;
   static const hipError_t attr = [] {
     const hipError_t e = hipFuncSetAttribute(
@@ -619,32 +843,82 @@ hipError_t launch_tiles(const Mx4& w, const uint8_t* xc, const uint8_t* xs, int6
                      hipFuncAttributeMaxDynamicSharedMemorySize, G::LDS_MAIN);
   }();
   if (attr != hipSuccess) return attr;
-  const int64_t tm = (M + G::BM - 1) / G::BM, tn = (w.rows + G::BN - 1) / G::BN;
+  const int64_t tm = (x.M + G::BM - 1) / G::BM, tn = (w.rows + G::BN - 1) / G::BN;
   const dim3 grid((unsigned)(tm * tn)), block(G::THREADS);
-  const int J = (int)mx4_steps(w.cols);
-  if (r == 16)
+  const int J = (int)mx4_steps(w.cols), nj = (x.r + 15) / 16;
+  if (nj == 1)
     hipLaunchKernelGGL((k_mx4_gemm<WVM, WVN, TM, TN, true>), grid, block, G::LDS_BYTES, st, w.codes,
-                       w.scales, xc, xs, M, w.rows, J, u, B, r, s, y, (int)tm, (int)tn);
+                       w.scales, x.codes, x.scales, x.M, w.rows, J, x.su, x.bo, nj, y, (int)tm,
+                       (int)tn);
   else
     hipLaunchKernelGGL((k_mx4_gemm<WVM, WVN, TM, TN, false>), grid, block, G::LDS_MAIN, st, w.codes,
-                       w.scales, xc, xs, M, w.rows, J, u, B, r, s, y, (int)tm, (int)tn);
+                       w.scales, x.codes, x.scales, x.M, w.rows, J, x.su, x.bo, nj, y, (int)tm,
+                       (int)tn);
   return hipGetLastError();
+}
+
+template <int MT, int NT, int WAVES>
+hipError_t launch_rows(const Mx4& w, const Mx4X& x, const uint16_t* B, float s, uint16_t* y,
+                       hipStream_t st) {
+  const dim3 grid((unsigned)((w.rows + 16 * NT - 1) / (16 * NT)));
+  hipLaunchKernelGGL((k_mx4_rows<MT, NT, WAVES>), grid, dim3(64 * WAVES),
+                     (size_t)x.M * x.r * sizeof(float), st, w.codes, w.scales, x.codes, x.scales,
+                     (int)x.M, w.rows, (int)mx4_steps(w.cols), x.u, x.upart, x.S,
+                     x.S > 1 ? x.u : nullptr, B, x.r, s, y);
+  return hipGetLastError();
+}
+
+template <int RT, int NJ>
+hipError_t launch_x(const uint16_t* x, int64_t K, const Mx4X& o, const Drop& d, const uint16_t* A,
+                    const uint16_t* B, int64_t N, float s, hipStream_t st) {
+  const int J = (int)mx4_steps(K);
+  const int64_t b_wgs = o.bo ? ((N + 15) / 16 * NJ * 32 + 64 * kXWaves - 1) / (64 * kXWaves) : 0;
+  const dim3 grid((unsigned)(b_wgs + (o.M + 16 * RT - 1) / (16 * RT) * o.S));
+  if (d.on)
+    hipLaunchKernelGGL((k_mx4_x<RT, NJ, true>), grid, dim3(64 * kXWaves), 0, st, x, o.M, K, J, o.S,
+                       d, A, B, N, o.r, s, o.codes, o.scales, o.u, o.upart, o.su, o.bo, (int)b_wgs);
+  else
+    hipLaunchKernelGGL((k_mx4_x<RT, NJ, false>), grid, dim3(64 * kXWaves), 0, st, x, o.M, K, J, o.S,
+                       d, A, B, N, o.r, s, o.codes, o.scales, o.u, o.upart, o.su, o.bo, (int)b_wgs);
+  return hipGetLastError();
+}
+template <int RT>
+hipError_t launch_x(const uint16_t* x, int64_t K, const Mx4X& o, const Drop& d, const uint16_t* A,
+                    const uint16_t* B, int64_t N, float s, hipStream_t st) {
+  switch ((o.r + 15) / 16) {
+    case 1: return launch_x<RT, 1>(x, K, o, d, A, B, N, s, st);
+    case 2: return launch_x<RT, 2>(x, K, o, d, A, B, N, s, st);
+    case 3: return launch_x<RT, 3>(x, K, o, d, A, B, N, s, st);
+    default: return launch_x<RT, 4>(x, K, o, d, A, B, N, s, st);
+  }
 }
 }  // namespace
 
-hipError_t launch_mx4_mm(const Mx4& w, const uint8_t* xc, const uint8_t* xs, int64_t M,
-                         const float* u, const uint16_t* B, int r, float s, uint16_t* y,
+int mx4_x_slices(int64_t M, int64_t K) {
+  if (!mx4_few_rows(M)) return 1;
+  return (int)std::min<int64_t>(mx4_steps(K), 32);
+}
+
+hipError_t launch_mx4_x(const uint16_t* x, int64_t K, const Mx4X& o, const Drop& d,
+                        const uint16_t* A, const uint16_t* B, int64_t N, float s, hipStream_t st) {
+  if (o.r == 0) return launch_mx4_quant(x, false, o.M, K, o.codes, o.scales, st);
+  if (o.M >= 32 * 192) return launch_x<2>(x, K, o, d, A, B, N, s, st);
+  return launch_x<1>(x, K, o, d, A, B, N, s, st);
+}
+
+hipError_t launch_mx4_mm(const Mx4& w, const Mx4X& x, const uint16_t* B, float s, uint16_t* y,
                          hipStream_t st) {
-  if (M > 64) {
-    if ((M + 255) / 256 * ((w.rows + 255) / 256) >= 240)
-      return launch_tiles<2, 4, 8, 4>(w, xc, xs, M, u, B, r, s, y, st);
-    return launch_tiles<2, 2, 4, 4>(w, xc, xs, M, u, B, r, s, y, st);
+  if (mx4_few_rows(x.M)) {
+    const bool wide = w.rows >= 16 * 512;
+    if (x.M <= 16)
+      return wide ? launch_rows<1, 2, 8>(w, x, B, s, y, st)
+                  : launch_rows<1, 1, 16>(w, x, B, s, y, st);
+    if (x.M <= 32) return launch_rows<2, 2, 8>(w, x, B, s, y, st);
+    return launch_rows<4, 2, 8>(w, x, B, s, y, st);
   }
-  const uint32_t cols_wgs = (uint32_t)((w.rows + 127) / 128);
-  const dim3 grid(cols_wgs * (uint32_t)((M + 31) / 32));  // (at most 2^31)
-  hipLaunchKernelGGL(k_mx4_mm, grid, dim3(kThreads), 0, st, w.codes, w.scales, xc, xs, M, w.rows,
-                     (int)mx4_steps(w.cols), u, B, r, s, y, cols_wgs);
-  return hipGetLastError();
+  if ((x.M + 255) / 256 * ((w.rows + 255) / 256) >= 240)
+    return launch_tiles<2, 4, 8, 4>(w, x, y, st);
+  return launch_tiles<2, 2, 4, 4>(w, x, y, st);
 }
 
 }  // namespace qn

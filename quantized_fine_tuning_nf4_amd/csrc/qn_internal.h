@@ -435,9 +435,26 @@ hipError_t launch_mx4_dequant(const Mx4& w, bool f32, void* out, hipStream_t st)
 // rows <= n < ldt).  The jobs of aux run in extra workgroups of the same launch.
 hipError_t launch_mx4_dequant_t(const Mx4& w, uint16_t* out, int64_t ldt, const BwdAux& aux,
                                 hipStream_t st);
-// y [M, rows] bf16 = x W^T + s u B^T, x [M, cols] in MXFP4; r == 0: no second term.
-hipError_t launch_mx4_mm(const Mx4& w, const uint8_t* xc, const uint8_t* xs, int64_t M,
-                         const float* u, const uint16_t* B, int r, float s, uint16_t* y,
+// The linear's input as its product takes it.
+struct Mx4X {
+  int64_t M;
+  int r;            // 0: no adapter
+  uint8_t* codes;   // x [M, cols] in MXFP4
+  uint8_t* scales;
+  float* u;         // [M, r]
+  float* upart;     // [S, M, r] its slices when S > 1: launch_mx4_mm adds them into u
+  int S;            // mx4_x_slices(M, cols)
+  uint16_t* su;     // many rows: (s u) and B in the order of the product's lanes,
+  uint16_t* bo;     // 512 and 256 values for 16 rows and 16 ranks
+};
+// Batches whose product reads W straight into registers.
+inline bool mx4_few_rows(int64_t M) { return M <= 64; }
+int mx4_x_slices(int64_t M, int64_t K);
+// Fills o from x [M, K] (K % 64 == 0 with an adapter), u = drop(x) A^T.
+hipError_t launch_mx4_x(const uint16_t* x, int64_t K, const Mx4X& o, const Drop& d,
+                        const uint16_t* A, const uint16_t* B, int64_t N, float s, hipStream_t st);
+// y [M, rows] bf16 = x W^T + s u B^T.
+hipError_t launch_mx4_mm(const Mx4& w, const Mx4X& x, const uint16_t* B, float s, uint16_t* y,
                          hipStream_t st);
 
 }  // namespace qn

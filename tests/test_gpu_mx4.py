@@ -153,7 +153,8 @@ def test_product(qn, M, rows, cols):
 
 ADAPTED = [(1, 8, 64, 1), (2, 64, 128, 16), (16, 72, 192, 5), (31, 136, 320, 17), (40, 256, 1024, 64),
            (130, 264, 576, 16), (257, 512, 832, 33), (1, 1024, 4096, 16), (520, 768, 2048, 8),
-           (4000, 4104, 320, 16), (3841, 4000, 832, 40)]
+           (4000, 4104, 320, 16), (3841, 4000, 832, 40), (6150, 72, 128, 20), (6177, 256, 320, 7),
+           (50, 72, 640, 64), (33, 64, 2112, 3)]
 
 
 def _linear(qn, M, rows, cols, r, seed=0):
@@ -189,6 +190,26 @@ def test_forward(qn, M, rows, cols, r, p):
         none, no_u = qn.mx4_linear_fwd(w, d["x"], d["A"], d["B"], 2.0 * r, save_u=False,
                                        rslora=rslora, drop=drop)
         assert no_u is None and torch.equal(none, y)
+
+
+@pytest.mark.parametrize("M", [1, 16, 40, 70, 6145])
+@pytest.mark.parametrize("r", [0, 3, 40])
+def test_input_is_rounded_as_a_stored_matrix_is(qn, M, r):
+    """With W = 2^e I the product is x in MXFP4, times 2^e."""
+    say(f"[mx4 input] M={M} r={r}")
+    cols = 320
+    for e, lo, hi in ((0, -90, 90), (100, -133, -110)):
+        x = _normal(M + r, M, cols, dtype=torch.float32)
+        x *= torch.exp2(torch.randint(lo, hi, (M, cols // 32), device="cuda").float()
+                        ).repeat_interleave(32, dim=1)
+        x = x.to(torch.bfloat16)
+        x[0, 32:64], x[-1, 5] = 0.0, -0.0
+        w = qn.mx4_quantize(torch.eye(cols, device="cuda") * 2.0 ** e)
+        A = _normal(1, r, cols) if r else None
+        B = torch.zeros(cols, r, dtype=torch.bfloat16, device="cuda") if r else None
+        y, _ = qn.mx4_linear_fwd(w, x, A, B, 1.0)
+        want = qn.mx4_dequantize(qn.mx4_quantize(x), torch.float32).double() * 2.0 ** e
+        assert torch.equal(y.double(), want), (e, float((y.double() - want).abs().max()))
 
 
 def test_no_numbers_reach_their_rows_alone(qn):
