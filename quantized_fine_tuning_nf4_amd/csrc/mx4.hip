@@ -174,7 +174,6 @@ __global__ __launch_bounds__(kThreads) void k_mx4_dequant(const uint8_t* __restr
 // waves' sums of u meet in LDS, and the workgroup writes u and (s u) as the
 // product's epilogue takes it; else the slices' sums are written, for the product's
 // workgroups to add.
-constexpr int kXWaves = 8;
 __device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
                                                                 __builtin_bit_cast(u16x2, b)));
@@ -215,18 +214,18 @@ __device__ __forceinline__ void order_b(const uint16_t* B, int64_t N, int r, int
   reinterpret_cast<u32x4*>(out)[i] = u32x4{w[0], w[1], w[2], w[3]};
 }
 
-template <int RT, int NJ, bool DROP>
-__global__ __launch_bounds__(64 * kXWaves) void k_mx4_x(
+template <int RT, int NJ, bool DROP, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_mx4_x(
     const uint16_t* __restrict__ x, int64_t M, int64_t K, int J, int S, Drop d,
     const uint16_t* __restrict__ A, const uint16_t* __restrict__ B, int64_t N, int r, float s,
     uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, float* __restrict__ u,
     float* __restrict__ upart, uint16_t* __restrict__ su, uint16_t* __restrict__ bo, int b_wgs) {
   constexpr int PITCH = 16 * RT + 4;
-  __shared__ __attribute__((aligned(16))) float sums[kXWaves][16 * NJ][PITCH];
+  __shared__ __attribute__((aligned(16))) float sums[WAVES][16 * NJ][PITCH];
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   if ((int)blockIdx.x < b_wgs) {
-    const int64_t i = (int64_t)blockIdx.x * (64 * kXWaves) + tid;
+    const int64_t i = (int64_t)blockIdx.x * (64 * WAVES) + tid;
     if (i < (N + 15) / 16 * NJ * 32) order_b(B, N, r, NJ, i, bo);
     return;
   }
@@ -242,43 +241,47 @@ __global__ __launch_bounds__(64 * kXWaves) void k_mx4_x(
 #pragma unroll
   for (int q = 0; q < NJ; ++q) ap[q] = A + (int64_t)min(16 * q + n, r - 1) * K + 8 * g;
   f32x4 acc[RT][NJ] = {};
-  for (int j = j0 + wave; j < j1; j += kXWaves) {
+  for (int j = j0 + wave; j < j1; j += WAVES) {
     const int64_t k0 = (int64_t)j * kMx4Step;
     const int blocks = (int)min((K - k0) / kMx4Block, (int64_t)8);  // (K is a multiple of 64)
     u32x4 v[RT][8];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int b = 0; b < 8; ++b) {  // past the row: its first columns, zeroed below
+      for (int b = 0; b < 8; ++b)  // past the row: its first columns, zeroed below
         v[i][b] = *reinterpret_cast<const u32x4*>(xp[i] + (b < blocks ? k0 + 32 * b : 0));
-      }
+    constexpr int CB = NJ == 1 ? 8 : NJ == 2 ? 4 : 2;  // blocks whose rows of A come together
+    unrolled<8 / CB>([&](auto c_t) {
+      constexpr int c = decltype(c_t)::value * CB;
+      u32x4 a[CB][NJ];
 #pragma unroll
-    for (int b = 0; b < 8; ++b) {
-      if (b >= blocks) {
-#pragma unroll
-        for (int i = 0; i < RT; ++i) v[i][b] = u32x4{0u, 0u, 0u, 0u};
-        continue;
-      }
-      bf16x8 a[NJ];
-#pragma unroll
-      for (int q = 0; q < NJ; ++q) {
-        u32x4 w = *reinterpret_cast<const u32x4*>(ap[q] + k0 + 32 * b);
-        if (16 * q + n >= r) w = u32x4{0u, 0u, 0u, 0u};
-        a[q] = __builtin_bit_cast(bf16x8, w);
-      }
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        u32x4 w = v[i][b];
-        if constexpr (DROP) {
-          const int64_t m = min(m0 + 16 * i + n, M - 1);
-          w = drop8(w, philox(d, offset, (uint64_t)(m * K + k0 + 32 * b + 8 * g) >> 3), d.less);
-        }
+      for (int b = 0; b < CB; ++b)
 #pragma unroll
         for (int q = 0; q < NJ; ++q)
-          acc[i][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), a[q],
-                                                              acc[i][q], 0, 0, 0);
+          a[b][q] = *reinterpret_cast<const u32x4*>(ap[q] + (c + b < blocks ? k0 + 32 * (c + b) : 0));
+#pragma unroll
+      for (int b = 0; b < CB; ++b) {
+        const bool in = c + b < blocks;
+#pragma unroll
+        for (int q = 0; q < NJ; ++q)
+          if (!in || 16 * q + n >= r) a[b][q] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          if (!in) v[i][c + b] = u32x4{0u, 0u, 0u, 0u};
+          u32x4 w = v[i][c + b];
+          if constexpr (DROP) {
+            const int64_t m = min(m0 + 16 * i + n, M - 1);
+            w = drop8(w, philox(d, offset, (uint64_t)(m * K + k0 + 32 * (c + b) + 8 * g) >> 3),
+                      d.less);
+          }
+#pragma unroll
+          for (int q = 0; q < NJ; ++q)
+            acc[i][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, a[b][q]), acc[i][q], 0, 0,
+                0);
+        }
       }
-    }
+    });
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const int64_t m = m0 + 16 * i + n;
@@ -331,18 +334,18 @@ __global__ __launch_bounds__(64 * kXWaves) void k_mx4_x(
       *reinterpret_cast<f32x4*>(&sums[wave][16 * q + n][16 * i + 4 * g]) = acc[i][q];
   __syncthreads();
   float* dst = S > 1 ? upart + (int64_t)z * M * r : u;
-  for (int e = tid; e < 16 * RT * 16 * NJ; e += 64 * kXWaves) {
+  for (int e = tid; e < 16 * RT * 16 * NJ; e += 64 * WAVES) {
     const int row = e / (16 * NJ), j = e % (16 * NJ);
     float t = sums[0][j][row];
 #pragma unroll
-    for (int w = 1; w < kXWaves; ++w) t += sums[w][j][row];
+    for (int w = 1; w < WAVES; ++w) t += sums[w][j][row];
     sums[0][j][row] = t;  // (read and written by this thread alone)
     if (j < r && m0 + row < M) dst[(m0 + row) * r + j] = t;
   }
   if (!su) return;
   __syncthreads();
   // (s u): 16 rows and 16 ranks are 1 KB in the order of the product's lanes
-  for (int e = tid; e < 64 * RT * NJ; e += 64 * kXWaves) {
+  for (int e = tid; e < 64 * RT * NJ; e += 64 * WAVES) {
     const int l = e & 63, q = (e >> 6) % NJ, i = (e >> 6) / NJ;
     uint32_t w[4];
 #pragma unroll
@@ -660,16 +663,38 @@ __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_mx4_gemm(
 // ---- The product of few rows: W is read once, straight into registers.  A workgroup
 // takes 16 NT rows of W and all of x's 16 MT, its waves the steps in turn; their sums meet
 // in LDS.  u comes whole or in S slices, which every workgroup adds (u_out: the first
-// one writes the sum).
+// one writes the sum); its loads and those of B go out ahead of W's.
+constexpr int kFewSlices = 8;
+// ranks j .. j + 15 of a row of B (zero past r)
+__device__ __forceinline__ void load_ranks(const uint16_t* row, int j, int r, float v[16]) {
+  if ((r & 7) == 0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(row + min(j + 8 * h, r - 8));
+      const bool in = j + 8 * h < r;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[8 * h + 2 * q] = in ? bf16_lo(w[q]) : 0.f;
+        v[8 * h + 2 * q + 1] = in ? bf16_hi(w[q]) : 0.f;
+      }
+    }
+  } else {
+    uint16_t w[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) w[q] = row[min(j + q, r - 1)];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) v[q] = j + q < r ? as_f32((uint32_t)w[q] << 16) : 0.f;
+  }
+}
 template <int MT, int NT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_mx4_rows(
     const uint8_t* __restrict__ wc, const uint8_t* __restrict__ ws,
     const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs, int M, int64_t N, int J,
     const float* __restrict__ u, const float* __restrict__ upart, int S, float* __restrict__ u_out,
     const uint16_t* __restrict__ B, int r, float s, uint16_t* __restrict__ y) {
-  constexpr int ROWS = 16 * NT, PITCH = ROWS + 4;
+  constexpr int ROWS = 16 * NT, PITCH = ROWS + 4, THREADS = 64 * WAVES;
   __shared__ __attribute__((aligned(16))) float sums[WAVES][16 * MT][PITCH];
-  extern __shared__ __attribute__((aligned(16))) float us[];  // u of all rows
+  extern __shared__ __attribute__((aligned(16))) float us[];  // u, rows of 16 ceil(r / 16)
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t n0 = (int64_t)blockIdx.x * ROWS;
@@ -681,6 +706,17 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx4_rows(
   // (16 rows of W: their half of the 32 rows' scales)
   const uint8_t* wsp = ws + n0 / 32 * J * 256 + 4 * lane + (NT == 1 ? 2 * ((n0 >> 4) & 1) : 0);
   const uint32_t* xsp = reinterpret_cast<const uint32_t*>(xs) + lane;
+  // this thread's column of y, its row of B, its first element of u
+  const int c = tid % ROWS, rp = (r + 15) & ~15, mr = M * r;
+  const uint16_t* bp = B + min(n0 + c, N - 1) * r;
+  float bv[16], uv[kFewSlices];
+  if (r > 0) {
+#pragma unroll
+    for (int k = 0; k < kFewSlices; ++k)
+      uv[k] = S > 1 ? upart[min(k, S - 1) * (int64_t)mr + min(tid, mr - 1)]
+                    : u[min(tid, mr - 1)];
+    load_ranks(bp, 0, r, bv);
+  }
   f32x4 acc[NT][MT] = {};
   constexpr int U = 2;  // steps whose loads go out together
   for (int j0 = wave; j0 < J; j0 += U * WAVES) {
@@ -720,10 +756,16 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx4_rows(
         });
     });
   }
-  // u (all threads; while the last products run)
-  for (int e = tid; e < M * r; e += 64 * WAVES) {
-    const float t = S > 1 ? slice_sum(upart, (int64_t)M * r, S, e) : u[e];
-    us[e] = t;
+  for (int e = tid; e < mr; e += THREADS) {
+    float t = uv[0];
+    if (e == tid) {
+#pragma unroll
+      for (int k = 1; k < kFewSlices; ++k)
+        if (k < S) t += uv[k];
+    } else {
+      t = S > 1 ? slice_sum(upart, (int64_t)mr, S, e) : u[e];
+    }
+    us[e / r * rp + e % r] = t;
     if (u_out && blockIdx.x == 0) u_out[e] = t;
   }
   // lane: row 16 m + n of y, columns 16 i + 4 g + 0 .. 3
@@ -733,19 +775,17 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx4_rows(
     for (int m = 0; m < MT; ++m)
       *reinterpret_cast<f32x4*>(&sums[wave][16 * m + n][16 * i + 4 * g]) = acc[i][m];
   __syncthreads();
-  for (int e = tid; e < M * ROWS; e += 64 * WAVES) {
-    const int m = e / ROWS, c = e % ROWS;
-    if (n0 + c >= N) continue;
-    float t = sums[0][m][c];
+  for (int m = tid / ROWS; m < M; m += THREADS / ROWS) {
+    float t = sums[0][m][c], low = 0.f;
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) t += sums[w][m][c];
-    if (r > 0) {
-      float low = 0.f;
-      const uint16_t* bp = B + (n0 + c) * r;
-      for (int k = 0; k < r; ++k) low += us[m * r + k] * load_f32(bp + k);
-      t += s * low;
+    for (int j = 0; j < r; j += 16) {
+      if (r > 16) load_ranks(bp, j, r, bv);
+      const float* um = us + m * rp + j;
+#pragma unroll
+      for (int q = 0; q < 16; ++q) low += j + q < r ? um[q] * bv[q] : 0.f;
     }
-    y[(int64_t)m * N + n0 + c] = to_bf16(t);
+    if (n0 + c < N) y[(int64_t)m * N + n0 + c] = to_bf16(t + s * low);
   }
 }
 
@@ -862,48 +902,52 @@ hipError_t launch_rows(const Mx4& w, const Mx4X& x, const uint16_t* B, float s, 
                        hipStream_t st) {
   const dim3 grid((unsigned)((w.rows + 16 * NT - 1) / (16 * NT)));
   hipLaunchKernelGGL((k_mx4_rows<MT, NT, WAVES>), grid, dim3(64 * WAVES),
-                     (size_t)x.M * x.r * sizeof(float), st, w.codes, w.scales, x.codes, x.scales,
+                     (size_t)x.M * ((x.r + 15) / 16 * 16) * sizeof(float), st, w.codes, w.scales, x.codes,
+                     x.scales,
                      (int)x.M, w.rows, (int)mx4_steps(w.cols), x.u, x.upart, x.S,
                      x.S > 1 ? x.u : nullptr, B, x.r, s, y);
   return hipGetLastError();
 }
 
-template <int RT, int NJ>
+template <int RT, int NJ, int WAVES>
 hipError_t launch_x(const uint16_t* x, int64_t K, const Mx4X& o, const Drop& d, const uint16_t* A,
                     const uint16_t* B, int64_t N, float s, hipStream_t st) {
   const int J = (int)mx4_steps(K);
-  const int64_t b_wgs = o.bo ? ((N + 15) / 16 * NJ * 32 + 64 * kXWaves - 1) / (64 * kXWaves) : 0;
+  const int64_t b_wgs = o.bo ? ((N + 15) / 16 * NJ * 32 + 64 * WAVES - 1) / (64 * WAVES) : 0;
   const dim3 grid((unsigned)(b_wgs + (o.M + 16 * RT - 1) / (16 * RT) * o.S));
   if (d.on)
-    hipLaunchKernelGGL((k_mx4_x<RT, NJ, true>), grid, dim3(64 * kXWaves), 0, st, x, o.M, K, J, o.S,
-                       d, A, B, N, o.r, s, o.codes, o.scales, o.u, o.upart, o.su, o.bo, (int)b_wgs);
+    hipLaunchKernelGGL((k_mx4_x<RT, NJ, true, WAVES>), grid, dim3(64 * WAVES), 0, st, x, o.M, K, J,
+                       o.S, d, A, B, N, o.r, s, o.codes, o.scales, o.u, o.upart, o.su, o.bo,
+                       (int)b_wgs);
   else
-    hipLaunchKernelGGL((k_mx4_x<RT, NJ, false>), grid, dim3(64 * kXWaves), 0, st, x, o.M, K, J, o.S,
-                       d, A, B, N, o.r, s, o.codes, o.scales, o.u, o.upart, o.su, o.bo, (int)b_wgs);
+    hipLaunchKernelGGL((k_mx4_x<RT, NJ, false, WAVES>), grid, dim3(64 * WAVES), 0, st, x, o.M, K, J,
+                       o.S, d, A, B, N, o.r, s, o.codes, o.scales, o.u, o.upart, o.su, o.bo,
+                       (int)b_wgs);
   return hipGetLastError();
 }
-template <int RT>
+template <int RT, int WAVES>
 hipError_t launch_x(const uint16_t* x, int64_t K, const Mx4X& o, const Drop& d, const uint16_t* A,
                     const uint16_t* B, int64_t N, float s, hipStream_t st) {
   switch ((o.r + 15) / 16) {
-    case 1: return launch_x<RT, 1>(x, K, o, d, A, B, N, s, st);
-    case 2: return launch_x<RT, 2>(x, K, o, d, A, B, N, s, st);
-    case 3: return launch_x<RT, 3>(x, K, o, d, A, B, N, s, st);
-    default: return launch_x<RT, 4>(x, K, o, d, A, B, N, s, st);
+    case 1: return launch_x<RT, 1, WAVES>(x, K, o, d, A, B, N, s, st);
+    case 2: return launch_x<RT, 2, WAVES>(x, K, o, d, A, B, N, s, st);
+    case 3: return launch_x<RT, 3, WAVES>(x, K, o, d, A, B, N, s, st);
+    default: return launch_x<RT, 4, WAVES>(x, K, o, d, A, B, N, s, st);
   }
 }
 }  // namespace
 
 int mx4_x_slices(int64_t M, int64_t K) {
   if (!mx4_few_rows(M)) return 1;
-  return (int)std::min<int64_t>(mx4_steps(K), 32);
+  return (int)std::min<int64_t>(mx4_steps(K), kFewSlices);
 }
 
 hipError_t launch_mx4_x(const uint16_t* x, int64_t K, const Mx4X& o, const Drop& d,
                         const uint16_t* A, const uint16_t* B, int64_t N, float s, hipStream_t st) {
   if (o.r == 0) return launch_mx4_quant(x, false, o.M, K, o.codes, o.scales, st);
-  if (o.M >= 32 * 192) return launch_x<2>(x, K, o, d, A, B, N, s, st);
-  return launch_x<1>(x, K, o, d, A, B, N, s, st);
+  if (o.M > 4096) return launch_x<2, 8>(x, K, o, d, A, B, N, s, st);
+  if (mx4_few_rows(o.M)) return launch_x<1, 8>(x, K, o, d, A, B, N, s, st);
+  return launch_x<1, 16>(x, K, o, d, A, B, N, s, st);
 }
 
 hipError_t launch_mx4_mm(const Mx4& w, const Mx4X& x, const uint16_t* B, float s, uint16_t* y,
