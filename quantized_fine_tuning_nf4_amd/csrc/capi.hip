@@ -140,7 +140,7 @@ struct FwdWs {
 // (one set of x fragments for both products) do not take; such forwards use
 // the GEMM routes.  Every route takes every state format.
 FwdWs carve_fwd(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool need_u,
-                bool counters = true, bool dropout = false) {
+                bool counters = true, bool dropout = false, bool counter = false) {
   FwdWs f;
   f.arrivals = counters ? c.take<unsigned>(kArrivalWords) : nullptr;
   const bool dec = rows > 0 && !dropout;
@@ -151,7 +151,9 @@ FwdWs carve_fwd(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool ne
   f.S = thin_nt_slices(M, cols);
   f.u = need_u ? c.take<float>((size_t)M * r) : nullptr;
   f.upart = f.S > 1 && !decode ? c.take<float>((size_t)f.S * M * r) : nullptr;
-  f.wd = rows > 0 && M > 0 && !decode && dense_path(M, rows)
+  // (dropout from a counter: at every size, as in its backward; M = 100, 1024x1024: the
+  // product 26 us with the dequantizing one, 12 from the copy)
+  f.wd = rows > 0 && M > 0 && !decode && (counter || dense_path(M, rows))
              ? c.take<uint16_t>((size_t)rows * cols)
              : nullptr;
   f.dpart = f.dS > 0 ? c.take<float>((size_t)f.dS * M * rows) : nullptr;
@@ -164,13 +166,13 @@ FwdWs carve_fwd(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool ne
 struct BwdWs {
   unsigned* arrivals;  // [kArrivalWords] arrival counters
   FwdWs fu;      // recomputed u (if not saved)
-  uint16_t* Bt;  // [r, rows]; x in 8 bits: B in launch_thin_v's order, [rp, rows up to 32]
+  uint16_t* Bt;  // [r, rows]; three parts: B in launch_thin_v's order, [rp, rows up to 32]
   float* v;      // [M, r]
   float* vpart;  // [Sv, M, r]
   int Sv;
   float* dBpart;  // [Sb, rows, r]
   int Sb;
-  uint16_t* su;   // [2][rp][Mpb] (s u)^T high and remainder parts ([3]: x in 8 bits)
+  uint16_t* su;   // [2][rp][Mpb] (s u)^T high and remainder parts (or [3])
   float* dApart;  // [Sa, cols, r]
   int Sa;
   uint16_t* sv;   // [2][rp][Mpa] (s v)^T
@@ -180,9 +182,10 @@ struct BwdWs {
   uint8_t* bits;  // [M cols / 8] keep bits (dropout from a counter)
 };
 
+// three: u and v enter the adapter gradients in three parts (x in 8 bits, dropout from a
+// counter, MXFP4 weights).
 BwdWs carve_bwd(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool need_u,
-                bool act8 = false, bool need_dx = true, bool always_dense = false,
-                bool drop = false) {
+                bool three = false, bool need_dx = true, bool drop = false) {
   BwdWs b;
   b.arrivals = c.take<unsigned>(kArrivalWords);
   if (need_u) {
@@ -192,23 +195,23 @@ BwdWs carve_bwd(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, bool ne
     b.fu.S = 1;
   }
   const int64_t rp = 16 * ((r + 15) / 16);
-  b.Bt = c.take<uint16_t>((size_t)(act8 ? rp * round_up(rows, 32) : r * rows));
+  b.Bt = c.take<uint16_t>((size_t)(three ? rp * round_up(rows, 32) : r * rows));
   b.Sv = thin_nt_slices(M, rows);
   b.v = c.take<float>((size_t)M * r);
-  b.vpart = b.Sv > 1 && !act8 ? c.take<float>((size_t)b.Sv * M * r) : nullptr;
-  b.Sb = thin_tn_slices(M, rows, act8);
+  b.vpart = b.Sv > 1 && !three ? c.take<float>((size_t)b.Sv * M * r) : nullptr;
+  b.Sb = thin_tn_slices(M, rows, three);
   b.dBpart = c.take<float>((size_t)b.Sb * rows * r);
-  const size_t parts = act8 ? 3 : 2;
-  b.su = c.take<uint16_t>(parts * rp * thin_tn_rows_padded(M, rows, act8));
-  b.Sa = thin_tn_slices(M, cols, act8);
+  const size_t parts = three ? 3 : 2;
+  b.su = c.take<uint16_t>(parts * rp * thin_tn_rows_padded(M, rows, three));
+  b.Sa = thin_tn_slices(M, cols, three);
   b.dApart = c.take<float>((size_t)b.Sa * cols * r);
-  b.sv = c.take<uint16_t>(parts * rp * thin_tn_rows_padded(M, cols, act8));
+  b.sv = c.take<uint16_t>(parts * rp * thin_tn_rows_padded(M, cols, three));
   b.ldt = round_up(rows, 64);
-  // with x in 8 bits at every size: a weight read once and a product of few tiles
+  // with three parts at every size: a weight read once and a product of few tiles
   // beat the dequantizing product, whose tiles walk the rows of W at 57 us per
   // 1024 (M = 300, 4096x4096: 285 us with it, 55 from the copy; M = 1, 1024x4096:
   // 64 and 30; even at 64 rows, 24 us)
-  const bool dense = M > 0 && (act8 || always_dense ? need_dx : dense_path(M, cols));
+  const bool dense = M > 0 && (three ? need_dx : dense_path(M, cols));
   b.wt = dense ? c.take<uint16_t>((size_t)cols * b.ldt) : nullptr;
   b.At = dense ? c.take<uint16_t>((size_t)cols * r) : nullptr;
   b.bits = drop ? c.take<uint8_t>((size_t)M * cols / 8) : nullptr;
@@ -286,14 +289,14 @@ qn_status forward(const qn_nf4dq* w, const uint16_t* x, int64_t M, const uint16_
     return QN_EALIGN;
   Carver probe(nullptr);
   const bool drop = lo.mask != nullptr || lo.drop.on;
-  carve_fwd(probe, M, w->rows, w->cols, r, u_out == nullptr, true, drop);
+  carve_fwd(probe, M, w->rows, w->cols, r, u_out == nullptr, true, drop, lo.drop.on);
   if (probe.used > 0) {
     if (!workspace) return QN_EINVAL;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return QN_EALIGN;
     if (workspace_bytes < probe.used) return QN_EWORKSPACE;
   }
   Carver c(workspace);
-  FwdWs f = carve_fwd(c, M, w->rows, w->cols, r, u_out == nullptr, true, drop);
+  FwdWs f = carve_fwd(c, M, w->rows, w->cols, r, u_out == nullptr, true, drop, lo.drop.on);
   float* u = u_out ? u_out : f.u;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const float scale = lo.s;
@@ -406,46 +409,42 @@ qn_status backward(const Base& base, const uint16_t* x, const qn_act8* x8, const
     return from_hip(e);
   }
   Carver probe(nullptr);
-  const bool always_dense = base.mx != nullptr;  // MXFP4 has no dequantizing product
-  carve_bwd(probe, M, N, K, r, u_saved == nullptr, x8 != nullptr, dX != nullptr, always_dense,
-            lo.drop.on);
+  const bool three = x8 || base.mx || lo.drop.on;
+  carve_bwd(probe, M, N, K, r, u_saved == nullptr, three, dX != nullptr, lo.drop.on);
   if (!workspace) return QN_EINVAL;
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return QN_EALIGN;
   if (workspace_bytes < probe.used) return QN_EWORKSPACE;
   Carver c(workspace);
-  BwdWs b = carve_bwd(c, M, N, K, r, u_saved == nullptr, x8 != nullptr, dX != nullptr,
-                      always_dense, lo.drop.on);
+  BwdWs b = carve_bwd(c, M, N, K, r, u_saved == nullptr, three, dX != nullptr, lo.drop.on);
   const float scale = lo.s;
   hipError_t e = hipSuccess;
-  if (lo.drop.on) {
-    e = launch_keep_bits(M * K, lo.drop, b.bits, st);
-    lo.mask = b.bits;
-  }
+  if (lo.drop.on) lo.mask = b.bits;  // (drawn with the small jobs below)
   const float* u = u_saved;
   // an early launch of the call zeroes the arrival counters the adapter
   // gradients' launch counts on, so the backward never depends on what the
-  // workspace held before.  With x in 8 bits the slices of those gradients are
+  // workspace held before.  With three parts the slices of those gradients are
   // added by a launch of their own instead, unless the call is so short that it
   // waits for its launches: without dX 8192x4096x4096 at r = 16 40.3 -> 38.0 us,
   // 4096x4096x2048 at r = 8 25.8 -> 23.6, but 1024x1024x2048 17.3 -> 21.6; past 16
   // ranks a tile's last workgroup has too many values to add (4096x1024x4096 at
   // r = 64: 66 us for what takes 30)
   const bool few_launches = r <= 16 && M * (N + K) < (int64_t)1 << 24;
-  unsigned* arrivals = x8 && !few_launches ? nullptr : b.arrivals;
+  unsigned* arrivals = three && !few_launches ? nullptr : b.arrivals;
   Clear clr{arrivals, arrivals ? kArrivalWords : 0};
   if (!u && e == hipSuccess) {
-    e = launch_thin_nt(x, A, M, K, r, b.fu.u, b.fu.upart, b.fu.S, st, true, false, clr, lo.mask);
+    e = launch_thin_nt(x, A, M, K, r, b.fu.u, b.fu.upart, b.fu.S, st, true, false, clr,
+                       lo.drop.on ? nullptr : lo.mask, lo.drop);
     clr = Clear{nullptr, 0};
     u = b.fu.u;
   }
-  // v = G B.  With x in 8 bits: whole, and (s v)^T with it, from B in the order of
+  // v = G B.  With three parts: whole, and (s v)^T with it, from B in the order of
   // the product's operands, made first (and with that (s u)^T, and A^T for the dense
   // dX product; in spare workgroups of the transposed dequantization when there is
   // one).  Else in slices
   // (added below); the product takes B as stored when it can, else B^T made first.
   const bool b_rows = thin_nt_rows_ok(M, N, r);
   const bool dense_dx = dX && b.wt;
-  if (e == hipSuccess && x8) {
+  if (e == hipSuccess && three) {
     BwdAux t{};
     t.B = B;
     t.Bf = b.Bt;
@@ -457,6 +456,11 @@ qn_status backward(const Base& base, const uint16_t* x, const qn_act8* x8, const
     t.r = r;
     t.s = scale;
     t.three_parts = true;
+    if (lo.drop.on) {
+      t.drop = lo.drop;
+      t.bits = b.bits;
+      t.bits64 = M * K / 64;
+    }
     t.A = A;
     t.At = dense_dx ? b.At : nullptr;
     t.K = K;
@@ -468,7 +472,7 @@ qn_status backward(const Base& base, const uint16_t* x, const qn_act8* x8, const
       e = launch_thin_v(dY, b.Bt, M, N, r, b.v, b.sv, thin_tn_rows_padded(M, K, true), scale, st,
                         clr);
   }
-  if (e == hipSuccess && !x8 && !b_rows) {
+  if (e == hipSuccess && !three && !b_rows) {
     if (clr.n) {  // (no earlier launch: a kernel, not a memset, for graph capture)
       e = launch_fill_zero(reinterpret_cast<float*>(clr.p), clr.n, st);
       clr = Clear{nullptr, 0};
@@ -480,13 +484,13 @@ qn_status backward(const Base& base, const uint16_t* x, const qn_act8* x8, const
     t.r = r;
     e = launch_bwd_aux(t, st);
   }
-  if (e == hipSuccess && !x8)
+  if (e == hipSuccess && !three)
     e = launch_thin_nt(dY, b_rows ? B : b.Bt, M, N, r, b.v, b.vpart, b.Sv, st, false, b_rows,
                        clr);
   // the small jobs: v's slice sum, (s u)^T and (s v)^T split for the
   // transposed products, A^T for the dense dX product; in spare workgroups of
   // the transposed dequantization when there is one
-  if (e == hipSuccess && !x8) {
+  if (e == hipSuccess && !three) {
     BwdAux aux{};
     aux.A = A;
     aux.At = dense_dx ? b.At : nullptr;
@@ -518,7 +522,7 @@ qn_status backward(const Base& base, const uint16_t* x, const qn_act8* x8, const
     e = launch_thin_tn2(ThinTn{dY, b.su, N, dB, false, b.dBpart},
                         ThinTn{x, b.sv, K, dA, true, b.dApart, lo.mask, x8 ? x8->codes : nullptr,
                                x8 ? x8->exps : nullptr},
-                        M, r, arrivals, st);
+                        M, r, three, arrivals, st);
   return from_hip(e);
 }
 
@@ -1011,9 +1015,9 @@ size_t qlora_linear_drop_workspace(int64_t M, int64_t rows, int64_t cols, int r,
     return 0;
   Carver c(nullptr);
   if (backward)
-    carve_bwd(c, M, rows, cols, r, !act8, act8 != 0, true, false, true);
+    carve_bwd(c, M, rows, cols, r, !act8, true, true, true);
   else
-    carve_fwd(c, M, rows, cols, r, true, true, true);
+    carve_fwd(c, M, rows, cols, r, true, true, true, true);
   return c.used;
 }
 
@@ -1082,7 +1086,7 @@ size_t mx4_linear_workspace(int64_t M, int64_t rows, int64_t cols, int r, int ba
   else if (r == 0)
     carve_mx4_dx(c, rows, cols);
   else
-    carve_bwd(c, M, rows, cols, r, !act8, act8 != 0, true, true, drop != 0);
+    carve_bwd(c, M, rows, cols, r, !act8, true, true, drop != 0);
   return c.used;
 }
 

@@ -1,6 +1,5 @@
-// Dropout without a stored mask (generator and element order in qn_device.h): an
-// activation by itself, and the keep bits of a linear's input for the products of
-// one backward call.
+// Dropout of an activation without a stored mask (generator and element order in
+// qn_device.h).
 #include "qn_device.h"
 #include "qn_internal.h"
 
@@ -62,18 +61,6 @@ __global__ __launch_bounds__(kThreads) void k_dropout(const T* x, int64_t n, Dro
   }
 }
 
-// The keep bits of n elements (a multiple of 32), four bytes a thread.
-__global__ __launch_bounds__(kThreads) void k_keep_bits(int64_t words, Drop d, uint32_t* bits) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= words) return;
-  const uint64_t offset = drop_offset(d);
-  uint32_t b = 0;
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    b |= keep_byte(philox(d, offset, (uint64_t)(4 * i + q)), d.less) << (8 * q);
-  bits[i] = b;
-}
-
 }  // namespace
 
 hipError_t launch_dropout(const void* x, bool f32, int64_t n, const Drop& d, float scale,
@@ -86,14 +73,6 @@ hipError_t launch_dropout(const void* x, bool f32, int64_t n, const Drop& d, flo
   else
     hipLaunchKernelGGL(k_dropout<uint16_t>, dim3((unsigned)wgs), dim3(kThreads), 0, st,
                        static_cast<const uint16_t*>(x), n, d, scale, static_cast<uint16_t*>(out));
-  return hipGetLastError();
-}
-
-hipError_t launch_keep_bits(int64_t n, const Drop& d, uint8_t* bits, hipStream_t st) {
-  const int64_t words = n / 32;
-  if (words <= 0) return hipSuccess;
-  hipLaunchKernelGGL(k_keep_bits, dim3((unsigned)((words + kThreads - 1) / kThreads)),
-                     dim3(kThreads), 0, st, words, d, reinterpret_cast<uint32_t*>(bits));
   return hipGetLastError();
 }
 

@@ -553,7 +553,7 @@ struct TnJob {
   const uint8_t* zmask;  // keep bits of Z (dropout on x), or null
 };
 
-// With an 8-bit checkpoint (one-dimensional grid): workgroups of a job per XCD.
+// With (s V)^T in three parts (one-dimensional grid): workgroups of a job per XCD.
 // The XCDs take workgroups round robin; each takes a run of each job's
 // workgroups, ordered slice by slice, so that an XCD's L2 holds the (s V)^T of its
 // own slices alone (an eighth of it) rather than all of it, and every XCD has the
@@ -588,7 +588,7 @@ __device__ __forceinline__ void wait_vm() {
 // lane's eight rows of its wave's word are 32 bytes in a row, and the dropped
 // values are zeroed in the A operand after the transposed reads.
 //
-// Z8: the second job's Z is an 8-bit checkpoint.  Its 32 rows of 128 codes are
+// Z8: the second job's Z may be an 8-bit checkpoint (else it has no codes).  Its 32 rows of 128 codes are
 // half the bytes of bf16 rows: one 16-byte-per-lane load per wave (8 rows each;
 // row y's 16-byte chunk c at unit c ^ ((y >> 1) & 7), so that the 16 rows of a
 // transposed read fill 256 bytes of banks), read as columns by
@@ -643,7 +643,7 @@ __global__ __launch_bounds__(kThreads) void k_thin_tn(TnJob j0, TnJob j1, int64_
   float* part = second ? j1.part : j0.part;
   const uint8_t* zmask = MASK ? (second ? j1.zmask : j0.zmask) : nullptr;
   const bool hm = MASK && zmask != nullptr;  // workgroup-uniform
-  const bool z8 = Z8 && second;              // workgroup-uniform
+  const bool z8 = Z8 && second && j1.codes != nullptr;  // workgroup-uniform
   if (z_wg >= S) return;  // past the job's workgroups
   const int64_t p0 = (int64_t)pt_wg * TN_COLS;
   const int64_t mb = (int64_t)z_wg * slice;
@@ -1042,12 +1042,12 @@ __global__ void k_sum_parts(TnSum a, TnSum b, int r) {
 // column tile: the tile's last workgroup adds the slices, and with 64 of them
 // (a 1024-column dB at M = 4096) that sum took longer than the products
 // (the k_proj backward's dA/dB launch: 24 us).
-// With x in 8 bits (act8) at most 8: a slice's partial sums weigh as much
+// With three parts at most 8: from x in 8 bits a slice's partial sums weigh as much
 // against half the bytes of x, and the sums are nearer (4096x1024x4096, r = 64:
 // 48.4 -> 45.8 us; 8192x4096x4096, r = 16: 45.0 -> 43.1).
-int64_t thin_tn_slice_rows(int64_t M, int64_t P, bool act8) {
+int64_t thin_tn_slice_rows(int64_t M, int64_t P, bool three) {
   const int64_t pt = (P + TN_COLS - 1) / TN_COLS;
-  const int64_t S = std::min<int64_t>((512 + pt - 1) / pt, act8 ? 8 : 16);
+  const int64_t S = std::min<int64_t>((512 + pt - 1) / pt, three ? 8 : 16);
   int64_t slice = (M + S - 1) / S;
   slice = (slice + 31) / 32 * 32;
   const int64_t cap = ((((int64_t)1 << 31) - 1) / std::max<int64_t>(2 * P, 384)) / 32 * 32;
@@ -1056,20 +1056,21 @@ int64_t thin_tn_slice_rows(int64_t M, int64_t P, bool act8) {
   return slice;
 }
 
-int thin_tn_slices(int64_t M, int64_t P, bool act8) {
-  const int64_t slice = thin_tn_slice_rows(M, P, act8);
+int thin_tn_slices(int64_t M, int64_t P, bool three) {
+  const int64_t slice = thin_tn_slice_rows(M, P, three);
   return (int)((M + slice - 1) / slice);
 }
 
 // Row length of the staged (sV)^T: every slice's rows exist (zero past M).
-int64_t thin_tn_rows_padded(int64_t M, int64_t P, bool act8) {
-  return (int64_t)thin_tn_slices(M, P, act8) * thin_tn_slice_rows(M, P, act8);
+int64_t thin_tn_rows_padded(int64_t M, int64_t P, bool three) {
+  return (int64_t)thin_tn_slices(M, P, three) * thin_tn_slice_rows(M, P, three);
 }
 
-hipError_t launch_thin_tn2(const ThinTn& a, const ThinTn& b, int64_t M, int r,
+hipError_t launch_thin_tn2(const ThinTn& a, const ThinTn& b, int64_t M, int r, bool three,
                            unsigned* arrivals, hipStream_t st) {
   const int nj = (r + 15) / 16;
-  const bool z8 = b.codes != nullptr;
+  const bool z8 = three;  // (codes or bf16 by the second job itself)
+  if (b.codes && !three) return hipErrorInvalidValue;
   TnJob job[2];
   const ThinTn* in[2] = {&a, &b};
   int s_max = 1;

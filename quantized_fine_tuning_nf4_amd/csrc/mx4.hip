@@ -416,19 +416,13 @@ __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_mx4_gemm(
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WVN, wn = wave % WVN;
 
   // tile order: each XCD (they take workgroups round robin) a contiguous run of the
-  // tiles, four tile rows at a time across the columns
-  int bid = blockIdx.x;
-  const int ntiles = tiles_m * tiles_n;
-  if (ntiles % 8 == 0) bid = (bid & 7) * (ntiles >> 3) + (bid >> 3);
-  int tm, tn;
-  if (tiles_m % 4 == 0) {
-    const int grp = bid / (4 * tiles_n), in = bid % (4 * tiles_n);
-    tm = 4 * grp + (in & 3);
-    tn = in >> 2;
-  } else {
-    tm = bid / tiles_n;
-    tn = bid % tiles_n;
-  }
+  // tiles, which go down up to four tile rows at a time and then across the columns, so
+  // that the workgroups that share an L2 share rows of both operands
+  const int ntiles = tiles_m * tiles_n, xcd = blockIdx.x & 7;
+  const int bid = xcd * (ntiles >> 3) + min(xcd, ntiles & 7) + (blockIdx.x >> 3);
+  const int grp = bid / (4 * tiles_n), in = bid - grp * 4 * tiles_n;
+  const int deep = min(4, tiles_m - 4 * grp);
+  int tm = 4 * grp + in % deep, tn = in / deep;
   tm = __builtin_amdgcn_readfirstlane(tm);
   tn = __builtin_amdgcn_readfirstlane(tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
@@ -789,47 +783,58 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx4_rows(
   }
 }
 
-// out[k][n] = W[n][k] as bf16, row length ldt (zero for rows <= n < ldt).  A
-// workgroup takes 32 rows x 256 columns as above, through LDS.
+// out[k][n] = W[n][k] as bf16, row length ldt (zero for rows <= n < ldt).  A workgroup
+// takes 128 rows x 128 columns through LDS: thread (q, l) = (t / 64, t % 64) the block q
+// of rows 2 l and 2 l + 1, whose columns leave as pairs of rows, a word each.
+constexpr int kDtRows = 128, kDtPitch = 2 * kDtRows + 16;
 __global__ __launch_bounds__(kThreads) void k_mx4_dequant_t(
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows,
-    int64_t K, int J, uint16_t* __restrict__ out, int64_t ldt, BwdAux aux, int aux_wgs) {
-  constexpr int PITCH = 32 + 2;  // values of a column of the tile
-  __shared__ uint16_t tile[256 * PITCH];
+    int64_t K, int J, uint16_t* __restrict__ out, int64_t ldt, BwdAux aux, int aux_wgs, int gx) {
+  __shared__ __attribute__((aligned(16))) uint8_t tile[128 * kDtPitch];
   const int t = threadIdx.x;
   if ((int)blockIdx.x < aux_wgs) {  // one job per thread
     const int64_t i = (int64_t)blockIdx.x * kThreads + t;
     if (i < bwd_aux_count(aux)) bwd_aux_at(aux, i);
     return;
   }
-  const int64_t d = (int64_t)blockIdx.x - aux_wgs, R = d / J, j = d - R * J;
-  const int64_t rr = (rows + 31) / 32;  // (ldt may go past the scales' last 32 rows)
+  const int64_t d = (int64_t)blockIdx.x - aux_wgs, kh = d / gx;
+  const int64_t n0 = (d - kh * gx) * kDtRows, k0 = kh * 128;
+  const int q = t >> 6, l = t & 63, j = (int)(kh >> 1), b = 4 * (int)(kh & 1) + q;
+  u32x4 c[2];
+  float s[2];
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const int n = 8 * p + (t >> 5);
-    const int64_t row = 32 * R + n;
-    float v[8] = {};
-    if (row < rows) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + row * 128 * J + 128 * j +
-                                                            4 * (t & 31));
-      decode8(w, mx4_scale(scales[(min(R, rr - 1) * J + j) * 256 +
-                                  mx4_scale_at(n, (t & 31) >> 2)]), v);
+  for (int i = 0; i < 2; ++i) {
+    const int64_t row = n0 + 2 * l + i, rr = min(row, rows - 1);
+    c[i] = *reinterpret_cast<const u32x4*>(codes + rr * 128 * J + 128 * j + 16 * b);
+    s[i] = mx4_scale(scales[((rr >> 5) * J + j) * 256 + mx4_scale_at((int)(rr & 31), b)]);
+    if (row >= rows) {
+      c[i] = u32x4{0u, 0u, 0u, 0u};
+      s[i] = 1.f;
     }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) tile[(8 * (t & 31) + q) * PITCH + n] = to_bf16(v[q]);
   }
+  uint8_t* trow = tile + 32 * q * kDtPitch + 4 * l;
+  unrolled<4>([&](auto w_t) {
+    constexpr int w = decltype(w_t)::value;
+    const uint32_t ca = c[0][w], cb = c[1][w];
+    unrolled<4>([&](auto p_t) {  // columns 8 w + 2 p, + 1
+      constexpr int p = decltype(p_t)::value;
+      const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(ca, 1.f, p);
+      const f32x2 e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cb, 1.f, p);
+      const float a0 = a[0], a1 = a[1], e0 = e[0], e1 = e[1];
+      *reinterpret_cast<uint32_t*>(trow + (8 * w + 2 * p) * kDtPitch) =
+          pack_bf16x2(a0 * s[0], e0 * s[1]);
+      *reinterpret_cast<uint32_t*>(trow + (8 * w + 2 * p + 1) * kDtPitch) =
+          pack_bf16x2(a1 * s[0], e1 * s[1]);
+    });
+  });
   __syncthreads();
-  // thread: column t of the step, 32 values
-  const int64_t k = j * kMx4Step + t;
-  if (k >= K) return;
-  uint16_t* dst = out + k * ldt + 32 * R;
+  // 128 rows of 256 bytes: pass h, thread t -> row 16 h + t / 16, chunk t % 16
+  const int64_t col = n0 + 8 * (t & 15);
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint32_t w[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      w[q] = *reinterpret_cast<const uint32_t*>(tile + t * PITCH + 8 * c + 2 * q);
-    *reinterpret_cast<u32x4*>(dst + 8 * c) = u32x4{w[0], w[1], w[2], w[3]};
+  for (int h = 0; h < 8; ++h) {
+    const int k = 16 * h + (t >> 4);
+    const u32x4 v = *reinterpret_cast<const u32x4*>(tile + k * kDtPitch + 16 * (t & 15));
+    if (col < ldt && k0 + k < K) *reinterpret_cast<u32x4*>(out + (k0 + k) * ldt + col) = v;
   }
 }
 
@@ -862,9 +867,11 @@ hipError_t launch_mx4_dequant(const Mx4& w, bool f32, void* out, hipStream_t st)
 
 hipError_t launch_mx4_dequant_t(const Mx4& w, uint16_t* out, int64_t ldt, const BwdAux& aux,
                                 hipStream_t st) {
-  const int64_t J = mx4_steps(w.cols), wgs = (bwd_aux_count(aux) + kThreads - 1) / kThreads;
-  hipLaunchKernelGGL(k_mx4_dequant_t, dim3((unsigned)(wgs + ldt / 32 * J)), dim3(kThreads), 0, st,
-                     w.codes, w.scales, w.rows, w.cols, (int)J, out, ldt, aux, (int)wgs);
+  const int64_t wgs = (bwd_aux_count(aux) + kThreads - 1) / kThreads;
+  const int64_t gx = (ldt + kDtRows - 1) / kDtRows, gk = (w.cols + 127) / 128;
+  hipLaunchKernelGGL(k_mx4_dequant_t, dim3((unsigned)(wgs + gx * gk)), dim3(kThreads), 0, st,
+                     w.codes, w.scales, w.rows, w.cols, (int)mx4_steps(w.cols), out, ldt, aux,
+                     (int)wgs, (int)gx);
   return hipGetLastError();
 }
 
@@ -937,6 +944,19 @@ hipError_t launch_x(const uint16_t* x, int64_t K, const Mx4X& o, const Drop& d, 
 }
 }  // namespace
 
+namespace {
+int64_t compute_units() {
+  static const int n = [] {
+    int dev = 0, cus = 0;
+    if (hipGetDevice(&dev) != hipSuccess ||
+        hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+      return 256;
+    return cus > 0 ? cus : 256;
+  }();
+  return n;
+}
+}  // namespace
+
 int mx4_x_slices(int64_t M, int64_t K) {
   if (!mx4_few_rows(M)) return 1;
   return (int)std::min<int64_t>(mx4_steps(K), kFewSlices);
@@ -960,7 +980,15 @@ hipError_t launch_mx4_mm(const Mx4& w, const Mx4X& x, const uint16_t* B, float s
     if (x.M <= 32) return launch_rows<2, 2, 8>(w, x, B, s, y, st);
     return launch_rows<4, 2, 8>(w, x, B, s, y, st);
   }
-  if ((x.M + 255) / 256 * ((w.rows + 255) / 256) >= 240)
+  // 256 x 256 tiles, one a compute unit, or 128 x 128, two: a round of the small ones
+  // takes 0.57 of a round of the large ones (8192x4096x4096: 84 us in 4 against 74 in 2), so
+  // the large ones where they need no more than 0.6 as many (301x50021x1000, 2 rounds and
+  // 3: 28.9 us and 23.8; 4096x14336x4096, 4 and 7: 134 and 155)
+  const int64_t cu = compute_units();
+  const auto rounds = [&](int64_t t, int64_t at_once) {
+    return ((x.M + t - 1) / t * ((w.rows + t - 1) / t) + at_once - 1) / at_once;
+  };
+  if (10 * rounds(256, cu) <= 6 * rounds(128, 2 * cu))
     return launch_tiles<2, 4, 8, 4>(w, x, y, st);
   return launch_tiles<2, 2, 4, 4>(w, x, y, st);
 }

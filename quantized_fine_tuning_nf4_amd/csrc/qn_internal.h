@@ -80,9 +80,12 @@ struct BwdAux {
   int r;
   float s;
   bool three_parts;
+  Drop drop;       // keep bits of `bits64` times 64 elements (dropout from a counter)
+  uint8_t* bits;
+  int64_t bits64;
 };
 constexpr int kAuxRanks = 4;
-// The jobs but Bf's are rows in blocks of kAuxRanks ranks (16 ceil(r / 16) in all),
+// The jobs but the keep bits' and Bf's are rows in blocks of kAuxRanks ranks (16 ceil(r / 16) in all),
 // one per thread: a row n of B (Bt[j][n] = B[n][j]), a column k of A (At[k][j] =
 // A[j][k]), a column m of su and of sv.  A thread reads its ranks of B, u or v's
 // slices in one load when r allows, the threads of a wave read neighbouring
@@ -94,7 +97,7 @@ __host__ __device__ inline int64_t bwd_frags(const BwdAux& a) {  // 16-byte piec
   return a.Bf ? (a.N + 31) / 32 * 64 * ((a.r + 15) / 16) : 0;
 }
 __host__ __device__ inline int64_t bwd_aux_count(const BwdAux& a) {
-  return bwd_frags(a) +
+  return (a.bits ? a.bits64 : 0) + bwd_frags(a) +
          ((a.Bt ? a.N : 0) + (a.At ? a.K : 0) + (a.su ? a.Mpu : 0) + (a.sv ? a.Mpv : 0)) *
          ((a.r + 15) / 16 * (16 / kAuxRanks));
 }
@@ -108,12 +111,24 @@ __device__ inline void put_split(uint16_t* dst, int64_t half, int64_t idx, float
   dst[half + idx] = (uint16_t)l;
   if (three) dst[2 * half + idx] = (uint16_t)(pack_bf16x2(rest - bf16_lo(l), 0.f) & 0xffffu);
 }
-// job i of the concatenated jobs (Bf; then by rows Bt, At, su, sv in that order, a
-// block of ranks of all of them before the next block)
+// job i of the concatenated jobs (keep bits; Bf; then by rows Bt, At, su, sv in that
+// order, a block of ranks of all of them before the next block)
 __device__ inline void bwd_aux_at(const BwdAux& a, int64_t i) {
   const int r = a.r;
   const int64_t rp = 16 * ((r + 15) / 16);
-  const int64_t frags = bwd_frags(a);
+  const int64_t frags = bwd_frags(a), bits = a.bits ? a.bits64 : 0;
+  if (i < bits) {
+    const uint64_t offset = drop_offset(a.drop);
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll 2
+    for (int q = 0; q < 8; ++q) {
+      const uint32_t b = keep_byte(philox(a.drop, offset, (uint64_t)(8 * i + q)), a.drop.less);
+      if (q < 4) w[0] |= b << (8 * q); else w[1] |= b << (8 * (q - 4));
+    }
+    reinterpret_cast<u32x2*>(a.bits)[i] = u32x2{w[0], w[1]};
+    return;
+  }
+  i -= bits;
   if (i < frags) {  // rows n .. n + 7 of rank j
     const int64_t n = i / (4 * rp) * 32 + (i >> 4) % 4 * 8, j = (i >> 6) % (rp / 16) * 16 + i % 16;
     uint32_t w[4] = {0u, 0u, 0u, 0u};
@@ -124,7 +139,7 @@ __device__ inline void bwd_aux_at(const BwdAux& a, int64_t i) {
     return;
   }
   i -= frags;
-  const int64_t rows = (bwd_aux_count(a) - frags) / (rp / kAuxRanks);
+  const int64_t rows = (bwd_aux_count(a) - bits - frags) / (rp / kAuxRanks);
   const int jb = (int)(i / rows) * kAuxRanks;  // this block's ranks: jb .. je - 1
   i %= rows;
   const int je = min(jb + kAuxRanks, r);
@@ -298,8 +313,8 @@ hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t st);
 // One transposed adapter product out = Z^T (s V), reduced over the M rows:
 // Z bf16 [M, P] (null: no product) or, for the second product, an 8-bit
 // checkpoint of it (codes and exps; P % 64 == 0), vt = (s V)^T split as BwdAux
-// makes it (in three parts for both products when there are codes) up to row
-// thin_tn_rows_padded(M, P, act8); transposed == false: out fp32 [P, r]; true: out
+// makes it (with `three` in three parts for both products, as codes need it) up to row
+// thin_tn_rows_padded(M, P, three); transposed == false: out fp32 [P, r]; true: out
 // fp32 [r, P].  Split over thin_tn_slices(M, P, act8) row slices with partials
 // part[S][P][r], summed in slice order.  P % 8 == 0.
 struct ThinTn {
@@ -317,10 +332,10 @@ struct ThinTn {
 // the last workgroup of each column tile to finish (arrivals: kArrivalWords
 // counters, zero at the launch and left at zero), or, past kArrivalWords
 // column tiles or with arrivals == null, by a second launch.
-hipError_t launch_thin_tn2(const ThinTn& a, const ThinTn& b, int64_t M, int r,
+hipError_t launch_thin_tn2(const ThinTn& a, const ThinTn& b, int64_t M, int r, bool three,
                            unsigned* arrivals, hipStream_t st);
-int thin_tn_slices(int64_t M, int64_t P, bool act8);
-int64_t thin_tn_rows_padded(int64_t M, int64_t P, bool act8);
+int thin_tn_slices(int64_t M, int64_t P, bool three);
+int64_t thin_tn_rows_padded(int64_t M, int64_t P, bool three);
 
 // Decode forward, u = X A^T included (written to u_out [M, r]); workspace
 // part [S, M, rows] and upart [S, M, r] fp32, S = decode_slices(...).
@@ -411,11 +426,9 @@ hipError_t launch_logprobs_bwd(const void* x, bool f32, int64_t T, int64_t V, in
                                void* dx, int64_t ldd, hipStream_t st);
 
 // Dropout from a counter (qn_device.h): out = x scale where kept, else 0, over n
-// elements of bf16 or fp32 (out may be x), and the keep bits of n elements
-// (n % 32 == 0), bit e % 8 of byte e / 8.
+// elements of bf16 or fp32 (out may be x).
 hipError_t launch_dropout(const void* x, bool f32, int64_t n, const Drop& d, float scale,
                           void* out, hipStream_t st);
-hipError_t launch_keep_bits(int64_t n, const Drop& d, uint8_t* bits, hipStream_t st);
 
 // MXFP4 (format in the header).
 struct Mx4 {
@@ -431,7 +444,7 @@ inline int64_t mx4_scale_bytes(int64_t rows, int64_t cols) {
 hipError_t launch_mx4_quant(const void* x, bool f32, int64_t rows, int64_t K, uint8_t* codes,
                             uint8_t* scales, hipStream_t st);
 hipError_t launch_mx4_dequant(const Mx4& w, bool f32, void* out, hipStream_t st);
-// out[k][n] = W[n][k] as bf16, row length ldt (ldt % 32 == 0, ldt >= rows; zero for
+// out[k][n] = W[n][k] as bf16, row length ldt (ldt % 64 == 0, ldt >= rows; zero for
 // rows <= n < ldt).  The jobs of aux run in extra workgroups of the same launch.
 hipError_t launch_mx4_dequant_t(const Mx4& w, uint16_t* out, int64_t ldt, const BwdAux& aux,
                                 hipStream_t st);

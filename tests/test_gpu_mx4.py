@@ -272,6 +272,42 @@ def test_backward(qn, M, rows, cols, r, act8, p):
         _check(dB3, dB.double(), 2 * part * s * G.abs().t() @ u.double().abs() + 1e-30, "dB, no u")
 
 
+def test_no_numbers_in_the_backward(qn):
+    """A block of W that is no number makes its columns of dX NaN, a NaN of dY its row."""
+    say("[mx4 bwd nan]")
+    W = _normal(2, 72, 320)
+    clean = qn.mx4_quantize(W)
+    W[70, 100], W[3, 0] = float("nan"), float("inf")
+    w, G = qn.mx4_quantize(W), _normal(3, 150, 72)
+    base, _, _ = qn.mx4_linear_bwd(clean, None, G)
+    dX, _, _ = qn.mx4_linear_bwd(w, None, G)
+    bad = torch.zeros(150, 320, dtype=torch.bool, device="cuda")
+    bad[:, 96:128], bad[:, :32] = True, True
+    assert torch.equal(torch.isnan(dX), bad) and torch.equal(dX[~bad], base[~bad])
+    G[17, 5] = float("nan")
+    dX, _, _ = qn.mx4_linear_bwd(clean, None, G)
+    assert bool(torch.isnan(dX[17]).all()) and not bool(torch.isnan(dX[:17]).any())
+
+
+def test_adapter_gradients_keep_24_bits(qn):
+    """u and v enter in three bf16 parts: over all elements dA and dB are within 1e-6 (the
+    fp32 sums; two parts leave 2e-6)."""
+    say("[mx4 bwd parts]")
+    M, rows, cols, r = 1500, 264, 576, 16
+    w, d = _linear(qn, M, rows, cols, r, seed=5)
+    st = qn.nf4_quantize_dq(_normal(6, rows, cols, dtype=torch.float32))
+    drop = qn.Dropout(0.2, 1)
+    keep, f = _keep(M, cols, drop)
+    G, B, x = d["dY"].double(), d["B"].double(), d["x"].double() * keep
+    for fwd, bwd, base in ((qn.mx4_linear_fwd, qn.mx4_linear_bwd, w),
+                           (qn.qlora_linear_fwd, qn.qlora_linear_bwd, st)):
+        _, u = fwd(base, d["x"], d["A"], d["B"], 32.0, drop=drop)
+        _, dA, dB = bwd(base, d["x"], d["dY"], d["A"], d["B"], 32.0, u, drop=drop)
+        s = 2.0 * f
+        for got, want in ((dA, s * (G @ B).t() @ x), (dB, s * G.t() @ u.double())):
+            assert float((got.double() - want).norm() / want.norm()) <= 1e-6
+
+
 def test_backward_without_adapter(qn):
     say("[mx4 bwd r=0]")
     for M, rows, cols in [(1, 8, 64), (33, 72, 320), (300, 264, 576)]:
