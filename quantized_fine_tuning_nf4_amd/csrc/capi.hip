@@ -1106,12 +1106,14 @@ qn_status mx4_linear_fwd(const qn_mx4* w, const uint16_t* x, int64_t M, const ui
     return QN_EALIGN;
   Carver probe(nullptr);
   carve_mx4(probe, M, w->rows, w->cols, r, u_out, u_out == nullptr);
+  hipStream_t st = static_cast<hipStream_t>(stream);
   if (!workspace) return QN_EINVAL;
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return QN_EALIGN;
   if (workspace_bytes < probe.used) return QN_EWORKSPACE;
   Carver c(workspace);
+  if (mx4_one_launch(M, w->cols, r))  // (rows of such a width are 16-byte aligned)
+    return from_hip(launch_mx4_token(to_mx4(w), x, M, y, st));
   const Mx4X f = carve_mx4(c, M, w->rows, w->cols, r, u_out, u_out == nullptr);
-  hipStream_t st = static_cast<hipStream_t>(stream);
   hipError_t e = launch_mx4_x(x, w->cols, f, lo.drop, A, B, w->rows, lo.s, st);
   if (e == hipSuccess) e = launch_mx4_mm(to_mx4(w), f, B, lo.s, y, st);
   return from_hip(e);

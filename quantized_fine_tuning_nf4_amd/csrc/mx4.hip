@@ -783,6 +783,81 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx4_rows(
   }
 }
 
+// The same from x itself, in one launch, without an adapter: every workgroup rounds all
+// of x, from the second level cache.  Lane (g, n) takes all 32 columns of its block of
+// row n, so that the block's largest magnitude needs no exchange.  Against a pass of its
+// own for x: 14336x4096 10.2 us a call instead of 12.2 for one row and 11.8 instead of 12.7
+// for eight (four rounds of x's bytes for one of W's: 14.4 and 13.9 for sixteen),
+// 4096x4096 4.7 and 7.1, 5.8 and 7.5.  With u formed in every workgroup as well (r = 16)
+// 17.5 instead of 14.5: A is more bytes than the workgroup's rows of W.
+template <int NT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_mx4_token(
+    const uint8_t* __restrict__ wc, const uint8_t* __restrict__ ws,
+    const uint16_t* __restrict__ x, int M, int64_t N, int64_t K, int J,
+    uint16_t* __restrict__ y) {
+  constexpr int ROWS = 16 * NT, PITCH = ROWS + 4, THREADS = 64 * WAVES;
+  __shared__ __attribute__((aligned(16))) float sums[WAVES][16][PITCH];
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * ROWS;
+  const uint8_t* wp[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) wp[i] = wc + min(n0 + 16 * i + n, N - 1) * 128 * J + 16 * g;
+  const uint8_t* wsp = ws + n0 / 32 * J * 256 + 4 * lane + (NT == 1 ? 2 * ((n0 >> 4) & 1) : 0);
+  const uint16_t* xp = x + (int64_t)min(n, M - 1) * K;
+  f32x4 acc[NT] = {};
+  for (int j = wave; j < J; j += WAVES) {
+    u32x4 a[NT][2], xv[2][4], b[2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        a[i][t] = *reinterpret_cast<const u32x4*>(wp[i] + 128 * (int64_t)j + 64 * t);
+    const int sa = NT == 1 ? (int)*reinterpret_cast<const uint16_t*>(wsp + 256 * (int64_t)j)
+                           : *reinterpret_cast<const int*>(wsp + 256 * (int64_t)j);
+    bool in[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {  // past the row (K is a multiple of 32): its first columns
+      const int64_t col = (int64_t)j * kMx4Step + 32 * (4 * t + g);
+      in[t] = col < K;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        xv[t][q] = *reinterpret_cast<const u32x4*>(xp + (in[t] ? col : 0) + 8 * q);
+    }
+    int sb = 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (!in[t]) xv[t][q] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = pk_max(top, xv[t][q][e] & 0x7fff7fffu);
+      }
+      const uint32_t E = mx4_exp(max(top << 16, top & 0xffff0000u));
+      b[t] = u32x4{encode8(xv[t][0], E), encode8(xv[t][1], E), encode8(xv[t][2], E),
+                   encode8(xv[t][3], E)};
+      sb |= (int)(E << (8 * t));
+    }
+    unrolled<2 * NT>([&](auto k_t) {
+      constexpr int k = decltype(k_t)::value, t = k & 1, i = k >> 1;
+      acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag4(a[i][t]), frag4(b[t]), acc[i],
+                                                                4, 4, 2 * i + t, sa, t, sb);
+    });
+  }
+  // lane: row n of y, columns 16 i + 4 g + 0 .. 3
+#pragma unroll
+  for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4*>(&sums[wave][n][16 * i + 4 * g]) = acc[i];
+  __syncthreads();
+  const int c = tid % ROWS;
+  for (int m = tid / ROWS; m < M; m += THREADS / ROWS) {
+    float t = sums[0][m][c];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) t += sums[w][m][c];
+    if (n0 + c < N) y[(int64_t)m * N + n0 + c] = to_bf16(t);
+  }
+}
+
 // out[k][n] = W[n][k] as bf16, row length ldt (zero for rows <= n < ldt).  A workgroup
 // takes 128 rows x 128 columns through LDS: thread (q, l) = (t / 64, t % 64) the block q
 // of rows 2 l and 2 l + 1, whose columns leave as pairs of rows, a word each.
@@ -968,6 +1043,23 @@ hipError_t launch_mx4_x(const uint16_t* x, int64_t K, const Mx4X& o, const Drop&
   if (o.M > 4096) return launch_x<2, 8>(x, K, o, d, A, B, N, s, st);
   if (mx4_few_rows(o.M)) return launch_x<1, 8>(x, K, o, d, A, B, N, s, st);
   return launch_x<1, 16>(x, K, o, d, A, B, N, s, st);
+}
+
+namespace {
+template <int NT, int WAVES>
+hipError_t launch_token(const Mx4& w, const uint16_t* x, int64_t M, uint16_t* y, hipStream_t st) {
+  const dim3 grid((unsigned)((w.rows + 16 * NT - 1) / (16 * NT)));
+  hipLaunchKernelGGL((k_mx4_token<NT, WAVES>), grid, dim3(64 * WAVES), 0, st, w.codes, w.scales, x,
+                     (int)M, w.rows, w.cols, (int)mx4_steps(w.cols), y);
+  return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_mx4_token(const Mx4& w, const uint16_t* x, int64_t M, uint16_t* y,
+                            hipStream_t st) {
+  if (!mx4_one_launch(M, w.cols, 0)) return hipErrorInvalidValue;
+  return w.rows >= 16 * 512 ? launch_token<2, 8>(w, x, M, y, st)
+                            : launch_token<1, 16>(w, x, M, y, st);
 }
 
 hipError_t launch_mx4_mm(const Mx4& w, const Mx4X& x, const uint16_t* B, float s, uint16_t* y,

@@ -463,6 +463,12 @@ struct Mx4X {
 // Batches whose product reads W straight into registers.
 inline bool mx4_few_rows(int64_t M) { return M <= 64; }
 int mx4_x_slices(int64_t M, int64_t K);
+// A token or a few without an adapter: y from x itself (16-byte aligned) in one launch.
+inline bool mx4_one_launch(int64_t M, int64_t K, int r) {
+  return M <= 8 && r == 0 && K % kMx4Block == 0;
+}
+hipError_t launch_mx4_token(const Mx4& w, const uint16_t* x, int64_t M, uint16_t* y,
+                            hipStream_t st);
 // Fills o from x [M, K] (K % 64 == 0 with an adapter), u = drop(x) A^T.
 hipError_t launch_mx4_x(const uint16_t* x, int64_t K, const Mx4X& o, const Drop& d,
                         const uint16_t* A, const uint16_t* B, int64_t N, float s, hipStream_t st);

@@ -15,6 +15,7 @@ current stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -28,18 +29,30 @@ MX4_BLOCK = 32   # columns of a row that share a scale
 MX4_STEP = 256   # columns that a row of codes is padded to
 
 
-def _here(t: torch.Tensor) -> bool:
-    """Whether t lies on the current device (kernels are launched there)."""
-    return t.device.index == torch.cuda.current_device()
+@functools.lru_cache(maxsize=None)
+def _one_device() -> bool:
+    return torch.cuda.device_count() == 1
 
 
-def _together(*ts: torch.Tensor | None) -> None:
+def _here(*ts: torch.Tensor | None) -> bool:
+    """Whether the tensors, which must share a device, lie on the current one (kernels
+    are launched there).  (With one device there is nothing to ask: 1.5 us of a small
+    call's 12.)"""
+    if _one_device():
+        return True
     dev = None
     for t in ts:
         if t is not None:
             if dev is not None and t.device != dev:
                 raise ValueError("all tensors must be on one device")
             dev = t.device
+    return dev is None or dev.index == torch.cuda.current_device()
+
+
+@functools.lru_cache(maxsize=4096)
+def _need(*sizes: int) -> int:
+    """mx4_linear_workspace(*sizes) (asked again each time it is 0.8 us)."""
+    return load_library().mx4_linear_workspace(*sizes)
 
 
 # ------------------------------------------------------- dropout from a counter
@@ -78,7 +91,7 @@ def _drop(drop: Dropout | None, *beside: torch.Tensor):
     if not isinstance(drop, Dropout):
         raise ValueError("drop must be a Dropout")
     if drop.step is not None:
-        _together(drop.step, *beside)
+        _here(drop.step, *beside)
     return ctypes.byref(drop.c_struct())
 
 
@@ -96,11 +109,10 @@ def dropout_apply(x: torch.Tensor, drop: Dropout, out: torch.Tensor | None = Non
     elif _dev(out, x.dtype, "out").shape != x.shape:
         raise ValueError("out must have x's shape")
     if given:
-        _together(x, out)
         a, b, n = x.data_ptr(), out.data_ptr(), x.numel() * x.element_size()
         if a != b and a < b + n and b < a + n:
             raise ValueError("out may be x itself but may not overlap it otherwise")
-    if not _here(x):
+    if not _here(x, out):
         with torch.cuda.device(x.device):
             return dropout_apply(x, drop, out)
     _check(load_library().dropout_apply(x.data_ptr(), _DTYPES[x.dtype], x.numel(),
@@ -160,9 +172,9 @@ def _mx4(w: MX4, name: str = "w") -> MX4:
     if not isinstance(w, MX4):
         raise ValueError(f"{name} must be an MX4")
     codes, scales = _shapes(w.rows, w.cols)
-    if _dev(w.codes, torch.uint8, f"{name}.codes").shape != codes:
+    if _dev(w.codes, torch.uint8, "codes").shape != codes:
         raise ValueError(f"{name}.codes must be {list(codes)}")
-    if _dev(w.scales, torch.uint8, f"{name}.scales").shape != scales:
+    if _dev(w.scales, torch.uint8, "scales").shape != scales:
         raise ValueError(f"{name}.scales must be {list(scales)}")
     return w
 
@@ -179,12 +191,11 @@ def mx4_quantize(x: torch.Tensor, out: MX4 | None = None) -> MX4:
     given = out is not None
     if not given:
         codes, scales = _shapes(rows, cols)
-        out = MX4(torch.empty(codes, dtype=torch.uint8, device=x.device),
-                  torch.empty(scales, dtype=torch.uint8, device=x.device), rows, cols)
+        out = MX4(torch.empty(*codes, dtype=torch.uint8, device=x.device),
+                  torch.empty(*scales, dtype=torch.uint8, device=x.device), rows, cols)
     elif (_mx4(out, "out").rows, out.cols) != (rows, cols):
         raise ValueError(f"out must be [{rows}, {cols}]")
-    _together(x, out.codes, out.scales)
-    if not _here(x):
+    if not _here(x, out.codes, out.scales):
         with torch.cuda.device(x.device):
             return mx4_quantize(x, out)
     rc = load_library().mx4_quantize(x.data_ptr(), _DTYPES[x.dtype], rows, cols,
@@ -208,8 +219,7 @@ def mx4_dequantize(w: MX4, dtype=torch.bfloat16, out: torch.Tensor | None = None
         out = torch.empty(w.rows, w.cols, dtype=dtype, device=w.device)
     elif _dev(out, dtype, "out").shape != (w.rows, w.cols):
         raise ValueError(f"out must be [{w.rows}, {w.cols}]")
-    _together(w.codes, w.scales, out)
-    if not _here(w.codes):
+    if not _here(w.codes, w.scales, out):
         with torch.cuda.device(w.device):
             return mx4_dequantize(w, dtype, out)
     _check(load_library().mx4_dequantize(ctypes.byref(w.c_struct()), _DTYPES[dtype],
@@ -240,7 +250,7 @@ def _workspace(need: int, given: torch.Tensor | None, device) -> torch.Tensor:
         if not given.is_contiguous() or given.dtype != torch.uint8 or given.device != device:
             raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
         return given
-    return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    return torch.empty(need, dtype=torch.uint8, device=device)
 
 
 def mx4_linear_fwd(w: MX4, x: torch.Tensor, A: torch.Tensor | None = None,
@@ -260,13 +270,12 @@ def mx4_linear_fwd(w: MX4, x: torch.Tensor, A: torch.Tensor | None = None,
         y = torch.empty(M, w.rows, dtype=torch.bfloat16, device=x.device)
     elif _dev(y, torch.bfloat16, "y").shape != (M, w.rows):
         raise ValueError(f"y must be [{M}, {w.rows}]")
-    _together(w.codes, w.scales, x, A, B, y)
-    if not _here(x):
+    if not _here(w.codes, w.scales, x, A, B, y):
         with torch.cuda.device(x.device):
             return mx4_linear_fwd(w, x, A, B, alpha, save_u, y, workspace, rslora, drop)
     L = load_library()
     u = torch.empty(M, r, dtype=torch.float32, device=x.device) if save_u and r else None
-    ws = _workspace(L.mx4_linear_workspace(M, w.rows, w.cols, r, 0, 0, 0), workspace, x.device)
+    ws = _workspace(_need(M, w.rows, w.cols, r, 0, 0, 0), workspace, x.device)
     rc = L.mx4_linear_fwd(ctypes.byref(w.c_struct()), x.data_ptr(), M, _ptr(A), _ptr(B), r,
                           float(alpha), int(bool(rslora)), _drop(drop, x), y.data_ptr(), _ptr(u),
                           ws.data_ptr(), ws.numel(), _stream(x.device))
@@ -315,16 +324,15 @@ def mx4_linear_bwd(w: MX4, x, dY: torch.Tensor, A: torch.Tensor | None = None,
             raise ValueError(f"u must be [{M}, {r}]")
     dev = dY.device
     codes, exps = (None, None) if x8 is None else (x8.codes, x8.exps)
-    _together(w.codes, w.scales, dY, xb, codes, exps, A, B, u)
-    if not _here(dY):
+    if not _here(w.codes, w.scales, dY, xb, codes, exps, A, B, u):
         with torch.cuda.device(dev):
             return mx4_linear_bwd(w, x, dY, A, B, alpha, u, need_dx, workspace, rslora, drop)
     L = load_library()
     dX = torch.empty(M, w.cols, dtype=torch.bfloat16, device=dev) if need_dx else None
     dA = torch.empty(r, w.cols, dtype=torch.float32, device=dev) if r else None
     dB = torch.empty(w.rows, r, dtype=torch.float32, device=dev) if r else None
-    ws = _workspace(L.mx4_linear_workspace(M, w.rows, w.cols, r, 1, int(x8 is not None),
-                                           int(drop is not None)), workspace, dev)
+    ws = _workspace(_need(M, w.rows, w.cols, r, 1, int(x8 is not None), int(drop is not None)),
+                    workspace, dev)
     c8 = ctypes.byref(x8.c_struct()) if x8 is not None else None
     rc = L.mx4_linear_bwd(ctypes.byref(w.c_struct()), _ptr(xb), c8, dY.data_ptr(), M, _ptr(A),
                           _ptr(B), r, float(alpha), int(bool(rslora)), _drop(drop, dY), _ptr(u),

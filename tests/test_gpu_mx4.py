@@ -133,7 +133,7 @@ def _check(got, want, tol, name):
 
 # M, rows, cols, r: no adapter at odd sizes, then ranks of one block of 16 and several,
 # tiles that end inside, one row, few and many
-PLAIN = [(1, 1, 1), (1, 5, 33), (3, 17, 100), (16, 64, 256), (17, 31, 1000), (33, 257, 511),
+PLAIN = [(1, 1, 1), (1, 5, 32), (8, 300, 1056), (7, 8210, 288), (1, 5, 33), (3, 17, 100), (16, 64, 256), (17, 31, 1000), (33, 257, 511),
          (100, 130, 2048), (128, 128, 64), (129, 129, 300), (300, 1001, 129), (256, 512, 4096),
          (65, 33, 4000), (4001, 4099, 300), (3841, 4096, 1025)]
 
