@@ -462,8 +462,8 @@ def qlora_linear_fwd(st: NF4State, x: torch.Tensor, A: torch.Tensor, B: torch.Te
     B = _dev(B, torch.bfloat16, "B")
     M, r = _linear_args(st, x, A, B)
     if y is None:
-        y = torch.empty((M, st.rows), dtype=torch.bfloat16, device=x.device)
-    u = torch.empty((M, r), dtype=torch.float32, device=x.device) if save_u else None
+        y = torch.empty(M, st.rows, dtype=torch.bfloat16, device=x.device)
+    u = torch.empty(M, r, dtype=torch.float32, device=x.device) if save_u else None
     if drop is not None:
         _one_dropout(dropout_mask, dropout_p)
         return _qlora_fwd_drop(st, x, A, B, r, alpha, rslora, drop, y, u, workspace)
@@ -499,9 +499,9 @@ def qlora_linear_bwd(st: NF4State, x: torch.Tensor, dY: torch.Tensor, A: torch.T
         _dev(u, torch.float32, "u")
         if u.shape != (M, r):
             raise ValueError(f"u must be [{M}, {r}]")
-    dX = torch.empty((M, st.cols), dtype=torch.bfloat16, device=x.device) if need_dx else None
-    dA = torch.empty((r, st.cols), dtype=torch.float32, device=x.device)
-    dB = torch.empty((st.rows, r), dtype=torch.float32, device=x.device)
+    dX = torch.empty(M, st.cols, dtype=torch.bfloat16, device=x.device) if need_dx else None
+    dA = torch.empty(r, st.cols, dtype=torch.float32, device=x.device)
+    dB = torch.empty(st.rows, r, dtype=torch.float32, device=x.device)
     if drop is not None:
         _one_dropout(dropout_mask, dropout_p)
         _check(_qlora_bwd_drop(st, x, None, dY, A, B, r, alpha, rslora, drop, u, dX, dA, dB,

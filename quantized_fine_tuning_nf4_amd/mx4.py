@@ -55,6 +55,11 @@ def _need(*sizes: int) -> int:
     return load_library().mx4_linear_workspace(*sizes)
 
 
+@functools.lru_cache(maxsize=4096)
+def _need_drop(*sizes: int) -> int:
+    return load_library().qlora_linear_drop_workspace(*sizes)
+
+
 # ------------------------------------------------------- dropout from a counter
 @dataclass(frozen=True, eq=False)
 class Dropout:
@@ -351,9 +356,10 @@ def mx4_linear_bwd(w: MX4, x, dY: torch.Tensor, A: torch.Tensor | None = None,
 def _qlora_fwd_drop(st: NF4State, x, A, B, r, alpha, rslora, drop, y, u, workspace):
     L = load_library()
     M = x.shape[0]
-    need = L.qlora_linear_drop_workspace(M, st.rows, st.cols, r, 0, 0)
+    need = _need_drop(M, st.rows, st.cols, r, 0, 0)
     if workspace is None or workspace.numel() < need:
-        workspace = torch.zeros(max(need, 1), dtype=torch.uint8, device=x.device)
+        # (under dropout no launch counts arrivals: nothing to clear)
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     _check(L.qlora_linear_fwd_drop(ctypes.byref(st.c_struct()), x.data_ptr(), M, A.data_ptr(),
                                    B.data_ptr(), r, float(alpha), int(bool(rslora)),
                                    _drop(drop, x), y.data_ptr(), _ptr(u), workspace.data_ptr(),
@@ -365,9 +371,9 @@ def _qlora_bwd_drop(st: NF4State, x, x8, dY, A, B, r, alpha, rslora, drop, u, dX
                     workspace):
     L = load_library()
     M = dY.shape[0]
-    need = L.qlora_linear_drop_workspace(M, st.rows, st.cols, r, 1, int(x8 is not None))
+    need = _need_drop(M, st.rows, st.cols, r, 1, int(x8 is not None))
     if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dY.device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dY.device)
     return L.qlora_linear_bwd_drop(
         ctypes.byref(st.c_struct()), _ptr(x), None if x8 is None else ctypes.byref(x8.c_struct()),
         dY.data_ptr(), M, A.data_ptr(), B.data_ptr(), r, float(alpha), int(bool(rslora)),
