@@ -363,28 +363,30 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx4_x(
 // ---- The product of many rows.  Workgroup tile BM x BN (rows of x, rows of W), WVM x WVN
 // waves of TM x TN tiles of v_mfma_scale_f32_16x16x128_f8f6f4.  A step is 256 columns:
 // rows of 128 bytes of codes and 256 scale bytes per 32 rows go from global memory
-// straight into LDS, two stages deep.  Chunk c (16 bytes, a block) of row y sits at unit
+// straight into LDS, NST stages deep.  Chunk c (16 bytes, a block) of row y sits at unit
 // c ^ ((y >> 1) & 7), so that 16 rows of a fragment read sit on distinct banks.  In
 // half t of a step lane (g, n) = (l / 16, l % 16) takes row n's block 4 t + g, whose scale
 // is byte 2 (tile % 2) + t of the lane's four.
-template <int WVM, int WVN, int TM, int TN>
+template <int WVM, int WVN, int TM, int TN, int STAGES>
 struct MxGeo {
+  static constexpr int NST = STAGES;
   static constexpr int WAVES = WVM * WVN, THREADS = 64 * WAVES;
   static constexpr int BM = 16 * TM * WVM, BN = 16 * TN * WVN;
   static constexpr int XB = BM * 128, WB = BN * 128;   // codes of a stage
   static constexpr int XS = XB + WB, WS = XS + BM * 8;  // its scales
-  static constexpr int STB = WS + BN * 8;              // bytes of a stage
+  static constexpr int SL = (BM + BN + 127) / 128;     // loads of scales, 1 KB each
+  static constexpr int STB = XS + 1024 * SL;           // bytes of a stage
   // output staging of a wave: half its rows at a time
   static constexpr int OUTP = 32 * TN + 16, OUTW = 8 * TM * OUTP;
-  static constexpr int LDS_MAIN = 2 * STB > WAVES * OUTW ? 2 * STB : WAVES * OUTW;
+  static constexpr int LDS_MAIN = NST * STB > WAVES * OUTW ? NST * STB : WAVES * OUTW;
   static constexpr int LDS_V = LDS_MAIN, LDS_L = LDS_V + BM * 64;  // r <= 16: s u and B
   static constexpr int LDS_BYTES = LDS_L + BN * 32;
-  static constexpr int XL = BM / 8 / WAVES, WL = BN / 8 / WAVES;   // loads of a wave and step ...
-  static constexpr int SL = (BM + BN) / 128;                       // ... and of all, of scales
+  static constexpr int XL = BM / 8 / WAVES, WL = BN / 8 / WAVES;   // loads of codes of a wave
   static_assert(LDS_BYTES <= 160 * 1024 && WAVES % SL == 0, "LDS");
 };
 
 typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) const void global_void;
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 __device__ __forceinline__ rsrc_t make_rs(const void* base, uint32_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(base);
@@ -403,13 +405,13 @@ __device__ __forceinline__ i32x8 frag4(u32x4 v) {
   return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
 }
 
-template <int WVM, int WVN, int TM, int TN, bool ONE>
+template <int WVM, int WVN, int TM, int TN, int NST, bool ONE>
 __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_mx4_gemm(
     const uint8_t* __restrict__ wc, const uint8_t* __restrict__ ws,
     const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs, int64_t M, int64_t N, int J,
     const uint16_t* __restrict__ su, const uint16_t* __restrict__ bo, int nj,
     uint16_t* __restrict__ y, int tiles_m, int tiles_n) {
-  using G = MxGeo<WVM, WVN, TM, TN>;
+  using G = MxGeo<WVM, WVN, TM, TN, NST>;
   constexpr int BM = G::BM, BN = G::BN, STB = G::STB, XL = G::XL, WL = G::WL, LPS = XL + WL;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -444,15 +446,16 @@ __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_mx4_gemm(
     const int row = 8 * (WL * wave + i) + (lane >> 3);
     woff[i] = (uint32_t)(min(row, nrows - 1) * pitch + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
   }
-  // scales: 1 KB (four groups of 32 rows) a wave, those of x first; there are twice as
-  // many waves, and the upper ones load the same again
-  const int sq = wave % G::SL;
-  const bool sx = sq < BM / 128;
-  const int sg = 4 * (sx ? sq : sq - BM / 128) + (lane >> 4);  // group of the tile
-  const int sgroups = ((sx ? mrows : nrows) + 31) >> 5;
-  const rsrc_t rs = make_rs(sx ? xs + m0 / 32 * J * 256 : ws + n0 / 32 * J * 256,
-                            (uint32_t)(sgroups * J * 256));
-  const uint32_t soff = (uint32_t)(min(sg, sgroups - 1) * J * 256 + 16 * (lane & 15));
+  // scales: 1 KB (four groups of 32 rows) a wave, those of x first; there are more waves
+  // than that, and the upper ones load the same again
+  constexpr bool MIXED = BM % 128 != 0;  // (groups of x and of W in one load)
+  const int sq = wave % G::SL, xg = (mrows + 31) >> 5, wg = (nrows + 31) >> 5;
+  const int sg = 4 * sq + (lane >> 4);  // group of the tile
+  const bool sx = MIXED ? sg < BM / 32 : sq < BM / 128;
+  const int sk = sx ? min(sg, xg - 1) : min(sg - BM / 32, wg - 1);
+  const uint8_t* sbase = sx ? xs + m0 / 32 * J * 256 : ws + n0 / 32 * J * 256;
+  const rsrc_t rs = make_rs(sbase, MIXED ? 0u : (uint32_t)((sx ? xg : wg) * J * 256));
+  const uint32_t soff = (uint32_t)(sk * J * 256 + 16 * (lane & 15));
   // load q (0 .. LPS) of step st
   auto load_one = [&](int q, int st, int stage) {
     uint8_t* base = smem + stage * STB;
@@ -461,6 +464,9 @@ __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_mx4_gemm(
       dma16(rx, xoff[q], so, base + 1024 * (XL * wave + q));
     else if (q < LPS)
       dma16(rw, woff[q - XL], so, base + G::XB + 1024 * (WL * wave + q - XL));
+    else if constexpr (MIXED)
+      __builtin_amdgcn_global_load_lds((global_void*)(sbase + soff + 2 * so),
+                                       (lds_void*)(base + G::XS + 1024 * sq), 16, 0, 0);
     else
       dma16(rs, soff, 2 * so, base + G::XS + 1024 * sq);
   };
@@ -499,16 +505,16 @@ __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_mx4_gemm(
       dma16(ru, (uint32_t)(1024 * q + 16 * lane), 0, smem + G::LDS_V + 1024 * q);
     }
 #pragma unroll
-    for (int k = 0; k < BN / 32 / G::WAVES; ++k) {
-      const int q = BN / 32 / G::WAVES * wave + k;
+    for (int k = 0; k < (BN / 32 + G::WAVES - 1) / G::WAVES; ++k) {
+      const int q = (k * G::WAVES + wave) % (BN / 32);  // (again where waves are more)
       dma16(rb, (uint32_t)(1024 * q + 16 * lane), 0, smem + G::LDS_L + 1024 * q);
     }
   }
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
+  for (int k = 0; k < NST; ++k)
 #pragma unroll
     for (int q = 0; q <= LPS; ++q) load_one(q, min(k, J - 1), k);
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LPS + 1) : "memory");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 1) * (LPS + 1)) : "memory");
   barrier_lds();
 #pragma unroll
   for (int i = 0; i < TM; ++i) fx[i] = frag(0, xbase, i, 0);
@@ -519,24 +525,26 @@ __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_mx4_gemm(
 #pragma unroll
   for (int j = 0; j < TN / 2; ++j) ew[0][j] = scale(0, wsb, j);
 
-  // half t of step st on stage P = st % 2.  The fragments of the next half are read while
+  // half t of step st on stage P = st % NST.  The fragments of the next half are read while
   // this one's products run (those of W in a second set, those of x in place after their
   // row).  At the end of half 0 every wave has read the stage and step st + 1 has
-  // landed; half 1 sends the loads of step st + 2 into the stage.
+  // landed; half 1 sends the loads of step st + NST into the stage.
   auto half = [&](auto p_t, auto t_t, int st) {
     constexpr int P = decltype(p_t)::value, H = decltype(t_t)::value;
-    constexpr int RS = H == 0 ? P : P ^ 1, RH = H ^ 1;
-    const int lst = min(st + 2, J - 1);
+    constexpr int RS = H == 0 ? P : (P + 1) % NST, RH = H ^ 1, E = P & 1;
+    const int lst = min(st + NST, J - 1);
     unrolled<TM>([&](auto i_t) {
       constexpr int i = decltype(i_t)::value;
       unrolled<TN>([&](auto j_t) {
         constexpr int j = decltype(j_t)::value;
         acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            frag4(fw[H][j]), frag4(fx[i]), acc[i][j], 4, 4, 2 * (j & 1) + H, ew[P][j / 2],
-            2 * (i & 1) + H, ex[P][i / 2]);
+            frag4(fw[H][j]), frag4(fx[i]), acc[i][j], 4, 4, 2 * (j & 1) + H, ew[E][j / 2],
+            2 * (i & 1) + H, ex[E][i / 2]);
         if (i == 0) fw[RH][j] = frag(RS, wbase, j, RH);
-        if (H == 1 && i == 1 && j < TN / 2) ew[P ^ 1][j] = scale(RS, wsb, j);
-        if (H == 1 && i >= 2 && j == 0 && i - 2 < TM / 2) ex[P ^ 1][i - 2] = scale(RS, xsb, i - 2);
+        if (H == 1 && i == 1 && j < TN / 2) ew[E ^ 1][j] = scale(RS, wsb, j);
+        constexpr int K0 = TM == 2 ? 1 : 2;  // row of the first of x's scales
+        if (H == 1 && i >= K0 && j == 0 && i - K0 < TM / 2)
+          ex[E ^ 1][i - K0] = scale(RS, xsb, i - K0);
         if (H == 1 && j == TN / 2)
           for (int q = (LPS + TM) / TM * i; q < (LPS + TM) / TM * (i + 1); ++q)
             if (q <= LPS) load_one(q, lst, P);
@@ -545,23 +553,24 @@ __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_mx4_gemm(
       __builtin_amdgcn_sched_barrier(0);
     });
     if (H == 0) {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * (LPS + 1)) : "memory");
       barrier_lds();
     }
   };
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
   int st = 0;
-  for (; st + 2 <= J; st += 2) {
-    half(I0{}, I0{}, st);
-    half(I0{}, I1{}, st);
-    half(I1{}, I0{}, st + 1);
-    half(I1{}, I1{}, st + 1);
-  }
-  if (st < J) {
-    half(I0{}, I0{}, st);
-    half(I0{}, I1{}, st);
-  }
+  for (; st + NST <= J; st += NST)
+    unrolled<NST>([&](auto p) {
+      half(p, I0{}, st + (int)p);
+      half(p, I1{}, st + (int)p);
+    });
+  unrolled<NST - 1>([&](auto p) {
+    if (st < J) {
+      half(p, I0{}, st);
+      half(p, I1{}, st++);
+    }
+  });
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   barrier_lds();
 
@@ -951,17 +960,17 @@ hipError_t launch_mx4_dequant_t(const Mx4& w, uint16_t* out, int64_t ldt, const 
 }
 
 namespace {
-template <int WVM, int WVN, int TM, int TN>
+template <int WVM, int WVN, int TM, int TN, int NST>
 hipError_t launch_tiles(const Mx4& w, const Mx4X& x, uint16_t* y, hipStream_t st) {
-  using G = MxGeo<WVM, WVN, TM, TN>;
+  using G = MxGeo<WVM, WVN, TM, TN, NST>;
   static const hipError_t attr = [] {
     const hipError_t e = hipFuncSetAttribute(
-        reinterpret_cast<const void*>(k_mx4_gemm<WVM, WVN, TM, TN, true>),
+        reinterpret_cast<const void*>(k_mx4_gemm<WVM, WVN, TM, TN, NST, true>),
         hipFuncAttributeMaxDynamicSharedMemorySize, G::LDS_BYTES);
     return e != hipSuccess
                ? e
                : hipFuncSetAttribute(
-                     reinterpret_cast<const void*>(k_mx4_gemm<WVM, WVN, TM, TN, false>),
+                     reinterpret_cast<const void*>(k_mx4_gemm<WVM, WVN, TM, TN, NST, false>),
                      hipFuncAttributeMaxDynamicSharedMemorySize, G::LDS_MAIN);
   }();
   if (attr != hipSuccess) return attr;
@@ -969,11 +978,11 @@ hipError_t launch_tiles(const Mx4& w, const Mx4X& x, uint16_t* y, hipStream_t st
   const dim3 grid((unsigned)(tm * tn)), block(G::THREADS);
   const int J = (int)mx4_steps(w.cols), nj = (x.r + 15) / 16;
   if (nj == 1)
-    hipLaunchKernelGGL((k_mx4_gemm<WVM, WVN, TM, TN, true>), grid, block, G::LDS_BYTES, st, w.codes,
+    hipLaunchKernelGGL((k_mx4_gemm<WVM, WVN, TM, TN, NST, true>), grid, block, G::LDS_BYTES, st, w.codes,
                        w.scales, x.codes, x.scales, x.M, w.rows, J, x.su, x.bo, nj, y, (int)tm,
                        (int)tn);
   else
-    hipLaunchKernelGGL((k_mx4_gemm<WVM, WVN, TM, TN, false>), grid, block, G::LDS_MAIN, st, w.codes,
+    hipLaunchKernelGGL((k_mx4_gemm<WVM, WVN, TM, TN, NST, false>), grid, block, G::LDS_MAIN, st, w.codes,
                        w.scales, x.codes, x.scales, x.M, w.rows, J, x.su, x.bo, nj, y, (int)tm,
                        (int)tn);
   return hipGetLastError();
@@ -1072,17 +1081,28 @@ hipError_t launch_mx4_mm(const Mx4& w, const Mx4X& x, const uint16_t* B, float s
     if (x.M <= 32) return launch_rows<2, 2, 8>(w, x, B, s, y, st);
     return launch_rows<4, 2, 8>(w, x, B, s, y, st);
   }
-  // 256 x 256 tiles, one a compute unit, or 128 x 128, two: a round of the small ones
-  // takes 0.57 of a round of the large ones (8192x4096x4096: 84 us in 4 against 74 in 2), so
-  // the large ones where they need no more than 0.6 as many (301x50021x1000, 2 rounds and
-  // 3: 28.9 us and 23.8; 4096x14336x4096, 4 and 7: 134 and 155)
   const int64_t cu = compute_units();
+  const auto tiles = [&](int64_t tm, int64_t tn) {
+    return (x.M + tm - 1) / tm * ((w.rows + tn - 1) / tn);
+  };
+  // Few tiles: the smallest that still go one to a compute unit, four stages deep (a
+  // unit's loads in flight bound it: 128x4096x14336 by 64 x 64 tiles 14.2 us, by 64 x 128
+  // 18.8, by 128 x 128 26.2; 300x4096x4096, 320 of the first kind, 10.9, 8.7 and 12.4;
+  // 1000x4096x4096 19.7, 17.8 and 13.8).
+  if (tiles(64, 64) <= cu) return launch_tiles<2, 2, 2, 2, 4>(w, x, y, st);
+  if (tiles(64, 128) <= cu) return launch_tiles<2, 2, 2, 4, 4>(w, x, y, st);
+  if (tiles(128, 128) <= cu) return launch_tiles<2, 4, 4, 2, 4>(w, x, y, st);
+  // Many: 256 x 256, one a compute unit, or 128 x 128, two, two stages deep.  A round of the
+  // small ones takes 0.57 of a round of the large ones (8192x4096x4096: 84 us in 4 against
+  // 74 in 2), so the large ones where they need no more than 0.6 as many
+  // (301x50021x1000, 2 rounds and 3: 28.9 us and 23.8; 4096x14336x4096, 4 and 7: 134
+  // and 155).
   const auto rounds = [&](int64_t t, int64_t at_once) {
-    return ((x.M + t - 1) / t * ((w.rows + t - 1) / t) + at_once - 1) / at_once;
+    return (tiles(t, t) + at_once - 1) / at_once;
   };
   if (10 * rounds(256, cu) <= 6 * rounds(128, 2 * cu))
-    return launch_tiles<2, 4, 8, 4>(w, x, y, st);
-  return launch_tiles<2, 2, 4, 4>(w, x, y, st);
+    return launch_tiles<2, 4, 8, 4, 2>(w, x, y, st);
+  return launch_tiles<2, 2, 4, 4, 2>(w, x, y, st);
 }
 
 }  // namespace qn

@@ -135,7 +135,8 @@ def _check(got, want, tol, name):
 # tiles that end inside, one row, few and many
 PLAIN = [(1, 1, 1), (1, 5, 32), (8, 300, 1056), (7, 8210, 288), (1, 5, 33), (3, 17, 100), (16, 64, 256), (17, 31, 1000), (33, 257, 511),
          (100, 130, 2048), (128, 128, 64), (129, 129, 300), (300, 1001, 129), (256, 512, 4096),
-         (65, 33, 4000), (4001, 4099, 300), (3841, 4096, 1025)]
+         (65, 33, 4000), (4001, 4099, 300), (3841, 4096, 1025), (300, 4096, 257), (1000, 4095, 1281),
+         (2049, 4097, 130), (130, 520, 2304)]
 
 
 @pytest.mark.parametrize("M,rows,cols", PLAIN)
@@ -154,7 +155,8 @@ def test_product(qn, M, rows, cols):
 ADAPTED = [(1, 8, 64, 1), (2, 64, 128, 16), (16, 72, 192, 5), (31, 136, 320, 17), (40, 256, 1024, 64),
            (130, 264, 576, 16), (257, 512, 832, 33), (1, 1024, 4096, 16), (520, 768, 2048, 8),
            (4000, 4104, 320, 16), (3841, 4000, 832, 40), (6150, 72, 128, 20), (6177, 256, 320, 7),
-           (50, 72, 640, 64), (33, 64, 2112, 3)]
+           (50, 72, 640, 64), (33, 64, 2112, 3), (300, 4096, 192, 16), (300, 4096, 1344, 40),
+           (1000, 4096, 192, 9), (1000, 4096, 1344, 40), (2056, 4104, 128, 5), (2056, 4104, 128, 40)]
 
 
 def _linear(qn, M, rows, cols, r, seed=0):
