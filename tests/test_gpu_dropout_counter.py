@@ -114,7 +114,7 @@ def test_gradient_and_step(qn):
 
 # M, rows, cols, r: every route of the NF4 linear: products of 32 rows, of 128 x 128 and
 # the dense one, u with ranks up to 16 and past them
-LINEAR = [(1, 8, 64, 1), (7, 72, 192, 16), (130, 136, 576, 20), (300, 64, 1024, 64),
+LINEAR = [(1, 8, 64, 1), (7, 72, 192, 16), (60, 8208, 320, 5), (100, 136, 1088, 40), (130, 136, 576, 20), (300, 64, 1024, 64),
           (2050, 2112, 72 * 64, 16), (2048, 2048, 256, 33)]
 
 

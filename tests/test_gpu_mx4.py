@@ -156,7 +156,8 @@ ADAPTED = [(1, 8, 64, 1), (2, 64, 128, 16), (16, 72, 192, 5), (31, 136, 320, 17)
            (130, 264, 576, 16), (257, 512, 832, 33), (1, 1024, 4096, 16), (520, 768, 2048, 8),
            (4000, 4104, 320, 16), (3841, 4000, 832, 40), (6150, 72, 128, 20), (6177, 256, 320, 7),
            (50, 72, 640, 64), (33, 64, 2112, 3), (300, 4096, 192, 16), (300, 4096, 1344, 40),
-           (1000, 4096, 192, 9), (1000, 4096, 1344, 40), (2056, 4104, 128, 5), (2056, 4104, 128, 40)]
+           (1000, 4096, 192, 9), (1000, 4096, 1344, 40), (2056, 4104, 128, 5), (2056, 4104, 128, 40), (60, 72, 8256, 5), (100, 136, 1088, 20),
+           (128, 64, 320, 64), (20, 1000, 8192, 33)]
 
 
 def _linear(qn, M, rows, cols, r, seed=0):
