@@ -486,7 +486,10 @@ qn_status dropout_apply(const void* x, qn_dtype dtype, int64_t n, const qn_dropo
 /* qlora_linear_fwd and qlora_linear_bwd (from x, or from x8, the other NULL) under
  * such dropout (drop nullable; rslora 0 or 1 as in qn_lora_opts): the same results
  * as with a stored mask of the same bits and the branch's scale times
- * 2^16 / (2^16 - t).  The backward holds the bits in its workspace while it runs. */
+ * 2^16 / (2^16 - t), up to the order of the sums (batches of any size take the
+ * routes through a bf16 copy of the weight, and u and v enter dA and dB in three bf16
+ * parts).  The backward holds the bits in its workspace while it runs.  Workspaces
+ * need no clearing. */
 size_t qlora_linear_drop_workspace(int64_t M, int64_t rows, int64_t cols, int r, int backward,
                                    int act8);
 qn_status qlora_linear_fwd_drop(const qn_nf4dq* w, const uint16_t* x, int64_t M, const uint16_t* A,

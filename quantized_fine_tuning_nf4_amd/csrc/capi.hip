@@ -1018,12 +1018,16 @@ size_t qlora_linear_drop_workspace(int64_t M, int64_t rows, int64_t cols, int r,
   if (M < 0 || M > kMaxRowsM || rows < 1 || rows > kMaxDim || cols < 1 || cols > kMaxDim ||
       r < 1 || r > 64)
     return 0;
-  Carver c(nullptr);
-  if (backward)
-    carve_bwd(c, M, rows, cols, r, !act8, true, true, true);
-  else
-    carve_fwd(c, M, rows, cols, r, true, true, true, true);
-  return c.used;
+  // with dropout, and where it drops nothing (drop NULL, or p less than half a step)
+  Carver with(nullptr), without(nullptr);
+  if (backward) {
+    carve_bwd(with, M, rows, cols, r, !act8, true, true, true);
+    carve_bwd(without, M, rows, cols, r, !act8, act8 != 0);
+  } else {
+    carve_fwd(with, M, rows, cols, r, true, true, true, true);
+    carve_fwd(without, M, rows, cols, r, true);
+  }
+  return std::max(with.used, without.used);
 }
 
 qn_status qlora_linear_fwd_drop(const qn_nf4dq* w, const uint16_t* x, int64_t M, const uint16_t* A,
@@ -1034,7 +1038,9 @@ qn_status qlora_linear_fwd_drop(const qn_nf4dq* w, const uint16_t* x, int64_t M,
   Lora lo;
   qn_status s = lora_drop_options(rslora, drop, alpha, r, &lo);
   if (s != QN_OK) return s;
-  return forward(w, x, M, A, B, r, lo, y, u_out, workspace, workspace_bytes, stream, false);
+  // (without dropout the decode kernels may count arrivals: in a workspace that need not
+  // have been cleared)
+  return forward(w, x, M, A, B, r, lo, y, u_out, workspace, workspace_bytes, stream, true);
 }
 
 qn_status qlora_linear_bwd_drop(const qn_nf4dq* w, const uint16_t* x, const qn_act8* x8,

@@ -165,6 +165,34 @@ def test_nf4_linear_takes_the_same_mask(qn, M, rows, cols, r, act8):
                   ).max()) <= 0
 
 
+@pytest.mark.parametrize("M,rows,cols,r", [(1, 64, 1024, 8), (3, 4096, 4096, 16), (16, 64, 2048, 40),
+                                           (40, 136, 320, 7), (2050, 2112, 4608, 16)])
+@pytest.mark.parametrize("p", [0.0, 1e-7])
+def test_dropping_nothing_is_the_linear_itself(qn, M, rows, cols, r, p):
+    """A threshold of zero: every route of the call without dropout, in workspaces that
+    hold anything."""
+    say(f"[drop none] M={M} rows={rows} cols={cols} r={r} p={p}")
+    st = qn.nf4_quantize_dq(_normal(1, rows, cols, std=0.02, dtype=torch.float32))
+    x, G = _normal(2, M, cols), _normal(3, M, rows)
+    A, B = _normal(4, r, cols, std=0.1), _normal(5, rows, r, std=0.1)
+    drop = qn.Dropout(p, 1)
+    L = qn.load_library()
+    ws = [torch.full((L.qlora_linear_drop_workspace(M, rows, cols, r, b, 0),), 255,
+                     dtype=torch.uint8, device="cuda") for b in (0, 1)]
+    want = qn.qlora_linear_fwd(st, x, A, B, 16.0)
+    grads = qn.qlora_linear_bwd(st, x, G, A, B, 16.0, want[1])
+    for k in range(2):
+        got = qn.qlora_linear_fwd(st, x, A, B, 16.0, drop=drop, workspace=ws[0])
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        got = qn.qlora_linear_bwd(st, x, G, A, B, 16.0, want[1], drop=drop, workspace=ws[1])
+        assert all(torch.equal(a, b) for a, b in zip(got, grads))
+    x8 = qn.act8_pack(x)
+    want = qn.qlora_linear_bwd_act8(st, x8, G, A, B, 16.0, want[1])
+    got = qn.qlora_linear_bwd_act8(st, x8, G, A, B, 16.0, qn.qlora_linear_fwd(st, x, A, B, 16.0)[1],
+                                   drop=drop)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("base", ["nf4", "mx4"])
 @pytest.mark.parametrize("act8", [False, True])
 def test_modules(qn, base, act8):
