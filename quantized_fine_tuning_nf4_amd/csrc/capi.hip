@@ -325,8 +325,8 @@ qn_status forward(const qn_nf4dq* w, const uint16_t* x, int64_t M, const uint16_
                          fold ? SliceSum{f.upart, M * (int64_t)r, f.S, u} : SliceSum{},
                          w->codebook, w->absmax);
     if (e == hipSuccess)
-      e = (lo.drop.on && gemm_few_ok(M, N) ? launch_gemm_few : launch_gemm_nt)(
-          x, K, K, f.wd, K, M, N, u, B, r, scale, y, st, nullptr);
+      e = (lo.drop.on ? launch_gemm_any : launch_gemm_nt)(x, K, K, f.wd, K, M, N, u, B, r, scale, y,
+                                                          st, nullptr);
   } else if (e == hipSuccess) {
     e = launch_qgemm_fwd(to_state(w), x, M, u, B, r, scale, y, st);
   }
@@ -513,12 +513,12 @@ qn_status backward(const Base& base, const uint16_t* x, const qn_act8* x8, const
     else
       e = launch_bwd_aux(aux, st);
   }
-  // (the backward from an 8-bit checkpoint under a stored mask or none keeps its product)
-  const bool few = (base.mx || lo.drop.on) && gemm_few_ok(M, K);
+  // (the calls that were there keep their product)
+  const bool any = base.mx || lo.drop.on;
   if (e == hipSuccess && dX) {
     if (dense_dx)
-      e = (few ? launch_gemm_few : launch_gemm_nt)(dY, N, N, b.wt, b.ldt, M, K, b.v, b.At, r,
-                                                   scale, dX, st, lo.mask);
+      e = (any ? launch_gemm_any : launch_gemm_nt)(dY, N, N, b.wt, b.ldt, M, K, b.v, b.At, r, scale,
+                                                   dX, st, lo.mask);
     else
       e = launch_qgemm_dx(to_state(base.w), dY, M, b.v, A, r, scale, dX, st, lo.mask);
   }
@@ -1161,8 +1161,7 @@ qn_status mx4_linear_bwd(const qn_mx4* w, const uint16_t* x, const qn_act8* x8,
   hipStream_t st = static_cast<hipStream_t>(stream);
   hipError_t e = launch_mx4_dequant_t(to_mx4(w), wt, ldt, BwdAux{}, st);
   if (e == hipSuccess)
-    e = (gemm_few_ok(M, w->cols) ? launch_gemm_few : launch_gemm_nt)(
-        dY, N, N, wt, ldt, M, w->cols, nullptr, nullptr, 0, 0.f, dX, st, nullptr);
+    e = launch_gemm_any(dY, N, N, wt, ldt, M, w->cols, nullptr, nullptr, 0, 0.f, dX, st, nullptr);
   return from_hip(e);
 }
 

@@ -9,6 +9,8 @@
 // sums meet in LDS.  Bound by Bm from memory for a few rows, else by A from the second
 // level cache, which the workgroups of a block of rows all read.  M = 1, Nc = 5112,
 // R = 2688 9.0 us (27 MB of Bm), M = 100, 1024 and 1024 7.7; by tiles 23 and 12.4.
+#include <type_traits>
+
 #include "qn_device.h"
 #include "qn_internal.h"
 
@@ -38,6 +40,18 @@ __device__ __forceinline__ void ranks(const float* row, int j, int r, f32x4 v[2]
   if (j >= r) return;
 #pragma unroll
   for (int q = 0; q < 8; ++q) v[q >> 2][q & 3] = j + q < r ? row[j + q] : 0.f;
+}
+
+// s V's eight ranks as bf16: the high parts, or what they leave
+__device__ __forceinline__ bf16x8 split(const f32x4 v[2], float s, bool rest) {
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float x = s * v[q >> 1][2 * (q & 1)], z = s * v[q >> 1][2 * (q & 1) + 1];
+    const uint32_t hi = pack_bf16x2(x, z);
+    w[q] = rest ? pack_bf16x2(x - bf16_lo(hi), z - bf16_hi(hi)) : hi;
+  }
+  return __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
 }
 
 template <int MT, int NT>
@@ -119,14 +133,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_gemm_few(
   if (share) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      uint32_t w[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float x = s * va[m][q >> 1][2 * (q & 1)], z = s * va[m][q >> 1][2 * (q & 1) + 1];
-        const uint32_t hi = pack_bf16x2(x, z);
-        w[q] = g >= 2 ? pack_bf16x2(x - bf16_lo(hi), z - bf16_hi(hi)) : hi;
-      }
-      const bf16x8 v = __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
+      const bf16x8 v = split(va[m], s, g >= 2);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         f32x4 low = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, lb[i]), v,
@@ -154,6 +161,224 @@ __global__ __launch_bounds__(64 * kWaves) void k_gemm_few(
   }
 }
 
+// ---- A few tiles: the product by LDS tiles BM x BN, WVM x WVN waves of TM x TN tiles of
+// v_mfma_f32_16x16x32_bf16, four stages of 64 columns deep.  Where tiles are fewer than
+// compute units, loads in flight bound a unit: four stages of small tiles on many units
+// instead of gemm_bf16.hip's 128 x 128 (M = 128, 4096 x 4096: the product 15 us).  Rows of
+// 128 bytes go from global memory straight into LDS; chunk c (16 bytes) of row y
+// sits at unit c ^ ((y >> 1) & 7); lane (g, n) takes row n's chunk 4 t + g in half t.  The
+// fragments of the next half are read while this one's products run; at the end of
+// half 0 every wave has read the stage and the next step has landed, and half 1 sends the
+// step four ahead into it.
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ rsrc_t make_rs(const void* base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  const uint64_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+  const uint64_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(lo | (hi << 32)), 0,
+                                           __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
+}
+__device__ __forceinline__ void dma16(rsrc_t rs, uint32_t voff, uint32_t soff, uint8_t* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)lds, 16, voff, soff, 0, 0);
+}
+__device__ __forceinline__ void barrier_lds() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void unrolled(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    unrolled<N, I + 1>(f);
+  }
+}
+
+template <int WVM, int WVN, int TM, int TN>
+struct TileGeo {
+  static constexpr int WAVES = WVM * WVN, NST = 4;
+  static constexpr int BM = 16 * TM * WVM, BN = 16 * TN * WVN;
+  static constexpr int AB = BM * 128, STB = AB + BN * 128;          // bytes of A, of a stage
+  static constexpr int OUTP = 32 * TN + 16, OUTW = 16 * TM * OUTP;  // output staging of a wave
+  static constexpr int LDS = NST * STB;
+  static constexpr int AL = BM / 8 / WAVES, BL = BN / 8 / WAVES;    // loads of a wave and step
+  static_assert(WAVES * OUTW <= LDS && LDS <= 160 * 1024, "LDS");
+};
+
+template <int WVM, int WVN, int TM, int TN>
+__global__ __launch_bounds__(64 * WVM * WVN) void k_gemm_tiles(
+    const uint16_t* __restrict__ A, int64_t lda, int64_t R, const uint16_t* __restrict__ Bm,
+    int64_t ldb, int64_t M, int64_t Nc, const float* __restrict__ V,
+    const uint16_t* __restrict__ L, int r, float s, uint16_t* __restrict__ C,
+    const uint8_t* __restrict__ mask, int tiles_m) {
+  using G = TileGeo<WVM, WVN, TM, TN>;
+  constexpr int BM = G::BM, BN = G::BN, NST = G::NST, AL = G::AL, BL = G::BL, LPS = AL + BL;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WVN, wn = wave % WVN;
+  // neighbouring tiles on one XCD (a workgroup's is its index mod 8): Bm's rows come into
+  // one second level cache only
+  const int per = (int)gridDim.x / 8, more = (int)gridDim.x % 8, xcd = (int)blockIdx.x % 8;
+  const int tile = xcd * per + min(xcd, more) + (int)blockIdx.x / 8;
+  const int tn = tile / tiles_m, tm = tile - tn * tiles_m;
+  const int64_t m0 = (int64_t)tm * BM, c0 = (int64_t)tn * BN;
+  const int mrows = (int)min((int64_t)BM, M - m0), ncols = (int)min((int64_t)BN, Nc - c0);
+  const int steps = (int)((R + 63) / 64);
+
+  // load i of wave w: rows 8 (AL w + i) + l / 8 (past the matrix: its last row)
+  const rsrc_t ra = make_rs(A + m0 * lda, (uint32_t)(mrows * lda * 2));
+  const rsrc_t rb = make_rs(Bm + c0 * ldb, (uint32_t)(ncols * ldb * 2));
+  uint32_t aoff[AL], back[AL], boff[BL];
+#pragma unroll
+  for (int i = 0; i < AL; ++i) {
+    const int row = 8 * (AL * wave + i) + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
+    aoff[i] = (uint32_t)((min(row, mrows - 1) * lda + 8 * chunk) * 2);
+    // a chunk of the last step past R: the row's last one (its partner in Bm is zero)
+    const int64_t k = (int64_t)(steps - 1) * 64 + 8 * chunk;
+    back[i] = k >= R ? (uint32_t)(2 * (k - (R - 8))) : 0u;
+  }
+#pragma unroll
+  for (int i = 0; i < BL; ++i) {
+    const int row = 8 * (BL * wave + i) + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
+    boff[i] = (uint32_t)((min(row, ncols - 1) * ldb + 8 * chunk) * 2);
+  }
+  auto load_one = [&](int q, int st, int stage) {
+    uint8_t* base = smem + stage * G::STB;
+    const uint32_t so = (uint32_t)st * 128, last = st == steps - 1 ? ~0u : 0u;
+    if (q < AL)
+      dma16(ra, aoff[q] - (back[q] & last), so, base + 1024 * (AL * wave + q));
+    else
+      dma16(rb, boff[q - AL], so, base + G::AB + 1024 * (BL * wave + q - AL));
+  };
+  int roff[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) roff[t] = n * 128 + 16 * ((4 * t + g) ^ ((n >> 1) & 7));
+  const int abase = wm * 16 * TM * 128, bbase = G::AB + wn * 16 * TN * 128;
+  auto frag = [&](int stage, int base, int k, int t) {
+    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(
+                                          smem + stage * G::STB + base + k * 2048 + roff[t]));
+  };
+  f32x4 acc[TM][TN] = {};
+  bf16x8 fa[TM], fb[2][TN];
+#pragma unroll
+  for (int k = 0; k < NST; ++k)
+#pragma unroll
+    for (int q = 0; q < LPS; ++q) load_one(q, min(k, steps - 1), k);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 1) * LPS) : "memory");
+  barrier_lds();
+#pragma unroll
+  for (int i = 0; i < TM; ++i) fa[i] = frag(0, abase, i, 0);
+#pragma unroll
+  for (int j = 0; j < TN; ++j) fb[0][j] = frag(0, bbase, j, 0);
+
+  auto half = [&](auto p_t, auto t_t, int st) {
+    constexpr int P = decltype(p_t)::value, H = decltype(t_t)::value;
+    constexpr int RS = H == 0 ? P : (P + 1) % NST, RH = H ^ 1, PER = (LPS + TM - 1) / TM;
+    const int lst = min(st + NST, steps - 1);
+    unrolled<TM>([&](auto i_t) {
+      constexpr int i = decltype(i_t)::value;
+      unrolled<TN>([&](auto j_t) {
+        constexpr int j = decltype(j_t)::value;
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[H][j], fa[i], acc[i][j], 0, 0, 0);
+        if (i == 0) fb[RH][j] = frag(RS, bbase, j, RH);
+        if (H == 1 && j == TN / 2)
+          for (int q = PER * i; q < PER * (i + 1); ++q)
+            if (q < LPS) load_one(q, lst, P);
+      });
+      fa[i] = frag(RS, abase, i, RH);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    if (H == 0) {
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * LPS) : "memory");
+      barrier_lds();
+    }
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  int st = 0;
+  for (; st + NST <= steps; st += NST)
+    unrolled<NST>([&](auto p) {
+      half(p, I0{}, st + (int)p);
+      half(p, I1{}, st + (int)p);
+    });
+  unrolled<NST - 1>([&](auto p) {
+    if (st < steps) {
+      half(p, I0{}, st);
+      half(p, I1{}, st++);
+    }
+  });
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  barrier_lds();
+
+  // the adapter term, as in k_gemm_few, in accumulators of its own for the mask's sake
+  f32x4 low[TM][TN] = {};
+  for (int j0 = 0; j0 < r; j0 += 16) {
+    const int jl = j0 + 8 * (g & 1);
+    u32x4 lb[TN];
+    f32x4 va[TM][2];
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+      lb[j] = ranks(L + min(c0 + 16 * (TN * wn + j) + n, Nc - 1) * r, jl, r);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) ranks(V + min(m0 + 16 * (TM * wm + i) + n, M - 1) * r, jl, r, va[i]);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const bf16x8 v = split(va[i], s, g >= 2);
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        low[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, lb[j]), v,
+                                                            low[i][j], 0, 0, 0);
+    }
+  }
+  // lane: row n of tile (i, j), columns 4 g .. 4 g + 3; through the wave's LDS staging tile,
+  // which leaves as rows of 32 TN bytes
+  uint8_t* stg = smem + wave * G::OUTW;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int64_t row = min(m0 + 16 * (TM * wm + i) + n, M - 1);
+    uint32_t kb[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j)  // (Nc % 64 == 0 with a mask: a byte is half a tile's columns)
+      kb[j] = !mask ? 15u
+                    : mask[((row * Nc + min(c0 + 16 * (TN * wn + j), Nc - 16)) >> 3) + (g >> 1)] >>
+                          (4 * (g & 1));
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      f32x4 c = acc[i][j];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if ((kb[j] >> q) & 1) c[q] += low[i][j][q];
+      *reinterpret_cast<u32x2*>(stg + (16 * i + n) * G::OUTP + 2 * (16 * j + 4 * g)) =
+          u32x2{pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3])};
+    }
+  }
+  // (a wave's LDS accesses execute in order)
+  constexpr int LR = 2 * TN, RPS = 64 / LR;  // lanes of a row, rows a store
+  const int lc = lane % LR;
+  const int64_t col = c0 + 16 * TN * wn + 8 * lc, row0 = m0 + 16 * TM * wm;
+#pragma unroll
+  for (int q = 0; q < 16 * TM / RPS; ++q) {
+    const int rl = RPS * q + lane / LR;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(stg + rl * G::OUTP + 16 * lc);
+    if (row0 + rl < M && col < Nc) *reinterpret_cast<u32x4*>(C + (row0 + rl) * Nc + col) = v;
+  }
+}
+
+template <int WVM, int WVN, int TM, int TN>
+hipError_t launch_tiles(const uint16_t* A, int64_t lda, int64_t R, const uint16_t* Bm, int64_t ldb,
+                        int64_t M, int64_t Nc, const float* V, const uint16_t* L, int r, float s,
+                        uint16_t* C, const uint8_t* mask, hipStream_t st) {
+  using G = TileGeo<WVM, WVN, TM, TN>;
+  static const hipError_t attr =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(k_gemm_tiles<WVM, WVN, TM, TN>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, G::LDS);
+  if (attr != hipSuccess) return attr;
+  const int64_t tm = (M + G::BM - 1) / G::BM, tn = (Nc + G::BN - 1) / G::BN;
+  hipLaunchKernelGGL((k_gemm_tiles<WVM, WVN, TM, TN>), dim3((unsigned)(tm * tn)),
+                     dim3(64 * G::WAVES), G::LDS, st, A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, mask,
+                     (int)tm);
+  return hipGetLastError();
+}
+
 template <int MT, int NT>
 hipError_t launch(const uint16_t* A, int64_t lda, int64_t R, const uint16_t* Bm, int64_t ldb,
                   int64_t M, int64_t Nc, const float* V, const uint16_t* L, int r, float s,
@@ -167,20 +392,18 @@ hipError_t launch(const uint16_t* A, int64_t lda, int64_t R, const uint16_t* Bm,
 
 }  // namespace
 
-// 32 rows of Bm a workgroup instead of 16 where there are enough of them.  Every
-// workgroup's pass over A against the tiles' steps: M = 16, Nc = 4096, R = 14336 (the
-// whole backward) 81 us instead of 123, M = 1, 2688 and 5112 50 and 80, but M = 64, 14336
-// and 4096 97 and 68, M = 128, 4096 and 4096 70 and 58.
+// 32 rows of Bm a workgroup instead of 16 where there are enough of them.
 static bool wide_tiles(int64_t Nc) { return Nc >= 16 * 512; }
-bool gemm_few_ok(int64_t M, int64_t Nc) {
+// Every workgroup's pass over A against the tiles' steps: M = 16, Nc = 4096, R = 14336
+// (the whole backward) 77 us instead of 123, M = 1, 2688 and 5112 42 and 80, but M = 64,
+// 14336 and 4096 97 and 68.
+static bool few_rows(int64_t M, int64_t Nc) {
   return M <= 128 && M * Nc <= ((int64_t)1 << 18) * (wide_tiles(Nc) ? 2 : 1);
 }
 
-hipError_t launch_gemm_few(const uint16_t* A, int64_t lda, int64_t R, const uint16_t* Bm,
+static hipError_t launch_few(const uint16_t* A, int64_t lda, int64_t R, const uint16_t* Bm,
                            int64_t ldb, int64_t M, int64_t Nc, const float* V, const uint16_t* L,
                            int r, float s, uint16_t* C, hipStream_t st, const uint8_t* mask) {
-  if (M <= 0) return hipSuccess;
-  if (M > 128 || r > 16 * kWaves || (mask && Nc % 64 != 0) || R < 8 || R % 8 != 0 || R > ldb) return hipErrorInvalidValue;
   const bool wide = wide_tiles(Nc);
 #define QN_FEW(MT)                                                                          \
   return wide ? launch<MT, 2>(A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, mask, st)            \
@@ -189,6 +412,38 @@ hipError_t launch_gemm_few(const uint16_t* A, int64_t lda, int64_t R, const uint
   if (M <= 32) QN_FEW(2);
   QN_FEW(4);
 #undef QN_FEW
+}
+
+static int64_t compute_units() {
+  static const int n = [] {
+    int dev = 0, cus = 0;
+    if (hipGetDevice(&dev) != hipSuccess ||
+        hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+      return 256;
+    return cus > 0 ? cus : 256;
+  }();
+  return n;
+}
+
+hipError_t launch_gemm_any(const uint16_t* A, int64_t lda, int64_t R, const uint16_t* Bm,
+                           int64_t ldb, int64_t M, int64_t Nc, const float* V, const uint16_t* L,
+                           int r, float s, uint16_t* C, hipStream_t st, const uint8_t* mask) {
+  if (M <= 0) return hipSuccess;
+  if (r > 64 || (mask && Nc % 64 != 0) || R < 8 || R % 8 != 0 || ldb % 64 != 0 || R > ldb ||
+      Nc % 8 != 0)
+    return hipErrorInvalidValue;
+  if (few_rows(M, Nc)) return launch_few(A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, st, mask);
+  // the smallest tiles that still go one to a compute unit (the whole call, small tiles and
+  // gemm_bf16.hip's: M = 128, 4096 and 4096 37.4 and 48.2 us, M = 65, 10560 and 4768 64 and 88,
+  // by 64 x 128 tiles M = 512, 14336 and 4096 108 and 116, M = 126, 12896 and 12672 260 and
+  // 295; 128 x 128 tiles four stages deep lose: M = 1024, 4096 and 4096 52.5 and 48.4)
+  const int64_t cu = compute_units();
+  const auto tiles = [&](int64_t tm, int64_t tn) { return (M + tm - 1) / tm * ((Nc + tn - 1) / tn); };
+  if (tiles(64, 64) <= cu)
+    return launch_tiles<2, 2, 2, 2>(A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, mask, st);
+  if (tiles(64, 128) <= cu)
+    return launch_tiles<2, 2, 2, 4>(A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, mask, st);
+  return launch_gemm_nt(A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, st, mask);
 }
 
 }  // namespace qn

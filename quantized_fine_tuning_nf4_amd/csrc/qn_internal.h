@@ -257,13 +257,11 @@ hipError_t launch_gemm_nt(const uint16_t* A, int64_t lda, int64_t R, const uint1
                           int r, float s, uint16_t* C, hipStream_t st,
                           const uint8_t* mask = nullptr);
 
-// The same product for batches of few rows (M <= 128; ldb as R or longer, zero there),
-// worth it where gemm_few_ok.
-bool gemm_few_ok(int64_t M, int64_t Nc);
-hipError_t launch_gemm_few(const uint16_t* A, int64_t lda, int64_t R, const uint16_t* Bm,
+// The same product, by kernels for few rows and for few tiles where they are faster
+// (r == 0: no second term, V and L null).
+hipError_t launch_gemm_any(const uint16_t* A, int64_t lda, int64_t R, const uint16_t* Bm,
                            int64_t ldb, int64_t M, int64_t Nc, const float* V, const uint16_t* L,
-                           int r, float s, uint16_t* C, hipStream_t st,
-                           const uint8_t* mask = nullptr);
+                           int r, float s, uint16_t* C, hipStream_t st, const uint8_t* mask);
 
 // Weight state as the kernels take it.
 struct WState;

@@ -165,6 +165,12 @@ def test_nf4_linear_takes_the_same_mask(qn, M, rows, cols, r, act8):
                   ).max()) <= 0
 
 
+@pytest.mark.parametrize("M,rows,cols,r", [(300, 136, 320, 7), (1000, 1152, 1088, 16),
+                                           (1030, 2112, 2112, 33)])
+def test_nf4_linear_by_a_few_tiles(qn, M, rows, cols, r):
+    test_nf4_linear_takes_the_same_mask(qn, M, rows, cols, r, False)
+
+
 @pytest.mark.parametrize("M,rows,cols,r", [(1, 64, 1024, 8), (3, 4096, 4096, 16), (16, 64, 2048, 40),
                                            (40, 136, 320, 7), (2050, 2112, 4608, 16)])
 @pytest.mark.parametrize("p", [0.0, 1e-7])

@@ -275,6 +275,26 @@ def test_backward(qn, M, rows, cols, r, act8, p):
         _check(dB3, dB.double(), 2 * part * s * G.abs().t() @ u.double().abs() + 1e-30, "dB, no u")
 
 
+# a few tiles of each size, the last ones ragged; reductions of one chunk, of one step, of
+# one more than the stages
+TILES = [(300, 72, 320, 7), (129, 8, 64, 64), (1000, 264, 1152, 16), (1030, 328, 2112, 33)]
+
+
+@pytest.mark.parametrize("M,rows,cols,r", TILES)
+@pytest.mark.parametrize("p", [0.0, 0.2])
+def test_backward_by_a_few_tiles(qn, M, rows, cols, r, p):
+    test_backward(qn, M, rows, cols, r, False, p)
+
+
+@pytest.mark.parametrize("M,rows,cols,r", TILES)
+def test_frozen_backward_by_a_few_tiles(qn, M, rows, cols, r):
+    say(f"[mx4 frozen bwd] M={M} rows={rows} cols={cols}")
+    w, d = _linear(qn, M, rows, cols, r, seed=M + cols)
+    dX, _, _ = qn.mx4_linear_bwd(w, None, d["dY"])
+    G, b = d["dY"].double(), _values(w, qn)
+    _check(dX, G @ b, _bound(G @ b, G.abs() @ b.abs(), rows, 0), "dX")
+
+
 def test_no_numbers_in_the_backward(qn):
     """A block of W that is no number makes its columns of dX NaN, a NaN of dY its row."""
     say("[mx4 bwd nan]")
