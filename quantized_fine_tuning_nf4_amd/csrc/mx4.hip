@@ -30,8 +30,8 @@ __device__ __forceinline__ void load8(const uint16_t* row, int64_t c, int64_t K,
 }
 __device__ __forceinline__ void load8(const float* row, int64_t c, int64_t K, float v[8]) {
   if (c + 8 <= K) {
-    const u32x4 a = *reinterpret_cast<const u32x4_any*>(row + c);
-    const u32x4 b = *reinterpret_cast<const u32x4_any*>(row + c + 4);
+    const u32x4 a = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(row + c));
+    const u32x4 b = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(row + c + 4));
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       v[q] = as_f32(a[q]);
@@ -963,28 +963,16 @@ namespace {
 template <int WVM, int WVN, int TM, int TN, int NST>
 hipError_t launch_tiles(const Mx4& w, const Mx4X& x, uint16_t* y, hipStream_t st) {
   using G = MxGeo<WVM, WVN, TM, TN, NST>;
-  static const hipError_t attr = [] {
-    const hipError_t e = hipFuncSetAttribute(
-        reinterpret_cast<const void*>(k_mx4_gemm<WVM, WVN, TM, TN, NST, true>),
-        hipFuncAttributeMaxDynamicSharedMemorySize, G::LDS_BYTES);
-    return e != hipSuccess
-               ? e
-               : hipFuncSetAttribute(
-                     reinterpret_cast<const void*>(k_mx4_gemm<WVM, WVN, TM, TN, NST, false>),
-                     hipFuncAttributeMaxDynamicSharedMemorySize, G::LDS_MAIN);
-  }();
-  if (attr != hipSuccess) return attr;
   const int64_t tm = (x.M + G::BM - 1) / G::BM, tn = (w.rows + G::BN - 1) / G::BN;
-  const dim3 grid((unsigned)(tm * tn)), block(G::THREADS);
-  const int J = (int)mx4_steps(w.cols), nj = (x.r + 15) / 16;
-  if (nj == 1)
-    hipLaunchKernelGGL((k_mx4_gemm<WVM, WVN, TM, TN, NST, true>), grid, block, G::LDS_BYTES, st, w.codes,
-                       w.scales, x.codes, x.scales, x.M, w.rows, J, x.su, x.bo, nj, y, (int)tm,
-                       (int)tn);
-  else
-    hipLaunchKernelGGL((k_mx4_gemm<WVM, WVN, TM, TN, NST, false>), grid, block, G::LDS_MAIN, st, w.codes,
-                       w.scales, x.codes, x.scales, x.M, w.rows, J, x.su, x.bo, nj, y, (int)tm,
-                       (int)tn);
+  const int J = (int)mx4_steps(w.cols), nj = (x.r + 15) / 16, lds = nj == 1 ? G::LDS_BYTES : G::LDS_MAIN;
+  const auto kernel = nj == 1 ? k_mx4_gemm<WVM, WVN, TM, TN, NST, true>
+                              : k_mx4_gemm<WVM, WVN, TM, TN, NST, false>;
+  // (the attribute is the current device's)
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(tm * tn)), dim3(G::THREADS), lds, st, w.codes, w.scales,
+                     x.codes, x.scales, x.M, w.rows, J, x.su, x.bo, nj, y, (int)tm, (int)tn);
   return hipGetLastError();
 }
 
