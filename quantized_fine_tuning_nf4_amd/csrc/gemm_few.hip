@@ -1,14 +1,11 @@
-// bf16 product of few rows with the adapter term:
+// bf16 products of small outputs with the adapter term:
 //
 //   C[M, Nc] (bf16) = A[M, R] Bm[Nc, R]^T + s V[M, r] L[Nc, r]^T (.) mask
 //
-// the same as gemm_bf16.hip's, for batches of up to 128 rows, where that kernel has too
-// few tiles to fill the chip (M = 1, Nc = 5112, R = 2688: 40 workgroups walk 42 steps).
-// Here a workgroup takes 16 NT rows of Bm, straight into registers, and up to 64 rows of A
-// (16 MT), its eight waves the steps of 32 in turn and a block of 16 ranks each; their
-// sums meet in LDS.  Bound by Bm from memory for a few rows, else by A from the second
-// level cache, which the workgroups of a block of rows all read.  M = 1, Nc = 5112,
-// R = 2688 9.0 us (27 MB of Bm), M = 100, 1024 and 1024 7.7; by tiles 23 and 12.4.
+// the same as gemm_bf16.hip's, where that kernel's 128 x 128 tiles are too few to fill the
+// chip (M = 1, Nc = 5112, R = 2688: 40 workgroups walk 42 steps).  Two kernels:
+// k_gemm_few splits the reduction over a workgroup's waves, k_gemm_tiles takes small
+// LDS tiles; launch_gemm_any chooses.
 #include <type_traits>
 
 #include "qn_device.h"
@@ -54,59 +51,58 @@ __device__ __forceinline__ bf16x8 split(const f32x4 v[2], float s, bool rest) {
   return __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
 }
 
-template <int MT, int NT>
+// ---- 16 MT rows of A and 16 of Bm a workgroup, straight into registers: its eight waves
+// take the steps of 32 in turn, their loads out together, and a block of 16 ranks each;
+// their sums meet in LDS.  Bound by the latency of one pass over the operands, so
+// worth it where every workgroup has a compute unit of its own (M = 100, Nc = R = 1024
+// 6.1 us by 256 workgroups; M = 1, 4096 and 4096 8.1, 34 MB of Bm).
+template <int MT>
 __global__ __launch_bounds__(64 * kWaves) void k_gemm_few(
     const uint16_t* __restrict__ A, int64_t lda, int64_t R, const uint16_t* __restrict__ Bm,
     int64_t ldb, int M, int64_t Nc, const float* __restrict__ V, const uint16_t* __restrict__ L,
     int r, float s, uint16_t* __restrict__ C, const uint8_t* __restrict__ mask, int col_wgs) {
-  constexpr int ROWS = 16 * NT, PITCH = ROWS + 4, THREADS = 64 * kWaves;
-  constexpr int U = MT * NT >= 4 ? 4 : 8;  // steps whose loads go out together
+  constexpr int PITCH = 16 + 4, THREADS = 64 * kWaves;
+  constexpr int U = 8;  // steps whose loads go out together
   __shared__ __attribute__((aligned(16))) float sums[kWaves][16 * MT][PITCH];
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int mb = (int)blockIdx.x / col_wgs;  // a batch past 64 rows goes in two
-  const int64_t c0 = (int64_t)((int)blockIdx.x - mb * col_wgs) * ROWS;
+  const int mb = (int)blockIdx.x / col_wgs;  // block of 16 MT rows
+  const int64_t c0 = (int64_t)((int)blockIdx.x - mb * col_wgs) * 16;
   A += (int64_t)mb * 16 * MT * lda;
   V += (int64_t)mb * 16 * MT * r;
   C += (int64_t)mb * 16 * MT * Nc;
   if (mask) mask += (int64_t)mb * 16 * MT * Nc / 8;
   M = min(M - mb * 16 * MT, 16 * MT);
-  const uint16_t *ap[MT], *bp[NT];
+  const uint16_t* ap[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) ap[i] = A + (int64_t)min(16 * i + n, M - 1) * lda + 8 * g;
-#pragma unroll
-  for (int i = 0; i < NT; ++i) bp[i] = Bm + min(c0 + 16 * i + n, Nc - 1) * ldb + 8 * g;
+  const uint16_t* bp = Bm + min(c0 + n, Nc - 1) * ldb + 8 * g;
   const int64_t lim = R - 8 * g;  // columns left for this lane's chunk (R % 8 == 0)
   const int steps = (int)((R + 31) / 32);
   // a block of 16 ranks is a wave's: its operands and keep bits go out first
   const int jl = 16 * wave + 8 * (g & 1);
   const bool share = 16 * wave < r;
-  u32x4 lb[NT];
+  u32x4 lb;
   f32x4 va[MT][2];
-  uint32_t kb[MT][NT];
+  uint32_t kb[MT];
   if (share) {
-#pragma unroll
-    for (int i = 0; i < NT; ++i) lb[i] = ranks(L + min(c0 + 16 * i + n, Nc - 1) * r, jl, r);
+    lb = ranks(L + min(c0 + n, Nc - 1) * r, jl, r);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int64_t row = min(16 * m + n, M - 1);
       ranks(V + row * r, jl, r, va[m]);
       if (mask)  // (Nc % 64 == 0: a byte is half a tile's columns)
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-          kb[m][i] = mask[((row * Nc + min(c0 + 16 * i, Nc - 16)) >> 3) + (g >> 1)] >> (4 * (g & 1));
+        kb[m] = mask[((row * Nc + c0) >> 3) + (g >> 1)] >> (4 * (g & 1));
     }
   }
-  f32x4 acc[MT][NT] = {};
+  f32x4 acc[MT] = {};
   for (int s0 = wave * U; s0 < steps; s0 += U * kWaves) {
-    u32x4 a[U][MT], b[U][NT];
+    u32x4 a[U][MT], b[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t off = 32 * (int64_t)(s0 + u);
       const bool in = off < lim;  // past the row: its first columns, zero in both operands
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-        b[u][i] = *reinterpret_cast<const u32x4*>(bp[i] + (in ? off : -8 * g));
+      b[u] = *reinterpret_cast<const u32x4*>(bp + (in ? off : -8 * g));
 #pragma unroll
       for (int i = 0; i < MT; ++i)
         a[u][i] = *reinterpret_cast<const u32x4*>(ap[i] + (in ? off : -8 * g));
@@ -114,17 +110,13 @@ __global__ __launch_bounds__(64 * kWaves) void k_gemm_few(
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const bool in = 32 * (int64_t)(s0 + u) < lim;
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-        if (!in) b[u][i] = u32x4{0u, 0u, 0u, 0u};
+      if (!in) b[u] = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         if (!in) a[u][m] = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-          acc[m][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8, b[u][i]), __builtin_bit_cast(bf16x8, a[u][m]), acc[m][i],
-              0, 0, 0);
+        acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b[u]),
+                                                         __builtin_bit_cast(bf16x8, a[u][m]),
+                                                         acc[m], 0, 0, 0);
       }
     }
   }
@@ -133,27 +125,21 @@ __global__ __launch_bounds__(64 * kWaves) void k_gemm_few(
   if (share) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const bf16x8 v = split(va[m], s, g >= 2);
+      const f32x4 low = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+          __builtin_bit_cast(bf16x8, lb), split(va[m], s, g >= 2), f32x4{}, 0, 0, 0);
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        f32x4 low = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, lb[i]), v,
-                                                            f32x4{}, 0, 0, 0);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (!mask || ((kb[m][i] >> q) & 1)) acc[m][i][q] += low[q];
-      }
+      for (int q = 0; q < 4; ++q)
+        if (!mask || ((kb[m] >> q) & 1)) acc[m][q] += low[q];
     }
   }
-  // lane: row 16 m + n of C, columns 16 i + 4 g + 0 .. 3
+  // lane: row 16 m + n of C, columns 4 g + 0 .. 3
 #pragma unroll
   for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-      *reinterpret_cast<f32x4*>(&sums[wave][16 * m + n][16 * i + 4 * g]) = acc[m][i];
+    *reinterpret_cast<f32x4*>(&sums[wave][16 * m + n][4 * g]) = acc[m];
   __syncthreads();
-  const int c = tid % ROWS;
+  const int c = tid % 16;
   if (c0 + c >= Nc) return;
-  for (int m = tid / ROWS; m < M; m += THREADS / ROWS) {
+  for (int m = tid / 16; m < M; m += THREADS / 16) {
     float t = sums[0][m][c];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) t += sums[w][m][c];
@@ -368,7 +354,8 @@ hipError_t launch_tiles(const uint16_t* A, int64_t lda, int64_t R, const uint16_
                         int64_t M, int64_t Nc, const float* V, const uint16_t* L, int r, float s,
                         uint16_t* C, const uint8_t* mask, hipStream_t st) {
   using G = TileGeo<WVM, WVN, TM, TN>;
-  static const hipError_t attr =
+  // (the attribute is the current device's)
+  const hipError_t attr =
       hipFuncSetAttribute(reinterpret_cast<const void*>(k_gemm_tiles<WVM, WVN, TM, TN>),
                           hipFuncAttributeMaxDynamicSharedMemorySize, G::LDS);
   if (attr != hipSuccess) return attr;
@@ -379,40 +366,17 @@ hipError_t launch_tiles(const uint16_t* A, int64_t lda, int64_t R, const uint16_
   return hipGetLastError();
 }
 
-template <int MT, int NT>
-hipError_t launch(const uint16_t* A, int64_t lda, int64_t R, const uint16_t* Bm, int64_t ldb,
-                  int64_t M, int64_t Nc, const float* V, const uint16_t* L, int r, float s,
-                  uint16_t* C, const uint8_t* mask, hipStream_t st) {
-  const int col_wgs = (int)((Nc + 16 * NT - 1) / (16 * NT));
-  hipLaunchKernelGGL((k_gemm_few<MT, NT>), dim3((unsigned)(col_wgs * ((M + 16 * MT - 1) / (16 * MT)))),
-                     dim3(64 * kWaves), 0, st, A, lda, R, Bm, ldb, (int)M, Nc, V, L, r, s, C, mask,
-                     col_wgs);
+template <int MT>
+hipError_t launch_few(const uint16_t* A, int64_t lda, int64_t R, const uint16_t* Bm, int64_t ldb,
+                      int64_t M, int64_t Nc, const float* V, const uint16_t* L, int r, float s,
+                      uint16_t* C, const uint8_t* mask, hipStream_t st) {
+  const int64_t col_wgs = (Nc + 15) / 16, row_wgs = (M + 16 * MT - 1) / (16 * MT);
+  hipLaunchKernelGGL(k_gemm_few<MT>, dim3((unsigned)(col_wgs * row_wgs)), dim3(64 * kWaves), 0, st, A,
+                     lda, R, Bm, ldb, (int)M, Nc, V, L, r, s, C, mask, (int)col_wgs);
   return hipGetLastError();
 }
 
 }  // namespace
-
-// 32 rows of Bm a workgroup instead of 16 where there are enough of them.
-static bool wide_tiles(int64_t Nc) { return Nc >= 16 * 512; }
-// Every workgroup's pass over A against the tiles' steps: M = 16, Nc = 4096, R = 14336
-// (the whole backward) 77 us instead of 123, M = 1, 2688 and 5112 42 and 80, but M = 64,
-// 14336 and 4096 97 and 68.
-static bool few_rows(int64_t M, int64_t Nc) {
-  return M <= 128 && M * Nc <= ((int64_t)1 << 18) * (wide_tiles(Nc) ? 2 : 1);
-}
-
-static hipError_t launch_few(const uint16_t* A, int64_t lda, int64_t R, const uint16_t* Bm,
-                           int64_t ldb, int64_t M, int64_t Nc, const float* V, const uint16_t* L,
-                           int r, float s, uint16_t* C, hipStream_t st, const uint8_t* mask) {
-  const bool wide = wide_tiles(Nc);
-#define QN_FEW(MT)                                                                          \
-  return wide ? launch<MT, 2>(A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, mask, st)            \
-              : launch<MT, 1>(A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, mask, st)
-  if (M <= 16) QN_FEW(1);
-  if (M <= 32) QN_FEW(2);
-  QN_FEW(4);
-#undef QN_FEW
-}
 
 static int64_t compute_units() {
   static const int n = [] {
@@ -432,13 +396,18 @@ hipError_t launch_gemm_any(const uint16_t* A, int64_t lda, int64_t R, const uint
   if (r > 64 || (mask && Nc % 64 != 0) || R < 8 || R % 8 != 0 || ldb % 64 != 0 || R > ldb ||
       Nc % 8 != 0)
     return hipErrorInvalidValue;
-  if (few_rows(M, Nc)) return launch_few(A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, st, mask);
-  // the smallest tiles that still go one to a compute unit (the whole call, small tiles and
-  // gemm_bf16.hip's: M = 128, 4096 and 4096 37.4 and 48.2 us, M = 65, 10560 and 4768 64 and 88,
-  // by 64 x 128 tiles M = 512, 14336 and 4096 108 and 116, M = 126, 12896 and 12672 260 and
-  // 295; 128 x 128 tiles four stages deep lose: M = 1024, 4096 and 4096 52.5 and 48.4)
   const int64_t cu = compute_units();
   const auto tiles = [&](int64_t tm, int64_t tn) { return (M + tm - 1) / tm * ((Nc + tn - 1) / tn); };
+  // The smallest that still go one to a compute unit.  The reduction split over a
+  // workgroup's waves against 64 x 64 tiles: M = 64, 1024 and 1024 4.8 and 6.7 us, M = 128,
+  // 1024 and 4096 (two blocks of rows a workgroup) 13.7 and 14.2, M = 64, 2048 and 2048 8.4
+  // and 9.2; with two workgroups a unit and more M = 128, 2048 and 2048 16.8, by four blocks
+  // of rows 12.6, tiles 9.4.  Small tiles against gemm_bf16.hip's (the whole call): M = 128,
+  // 4096 and 4096 37.4 and 48.2 us, M = 65, 10560 and 4768 64 and 88; 64 x 128 tiles M = 512,
+  // 14336 and 4096 108 and 116, M = 126, 12896 and 12672 260 and 295; 128 x 128 tiles four
+  // stages deep lose: M = 1024, 4096 and 4096 52.5 and 48.4.
+  if (tiles(16, 16) <= cu) return launch_few<1>(A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, mask, st);
+  if (tiles(32, 16) <= cu) return launch_few<2>(A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, mask, st);
   if (tiles(64, 64) <= cu)
     return launch_tiles<2, 2, 2, 2>(A, lda, R, Bm, ldb, M, Nc, V, L, r, s, C, mask, st);
   if (tiles(64, 128) <= cu)

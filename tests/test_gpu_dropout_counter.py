@@ -166,6 +166,7 @@ def test_nf4_linear_takes_the_same_mask(qn, M, rows, cols, r, act8):
 
 
 @pytest.mark.parametrize("M,rows,cols,r", [(300, 136, 320, 7), (1000, 1152, 1088, 16),
+                                           (300, 136, 1344, 7), (70, 1344, 8192, 40),
                                            (1030, 2112, 2112, 33)])
 def test_nf4_linear_by_a_few_tiles(qn, M, rows, cols, r):
     test_nf4_linear_takes_the_same_mask(qn, M, rows, cols, r, False)

@@ -277,7 +277,8 @@ def test_backward(qn, M, rows, cols, r, act8, p):
 
 # a few tiles of each size, the last ones ragged; reductions of one chunk, of one step, of
 # one more than the stages
-TILES = [(300, 72, 320, 7), (129, 8, 64, 64), (1000, 264, 1152, 16), (1030, 328, 2112, 33)]
+TILES = [(300, 72, 320, 7), (129, 8, 64, 64), (1000, 264, 1152, 16), (1030, 328, 2112, 33),
+         (300, 72, 1344, 7), (200, 8, 1024, 64), (2000, 40, 64, 5)]
 
 
 @pytest.mark.parametrize("M,rows,cols,r", TILES)
