@@ -458,11 +458,6 @@ qn_status backward(const Base& base, const uint16_t* x, const qn_act8* x8, const
     t.r = r;
     t.s = scale;
     t.three_parts = true;
-    if (lo.drop.on) {
-      t.drop = lo.drop;
-      t.bits = b.bits;
-      t.bits64 = M * K / 64;
-    }
     t.A = A;
     t.At = dense_dx ? b.At : nullptr;
     t.K = K;
@@ -472,7 +467,7 @@ qn_status backward(const Base& base, const uint16_t* x, const qn_act8* x8, const
       e = launch_bwd_aux(t, st);
     if (e == hipSuccess)
       e = launch_thin_v(dY, b.Bt, M, N, r, b.v, b.sv, thin_tn_rows_padded(M, K, true), scale, st,
-                        clr);
+                        clr, lo.drop.on ? KeepBits{lo.drop, b.bits, M * K / 64} : KeepBits{});
   }
   if (e == hipSuccess && !three && !b_rows) {
     if (clr.n) {  // (no earlier launch: a kernel, not a memset, for graph capture)

@@ -138,14 +138,17 @@ __global__ __launch_bounds__(kThreads) void k_thin_nt(const uint16_t* __restrict
 // row.  From the rows of B^T (64 bytes of 16 rows a load) the three took 31.9, 79
 // and 49 us; 32 rows a workgroup, half the bytes of B, 33.0 and 61, since twice
 // the workgroups hide more of the latency.
+// BITS: the keep bits of a dropout from a counter, for the products that follow, are
+// formed while the operands are in flight (8192x4096x4096: 21.9 us with them, 16.4 alone;
+// beside the transposed dequantization they cost 12).
 constexpr int kVWaves = 8;
-template <int NJ>
+template <int NJ, bool BITS>
 __global__ __launch_bounds__(64 * kVWaves) void k_thin_v(const uint16_t* __restrict__ G,
                                                          const uint16_t* __restrict__ Bf,
                                                          int64_t M, int64_t N, int r,
                                                          float* __restrict__ v,
                                                          uint16_t* __restrict__ sv, int64_t Mp,
-                                                         float s, Clear clr) {
+                                                         float s, Clear clr, KeepBits kb) {
   constexpr int U = 4, PITCH = 16 + 4;
   __shared__ __attribute__((aligned(16))) float sums[kVWaves][16 * NJ][PITCH];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
@@ -155,6 +158,26 @@ __global__ __launch_bounds__(64 * kVWaves) void k_thin_v(const uint16_t* __restr
   const int64_t steps = (N + 31) / 32;
   const uint16_t* gp = G + min(m0 + l16, M - 1) * N + 8 * g;
   const int64_t lim = N - 8 * g;  // columns left for this lane's chunk
+  // 64 keep bits a thread and turn, the workgroups past v's rows first
+  const int row_wgs = (int)((Mp + 15) / 16), more = (int)gridDim.x - row_wgs;
+  const int turn = (int)blockIdx.x < row_wgs ? (int)blockIdx.x + more : (int)blockIdx.x - row_wgs;
+  int64_t job = (int64_t)turn * (64 * kVWaves) + tid;
+  const uint64_t offset = BITS ? drop_offset(kb.drop) : 0;
+  auto keep_bits = [&] {
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll 2
+      for (int q = 0; q < 4; ++q)
+        w[h] |= keep_byte(philox(kb.drop, offset, (uint64_t)(8 * job + 4 * h + q)), kb.drop.less)
+                << (8 * q);
+    reinterpret_cast<u32x2*>(kb.bits)[job] = u32x2{w[0], w[1]};
+    job += (int64_t)gridDim.x * (64 * kVWaves);
+  };
+  if (BITS && (int)blockIdx.x >= row_wgs) {
+    while (job < kb.n64) keep_bits();
+    return;
+  }
   f32x4 acc[NJ] = {};
   for (int64_t s0 = U * wave; s0 < steps; s0 += U * kVWaves) {
     u32x4 za[U], tb[U][NJ];
@@ -168,6 +191,7 @@ __global__ __launch_bounds__(64 * kVWaves) void k_thin_v(const uint16_t* __restr
         tb[u][jt] = *reinterpret_cast<const u32x4*>(
             Bf + ((min(s0 + u, steps - 1) * NJ + jt) * 64 + lane) * 8);
     }
+    if (BITS && job < kb.n64) keep_bits();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const bool ok = 32 * (s0 + u) < lim;
@@ -180,6 +204,8 @@ __global__ __launch_bounds__(64 * kVWaves) void k_thin_v(const uint16_t* __restr
       }
     }
   }
+  if constexpr (BITS)
+    while (job < kb.n64) keep_bits();
   // lane: column j = 16jt + l%16, rows 4(l/16) + i
 #pragma unroll
   for (int jt = 0; jt < NJ; ++jt)
@@ -214,10 +240,20 @@ __global__ __launch_bounds__(64 * kVWaves) void k_thin_v(const uint16_t* __restr
 }
 
 hipError_t launch_thin_v(const uint16_t* G, const uint16_t* Bf, int64_t M, int64_t N, int r,
-                         float* v, uint16_t* sv, int64_t Mp, float s, hipStream_t st, Clear clr) {
+                         float* v, uint16_t* sv, int64_t Mp, float s, hipStream_t st, Clear clr,
+                         const KeepBits& kb) {
+  // (keep bits: workgroups of their own, one job a thread, where v's are fewer than two a
+  // compute unit)
+  const int64_t row_wgs = (Mp + 15) / 16, bit_wgs = (kb.n64 + 64 * kVWaves - 1) / (64 * kVWaves);
+  const int64_t more = std::min(bit_wgs, std::max<int64_t>(0, 512 - row_wgs));
+  const dim3 grid((unsigned)(row_wgs + more)), block(64 * kVWaves);
 #define QN_V(NJ)                                                                              \
-  hipLaunchKernelGGL(k_thin_v<NJ>, dim3((unsigned)((Mp + 15) / 16)), dim3(64 * kVWaves), 0, st, G, \
-                     Bf, M, N, r, v, sv, Mp, s, clr)
+  if (kb.n64)                                                                                 \
+    hipLaunchKernelGGL((k_thin_v<NJ, true>), grid, block, 0, st, G, Bf, M, N, r, v, sv, Mp, s, \
+                       clr, kb);                                                              \
+  else                                                                                        \
+    hipLaunchKernelGGL((k_thin_v<NJ, false>), grid, block, 0, st, G, Bf, M, N, r, v, sv, Mp, s, \
+                       clr, kb)
   switch ((r + 15) / 16) {
     case 1: QN_V(1); break;
     case 2: QN_V(2); break;

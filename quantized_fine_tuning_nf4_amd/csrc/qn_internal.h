@@ -39,6 +39,13 @@ struct SliceSum {
   float* out;
 };
 
+// Keep bits of n64 times 64 elements (dropout from a counter); n64 == 0: none.
+struct KeepBits {
+  Drop drop;
+  uint8_t* bits;
+  int64_t n64;
+};
+
 // n weights -> bf16 or fp32 out; the slice sum ss (independent of the
 // weight) runs in spare workgroups of the same launch.
 // codebook and absmax (nullable: double quantized scales) as the state has
@@ -80,12 +87,9 @@ struct BwdAux {
   int r;
   float s;
   bool three_parts;
-  Drop drop;       // keep bits of `bits64` times 64 elements (dropout from a counter)
-  uint8_t* bits;
-  int64_t bits64;
 };
 constexpr int kAuxRanks = 4;
-// The jobs but the keep bits' and Bf's are rows in blocks of kAuxRanks ranks (16 ceil(r / 16) in all),
+// The jobs but Bf's are rows in blocks of kAuxRanks ranks (16 ceil(r / 16) in all),
 // one per thread: a row n of B (Bt[j][n] = B[n][j]), a column k of A (At[k][j] =
 // A[j][k]), a column m of su and of sv.  A thread reads its ranks of B, u or v's
 // slices in one load when r allows, the threads of a wave read neighbouring
@@ -97,7 +101,7 @@ __host__ __device__ inline int64_t bwd_frags(const BwdAux& a) {  // 16-byte piec
   return a.Bf ? (a.N + 31) / 32 * 64 * ((a.r + 15) / 16) : 0;
 }
 __host__ __device__ inline int64_t bwd_aux_count(const BwdAux& a) {
-  return (a.bits ? a.bits64 : 0) + bwd_frags(a) +
+  return bwd_frags(a) +
          ((a.Bt ? a.N : 0) + (a.At ? a.K : 0) + (a.su ? a.Mpu : 0) + (a.sv ? a.Mpv : 0)) *
          ((a.r + 15) / 16 * (16 / kAuxRanks));
 }
@@ -111,24 +115,12 @@ __device__ inline void put_split(uint16_t* dst, int64_t half, int64_t idx, float
   dst[half + idx] = (uint16_t)l;
   if (three) dst[2 * half + idx] = (uint16_t)(pack_bf16x2(rest - bf16_lo(l), 0.f) & 0xffffu);
 }
-// job i of the concatenated jobs (keep bits; Bf; then by rows Bt, At, su, sv in that
+// job i of the concatenated jobs (Bf; then by rows Bt, At, su, sv in that
 // order, a block of ranks of all of them before the next block)
 __device__ inline void bwd_aux_at(const BwdAux& a, int64_t i) {
   const int r = a.r;
   const int64_t rp = 16 * ((r + 15) / 16);
-  const int64_t frags = bwd_frags(a), bits = a.bits ? a.bits64 : 0;
-  if (i < bits) {
-    const uint64_t offset = drop_offset(a.drop);
-    uint32_t w[2] = {0u, 0u};
-#pragma unroll 2
-    for (int q = 0; q < 8; ++q) {
-      const uint32_t b = keep_byte(philox(a.drop, offset, (uint64_t)(8 * i + q)), a.drop.less);
-      if (q < 4) w[0] |= b << (8 * q); else w[1] |= b << (8 * (q - 4));
-    }
-    reinterpret_cast<u32x2*>(a.bits)[i] = u32x2{w[0], w[1]};
-    return;
-  }
-  i -= bits;
+  const int64_t frags = bwd_frags(a);
   if (i < frags) {  // rows n .. n + 7 of rank j
     const int64_t n = i / (4 * rp) * 32 + (i >> 4) % 4 * 8, j = (i >> 6) % (rp / 16) * 16 + i % 16;
     uint32_t w[4] = {0u, 0u, 0u, 0u};
@@ -139,7 +131,7 @@ __device__ inline void bwd_aux_at(const BwdAux& a, int64_t i) {
     return;
   }
   i -= frags;
-  const int64_t rows = (bwd_aux_count(a) - bits - frags) / (rp / kAuxRanks);
+  const int64_t rows = (bwd_aux_count(a) - frags) / (rp / kAuxRanks);
   const int jb = (int)(i / rows) * kAuxRanks;  // this block's ranks: jb .. je - 1
   i %= rows;
   const int je = min(jb + kAuxRanks, r);
@@ -306,10 +298,10 @@ hipError_t launch_adamw8(float* p, const float* g, int64_t n, uint8_t* mq, float
 int thin_nt_slices(int64_t M, int64_t P);
 // v [M, r] = G [M, N] B [N, r] in fp32 (Bf as BwdAux makes it), and sv = (s v)^T in three parts as
 // BwdAux makes it with three_parts; N % 8 == 0, Mp % 4 == 0.  clr: words the first
-// workgroup zeroes.
+// workgroup zeroes.  kb: keep bits that ride along.
 hipError_t launch_thin_v(const uint16_t* G, const uint16_t* Bf, int64_t M, int64_t N, int r,
                          float* v, uint16_t* sv, int64_t Mp, float s, hipStream_t st,
-                         Clear clr);
+                         Clear clr, const KeepBits& kb);
 bool thin_nt_rows_ok(int64_t M, int64_t P, int r);
 
 // p[0..n) = 0 (a kernel, so it may sit in a captured graph).
