@@ -10,7 +10,10 @@ typedef u32x4 u32x4_any __attribute__((aligned(1)));
 constexpr int kThreads = 256;
 constexpr int kU = 2;  // blocks of eight elements a thread takes, their loads together
 
-// out = kept ? x scale : 0 over n elements, eight a thread and turn.  out may be x.
+// out = kept ? x scale : 0 over n elements, eight a thread and turn.  out may be x.  Ten
+// rounds of Philox 4x32, two 32 x 32 -> 64 bit products each, make the bits of eight
+// elements; two such blocks a thread keep loads in flight beside them, and HBM is the bound:
+// 8192x4096 bf16 22.2 us (134 MB, 6.05 TB/s); 1003x1001 fp32 3.6, latency.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_dropout(const T* x, int64_t n, Drop d, float scale,
                                                       T* out) {

@@ -97,9 +97,15 @@ __device__ __forceinline__ void unrolled(F&& f) {
   }
 }
 
-// A workgroup takes 32 rows x 256 columns, a step of the scales' layout: pass p,
+// ---- Into the format: E = floor(log2 max |x|) - 2 + 127 per block of 32 columns, codes
+// the nearest levels of x 2^(127 - E) (hardware conversion, ties to the even code, 6 at
+// most).  A workgroup takes 32 rows x 256 columns, a step of the scales' layout: pass p,
 // thread t -> row 8 p + t / 32, columns 8 (t % 32) .. + 7; four lanes to a block.  The
-// 256 scale bytes leave together.
+// 256 scale bytes leave together.  Bound by HBM: 4096x14336 fp32 49.4 us (271 MB, 5.5
+// TB/s), 8192x4096 bf16 18.4 (85 MB, 4.6 TB/s); small matrices by one pass's latency (77x1000
+// 3.8 us).  fp32 matrices (weights, read once) come by streaming loads, with ordinary ones
+// 62.6 us; bf16 ones, activations that the kernel before may have left in the caches, by
+// ordinary loads, and streaming ones take as long (18.4).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_mx4_quant(const T* __restrict__ x, int64_t rows,
                                                         int64_t K, int J,
@@ -138,6 +144,8 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quant(const T* __restrict__ x,
         reinterpret_cast<const uint32_t*>(sc)[t];
 }
 
+// ---- And back, one rounding to T at most (fp32: none), the same tile.  Bound by HBM's
+// writes: 4096x14336 fp32 44.0 us (266 MB, 6.05 TB/s), 77x1000 bf16 2.9.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_mx4_dequant(const uint8_t* __restrict__ codes,
                                                           const uint8_t* __restrict__ scales,
@@ -173,7 +181,12 @@ __global__ __launch_bounds__(kThreads) void k_mx4_dequant(const uint8_t* __restr
 // between those lanes, so that each stores one block's 16 bytes.  With one slice the
 // waves' sums of u meet in LDS, and the workgroup writes u and (s u) as the
 // product's epilogue takes it; else the slices' sums are written, for the product's
-// workgroups to add.
+// workgroups to add.  With DROP each lane draws its eight elements' keep bits
+// (one counter) and masks the operand of u alone.  u's products are in the same pass, since x
+// is the larger part of the bytes: 8192x4096 at r = 16 20.3 us (85 MB, 4.2 TB/s), with
+// dropout 24.0-25.0: the Philox rounds (20 wide multiplies for eight elements) fill the
+// vector units beside the loads; at r = 64 37 us, A's four tiles of ranks from the L2 in
+// every workgroup.  Few rows: eight slices, 16x14336 7.4 us, 1x4096 4.6, latency.
 __device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
                                                                 __builtin_bit_cast(u16x2, b)));
@@ -367,6 +380,14 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx4_x(
 // c ^ ((y >> 1) & 7), so that 16 rows of a fragment read sit on distinct banks.  In
 // half t of a step lane (g, n) = (l / 16, l % 16) takes row n's block 4 t + g, whose scale
 // is byte 2 (tile % 2) + t of the lane's four.
+// 8192x4096x4096 at r = 16 69.0 us, 3.98 PFLOP/s (256 x 256 tiles, 109 MB read, 67 written):
+// power holds it.  4096x4096x16384 takes 113 us at 1.88 GHz on random operands and 87 at
+// 2.43 GHz on zeros, by the same instructions, of which MFMAs are 62% of the cycles (a wave
+// alone on its SIMD issues one in 24.4 cycles, 5.7 PFLOP/s by 256 units, two waves 7.3).
+// 32x32x64 tiles take 75 us; four stages for many tiles, loads or barriers elsewhere in the
+// step and wave priorities change nothing or lose.  301x50021x1000 22.5 us: four
+// steps a tile, so the first stage and the output (30 MB in rows at odd addresses) are most of it; 64 x 128
+// tiles 24.6 and 64 x 64 27.2 (two stages deep), eight waves 23.1.
 template <int WVM, int WVN, int TM, int TN, int STAGES>
 struct MxGeo {
   static constexpr int NST = STAGES;
@@ -666,7 +687,10 @@ __global__ __launch_bounds__(64 * WVM * WVN, 2) void k_mx4_gemm(
 // ---- The product of few rows: W is read once, straight into registers.  A workgroup
 // takes 16 NT rows of W and all of x's 16 MT, its waves the steps in turn; their sums meet
 // in LDS.  u comes whole or in S slices, which every workgroup adds (u_out: the first
-// one writes the sum); its loads and those of B go out ahead of W's.
+// one writes the sum); its loads and those of B go out ahead of W's.  Bound by W from
+// memory and by the latency of one pass: 1x14336x4096 8.9 us (31.8 MB, 3.6 TB/s),
+// 16x4096x14336 10.6 (34.4 MB).  Four steps' loads at once instead of two: slower; 16 slices
+// of u instead of 8: x's pass wins what this one loses.
 constexpr int kFewSlices = 8;
 // ranks j .. j + 15 of a row of B (zero past r)
 __device__ __forceinline__ void load_ranks(const uint16_t* row, int j, int r, float v[16]) {
@@ -867,7 +891,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx4_token(
   }
 }
 
-// out[k][n] = W[n][k] as bf16, row length ldt (zero for rows <= n < ldt).  A workgroup
+// ---- The backward's W: out[k][n] = W[n][k] as bf16 (exact: a level has two significant bits),
+// row length ldt (zero for rows <= n < ldt).  dX is a bf16 product on it: dY is not rounded
+// to 4 bits.  4096x4096 with A^T, B's operands and u's parts in spare workgroups 11.4 us
+// (44.5 MB, 3.9 TB/s; the write goes to the memory-side cache, where the product
+// reads it).  A workgroup
 // takes 128 rows x 128 columns through LDS: thread (q, l) = (t / 64, t % 64) the block q
 // of rows 2 l and 2 l + 1, whose columns leave as pairs of rows, a word each.
 constexpr int kDtRows = 128, kDtPitch = 2 * kDtRows + 16;
