@@ -479,7 +479,7 @@ typedef struct {
 
 /* out [n] = kept ? x * 2^16 / (2^16 - t) : 0 in x's type (QN_BF16 or QN_F32; a dropped NaN
  * is 0); out may be x.  Its gradient is the same call on the gradient.  Element
- * aligned; 0 <= n <= 2^40. */
+ * aligned; 0 <= n <= 2^35. */
 qn_status dropout_apply(const void* x, qn_dtype dtype, int64_t n, const qn_dropout* drop,
                         void* out, void* stream);
 
@@ -524,8 +524,8 @@ typedef struct {
   int64_t rows, cols;
 } qn_mx4;
 
-/* x [rows, cols] fp32 or bf16 -> codes, scales.  0 <= rows <= 2^23, 1 <= cols <= 2^20;
- * rows of a width that is no multiple of 8 may start on any element. */
+/* x [rows, cols] fp32 or bf16 -> codes, scales.  0 <= rows <= 2^23, 1 <= cols <= 2^20,
+ * at most 3 2^35 elements (rows counted up to a multiple of 32, columns of 256); rows of a width that is no multiple of 8 may start on any element. */
 qn_status mx4_quantize(const void* x, qn_dtype dtype, int64_t rows, int64_t cols, uint8_t* codes,
                        uint8_t* scales, void* stream);
 

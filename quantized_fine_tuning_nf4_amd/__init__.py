@@ -598,8 +598,11 @@ class QLoRALinear(torch.nn.Module):
     that share an input share it).  base: "nf4", or "mx4" for MXFP4 weights,
     whose product takes x in MXFP4 too (mx4_linear_fwd).  seed: the dropout's
     mask is drawn by the kernels from a counter and not kept, each forward's from
-    an offset of its own (Dropout; give every layer its seed); step: its device
-    tensor, for captured graphs, where the offset of the capture stays."""
+    an offset of its own (Dropout; give every layer, and every rank, its seed); step:
+    its device tensor, for captured graphs, where the offset of the capture stays.
+    A forward that is run again for the backward (activation checkpointing) would
+    draw another mask: give such a layer no seed, or call the linear with a Dropout of
+    your own."""
 
     def __init__(self, weight: torch.Tensor, r: int = 16, alpha: float = 32.0,
                  dropout: float = 0.0, rslora: bool = False, act8: bool = False,

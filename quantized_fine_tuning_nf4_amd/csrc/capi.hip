@@ -420,7 +420,7 @@ qn_status backward(const Base& base, const uint16_t* x, const qn_act8* x8, const
   BwdWs b = carve_bwd(c, M, N, K, r, u_saved == nullptr, three, dX != nullptr, lo.drop.on);
   const float scale = lo.s;
   hipError_t e = hipSuccess;
-  if (lo.drop.on) lo.mask = b.bits;  // (drawn with the small jobs below)
+  if (lo.drop.on) lo.mask = b.bits;  // (drawn beside v below)
   const float* u = u_saved;
   // an early launch of the call zeroes the arrival counters the adapter
   // gradients' launch counts on, so the backward never depends on what the
@@ -560,7 +560,12 @@ uint16_t* carve_mx4_dx(Carver& c, int64_t rows, int64_t cols) {
   c.take<unsigned>(kArrivalWords);
   return c.take<uint16_t>((size_t)cols * round_up(rows, 64));
 }
-constexpr int64_t kMaxElements = (int64_t)1 << 40;
+// Elements of dropout_apply and of a matrix into and out of MXFP4 (rows rounded up to 32,
+// columns to 256): a launch holds fewer than 2^32 threads, 16 and 32 elements each.
+constexpr int64_t kMaxElements = (int64_t)1 << 35;
+bool mx4_too_large(int64_t rows, int64_t cols) {
+  return round_up(rows, 32) * round_up(cols, 256) > kMaxElements * 3;
+}
 
 // Scratch of qlora_linear_fwd_noalloc: a file-scope device array, one copy
 // per GPU, held until the process ends.  Host code never passes its name to
@@ -1059,7 +1064,8 @@ qn_status qlora_linear_bwd_drop(const qn_nf4dq* w, const uint16_t* x, const qn_a
 qn_status mx4_quantize(const void* x, qn_dtype dtype, int64_t rows, int64_t cols, uint8_t* codes,
                        uint8_t* scales, void* stream) {
   if (dtype != QN_F32 && dtype != QN_BF16) return QN_EINVAL;
-  if (rows < 0 || rows > kMaxRowsM || cols < 1 || cols > kMaxDim) return QN_EINVAL;
+  if (rows < 0 || rows > kMaxRowsM || cols < 1 || cols > kMaxDim || mx4_too_large(rows, cols))
+    return QN_EINVAL;
   if (rows == 0) return QN_OK;
   if (!x || !codes || !scales) return QN_EINVAL;
   if (!aligned_rows(x, cols, dtype == QN_F32 ? 4 : 2) || !aligned16(codes) || !aligned16(scales))
@@ -1070,7 +1076,8 @@ qn_status mx4_quantize(const void* x, qn_dtype dtype, int64_t rows, int64_t cols
 
 qn_status mx4_dequantize(const qn_mx4* w, qn_dtype out_dtype, void* out, void* stream) {
   if (out_dtype != QN_F32 && out_dtype != QN_BF16) return QN_EINVAL;
-  if (!w || w->rows < 0 || w->rows > kMaxRowsM || w->cols < 1 || w->cols > kMaxDim)
+  if (!w || w->rows < 0 || w->rows > kMaxRowsM || w->cols < 1 || w->cols > kMaxDim ||
+      mx4_too_large(w->rows, w->cols))
     return QN_EINVAL;
   if (w->rows == 0) return QN_OK;
   if (!w->codes || !w->scales || !out) return QN_EINVAL;

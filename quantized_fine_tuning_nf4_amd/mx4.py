@@ -354,6 +354,9 @@ def mx4_linear_bwd(w: MX4, x, dY: torch.Tensor, A: torch.Tensor | None = None,
 
 # ------------------------------------------------- the NF4 linear under a Dropout
 def _qlora_fwd_drop(st: NF4State, x, A, B, r, alpha, rslora, drop, y, u, workspace):
+    if not _here(x, A, B, y, st.packed):
+        with torch.cuda.device(x.device):
+            return _qlora_fwd_drop(st, x, A, B, r, alpha, rslora, drop, y, u, workspace)
     L = load_library()
     M = x.shape[0]
     need = _need_drop(M, st.rows, st.cols, r, 0, 0)
@@ -369,6 +372,10 @@ def _qlora_fwd_drop(st: NF4State, x, A, B, r, alpha, rslora, drop, y, u, workspa
 
 def _qlora_bwd_drop(st: NF4State, x, x8, dY, A, B, r, alpha, rslora, drop, u, dX, dA, dB,
                     workspace):
+    if not _here(dY, x, A, B, u, st.packed):
+        with torch.cuda.device(dY.device):
+            return _qlora_bwd_drop(st, x, x8, dY, A, B, r, alpha, rslora, drop, u, dX, dA, dB,
+                                   workspace)
     L = load_library()
     M = dY.shape[0]
     need = _need_drop(M, st.rows, st.cols, r, 1, int(x8 is not None))

@@ -73,6 +73,14 @@ def test_quantize_refusals(qn):
     assert d(_mx(0, 64), 0, None, None) == qn.QN_OK
 
 
+def test_sizes_past_a_launch(qn):
+    """More elements than one launch has threads for are refused, not cut off."""
+    L = qn.load_library()
+    assert L.dropout_apply(FAKE, 1, (1 << 35) + 1, _do(), FAKE, None) == qn.QN_EINVAL
+    assert L.mx4_quantize(FAKE, 1, 1 << 18, 1 << 19, FAKE, FAKE, None) == qn.QN_EINVAL
+    assert L.mx4_dequantize(_mx(1 << 18, 1 << 19), 1, FAKE, None) == qn.QN_EINVAL
+
+
 def test_linear_refusals(qn):
     L = qn.load_library()
 
