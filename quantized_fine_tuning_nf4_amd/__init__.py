@@ -599,7 +599,9 @@ class QLoRALinear(torch.nn.Module):
     whose product takes x in MXFP4 too (mx4_linear_fwd).  seed: the dropout's
     mask is drawn by the kernels from a counter and not kept, each forward's from
     an offset of its own (Dropout; give every layer, and every rank, its seed); step:
-    its device tensor, for captured graphs, where the offset of the capture stays.
+    its device tensor, for captured graphs, where the offset of the capture stays
+    (before a backward is captured, let go of every eager output of the layer: torch ends
+    the process where an eager graph of the same parameters lives).
     A forward that is run again for the backward (activation checkpointing) would
     draw another mask: give such a layer no seed, or call the linear with a Dropout of
     your own."""
