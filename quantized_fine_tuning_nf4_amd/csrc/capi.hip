@@ -545,10 +545,10 @@ Mx4X carve_mx4(Carver& c, int64_t M, int64_t rows, int64_t cols, int r, float* u
   f.r = r;
   f.codes = c.take<uint8_t>((size_t)mx4_code_bytes(M, cols));
   f.scales = c.take<uint8_t>((size_t)mx4_scale_bytes(M, cols));
-  f.S = r > 0 ? mx4_x_slices(M, cols) : 1;
+  f.S = r > 0 ? mx4_x_slices(M, cols, r) : 1;
   f.u = need_u && r > 0 ? c.take<float>((size_t)M * r) : u;
   f.upart = f.S > 1 ? c.take<float>((size_t)f.S * M * r) : nullptr;
-  if (r > 0 && !mx4_few_rows(M)) {
+  if (r > 0 && !mx4_few_rows(M, r)) {
     const size_t nj = (r + 15) / 16;
     f.su = c.take<uint16_t>((size_t)round_up(M, 32) * nj * 32);
     f.bo = c.take<uint16_t>((size_t)round_up(rows, 16) * nj * 16);

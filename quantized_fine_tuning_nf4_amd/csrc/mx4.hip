@@ -181,7 +181,7 @@ __global__ __launch_bounds__(kThreads) void k_mx4_dequant(const uint8_t* __restr
 // between those lanes, so that each stores one block's 16 bytes.  With one slice the
 // waves' sums of u meet in LDS, and the workgroup writes u and (s u) as the
 // product's epilogue takes it; else the slices' sums are written, for the product's
-// workgroups to add.  With DROP each lane draws its eight elements' keep bits
+// workgroups to add (few rows) or for k_mx4_u.  With DROP each lane draws its eight elements' keep bits
 // (one counter) and masks the operand of u alone.  u's products are in the same pass, since x
 // is the larger part of the bytes: 8192x4096 at r = 16 20.3 us (85 MB, 4.2 TB/s), with
 // dropout 24.0-25.0: the Philox rounds (20 wide multiplies for eight elements) fill the
@@ -371,6 +371,51 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx4_x(
     }
     reinterpret_cast<u32x4*>(su)[((rt * RT + i) * NJ + q) * 64 + l] = u32x4{w[0], w[1], w[2], w[3]};
   }
+}
+
+// u = the sum of its S slices in slice order, and (s u) as above: a thread takes eight
+// ranks of a row (zero past M and r).
+constexpr int kThreadsU = 64;  // (few threads in all: over many compute units)
+__global__ __launch_bounds__(kThreadsU) void k_mx4_u(const float* __restrict__ upart, int S,
+                                                     int64_t M, int r, int nj, float s,
+                                                     float* __restrict__ u,
+                                                     uint16_t* __restrict__ su, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * kThreadsU + threadIdx.x;
+  if (i >= n) return;
+  const int l = (int)(i & 31);
+  const int64_t t = i >> 5, row = t / nj * 16 + (l & 15);
+  const int j = (int)(t % nj) * 16 + 8 * (l >> 4), left = row < M ? min(r - j, 8) : 0;
+  float v[8] = {};
+  const float* p = upart + row * r + j;
+  if (left == 8) {
+#pragma unroll 4
+    for (int z = 0; z < S; ++z) {
+      const u32x4 a = *reinterpret_cast<const u32x4_any*>(p + z * M * r);
+      const u32x4 b = *reinterpret_cast<const u32x4_any*>(p + z * M * r + 4);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[q] += as_f32(a[q]);
+        v[4 + q] += as_f32(b[q]);
+      }
+    }
+  } else {
+    for (int z = 0; z < S; ++z)
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < left) v[q] += p[z * M * r + q];
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    if (q < left) u[row * r + j + q] = v[q];
+  uint32_t hi[4], lo[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float a = s * v[2 * q], b = s * v[2 * q + 1];
+    hi[q] = pack_bf16x2(a, b);
+    lo[q] = pack_bf16x2(a - bf16_lo(hi[q]), b - bf16_hi(hi[q]));
+  }
+  reinterpret_cast<u32x4*>(su)[t * 64 + l] = u32x4{hi[0], hi[1], hi[2], hi[3]};
+  reinterpret_cast<u32x4*>(su)[t * 64 + 32 + l] = u32x4{lo[0], lo[1], lo[2], lo[3]};
 }
 
 // ---- The product of many rows.  Workgroup tile BM x BN (rows of x, rows of W), WVM x WVN
@@ -1057,9 +1102,16 @@ int64_t compute_units() {
 }
 }  // namespace
 
-int mx4_x_slices(int64_t M, int64_t K) {
-  if (!mx4_few_rows(M)) return 1;
-  return (int)std::min<int64_t>(mx4_steps(K), kFewSlices);
+int mx4_x_slices(int64_t M, int64_t K, int r) {
+  const int64_t J = mx4_steps(K), most = std::min<int64_t>(J, kFewSlices);
+  if (mx4_few_rows(M, r)) return (int)most;
+  // More rows in slices where one workgroup's walk takes longer than the launch that adds
+  // them (pass, sum and product at 4096 columns 14.4 us instead of 17.8 for 128 rows and 16
+  // ranks, at 14336 25.2 instead of 45.2, with 64 ranks 34.0 instead of 83.7; at 2048 with 16
+  // ranks 12.3 and 12.8, with 64 17.0 and 20.4, at 1024 11.2 and 10.3), as many as leave a
+  // workgroup to a compute unit
+  if (J * ((r + 15) / 16 + 2) < 48) return 1;
+  return (int)std::max<int64_t>(1, std::min(most, 256 / ((M + 15) / 16)));
 }
 
 hipError_t launch_mx4_x(const uint16_t* x, int64_t K, const Mx4X& o, const Drop& d,
@@ -1070,7 +1122,18 @@ hipError_t launch_mx4_x(const uint16_t* x, int64_t K, const Mx4X& o, const Drop&
   if (o.M > 4096)
     return o.r <= 16 && mx4_steps(K) >= 16 ? launch_x<2, 1, 16>(x, K, o, d, A, B, N, s, st)
                                            : launch_x<2, 8>(x, K, o, d, A, B, N, s, st);
-  if (mx4_few_rows(o.M)) return launch_x<1, 8>(x, K, o, d, A, B, N, s, st);
+  if (mx4_few_rows(o.M, o.r)) return launch_x<1, 8>(x, K, o, d, A, B, N, s, st);
+  if (o.S > 1) {
+    Mx4X part = o;
+    part.su = nullptr;
+    const hipError_t e = launch_x<1, 8>(x, K, part, d, A, B, N, s, st);
+    const int nj = (o.r + 15) / 16;
+    const int64_t n = (o.M + 15) / 16 * nj * 32;
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_mx4_u, dim3((unsigned)((n + kThreadsU - 1) / kThreadsU)), dim3(kThreadsU),
+                       0, st, o.upart, o.S, o.M, o.r, nj, s, o.u, o.su, n);
+    return hipGetLastError();
+  }
   return launch_x<1, 16>(x, K, o, d, A, B, N, s, st);
 }
 
@@ -1093,13 +1156,12 @@ hipError_t launch_mx4_token(const Mx4& w, const uint16_t* x, int64_t M, uint16_t
 
 hipError_t launch_mx4_mm(const Mx4& w, const Mx4X& x, const uint16_t* B, float s, uint16_t* y,
                          hipStream_t st) {
-  if (mx4_few_rows(x.M)) {
+  if (mx4_few_rows(x.M, x.r)) {
     const bool wide = w.rows >= 16 * 512;
     if (x.M <= 16)
       return wide ? launch_rows<1, 2, 8>(w, x, B, s, y, st)
                   : launch_rows<1, 1, 16>(w, x, B, s, y, st);
-    if (x.M <= 32) return launch_rows<2, 2, 8>(w, x, B, s, y, st);
-    return launch_rows<4, 2, 8>(w, x, B, s, y, st);
+    return launch_rows<2, 2, 8>(w, x, B, s, y, st);
   }
   const int64_t cu = compute_units();
   const auto tiles = [&](int64_t tm, int64_t tn) {

@@ -453,14 +453,17 @@ struct Mx4X {
   uint8_t* codes;   // x [M, cols] in MXFP4
   uint8_t* scales;
   float* u;         // [M, r]
-  float* upart;     // [S, M, r] its slices when S > 1: launch_mx4_mm adds them into u
-  int S;            // mx4_x_slices(M, cols)
+  float* upart;     // [S, M, r] its slices when S > 1: added into u by launch_mx4_mm (few
+                    // rows) or launch_mx4_x
+  int S;            // mx4_x_slices(M, cols, r)
   uint16_t* su;     // many rows: (s u) and B in the order of the product's lanes,
   uint16_t* bo;     // 512 and 256 values for 16 rows and 16 ranks
 };
-// Batches whose product reads W straight into registers.
-inline bool mx4_few_rows(int64_t M) { return M <= 64; }
-int mx4_x_slices(int64_t M, int64_t K);
+// Batches whose product reads W straight into registers: against tiles (with x's pass) M =
+// 24, 4096x4096, r = 16 13.1 and 14.4 us, with 64 ranks 21 and 18.5, 14336x4096 without an
+// adapter 14.0 and 11.3.
+inline bool mx4_few_rows(int64_t M, int r) { return M <= (r >= 1 && r <= 16 ? 32 : 16); }
+int mx4_x_slices(int64_t M, int64_t K, int r);
 // A token or a few without an adapter: y from x itself (16-byte aligned) in one launch.
 inline bool mx4_one_launch(int64_t M, int64_t K, int r) {
   return M <= 8 && r == 0 && K % kMx4Block == 0;

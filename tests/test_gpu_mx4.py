@@ -195,6 +195,15 @@ def test_forward(qn, M, rows, cols, r, p):
         assert no_u is None and torch.equal(none, y)
 
 
+# u in slices ahead of a product by tiles, ragged rows and ranks, two slices to eight
+@pytest.mark.parametrize("M,rows,cols,r", [(33, 72, 4160, 5), (40, 264, 8192, 64), (300, 136, 4096, 16),
+                                           (530, 72, 2112, 51), (1001, 64, 4096, 23),
+                                           (2040, 64, 4352, 1)])
+@pytest.mark.parametrize("p", [0.0, 0.1])
+def test_forward_in_slices(qn, M, rows, cols, r, p):
+    test_forward(qn, M, rows, cols, r, p)
+
+
 @pytest.mark.parametrize("M", [1, 16, 40, 70, 6145])
 @pytest.mark.parametrize("r", [0, 3, 40])
 def test_input_is_rounded_as_a_stored_matrix_is(qn, M, r):
