@@ -26,9 +26,8 @@
 // c ^ ((y >> 1) & 7), which keeps the sixteen rows of one fragment read on
 // distinct banks.  The next half's B fragments are read during the first
 // row of a half's MFMAs (its first row uses all eight), its A fragments one
-// per row.  Rows of A past its length R are moved back onto its last
-// chunk; Bm is zero there (its rows are padded to a multiple of 64 with
-// zeros).
+// per row.  Rows of A past their length R read as zero, as Bm's rows do
+// (padded to a multiple of 64 with zeros).
 #include <type_traits>
 
 #include "qn_device.h"
@@ -94,6 +93,8 @@ __device__ __forceinline__ rsrc_t make_rs(const void* base, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(lo | (hi << 32)), 0,
                                            __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
 }
+// past every buffer made here (256 rows of 2^20 bf16): such a load gives zero
+constexpr uint32_t kPastBuffer = 0x7ffffff0u;
 // lane l's 16 bytes at base + voff + soff land at lds + 16 l
 __device__ __forceinline__ void dma16(rsrc_t rs, uint32_t voff, uint32_t soff, uint8_t* lds) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)lds, 16, voff, soff, 0, 0);
@@ -107,7 +108,7 @@ __device__ __forceinline__ void wait_all_loads() { asm volatile("s_waitcnt vmcnt
 // LORA16: r == 16, the LoRA operands prefetched into LDS; otherwise read in
 // the tail from global memory (one tail per instance keeps the registers of
 // the other out of the kernel).  ATAIL: the reduction length R is shorter
-// than the steps cover (R < ldb), so A's chunks past R are moved back; with
+// than the steps cover (R < ldb), so A's chunks past R are taken as zero; with
 // R == ldb the A loads need no address arithmetic per step (the 64-bit
 // clamp in the loop cost 12% of the main loop's cycles at 8192x4096x4096).
 // MASK: the LoRA term counts only where the keep mask (bit-packed over the
@@ -172,18 +173,18 @@ __global__ __launch_bounds__(T, 1) void k_gemm_nt(
     const int chunk = (lane & 7) ^ (int)((row >> 1) & 7);
     boff[i] = (uint32_t)((min(row, ncols - 1) * ldb + 8 * chunk) * 2);
   }
-  // A's reduction tail: a chunk past R is moved back onto the row's last
-  // chunk (its Bm partner is zero)
-  auto a_back = [&](int st, int i) {
-    if constexpr (!ATAIL) return 0u;
-    const int64_t k = (int64_t)st * BK + 8 * achunk[i];
-    return (uint32_t)(2 * (k - min(k, R - 8)));
+  // A's reduction tail: a chunk past R lies past the buffer, which reads as
+  // zero, as its Bm partner is (the row's own values there would make an
+  // infinity of the row a NaN)
+  auto a_off = [&](int st, int i) {
+    if constexpr (!ATAIL) return aoff[i];
+    return (int64_t)st * BK + 8 * achunk[i] >= R ? kPastBuffer : aoff[i];
   };
   // load q (0 .. LPS - 1) of step st: q < WTM A rows, else Bm rows
   auto load_one = [&](int q, int st, int stage) {
     const uint32_t so = (uint32_t)st * (BK * 2);
     if (q < WTM) {
-      dma16(rsA, aoff[q] - a_back(st, q), so,
+      dma16(rsA, a_off(st, q), so,
             smem + stage * STB + wave * (1024 * WTM) + 1024 * q);
     } else {
       dma16(rsB, boff[q - WTM], so,

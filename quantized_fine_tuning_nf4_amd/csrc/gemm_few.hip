@@ -165,6 +165,8 @@ __device__ __forceinline__ rsrc_t make_rs(const void* base, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(lo | (hi << 32)), 0,
                                            __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
 }
+// past every buffer made here (128 rows of 2^20 bf16): such a load gives zero
+constexpr uint32_t kPastBuffer = 0x7ffffff0u;
 __device__ __forceinline__ void dma16(rsrc_t rs, uint32_t voff, uint32_t soff, uint8_t* lds) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)lds, 16, voff, soff, 0, 0);
 }
@@ -213,14 +215,14 @@ __global__ __launch_bounds__(64 * WVM * WVN) void k_gemm_tiles(
   // load i of wave w: rows 8 (AL w + i) + l / 8 (past the matrix: its last row)
   const rsrc_t ra = make_rs(A + m0 * lda, (uint32_t)(mrows * lda * 2));
   const rsrc_t rb = make_rs(Bm + c0 * ldb, (uint32_t)(ncols * ldb * 2));
-  uint32_t aoff[AL], back[AL], boff[BL];
+  uint32_t aoff[AL], alast[AL], boff[BL];
 #pragma unroll
   for (int i = 0; i < AL; ++i) {
     const int row = 8 * (AL * wave + i) + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
     aoff[i] = (uint32_t)((min(row, mrows - 1) * lda + 8 * chunk) * 2);
-    // a chunk of the last step past R: the row's last one (its partner in Bm is zero)
-    const int64_t k = (int64_t)(steps - 1) * 64 + 8 * chunk;
-    back[i] = k >= R ? (uint32_t)(2 * (k - (R - 8))) : 0u;
+    // a chunk of the last step past R: past the buffer, which reads as zero, as its
+    // partner in Bm is (the row's own values there would make an infinity of the row a NaN)
+    alast[i] = (int64_t)(steps - 1) * 64 + 8 * chunk >= R ? kPastBuffer : aoff[i];
   }
 #pragma unroll
   for (int i = 0; i < BL; ++i) {
@@ -229,9 +231,9 @@ __global__ __launch_bounds__(64 * WVM * WVN) void k_gemm_tiles(
   }
   auto load_one = [&](int q, int st, int stage) {
     uint8_t* base = smem + stage * G::STB;
-    const uint32_t so = (uint32_t)st * 128, last = st == steps - 1 ? ~0u : 0u;
+    const uint32_t so = (uint32_t)st * 128;
     if (q < AL)
-      dma16(ra, aoff[q] - (back[q] & last), so, base + 1024 * (AL * wave + q));
+      dma16(ra, st == steps - 1 ? alast[q] : aoff[q], so, base + 1024 * (AL * wave + q));
     else
       dma16(rb, boff[q - AL], so, base + G::AB + 1024 * (BL * wave + q - AL));
   };
