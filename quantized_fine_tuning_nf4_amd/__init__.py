@@ -596,15 +596,16 @@ class QLoRALinear(torch.nn.Module):
     of x is kept as an 8-bit checkpoint instead of x itself; forward's x8
     passes one that is at hand already (BlockNorm makes it, and the linears
     that share an input share it).  base: "nf4", or "mx4" for MXFP4 weights,
-    whose product takes x in MXFP4 too (mx4_linear_fwd).  seed: the dropout's
+    whose product takes x in MXFP4 too (mx4_linear_fwd).  Without a seed the
+    dropout's mask is drawn from torch's generators (on MXFP4 weights by the kernels
+    from a counter, its key from the host's generator), so that a forward that is run
+    again for the backward (torch.utils.checkpoint) has the same one.  seed: the
     mask is drawn by the kernels from a counter and not kept, each forward's from
-    an offset of its own (Dropout; give every layer, and every rank, its seed); step:
+    an offset of its own (Dropout; give every layer, and every rank, its seed), and
+    a forward that is run again would draw another: it raises.  step:
     its device tensor, for captured graphs, where the offset of the capture stays
     (before a backward is captured, let go of every eager output of the layer: torch ends
-    the process where an eager graph of the same parameters lives).
-    A forward that is run again for the backward (activation checkpointing) would
-    draw another mask: give such a layer no seed, or call the linear with a Dropout of
-    your own."""
+    the process where an eager graph of the same parameters lives)."""
 
     def __init__(self, weight: torch.Tensor, r: int = 16, alpha: float = 32.0,
                  dropout: float = 0.0, rslora: bool = False, act8: bool = False,
@@ -613,10 +614,10 @@ class QLoRALinear(torch.nn.Module):
         self.act8 = bool(act8)
         if base not in ("nf4", "mx4"):
             raise ValueError('base must be "nf4" or "mx4"')
-        if base == "mx4" and dropout and seed is None:
-            raise ValueError('dropout with base="mx4" needs a seed')
         if step is not None and seed is None:
             raise ValueError("step belongs to a seed")
+        if seed is not None:
+            Dropout(0.0, seed, step=step)  # (what it refuses)
         self.seed, self.step, self.draws = seed, step, 0
         d_out, d_in = weight.shape
         W = weight.detach().float().contiguous()
@@ -628,6 +629,20 @@ class QLoRALinear(torch.nn.Module):
         self.lora_B = torch.nn.Parameter(torch.zeros(d_out, r, dtype=torch.bfloat16,
                                                      device=weight.device))
 
+    def _draw(self, p):
+        """The mask of a forward."""
+        if self.seed is None:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("a captured forward would have the same mask at every replay: "
+                                   "give the layer a seed and a step")
+            key = torch.empty((), dtype=torch.int64, device="cpu").random_()
+            return Dropout(p, int(key))
+        if torch._C._current_graph_task_id() != -1:
+            raise RuntimeError("a forward run again in a backward (activation checkpointing) "
+                               "would draw another mask: give the layer no seed")
+        self.draws += 1
+        return Dropout(p, self.seed, self.draws - 1, self.step)
+
     def forward(self, x, x8=None):
         if x8 is not None and not self.act8:
             raise ValueError("x8 is for a layer with act8=True")
@@ -635,10 +650,7 @@ class QLoRALinear(torch.nn.Module):
         x2 = x.reshape(-1, shp[-1]).contiguous()
         p = self.dropout if self.training else 0.0
         if isinstance(self.st, MX4) or (self.seed is not None and p > 0):
-            drop = None
-            if p > 0:
-                drop = Dropout(p, self.seed, self.draws, self.step)
-                self.draws += 1
+            drop = self._draw(p) if p > 0 else None
             y = _LinearFn.apply(x2, self.lora_A, self.lora_B, self.st, self.alpha, self.rslora,
                                 drop, self.act8, x8)
             return y.reshape(*shp[:-1], y.shape[-1])
