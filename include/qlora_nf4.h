@@ -470,7 +470,9 @@ qn_status token_logprobs_bwd(const void* logits, qn_dtype dtype, int64_t T, int6
  *   step (nullable, 8-byte aligned): a number in device memory that is added to
  *     it, read when the kernels run, so that a captured graph draws another mask at
  *     every replay once the caller has changed it.  A forward and its backward have
- *     to find the same number. */
+ *     to find the same number.  The two are one sum: offsets of uses in one graph
+ *     lie further apart than the number gets, or one use has another's mask of a
+ *     later replay. */
 typedef struct {
   uint64_t seed, offset;
   const uint64_t* step;

@@ -603,7 +603,8 @@ class QLoRALinear(torch.nn.Module):
     mask is drawn by the kernels from a counter and not kept, each forward's from
     an offset of its own (Dropout; give every layer, and every rank, its seed), and
     a forward that is run again would draw another: it raises.  step:
-    its device tensor, for captured graphs, where the offset of the capture stays
+    its device tensor, for captured graphs, where the offset of the capture stays:
+    count it up by one between replays (offsets are 2^32 apart then)
     (before a backward is captured, let go of every eager output of the layer: torch ends
     the process where an eager graph of the same parameters lives)."""
 
@@ -640,8 +641,12 @@ class QLoRALinear(torch.nn.Module):
         if torch._C._current_graph_task_id() != -1:
             raise RuntimeError("a forward run again in a backward (activation checkpointing) "
                                "would draw another mask: give the layer no seed")
+        offset = self.draws
         self.draws += 1
-        return Dropout(p, self.seed, self.draws - 1, self.step)
+        if self.step is not None:
+            # (what step counts is added: the uses in a graph stay apart for 2^32 of it)
+            offset = (offset << 32) & ((1 << 64) - 1)
+        return Dropout(p, self.seed, offset, self.step)
 
     def forward(self, x, x8=None):
         if x8 is not None and not self.act8:

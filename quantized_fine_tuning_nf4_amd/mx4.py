@@ -69,7 +69,8 @@ class Dropout:
     uses of one seed apart (layers, steps).  step: an int64 tensor of one element on
     the device that is added to offset when the kernels run, so that a captured
     graph draws another mask at each replay; it must not change between a forward
-    and its backward."""
+    and its backward.  Offset and step are one sum: uses in one graph whose offsets
+    lie nearer than step gets have each other's masks at other replays."""
     p: float
     seed: int
     offset: int = 0
