@@ -1,0 +1,116 @@
+"""A training step of the layers in a captured graph, replayed with other inputs and steps and
+with eager work between the replays; and the order that such a capture refuses."""
+import pytest
+import torch
+
+from tests._gpu import needs_gpu, say
+
+pytestmark = [pytest.mark.gpu, needs_gpu]
+
+
+def _layer(qn, base, act8, step):
+    torch.manual_seed(0)
+    lin = qn.QLoRALinear(torch.randn(72, 128, device="cuda") * 0.1, r=8, alpha=16.0,
+                         dropout=0.3 if step is not None else 0.0, act8=act8, base=base,
+                         seed=None if step is None else 11, step=step)
+    with torch.no_grad():
+        lin.lora_B.normal_(std=0.1)
+    return lin
+
+
+def _inputs(seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    draw = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    return draw(40, 128), draw(40, 72)
+
+
+def _functional(qn, lin, act8, x, g, drop):
+    from quantized_fine_tuning_nf4_amd.mx4 import linear_bwd, linear_fwd
+    y, u = linear_fwd(lin.st, x, lin.lora_A, lin.lora_B, 16.0, drop=drop)
+    keep = qn.act8_pack(x) if act8 else x
+    _, dA, dB = linear_bwd(lin.st, keep, g, lin.lora_A, lin.lora_B, 16.0, u, need_dx=False,
+                           drop=drop)
+    return y, dA.to(torch.bfloat16), dB.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("base", ["nf4", "mx4"])
+@pytest.mark.parametrize("act8", [False, True])
+@pytest.mark.parametrize("drops", [False, True])
+def test_captured_step(base, act8, drops):
+    import quantized_fine_tuning_nf4_amd as qn
+    say(f"[module graph] {base} act8={act8} drops={drops}")
+    step = torch.zeros(1, dtype=torch.int64, device="cuda") if drops else None
+    lin = _layer(qn, base, act8, step)
+    x, g = (t.clone() for t in _inputs(1))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        warm = lin(x)
+        warm.backward(g)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    del warm  # (with it the eager graph)
+    for p in lin.parameters():
+        p.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = lin(x)
+        y.backward(g)
+    for k in range(4):
+        nx, ng = _inputs(10 + k)
+        x.copy_(nx)
+        g.copy_(ng)
+        if drops:
+            step.fill_(3 * k)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        drop = qn.Dropout(0.3, 11, (1 << 32) + 3 * k) if drops else None
+        want = _functional(qn, lin, act8, nx, ng, drop)
+        torch.cuda.synchronize()
+        for got, w in zip((y, lin.lora_A.grad, lin.lora_B.grad), want):
+            assert torch.equal(got, w)
+
+
+@pytest.mark.parametrize("base", ["nf4", "mx4"])
+@pytest.mark.parametrize("act8", [False, True])
+def test_captured_beside_an_eager_graph(base, act8):
+    """The forward is captured as ever; its backward raises in Python."""
+    import quantized_fine_tuning_nf4_amd as qn
+    say(f"[module graph refused] {base} act8={act8}")
+    lin = _layer(qn, base, act8, None)
+    x, g = _inputs(1)
+    eager = lin(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = lin(x)
+        node = y.grad_fn
+        while node is not None and not hasattr(node, "older"):
+            node = node.next_functions[0][0]
+        assert node is not None and node.older  # (else the backward does not run)
+        with pytest.raises(RuntimeError, match="let go of every eager output"):
+            y.backward(g)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, eager) and lin.lora_A.grad is None
+    eager.backward(g)  # the eager graph is as good as before
+    assert lin.lora_B.grad is not None
+
+
+def test_norm_beside_an_eager_graph():
+    import quantized_fine_tuning_nf4_amd as qn
+    say("[norm graph refused]")
+    norm = qn.BlockNorm(128)
+    h = _inputs(2)[0]
+    eager = norm(h)[1]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = norm(h)[1]
+        assert y.grad_fn.older
+        with pytest.raises(RuntimeError, match="let go of every eager output"):
+            y.backward(torch.empty_like(y))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, eager)
