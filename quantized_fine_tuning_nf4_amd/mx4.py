@@ -87,7 +87,8 @@ class Dropout:
             raise ValueError("step must hold one int64")
 
     def c_struct(self) -> _Dropout:
-        return _Dropout(self.seed, self.offset, _ptr(self.step), self.p)
+        # (the C side has p in 32 bits, where the nearest number may be 1, which it refuses)
+        return _Dropout(self.seed, self.offset, _ptr(self.step), min(self.p, 1 - 2.0 ** -24))
 
 
 def _drop(drop: Dropout | None, *beside: torch.Tensor):
