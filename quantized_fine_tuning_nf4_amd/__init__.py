@@ -209,6 +209,17 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _room(given: torch.Tensor | None, need: int, device, zeroed: bool = False) -> torch.Tensor:
+    """A call's workspace: the given one where it is large enough (the calls write its first
+    bytes in a row, so a strided one is refused: it may end before them), else a new one."""
+    if given is None or given.numel() < need:
+        return (torch.zeros if zeroed else torch.empty)(max(need, 1), dtype=torch.uint8,
+                                                        device=device)
+    if not given.is_contiguous() or given.device != device:
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return given
+
+
 @dataclass
 class NF4State:
     """Quantized weight on the device: packed 4-bit codes and either the
@@ -275,8 +286,7 @@ def nf4_quantize_dq(W: torch.Tensor, out: NF4State | None = None,
         raise ValueError("W must be 1-D or 2-D")
     st = out if out is not None else empty_state(rows, cols, W.device)
     ws_bytes = L.nf4_quantize_dq_workspace(rows, cols)
-    ws = workspace if workspace is not None else torch.empty(max(ws_bytes, 1), dtype=torch.uint8,
-                                                             device=W.device)
+    ws = _room(workspace, ws_bytes if workspace is None else 0, W.device)
     if nonfinite is not None:
         _dev(nonfinite, torch.int32, "nonfinite")
         if nonfinite.numel() != 1:
@@ -310,8 +320,7 @@ def qn_quantize(W: torch.Tensor, codebook: str = "nf4", double_quant: bool = Tru
         st = NF4State(torch.empty(32 * nb, dtype=torch.uint8, device=dev), None, None, None,
                       rows, cols, torch.empty(nb, dtype=torch.float32, device=dev), cb)
     ws_bytes = L.nf4_quantize_dq_workspace(rows, cols)
-    ws = workspace if workspace is not None else torch.empty(max(ws_bytes, 1), dtype=torch.uint8,
-                                                             device=dev)
+    ws = _room(workspace, ws_bytes if workspace is None else 0, dev)
     if nonfinite is not None:
         _dev(nonfinite, torch.int32, "nonfinite")
     _check(L.qn_quantize(W.data_ptr(), rows, cols, cb, int(bool(double_quant)),
@@ -471,8 +480,7 @@ def qlora_linear_fwd(st: NF4State, x: torch.Tensor, A: torch.Tensor, B: torch.Te
     op = ctypes.byref(o) if o is not None else None
     sc = st.c_struct()
     ws_bytes = L.qlora_linear_workspace_state(ctypes.byref(sc), M, r, 0, op)
-    if workspace is None or workspace.numel() < ws_bytes:
-        workspace = linear_workspace(ws_bytes, x.device)
+    workspace = _room(workspace, ws_bytes, x.device, zeroed=True)
     s = st.c_struct()
     _check(L.qlora_linear_fwd_ex(ctypes.byref(s), x.data_ptr(), M, A.data_ptr(), B.data_ptr(), r,
                                  float(alpha), op, y.data_ptr(), _ptr(u), workspace.data_ptr(),
@@ -511,8 +519,7 @@ def qlora_linear_bwd(st: NF4State, x: torch.Tensor, dY: torch.Tensor, A: torch.T
     op = ctypes.byref(o) if o is not None else None
     sc = st.c_struct()
     ws_bytes = L.qlora_linear_workspace_state(ctypes.byref(sc), M, r, 1, op)
-    if workspace is None or workspace.numel() < ws_bytes:
-        workspace = linear_workspace(ws_bytes, x.device)
+    workspace = _room(workspace, ws_bytes, x.device, zeroed=True)
     s = st.c_struct()
     _check(L.qlora_linear_bwd_ex(ctypes.byref(s), x.data_ptr(), dY.data_ptr(), M, A.data_ptr(),
                                  B.data_ptr(), r, float(alpha), op, _ptr(u), _ptr(dX),

@@ -22,7 +22,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import (QN_BF16, QN_EALIGN, QN_F32, NF4State, _Act8, _BlockNorm, _capture_nodes, _check,
-               _dev, _linear_args, _opts, _ptr, _refuse_older, _stream, load_library)
+               _dev, _linear_args, _opts, _ptr, _refuse_older, _room, _stream, load_library)
 
 ACT8_BLOCK = 64
 MAX_TOP = 32  # alternatives of a row
@@ -168,8 +168,7 @@ def qlora_linear_bwd_act8(st: NF4State, x8: Act8, dY: torch.Tensor, A: torch.Ten
         return dX, dA, dB
     o = _opts(rslora, dropout_mask, dropout_p)
     need = L.qlora_linear_bwd_act8_workspace(M, st.rows, st.cols, r, int(need_dx))
-    if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    workspace = _room(workspace, need, dev)
     s, c = st.c_struct(), x8.c_struct()
     rc = L.qlora_linear_bwd_act8(ctypes.byref(s), ctypes.byref(c), dY.data_ptr(), M,
                                  A.data_ptr(), B.data_ptr(), r, float(alpha),
@@ -284,8 +283,8 @@ def block_norm_bwd(dy: torch.Tensor, h_new: torch.Tensor, w_pre: torch.Tensor,
         if w_post is not None:
             dw_post = torch.empty(D, dtype=torch.float32, device=dev)
     need = L.block_norm_bwd_workspace(ctypes.byref(n), int(need_weights), int(dgate is not None))
-    if need > 0 and (workspace is None or workspace.numel() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if need > 0:
+        workspace = _room(workspace, need, dev)
     rc = L.block_norm_bwd(ctypes.byref(n), dy.data_ptr(), _ptr(dh_new), h_new.data_ptr(),
                           _ptr(o), dh.data_ptr(), _ptr(do), _ptr(dgate), _ptr(dw_post),
                           _ptr(dw_pre), _ptr(workspace),
@@ -395,8 +394,8 @@ def token_logprobs_fwd(logits: torch.Tensor, targets: torch.Tensor | None = None
         top_ids = torch.empty(T, top_k, dtype=torch.int32, device=dev)
     dt = _DTYPES[logits.dtype]
     need = L.token_logprobs_workspace(T, V, dt, top_k)
-    if need > 0 and (workspace is None or workspace.numel() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if need > 0:
+        workspace = _room(workspace, need, dev)
     _check(L.token_logprobs_fwd(logits.data_ptr(), dt, T, V, ld, _ptr(targets), scale, top_k,
                                 _ptr(logp), entropy.data_ptr(), stats.data_ptr(), _ptr(top_logp),
                                 _ptr(top_ids), _ptr(workspace),

@@ -22,7 +22,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import (NF4State, QNError, _check, _dev, _Dropout, _MX4, _ptr,  # noqa: F401
-               _refuse_older, _stream, load_library)
+               _refuse_older, _room, _stream, load_library)
 from .finetune import _DTYPES, Act8, _act8, _aligned, _written
 
 MX4_BLOCK = 32   # columns of a row that share a scale
@@ -253,11 +253,10 @@ def _adapter(w, M, A, B, drop):
 
 
 def _workspace(need: int, given: torch.Tensor | None, device) -> torch.Tensor:
-    if given is not None and given.numel() >= need:
-        if not given.is_contiguous() or given.dtype != torch.uint8 or given.device != device:
-            raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
-        return given
-    return torch.empty(need, dtype=torch.uint8, device=device)
+    ws = _room(given, need, device)
+    if ws.dtype != torch.uint8:
+        raise ValueError("workspace must be a uint8 tensor")
+    return ws
 
 
 def mx4_linear_fwd(w: MX4, x: torch.Tensor, A: torch.Tensor | None = None,
@@ -362,9 +361,7 @@ def _qlora_fwd_drop(st: NF4State, x, A, B, r, alpha, rslora, drop, y, u, workspa
     L = load_library()
     M = x.shape[0]
     need = _need_drop(M, st.rows, st.cols, r, 0, 0)
-    if workspace is None or workspace.numel() < need:
-        # (under dropout no launch counts arrivals: nothing to clear)
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    workspace = _room(workspace, need, x.device)  # (nothing to clear, whatever the route)
     _check(L.qlora_linear_fwd_drop(ctypes.byref(st.c_struct()), x.data_ptr(), M, A.data_ptr(),
                                    B.data_ptr(), r, float(alpha), int(bool(rslora)),
                                    _drop(drop, x), y.data_ptr(), _ptr(u), workspace.data_ptr(),
@@ -381,8 +378,7 @@ def _qlora_bwd_drop(st: NF4State, x, x8, dY, A, B, r, alpha, rslora, drop, u, dX
     L = load_library()
     M = dY.shape[0]
     need = _need_drop(M, st.rows, st.cols, r, 1, int(x8 is not None))
-    if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dY.device)
+    workspace = _room(workspace, need, dY.device)
     return L.qlora_linear_bwd_drop(
         ctypes.byref(st.c_struct()), _ptr(x), None if x8 is None else ctypes.byref(x8.c_struct()),
         dY.data_ptr(), M, A.data_ptr(), B.data_ptr(), r, float(alpha), int(bool(rslora)),
