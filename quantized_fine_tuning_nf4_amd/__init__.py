@@ -205,6 +205,22 @@ def _dev(t: torch.Tensor, dtype, name: str) -> torch.Tensor:
     return t
 
 
+def _given(t: torch.Tensor, dtype, n: int, name: str) -> torch.Tensor:
+    """An output that a call is given: contiguous, of that type and with room for the n
+    elements that the call writes."""
+    if _dev(t, dtype, name).numel() < n:
+        raise ValueError(f"{name} must hold {n} elements")
+    return t
+
+
+def _written(*ts: torch.Tensor) -> None:
+    """Tells autograd that a call wrote tensors it was given: one that was saved for a
+    backward before raises there, as after any other write in place."""
+    for t in ts:
+        if not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -284,7 +300,14 @@ def nf4_quantize_dq(W: torch.Tensor, out: NF4State | None = None,
     rows, cols = (W.shape[0], W.shape[1]) if W.dim() == 2 else (1, W.numel())
     if W.dim() not in (1, 2):
         raise ValueError("W must be 1-D or 2-D")
-    st = out if out is not None else empty_state(rows, cols, W.device)
+    if out is None:
+        st = empty_state(rows, cols, W.device)
+    else:
+        st, (nb, ng) = out, state_sizes(rows, cols)
+        _given(st.packed, torch.uint8, 32 * nb, "out.packed")
+        _given(st.qscale, torch.uint8, nb, "out.qscale")
+        _given(st.scale2, torch.float32, ng, "out.scale2")
+        _given(st.offset, torch.float32, 1, "out.offset")
     ws_bytes = L.nf4_quantize_dq_workspace(rows, cols)
     ws = _room(workspace, ws_bytes if workspace is None else 0, W.device)
     if nonfinite is not None:
@@ -333,11 +356,14 @@ def qn_quantize(W: torch.Tensor, codebook: str = "nf4", double_quant: bool = Tru
 def nf4_dequantize(st: NF4State, dtype=torch.bfloat16, out: torch.Tensor | None = None):
     L = load_library()
     code = {torch.float32: QN_F32, torch.bfloat16: QN_BF16}[dtype]
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty((st.rows, st.cols), dtype=dtype, device=st.device)
-    _dev(out, dtype, "out")
+    _given(out, dtype, st.rows * st.cols, "out")
     s = st.c_struct()
     _check(L.nf4_dequantize(ctypes.byref(s), code, out.data_ptr(), _stream(st.device)))
+    if given:
+        _written(out)
     return out
 
 
@@ -351,12 +377,15 @@ def nf4_merge_lora(st: NF4State, A: torch.Tensor, B: torch.Tensor, alpha: float,
     r = A.shape[0]
     if A.dim() != 2 or A.shape[1] != st.cols or B.shape != (st.rows, r):
         raise ValueError(f"A must be [r, {st.cols}] and B [{st.rows}, r]")
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty((st.rows, st.cols), dtype=torch.float32, device=st.device)
-    _dev(out, torch.float32, "out")
+    _given(out, torch.float32, st.rows * st.cols, "out")
     s = st.c_struct()
     _check(L.nf4_merge_lora(ctypes.byref(s), A.data_ptr(), B.data_ptr(), r, float(alpha),
                             out.data_ptr(), _stream(st.device)))
+    if given:
+        _written(out)
     return out
 
 
@@ -388,7 +417,7 @@ class Adam8:
         if g.numel() != self.p.numel():
             raise ValueError("grad must have the parameter's size")
         if p_bf16 is not None:
-            _dev(p_bf16, torch.bfloat16, "p_bf16")
+            _given(p_bf16, torch.bfloat16, self.p.numel(), "p_bf16")
         self.t += 1
         h = _AdamHP(self.lr, self.betas[0], self.betas[1], self.eps, self.wd, self.t)
         _check(load_library().adamw8_step(self.p.data_ptr(), g.data_ptr(), self.p.numel(),
@@ -470,12 +499,18 @@ def qlora_linear_fwd(st: NF4State, x: torch.Tensor, A: torch.Tensor, B: torch.Te
     A = _dev(A, torch.bfloat16, "A")
     B = _dev(B, torch.bfloat16, "B")
     M, r = _linear_args(st, x, A, B)
-    if y is None:
+    given = y is not None
+    if not given:
         y = torch.empty(M, st.rows, dtype=torch.bfloat16, device=x.device)
+    else:
+        _given(y, torch.bfloat16, M * st.rows, "y")
     u = torch.empty(M, r, dtype=torch.float32, device=x.device) if save_u else None
     if drop is not None:
         _one_dropout(dropout_mask, dropout_p)
-        return _qlora_fwd_drop(st, x, A, B, r, alpha, rslora, drop, y, u, workspace)
+        _qlora_fwd_drop(st, x, A, B, r, alpha, rslora, drop, y, u, workspace)
+        if given:
+            _written(y)
+        return y, u
     o = _opts(rslora, dropout_mask, dropout_p)
     op = ctypes.byref(o) if o is not None else None
     sc = st.c_struct()
@@ -485,6 +520,8 @@ def qlora_linear_fwd(st: NF4State, x: torch.Tensor, A: torch.Tensor, B: torch.Te
     _check(L.qlora_linear_fwd_ex(ctypes.byref(s), x.data_ptr(), M, A.data_ptr(), B.data_ptr(), r,
                                  float(alpha), op, y.data_ptr(), _ptr(u), workspace.data_ptr(),
                                  workspace.numel(), _stream(x.device)))
+    if given:
+        _written(y)
     return y, u
 
 
@@ -543,10 +580,15 @@ def lora_linear_bf16(x: torch.Tensor, W: torch.Tensor, V: torch.Tensor, L_: torc
     r = V.shape[1] if V.dim() == 2 else -1
     if V.shape != (M, r) or L_.shape != (rows, r):
         raise ValueError("V must be [M, r] and L [d_out, r]")
-    if y is None:
+    given = y is not None
+    if not given:
         y = torch.empty((M, rows), dtype=torch.bfloat16, device=x.device)
+    else:
+        _given(y, torch.bfloat16, M * rows, "y")
     _check(L.lora_linear_bf16(x.data_ptr(), M, W.data_ptr(), rows, cols, V.data_ptr(),
                               L_.data_ptr(), r, float(alpha), y.data_ptr(), _stream(x.device)))
+    if given:
+        _written(y)
     return y
 
 

@@ -22,7 +22,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import (QN_BF16, QN_EALIGN, QN_F32, NF4State, _Act8, _BlockNorm, _capture_nodes, _check,
-               _dev, _linear_args, _opts, _ptr, _refuse_older, _room, _stream, load_library)
+               _dev, _linear_args, _opts, _ptr, _refuse_older, _room, _stream, _written,
+               load_library)
 
 ACT8_BLOCK = 64
 MAX_TOP = 32  # alternatives of a row
@@ -39,14 +40,6 @@ def _aligned(status: int, *ts: torch.Tensor | None):
     if status != QN_EALIGN or not any(t is not None and t.data_ptr() % 16 for t in ts):
         return None
     return [t.clone() if t is not None and t.data_ptr() % 16 else t for t in ts]
-
-
-def _written(*ts: torch.Tensor) -> None:
-    """Tells autograd that a call wrote tensors it was given: one that was saved for a
-    backward before raises there, as after any other write in place."""
-    for t in ts:
-        if not t.is_inference():
-            torch.autograd.graph.increment_version(t)
 
 
 # ------------------------------------------------- activation checkpoints in 8 bits
