@@ -471,11 +471,11 @@ def dropout_mask(M: int, cols: int, p: float, device="cuda", generator=None) -> 
     return (keep.view(-1, 8).to(torch.int32) * w).sum(dim=1).to(torch.uint8)
 
 
-def _opts(rslora, mask, p):
+def _opts(rslora, mask, p, n):
     if not rslora and mask is None and not p:
         return None
-    if mask is not None:
-        _dev(mask, torch.uint8, "dropout_mask")
+    if mask is not None and 8 * _dev(mask, torch.uint8, "dropout_mask").numel() < n:
+        raise ValueError(f"dropout_mask must hold {n} bits")
     return _LoraOpts(int(bool(rslora)), _ptr(mask), float(p))
 
 
@@ -511,7 +511,7 @@ def qlora_linear_fwd(st: NF4State, x: torch.Tensor, A: torch.Tensor, B: torch.Te
         if given:
             _written(y)
         return y, u
-    o = _opts(rslora, dropout_mask, dropout_p)
+    o = _opts(rslora, dropout_mask, dropout_p, M * st.cols)
     op = ctypes.byref(o) if o is not None else None
     sc = st.c_struct()
     ws_bytes = L.qlora_linear_workspace_state(ctypes.byref(sc), M, r, 0, op)
@@ -552,7 +552,7 @@ def qlora_linear_bwd(st: NF4State, x: torch.Tensor, dY: torch.Tensor, A: torch.T
         _check(_qlora_bwd_drop(st, x, None, dY, A, B, r, alpha, rslora, drop, u, dX, dA, dB,
                                workspace))
         return dX, dA, dB
-    o = _opts(rslora, dropout_mask, dropout_p)
+    o = _opts(rslora, dropout_mask, dropout_p, M * st.cols)
     op = ctypes.byref(o) if o is not None else None
     sc = st.c_struct()
     ws_bytes = L.qlora_linear_workspace_state(ctypes.byref(sc), M, r, 1, op)

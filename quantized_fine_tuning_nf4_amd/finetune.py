@@ -139,8 +139,6 @@ def qlora_linear_bwd_act8(st: NF4State, x8: Act8, dY: torch.Tensor, A: torch.Ten
         raise ValueError(f"dY must be [{M}, {st.rows}]")
     if u.shape != (M, r):
         raise ValueError(f"u must be [{M}, {r}]")
-    if dropout_mask is not None and dropout_mask.numel() * 8 < M * st.cols:
-        raise ValueError(f"dropout_mask must hold {M * st.cols} bits")
     dev = dY.device
     dX = torch.empty(M, st.cols, dtype=torch.bfloat16, device=dev) if need_dx else None
     dA = torch.empty(r, st.cols, dtype=torch.float32, device=dev)
@@ -159,7 +157,7 @@ def qlora_linear_bwd_act8(st: NF4State, x8: Act8, dY: torch.Tensor, A: torch.Ten
                                          need_dx=need_dx, workspace=workspace, rslora=rslora,
                                          drop=drop)
         return dX, dA, dB
-    o = _opts(rslora, dropout_mask, dropout_p)
+    o = _opts(rslora, dropout_mask, dropout_p, M * st.cols)
     need = L.qlora_linear_bwd_act8_workspace(M, st.rows, st.cols, r, int(need_dx))
     workspace = _room(workspace, need, dev)
     s, c = st.c_struct(), x8.c_struct()
