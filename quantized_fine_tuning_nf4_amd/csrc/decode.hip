@@ -14,6 +14,7 @@
 // 64g + 16w .. +15), blocks z*nbs .. (z+1)*nbs-1 of every row; X's slice is
 // staged in LDS once for the four waves.  Partial sums go to part[z][m][n];
 // a second kernel adds the slices, the LoRA term and rounds to bf16.
+#include "lds_limit.h"
 #include "qn_device.h"
 #include "qn_internal.h"
 
@@ -977,29 +978,24 @@ hipError_t launch_decode_fwd(const WState& w, const uint16_t* X, int64_t M, cons
   const int nbs = (int)(K / 64 / S);
   const size_t lds = (size_t)M * (nbs * 128 + 16);
   constexpr size_t kMaxLds = 64 * 1024;  // X slice: at most 16 rows of 16 blocks
-  static hipError_t attr = [] {
-    const void* k[4] = {reinterpret_cast<const void*>(k_decode_partial<kCodeNF4, false>),
-                        reinterpret_cast<const void*>(k_decode_partial<kCodeNF4, true>),
-                        reinterpret_cast<const void*>(k_decode_partial<kCodeFP4, false>),
-                        reinterpret_cast<const void*>(k_decode_partial<kCodeFP4, true>)};
-    for (const void* f : k) {
-      const hipError_t e =
-          hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxLds);
-      if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
-  }();
-  if (attr != hipSuccess) return attr;
   if (nbs != 16 || lds > kMaxLds) return hipErrorInvalidValue;
+  const void* kernels[2][2] = {{reinterpret_cast<const void*>(k_decode_partial<kCodeNF4, false>),
+                                reinterpret_cast<const void*>(k_decode_partial<kCodeNF4, true>)},
+                               {reinterpret_cast<const void*>(k_decode_partial<kCodeFP4, false>),
+                                reinterpret_cast<const void*>(k_decode_partial<kCodeFP4, true>)}};
+  static LdsLimit limits[2][2];
+  const bool fp4 = w.codebook == kCodeFP4, abs = w.absmax != nullptr;
+  const hipError_t limit = limits[fp4][abs](kernels[fp4][abs], kMaxLds);
+  if (limit != hipSuccess) return limit;
   const int64_t groups = (N + 63) / 64;
   const dim3 grid((unsigned)(groups + 1), (unsigned)S);
 #define QN_PART(CBK, ABS)                                                                      \
   hipLaunchKernelGGL((k_decode_partial<CBK, ABS>), grid, dim3(T), lds, st, w.packed, w.qscale, \
                      w.scale2, w.offset, w.absmax, X, A, r, M, N, K, nbs, part, upart)
-  if (w.codebook == kCodeFP4) {
-    if (w.absmax) QN_PART(kCodeFP4, true); else QN_PART(kCodeFP4, false);
+  if (fp4) {
+    if (abs) QN_PART(kCodeFP4, true); else QN_PART(kCodeFP4, false);
   } else {
-    if (w.absmax) QN_PART(kCodeNF4, true); else QN_PART(kCodeNF4, false);
+    if (abs) QN_PART(kCodeNF4, true); else QN_PART(kCodeNF4, false);
   }
 #undef QN_PART
   hipError_t e = hipGetLastError();

@@ -30,6 +30,7 @@
 // (padded to a multiple of 64 with zeros).
 #include <type_traits>
 
+#include "lds_limit.h"
 #include "qn_device.h"
 #include "qn_internal.h"
 
@@ -519,22 +520,6 @@ hipError_t launch_wt(const uint16_t* A, int64_t lda, int64_t R, const uint16_t* 
                      int64_t M, int64_t Nc, const float* V, const uint16_t* L, int r, float s,
                      uint16_t* C, const uint8_t* mask, hipStream_t st) {
   using G = Geo<WTM, WTN>;
-  static hipError_t attr = [] {
-    const void* k16[2] = {reinterpret_cast<const void*>(k_gemm_nt<true, WTM, WTN, false, MASK>),
-                          reinterpret_cast<const void*>(k_gemm_nt<true, WTM, WTN, true, MASK>)};
-    const void* kr[2] = {reinterpret_cast<const void*>(k_gemm_nt<false, WTM, WTN, false, MASK>),
-                         reinterpret_cast<const void*>(k_gemm_nt<false, WTM, WTN, true, MASK>)};
-    for (int t = 0; t < 2; ++t) {
-      hipError_t e = hipFuncSetAttribute(k16[t], hipFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)G::LDS_BYTES);
-      if (e == hipSuccess)
-        e = hipFuncSetAttribute(kr[t], hipFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)G::LDS_MAIN);
-      if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
-  }();
-  if (attr != hipSuccess) return attr;
   const int64_t tm = (M + G::BM - 1) / G::BM, tc = (Nc + G::BN - 1) / G::BN;
   const int steps = (int)(ldb / BK);
   const dim3 grid((unsigned)(tm * tc)), block(T);
@@ -543,7 +528,16 @@ hipError_t launch_wt(const uint16_t* A, int64_t lda, int64_t R, const uint16_t* 
                      L16 ? G::LDS_BYTES : G::LDS_MAIN, st, A, lda, R, Bm, ldb, steps, M, Nc, V, \
                      L, r, s, C, (int)tm, (int)tc, mask)
   const bool tail = R != ldb;
-  if (r == LORA_R) {
+  const void* kernels[2][2] = {{reinterpret_cast<const void*>(k_gemm_nt<false, WTM, WTN, false, MASK>),
+                                reinterpret_cast<const void*>(k_gemm_nt<false, WTM, WTN, true, MASK>)},
+                               {reinterpret_cast<const void*>(k_gemm_nt<true, WTM, WTN, false, MASK>),
+                                reinterpret_cast<const void*>(k_gemm_nt<true, WTM, WTN, true, MASK>)}};
+  static LdsLimit limits[2][2];
+  const bool l16 = r == LORA_R;
+  const hipError_t limit =
+      limits[l16][tail](kernels[l16][tail], l16 ? G::LDS_BYTES : G::LDS_MAIN);
+  if (limit != hipSuccess) return limit;
+  if (l16) {
     if (tail) QN_GEMM(true, true); else QN_GEMM(true, false);
   } else {
     if (tail) QN_GEMM(false, true); else QN_GEMM(false, false);

@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "lds_limit.h"
 #include "qn_device.h"
 #include "qn_internal.h"
 
@@ -470,20 +471,13 @@ hipError_t launch_thin_nt(const uint16_t* Z, const uint16_t* T, int64_t M, int64
   if (r <= 16 && slice <= kThinNt1MaxSlice) {
     if (d.on && t_rows) return hipErrorInvalidValue;  // (T of a dropped Z is A, as rows)
     const int mode = d.on ? 3 : !t_rows ? 0 : r == 16 ? 1 : 2;
-    static const hipError_t attr[4] = {
-        hipFuncSetAttribute(reinterpret_cast<const void*>(k_thin_nt1<0>),
-                            hipFuncAttributeMaxDynamicSharedMemorySize,
-                            (int)(16 * (kThinNt1MaxSlice * 2 + 16))),
-        hipFuncSetAttribute(reinterpret_cast<const void*>(k_thin_nt1<1>),
-                            hipFuncAttributeMaxDynamicSharedMemorySize,
-                            (int)(16 * (kThinNt1MaxSlice * 2 + 16))),
-        hipFuncSetAttribute(reinterpret_cast<const void*>(k_thin_nt1<2>),
-                            hipFuncAttributeMaxDynamicSharedMemorySize,
-                            (int)(16 * (kThinNt1MaxSlice * 2 + 16))),
-        hipFuncSetAttribute(reinterpret_cast<const void*>(k_thin_nt1<0, true>),
-                            hipFuncAttributeMaxDynamicSharedMemorySize,
-                            (int)(16 * (kThinNt1MaxSlice * 2 + 16)))};
-    if (attr[mode] != hipSuccess) return attr[mode];
+    const void* kernels[4] = {reinterpret_cast<const void*>(k_thin_nt1<0>),
+                              reinterpret_cast<const void*>(k_thin_nt1<1>),
+                              reinterpret_cast<const void*>(k_thin_nt1<2>),
+                              reinterpret_cast<const void*>(k_thin_nt1<0, true>)};
+    static LdsLimit limits[4];
+    const hipError_t limit = limits[mode](kernels[mode], 16 * (kThinNt1MaxSlice * 2 + 16));
+    if (limit != hipSuccess) return limit;
     const int steps = (int)((slice + 31) / 32);
     const size_t lds = (size_t)16 * (steps * 64 + 16);
     if (mode == 0)

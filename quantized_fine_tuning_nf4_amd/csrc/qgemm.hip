@@ -24,6 +24,7 @@
 // 8(v/4) + 4(l/32) + v%4, column l%32 of the 32x32 tile.
 #include <type_traits>
 
+#include "lds_limit.h"
 #include "qn_device.h"
 #include "qn_internal.h"
 
@@ -431,19 +432,14 @@ __global__ __launch_bounds__(64 * WM * WN) void k_qgemm_dx(
   store_tile<WM, WN, TM, TN>(acc, dX, M, K, m0, k0);
 }
 
-template <class Kern>
-hipError_t set_lds(Kern k, size_t bytes) {
-  return hipFuncSetAttribute(reinterpret_cast<const void*>(k),
-                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 template <int WM, int WN, int TM, int TN, int CB, bool ABS>
 hipError_t run_fwd_f(const WState& w, const uint16_t* X, int64_t M, const float* u,
                      const uint16_t* B, int r, float s, uint16_t* Y, hipStream_t st) {
   using Cfg = Tile<WM, WN, TM, TN>;
   auto kern = k_qgemm_fwd<WM, WN, TM, TN, CB, ABS>;
-  static hipError_t attr = set_lds(kern, Cfg::LDS);
-  if (attr != hipSuccess) return attr;
+  static LdsLimit limit;
+  const hipError_t e = limit(reinterpret_cast<const void*>(kern), Cfg::LDS);
+  if (e != hipSuccess) return e;
   const int64_t tm = (M + Cfg::BM - 1) / Cfg::BM, tn = (w.rows + Cfg::BN - 1) / Cfg::BN;
   hipLaunchKernelGGL(kern, dim3((unsigned)(tm * tn)), dim3(Cfg::T), Cfg::LDS, st, w.packed,
                      w.qscale, w.scale2, w.offset, w.absmax, X, u, B, M, w.rows, w.cols, r, s, Y,
@@ -457,8 +453,9 @@ hipError_t run_dx_f(const WState& w, const uint16_t* G, int64_t M, const float* 
                     hipStream_t st) {
   using Cfg = Tile<WM, WN, TM, TN>;
   auto kern = k_qgemm_dx<WM, WN, TM, TN, CB, ABS, MASK>;
-  static hipError_t attr = set_lds(kern, Cfg::LDS);
-  if (attr != hipSuccess) return attr;
+  static LdsLimit limit;
+  const hipError_t e = limit(reinterpret_cast<const void*>(kern), Cfg::LDS);
+  if (e != hipSuccess) return e;
   const int64_t tm = (M + Cfg::BM - 1) / Cfg::BM, tk = (w.cols + Cfg::BN - 1) / Cfg::BN;
   hipLaunchKernelGGL(kern, dim3((unsigned)(tm * tk)), dim3(Cfg::T), Cfg::LDS, st, w.packed,
                      w.qscale, w.scale2, w.offset, w.absmax, G, v, A, M, w.rows, w.cols, r, s, dX,
