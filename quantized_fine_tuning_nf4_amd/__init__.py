@@ -687,17 +687,18 @@ class QLoRALinear(torch.nn.Module):
     of x is kept as an 8-bit checkpoint instead of x itself; forward's x8
     passes one that is at hand already (BlockNorm makes it, and the linears
     that share an input share it).  base: "nf4", or "mx4" for MXFP4 weights,
-    whose product takes x in MXFP4 too (mx4_linear_fwd).  Without a seed the
-    dropout's mask is drawn from torch's generators (on MXFP4 weights by the kernels
-    from a counter, its key from the host's generator), so that a forward that is run
-    again for the backward (torch.utils.checkpoint) has the same one.  seed: the
-    mask is drawn by the kernels from a counter and not kept, each forward's from
-    an offset of its own (Dropout; give every layer, and every rank, its seed), and
-    a forward that is run again would draw another: it raises.  step:
-    its device tensor, for captured graphs, where the offset of the capture stays:
-    count it up by one between replays (offsets are 2^32 apart then).  Before a
-    backward is captured, let go of every eager output of the layer: with an eager
-    graph of its parameters alive a captured backward raises."""
+    whose product takes x in MXFP4 too (mx4_linear_fwd).
+    Without a seed the dropout's mask is drawn from torch's generators (on MXFP4
+    weights by the kernels from a counter, its key from the host's generator),
+    so that a forward that is run again for the backward (torch.utils.checkpoint)
+    has the same one.  seed: the mask is drawn by the kernels from a counter and
+    not kept, each forward's from an offset of its own (Dropout; give every layer,
+    and every rank, its seed; how many forwards there were is in the state dict);
+    a forward that is run again would draw another, and raises.  step: the
+    Dropout's device tensor, for captured graphs, where the offset of the capture
+    stays: count it up by one between replays (offsets are 2^32 apart then).
+    Before a backward is captured, let go of every eager output of the layer: with
+    an eager graph of its parameters alive a captured backward raises."""
 
     def __init__(self, weight: torch.Tensor, r: int = 16, alpha: float = 32.0,
                  dropout: float = 0.0, rslora: bool = False, act8: bool = False,
@@ -720,6 +721,17 @@ class QLoRALinear(torch.nn.Module):
         self.lora_A = torch.nn.Parameter(A.to(torch.bfloat16))
         self.lora_B = torch.nn.Parameter(torch.zeros(d_out, r, dtype=torch.bfloat16,
                                                      device=weight.device))
+
+    def _save_to_state_dict(self, destination, prefix, keep_vars):
+        super()._save_to_state_dict(destination, prefix, keep_vars)
+        if self.seed is not None:  # (a run that goes on from here draws other masks than so far)
+            destination[prefix + "draws"] = torch.tensor(self.draws)
+
+    def _load_from_state_dict(self, state_dict, prefix, *args):
+        draws = state_dict.pop(prefix + "draws", None)  # (absent: the counter stays)
+        if draws is not None and self.seed is not None:
+            self.draws = int(draws)
+        super()._load_from_state_dict(state_dict, prefix, *args)
 
     def _draw(self, p):
         """The mask of a forward."""
