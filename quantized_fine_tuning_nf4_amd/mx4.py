@@ -371,7 +371,8 @@ def _qlora_fwd_drop(st: NF4State, x, A, B, r, alpha, rslora, drop, y, u, workspa
 
 def _qlora_bwd_drop(st: NF4State, x, x8, dY, A, B, r, alpha, rslora, drop, u, dX, dA, dB,
                     workspace):
-    if not _here(dY, x, A, B, u, st.packed):
+    codes, exps = (None, None) if x8 is None else (x8.codes, x8.exps)
+    if not _here(dY, x, codes, exps, A, B, u, st.packed):
         with torch.cuda.device(dY.device):
             return _qlora_bwd_drop(st, x, x8, dY, A, B, r, alpha, rslora, drop, u, dX, dA, dB,
                                    workspace)
