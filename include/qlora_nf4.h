@@ -527,7 +527,8 @@ typedef struct {
 } qn_mx4;
 
 /* x [rows, cols] fp32 or bf16 -> codes, scales.  0 <= rows <= 2^23, 1 <= cols <= 2^20,
- * at most 3 2^35 elements (rows counted up to a multiple of 32, columns of 256); rows of a width that is no multiple of 8 may start on any element. */
+ * at most 3 2^35 elements (rows counted up to a multiple of 32, columns of 256); rows of
+ * a width that is no multiple of 8 may start on any element. */
 qn_status mx4_quantize(const void* x, qn_dtype dtype, int64_t rows, int64_t cols, uint8_t* codes,
                        uint8_t* scales, void* stream);
 

@@ -425,13 +425,17 @@ __global__ __launch_bounds__(kThreadsU) void k_mx4_u(const float* __restrict__ u
 // c ^ ((y >> 1) & 7), so that 16 rows of a fragment read sit on distinct banks.  In
 // half t of a step lane (g, n) = (l / 16, l % 16) takes row n's block 4 t + g, whose scale
 // is byte 2 (tile % 2) + t of the lane's four.
-// 8192x4096x4096 at r = 16 69.0 us, 3.98 PFLOP/s (256 x 256 tiles, 109 MB read, 67 written):
-// power holds it.  4096x4096x16384 takes 113 us at 1.88 GHz on random operands and 87 at
-// 2.43 GHz on zeros, by the same instructions, of which MFMAs are 62% of the cycles (a wave
-// alone on its SIMD issues one in 24.4 cycles, 5.7 PFLOP/s by 256 units, two waves 7.3).
+// 8192x4096x4096 at r = 16 69.0 us, 3.98 PFLOP/s (256 x 256 tiles, 109 MB read, 67 written).
+// Three things hold it: the clock (4096x4096x16384, 4.87 PFLOP/s, takes 113 us at 1.88 GHz on
+// random operands and 87 at 2.43 GHz on zeros, by the same instructions: power), issue (on
+// either operands MFMAs are 62% of the cycles; the instruction alone reaches 5.7 PFLOP/s
+// with one wave a SIMD and 7.3 with two, on random operands) and what a round of tiles costs
+// outside its steps, some 6 us (at the rate of 16384 columns the two rounds take 56 us).
 // 32x32x64 tiles take 75 us; four stages for many tiles, loads or barriers elsewhere in the
-// step and wave priorities change nothing or lose.  301x50021x1000 22.5 us: four
-// steps a tile, so the first stage and the output (30 MB in rows at odd addresses) are most of it; 64 x 128
+// step and wave priorities change nothing or lose.  301x50021x1000 22.5 us:
+// 2.3 rounds of tiles take three, of four steps each, whose first stage and output nothing
+// overlaps (the call 26.8 us, with 256 rows of x, two rounds, 22.6), and rows of an odd
+// length (with 50016 columns 22.6, 50024 25.1, though no more bytes are written); 64 x 128
 // tiles 24.6 and 64 x 64 27.2 (two stages deep), eight waves 23.1.
 template <int WVM, int WVN, int TM, int TN, int STAGES>
 struct MxGeo {

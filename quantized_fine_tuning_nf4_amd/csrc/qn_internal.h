@@ -460,8 +460,10 @@ struct Mx4X {
   uint16_t* bo;     // 512 and 256 values for 16 rows and 16 ranks
 };
 // Batches whose product reads W straight into registers: against tiles (with x's pass) M =
-// 24, 4096x4096, r = 16 13.1 and 14.4 us, with 64 ranks 21 and 18.5, 14336x4096 without an
-// adapter 14.0 and 11.3.
+// 24, 4096x4096, r = 16 12.2 and 13.6 us, with 64 ranks 21 and 18.5, 14336x4096 without an
+// adapter 14.0 and 11.3.  W's rows are not in the rule, and past some thousands of them
+// tiles are ahead at r = 16 too: 17, 24 and 32 rows of x by 14336x4096 16.0, 16.2, 16.7
+// and 15.0, 15.9, 14.6 us, by 32000x4096 28.4, 29.6, 31.6 and 23.4, 23.3, 22.7.
 inline bool mx4_few_rows(int64_t M, int r) { return M <= (r >= 1 && r <= 16 ? 32 : 16); }
 int mx4_x_slices(int64_t M, int64_t K, int r);
 // A token or a few without an adapter: y from x itself (16-byte aligned) in one launch.
