@@ -594,69 +594,60 @@ def lora_linear_bf16(x: torch.Tensor, W: torch.Tensor, V: torch.Tensor, L_: torc
 
 # ---- Backwards in captured graphs.  torch adds a leaf's gradient in a node of that leaf, which
 # belongs to the stream that was current when the node was made and lives as long as any graph
-# that ends in it.  A captured backward that meets a node of an eager graph's stream has that
-# stream wait for the capture's: it is no part of the capture, the error comes up where
-# torch cannot pass it on, and the process ends.  So a forward under capture looks at its
-# parameters' nodes, and its backward raises where one is older.
-_MADE_ON, _SEEN = "qlora_nf4_made_on", "qlora_nf4_seen"
+# that ends in it.  A captured backward that meets a node of the default stream has that
+# stream wait for the capture's, which it may not: the error comes up where torch cannot pass
+# it on, and the process ends.  So a layer's forward marks the nodes of its inputs
+# with their stream, and its backward raises under capture where one is the default stream's
+# (other streams join the capture and are no fault).
+_MADE_ON = "qlora_nf4_made_on"
 
 
-def _nodes(leaves, stream: int):
-    """(nodes, older) for the leaves under capture on that stream: their nodes, to be held until
-    the graph holds them, and whether another stream's graph holds one already."""
-    nodes, older = [], False
-    for p in leaves:
-        if p is None or not (p.is_leaf and p.requires_grad):
-            continue
-        node = torch.autograd.graph.get_gradient_edge(p).node
-        if _MADE_ON not in node.metadata:  # a new one, unless it outlives this name
-            node.metadata[_SEEN] = True
-            del node
-            node = torch.autograd.graph.get_gradient_edge(p).node
-            node.metadata[_MADE_ON] = None if node.metadata.pop(_SEEN, False) else stream
-        older |= node.metadata[_MADE_ON] != stream
-        nodes.append(node)
-    return nodes, older
+def _mark_nodes(y: torch.Tensor, stream: int | None = None) -> None:
+    """Marks the leaves' nodes behind a layer's output as made on the current stream, those
+    that are not marked yet, and the layer's where one is the default stream's and it is not."""
+    fn = y.grad_fn
+    if fn is None:
+        return
+    if stream is None:
+        stream = _stream(y.device)
+    for node, _ in fn.next_functions:
+        if (hasattr(node, "variable") and not node.metadata.setdefault(_MADE_ON, stream)
+                and stream):
+            fn.meets_default_stream = True
 
 
-def _capture_nodes(*leaves):
-    if not (torch.is_grad_enabled() and torch.cuda.is_current_stream_capturing()):
-        return None, False
-    return _nodes(leaves, torch.cuda.current_stream().cuda_stream)
-
-
-def _refuse_older(older: bool) -> None:
-    if older and torch.cuda.is_current_stream_capturing():
-        raise RuntimeError("an eager graph of the layer's parameters still lives, and a backward "
-                           "captured now would end the process: let go of every eager output "
-                           "that leads to them before the capture")
+def _refuse_default_stream(ctx) -> None:
+    if getattr(ctx, "meets_default_stream", False) and torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("an eager graph of the layer's parameters, made on the default stream, "
+                           "still lives, and a backward captured now would end the process: let "
+                           "go of every eager output that leads to them before the capture")
 
 
 class _QLoRAFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, A, B, st, alpha, rslora, mask, p, older):
+    def forward(ctx, x, A, B, st, alpha, rslora, mask, p):
         y, u = qlora_linear_fwd(st, x, A, B, alpha, rslora=rslora, dropout_mask=mask,
                                 dropout_p=p)
         ctx.save_for_backward(x, A, B, u, mask)
-        ctx.st, ctx.alpha, ctx.rslora, ctx.p, ctx.older = st, alpha, rslora, p, older
+        ctx.st, ctx.alpha, ctx.rslora, ctx.p = st, alpha, rslora, p
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dY):
-        _refuse_older(ctx.older)
+        _refuse_default_stream(ctx)
         x, A, B, u, mask = ctx.saved_tensors
         dX, dA, dB = qlora_linear_bwd(ctx.st, x, dY.contiguous(), A, B, ctx.alpha, u,
                                       need_dx=ctx.needs_input_grad[0], rslora=ctx.rslora,
                                       dropout_mask=mask, dropout_p=ctx.p)
-        return dX, dA.to(A.dtype), dB.to(B.dtype), None, None, None, None, None, None
+        return dX, dA.to(A.dtype), dB.to(B.dtype), None, None, None, None, None
 
 
 class _QLoRAAct8Fn(torch.autograd.Function):
     """_QLoRAFn that keeps x for the backward as an 8-bit checkpoint."""
 
     @staticmethod
-    def forward(ctx, x, A, B, st, alpha, rslora, mask, p, x8, older):
+    def forward(ctx, x, A, B, st, alpha, rslora, mask, p, x8):
         if x8 is not None:
             _act8(x8, *x.shape)
         y, u = qlora_linear_fwd(st, x, A, B, alpha, rslora=rslora, dropout_mask=mask,
@@ -664,18 +655,18 @@ class _QLoRAAct8Fn(torch.autograd.Function):
         if x8 is None:
             x8 = act8_pack(x)
         ctx.save_for_backward(x8.codes, x8.exps, A, B, u, mask)
-        ctx.st, ctx.alpha, ctx.rslora, ctx.p, ctx.older = st, alpha, rslora, p, older
+        ctx.st, ctx.alpha, ctx.rslora, ctx.p = st, alpha, rslora, p
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dY):
-        _refuse_older(ctx.older)
+        _refuse_default_stream(ctx)
         codes, exps, A, B, u, mask = ctx.saved_tensors
         dX, dA, dB = qlora_linear_bwd_act8(ctx.st, Act8(codes, exps), dY.contiguous(), A, B,
                                            ctx.alpha, u, need_dx=ctx.needs_input_grad[0],
                                            rslora=ctx.rslora, dropout_mask=mask, dropout_p=ctx.p)
-        return dX, dA.to(A.dtype), dB.to(B.dtype), None, None, None, None, None, None, None
+        return dX, dA.to(A.dtype), dB.to(B.dtype), None, None, None, None, None, None
 
 
 class QLoRALinear(torch.nn.Module):
@@ -697,8 +688,8 @@ class QLoRALinear(torch.nn.Module):
     a forward that is run again would draw another, and raises.  step: the
     Dropout's device tensor, for captured graphs, where the offset of the capture
     stays: count it up by one between replays (offsets are 2^32 apart then).
-    Before a backward is captured, let go of every eager output of the layer: with
-    an eager graph of its parameters alive a captured backward raises."""
+    Before a backward is captured, let go of the layer's outputs of the default
+    stream: with such a graph of its parameters alive a captured backward raises."""
 
     def __init__(self, weight: torch.Tensor, r: int = 16, alpha: float = 32.0,
                  dropout: float = 0.0, rslora: bool = False, act8: bool = False,
@@ -757,19 +748,19 @@ class QLoRALinear(torch.nn.Module):
         shp = x.shape
         x2 = x.reshape(-1, shp[-1]).contiguous()
         p = self.dropout if self.training else 0.0
-        nodes, older = _capture_nodes(self.lora_A, self.lora_B)  # (held until the graph has them)
         if isinstance(self.st, MX4) or (self.seed is not None and p > 0):
             drop = self._draw(p) if p > 0 else None
             y = _LinearFn.apply(x2, self.lora_A, self.lora_B, self.st, self.alpha, self.rslora,
-                                drop, self.act8, x8, older)
-            return y.reshape(*shp[:-1], y.shape[-1])
-        mask = dropout_mask(x2.shape[0], x2.shape[1], p, x2.device) if p > 0 else None
-        if self.act8:
-            y = _QLoRAAct8Fn.apply(x2, self.lora_A, self.lora_B, self.st, self.alpha, self.rslora,
-                                   mask, p, x8, older)
+                                drop, self.act8, x8)
         else:
-            y = _QLoRAFn.apply(x2, self.lora_A, self.lora_B, self.st, self.alpha, self.rslora,
-                               mask, p, older)
+            mask = dropout_mask(x2.shape[0], x2.shape[1], p, x2.device) if p > 0 else None
+            if self.act8:
+                y = _QLoRAAct8Fn.apply(x2, self.lora_A, self.lora_B, self.st, self.alpha,
+                                       self.rslora, mask, p, x8)
+            else:
+                y = _QLoRAFn.apply(x2, self.lora_A, self.lora_B, self.st, self.alpha, self.rslora,
+                                   mask, p)
+        _mark_nodes(y)
         return y.reshape(*shp[:-1], y.shape[-1])
 
 

@@ -21,9 +21,9 @@ from dataclasses import dataclass
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (QN_BF16, QN_EALIGN, QN_F32, NF4State, _Act8, _BlockNorm, _capture_nodes, _check,
-               _dev, _linear_args, _opts, _ptr, _refuse_older, _room, _stream, _written,
-               load_library)
+from . import (QN_BF16, QN_EALIGN, QN_F32, NF4State, _Act8, _BlockNorm, _check, _dev,
+               _linear_args, _mark_nodes, _opts, _ptr, _refuse_default_stream, _room, _stream,
+               _written, load_library)
 
 ACT8_BLOCK = 64
 MAX_TOP = 32  # alternatives of a row
@@ -289,12 +289,12 @@ def block_norm_bwd(dy: torch.Tensor, h_new: torch.Tensor, w_pre: torch.Tensor,
 
 class _BlockNormFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, h, o, w_pre, w_post, gate, scale, eps, pack, older):
+    def forward(ctx, h, o, w_pre, w_post, gate, scale, eps, pack):
         h_new, y, x8 = block_norm_fwd(h, w_pre, o=o, w_post=w_post, gate=gate, scale=scale,
                                       eps=eps, pack=pack)
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(h_new, o, w_pre, w_post, gate)
-        ctx.scale, ctx.eps, ctx.older = scale, eps, older
+        ctx.scale, ctx.eps = scale, eps
         codes, exps = (x8.codes, x8.exps) if pack else (None, None)
         if pack:
             ctx.mark_non_differentiable(codes, exps)
@@ -303,12 +303,12 @@ class _BlockNormFn(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dh_new, dy, *_):
-        _refuse_older(ctx.older)
+        _refuse_default_stream(ctx)
         h_new, o, w_pre, w_post, gate = ctx.saved_tensors
         need = ctx.needs_input_grad
         if dy is None:
             if not (need[1] or need[3] or need[4]):  # h' alone, and only h behind it
-                return dh_new, None, None, None, None, None, None, None, None
+                return dh_new, None, None, None, None, None, None, None
             dy = torch.zeros(h_new.shape, dtype=torch.bfloat16, device=h_new.device)
         g = block_norm_bwd(dy.contiguous(), h_new, w_pre,
                            dh_new=None if dh_new is None else dh_new.contiguous(), o=o,
@@ -316,7 +316,7 @@ class _BlockNormFn(torch.autograd.Function):
                            need_weights=need[2] or need[3], need_gate=need[4])
         cast = lambda d, w: None if d is None else d.to(w.dtype)  # noqa: E731
         return (g.dh, g.do, cast(g.dw_pre, w_pre), cast(g.dw_post, w_post),
-                cast(g.dgate, gate), None, None, None, None)
+                cast(g.dgate, gate), None, None, None)
 
 
 class BlockNorm(torch.nn.Module):
@@ -335,9 +335,9 @@ class BlockNorm(torch.nn.Module):
 
     def forward(self, h, o=None, pack=False):
         w_post, gate = (None, None) if o is None else (self.w_post, self.gate)
-        nodes, older = _capture_nodes(self.w_pre, w_post, gate)  # (held until the graph has them)
         h_new, y, codes, exps = _BlockNormFn.apply(h, o, self.w_pre, w_post, gate, self.scale,
-                                                   self.eps, pack, older)
+                                                   self.eps, pack)
+        _mark_nodes(y)
         return (h if o is None else h_new), y, Act8(codes, exps) if pack else None
 
 

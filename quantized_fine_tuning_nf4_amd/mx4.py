@@ -22,7 +22,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import (NF4State, QNError, _check, _dev, _Dropout, _MX4, _ptr,  # noqa: F401
-               _refuse_older, _room, _stream, load_library)
+               _refuse_default_stream, _room, _stream, load_library)
 from .finetune import _DTYPES, Act8, _act8, _aligned, _written
 
 MX4_BLOCK = 32   # columns of a row that share a scale
@@ -409,7 +409,7 @@ class _LinearFn(torch.autograd.Function):
     backward needs of x is kept in 8 bits (x8, or x packed here)."""
 
     @staticmethod
-    def forward(ctx, x, A, B, w, alpha, rslora, drop, keep8, x8, older):
+    def forward(ctx, x, A, B, w, alpha, rslora, drop, keep8, x8):
         if x8 is not None:
             _act8(x8, *x.shape)
         y, u = linear_fwd(w, x, A, B, alpha, rslora, drop)
@@ -420,15 +420,14 @@ class _LinearFn(torch.autograd.Function):
         # (the step with them: changed before the backward it is an error)
         ctx.save_for_backward(*kept, A, B, u, None if drop is None else drop.step)
         ctx.w, ctx.alpha, ctx.rslora, ctx.drop, ctx.keep8 = w, alpha, rslora, drop, keep8
-        ctx.older = older
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dY):
-        _refuse_older(ctx.older)
+        _refuse_default_stream(ctx)
         x, exps, A, B, u, _ = ctx.saved_tensors
         dX, dA, dB = linear_bwd(ctx.w, Act8(x, exps) if ctx.keep8 else x, dY.contiguous(), A, B,
                                 ctx.alpha, u, need_dx=ctx.needs_input_grad[0],
                                 rslora=ctx.rslora, drop=ctx.drop)
-        return dX, dA.to(A.dtype), dB.to(B.dtype), None, None, None, None, None, None, None
+        return dX, dA.to(A.dtype), dB.to(B.dtype), None, None, None, None, None, None

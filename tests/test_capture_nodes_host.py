@@ -1,34 +1,64 @@
-"""What a forward under capture finds out about its parameters: whether a graph that is not
-the capture's still holds the nodes that add up their gradients."""
+"""What the layers' forwards note about their parameters' nodes: whether one belongs to the
+default stream while the forward runs on another (a capture's)."""
+import pytest
 import torch
 
 
-def _nodes(*leaves, stream=7):
+class Two(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, A, B, other):
+        return x + A + B
+
+    @staticmethod
+    def backward(ctx, g):
+        import quantized_fine_tuning_nf4_amd as qn
+        qn._refuse_default_stream(ctx)
+        return g, g, g, None
+
+
+def _call(A, B, stream, x=None):
     import quantized_fine_tuning_nf4_amd as qn
-    return qn._nodes(leaves, stream)
+    y = Two.apply(torch.zeros(3) if x is None else x, A, B, "other")
+    qn._mark_nodes(y, stream)
+    return y
 
 
-def test_nodes_of_eager_graphs():
-    A, B = torch.nn.Parameter(torch.randn(3)), torch.nn.Parameter(torch.randn(3))
-    frozen = torch.nn.Parameter(torch.randn(3), requires_grad=False)
-    assert _nodes(A, B, None, frozen, torch.nn.Parameter(torch.randn(3)) * 2)[1] is False
-    eager = (A * B).sum()
-    assert _nodes(A)[1] and _nodes(B, A)[1]
-    assert _nodes(A)[1]  # asked again: the same answer
-    eager.backward()
-    assert _nodes(A)[1]  # a backward that has run leaves the graph with its outputs
+def _meets(y):
+    return getattr(y.grad_fn, "meets_default_stream", False)
+
+
+def test_nodes_and_their_streams():
+    A, B = (torch.nn.Parameter(torch.randn(3)) for _ in range(2))
+    eager = _call(A, B, 0)
+    assert not _meets(eager)  # on the default stream itself
+    assert not _meets(_call(A, B, 0))
+    assert _meets(_call(A, B, 7)) and _meets(_call(A, B, 9))
+    eager.sum().backward()
+    assert _meets(_call(A, B, 7))  # a backward that has run leaves the graph with its output
     del eager
-    assert _nodes(A, B)[1] is False
-
-
-def test_nodes_of_the_capture():
-    A = torch.nn.Parameter(torch.randn(3))
-    held, older = _nodes(A)
-    y = A.exp()  # the first use takes the node that was looked at
-    del held
-    assert older is False
-    assert _nodes(A)[1] is False  # the second use in the same capture
-    assert _nodes(A, stream=8)[1]  # a capture on another stream
+    y = _call(A, B, 7)
+    assert not _meets(y) and not _meets(_call(A, B, 8))  # of other streams: no fault
     del y
-    assert _nodes(A, stream=8)[1] is False
-    assert A.grad is None and A.grad_fn is None
+    z = _call(A, B, 0, x=A)  # the same leaf twice
+    assert not _meets(z) and _meets(_call(B, A, 7))
+
+
+def test_graphs_without_parameters():
+    A, B = (torch.nn.Parameter(torch.randn(3), requires_grad=False) for _ in range(2))
+    assert _call(A, B, 7).grad_fn is None
+    x = (torch.zeros(3, requires_grad=True) * 2)
+    held = _call(A, B, 0, x=x)
+    assert not _meets(held) and not _meets(_call(A, B, 7, x=x))
+
+
+def test_a_captured_backward_raises(monkeypatch):
+    A, B = (torch.nn.Parameter(torch.randn(3)) for _ in range(2))
+    eager = _call(A, B, 0)
+    y = _call(A, B, 7)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError, match="let go of every eager output"):
+        y.sum().backward()
+    assert A.grad is None
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    eager.sum().backward()
+    assert A.grad is not None

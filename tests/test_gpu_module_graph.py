@@ -86,9 +86,9 @@ def test_captured_beside_an_eager_graph(base, act8):
     with torch.cuda.graph(graph):
         y = lin(x)
         node = y.grad_fn
-        while node is not None and not hasattr(node, "older"):
+        while node is not None and not hasattr(node, "meets_default_stream"):
             node = node.next_functions[0][0]
-        assert node is not None and node.older  # (else the backward does not run)
+        assert node is not None and node.meets_default_stream  # (else no backward runs here)
         with pytest.raises(RuntimeError, match="let go of every eager output"):
             y.backward(g)
     graph.replay()
@@ -108,7 +108,7 @@ def test_norm_beside_an_eager_graph():
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         y = norm(h)[1]
-        assert y.grad_fn.older
+        assert y.grad_fn.meets_default_stream
         with pytest.raises(RuntimeError, match="let go of every eager output"):
             y.backward(torch.empty_like(y))
     graph.replay()
