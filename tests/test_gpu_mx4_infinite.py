@@ -34,3 +34,27 @@ def test_infinite_gradients(M, rows, cols):
     for m, n, sign in at:
         want[m] = W[n].sign() * (sign * float("inf"))
     assert torch.equal(dX, want)
+
+
+@pytest.mark.parametrize("M,rows,cols", [(16, 72, 64), (300, 72, 320), (520, 72, 1344),
+                                         (520, 8, 1344), (1000, 264, 1152), (1030, 328, 2112),
+                                         (4096, 72, 4096), (4096, 8, 4096)])
+def test_reads_zero_past_its_rows(M, rows, cols):
+    """What lies past the rows of dY counts as zero, whatever the workgroup's memory held before:
+    the result is that of the same operands padded with zeros to whole steps, after a product
+    that left NaNs there."""
+    import quantized_fine_tuning_nf4_amd as qn
+    say(f"[mx4 past dY] {M}x{rows}x{cols}")
+    g = torch.Generator(device="cuda").manual_seed(M + rows)
+    W = torch.randn(rows, cols, generator=g, device="cuda")
+    dY = torch.randn(M, rows, generator=g, device="cuda").to(torch.bfloat16)
+    more = -rows % 64
+    Wp = torch.nn.functional.pad(W, (0, 0, 0, more))
+    want, _, _ = qn.mx4_linear_bwd(qn.mx4_quantize(Wp), None,
+                                   torch.nn.functional.pad(dY, (0, more)))
+    w = qn.mx4_quantize(W)
+    wide = qn.mx4_quantize(torch.ones(512, cols, device="cuda"))
+    bad = torch.full((M, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+    for _ in range(3):
+        assert bool(torch.isnan(qn.mx4_linear_bwd(wide, None, bad)[0]).all())
+        assert torch.equal(qn.mx4_linear_bwd(w, None, dY)[0], want)
