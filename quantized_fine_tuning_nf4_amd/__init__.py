@@ -700,7 +700,7 @@ class QLoRALinear(torch.nn.Module):
             raise ValueError('base must be "nf4" or "mx4"')
         if step is not None and seed is None:
             raise ValueError("step belongs to a seed")
-        if seed is not None:
+        if seed is not None and dropout:
             Dropout(0.0, seed, step=step)  # (what it refuses)
         self.seed, self.step, self.draws = seed, step, 0
         d_out, d_in = weight.shape
