@@ -556,7 +556,8 @@ qn_status mx4_linear_fwd(const qn_mx4* w, const uint16_t* x, int64_t M, const ui
  *   dB = s G^T u
  * from x or x8 as above, u_saved nullable with x.  rows a multiple of 8, cols of 64;
  * r == 0: dX alone (the other outputs and x unused).  W enters the product as bf16,
- * which holds its values exactly where they are at least 2^-126. */
+ * which holds its values exactly where they are at least 2^-126.  u and v = G B enter
+ * theirs in bf16 parts: where one of them is infinite the result may be a NaN. */
 qn_status mx4_linear_bwd(const qn_mx4* w, const uint16_t* x, const qn_act8* x8,
                          const uint16_t* dY, int64_t M, const uint16_t* A, const uint16_t* B,
                          int r, float alpha, int rslora, const qn_dropout* drop,
